@@ -9,7 +9,7 @@ The functions keep the C names (``gdn_fwd``, ``gdn_bwd``, ``gdn_summary``,
 ``gdn_summary_bwd``, ``gdn_compose``, ``gdn_prefix_compose``,
 ``gdn_prefix_compose_bwd``, ``gdn_apply_state``, ``gdn_apply_state_bwd``,
 ``gdn_gate_param_bwd``, ``gdn_query_support``, ``gdn_resolved_segments``, ``gdn_workspace_size``,
-``gdn_check_device_status``) and
+``gdn_check_device_status``, and the decode-step calls at the end) and
 take torch tensors in the token-major layouts of the header: q, k
 [B,T,Hqk,dk]; v [B,T,H,dv]; a, b [B,T,H]; A_log, dt_bias [H] fp32; states
 [B,H,dk,dv] fp32.
@@ -44,6 +44,9 @@ EXPORTS = (
     "gdn_rmsnorm_gated_bwd_workspace_size", "gdn_rmsnorm_gated_bwd",
     "gdn_varlen_workspace_size", "gdn_fwd_varlen", "gdn_bwd_varlen",
     "gdn_varlen_check_device_status",
+    "gdn_step", "gdn_qk_norm_rope_fwd", "gdn_qk_norm_rope_bwd_workspace_size",
+    "gdn_qk_norm_rope_bwd", "gdn_qk_norm_rope_cache", "gdn_attn_decode_workspace_size",
+    "gdn_attn_decode", "gdn_slot_map",
 )
 
 
@@ -85,6 +88,34 @@ class RmsNormProblem(ctypes.Structure):
                 ("eps", ctypes.c_float)]
 
 
+class RopeProblem(ctypes.Structure):
+    """Mirror of ``gdn_rope_problem`` (include/gdn.h)."""
+
+    _fields_ = [("dtype", ctypes.c_int32), ("D", ctypes.c_int32), ("R", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("N", ctypes.c_int64), ("T", ctypes.c_int64),
+                ("Hq", ctypes.c_int64), ("Hk", ctypes.c_int64), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("eps", ctypes.c_float), ("rope_scale", ctypes.c_float)]
+
+
+class AttnProblem(ctypes.Structure):
+    """Mirror of ``gdn_attn_problem`` (include/gdn.h)."""
+
+    _fields_ = [("dtype", ctypes.c_int32), ("D", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("B", ctypes.c_int64), ("Hq", ctypes.c_int64),
+                ("Hk", ctypes.c_int64), ("pages", ctypes.c_int64),
+                ("max_blocks", ctypes.c_int64), ("q_stride", ctypes.c_int64)]
+
+
+class SlotProblem(ctypes.Structure):
+    """Mirror of ``gdn_slot_problem`` (include/gdn.h)."""
+
+    _fields_ = [("page_size", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("B", ctypes.c_int64), ("max_blocks", ctypes.c_int64),
+                ("pages", ctypes.c_int64), ("n_free", ctypes.c_int64),
+                ("n_tokens", ctypes.c_int64)]
+
+
 _lock = threading.Lock()
 _lib = None
 _VP = ctypes.c_void_p
@@ -92,6 +123,8 @@ _PP = ctypes.POINTER(Problem)
 _I64 = ctypes.c_int64
 _CPP = ctypes.POINTER(ConvProblem)
 _RPP = ctypes.POINTER(RmsNormProblem)
+_ROPP = ctypes.POINTER(RopeProblem)
+_APP = ctypes.POINTER(AttnProblem)
 
 
 def load_library(path: str | None = None):
@@ -162,6 +195,17 @@ def load_library(path: str | None = None):
                                + [ctypes.c_size_t, _VP], ctypes.c_int),
             "gdn_varlen_check_device_status": ([_VP, _PP, _VP, ctypes.c_int32, ctypes.c_int32,
                                                 _VP], ctypes.c_int),
+            "gdn_step": ([_PP, _I64] + [_VP] * 12, ctypes.c_int),
+            "gdn_qk_norm_rope_fwd": ([_ROPP] + [_VP] * 9, ctypes.c_int),
+            "gdn_qk_norm_rope_bwd_workspace_size": ([_ROPP, ctypes.POINTER(ctypes.c_size_t)],
+                                                    ctypes.c_int),
+            "gdn_qk_norm_rope_bwd": ([_ROPP] + [_VP] * 13 + [ctypes.c_size_t, _VP],
+                                     ctypes.c_int),
+            "gdn_qk_norm_rope_cache": ([_ROPP] + [_VP] * 7 + [_I64] + [_VP] * 6, ctypes.c_int),
+            "gdn_attn_decode_workspace_size": ([_APP, ctypes.POINTER(ctypes.c_size_t)],
+                                               ctypes.c_int),
+            "gdn_attn_decode": ([_APP] + [_VP] * 8 + [ctypes.c_size_t, _VP, _VP], ctypes.c_int),
+            "gdn_slot_map": ([ctypes.POINTER(SlotProblem)] + [_VP] * 11, ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             fn = getattr(lib, name)
@@ -811,3 +855,267 @@ def gdn_varlen_check_device_status(ws, problem: Problem, cu: Varlen, op: int,
     """Synchronises and reads/clears the status words of a varlen call's workspace."""
     return load_library().gdn_varlen_check_device_status(
         _ptr(ws), ctypes.byref(problem), cu.host_ptr(), cu.n, op, _stream(stream))
+
+
+# ------------------------------------------------- one decode step of a hybrid model
+#
+# These calls check what the C side cannot see (type, shape, layout and device of every
+# tensor) and run on the current stream of the tensors' device, whichever device is current.
+
+def _arg(name, t, dev, dtype, shape):
+    """Address of a contiguous tensor of this type and shape on device `dev`."""
+    if (t.get_device() != dev or t.dtype is not dtype or t.shape != shape
+            or not t.is_contiguous()):
+        raise ValueError(
+            f"{name}: expected a contiguous {dtype} tensor {list(shape)} on cuda:{dev}, got "
+            f"{t.dtype} {list(t.shape)} with strides {list(t.stride())} on {t.device}")
+    return t.data_ptr()
+
+
+def _flat(name, t, dev, n):
+    """Address of a contiguous int32 tensor of n elements in any shape."""
+    if t.get_device() != dev or t.dtype is not torch.int32 or t.numel() != n \
+            or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous int32 tensor of {n} elements on "
+                         f"cuda:{dev}, got {t.dtype} {list(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _rows(name, t, dev, dtype, shape):
+    """(address, elements between tokens) of [..., heads, D] whose rows of one token are
+    contiguous and whose tokens are evenly spaced (a slice of a fused projection, say)."""
+    st, sh = t.stride(), t.shape
+    if t.get_device() != dev or t.dtype is not dtype or sh != shape:
+        raise ValueError(f"{name}: expected a {dtype} tensor {list(shape)} on cuda:{dev}, got "
+                         f"{t.dtype} {list(sh)} on {t.device}")
+    heads, D = sh[-2], sh[-1]
+    ok = (st[-1] == 1 or D == 1) and (st[-2] == D or heads == 1)
+    step, span = None, 1
+    for n, s in zip(reversed(sh[:-2]), reversed(st[:-2])):
+        if n == 1:
+            continue
+        if step is None:
+            step = s
+        ok = ok and s == step * span
+        span *= n
+    if not ok and t.numel():
+        raise ValueError(f"{name}: the elements of a token have to be contiguous and the tokens "
+                         f"evenly spaced, got strides {list(st)} for {list(sh)}")
+    return t.data_ptr(), (step if step is not None and t.numel() else 0)
+
+
+def _device_of(t):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("GDN tensors must be CUDA tensors")
+    return dev
+
+
+def _call(name, dev, *args):
+    """Call a library function with the raw stream appended, `dev` current meanwhile."""
+    fn = getattr(_lib or load_library(), name)
+    if torch.cuda.current_device() == dev:
+        _check(name, fn(*args))
+    else:
+        with torch.cuda.device(dev):
+            _check(name, fn(*args))
+
+
+def _raw_stream(stream, dev):
+    return (stream or torch.cuda.current_stream(dev)).cuda_stream
+
+
+def status_word(device="cuda") -> torch.Tensor:
+    """A zeroed device status word for the ``status`` argument of the calls below, read and
+    cleared by gdn_check_device_status."""
+    return torch.zeros(64, dtype=torch.int32, device=device)
+
+
+def _status(status, dev):
+    return None if status is None else _arg("status", status, dev, torch.int32, (64,))
+
+
+def gdn_step(q, k, v, a, b, A_log, dt_bias, state, slots=None, *, l2norm=True, eps=1e-6,
+             scale=0.0, o=None, status=None, stream=None):
+    """The core for one token per row, over a pool of states updated in place: q, k
+    [B,1,Hqk,dk], v [B,1,H,dv], a, b [B,1,H]; row b uses state[slots[b]] (state
+    [n_slots,H,dk,dv] fp32, slots int32 [B]; None: state[b]); slots[b] = -1 is a padded row
+    (zero output).  Returns o [B,1,H,dv]."""
+    dev, dt = _device_of(q), q.dtype
+    B, T, Hqk, dk = q.shape
+    H, dv = v.shape[2], v.shape[3]
+    n = state.shape[0]
+    if T != 1:
+        raise ValueError(f"gdn_step takes one token per row, got {T}")
+    p = Problem(_dtype_code(dt), 64, B, 1, 0, Hqk, H, dk, dv, 1 if l2norm else 0, eps, scale, 0)
+    gates = (B, 1, H)
+    if o is None:
+        o = torch.empty((B, 1, H, dv), dtype=dt, device=q.device)
+    _call("gdn_step", dev, p, n,
+          None if slots is None else _arg("slots", slots, dev, torch.int32, (B,)),
+          _arg("q", q, dev, dt, (B, 1, Hqk, dk)), _arg("k", k, dev, dt, (B, 1, Hqk, dk)),
+          _arg("v", v, dev, dt, (B, 1, H, dv)), _arg("a", a, dev, dt, gates),
+          _arg("b", b, dev, dt, gates), _arg("A_log", A_log, dev, torch.float32, (H,)),
+          _arg("dt_bias", dt_bias, dev, torch.float32, (H,)),
+          _arg("state", state, dev, torch.float32, (n, H, dk, dv)),
+          _arg("o", o, dev, dt, (B, 1, H, dv)), _status(status, dev), _raw_stream(stream, dev))
+    return o
+
+
+def _rope_problem(q, k, v, dev, inv_freq, T, interleaved, eps, rope_scale):
+    """(problem, addresses of q, k and v) for q [..., Hq, D], k, v [..., Hk, D]."""
+    lead, D = q.shape[:-2], q.shape[-1]
+    N = 1
+    for n in lead:
+        N *= n
+    Hq, Hk = q.shape[-2], k.shape[-2]
+    qp, qs = _rows("q", q, dev, q.dtype, q.shape)
+    kp, ks = _rows("k", k, dev, q.dtype, lead + (Hk, D))
+    vp, vs = (None, 0) if v is None else _rows("v", v, dev, q.dtype, lead + (Hk, D))
+    if T is None:
+        T = lead[-1] if len(lead) > 1 else 0
+    R = 2 * inv_freq.numel()
+    return RopeProblem(_dtype_code(q.dtype), D, R, 1 if interleaved else 0, N, T, Hq, Hk, qs, ks,
+                       vs, eps, rope_scale), qp, kp, vp
+
+
+def _rope_tables(wq, wk, inv_freq, positions, p, dev):
+    f32 = torch.float32
+    return (_arg("wq", wq, dev, f32, (p.D,)), _arg("wk", wk, dev, f32, (p.D,)),
+            _arg("inv_freq", inv_freq, dev, f32, (p.R // 2,)),
+            None if positions is None else
+            _flat("positions", positions, dev, p.N))
+
+
+def gdn_qk_norm_rope_fwd(q, k, wq, wk, inv_freq, positions=None, *, T=None, interleaved=False,
+                         eps=1e-6, rope_scale=1.0, q_out=None, k_out=None, stream=None):
+    """RMSNorm of every head of q [..., Hq, D] and k [..., Hk, D] (weights wq, wk [D] fp32) and
+    the rotation of its first 2 * len(inv_freq) elements by positions * inv_freq, in one pass.
+    positions int32, one per token; None: token n of q's [B, T, ...] is at n % T ([N, ...]:
+    at n).  q and k may be slices of one projection.  Returns (q_out, k_out), contiguous."""
+    dev, dt = _device_of(q), q.dtype
+    p, qp, kp, _ = _rope_problem(q, k, None, dev, inv_freq, T, interleaved, eps, rope_scale)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=dt, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=dt, device=q.device)
+    _call("gdn_qk_norm_rope_fwd", dev, p, qp, kp,
+          *_rope_tables(wq, wk, inv_freq, positions, p, dev),
+          _arg("q_out", q_out, dev, dt, q.shape), _arg("k_out", k_out, dev, dt, k.shape),
+          _raw_stream(stream, dev))
+    return q_out, k_out
+
+
+def gdn_qk_norm_rope_bwd_workspace_size(problem: RopeProblem) -> int:
+    n = ctypes.c_size_t(0)
+    _check("gdn_qk_norm_rope_bwd_workspace_size",
+           load_library().gdn_qk_norm_rope_bwd_workspace_size(problem, ctypes.byref(n)))
+    return n.value
+
+
+def gdn_qk_norm_rope_bwd(q, k, wq, wk, inv_freq, positions, dq_out, dk_out, *, T=None,
+                         interleaved=False, eps=1e-6, rope_scale=1.0, dq=None, dk=None, dwq=None,
+                         dwk=None, ws=None, stream=None):
+    """Backward of gdn_qk_norm_rope_fwd: (dq, dk contiguous in q's type, dwq, dwk [D] fp32)."""
+    dev, dt, f32 = _device_of(q), q.dtype, torch.float32
+    p, qp, kp, _ = _rope_problem(q, k, None, dev, inv_freq, T, interleaved, eps, rope_scale)
+    dq = torch.empty(q.shape, dtype=dt, device=q.device) if dq is None else dq
+    dk = torch.empty(k.shape, dtype=dt, device=q.device) if dk is None else dk
+    dwq = torch.empty(p.D, dtype=f32, device=q.device) if dwq is None else dwq
+    dwk = torch.empty(p.D, dtype=f32, device=q.device) if dwk is None else dwk
+    if ws is None:
+        ws = torch.empty(max(gdn_qk_norm_rope_bwd_workspace_size(p), 16), dtype=torch.uint8,
+                         device=q.device)
+    _call("gdn_qk_norm_rope_bwd", dev, p, qp, kp,
+          *_rope_tables(wq, wk, inv_freq, positions, p, dev),
+          _arg("dq_out", dq_out, dev, dt, q.shape), _arg("dk_out", dk_out, dev, dt, k.shape),
+          _arg("dq", dq, dev, dt, q.shape), _arg("dk", dk, dev, dt, k.shape),
+          _arg("dwq", dwq, dev, f32, (p.D,)), _arg("dwk", dwk, dev, f32, (p.D,)),
+          _arg("ws", ws, dev, torch.uint8, ws.shape), ws.numel(), _raw_stream(stream, dev))
+    return dq, dk, dwq, dwk
+
+
+def gdn_qk_norm_rope_cache(q, k, v, wq, wk, inv_freq, positions, slots, k_cache, v_cache, *,
+                           T=None, interleaved=False, eps=1e-6, rope_scale=1.0, q_out=None,
+                           status=None, stream=None):
+    """gdn_qk_norm_rope_fwd that writes the key of token n, and v's row, to cache row slots[n]
+    (int32, one per token; -1: nowhere; the others have to differ) of k_cache, v_cache
+    [pages, page_size, Hk, D].  Returns q_out."""
+    dev, dt = _device_of(q), q.dtype
+    p, qp, kp, vp = _rope_problem(q, k, v, dev, inv_freq, T, interleaved, eps, rope_scale)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=dt, device=q.device)
+    cache = k_cache.shape[:-2] + (p.Hk, p.D)
+    n_slots = 1
+    for n in cache[:-2]:
+        n_slots *= n
+    _call("gdn_qk_norm_rope_cache", dev, p, qp, kp, vp,
+          *_rope_tables(wq, wk, inv_freq, positions, p, dev), n_slots,
+          _flat("slots", slots, dev, p.N), _arg("q_out", q_out, dev, dt, q.shape),
+          _arg("k_cache", k_cache, dev, dt, cache), _arg("v_cache", v_cache, dev, dt, cache),
+          _status(status, dev), _raw_stream(stream, dev))
+    return q_out
+
+
+def gdn_attn_decode_workspace_size(problem: AttnProblem) -> int:
+    n = ctypes.c_size_t(0)
+    _check("gdn_attn_decode_workspace_size",
+           load_library().gdn_attn_decode_workspace_size(problem, ctypes.byref(n)))
+    return n.value
+
+
+def gdn_attn_decode(q, k_cache, v_cache, block_table, seq_len, *, scale=0.0, o=None, lse=None,
+                    want_lse=True, ws=None, status=None, stream=None):
+    """Attention of one new token per request, q [B,Hq,D], over the paged caches
+    [pages, page_size, Hk, D]: token j of request b is row j % page_size of page
+    block_table[b, j // page_size] (int32 [B, max_blocks]), j < seq_len[b] (int32 [B]).
+    Returns (o [B,Hq,D], lse [B,Hq] fp32 or None)."""
+    dev, dt = _device_of(q), q.dtype
+    B, Hq, D = q.shape
+    pages, P, Hk, _ = k_cache.shape
+    qp, qs = _rows("q", q, dev, dt, q.shape)
+    blocks = block_table.shape[1]
+    p = AttnProblem(_dtype_code(dt), D, P, scale, B, Hq, Hk, pages, blocks, qs)
+    if o is None:
+        o = torch.empty((B, Hq, D), dtype=dt, device=q.device)
+    if lse is None and want_lse:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
+    if ws is None:
+        ws = torch.empty(gdn_attn_decode_workspace_size(p), dtype=torch.uint8, device=q.device)
+    cache = (pages, P, Hk, D)
+    _call("gdn_attn_decode", dev, p, qp, _arg("k_cache", k_cache, dev, dt, cache),
+          _arg("v_cache", v_cache, dev, dt, cache),
+          _arg("block_table", block_table, dev, torch.int32, (B, blocks)),
+          _arg("seq_len", seq_len, dev, torch.int32, (B,)), _arg("o", o, dev, dt, (B, Hq, D)),
+          None if lse is None else _arg("lse", lse, dev, torch.float32, (B, Hq)),
+          _arg("ws", ws, dev, torch.uint8, ws.shape), ws.numel(), _status(status, dev),
+          _raw_stream(stream, dev))
+    return o, lse
+
+
+def gdn_slot_map(ctx_len, new_len, free_pages, block_table, *, page_size, pages, n_tokens,
+                 seq_len=None, cu_seqlens=None, positions=None, slots=None, used=None,
+                 status=None, stream=None):
+    """Block tables and slots of a step from ctx_len, new_len (int32 [B]): new pages from the
+    front of free_pages (int32) into block_table (int32 [B, max_blocks], in place).  Returns
+    (seq_len [B], cu_seqlens [B+1], positions [n_tokens], slots [n_tokens], used [1]), int32."""
+    dev, i32 = _device_of(ctx_len), torch.int32
+    B, blocks = block_table.shape
+    n_free = free_pages.numel()
+
+    def out(t, n):
+        return torch.empty(n, dtype=i32, device=ctx_len.device) if t is None else t
+
+    seq_len, cu_seqlens, used = out(seq_len, B), out(cu_seqlens, B + 1), out(used, 1)
+    positions, slots = out(positions, n_tokens), out(slots, n_tokens)
+    p = SlotProblem(page_size, 0, B, blocks, pages, n_free, n_tokens)
+    _call("gdn_slot_map", dev, p, _arg("ctx_len", ctx_len, dev, i32, (B,)),
+          _arg("new_len", new_len, dev, i32, (B,)),
+          _arg("free_pages", free_pages, dev, i32, (n_free,)),
+          _arg("block_table", block_table, dev, i32, (B, blocks)),
+          _arg("seq_len", seq_len, dev, i32, (B,)),
+          _arg("cu_seqlens", cu_seqlens, dev, i32, (B + 1,)),
+          _arg("positions", positions, dev, i32, (n_tokens,)),
+          _arg("slots", slots, dev, i32, (n_tokens,)), _arg("used", used, dev, i32, (1,)),
+          _status(status, dev), _raw_stream(stream, dev))
+    return seq_len, cu_seqlens, positions, slots, used

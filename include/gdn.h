@@ -501,6 +501,171 @@ gdn_status gdn_rmsnorm_gated_bwd(const gdn_rmsnorm_problem* p, const void* o, co
                                  const float* w, const void* dy, void* d_o, void* dz, float* dw,
                                  void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * ---- One decode step of a hybrid model ----
+ *
+ * The models of the pages alternate Gated DeltaNet and full-attention layers 3:1 ("linear
+ * attention cp #1035", section "What does this PR do").  The calls below serve such a model
+ * token by token: the single-token form of the core over a pool of states (gdn_step) and,
+ * for the full-attention layers, the step's cache rows (gdn_slot_map), the q/k norm with the
+ * position rotation (gdn_qk_norm_rope_*, also the training form and its backward) and the
+ * attention of the new token over the paged key-value cache (gdn_attn_decode).  The pages do
+ * not print these formulas; each call states its own.
+ *
+ * In these calls int32 arrays need 4-byte alignment only, every other pointer 16 bytes.
+ * Indices that live in device memory (slots, pages, lengths) cannot be checked on the host:
+ * the kernels skip what an index outside its range would touch, and record it in `status`,
+ * a device status word like the one at the start of a workspace: NULL, or a 256-byte aligned
+ * buffer that the caller has zeroed once; the calls only add bits to it, and
+ * gdn_check_device_status(status, stream) reads and clears it (GDN_ERR_INVALID_ARG).
+ */
+
+/*
+ * The core for one token per row over a pool of states, updated in place.  Row b of the
+ * batch (q, k [B,1,Hqk,dk], v, o [B,1,H,dv], a, b [B,1,H]: the layouts of gdn_fwd with
+ * p->T = 1) uses state[slots[b]], state [n_slots,H,dk,dv] fp32; slots NULL: row b uses
+ * state[b].  Result per row and V head: that of gdn_fwd with h0 = hT = the row's state.
+ * slots[b] = -1 is a padded row: o is zero and no state is touched.  A slot outside
+ * [-1, n_slots), or one that an earlier row of the batch has already (the first row keeps
+ * it), is recorded in `status` and treated as -1.  fp32 arithmetic for both dtypes.  One
+ * launch, no workspace.
+ * Errors: those of gdn_query_support; p->T != 1, n_slots < 0, null slots with n_slots < B, a
+ * null or misaligned pointer: GDN_ERR_INVALID_ARG; n_slots >= 2^31: GDN_ERR_UNSUPPORTED.
+ */
+gdn_status gdn_step(const gdn_problem* p, int64_t n_slots, const int32_t* slots, const void* q,
+                    const void* k, const void* v, const void* a, const void* b,
+                    const float* A_log, const float* dt_bias, float* state, void* o,
+                    int32_t* status, void* stream);
+
+/*
+ * RMSNorm of every query and key head with the position rotation, in one pass.  For a head
+ * row x of D elements at position t, with r = 1 / sqrt(mean(x^2) + eps):
+ *   n = x r w;  for i < R/2, angle t inv_freq[i], c = rope_scale cos, s = rope_scale sin:
+ *   y1 = n1 c - n2 s,  y2 = n2 c + n1 s  on the pair (n1, n2) = (n[i], n[i + R/2]), or
+ *   (n[2i], n[2i+1]) when interleaved;  y = n for the elements from R on.
+ * w is wq for the Hq query heads, wk for the Hk key heads.  Long-context scalings of the
+ * rotation are given through inv_freq (scaled frequencies) and rope_scale (their factor on
+ * cos and sin).  The angle's product is exact before it is reduced, for any int32 position.
+ *  - q [N,Hq,D], k, v [N,Hk,D] in p->dtype with q_stride, k_stride, v_stride elements between
+ *    tokens (0: contiguous; they may be slices of one fused projection); q_out [N,Hq,D],
+ *    k_out [N,Hk,D], dq_out, dk_out, dq, dk contiguous.
+ *  - wq, wk [D], inv_freq [R/2] fp32 (null allowed when R = 0); positions int32 [N], or NULL:
+ *    token n is at position n % T (T tokens per row of the batch; T = 0: position n).
+ *  - fp32 arithmetic.
+ * Backward: from dq_out, dk_out and the forward's q, k: with dn the transposed rotation of dy,
+ *   dx = r (g - x r mean(g x r)), g = dn w;   dw = sum over tokens and heads of dn x r
+ *   (fixed-order sums: deterministic; dwq, dwk [D] fp32).
+ * Cache form (serving): as the forward, but the rotated key of token n and v's row n are
+ * written to row slots[n] of the key and the value cache, [n_slots][Hk][D] (the pages of a
+ * paged cache in a row); slots[n] = -1 writes nowhere, a slot outside [-1, n_slots) is
+ * recorded in `status` and writes nowhere.  q_out is written for every token.  Slots other
+ * than -1 must differ: of two tokens with one slot, each element keeps either's value.
+ * Errors: null or misaligned pointer, sizes < 0, Hq or Hk < 0 (both may not be 0), D < 1,
+ * R outside [0, D], a stride smaller than a token or no multiple of 16 bytes, eps < 0, a
+ * rope_scale that is not finite: GDN_ERR_INVALID_ARG; D above 256 or no multiple of 8, R no
+ * multiple of 16, N (Hq + Hk) >= 2^31 or n_slots >= 2^31: GDN_ERR_UNSUPPORTED; workspace
+ * smaller than gdn_qk_norm_rope_bwd_workspace_size: GDN_ERR_WORKSPACE.
+ */
+typedef struct gdn_rope_problem {
+  int32_t dtype;       /* GDN_BF16 or GDN_FP32 */
+  int32_t D;           /* head dim, a multiple of 8, at most 256 */
+  int32_t R;           /* rotated elements at the start of a head, a multiple of 16, 0..D */
+  int32_t interleaved; /* pairs: 0 (i, i + R/2), 1 (2i, 2i + 1) */
+  int64_t N;           /* tokens */
+  int64_t T;           /* tokens per batch row when positions is NULL; 0: N */
+  int64_t Hq, Hk;      /* query heads, key (and value) heads */
+  int64_t q_stride, k_stride, v_stride;  /* elements between tokens; 0: contiguous */
+  float eps;           /* of the norm, 1e-6 */
+  float rope_scale;    /* factor on cos and sin, 1 */
+} gdn_rope_problem;
+
+gdn_status gdn_qk_norm_rope_fwd(const gdn_rope_problem* p, const void* q, const void* k,
+                                const float* wq, const float* wk, const float* inv_freq,
+                                const int32_t* positions, void* q_out, void* k_out,
+                                void* stream);
+gdn_status gdn_qk_norm_rope_bwd_workspace_size(const gdn_rope_problem* p, size_t* bytes);
+gdn_status gdn_qk_norm_rope_bwd(const gdn_rope_problem* p, const void* q, const void* k,
+                                const float* wq, const float* wk, const float* inv_freq,
+                                const int32_t* positions, const void* dq_out,
+                                const void* dk_out, void* dq, void* dk, float* dwq, float* dwk,
+                                void* workspace, size_t workspace_bytes, void* stream);
+gdn_status gdn_qk_norm_rope_cache(const gdn_rope_problem* p, const void* q, const void* k,
+                                  const void* v, const float* wq, const float* wk,
+                                  const float* inv_freq, const int32_t* positions,
+                                  int64_t n_slots, const int32_t* slots, void* q_out,
+                                  void* k_cache, void* v_cache, int32_t* status, void* stream);
+
+/*
+ * Attention of one new token per request over a paged key-value cache.  Request b has
+ * seq_len[b] cached tokens (the new one among them); token j is row j % page_size of page
+ * block_table[b][j / page_size] of k_cache, v_cache [pages][page_size][Hk][D]; query head h
+ * reads key head h / (Hq/Hk).  With s_j = scale q.k_j over j < seq_len[b]:
+ *   o = sum_j exp(s_j - lse) v_j,   lse = log sum_j exp(s_j)
+ * o [B,Hq,D] in p->dtype; lse [B,Hq] fp32, nullable.  seq_len[b] = 0: o = 0, lse = -inf.
+ * Cache rows past seq_len are never used, whatever they hold.  Entries of block_table behind
+ * the last used page are not read.  fp32 sums and softmax; on bf16 the weights exp(s_j - m)
+ * are rounded to bf16 for their product with v, and lse is taken before that rounding.
+ *  - seq_len int32 [B]; a length outside [0, max_blocks page_size] is clamped, a used page
+ *    outside [0, pages) has its tokens left out; both are recorded in `status`.
+ *  - Workspace: gdn_attn_decode_workspace_size, 256-byte aligned: the pieces of requests whose
+ *    cache is split over several CTAs.  Its size depends on p only through D and dtype.
+ * The split is chosen on the device from seq_len (the host reads nothing) and depends on the
+ * lengths alone: deterministic.  Two launches.
+ * Errors: null or misaligned pointer, sizes < 0, Hq % Hk != 0, q_stride < Hq D or no multiple
+ * of 16 bytes: GDN_ERR_INVALID_ARG; D other than 64, 128 or 256, page_size no multiple of 16,
+ * pages page_size or max_blocks page_size >= 2^31, B Hq >= 2^31: GDN_ERR_UNSUPPORTED.
+ */
+typedef struct gdn_attn_problem {
+  int32_t dtype;      /* GDN_BF16 or GDN_FP32: q, both caches, o */
+  int32_t D;          /* head dim: 64, 128 or 256 */
+  int32_t page_size;  /* tokens per page, a multiple of 16 */
+  float scale;        /* of the scores; <= 0 means 1/sqrt(D) */
+  int64_t B, Hq, Hk;  /* requests, query heads, key and value heads */
+  int64_t pages;      /* pages of each cache */
+  int64_t max_blocks; /* entries per row of block_table */
+  int64_t q_stride;   /* elements between the requests' rows of q; 0: Hq D */
+} gdn_attn_problem;
+
+gdn_status gdn_attn_decode_workspace_size(const gdn_attn_problem* p, size_t* bytes);
+gdn_status gdn_attn_decode(const gdn_attn_problem* p, const void* q, const void* k_cache,
+                           const void* v_cache, const int32_t* block_table,
+                           const int32_t* seq_len, void* o, float* lse, void* workspace,
+                           size_t workspace_bytes, int32_t* status, void* stream);
+
+/*
+ * Block tables and slots of a step, built on the device from the requests' lengths.  Request
+ * b has ctx_len[b] tokens in the cache already and new_len[b] tokens in this step, packed one
+ * request after another in n_tokens token rows (rows behind the last are padding).
+ *  - seq_len[b] = ctx_len[b] + new_len[b]; cu_seqlens [B+1]: offsets of the packed tokens (as
+ *    gdn_fwd_varlen takes).
+ *  - Request b needs ceil(seq_len/page_size) - ceil(ctx_len/page_size) new pages; they are
+ *    taken from the front of free_pages [n_free] in the order of the requests and written to
+ *    block_table [B][max_blocks] behind the pages it has; the other entries stay as they are.
+ *    used[0] = the pages the step needs (more than n_free: not all could be given).
+ *  - positions[t], slots[t] of packed token t: its position in its request and its cache row
+ *    page * page_size + position % page_size; padding rows get position 0 and slot -1.
+ * A token whose page is missing gets slot -1: past max_blocks, past the free list, or a page
+ * outside [0, pages).  That, a negative length (taken as 0) and packed tokens past n_tokens
+ * (dropped) are recorded in `status`; seq_len stops at max_blocks page_size.  One launch, no
+ * workspace; all outputs int32.
+ * Errors: null or misaligned pointer, sizes < 0, page_size < 1: GDN_ERR_INVALID_ARG;
+ * pages page_size, max_blocks page_size, n_tokens, n_free or B >= 2^31: GDN_ERR_UNSUPPORTED.
+ */
+typedef struct gdn_slot_problem {
+  int32_t page_size;  /* tokens per page, >= 1 */
+  int32_t reserved;   /* 0 */
+  int64_t B;          /* requests */
+  int64_t max_blocks; /* entries per row of block_table */
+  int64_t pages;      /* pages of the cache */
+  int64_t n_free;     /* entries of free_pages */
+  int64_t n_tokens;   /* entries of positions and slots */
+} gdn_slot_problem;
+
+gdn_status gdn_slot_map(const gdn_slot_problem* p, const int32_t* ctx_len,
+                        const int32_t* new_len, const int32_t* free_pages, int32_t* block_table,
+                        int32_t* seq_len, int32_t* cu_seqlens, int32_t* positions,
+                        int32_t* slots, int32_t* used, int32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
