@@ -1,83 +1,611 @@
-// gdn_attn.cu -- attention of one new token per request over a paged key-value cache.
+// gdn_attn.cu -- attention of one new token per request over a paged key-value cache.  Per
+// request and query head, over its n cached tokens:
+//   s_j = scale q.k_j,  o = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),  lse = m + log(sum)
+// with the running maximum m and sum of a one-pass softmax.
+//
+// Bound by HBM: every K and V row is read once.  A piece of work is (request, key head, range
+// of tokens); the query heads of a key head are the 8 columns of the products
+//   S^T [16 keys x 8 heads] = K [16 x D] Q^T,   O^T [D x 8] += V^T [D x 16 keys] P^T
+// so a group of 8 query heads fills mma.sync's tile and K, V need no transposition: both are
+// the products' A operand, whose fragments are loaded from global memory straight into
+// registers, 16 bytes per lane.  That works because the contraction index of the first
+// product (the head's elements) and the output rows of the second may be permuted freely:
+//   K: lane (g, t) = (lane / 4, lane % 4) loads 16-byte chunk t + 4c of key rows g and g + 8,
+//      and the 4 (2) words of a chunk serve 2 products, Q's fragment being the same chunk;
+//   V: the lane loads chunk g + 8c of the rows of the 4 keys of its fragment; the pairs of
+//      keys are put together with byte permutes.
+// P^T comes out of the first product transposed (keys by heads) and is turned with movmatrix
+// (bf16) or shuffles (fp32).  No shared memory, barrier or copy wait is on the path of the
+// data: a warp's next K tile is on its way while it does the softmax and V's product, and the
+// next V tile during the next K product; 8 to 16 such warps per SM keep 64 to 128 KB in flight.
+// fp32 caches use tf32 products of the two-term split x = hi + lo (hi hi + hi lo + lo hi:
+// 2^-21 of each product's size), which keeps fp32 accuracy at the same layout.
+//
+// Split: the unit is a CTA tile of one (request, key head); the units of all requests in a
+// row are divided evenly over the CTAs of one wave, whatever the lengths: no tail, and one long
+// request uses the whole GPU.  A CTA's first and last pieces may be parts of a request; these
+// go to the workspace and k_attn_join adds them up.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <string.h>
 
+#include <type_traits>
+
 #include "gdn_internal.h"
-#include "gdn_vec.cuh"
 
 namespace gdn {
 namespace {
 
-using namespace vec;
+constexpr int AT_W = 4;            // warps per CTA
+constexpr int AT_NT = 32 * AT_W;
+constexpr int AT_G = 8;            // query heads per piece
+constexpr int AT_SMS = 152;
 
-constexpr int AT_NT = 128;
+// Keys per warp tile and CTAs per SM: the K and V tiles and the accumulators of D x 8 fill
+// most of a CTA's share of the registers.
+// kParts > 1: the two tiles do not fit; they are loaded that many parts of D at a time, as used.
+template <int D, typename T> struct Cfg;
+template <> struct Cfg<64, __nv_bfloat16> { static constexpr int kKeys = 32, kCtas = 4, kParts = 1; };
+template <> struct Cfg<128, __nv_bfloat16> { static constexpr int kKeys = 16, kCtas = 3, kParts = 1; };
+template <> struct Cfg<256, __nv_bfloat16> { static constexpr int kKeys = 16, kCtas = 2, kParts = 1; };
+template <> struct Cfg<64, float> { static constexpr int kKeys = 16, kCtas = 3, kParts = 1; };
+template <> struct Cfg<128, float> { static constexpr int kKeys = 16, kCtas = 2, kParts = 1; };
+template <> struct Cfg<256, float> { static constexpr int kKeys = 16, kCtas = 2, kParts = 4; };
+
+// A partial piece in the workspace: slot 2c of CTA c is the piece that began before it, slot
+// 2c + 1 the one that goes on behind it.
+struct Join {
+  int32_t b, h;   // request, first query head (h < 0: no piece begins in this CTA and goes on)
+  int32_t heads;  // query heads of the piece
+  int32_t last;   // CTA that ends it
+};
 
 struct AttnArgs {
   int64_t B, Hq, Hk, pages, max_blocks, qs;
-  int P;
-  float scale;
+  int P, G, HG;   // tokens per page, query heads per key head, pieces of AT_G of them
+  float sl;       // scale log2(e)
   const void *q, *kc, *vc;
   const int32_t *table, *len;
   void* o;
   float* lse;
+  Join* join;     // [CTAs]
+  float2* ml;     // [CTAs][2][AT_G] maximum (log2 units) and sum
+  float* acc;     // [CTAs][2][AT_G][D]
   int32_t* status;
 };
 
-// one CTA per request and query head; a warp per key, D / 32 elements per lane
-template <int D, typename T>
-__global__ void __launch_bounds__(AT_NT) k_attn_decode(AttnArgs ar) {
-  constexpr int E = D / 32, W = AT_NT / 32;
-  __shared__ float s_m[W], s_l[W], s_o[W][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t b = blockIdx.x / ar.Hq, h = blockIdx.x % ar.Hq, hk = h / (ar.Hq / ar.Hk);
-  const int64_t cap = ar.max_blocks * ar.P;
-  int64_t len = ar.len[b];
-  bool bad = len < 0 || len > cap;
-  len = len < 0 ? 0 : len > cap ? cap : len;
-  float q[E], acc[E] = {}, m = -INFINITY, l = 0.f;
-  const T* qp = reinterpret_cast<const T*>(ar.q) + b * ar.qs + h * D;
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint4 ldg16(const void* p) {
+  uint4 v;
+  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// x = hi + lo with hi, lo in tf32 (lo's own rounding is 2^-23 of x).  An infinite or NaN x (or one
+// that hi's rounding would make infinite) goes into lo alone: mma_split multiplies lo only with the
+// other operand's hi, so that no 0 * inf arises beside the product itself.
+__device__ __forceinline__ void split_tf32(uint32_t x, uint32_t* hi, uint32_t* lo) {
+  uint32_t h, l;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(h) : "f"(__uint_as_float(x)));
+  const float r = __uint_as_float(x) - __uint_as_float(h);
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(l) : "f"(r));
+  const bool huge = (x & 0x7f800000u) >= 0x7f000000u;
+  *hi = huge ? 0u : h;
+  *lo = huge ? x : l;
+}
+// c += A B with A and B given as split values
+__device__ __forceinline__ void mma_split(float (&c)[4], const uint32_t (&ah)[4],
+                                          const uint32_t (&al)[4], const uint32_t (&bh)[2],
+                                          const uint32_t (&bl)[2]) {
+  mma_tf32(c, al, bh[0], bh[1]);
+  mma_tf32(c, ah, bl[0], bl[1]);
+  mma_tf32(c, ah, bh[0], bh[1]);
+}
+
+// Q of the piece in shared memory: AT_G rows (zeros past the piece's heads); rows are 64 bytes
+// longer than D elements, so that the 8 lanes of a 16-byte read phase (2 rows x 4 chunks)
+// fall on different banks.  fp32: hi rows, then lo rows.
+template <int D, typename T> struct Smem {
+  static constexpr int kRow = D * (int)sizeof(T) + 64;  // bytes
+  static constexpr int kQ = AT_G * kRow * (sizeof(T) == 4 ? 2 : 1);
+  static constexpr int kORow = D + 2;                   // floats
+  static constexpr int kO = AT_W * AT_G * kORow * 4;
+  static constexpr int kBytes = kQ > kO ? kQ : kO;      // Q and O take turns
+};
+
+// What a warp keeps of its piece.
+template <int D> struct Acc {
+  float o[D / 16][4];  // O^T tiles
+  float m[2], l[2];    // of heads 2t, 2t + 1: maximum (log2 units), this lane's part of the sum
+};
+
+// NK blocks of 16 keys by DP elements.
+template <int DP, typename T, int NK>
+struct Tile {
+  static constexpr int EL = 16 / (int)sizeof(T);
+  uint4 r[NK][4][DP / (8 * EL)];  // K: rows g, g + 8 of even, then odd chunks; V: 4 keys
+};
+
+// One 16-key block's place in the cache: rows kept, and the block's first row.
+struct Block {
+  int64_t off;  // element offset of its first row
+  int n;        // rows that count (0..16)
+};
+
+// s += the scores of NK blocks over one part of D, for heads 2t, 2t + 1 of the lane's rows g, g + 8;
+// qs points at the part in Q's rows.
+template <int D, int DP, int NK>
+__device__ __forceinline__ void scores(const Tile<DP, __nv_bfloat16, NK>& k, const char* qs,
+                                       float (&s)[NK][4]) {
+  constexpr int kRow = Smem<D, __nv_bfloat16>::kRow;
+  const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
 #pragma unroll
-  for (int j = 0; j < E; ++j) q[j] = (float)qp[j * 32 + lane] * ar.scale;
-  for (int64_t t = warp; t < len; t += W) {
-    const int64_t page = ar.table[b * ar.max_blocks + t / ar.P];
-    if (page < 0 || page >= ar.pages) {
-      bad = true;
+  for (int c = 0; c < DP / 32; ++c) {
+    const uint4 b = *reinterpret_cast<const uint4*>(qs + g * kRow + (t + 4 * c) * 16);
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      const uint4 a0 = k.r[i][(c & 1) * 2][c >> 1], a1 = k.r[i][(c & 1) * 2 + 1][c >> 1];
+      mma_bf16(s[i], a0.x, a1.x, a0.y, a1.y, b.x, b.y);
+      mma_bf16(s[i], a0.z, a1.z, a0.w, a1.w, b.z, b.w);
+    }
+  }
+}
+template <int D, int DP, int NK>
+__device__ __forceinline__ void scores(const Tile<DP, float, NK>& k, const char* qs,
+                                       float (&s)[NK][4]) {
+  constexpr int kRow = Smem<D, float>::kRow;
+  const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+#pragma unroll
+  for (int c = 0; c < DP / 16; ++c) {
+    const uint4 bh = *reinterpret_cast<const uint4*>(qs + g * kRow + (t + 4 * c) * 16);
+    const uint4 bl = *reinterpret_cast<const uint4*>(qs + (AT_G + g) * kRow + (t + 4 * c) * 16);
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      const uint4 a0 = k.r[i][(c & 1) * 2][c >> 1], a1 = k.r[i][(c & 1) * 2 + 1][c >> 1];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint32_t ah[4], al[4];
+        split_tf32(word(a0, 2 * u), &ah[0], &al[0]);
+        split_tf32(word(a1, 2 * u), &ah[1], &al[1]);
+        split_tf32(word(a0, 2 * u + 1), &ah[2], &al[2]);
+        split_tf32(word(a1, 2 * u + 1), &ah[3], &al[3]);
+        const uint32_t h[2] = {word(bh, 2 * u), word(bh, 2 * u + 1)};
+        const uint32_t l[2] = {word(bl, 2 * u), word(bl, 2 * u + 1)};
+        mma_split(s[i], ah, al, h, l);
+      }
+    }
+  }
+}
+
+// O^T += V^T P^T over part `part` of D; p holds the weights in the scores' layout.
+template <int D, int DP, int NK>
+__device__ __forceinline__ void weigh(const Tile<DP, __nv_bfloat16, NK>& v,
+                                      const float (&p)[NK][4], Acc<D>& a, int part) {
+#pragma unroll
+  for (int i = 0; i < NK; ++i) {
+    // the weights' one rounding: half a bf16 step each, of random sign over the keys
+    const __nv_bfloat162 p0 = __floats2bfloat162_rn(p[i][0], p[i][1]);
+    const __nv_bfloat162 p1 = __floats2bfloat162_rn(p[i][2], p[i][3]);
+    const uint32_t b0 = transpose8x8(*reinterpret_cast<const uint32_t*>(&p0));
+    const uint32_t b1 = transpose8x8(*reinterpret_cast<const uint32_t*>(&p1));
+#pragma unroll
+    for (int c = 0; c < DP / 64; ++c)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t x0 = word(v.r[i][0][c], w), x1 = word(v.r[i][1][c], w);
+        const uint32_t x2 = word(v.r[i][2][c], w), x3 = word(v.r[i][3][c], w);
+        mma_bf16(a.o[part * (DP / 16) + c * 4 + w], __byte_perm(x0, x1, 0x5410), __byte_perm(x0, x1, 0x7632),
+                 __byte_perm(x2, x3, 0x5410), __byte_perm(x2, x3, 0x7632), b0, b1);
+      }
+  }
+}
+template <int D, int DP, int NK>
+__device__ __forceinline__ void weigh(const Tile<DP, float, NK>& v, const float (&p)[NK][4],
+                                      Acc<D>& a, int part) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int i = 0; i < NK; ++i)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {  // keys 8u .. 8u + 7
+      uint32_t bh[2], bl[2];
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {  // P[key 8u + t + 4z][head g] from lane (t + 4z, g / 2)
+        const int src = (t + 4 * z) * 4 + (g >> 1);
+        const float e = __shfl_sync(0xffffffffu, p[i][2 * u], src);
+        const float f = __shfl_sync(0xffffffffu, p[i][2 * u + 1], src);
+        split_tf32(__float_as_uint(g & 1 ? f : e), &bh[z], &bl[z]);
+      }
+#pragma unroll
+      for (int c = 0; c < DP / 32; ++c)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          uint32_t ah[4], al[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+            split_tf32(word(v.r[i][2 * u + (z >> 1)][c], 2 * w + (z & 1)), &ah[z], &al[z]);
+          mma_split(a.o[part * (DP / 16) + c * 2 + w], ah, al, bh, bl);
+        }
+    }
+}
+
+template <int DP, typename T, int NK>
+__device__ __forceinline__ void load_k(Tile<DP, T, NK>& k, const T* base, const Block (&blk)[NK],
+                                       int64_t row) {
+  constexpr int EL = 16 / (int)sizeof(T);
+  const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+#pragma unroll
+  for (int i = 0; i < NK; ++i) {
+    const T* p = base + blk[i].off + g * row + t * EL;
+    const bool in0 = g < blk[i].n, in1 = g + 8 < blk[i].n;
+#pragma unroll
+    for (int c = 0; c < DP / (4 * EL); ++c) {
+      const uint4 z = make_uint4(0, 0, 0, 0);
+      k.r[i][(c & 1) * 2][c >> 1] = in0 ? ldg16(p + c * 4 * EL) : z;
+      k.r[i][(c & 1) * 2 + 1][c >> 1] = in1 ? ldg16(p + 8 * row + c * 4 * EL) : z;
+    }
+  }
+}
+template <int DP, typename T, int NK>
+__device__ __forceinline__ void load_v(Tile<DP, T, NK>& v, const T* base, const Block (&blk)[NK],
+                                       int64_t row) {
+  constexpr int EL = 16 / (int)sizeof(T);
+  const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+#pragma unroll
+  for (int i = 0; i < NK; ++i)
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {
+      // the fragment's keys: 2t, 2t + 1, 2t + 8, 2t + 9 (bf16), t, t + 4, t + 8, t + 12 (fp32)
+      const int key = sizeof(T) == 2 ? 2 * t + (z & 1) + 8 * (z >> 1) : t + 4 * z;
+      const T* p = base + blk[i].off + key * row + g * EL;
+      const bool in = key < blk[i].n;
+#pragma unroll
+      for (int c = 0; c < DP / (8 * EL); ++c)
+        v.r[i][z][c] = in ? ldg16(p + c * 8 * EL) : make_uint4(0, 0, 0, 0);
+    }
+}
+
+// Tokens [0, n) of request b, units [t0, t1) of CTA tiles.
+template <int D, typename T>
+__device__ void piece(const AttnArgs& ar, char* smem, int64_t b, int n, int hk, int hg, int t0,
+                      int t1, Acc<D>& a, int* bad) {
+  constexpr int KT = Cfg<D, T>::kKeys, NK = KT / 16, EL = 16 / (int)sizeof(T);
+  constexpr int kRow = Smem<D, T>::kRow;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2;
+  const int heads = min(AT_G, ar.G - hg * AT_G);
+  // Q (the barrier in front: other warps may still read what was there)
+  __syncthreads();
+  const T* q = reinterpret_cast<const T*>(ar.q) + b * ar.qs + ((int64_t)hk * ar.G + hg * AT_G) * D;
+  for (int i = threadIdx.x; i < AT_G * D / EL; i += AT_NT) {
+    const int h = i / (D / EL), c = i % (D / EL);
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (h < heads) x = *reinterpret_cast<const uint4*>(q + (int64_t)h * D + c * EL);
+    char* dst = smem + h * kRow + c * 16;
+    if constexpr (sizeof(T) == 4) {
+      uint4 hi, lo;
+      split_tf32(x.x, &hi.x, &lo.x);
+      split_tf32(x.y, &hi.y, &lo.y);
+      split_tf32(x.z, &hi.z, &lo.z);
+      split_tf32(x.w, &hi.w, &lo.w);
+      *reinterpret_cast<uint4*>(dst) = hi;
+      *reinterpret_cast<uint4*>(dst + AT_G * kRow) = lo;
+    } else {
+      *reinterpret_cast<uint4*>(dst) = x;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) a.o[i][0] = a.o[i][1] = a.o[i][2] = a.o[i][3] = 0.f;
+  a.m[0] = a.m[1] = -INFINITY;
+  a.l[0] = a.l[1] = 0.f;
+
+  constexpr int kParts = Cfg<D, T>::kParts, DP = D / kParts;
+  const int64_t row = ar.Hk * D;  // elements between a page's rows
+  const T* kc = reinterpret_cast<const T*>(ar.kc) + (int64_t)hk * D;
+  const T* vc = reinterpret_cast<const T*>(ar.vc) + (int64_t)hk * D;
+  const int32_t* table = ar.table + b * ar.max_blocks;
+  const int pb = ar.P / 16, nb = (n - 1) / 16 + 1;  // 16-key blocks per page, and in all
+  auto page_of = [&](int tile, int i) {
+    const int blk = (tile * AT_W + warp) * NK + i;
+    return blk < nb && tile < t1 ? table[blk / pb] : -1;
+  };
+  auto place = [&](int tile, int i, int32_t page) {
+    const int blk = (tile * AT_W + warp) * NK + i;
+    Block x;
+    x.n = blk < nb && tile < t1 ? min(16, n - blk * 16) : 0;
+    if (x.n > 0 && (page < 0 || page >= ar.pages)) {
+      *bad = 1;
+      x.n = 0;
+    }
+    x.off = x.n > 0 ? ((int64_t)page * ar.P + (blk % pb) * 16) * row : 0;
+    return x;
+  };
+  Tile<DP, T, NK> k, v;
+  Block cur[NK];
+  int32_t page[NK];
+#pragma unroll
+  for (int i = 0; i < NK; ++i) cur[i] = place(t0, i, page_of(t0, i));
+  if constexpr (kParts == 1) {
+    load_k(k, kc, cur, row);
+    load_v(v, vc, cur, row);
+  }
+#pragma unroll
+  for (int i = 0; i < NK; ++i) page[i] = page_of(t0 + 1, i);
+  __syncthreads();  // Q is there
+#pragma unroll 1
+  for (int tile = t0; tile < t1; ++tile) {
+    Block nxt[NK];
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      nxt[i] = place(tile + 1, i, page[i]);
+      page[i] = page_of(tile + 2, i);
+    }
+    float s[NK][4] = {};
+#pragma unroll
+    for (int z = 0; z < kParts; ++z) {
+      if constexpr (kParts > 1) load_k(k, kc + z * DP, cur, row);
+      scores<D, DP, NK>(k, smem + z * DP * sizeof(T), s);
+    }
+    if constexpr (kParts == 1) load_k(k, kc, nxt, row);
+    float mx[2] = {a.m[0], a.m[1]};
+#pragma unroll
+    for (int i = 0; i < NK; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = g + 8 * (j >> 1) < cur[i].n ? s[i][j] * ar.sl : -INFINITY;
+        mx[j & 1] = fmaxf(mx[j & 1], s[i][j]);
+      }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], o));
+    if (__any_sync(0xffffffffu, mx[0] > a.m[0] || mx[1] > a.m[1])) {
+      float f[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        f[j] = ex2(a.m[j] - mx[j]);  // 0 from -inf; mx is finite or above m where it is used
+        if (mx[j] == a.m[j]) f[j] = 1.f;
+        a.l[j] *= f[j];
+        a.m[j] = mx[j];
+      }
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) a.o[i][j] *= f[j & 1];
+    }
+    const float base[2] = {a.m[0] == -INFINITY ? 0.f : a.m[0], a.m[1] == -INFINITY ? 0.f : a.m[1]};
+#pragma unroll
+    for (int i = 0; i < NK; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = ex2(s[i][j] - base[j & 1]);
+        a.l[j & 1] += s[i][j];
+      }
+#pragma unroll
+    for (int z = 0; z < kParts; ++z) {
+      if constexpr (kParts > 1) load_v(v, vc + z * DP, cur, row);
+      weigh<D, DP, NK>(v, s, a, z);
+    }
+    if constexpr (kParts == 1) load_v(v, vc, nxt, row);
+#pragma unroll
+    for (int i = 0; i < NK; ++i) cur[i] = nxt[i];
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) a.l[j] += __shfl_xor_sync(0xffffffffu, a.l[j], o);
+}
+
+// The 4 warps' results joined: to o and lse (slot < 0), or as the partial piece `slot`.
+template <int D, typename T>
+__device__ void finish(const AttnArgs& ar, char* smem, float2 (*ml)[AT_G], int64_t b, int h0,
+                       int heads, const Acc<D>& a, int64_t slot) {
+  constexpr int kORow = Smem<D, T>::kORow, EL = 16 / (int)sizeof(T);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  __syncthreads();  // every warp is done with Q
+  float* so = reinterpret_cast<float*>(smem);
+  if (g == 0) {
+    ml[warp][2 * t] = make_float2(a.m[0], a.l[0]);
+    ml[warp][2 * t + 1] = make_float2(a.m[1], a.l[1]);
+  }
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) {
+    const int d = EL * (g + 8 * (i / (EL / 2))) + 2 * (i % (EL / 2));
+    *reinterpret_cast<float2*>(so + (warp * AT_G + 2 * t) * kORow + d) =
+        make_float2(a.o[i][0], a.o[i][2]);
+    *reinterpret_cast<float2*>(so + (warp * AT_G + 2 * t + 1) * kORow + d) =
+        make_float2(a.o[i][1], a.o[i][3]);
+  }
+  __syncthreads();
+  for (int x = threadIdx.x; x < heads * (D / 2); x += AT_NT) {
+    const int h = x / (D / 2), d = (x % (D / 2)) * 2;
+    float m = -INFINITY, l = 0.f;
+    float2 o = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < AT_W; ++w) m = fmaxf(m, ml[w][h].x);
+    const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int w = 0; w < AT_W; ++w) {
+      const float f = ex2(ml[w][h].x - base);
+      const float2 y = *reinterpret_cast<const float2*>(so + (w * AT_G + h) * kORow + d);
+      l = fmaf(ml[w][h].y, f, l);
+      o.x = fmaf(y.x, f, o.x);
+      o.y = fmaf(y.y, f, o.y);
+    }
+    if (slot >= 0) {
+      *reinterpret_cast<float2*>(ar.acc + (slot * AT_G + h) * D + d) = o;
+      if (d == 0) ar.ml[slot * AT_G + h] = make_float2(m, l);
       continue;
     }
-    const int64_t off = ((page * ar.P + t % ar.P) * ar.Hk + hk) * D;
-    const T* kp = reinterpret_cast<const T*>(ar.kc) + off;
-    const T* vp = reinterpret_cast<const T*>(ar.vc) + off;
-    float s = 0.f;
-#pragma unroll
-    for (int j = 0; j < E; ++j) s = fmaf(q[j], (float)kp[j * 32 + lane], s);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float mn = fmaxf(m, s), base = mn == -INFINITY ? 0.f : mn;
-    const float f = expf(m - base), p = expf(s - base);
-    m = mn;
-    l = l * f + p;
-#pragma unroll
-    for (int j = 0; j < E; ++j) acc[j] = acc[j] * f + p * (float)vp[j * 32 + lane];
+    const float r = l != 0.f ? 1.f / l : 0.f;  // nothing counted: zero, not 0 / 0
+    T* out = reinterpret_cast<T*>(ar.o) + (b * ar.Hq + h0 + h) * D + d;
+    if constexpr (sizeof(T) == 2)
+      *reinterpret_cast<__nv_bfloat162*>(out) = __floats2bfloat162_rn(o.x * r, o.y * r);
+    else
+      *reinterpret_cast<float2*>(out) = make_float2(o.x * r, o.y * r);
+    if (d == 0 && ar.lse)
+      ar.lse[b * ar.Hq + h0 + h] = (base + log2f(l)) * 0.69314718055994531f;
   }
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
+}
+
+__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* part, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-  for (int j = 0; j < E; ++j) s_o[warp][j * 32 + lane] = acc[j];
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
   __syncthreads();
-  float M = -INFINITY, L = 0.f;
-  for (int w = 0; w < W; ++w) M = fmaxf(M, s_m[w]);
-  const float base = M == -INFINITY ? 0.f : M;
-  for (int w = 0; w < W; ++w) L += s_l[w] * expf(s_m[w] - base);
-  for (int e = threadIdx.x; e < D; e += AT_NT) {
-    float x = 0.f;
-    for (int w = 0; w < W; ++w) x += s_o[w][e] * expf(s_m[w] - base);
-    reinterpret_cast<T*>(ar.o)[(b * ar.Hq + h) * D + e] = (T)(L > 0.f ? x / L : x);
+  if (lane == 31) part[warp] = x;
+  __syncthreads();
+  int64_t sum = 0;
+#pragma unroll
+  for (int w = 0; w < AT_W; ++w) {
+    if (w < warp) x += part[w];
+    sum += part[w];
   }
-  if (threadIdx.x == 0 && ar.lse) ar.lse[b * ar.Hq + h] = base + logf(L);
+  *total = sum;
+  return x;  // inclusive
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(AT_NT, Cfg<D, T>::kCtas) k_attn_decode(AttnArgs ar) {
+  extern __shared__ __align__(16) char smem[];
+  __shared__ int64_t part[AT_W];
+  __shared__ float2 ml[AT_W][AT_G];
+  __shared__ int64_t s_b, s_r;
+  constexpr int TK = Cfg<D, T>::kKeys * AT_W;  // keys per unit
+  const int tid = threadIdx.x;
+  const int64_t c = blockIdx.x, cap = ar.max_blocks * ar.P, per = ar.Hk * ar.HG;
+  asm volatile("griddepcontrol.launch_dependents;");
+  int bad = 0;
+  auto length = [&](int64_t b) {
+    const int32_t n = ar.len[b];
+    return (int)(n < 0 ? 0 : n > cap ? cap : n);
+  };
+  auto tiles = [&](int n) { return n > 0 ? (n - 1) / TK + 1 : 0; };
+  auto units = [&](int64_t b) { return tiles(length(b)) * per; };
+  // the units of all requests, and this CTA's share of them
+  int64_t W = 0, first = 0;
+  for (int64_t b0 = 0; b0 < ar.B; b0 += AT_NT) {
+    int64_t sum;
+    const int64_t b = b0 + tid;
+    first = block_scan(b < ar.B ? units(b) : 0, part, &sum);
+    if (c == 0 && b < ar.B && length(b) != ar.len[b]) bad = 1;
+    W += sum;
+  }
+  const int64_t C = W < gridDim.x ? W : gridDim.x;
+  const int64_t u0 = c < C ? W * c / C : 0, u1 = c < C ? W * (c + 1) / C : 0;
+  // requests without tokens
+  for (int64_t b = c; b < ar.B; b += gridDim.x)
+    if (length(b) == 0) {
+      T* o = reinterpret_cast<T*>(ar.o) + b * ar.Hq * D;
+      for (int64_t i = tid; i < ar.Hq * D; i += AT_NT) o[i] = (T)0.f;
+      if (ar.lse)
+        for (int64_t i = tid; i < ar.Hq; i += AT_NT) ar.lse[b * ar.Hq + i] = -INFINITY;
+    }
+  if (tid == 0) ar.join[c] = Join{0, -1, 0, 0};
+  if (u0 < u1) {
+    // the request that unit u0 falls in
+    int64_t done = 0;
+    for (int64_t b0 = 0; b0 < ar.B && done <= u0; b0 += AT_NT) {
+      int64_t sum;
+      const int64_t b = b0 + tid, n = b < ar.B ? units(b) : 0;
+      if (ar.B > AT_NT) first = block_scan(n, part, &sum);
+      else sum = W;
+      if (u0 >= done + first - n && u0 < done + first) {
+        s_b = b;
+        s_r = u0 - (done + first - n);
+      }
+      done += sum;
+    }
+    __syncthreads();
+    int64_t b = s_b, u = u0;
+    int n = length(b), nt = tiles(n);
+    int h = (int)(s_r / nt), t0 = (int)(s_r % nt);  // piece of the request, unit in it
+    while (u < u1) {
+      const int t1 = (int)(u1 - u < nt - t0 ? t0 + (u1 - u) : nt);
+      const int hk = h / ar.HG, hg = h % ar.HG, heads = min(AT_G, ar.G - hg * AT_G);
+      const int h0 = hk * ar.G + hg * AT_G;
+      Acc<D> a;
+      piece<D, T>(ar, smem, b, n, hk, hg, t0, t1, a, &bad);
+      const int64_t slot = t0 == 0 && t1 == nt ? -1 : t0 == 0 ? 2 * c + 1 : 2 * c;
+      finish<D, T>(ar, smem, ml, b, h0, heads, a, slot);
+      if (t0 == 0 && t1 < nt && tid == 0) {
+        const int64_t end = u + nt - 1;  // its last unit: the CTA with W c / C <= end
+        ar.join[c] = Join{(int32_t)b, h0, heads, (int32_t)(((end + 1) * C - 1) / W)};
+      }
+      u += t1 - t0;
+      t0 = 0;
+      if (u < u1 && ++h == per) {
+        h = 0;
+        do n = length(++b); while (n == 0);
+        nt = tiles(n);
+      }
+    }
+  }
   if (bad && ar.status) atomicOr(ar.status, kStatusClamped);
+}
+
+// Adds up the partial pieces of one (request, key head): CTA (c, h) for the piece that began in
+// CTA c of the pass above, query head h of it.  4 groups of D threads take every fourth part.
+template <int D, typename T>
+__global__ void __launch_bounds__(4 * D) k_attn_join(AttnArgs ar) {
+  __shared__ float s_o[4][D], s_m[4], s_l[4];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t c = blockIdx.x;
+  const int h = blockIdx.y, d = threadIdx.x % D, w = threadIdx.x / D;
+  const Join j = ar.join[c];
+  if (j.h < 0 || h >= j.heads) return;
+  const int n = (int)(j.last - c) + 1;  // parts: slot 2c + 1, then slot 2i of the CTAs behind
+  auto slot = [&](int i) { return (i == 0 ? 2 * c + 1 : 2 * (c + i)) * AT_G + h; };
+  float m = -INFINITY, l = 0.f, o = 0.f;
+  for (int i = w; i < n; i += 4) m = fmaxf(m, ar.ml[slot(i)].x);
+  if (d == 0) s_m[w] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+  const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll 4
+  for (int i = w; i < n; i += 4) {
+    const float2 x = ar.ml[slot(i)];
+    const float f = ex2(x.x - base);
+    l = fmaf(x.y, f, l);
+    o = fmaf(ar.acc[slot(i) * D + d], f, o);
+  }
+  s_o[w][d] = o;
+  if (d == 0) s_l[w] = l;
+  __syncthreads();
+  if (w > 0) return;
+  o = (s_o[0][d] + s_o[1][d]) + (s_o[2][d] + s_o[3][d]);
+  l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+  const float r = l != 0.f ? 1.f / l : 0.f;
+  const int64_t row = (int64_t)j.b * ar.Hq + j.h + h;
+  reinterpret_cast<T*>(ar.o)[row * D + d] = (T)(o * r);
+  if (d == 0 && ar.lse) ar.lse[row] = (base + log2f(l)) * 0.69314718055994531f;
 }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
@@ -102,13 +630,57 @@ gdn_status check_problem(const gdn_attn_problem* p) {
   return GDN_OK;
 }
 
-template <typename T>
-cudaError_t launch(const AttnArgs& ar, int D, cudaStream_t st) {
-  const unsigned ctas = (unsigned)(ar.B * ar.Hq);
-  if (D == 64) k_attn_decode<64, T><<<ctas, AT_NT, 0, st>>>(ar);
-  else if (D == 128) k_attn_decode<128, T><<<ctas, AT_NT, 0, st>>>(ar);
-  else k_attn_decode<256, T><<<ctas, AT_NT, 0, st>>>(ar);
-  return cudaGetLastError();
+// CTAs of the pass and the workspace's parts (a fixed count per D and type, so that results do
+// not depend on the device).
+struct Plan {
+  int ctas;
+  size_t join, ml, acc, total;
+};
+template <int D, typename T>
+Plan plan_of() {
+  Plan pl;
+  pl.ctas = AT_SMS * Cfg<D, T>::kCtas;
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  pl.join = 0;
+  pl.ml = up(pl.ctas * sizeof(Join));
+  pl.acc = pl.ml + up((size_t)pl.ctas * 2 * AT_G * sizeof(float2));
+  pl.total = pl.acc + (size_t)pl.ctas * 2 * AT_G * D * sizeof(float);
+  return pl;
+}
+
+// Runs f with the call's head dim and type as template arguments.
+template <typename F>
+auto with_types(const gdn_attn_problem* p, F f) {
+  using D64 = std::integral_constant<int, 64>;
+  using D128 = std::integral_constant<int, 128>;
+  using D256 = std::integral_constant<int, 256>;
+  if (p->dtype == GDN_BF16) {
+    const __nv_bfloat16 t{};
+    return p->D == 64 ? f(D64(), t) : p->D == 128 ? f(D128(), t) : f(D256(), t);
+  }
+  return p->D == 64 ? f(D64(), 0.f) : p->D == 128 ? f(D128(), 0.f) : f(D256(), 0.f);
+}
+
+template <int D, typename T>
+cudaError_t launch(AttnArgs ar, char* ws, cudaStream_t st) {
+  const Plan pl = plan_of<D, T>();
+  ar.join = (Join*)(ws + pl.join);
+  ar.ml = (float2*)(ws + pl.ml);
+  ar.acc = (float*)(ws + pl.acc);
+  k_attn_decode<D, T><<<pl.ctas, AT_NT, Smem<D, T>::kBytes, st>>>(ar);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // the join starts as the pass's CTAs leave and waits for its end on the device
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(pl.ctas, ar.G < AT_G ? ar.G : AT_G);
+  cfg.blockDim = dim3(4 * D);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_attn_join<D, T>, ar);
 }
 
 }  // namespace
@@ -122,7 +694,7 @@ gdn_status gdn_attn_decode_workspace_size(const gdn_attn_problem* p, size_t* byt
   if (!bytes) return GDN_ERR_INVALID_ARG;
   gdn_status s = check_problem(p);
   if (s != GDN_OK) return s;
-  *bytes = 256;
+  *bytes = with_types(p, [](auto d, auto t) { return plan_of<d(), decltype(t)>().total; });
   return GDN_OK;
 }
 
@@ -149,7 +721,9 @@ gdn_status gdn_attn_decode(const gdn_attn_problem* p, const void* q, const void*
   ar.max_blocks = p->max_blocks;
   ar.qs = p->q_stride ? p->q_stride : p->Hq * p->D;
   ar.P = p->page_size;
-  ar.scale = p->scale > 0.f ? p->scale : 1.0f / sqrtf((float)p->D);
+  ar.G = (int)(p->Hq / p->Hk);
+  ar.HG = (ar.G + AT_G - 1) / AT_G;
+  ar.sl = (p->scale > 0.f ? p->scale : 1.0f / sqrtf((float)p->D)) * 1.4426950408889634f;
   ar.q = q;
   ar.kc = k_cache;
   ar.vc = v_cache;
@@ -159,8 +733,9 @@ gdn_status gdn_attn_decode(const gdn_attn_problem* p, const void* q, const void*
   ar.lse = lse;
   ar.status = status;
   cudaStream_t st = (cudaStream_t)stream;
-  const cudaError_t e = p->dtype == GDN_BF16 ? launch<__nv_bfloat16>(ar, p->D, st)
-                                             : launch<float>(ar, p->D, st);
+  const cudaError_t e = with_types(p, [&](auto d, auto t) {
+    return launch<d(), decltype(t)>(ar, (char*)workspace, st);
+  });
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
