@@ -530,7 +530,8 @@ gdn_status gdn_rmsnorm_gated_bwd(const gdn_rmsnorm_problem* p, const void* o, co
  * it), is recorded in `status` and treated as -1.  fp32 arithmetic for both dtypes.  One
  * launch, no workspace.
  * Errors: those of gdn_query_support; p->T != 1, n_slots < 0, null slots with n_slots < B, a
- * null or misaligned pointer: GDN_ERR_INVALID_ARG; n_slots >= 2^31: GDN_ERR_UNSUPPORTED.
+ * null or misaligned pointer: GDN_ERR_INVALID_ARG; n_slots >= 2^31 or B H >= 2^29:
+ * GDN_ERR_UNSUPPORTED.
  */
 gdn_status gdn_step(const gdn_problem* p, int64_t n_slots, const int32_t* slots, const void* q,
                     const void* k, const void* v, const void* a, const void* b,
