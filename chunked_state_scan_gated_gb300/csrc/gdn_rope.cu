@@ -6,6 +6,14 @@
 //   dx = r (g - x r mean(g x r)),  dw = sum over rows of dn x r.
 // The angle is formed in revolutions: t * (inv_freq / 2 pi) as an exact two-term product, its
 // integer part dropped, so positions past 2^20 lose nothing (angle()).
+//
+// Bound by HBM (2 row accesses forward, 3 backward).  A warp takes one token and a run of its
+// heads: the token's R/2 angles are computed once, into the warp's own shared memory (no CTA
+// barrier), and serve all its heads.  A row is held 8 elements per lane (16 bytes of bf16) by
+// LPR = 8, 16 or 32 lanes, so a warp holds 32 / LPR heads at a time, and the loads of RO_UNR such
+// groups are issued together.  The halves of a rotated head meet through shuffles.  With many
+// tokens a warp takes all heads of its token; with few (decode) as few as one group, which
+// repeats the angles but spreads a token over many SMs.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <string.h>
@@ -19,12 +27,16 @@ namespace {
 using namespace vec;
 
 constexpr int RO_NT = 256;     // 8 warps
-constexpr int RO_BCTAS = 608;  // CTAs of the backward at most (4 per SM of a 152-SM GPU)
+constexpr int RO_W = RO_NT / 32;
+constexpr int RO_UNR = 4;      // head groups whose loads are issued together
+constexpr int RO_BCTAS = 304;  // CTAs of the backward at most (2 per SM of a 152-SM GPU)
 constexpr int RO_MAXD = 256;   // 8 elements per lane
+constexpr int RO_FILL = 152 * 16;  // warps that keep the GPU busy
 
 struct RopeArgs {
   int64_t N, T, qs, ks, vs, n_slots;
   int Hq, Hk, D, R, inter;
+  int heads, chunk, chunks;     // rows of a token, rows per warp (in heads), warps per token
   float eps, rscale;
   const void *q, *k, *v;
   const float *wq, *wk, *inv_freq;
@@ -36,14 +48,7 @@ struct RopeArgs {
   int32_t* status;
 };
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-template <typename T>
-__device__ __forceinline__ void ld8(const T* p, float (&v)[8]) {
+__device__ __forceinline__ void ld8(const float* p, float (&v)[8]) {
   float a[4], b[4];
   ld4(p, a);
   ld4(p + 4, b);
@@ -53,18 +58,6 @@ __device__ __forceinline__ void ld8(const T* p, float (&v)[8]) {
     v[j + 4] = b[j];
   }
 }
-template <typename T>
-__device__ __forceinline__ void st8(T* p, const float (&v)[8]) {
-  float a[4], b[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    a[j] = v[j];
-    b[j] = v[j + 4];
-  }
-  st4(p, a);
-  st4(p + 4, b);
-}
-
 // cos and sin of t * f, t any int32, f fp32.  In revolutions u = t f / (2 pi), with
 // 1/(2 pi) as the sum of two fp32 numbers: t is split into two parts that are exact in fp32
 // and f / (2 pi) into hi + lo, the product with hi is exact as value and remainder of an
@@ -86,134 +79,271 @@ __device__ __forceinline__ void angle(int32_t t, float f, float* c, float* s) {
   sincospif(2.f * u, s, c);
 }
 
-// The rotation of a row held 8 elements per lane (element 8 lane + j); sgn = -1 transposes.
-__device__ __forceinline__ void rotate(const RopeArgs& ar, int32_t t, float sgn, float (&n)[8]) {
-  const int lane = threadIdx.x & 31, e = lane * 8;
+// A row's 8 elements of one lane, as loaded.
+template <typename T> struct Raw;
+template <> struct Raw<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    u = __ldcs(reinterpret_cast<const uint4*>(p));
+  }
+  __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+  }
+};
+template <> struct Raw<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldcs(reinterpret_cast<const float4*>(p));
+    b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
+__device__ __forceinline__ void put(float* p, const float (&v)[8]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *(reinterpret_cast<float4*>(p) + 1) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void put(__nv_bfloat16* p, const float (&v)[8]) {
+  uint4 u;
+  uint32_t* w = &u.x;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+    w[j] = *reinterpret_cast<const uint32_t*>(&x);
+  }
+  *reinterpret_cast<uint4*>(p) = u;
+}
+
+// sum over the LPR lanes of a row
+template <int LPR>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// cos and sin of the token's angles into the warp's cs[0 .. R/2) and cs[128 ..)
+__device__ __forceinline__ void angles(const RopeArgs& ar, int64_t n, float* cs) {
+  const int lane = threadIdx.x & 31;
+  const int32_t t = ar.pos ? ar.pos[n] : (int32_t)(n % ar.T);
+  __syncwarp();  // the last token's readers are done
+  for (int i = lane; i < ar.R / 2; i += 32) {
+    float c, s;
+    angle(t, ar.inv_freq[i], &c, &s);
+    cs[i] = c * ar.rscale;
+    cs[RO_MAXD / 2 + i] = s * ar.rscale;
+  }
+  __syncwarp();
+}
+
+// The rotation of a row held 8 elements per lane (element 8 l + j, l the lane in the row);
+// sgn = -1 transposes.
+template <int LPR>
+__device__ __forceinline__ void rotate(const RopeArgs& ar, const float* cs, float sgn,
+                                       float (&n)[8]) {
+  const int l = threadIdx.x & (LPR - 1), e = l * 8;
   if (ar.inter) {
-    if (e < ar.R)
+    if (e < ar.R) {
+      const float4 c = *reinterpret_cast<const float4*>(cs + e / 2);
+      const float4 s = *reinterpret_cast<const float4*>(cs + RO_MAXD / 2 + e / 2);
+      const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        float c, s;
-        angle(t, ar.inv_freq[e / 2 + j], &c, &s);
-        c *= ar.rscale;
-        s *= sgn * ar.rscale;
-        const float a = n[2 * j], b = n[2 * j + 1];
-        n[2 * j] = a * c - b * s;
-        n[2 * j + 1] = b * c + a * s;
+        const float a = n[2 * j], b = n[2 * j + 1], sj = sgn * ss[j];
+        n[2 * j] = a * cc[j] - b * sj;
+        n[2 * j + 1] = b * cc[j] + a * sj;
       }
+    }
     return;
   }
   const int half = ar.R / 16;  // lanes per half
-  const bool first = lane < half;
-  const int other = first ? lane + half : lane - half;
+  const bool first = l < half;
+  const int other = first ? l + half : l - half;
+  const float sg = first ? -sgn : sgn;
+  const float* at = cs + (first ? e : e - ar.R / 2);
+  const bool in = e < ar.R;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float m = __shfl_sync(0xffffffffu, n[j], other & 31);
-    if (e < ar.R) {
-      float c, s;
-      angle(t, ar.inv_freq[(first ? e : e - ar.R / 2) + j], &c, &s);
-      c *= ar.rscale;
-      s *= sgn * ar.rscale;
-      n[j] = first ? n[j] * c - m * s : n[j] * c + m * s;
+  for (int z = 0; z < 2; ++z) {
+    float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (in) {
+      c = *reinterpret_cast<const float4*>(at + 4 * z);
+      s = *reinterpret_cast<const float4*>(at + RO_MAXD / 2 + 4 * z);
+    }
+    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float m = __shfl_sync(0xffffffffu, n[4 * z + j], other, LPR);
+      if (in) n[4 * z + j] = n[4 * z + j] * cc[j] + m * (sg * ss[j]);
     }
   }
 }
 
-// Mode 0: outputs; mode 1: k and v rows into the caches
-template <int Mode, typename T>
+// One head row: its input, output and kind.
+struct Row {
+  int kind;  // 0 query, 1 key, 2 value (cache form), -1 none
+  int h;     // head of its kind
+};
+__device__ __forceinline__ Row row_of(const RopeArgs& ar, int h, int end) {
+  if (h >= end) return Row{-1, 0};
+  if (h < ar.Hq) return Row{0, h};
+  if (h < ar.Hq + ar.Hk) return Row{1, h - ar.Hq};
+  return Row{2, h - ar.Hq - ar.Hk};
+}
+
+// CACHE: k and v rows go to the caches
+template <bool CACHE, int LPR, typename T>
 __global__ void __launch_bounds__(RO_NT) k_qk_norm_rope_fwd(RopeArgs ar) {
-  const int lane = threadIdx.x & 31, e = lane * 8;
-  const int H = ar.Hq + ar.Hk;
-  const int64_t row = (int64_t)blockIdx.x * (RO_NT / 32) + (threadIdx.x >> 5);
-  if (row >= ar.N * H) return;
-  const int64_t n = row / H;
-  const int h = (int)(row % H);
-  const bool isq = h < ar.Hq, in = e < ar.D;
-  const int hk = h - ar.Hq;
+  __shared__ __align__(16) float s_cs[RO_W][RO_MAXD];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LPR;
+  const int e = (lane & (LPR - 1)) * 8;
+  constexpr int RPL = 32 / LPR;
+  const int64_t task = (int64_t)blockIdx.x * RO_W + warp;
+  if (task >= ar.N * ar.chunks) return;
+  const int64_t n = task / ar.chunks;
+  const int h0 = (int)(task % ar.chunks) * ar.chunk;
+  const int end = min(h0 + ar.chunk, ar.heads);
+  const bool in = e < ar.D;
   int64_t dst = n;
-  if (Mode == 1 && !isq) {
+  if (CACHE) {
     dst = ar.slots[n];
     if (dst < 0 || dst >= ar.n_slots) {
-      if (dst != -1 && lane == 0 && hk == 0 && ar.status) atomicOr(ar.status, kStatusClamped);
-      return;
+      if (dst != -1 && lane == 0 && h0 == 0 && ar.status) atomicOr(ar.status, kStatusClamped);
+      dst = -1;
     }
   }
-  const T* x = isq ? reinterpret_cast<const T*>(ar.q) + n * ar.qs + (int64_t)h * ar.D
-                   : reinterpret_cast<const T*>(ar.k) + n * ar.ks + (int64_t)hk * ar.D;
-  float v[8] = {}, w[8] = {};
-  if (in) {
-    ld8(x + e, v);
-    ld8((isq ? ar.wq : ar.wk) + e, w);
-  }
-  float ss = 0.f;
+  const T* src[3] = {reinterpret_cast<const T*>(ar.q) + n * ar.qs + e,
+                     reinterpret_cast<const T*>(ar.k) + n * ar.ks + e,
+                     reinterpret_cast<const T*>(ar.v) + n * ar.vs + e};
+  bool have = false;
+  for (int hb = h0; hb < end; hb += RO_UNR * RPL) {
+    Raw<T> raw[RO_UNR];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
-  const float r = rsqrtf(warp_sum(ss) / (float)ar.D + ar.eps);
+    for (int u = 0; u < RO_UNR; ++u) {
+      const Row r = row_of(ar, hb + u * RPL + sub, end);
+      raw[u].zero();
+      if (r.kind >= 0 && in)
+        raw[u].load((r.kind == 0 ? src[0] : r.kind == 1 ? src[1] : src[2]) + (int64_t)r.h * ar.D);
+    }
+    if (!have) angles(ar, n, s_cs[warp]);  // under the first loads
+    have = true;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] *= r * w[j];
-  rotate(ar, ar.pos ? ar.pos[n] : (int32_t)(n % ar.T), 1.f, v);
-  T* y = isq ? reinterpret_cast<T*>(ar.q_out) + (n * ar.Hq + h) * ar.D
-             : reinterpret_cast<T*>(ar.k_out) + (dst * ar.Hk + hk) * ar.D;
-  if (in) st8(y + e, v);
-  if (Mode == 1 && !isq && in) {
-    ld8(reinterpret_cast<const T*>(ar.v) + n * ar.vs + (int64_t)hk * ar.D + e, v);
-    st8(reinterpret_cast<T*>(ar.v_out) + (dst * ar.Hk + hk) * ar.D + e, v);
+    for (int u = 0; u < RO_UNR; ++u) {
+      if (hb + u * RPL >= end) break;
+      const Row r = row_of(ar, hb + u * RPL + sub, end);
+      float v[8], w[8] = {};
+      raw[u].get(v);
+      float ss = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
+      const float f = rsqrtf(row_sum<LPR>(ss) / (float)ar.D + ar.eps);
+      if (in && r.kind >= 0 && r.kind < 2) ld8((r.kind == 0 ? ar.wq : ar.wk) + e, w);
+      float y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = v[j] * (f * w[j]);
+      rotate<LPR>(ar, s_cs[warp], 1.f, y);
+      if (r.kind < 0 || !in || (CACHE && r.kind > 0 && dst < 0)) continue;
+      const int64_t at = (r.kind == 0 ? n * ar.Hq : dst * ar.Hk) + r.h;
+      T* out = reinterpret_cast<T*>(r.kind == 0 ? ar.q_out : r.kind == 1 ? ar.k_out : ar.v_out);
+      if (CACHE && r.kind == 2) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = v[j];
+      }
+      put(out + at * ar.D + e, y);
+    }
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(RO_NT) k_qk_norm_rope_bwd(RopeArgs ar) {
-  __shared__ float red[RO_NT / 32][RO_MAXD];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = lane * 8;
-  const int H = ar.Hq + ar.Hk;
+// Persistent: a warp takes tasks in a fixed stride and keeps its lanes' dwq, dwk in registers.
+template <int LPR, typename T>
+__global__ void __launch_bounds__(RO_NT, 2) k_qk_norm_rope_bwd(RopeArgs ar) {
+  __shared__ __align__(16) float s_cs[RO_W][RO_MAXD];
+  __shared__ float red[RO_W][RO_MAXD];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LPR;
+  const int e = (lane & (LPR - 1)) * 8;
+  constexpr int RPL = 32 / LPR, UNR = sizeof(T) == 2 ? RO_UNR : RO_UNR / 2;
   const bool in = e < ar.D;
-  float dw[2][8] = {}, wq[8] = {}, wk[8] = {};
-  if (in) {
-    if (ar.Hq) ld8(ar.wq + e, wq);
-    if (ar.Hk) ld8(ar.wk + e, wk);
-  }
-  for (int64_t row = (int64_t)blockIdx.x * (RO_NT / 32) + warp; row < ar.N * H;
-       row += (int64_t)gridDim.x * (RO_NT / 32)) {
-    const int64_t n = row / H;
-    const int h = (int)(row % H);
-    const bool isq = h < ar.Hq;
-    const int hk = h - ar.Hq;
-    const int64_t src = isq ? n * ar.qs + (int64_t)h * ar.D : n * ar.ks + (int64_t)hk * ar.D;
-    const int64_t out = isq ? (n * ar.Hq + h) * ar.D : (n * ar.Hk + hk) * ar.D;
-    float x[8] = {}, g[8] = {};
-    if (in) {
-      ld8(reinterpret_cast<const T*>(isq ? ar.q : ar.k) + src + e, x);
-      ld8(reinterpret_cast<const T*>(isq ? ar.dq_out : ar.dk_out) + out + e, g);
+  float dw[2][8] = {};
+  for (int64_t task = (int64_t)blockIdx.x * RO_W + warp; task < ar.N * ar.chunks;
+       task += (int64_t)gridDim.x * RO_W) {
+    const int64_t n = task / ar.chunks;
+    const int h0 = (int)(task % ar.chunks) * ar.chunk;
+    const int end = min(h0 + ar.chunk, ar.heads);
+    bool have = false;
+    for (int hb = h0; hb < end; hb += UNR * RPL) {
+      Raw<T> rx[UNR], rg[UNR];
+#pragma unroll
+      for (int u = 0; u < UNR; ++u) {
+        const Row r = row_of(ar, hb + u * RPL + sub, end);
+        rx[u].zero();
+        rg[u].zero();
+        if (r.kind >= 0 && in) {
+          const bool isq = r.kind == 0;
+          const int64_t hd = (int64_t)r.h * ar.D + e;
+          rx[u].load(reinterpret_cast<const T*>(isq ? ar.q : ar.k) + n * (isq ? ar.qs : ar.ks) +
+                     hd);
+          rg[u].load(reinterpret_cast<const T*>(isq ? ar.dq_out : ar.dk_out) +
+                     n * (isq ? ar.Hq : ar.Hk) * ar.D + hd);
+        }
+      }
+      if (!have) angles(ar, n, s_cs[warp]);
+      have = true;
+#pragma unroll
+      for (int u = 0; u < UNR; ++u) {
+        if (hb + u * RPL >= end) break;
+        const Row r = row_of(ar, hb + u * RPL + sub, end);
+        const bool isq = r.kind == 0;
+        float x[8], g[8], w[8] = {};
+        rx[u].get(x);
+        rg[u].get(g);
+        rotate<LPR>(ar, s_cs[warp], -1.f, g);
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+        const float f = rsqrtf(row_sum<LPR>(ss) / (float)ar.D + ar.eps);
+        if (in && r.kind >= 0) ld8((isq ? ar.wq : ar.wk) + e, w);
+        float dot = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          x[j] *= f;
+          const float d = g[j] * x[j];
+          dw[0][j] += isq ? d : 0.f;
+          dw[1][j] += isq ? 0.f : d;  // absent rows hold zeros
+          g[j] *= w[j];
+          dot = fmaf(g[j], x[j], dot);
+        }
+        const float m = row_sum<LPR>(dot) / (float)ar.D;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] = f * (g[j] - x[j] * m);
+        if (r.kind >= 0 && in)
+          put(reinterpret_cast<T*>(isq ? ar.q_out : ar.k_out) +
+                  (n * (isq ? ar.Hq : ar.Hk) + r.h) * ar.D + e,
+              g);
+      }
     }
-    rotate(ar, ar.pos ? ar.pos[n] : (int32_t)(n % ar.T), -1.f, g);
-    float ss = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-    const float r = rsqrtf(warp_sum(ss) / (float)ar.D + ar.eps);
-    float dot = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      x[j] *= r;
-      const float d = g[j] * x[j];
-      if (isq) dw[0][j] += d; else dw[1][j] += d;
-      g[j] *= isq ? wq[j] : wk[j];
-      dot = fmaf(g[j], x[j], dot);
-    }
-    const float m = warp_sum(dot) / (float)ar.D;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) g[j] = r * (g[j] - x[j] * m);
-    if (in) st8(reinterpret_cast<T*>(isq ? ar.q_out : ar.k_out) + out + e, g);
   }
-  for (int z = 0; z < 2; ++z) {  // this CTA's dwq, dwk: its 8 warps added in order
+  for (int z = 0; z < 2; ++z) {  // this CTA's dwq, dwk: lanes of equal elements, then warps in order
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+      for (int o = LPR; o < 32; o <<= 1) dw[z][j] += __shfl_xor_sync(0xffffffffu, dw[z][j], o);
     __syncthreads();
-    if (in)
+    if (in && sub == 0)
 #pragma unroll
       for (int j = 0; j < 8; ++j) red[warp][e + j] = dw[z][j];
     __syncthreads();
     for (int c = threadIdx.x; c < ar.D; c += RO_NT) {
       float s = 0.f;
 #pragma unroll
-      for (int w = 0; w < RO_NT / 32; ++w) s += red[w][c];
+      for (int w = 0; w < RO_W; ++w) s += red[w][c];
       ar.part[((int64_t)blockIdx.x * 2 + z) * ar.D + c] = s;
     }
   }
@@ -285,20 +415,43 @@ bool inputs_ok(const RopeArgs& ar, const void* q, const void* k, const float* wq
          ok16(inv_freq, ar.R) && ok4(pos);
 }
 
+// Splits the heads of a token over warps: all of them to one warp when the tokens alone fill
+// the GPU, else runs of whole load groups.
+void split_heads(RopeArgs* ar, int heads) {
+  const int rpl = ar->D > 128 ? 1 : ar->D > 64 ? 2 : 4, group = rpl;
+  ar->heads = heads;
+  int64_t warps = ar->N > 0 ? (RO_FILL + ar->N - 1) / ar->N : 1;  // wanted per token
+  const int64_t most = (heads + group - 1) / group;
+  if (warps > most) warps = most;
+  if (warps < 1) warps = 1;
+  const int64_t chunk = (heads + warps - 1) / warps;
+  ar->chunk = (int)((chunk + group - 1) / group * group);
+  ar->chunks = (heads + ar->chunk - 1) / ar->chunk;
+}
+
 int64_t bwd_ctas(const RopeArgs& ar) {
-  const int64_t n = (ar.N * (ar.Hq + ar.Hk) + RO_NT / 32 - 1) / (RO_NT / 32);
+  const int64_t n = (ar.N * ar.chunks + RO_W - 1) / RO_W;
   return n < RO_BCTAS ? n : RO_BCTAS;
 }
 
-template <int Mode>
+template <bool CACHE, typename T>
+void launch_fwd_t(const RopeArgs& ar, cudaStream_t st) {
+  const unsigned ctas = (unsigned)((ar.N * ar.chunks + RO_W - 1) / RO_W);
+  if (ar.D <= 64) k_qk_norm_rope_fwd<CACHE, 8, T><<<ctas, RO_NT, 0, st>>>(ar);
+  else if (ar.D <= 128) k_qk_norm_rope_fwd<CACHE, 16, T><<<ctas, RO_NT, 0, st>>>(ar);
+  else k_qk_norm_rope_fwd<CACHE, 32, T><<<ctas, RO_NT, 0, st>>>(ar);
+}
+template <bool CACHE>
 gdn_status launch_fwd(const RopeArgs& ar, int dtype, cudaStream_t st) {
-  const int64_t rows = ar.N * (ar.Hq + ar.Hk);
-  const unsigned ctas = (unsigned)((rows + RO_NT / 32 - 1) / (RO_NT / 32));
-  if (dtype == GDN_BF16)
-    k_qk_norm_rope_fwd<Mode, __nv_bfloat16><<<ctas, RO_NT, 0, st>>>(ar);
-  else
-    k_qk_norm_rope_fwd<Mode, float><<<ctas, RO_NT, 0, st>>>(ar);
+  if (dtype == GDN_BF16) launch_fwd_t<CACHE, __nv_bfloat16>(ar, st);
+  else launch_fwd_t<CACHE, float>(ar, st);
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+template <typename T>
+void launch_bwd(const RopeArgs& ar, unsigned ctas, cudaStream_t st) {
+  if (ar.D <= 64) k_qk_norm_rope_bwd<8, T><<<ctas, RO_NT, 0, st>>>(ar);
+  else if (ar.D <= 128) k_qk_norm_rope_bwd<16, T><<<ctas, RO_NT, 0, st>>>(ar);
+  else k_qk_norm_rope_bwd<32, T><<<ctas, RO_NT, 0, st>>>(ar);
 }
 
 }  // namespace
@@ -327,7 +480,8 @@ gdn_status gdn_qk_norm_rope_fwd(const gdn_rope_problem* p, const void* q, const 
   ar.pos = positions;
   ar.q_out = q_out;
   ar.k_out = k_out;
-  return launch_fwd<0>(ar, p->dtype, (cudaStream_t)stream);
+  split_heads(&ar, ar.Hq + ar.Hk);
+  return launch_fwd<false>(ar, p->dtype, (cudaStream_t)stream);
 }
 
 gdn_status gdn_qk_norm_rope_cache(const gdn_rope_problem* p, const void* q, const void* k,
@@ -358,7 +512,8 @@ gdn_status gdn_qk_norm_rope_cache(const gdn_rope_problem* p, const void* q, cons
   ar.k_out = k_cache;
   ar.v_out = v_cache;
   ar.status = status;
-  return launch_fwd<1>(ar, p->dtype, (cudaStream_t)stream);
+  split_heads(&ar, ar.Hq + 2 * ar.Hk);
+  return launch_fwd<true>(ar, p->dtype, (cudaStream_t)stream);
 }
 
 gdn_status gdn_qk_norm_rope_bwd_workspace_size(const gdn_rope_problem* p, size_t* bytes) {
@@ -366,6 +521,7 @@ gdn_status gdn_qk_norm_rope_bwd_workspace_size(const gdn_rope_problem* p, size_t
   RopeArgs ar;
   gdn_status s = check_problem(p, &ar);
   if (s != GDN_OK) return s;
+  split_heads(&ar, ar.Hq + ar.Hk);
   *bytes = (size_t)bwd_ctas(ar) * 2 * (size_t)ar.D * sizeof(float);
   return GDN_OK;
 }
@@ -382,6 +538,7 @@ gdn_status gdn_qk_norm_rope_bwd(const gdn_rope_problem* p, const void* q, const 
       !ok16(dk_out, ar.N * ar.Hk) || !ok16(dq, ar.N * ar.Hq) || !ok16(dk, ar.N * ar.Hk) ||
       !ok16(dwq, ar.Hq) || !ok16(dwk, ar.Hk))
     return GDN_ERR_INVALID_ARG;
+  split_heads(&ar, ar.Hq + ar.Hk);
   const int64_t ctas = bwd_ctas(ar);
   const size_t need = (size_t)ctas * 2 * (size_t)ar.D * sizeof(float);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
@@ -399,10 +556,8 @@ gdn_status gdn_qk_norm_rope_bwd(const gdn_rope_problem* p, const void* q, const 
   ar.part = (float*)workspace;
   cudaStream_t st = (cudaStream_t)stream;
   if (ctas > 0) {
-    if (p->dtype == GDN_BF16)
-      k_qk_norm_rope_bwd<__nv_bfloat16><<<(unsigned)ctas, RO_NT, 0, st>>>(ar);
-    else
-      k_qk_norm_rope_bwd<float><<<(unsigned)ctas, RO_NT, 0, st>>>(ar);
+    if (p->dtype == GDN_BF16) launch_bwd<__nv_bfloat16>(ar, (unsigned)ctas, st);
+    else launch_bwd<float>(ar, (unsigned)ctas, st);
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
   }
   k_qk_norm_rope_dw<<<(unsigned)((2 * ar.D + 31) / 32), RO_NT, 0, st>>>(
