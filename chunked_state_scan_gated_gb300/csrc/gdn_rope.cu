@@ -18,6 +18,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <type_traits>
+
 #include "gdn_internal.h"
 #include "gdn_vec.cuh"
 
@@ -37,7 +39,7 @@ struct RopeArgs {
   int64_t N, T, qs, ks, vs, n_slots;
   int Hq, Hk, D, R, inter;
   int heads, chunk, chunks;     // rows of a token, rows per warp (in heads), warps per token
-  float eps, rscale;
+  float eps, rscale, inv_d;
   const void *q, *k, *v;
   const float *wq, *wk, *inv_freq;
   const int32_t* pos;
@@ -79,48 +81,103 @@ __device__ __forceinline__ void angle(int32_t t, float f, float* c, float* s) {
   sincospif(2.f * u, s, c);
 }
 
-// A row's 8 elements of one lane, as loaded.
+// Two fp32 numbers in a register pair: Blackwell's packed arithmetic halves the instructions.
+struct F2 {
+  uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 un(F2 a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ F2 mul(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
+// A row's 8 elements of one lane, as loaded; from(): the same of another lane of the row.
 template <typename T> struct Raw;
 template <> struct Raw<__nv_bfloat16> {
-  uint4 u;
+  uint32_t w[4];
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    u = __ldcs(reinterpret_cast<const uint4*>(p));
+    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
+    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
   }
-  __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0; }
+  template <int LPR> __device__ __forceinline__ Raw from(int lane) const {
+    Raw r;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(w[j] << 16);
-      v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-    }
+    for (int j = 0; j < 4; ++j) r.w[j] = __shfl_sync(0xffffffffu, w[j], lane, LPR);
+    return r;
+  }
+  __device__ __forceinline__ void get(F2 (&v)[4]) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[j] = f2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
   }
 };
 template <> struct Raw<float> {
-  float4 a, b;
+  float w[8];
   __device__ __forceinline__ void load(const float* p) {
-    a = __ldcs(reinterpret_cast<const float4*>(p));
-    b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
+    const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
   }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = 0.f;
+  }
+  template <int LPR> __device__ __forceinline__ Raw from(int lane) const {
+    Raw r;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r.w[j] = __shfl_sync(0xffffffffu, w[j], lane, LPR);
+    return r;
+  }
+  __device__ __forceinline__ void get(F2 (&v)[4]) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = f2(w[2 * j], w[2 * j + 1]);
   }
 };
-__device__ __forceinline__ void put(float* p, const float (&v)[8]) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  *(reinterpret_cast<float4*>(p) + 1) = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void put(float* p, const F2 (&v)[4]) {
+  const float2 a = un(v[0]), b = un(v[1]), c = un(v[2]), d = un(v[3]);
+  *reinterpret_cast<float4*>(p) = make_float4(a.x, a.y, b.x, b.y);
+  *(reinterpret_cast<float4*>(p) + 1) = make_float4(c.x, c.y, d.x, d.y);
 }
-__device__ __forceinline__ void put(__nv_bfloat16* p, const float (&v)[8]) {
-  uint4 u;
-  uint32_t* w = &u.x;
+__device__ __forceinline__ void put(__nv_bfloat16* p, const F2 (&v)[4]) {
+  uint32_t w[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const __nv_bfloat162 x = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+    const float2 a = un(v[j]);
+    const __nv_bfloat162 x = __floats2bfloat162_rn(a.x, a.y);
     w[j] = *reinterpret_cast<const uint32_t*>(&x);
   }
-  *reinterpret_cast<uint4*>(p) = u;
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+// A row's partner elements: of the pair's other half (another lane), or of the neighbour.
+template <bool INTER, int LPR, typename T>
+__device__ __forceinline__ void partner(const Raw<T>& raw, const F2 (&x)[4], int other,
+                                        F2 (&y)[4]) {
+  if constexpr (INTER) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 a = un(x[j]);
+      y[j] = f2(a.y, a.x);
+    }
+  } else {
+    raw.template from<LPR>(other).get(y);
+  }
 }
 
 // sum over the LPR lanes of a row
@@ -131,7 +188,7 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-// cos and sin of the token's angles into the warp's cs[0 .. R/2) and cs[128 ..)
+// cos and sin of the token's angles into the warp's cs[0 .. R/2) and cs[RO_MAXD / 2 ..)
 __device__ __forceinline__ void angles(const RopeArgs& ar, int64_t n, float* cs) {
   const int lane = threadIdx.x & 31;
   const int32_t t = ar.pos ? ar.pos[n] : (int32_t)(n % ar.T);
@@ -145,73 +202,93 @@ __device__ __forceinline__ void angles(const RopeArgs& ar, int64_t n, float* cs)
   __syncwarp();
 }
 
-// The rotation of a row held 8 elements per lane (element 8 l + j, l the lane in the row);
-// sgn = -1 transposes.
-template <int LPR>
-__device__ __forceinline__ void rotate(const RopeArgs& ar, const float* cs, float sgn,
-                                       float (&n)[8]) {
-  const int l = threadIdx.x & (LPR - 1), e = l * 8;
-  if (ar.inter) {
-    if (e < ar.R) {
-      const float4 c = *reinterpret_cast<const float4*>(cs + e / 2);
-      const float4 s = *reinterpret_cast<const float4*>(cs + RO_MAXD / 2 + e / 2);
-      const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+// A lane's view of the rotation: y_j = x_j c_j + xp_j s_j with xp the partner elements and the
+// sign of the pair's side in s (sgn = -1: the transposed rotation); c = 1, s = 0 past R.
+template <bool INTER>
+__device__ __forceinline__ void turn(const RopeArgs& ar, const float* cs, int e, float sgn,
+                                     float (&c)[8], float (&s)[8]) {
+  const bool in = e < ar.R, first = e < ar.R / 2;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float a = n[2 * j], b = n[2 * j + 1], sj = sgn * ss[j];
-        n[2 * j] = a * cc[j] - b * sj;
-        n[2 * j + 1] = b * cc[j] + a * sj;
-      }
-    }
-    return;
-  }
-  const int half = ar.R / 16;  // lanes per half
-  const bool first = l < half;
-  const int other = first ? l + half : l - half;
-  const float sg = first ? -sgn : sgn;
-  const float* at = cs + (first ? e : e - ar.R / 2);
-  const bool in = e < ar.R;
-#pragma unroll
-  for (int z = 0; z < 2; ++z) {
-    float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (in) {
-      c = *reinterpret_cast<const float4*>(at + 4 * z);
-      s = *reinterpret_cast<const float4*>(at + RO_MAXD / 2 + 4 * z);
-    }
-    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float m = __shfl_sync(0xffffffffu, n[4 * z + j], other, LPR);
-      if (in) n[4 * z + j] = n[4 * z + j] * cc[j] + m * (sg * ss[j]);
-    }
+  for (int j = 0; j < 8; ++j) {
+    const int i = INTER ? (e + j) / 2 : first ? e + j : e + j - ar.R / 2;
+    c[j] = in ? cs[i] : 1.f;
+    const bool neg = INTER ? !(j & 1) : first;
+    s[j] = in ? (neg ? -sgn : sgn) * cs[RO_MAXD / 2 + i] : 0.f;
   }
 }
+// The lane (of LPR) that holds the partner elements: its own past R (where they do not count).
+__device__ __forceinline__ int other_lane(const RopeArgs& ar, int e) {
+  if (e >= ar.R) return e / 8;
+  return (e < ar.R / 2 ? e + ar.R / 2 : e - ar.R / 2) / 8;
+}
 
-// One head row: its input, output and kind.
-struct Row {
-  int kind;  // 0 query, 1 key, 2 value (cache form), -1 none
-  int h;     // head of its kind
-};
-__device__ __forceinline__ Row row_of(const RopeArgs& ar, int h, int end) {
-  if (h >= end) return Row{-1, 0};
-  if (h < ar.Hq) return Row{0, h};
-  if (h < ar.Hq + ar.Hk) return Row{1, h - ar.Hq};
-  return Row{2, h - ar.Hq - ar.Hk};
+// The heads of one kind (query, key) of a token: y = f (x (w c) + xp (w_p s)).
+template <bool INTER, int LPR, typename T>
+__device__ __forceinline__ void norm_heads(const RopeArgs& ar, const T* src, T* dst,
+                                           const float* w, int h, int end, int64_t n, float* cs,
+                                           bool* have, bool store) {
+  constexpr int RPL = 32 / LPR;
+  const int lane = threadIdx.x & 31, sub = lane / LPR, e = (lane & (LPR - 1)) * 8;
+  const bool in = e < ar.D;
+  const int other = INTER ? 0 : other_lane(ar, e);
+  src += (int64_t)(h + sub) * ar.D + e;
+  dst += (int64_t)(h + sub) * ar.D + e;
+  F2 A[4], Bq[4];
+  bool first = true;
+  for (; h < end; h += RO_UNR * RPL) {
+    Raw<T> raw[RO_UNR];
+#pragma unroll
+    for (int u = 0; u < RO_UNR; ++u) {
+      if (in && h + u * RPL + sub < end) raw[u].load(src + u * RPL * ar.D);
+      else raw[u].zero();
+    }
+    if (first) {  // under the first loads
+      if (!*have) angles(ar, n, cs);
+      *have = true;
+      first = false;
+      float c[8], s[8], wv[8] = {}, wp[8] = {};
+      turn<INTER>(ar, cs, e, 1.f, c, s);
+      if (in) {
+        ld8(w + e, wv);
+        if constexpr (!INTER) ld8(w + other * 8, wp);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p0 = INTER ? wv[2 * j + 1] : wp[2 * j], p1 = INTER ? wv[2 * j] : wp[2 * j + 1];
+        A[j] = f2(wv[2 * j] * c[2 * j], wv[2 * j + 1] * c[2 * j + 1]);
+        Bq[j] = f2(p0 * s[2 * j], p1 * s[2 * j + 1]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < RO_UNR; ++u) {
+      if (h + u * RPL >= end) break;
+      F2 x[4], y[4];
+      raw[u].get(x);
+      F2 ss = mul(x[0], x[0]);
+#pragma unroll
+      for (int j = 1; j < 4; ++j) ss = fma(x[j], x[j], ss);
+      const float2 s2 = un(ss);
+      const float f = rsqrtf(fmaf(row_sum<LPR>(s2.x + s2.y), ar.inv_d, ar.eps));
+      partner<INTER, LPR>(raw[u], x, other, y);
+      const F2 ff = f2(f, f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = mul(fma(y[j], Bq[j], mul(x[j], A[j])), ff);
+      if (store && in && h + u * RPL + sub < end) put(dst + u * RPL * ar.D, y);
+    }
+    src += RO_UNR * RPL * ar.D;
+    dst += RO_UNR * RPL * ar.D;
+  }
 }
 
 // CACHE: k and v rows go to the caches
-template <bool CACHE, int LPR, typename T>
+template <bool CACHE, bool INTER, int LPR, typename T>
 __global__ void __launch_bounds__(RO_NT) k_qk_norm_rope_fwd(RopeArgs ar) {
   __shared__ __align__(16) float s_cs[RO_W][RO_MAXD];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LPR;
-  const int e = (lane & (LPR - 1)) * 8;
-  constexpr int RPL = 32 / LPR;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t task = (int64_t)blockIdx.x * RO_W + warp;
   if (task >= ar.N * ar.chunks) return;
   const int64_t n = task / ar.chunks;
-  const int h0 = (int)(task % ar.chunks) * ar.chunk;
-  const int end = min(h0 + ar.chunk, ar.heads);
-  const bool in = e < ar.D;
+  const int h0 = (int)(task % ar.chunks) * ar.chunk, h1 = min(h0 + ar.chunk, ar.heads);
   int64_t dst = n;
   if (CACHE) {
     dst = ar.slots[n];
@@ -220,125 +297,147 @@ __global__ void __launch_bounds__(RO_NT) k_qk_norm_rope_fwd(RopeArgs ar) {
       dst = -1;
     }
   }
-  const T* src[3] = {reinterpret_cast<const T*>(ar.q) + n * ar.qs + e,
-                     reinterpret_cast<const T*>(ar.k) + n * ar.ks + e,
-                     reinterpret_cast<const T*>(ar.v) + n * ar.vs + e};
   bool have = false;
-  for (int hb = h0; hb < end; hb += RO_UNR * RPL) {
-    Raw<T> raw[RO_UNR];
+  if (h0 < ar.Hq)
+    norm_heads<INTER, LPR>(ar, reinterpret_cast<const T*>(ar.q) + n * ar.qs,
+                           reinterpret_cast<T*>(ar.q_out) + n * ar.Hq * ar.D, ar.wq, h0,
+                           min(h1, ar.Hq), n, s_cs[warp], &have, true);
+  const int k0 = max(h0 - ar.Hq, 0), k1 = min(h1 - ar.Hq, ar.Hk);
+  if (k0 < k1 && dst >= 0)
+    norm_heads<INTER, LPR>(ar, reinterpret_cast<const T*>(ar.k) + n * ar.ks,
+                           reinterpret_cast<T*>(ar.k_out) + dst * ar.Hk * ar.D, ar.wk, k0, k1, n,
+                           s_cs[warp], &have, true);
+  if (CACHE && dst >= 0) {
+    const int v0 = max(h0 - ar.Hq - ar.Hk, 0), v1 = h1 - ar.Hq - ar.Hk;
+    constexpr int EL = 16 / (int)sizeof(T);
+    const T* src = reinterpret_cast<const T*>(ar.v) + n * ar.vs;
+    T* out = reinterpret_cast<T*>(ar.v_out) + dst * ar.Hk * ar.D;
+    for (int i = v0 * ar.D + lane * EL; i < v1 * ar.D; i += 32 * EL)
+      *reinterpret_cast<uint4*>(out + i) = *reinterpret_cast<const uint4*>(src + i);
+  }
+}
+
+// The gradients of the heads of one kind of a token.  With dn the turned dy:
+//   dx = f w dn - x f^3 sum(dn x w) / D,   dw += f dn x
+template <bool INTER, int LPR, int UNR, typename T>
+__device__ __forceinline__ void grad_heads(const RopeArgs& ar, const T* xs, const T* gs, T* dst,
+                                           const float* w, int h, int end, int64_t n, float* cs,
+                                           bool* have, F2 (&dw)[4]) {
+  constexpr int RPL = 32 / LPR;
+  const int lane = threadIdx.x & 31, sub = lane / LPR, e = (lane & (LPR - 1)) * 8;
+  const bool in = e < ar.D;
+  const int other = INTER ? 0 : other_lane(ar, e);
+  const int64_t at = (int64_t)(h + sub) * ar.D + e;
+  xs += at;
+  gs += at;
+  dst += at;
+  F2 C[4], S[4], W[4];
+  bool first = true;
+  for (; h < end; h += UNR * RPL) {
+    Raw<T> rx[UNR], rg[UNR];
 #pragma unroll
-    for (int u = 0; u < RO_UNR; ++u) {
-      const Row r = row_of(ar, hb + u * RPL + sub, end);
-      raw[u].zero();
-      if (r.kind >= 0 && in)
-        raw[u].load((r.kind == 0 ? src[0] : r.kind == 1 ? src[1] : src[2]) + (int64_t)r.h * ar.D);
-    }
-    if (!have) angles(ar, n, s_cs[warp]);  // under the first loads
-    have = true;
-#pragma unroll
-    for (int u = 0; u < RO_UNR; ++u) {
-      if (hb + u * RPL >= end) break;
-      const Row r = row_of(ar, hb + u * RPL + sub, end);
-      float v[8], w[8] = {};
-      raw[u].get(v);
-      float ss = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
-      const float f = rsqrtf(row_sum<LPR>(ss) / (float)ar.D + ar.eps);
-      if (in && r.kind >= 0 && r.kind < 2) ld8((r.kind == 0 ? ar.wq : ar.wk) + e, w);
-      float y[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = v[j] * (f * w[j]);
-      rotate<LPR>(ar, s_cs[warp], 1.f, y);
-      if (r.kind < 0 || !in || (CACHE && r.kind > 0 && dst < 0)) continue;
-      const int64_t at = (r.kind == 0 ? n * ar.Hq : dst * ar.Hk) + r.h;
-      T* out = reinterpret_cast<T*>(r.kind == 0 ? ar.q_out : r.kind == 1 ? ar.k_out : ar.v_out);
-      if (CACHE && r.kind == 2) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = v[j];
+    for (int u = 0; u < UNR; ++u) {
+      if (in && h + u * RPL + sub < end) {
+        rx[u].load(xs + u * RPL * ar.D);
+        rg[u].load(gs + u * RPL * ar.D);
+      } else {
+        rx[u].zero();
+        rg[u].zero();
       }
-      put(out + at * ar.D + e, y);
     }
+    if (first) {
+      if (!*have) angles(ar, n, cs);
+      *have = true;
+      first = false;
+      float c[8], s[8], wv[8] = {};
+      turn<INTER>(ar, cs, e, -1.f, c, s);
+      if (in) ld8(w + e, wv);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        C[j] = f2(c[2 * j], c[2 * j + 1]);
+        S[j] = f2(s[2 * j], s[2 * j + 1]);
+        W[j] = f2(wv[2 * j], wv[2 * j + 1]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < UNR; ++u) {
+      if (h + u * RPL >= end) break;
+      F2 x[4], g[4], y[4];
+      rx[u].get(x);
+      rg[u].get(g);
+      partner<INTER, LPR>(rg[u], g, other, y);
+      F2 ss = mul(x[0], x[0]);
+#pragma unroll
+      for (int j = 1; j < 4; ++j) ss = fma(x[j], x[j], ss);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) g[j] = fma(y[j], S[j], mul(g[j], C[j]));  // dn
+      F2 dot = f2(0.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        y[j] = mul(g[j], x[j]);
+        g[j] = mul(g[j], W[j]);
+        dot = fma(g[j], x[j], dot);
+      }
+      const float2 s2 = un(ss), d2 = un(dot);
+      const float f = rsqrtf(fmaf(row_sum<LPR>(s2.x + s2.y), ar.inv_d, ar.eps));
+      const float m = -(row_sum<LPR>(d2.x + d2.y) * ar.inv_d) * f * f * f;
+      const F2 ff = f2(f, f), mm = f2(m, m);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        dw[j] = fma(y[j], ff, dw[j]);  // absent rows hold zeros
+        g[j] = fma(x[j], mm, mul(g[j], ff));
+      }
+      if (in && h + u * RPL + sub < end) put(dst + u * RPL * ar.D, g);
+    }
+    xs += UNR * RPL * ar.D;
+    gs += UNR * RPL * ar.D;
+    dst += UNR * RPL * ar.D;
   }
 }
 
 // Persistent: a warp takes tasks in a fixed stride and keeps its lanes' dwq, dwk in registers.
-template <int LPR, typename T>
+template <bool INTER, int LPR, typename T>
 __global__ void __launch_bounds__(RO_NT, 2) k_qk_norm_rope_bwd(RopeArgs ar) {
   __shared__ __align__(16) float s_cs[RO_W][RO_MAXD];
   __shared__ float red[RO_W][RO_MAXD];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LPR;
   const int e = (lane & (LPR - 1)) * 8;
-  constexpr int RPL = 32 / LPR, UNR = sizeof(T) == 2 ? RO_UNR : RO_UNR / 2;
-  const bool in = e < ar.D;
-  float dw[2][8] = {};
+  constexpr int UNR = sizeof(T) == 2 ? RO_UNR : RO_UNR / 2;
+  F2 dw[2][4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) dw[0][j] = dw[1][j] = f2(0.f, 0.f);
   for (int64_t task = (int64_t)blockIdx.x * RO_W + warp; task < ar.N * ar.chunks;
        task += (int64_t)gridDim.x * RO_W) {
     const int64_t n = task / ar.chunks;
-    const int h0 = (int)(task % ar.chunks) * ar.chunk;
-    const int end = min(h0 + ar.chunk, ar.heads);
+    const int h0 = (int)(task % ar.chunks) * ar.chunk, h1 = min(h0 + ar.chunk, ar.heads);
     bool have = false;
-    for (int hb = h0; hb < end; hb += UNR * RPL) {
-      Raw<T> rx[UNR], rg[UNR];
-#pragma unroll
-      for (int u = 0; u < UNR; ++u) {
-        const Row r = row_of(ar, hb + u * RPL + sub, end);
-        rx[u].zero();
-        rg[u].zero();
-        if (r.kind >= 0 && in) {
-          const bool isq = r.kind == 0;
-          const int64_t hd = (int64_t)r.h * ar.D + e;
-          rx[u].load(reinterpret_cast<const T*>(isq ? ar.q : ar.k) + n * (isq ? ar.qs : ar.ks) +
-                     hd);
-          rg[u].load(reinterpret_cast<const T*>(isq ? ar.dq_out : ar.dk_out) +
-                     n * (isq ? ar.Hq : ar.Hk) * ar.D + hd);
-        }
-      }
-      if (!have) angles(ar, n, s_cs[warp]);
-      have = true;
-#pragma unroll
-      for (int u = 0; u < UNR; ++u) {
-        if (hb + u * RPL >= end) break;
-        const Row r = row_of(ar, hb + u * RPL + sub, end);
-        const bool isq = r.kind == 0;
-        float x[8], g[8], w[8] = {};
-        rx[u].get(x);
-        rg[u].get(g);
-        rotate<LPR>(ar, s_cs[warp], -1.f, g);
-        float ss = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
-        const float f = rsqrtf(row_sum<LPR>(ss) / (float)ar.D + ar.eps);
-        if (in && r.kind >= 0) ld8((isq ? ar.wq : ar.wk) + e, w);
-        float dot = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          x[j] *= f;
-          const float d = g[j] * x[j];
-          dw[0][j] += isq ? d : 0.f;
-          dw[1][j] += isq ? 0.f : d;  // absent rows hold zeros
-          g[j] *= w[j];
-          dot = fmaf(g[j], x[j], dot);
-        }
-        const float m = row_sum<LPR>(dot) / (float)ar.D;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = f * (g[j] - x[j] * m);
-        if (r.kind >= 0 && in)
-          put(reinterpret_cast<T*>(isq ? ar.q_out : ar.k_out) +
-                  (n * (isq ? ar.Hq : ar.Hk) + r.h) * ar.D + e,
-              g);
-      }
-    }
+    if (h0 < ar.Hq)
+      grad_heads<INTER, LPR, UNR>(ar, reinterpret_cast<const T*>(ar.q) + n * ar.qs,
+                                  reinterpret_cast<const T*>(ar.dq_out) + n * ar.Hq * ar.D,
+                                  reinterpret_cast<T*>(ar.q_out) + n * ar.Hq * ar.D, ar.wq, h0,
+                                  min(h1, ar.Hq), n, s_cs[warp], &have, dw[0]);
+    const int k0 = max(h0 - ar.Hq, 0), k1 = h1 - ar.Hq;
+    if (k0 < k1)
+      grad_heads<INTER, LPR, UNR>(ar, reinterpret_cast<const T*>(ar.k) + n * ar.ks,
+                                  reinterpret_cast<const T*>(ar.dk_out) + n * ar.Hk * ar.D,
+                                  reinterpret_cast<T*>(ar.k_out) + n * ar.Hk * ar.D, ar.wk, k0,
+                                  k1, n, s_cs[warp], &have, dw[1]);
   }
   for (int z = 0; z < 2; ++z) {  // this CTA's dwq, dwk: lanes of equal elements, then warps in order
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-      for (int o = LPR; o < 32; o <<= 1) dw[z][j] += __shfl_xor_sync(0xffffffffu, dw[z][j], o);
     __syncthreads();
-    if (in && sub == 0)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) red[warp][e + j] = dw[z][j];
+    for (int j = 0; j < 4; ++j) {
+      float2 d = un(z ? dw[1][j] : dw[0][j]);
+#pragma unroll
+      for (int o = LPR; o < 32; o <<= 1) {
+        d.x += __shfl_xor_sync(0xffffffffu, d.x, o);
+        d.y += __shfl_xor_sync(0xffffffffu, d.y, o);
+      }
+      if (e < ar.D && sub == 0) {
+        red[warp][e + 2 * j] = d.x;
+        red[warp][e + 2 * j + 1] = d.y;
+      }
+    }
     __syncthreads();
     for (int c = threadIdx.x; c < ar.D; c += RO_NT) {
       float s = 0.f;
@@ -404,6 +503,7 @@ gdn_status check_problem(const gdn_rope_problem* p, RopeArgs* ar) {
   ar->R = p->R;
   ar->inter = p->interleaved ? 1 : 0;
   ar->eps = p->eps;
+  ar->inv_d = 1.f / (float)p->D;
   ar->rscale = p->rope_scale;
   return GDN_OK;
 }
@@ -434,24 +534,29 @@ int64_t bwd_ctas(const RopeArgs& ar) {
   return n < RO_BCTAS ? n : RO_BCTAS;
 }
 
-template <bool CACHE, typename T>
-void launch_fwd_t(const RopeArgs& ar, cudaStream_t st) {
-  const unsigned ctas = (unsigned)((ar.N * ar.chunks + RO_W - 1) / RO_W);
-  if (ar.D <= 64) k_qk_norm_rope_fwd<CACHE, 8, T><<<ctas, RO_NT, 0, st>>>(ar);
-  else if (ar.D <= 128) k_qk_norm_rope_fwd<CACHE, 16, T><<<ctas, RO_NT, 0, st>>>(ar);
-  else k_qk_norm_rope_fwd<CACHE, 32, T><<<ctas, RO_NT, 0, st>>>(ar);
+// Runs f with the lanes per row, the pairing and the type as template arguments.
+template <typename F>
+void with_types(const RopeArgs& ar, int dtype, F f) {
+  auto lanes = [&](auto inter, auto t) {
+    if (ar.D <= 64) f(std::integral_constant<int, 8>(), inter, t);
+    else if (ar.D <= 128) f(std::integral_constant<int, 16>(), inter, t);
+    else f(std::integral_constant<int, 32>(), inter, t);
+  };
+  auto pairs = [&](auto t) {
+    if (ar.inter) lanes(std::true_type(), t);
+    else lanes(std::false_type(), t);
+  };
+  if (dtype == GDN_BF16) pairs(__nv_bfloat16());
+  else pairs(0.f);
 }
+
 template <bool CACHE>
 gdn_status launch_fwd(const RopeArgs& ar, int dtype, cudaStream_t st) {
-  if (dtype == GDN_BF16) launch_fwd_t<CACHE, __nv_bfloat16>(ar, st);
-  else launch_fwd_t<CACHE, float>(ar, st);
+  const unsigned ctas = (unsigned)((ar.N * ar.chunks + RO_W - 1) / RO_W);
+  with_types(ar, dtype, [&](auto lpr, auto inter, auto t) {
+    k_qk_norm_rope_fwd<CACHE, inter(), lpr(), decltype(t)><<<ctas, RO_NT, 0, st>>>(ar);
+  });
   return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
-}
-template <typename T>
-void launch_bwd(const RopeArgs& ar, unsigned ctas, cudaStream_t st) {
-  if (ar.D <= 64) k_qk_norm_rope_bwd<8, T><<<ctas, RO_NT, 0, st>>>(ar);
-  else if (ar.D <= 128) k_qk_norm_rope_bwd<16, T><<<ctas, RO_NT, 0, st>>>(ar);
-  else k_qk_norm_rope_bwd<32, T><<<ctas, RO_NT, 0, st>>>(ar);
 }
 
 }  // namespace
@@ -556,8 +661,9 @@ gdn_status gdn_qk_norm_rope_bwd(const gdn_rope_problem* p, const void* q, const 
   ar.part = (float*)workspace;
   cudaStream_t st = (cudaStream_t)stream;
   if (ctas > 0) {
-    if (p->dtype == GDN_BF16) launch_bwd<__nv_bfloat16>(ar, (unsigned)ctas, st);
-    else launch_bwd<float>(ar, (unsigned)ctas, st);
+    with_types(ar, p->dtype, [&](auto lpr, auto inter, auto t) {
+      k_qk_norm_rope_bwd<inter(), lpr(), decltype(t)><<<(unsigned)ctas, RO_NT, 0, st>>>(ar);
+    });
     if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
   }
   k_qk_norm_rope_dw<<<(unsigned)((2 * ar.D + 31) / 32), RO_NT, 0, st>>>(
