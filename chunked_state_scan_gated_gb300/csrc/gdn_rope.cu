@@ -7,13 +7,17 @@
 // The angle is formed in revolutions: t * (inv_freq / 2 pi) as an exact two-term product, its
 // integer part dropped, so positions past 2^20 lose nothing (angle()).
 //
-// Bound by HBM (2 row accesses forward, 3 backward).  A warp takes one token and a run of its
-// heads: the token's R/2 angles are computed once, into the warp's own shared memory (no CTA
-// barrier), and serve all its heads.  A row is held 8 elements per lane (16 bytes of bf16) by
-// LPR = 8, 16 or 32 lanes, so a warp holds 32 / LPR heads at a time, and the loads of RO_UNR such
-// groups are issued together.  The halves of a rotated head meet through shuffles.  With many
-// tokens a warp takes all heads of its token; with few (decode) as few as one group, which
-// repeats the angles but spreads a token over many SMs.
+// Bound by HBM (2 row accesses forward, 3 backward).  A row is held 8 elements per lane (16
+// bytes of bf16) by LPR = 8, 16 or 32 lanes, so a warp holds 32 / LPR heads at a time and takes U
+// such sets together (independent chains of shuffles: one at a time was bound by their latency,
+// 154 against 100 us for 32768 tokens of 18 heads of 256).  All these groups of all tokens, in order, are divided evenly over one wave of
+// warps, from a decode step's few (each warp one group) to a training batch: no tail.  A warp
+// streams its groups through a ring of its own in shared memory (16-byte asynchronous copies, RO_RING bytes in
+// flight) with warp barriers only; a rotated element's partner in the other half is read from
+// the ring.  The token's R/2 angles are computed once and folded with the weights:
+//   y = r (x (w c) + xp (w_p s)),  xp the partner elements, s with the sign of the pair's side
+// and the arithmetic is packed two fp32 numbers at a time: 2 (3) row accesses leave about
+// 44 issue slots of an SM's scheduler per 512-byte row.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <string.h>
@@ -30,15 +34,16 @@ using namespace vec;
 
 constexpr int RO_NT = 256;     // 8 warps
 constexpr int RO_W = RO_NT / 32;
-constexpr int RO_UNR = 4;      // head groups whose loads are issued together
-constexpr int RO_BCTAS = 304;  // CTAs of the backward at most (2 per SM of a 152-SM GPU)
+constexpr int RO_CTAS = 152 * 2;  // CTAs at most: one wave of 2 per SM of a 152-SM GPU
 constexpr int RO_MAXD = 256;   // 8 elements per lane
-constexpr int RO_FILL = 152 * 16;  // warps that keep the GPU busy
+constexpr int RO_RING = 12288;  // bytes of a warp's ring
+constexpr int RO_FU = 4, RO_GU = 2;  // sets of heads per group, forward and backward
+constexpr int RO_SMEM = RO_W * (RO_RING + RO_MAXD * 4);  // rings, cos and sin
 
 struct RopeArgs {
   int64_t N, T, qs, ks, vs, n_slots;
   int Hq, Hk, D, R, inter;
-  int heads, chunk, chunks;     // rows of a token, rows per warp (in heads), warps per token
+  int gq, gk, gv;               // groups of a token's query, key and (cache form) value heads
   float eps, rscale, inv_d;
   const void *q, *k, *v;
   const float *wq, *wk, *inv_freq;
@@ -106,50 +111,21 @@ __device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c) {
   return r;
 }
 
-// A row's 8 elements of one lane, as loaded; from(): the same of another lane of the row.
-template <typename T> struct Raw;
-template <> struct Raw<__nv_bfloat16> {
-  uint32_t w[4];
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
-    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-  }
-  __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0; }
-  template <int LPR> __device__ __forceinline__ Raw from(int lane) const {
-    Raw r;
+// 8 elements from a ring.
+__device__ __forceinline__ void get(const __nv_bfloat16* p, F2 (&v)[4]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) r.w[j] = __shfl_sync(0xffffffffu, w[j], lane, LPR);
-    return r;
-  }
-  __device__ __forceinline__ void get(F2 (&v)[4]) const {
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      v[j] = f2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
-  }
-};
-template <> struct Raw<float> {
-  float w[8];
-  __device__ __forceinline__ void load(const float* p) {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
-    const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
-  }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = 0.f;
-  }
-  template <int LPR> __device__ __forceinline__ Raw from(int lane) const {
-    Raw r;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) r.w[j] = __shfl_sync(0xffffffffu, w[j], lane, LPR);
-    return r;
-  }
-  __device__ __forceinline__ void get(F2 (&v)[4]) const {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = f2(w[2 * j], w[2 * j + 1]);
-  }
-};
+  for (int j = 0; j < 4; ++j)
+    v[j] = f2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
+}
+__device__ __forceinline__ void get(const float* p, F2 (&v)[4]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = f2(a.x, a.y);
+  v[1] = f2(a.z, a.w);
+  v[2] = f2(b.x, b.y);
+  v[3] = f2(b.z, b.w);
+}
 __device__ __forceinline__ void put(float* p, const F2 (&v)[4]) {
   const float2 a = un(v[0]), b = un(v[1]), c = un(v[2]), d = un(v[3]);
   *reinterpret_cast<float4*>(p) = make_float4(a.x, a.y, b.x, b.y);
@@ -165,27 +141,16 @@ __device__ __forceinline__ void put(__nv_bfloat16* p, const F2 (&v)[4]) {
   }
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
-// A row's partner elements: of the pair's other half (another lane), or of the neighbour.
-template <bool INTER, int LPR, typename T>
-__device__ __forceinline__ void partner(const Raw<T>& raw, const F2 (&x)[4], int other,
-                                        F2 (&y)[4]) {
-  if constexpr (INTER) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 a = un(x[j]);
-      y[j] = f2(a.y, a.x);
-    }
-  } else {
-    raw.template from<LPR>(other).get(y);
-  }
+// 16 bytes per lane, without waiting; zeros where !in.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool in) {
+  const uint32_t d = (uint32_t)__cvta_generic_to_shared(dst);
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(in ? 16 : 0)
+               : "memory");
 }
-
-// sum over the LPR lanes of a row
-template <int LPR>
-__device__ __forceinline__ float row_sum(float v) {
-#pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+template <typename T>
+__device__ __forceinline__ void copy8(T* dst, const T* src, bool in) {
+  copy16(dst, src, in);
+  if constexpr (sizeof(T) == 4) copy16(dst + 4, src + 4, in);
 }
 
 // cos and sin of the token's angles into the warp's cs[0 .. R/2) and cs[RO_MAXD / 2 ..)
@@ -222,208 +187,285 @@ __device__ __forceinline__ int other_lane(const RopeArgs& ar, int e) {
   return (e < ar.R / 2 ? e + ar.R / 2 : e - ar.R / 2) / 8;
 }
 
-// The heads of one kind (query, key) of a token: y = f (x (w c) + xp (w_p s)).
-template <bool INTER, int LPR, typename T>
-__device__ __forceinline__ void norm_heads(const RopeArgs& ar, const T* src, T* dst,
-                                           const float* w, int h, int end, int64_t n, float* cs,
-                                           bool* have, bool store) {
-  constexpr int RPL = 32 / LPR;
-  const int lane = threadIdx.x & 31, sub = lane / LPR, e = (lane & (LPR - 1)) * 8;
-  const bool in = e < ar.D;
-  const int other = INTER ? 0 : other_lane(ar, e);
-  src += (int64_t)(h + sub) * ar.D + e;
-  dst += (int64_t)(h + sub) * ar.D + e;
-  F2 A[4], Bq[4];
-  bool first = true;
-  for (; h < end; h += RO_UNR * RPL) {
-    Raw<T> raw[RO_UNR];
-#pragma unroll
-    for (int u = 0; u < RO_UNR; ++u) {
-      if (in && h + u * RPL + sub < end) raw[u].load(src + u * RPL * ar.D);
-      else raw[u].zero();
+// A place in the sequence of groups: token, group of its heads.
+struct Place {
+  int64_t n;
+  int g;
+  __device__ __forceinline__ void next(int groups) {
+    if (++g == groups) {
+      g = 0;
+      ++n;
     }
-    if (first) {  // under the first loads
-      if (!*have) angles(ar, n, cs);
-      *have = true;
-      first = false;
-      float c[8], s[8], wv[8] = {}, wp[8] = {};
-      turn<INTER>(ar, cs, e, 1.f, c, s);
-      if (in) {
-        ld8(w + e, wv);
-        if constexpr (!INTER) ld8(w + other * 8, wp);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float p0 = INTER ? wv[2 * j + 1] : wp[2 * j], p1 = INTER ? wv[2 * j] : wp[2 * j + 1];
-        A[j] = f2(wv[2 * j] * c[2 * j], wv[2 * j + 1] * c[2 * j + 1]);
-        Bq[j] = f2(p0 * s[2 * j], p1 * s[2 * j + 1]);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < RO_UNR; ++u) {
-      if (h + u * RPL >= end) break;
-      F2 x[4], y[4];
-      raw[u].get(x);
-      F2 ss = mul(x[0], x[0]);
-#pragma unroll
-      for (int j = 1; j < 4; ++j) ss = fma(x[j], x[j], ss);
-      const float2 s2 = un(ss);
-      const float f = rsqrtf(fmaf(row_sum<LPR>(s2.x + s2.y), ar.inv_d, ar.eps));
-      partner<INTER, LPR>(raw[u], x, other, y);
-      const F2 ff = f2(f, f);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) y[j] = mul(fma(y[j], Bq[j], mul(x[j], A[j])), ff);
-      if (store && in && h + u * RPL + sub < end) put(dst + u * RPL * ar.D, y);
-    }
-    src += RO_UNR * RPL * ar.D;
-    dst += RO_UNR * RPL * ar.D;
   }
+};
+// A group: kind 0 query, 1 key, 2 value; this lane's first head of that kind (the others
+// follow 32 / LPR apart) and how many heads the kind has (0 for a lane past D).
+struct Heads {
+  int kind, h, end;
+};
+template <int LPR, int U>
+__device__ __forceinline__ Heads heads_of(const RopeArgs& ar, int g) {
+  const int lane = threadIdx.x & 31, e = (lane & (LPR - 1)) * 8;
+  const int kind = g < ar.gq ? 0 : g < ar.gq + ar.gk ? 1 : 2;
+  const int i = g - (kind == 0 ? 0 : kind == 1 ? ar.gq : ar.gq + ar.gk);
+  return Heads{kind, i * U * (32 / LPR) + lane / LPR, e < ar.D ? kind == 0 ? ar.Hq : ar.Hk : 0};
+}
+// This warp's share [first, last) of the groups.
+__device__ __forceinline__ void share(const RopeArgs& ar, int groups, int64_t* first,
+                                      int64_t* last) {
+  const int64_t all = ar.N * groups, w = (int64_t)blockIdx.x * RO_W + (threadIdx.x >> 5);
+  const int64_t warps = (int64_t)gridDim.x * RO_W;
+  *first = all * w / warps;
+  *last = all * (w + 1) / warps;
 }
 
 // CACHE: k and v rows go to the caches
 template <bool CACHE, bool INTER, int LPR, typename T>
-__global__ void __launch_bounds__(RO_NT) k_qk_norm_rope_fwd(RopeArgs ar) {
-  __shared__ __align__(16) float s_cs[RO_W][RO_MAXD];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t task = (int64_t)blockIdx.x * RO_W + warp;
-  if (task >= ar.N * ar.chunks) return;
-  const int64_t n = task / ar.chunks;
-  const int h0 = (int)(task % ar.chunks) * ar.chunk, h1 = min(h0 + ar.chunk, ar.heads);
-  int64_t dst = n;
-  if (CACHE) {
-    dst = ar.slots[n];
-    if (dst < 0 || dst >= ar.n_slots) {
-      if (dst != -1 && lane == 0 && h0 == 0 && ar.status) atomicOr(ar.status, kStatusClamped);
-      dst = -1;
-    }
-  }
-  bool have = false;
-  if (h0 < ar.Hq)
-    norm_heads<INTER, LPR>(ar, reinterpret_cast<const T*>(ar.q) + n * ar.qs,
-                           reinterpret_cast<T*>(ar.q_out) + n * ar.Hq * ar.D, ar.wq, h0,
-                           min(h1, ar.Hq), n, s_cs[warp], &have, true);
-  const int k0 = max(h0 - ar.Hq, 0), k1 = min(h1 - ar.Hq, ar.Hk);
-  if (k0 < k1 && dst >= 0)
-    norm_heads<INTER, LPR>(ar, reinterpret_cast<const T*>(ar.k) + n * ar.ks,
-                           reinterpret_cast<T*>(ar.k_out) + dst * ar.Hk * ar.D, ar.wk, k0, k1, n,
-                           s_cs[warp], &have, true);
-  if (CACHE && dst >= 0) {
-    const int v0 = max(h0 - ar.Hq - ar.Hk, 0), v1 = h1 - ar.Hq - ar.Hk;
-    constexpr int EL = 16 / (int)sizeof(T);
-    const T* src = reinterpret_cast<const T*>(ar.v) + n * ar.vs;
-    T* out = reinterpret_cast<T*>(ar.v_out) + dst * ar.Hk * ar.D;
-    for (int i = v0 * ar.D + lane * EL; i < v1 * ar.D; i += 32 * EL)
-      *reinterpret_cast<uint4*>(out + i) = *reinterpret_cast<const uint4*>(src + i);
-  }
-}
-
-// The gradients of the heads of one kind of a token.  With dn the turned dy:
-//   dx = f w dn - x f^3 sum(dn x w) / D,   dw += f dn x
-template <bool INTER, int LPR, int UNR, typename T>
-__device__ __forceinline__ void grad_heads(const RopeArgs& ar, const T* xs, const T* gs, T* dst,
-                                           const float* w, int h, int end, int64_t n, float* cs,
-                                           bool* have, F2 (&dw)[4]) {
-  constexpr int RPL = 32 / LPR;
-  const int lane = threadIdx.x & 31, sub = lane / LPR, e = (lane & (LPR - 1)) * 8;
-  const bool in = e < ar.D;
+__global__ void __launch_bounds__(RO_NT, 2) k_qk_norm_rope_fwd(RopeArgs ar) {
+  extern __shared__ __align__(16) char smem[];
+  constexpr int U = RO_FU, RPL = 32 / LPR, SE = 32 * 8;
+  constexpr int NST = RO_RING / (U * SE * (int)sizeof(T));
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = (lane & (LPR - 1)) * 8;
+  T* ring = reinterpret_cast<T*>(smem + warp * RO_RING);
+  float* cs = reinterpret_cast<float*>(smem + RO_W * RO_RING) + warp * RO_MAXD;
+  const int groups = ar.gq + ar.gk + (CACHE ? ar.gv : 0);
+  int64_t left, last;
+  share(ar, groups, &left, &last);
+  Place load{left / groups, (int)(left % groups)}, at = load;
+  left = last - left;
+  int64_t ahead = left;  // groups still to be issued
   const int other = INTER ? 0 : other_lane(ar, e);
-  const int64_t at = (int64_t)(h + sub) * ar.D + e;
-  xs += at;
-  gs += at;
-  dst += at;
-  F2 C[4], S[4], W[4];
-  bool first = true;
-  for (; h < end; h += UNR * RPL) {
-    Raw<T> rx[UNR], rg[UNR];
+  const int mine = lane * 8, theirs = (lane / LPR * LPR + other) * 8;
+  auto issue = [&](int stage) {
+    if (ahead-- > 0) {
+      const Heads x = heads_of<LPR, U>(ar, load.g);
+      const T* src = reinterpret_cast<const T*>(x.kind == 0 ? ar.q : x.kind == 1 ? ar.k : ar.v);
+      const int64_t stride = x.kind == 0 ? ar.qs : x.kind == 1 ? ar.ks : ar.vs;
+      const T* row = src + load.n * stride + x.h * ar.D + e;
 #pragma unroll
-    for (int u = 0; u < UNR; ++u) {
-      if (in && h + u * RPL + sub < end) {
-        rx[u].load(xs + u * RPL * ar.D);
-        rg[u].load(gs + u * RPL * ar.D);
-      } else {
-        rx[u].zero();
-        rg[u].zero();
+      for (int u = 0; u < U; ++u) {
+        const bool in = x.h + u * RPL < x.end;
+        copy8(ring + (stage * U + u) * SE + mine, in ? row + u * RPL * ar.D : src, in);
+      }
+      load.next(groups);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  for (int i = 0; i < NST - 1; ++i) issue(i);
+  F2 A[4], B[4];
+  int64_t n = -1, dst = -1;
+  int kind = -1, stage = 0;
+  for (; left > 0; --left, at.next(groups)) {
+    const Heads x = heads_of<LPR, U>(ar, at.g);
+    if (at.n != n || x.kind != kind) {
+      if (at.n != n) {
+        angles(ar, at.n, cs);
+        if constexpr (CACHE) {
+          dst = ar.slots[at.n];
+          if (dst < 0 || dst >= ar.n_slots) {
+            if (dst != -1 && lane == 0 && ar.status) atomicOr(ar.status, kStatusClamped);
+            dst = -1;
+          }
+        } else {
+          dst = at.n;
+        }
+      }
+      n = at.n;
+      kind = x.kind;
+      if (!CACHE || kind < 2) {
+        const float* w = kind == 0 ? ar.wq : ar.wk;
+        float c[8], s[8], wv[8] = {}, wp[8] = {};
+        turn<INTER>(ar, cs, e, 1.f, c, s);
+        if (e < ar.D) {
+          ld8(w + e, wv);
+          if constexpr (!INTER) ld8(w + other * 8, wp);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float p0 = INTER ? wv[2 * j + 1] : wp[2 * j];
+          const float p1 = INTER ? wv[2 * j] : wp[2 * j + 1];
+          A[j] = f2(wv[2 * j] * c[2 * j], wv[2 * j + 1] * c[2 * j + 1]);
+          B[j] = f2(p0 * s[2 * j], p1 * s[2 * j + 1]);
+        }
       }
     }
-    if (first) {
-      if (!*have) angles(ar, n, cs);
-      *have = true;
-      first = false;
-      float c[8], s[8], wv[8] = {};
-      turn<INTER>(ar, cs, e, -1.f, c, s);
-      if (in) ld8(w + e, wv);
+    asm volatile("cp.async.wait_group %0;" ::"n"(NST - 2) : "memory");
+    __syncwarp();  // every lane's part has arrived, and the stage before this one is read
+    issue(stage == 0 ? NST - 1 : stage - 1);
+    const T* in = ring + stage * U * SE;
+    stage = stage == NST - 1 ? 0 : stage + 1;
+    F2 v[U][4];
+    float ss[U];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        C[j] = f2(c[2 * j], c[2 * j + 1]);
-        S[j] = f2(s[2 * j], s[2 * j + 1]);
-        W[j] = f2(wv[2 * j], wv[2 * j + 1]);
+    for (int u = 0; u < U; ++u) {
+      get(in + u * SE + mine, v[u]);
+      F2 sq = mul(v[u][0], v[u][0]);
+#pragma unroll
+      for (int j = 1; j < 4; ++j) sq = fma(v[u][j], v[u][j], sq);
+      const float2 s2 = un(sq);
+      ss[u] = s2.x + s2.y;
+    }
+    if (!CACHE || kind < 2) {
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int u = 0; u < U; ++u) ss[u] += __shfl_xor_sync(0xffffffffu, ss[u], o);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        F2 y[4];
+        if constexpr (INTER) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 a = un(v[u][j]);
+            y[j] = f2(a.y, a.x);
+          }
+        } else {
+          get(in + u * SE + theirs, y);
+        }
+        const float f = rsqrtf(fmaf(ss[u], ar.inv_d, ar.eps));
+        const F2 ff = f2(f, f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[u][j] = mul(fma(y[j], B[j], mul(v[u][j], A[j])), ff);
       }
     }
+    if (CACHE && kind > 0 && dst < 0) continue;
+    T* out = reinterpret_cast<T*>(kind == 0 ? ar.q_out : kind == 1 ? ar.k_out : ar.v_out);
+    out += ((kind == 0 ? at.n * ar.Hq : dst * ar.Hk) + x.h) * ar.D + e;
 #pragma unroll
-    for (int u = 0; u < UNR; ++u) {
-      if (h + u * RPL >= end) break;
-      F2 x[4], g[4], y[4];
-      rx[u].get(x);
-      rg[u].get(g);
-      partner<INTER, LPR>(rg[u], g, other, y);
-      F2 ss = mul(x[0], x[0]);
-#pragma unroll
-      for (int j = 1; j < 4; ++j) ss = fma(x[j], x[j], ss);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) g[j] = fma(y[j], S[j], mul(g[j], C[j]));  // dn
-      F2 dot = f2(0.f, 0.f);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        y[j] = mul(g[j], x[j]);
-        g[j] = mul(g[j], W[j]);
-        dot = fma(g[j], x[j], dot);
-      }
-      const float2 s2 = un(ss), d2 = un(dot);
-      const float f = rsqrtf(fmaf(row_sum<LPR>(s2.x + s2.y), ar.inv_d, ar.eps));
-      const float m = -(row_sum<LPR>(d2.x + d2.y) * ar.inv_d) * f * f * f;
-      const F2 ff = f2(f, f), mm = f2(m, m);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        dw[j] = fma(y[j], ff, dw[j]);  // absent rows hold zeros
-        g[j] = fma(x[j], mm, mul(g[j], ff));
-      }
-      if (in && h + u * RPL + sub < end) put(dst + u * RPL * ar.D, g);
-    }
-    xs += UNR * RPL * ar.D;
-    gs += UNR * RPL * ar.D;
-    dst += UNR * RPL * ar.D;
+    for (int u = 0; u < U; ++u)
+      if (x.h + u * RPL < x.end) put(out + u * RPL * ar.D, v[u]);
   }
 }
 
-// Persistent: a warp takes tasks in a fixed stride and keeps its lanes' dwq, dwk in registers.
+// dx = f w dn - x f^3 sum(dn x w) / D,  dw += f dn x  with dn the turned dy.  The ring's stages
+// hold a group of x and of dy; a warp keeps its lanes' dwq, dwk in registers.
 template <bool INTER, int LPR, typename T>
 __global__ void __launch_bounds__(RO_NT, 2) k_qk_norm_rope_bwd(RopeArgs ar) {
-  __shared__ __align__(16) float s_cs[RO_W][RO_MAXD];
-  __shared__ float red[RO_W][RO_MAXD];
+  extern __shared__ __align__(16) char smem[];
+  constexpr int U = RO_GU, RPL = 32 / LPR, SE = 32 * 8;
+  constexpr int NST = RO_RING / (2 * U * SE * (int)sizeof(T));
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LPR;
   const int e = (lane & (LPR - 1)) * 8;
-  constexpr int UNR = sizeof(T) == 2 ? RO_UNR : RO_UNR / 2;
-  F2 dw[2][4];
+  T* ring = reinterpret_cast<T*>(smem + warp * RO_RING);
+  float* cs = reinterpret_cast<float*>(smem + RO_W * RO_RING) + warp * RO_MAXD;
+  const int groups = ar.gq + ar.gk;
+  int64_t left, last;
+  share(ar, groups, &left, &last);
+  Place load{left / groups, (int)(left % groups)}, at = load;
+  left = last - left;
+  int64_t ahead = left;
+  const int other = INTER ? 0 : other_lane(ar, e);
+  const int mine = lane * 8, theirs = (lane / LPR * LPR + other) * 8;
+  auto issue = [&](int stage) {
+    if (ahead-- > 0) {
+      const Heads x = heads_of<LPR, U>(ar, load.g);
+      const bool isq = x.kind == 0;
+      const T* xs = reinterpret_cast<const T*>(isq ? ar.q : ar.k);
+      const T* gs = reinterpret_cast<const T*>(isq ? ar.dq_out : ar.dk_out);
+      const T* xr = xs + load.n * (isq ? ar.qs : ar.ks) + x.h * ar.D + e;
+      const T* gr = gs + (load.n * (isq ? ar.Hq : ar.Hk) + x.h) * ar.D + e;
+      T* dst = ring + stage * 2 * U * SE + mine;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool in = x.h + u * RPL < x.end;
+        copy8(dst + 2 * u * SE, in ? xr + u * RPL * ar.D : xs, in);
+        copy8(dst + (2 * u + 1) * SE, in ? gr + u * RPL * ar.D : gs, in);
+      }
+      load.next(groups);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  for (int i = 0; i < NST - 1; ++i) issue(i);
+  F2 C[4], S[4], W[4], dw[2][4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) dw[0][j] = dw[1][j] = f2(0.f, 0.f);
-  for (int64_t task = (int64_t)blockIdx.x * RO_W + warp; task < ar.N * ar.chunks;
-       task += (int64_t)gridDim.x * RO_W) {
-    const int64_t n = task / ar.chunks;
-    const int h0 = (int)(task % ar.chunks) * ar.chunk, h1 = min(h0 + ar.chunk, ar.heads);
-    bool have = false;
-    if (h0 < ar.Hq)
-      grad_heads<INTER, LPR, UNR>(ar, reinterpret_cast<const T*>(ar.q) + n * ar.qs,
-                                  reinterpret_cast<const T*>(ar.dq_out) + n * ar.Hq * ar.D,
-                                  reinterpret_cast<T*>(ar.q_out) + n * ar.Hq * ar.D, ar.wq, h0,
-                                  min(h1, ar.Hq), n, s_cs[warp], &have, dw[0]);
-    const int k0 = max(h0 - ar.Hq, 0), k1 = h1 - ar.Hq;
-    if (k0 < k1)
-      grad_heads<INTER, LPR, UNR>(ar, reinterpret_cast<const T*>(ar.k) + n * ar.ks,
-                                  reinterpret_cast<const T*>(ar.dk_out) + n * ar.Hk * ar.D,
-                                  reinterpret_cast<T*>(ar.k_out) + n * ar.Hk * ar.D, ar.wk, k0,
-                                  k1, n, s_cs[warp], &have, dw[1]);
+  int64_t n = -1;
+  int kind = -1, stage = 0;
+  for (; left > 0; --left, at.next(groups)) {
+    const Heads hd = heads_of<LPR, U>(ar, at.g);
+    if (at.n != n || hd.kind != kind) {
+      if (at.n != n) {
+        angles(ar, at.n, cs);
+        float c[8], s[8];
+        turn<INTER>(ar, cs, e, -1.f, c, s);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          C[j] = f2(c[2 * j], c[2 * j + 1]);
+          S[j] = f2(s[2 * j], s[2 * j + 1]);
+        }
+      }
+      if (hd.kind != kind) {
+        float wv[8] = {};
+        if (e < ar.D) ld8((hd.kind == 0 ? ar.wq : ar.wk) + e, wv);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) W[j] = f2(wv[2 * j], wv[2 * j + 1]);
+      }
+      n = at.n;
+      kind = hd.kind;
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(NST - 2) : "memory");
+    __syncwarp();
+    issue(stage == 0 ? NST - 1 : stage - 1);
+    const T* in = ring + stage * 2 * U * SE;
+    stage = stage == NST - 1 ? 0 : stage + 1;
+    F2 x[U][4], g[U][4], t[U][4];
+    float ss[U], dot[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      F2 y[4];
+      get(in + 2 * u * SE + mine, x[u]);
+      get(in + (2 * u + 1) * SE + mine, g[u]);
+      if constexpr (INTER) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 a = un(g[u][j]);
+          y[j] = f2(a.y, a.x);
+        }
+      } else {
+        get(in + (2 * u + 1) * SE + theirs, y);
+      }
+      F2 sq = f2(0.f, 0.f), dt = sq;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sq = fma(x[u][j], x[u][j], sq);
+        g[u][j] = fma(y[j], S[j], mul(g[u][j], C[j]));  // dn
+        t[u][j] = mul(g[u][j], x[u][j]);
+        g[u][j] = mul(g[u][j], W[j]);
+        dt = fma(g[u][j], x[u][j], dt);
+      }
+      const float2 s2 = un(sq), d2 = un(dt);
+      ss[u] = s2.x + s2.y;
+      dot[u] = d2.x + d2.y;
+    }
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1)
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        ss[u] += __shfl_xor_sync(0xffffffffu, ss[u], o);
+        dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], o);
+      }
+    T* out = reinterpret_cast<T*>(kind == 0 ? ar.q_out : ar.k_out);
+    out += (at.n * (kind == 0 ? ar.Hq : ar.Hk) + hd.h) * ar.D + e;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float f = rsqrtf(fmaf(ss[u], ar.inv_d, ar.eps));
+      const float m = -(dot[u] * ar.inv_d) * f * f * f;
+      const F2 ff = f2(f, f), mm = f2(m, m);
+      if (kind == 0) {  // lanes without a head hold zeros
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dw[0][j] = fma(t[u][j], ff, dw[0][j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dw[1][j] = fma(t[u][j], ff, dw[1][j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) g[u][j] = fma(x[u][j], mm, mul(g[u][j], ff));
+      if (hd.h + u * RPL < hd.end) put(out + u * RPL * ar.D, g[u]);
+    }
   }
-  for (int z = 0; z < 2; ++z) {  // this CTA's dwq, dwk: lanes of equal elements, then warps in order
+  // this CTA's dwq, dwk: lanes of equal elements, then the warps in order (cs is free now)
+  float* red = reinterpret_cast<float*>(smem + RO_W * RO_RING);
+  for (int z = 0; z < 2; ++z) {
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -433,16 +475,14 @@ __global__ void __launch_bounds__(RO_NT, 2) k_qk_norm_rope_bwd(RopeArgs ar) {
         d.x += __shfl_xor_sync(0xffffffffu, d.x, o);
         d.y += __shfl_xor_sync(0xffffffffu, d.y, o);
       }
-      if (e < ar.D && sub == 0) {
-        red[warp][e + 2 * j] = d.x;
-        red[warp][e + 2 * j + 1] = d.y;
-      }
+      if (e < ar.D && sub == 0)
+        *reinterpret_cast<float2*>(red + warp * RO_MAXD + e + 2 * j) = d;
     }
     __syncthreads();
     for (int c = threadIdx.x; c < ar.D; c += RO_NT) {
       float s = 0.f;
 #pragma unroll
-      for (int w = 0; w < RO_W; ++w) s += red[w][c];
+      for (int w = 0; w < RO_W; ++w) s += red[w * RO_MAXD + c];
       ar.part[((int64_t)blockIdx.x * 2 + z) * ar.D + c] = s;
     }
   }
@@ -515,23 +555,26 @@ bool inputs_ok(const RopeArgs& ar, const void* q, const void* k, const float* wq
          ok16(inv_freq, ar.R) && ok4(pos);
 }
 
-// Splits the heads of a token over warps: all of them to one warp when the tokens alone fill
-// the GPU, else runs of whole load groups.
-void split_heads(RopeArgs* ar, int heads) {
-  const int rpl = ar->D > 128 ? 1 : ar->D > 64 ? 2 : 4, group = rpl;
-  ar->heads = heads;
-  int64_t warps = ar->N > 0 ? (RO_FILL + ar->N - 1) / ar->N : 1;  // wanted per token
-  const int64_t most = (heads + group - 1) / group;
-  if (warps > most) warps = most;
-  if (warps < 1) warps = 1;
-  const int64_t chunk = (heads + warps - 1) / warps;
-  ar->chunk = (int)((chunk + group - 1) / group * group);
-  ar->chunks = (heads + ar->chunk - 1) / ar->chunk;
+// Groups of a token's heads; CTAs of a call (a warp has at least one group).
+void set_groups(RopeArgs* ar, int u, bool cache) {
+  const int rpl = (ar->D > 128 ? 1 : ar->D > 64 ? 2 : 4) * u;
+  ar->gq = (ar->Hq + rpl - 1) / rpl;
+  ar->gk = (ar->Hk + rpl - 1) / rpl;
+  ar->gv = cache ? ar->gk : 0;
+}
+int64_t ctas_of(const RopeArgs& ar) {
+  const int64_t n = (ar.N * (ar.gq + ar.gk + ar.gv) + RO_W - 1) / RO_W;
+  return n < RO_CTAS ? n : RO_CTAS;
 }
 
-int64_t bwd_ctas(const RopeArgs& ar) {
-  const int64_t n = (ar.N * ar.chunks + RO_W - 1) / RO_W;
-  return n < RO_BCTAS ? n : RO_BCTAS;
+// The kernels' dynamic shared memory is above the default limit: raised per kernel and call (a
+// host-side attribute of the current device's function, set to the same value every time).
+template <typename K>
+cudaError_t launch(K kernel, const RopeArgs& ar, cudaStream_t st) {
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RO_SMEM);
+  if (e != cudaSuccess) return e;
+  kernel<<<(unsigned)ctas_of(ar), RO_NT, RO_SMEM, st>>>(ar);
+  return cudaGetLastError();
 }
 
 // Runs f with the lanes per row, the pairing and the type as template arguments.
@@ -551,12 +594,13 @@ void with_types(const RopeArgs& ar, int dtype, F f) {
 }
 
 template <bool CACHE>
-gdn_status launch_fwd(const RopeArgs& ar, int dtype, cudaStream_t st) {
-  const unsigned ctas = (unsigned)((ar.N * ar.chunks + RO_W - 1) / RO_W);
+gdn_status launch_fwd(RopeArgs& ar, int dtype, cudaStream_t st) {
+  set_groups(&ar, RO_FU, CACHE);
+  cudaError_t e = cudaSuccess;
   with_types(ar, dtype, [&](auto lpr, auto inter, auto t) {
-    k_qk_norm_rope_fwd<CACHE, inter(), lpr(), decltype(t)><<<ctas, RO_NT, 0, st>>>(ar);
+    e = launch(k_qk_norm_rope_fwd<CACHE, inter(), lpr(), decltype(t)>, ar, st);
   });
-  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 }  // namespace
@@ -585,7 +629,6 @@ gdn_status gdn_qk_norm_rope_fwd(const gdn_rope_problem* p, const void* q, const 
   ar.pos = positions;
   ar.q_out = q_out;
   ar.k_out = k_out;
-  split_heads(&ar, ar.Hq + ar.Hk);
   return launch_fwd<false>(ar, p->dtype, (cudaStream_t)stream);
 }
 
@@ -617,7 +660,6 @@ gdn_status gdn_qk_norm_rope_cache(const gdn_rope_problem* p, const void* q, cons
   ar.k_out = k_cache;
   ar.v_out = v_cache;
   ar.status = status;
-  split_heads(&ar, ar.Hq + 2 * ar.Hk);
   return launch_fwd<true>(ar, p->dtype, (cudaStream_t)stream);
 }
 
@@ -626,8 +668,8 @@ gdn_status gdn_qk_norm_rope_bwd_workspace_size(const gdn_rope_problem* p, size_t
   RopeArgs ar;
   gdn_status s = check_problem(p, &ar);
   if (s != GDN_OK) return s;
-  split_heads(&ar, ar.Hq + ar.Hk);
-  *bytes = (size_t)bwd_ctas(ar) * 2 * (size_t)ar.D * sizeof(float);
+  set_groups(&ar, RO_GU, false);
+  *bytes = (size_t)ctas_of(ar) * 2 * (size_t)ar.D * sizeof(float);
   return GDN_OK;
 }
 
@@ -643,8 +685,8 @@ gdn_status gdn_qk_norm_rope_bwd(const gdn_rope_problem* p, const void* q, const 
       !ok16(dk_out, ar.N * ar.Hk) || !ok16(dq, ar.N * ar.Hq) || !ok16(dk, ar.N * ar.Hk) ||
       !ok16(dwq, ar.Hq) || !ok16(dwk, ar.Hk))
     return GDN_ERR_INVALID_ARG;
-  split_heads(&ar, ar.Hq + ar.Hk);
-  const int64_t ctas = bwd_ctas(ar);
+  set_groups(&ar, RO_GU, false);
+  const int64_t ctas = ctas_of(ar);
   const size_t need = (size_t)ctas * 2 * (size_t)ar.D * sizeof(float);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
     return GDN_ERR_WORKSPACE;
@@ -661,10 +703,11 @@ gdn_status gdn_qk_norm_rope_bwd(const gdn_rope_problem* p, const void* q, const 
   ar.part = (float*)workspace;
   cudaStream_t st = (cudaStream_t)stream;
   if (ctas > 0) {
+    cudaError_t e = cudaSuccess;
     with_types(ar, p->dtype, [&](auto lpr, auto inter, auto t) {
-      k_qk_norm_rope_bwd<inter(), lpr(), decltype(t)><<<(unsigned)ctas, RO_NT, 0, st>>>(ar);
+      e = launch(k_qk_norm_rope_bwd<inter(), lpr(), decltype(t)>, ar, st);
     });
-    if (cudaGetLastError() != cudaSuccess) return GDN_ERR_CUDA;
+    if (e != cudaSuccess) return GDN_ERR_CUDA;
   }
   k_qk_norm_rope_dw<<<(unsigned)((2 * ar.D + 31) / 32), RO_NT, 0, st>>>(
       (int)ctas, ar.D, (const float*)workspace, ar.Hq ? dwq : nullptr, ar.Hk ? dwk : nullptr);
