@@ -862,6 +862,16 @@ def gdn_varlen_check_device_status(ws, problem: Problem, cu: Varlen, op: int,
 # These calls check what the C side cannot see (type, shape, layout and device of every
 # tensor) and run on the current stream of the tensors' device, whichever device is current.
 
+# The host's share of a small call is most of its time (a launch is about 3 us, an allocation
+# 1.5 us), so the checks read each property once and outputs made here are not checked again.
+
+try:  # the stream's address without a Stream object (1 us per call)
+    from torch._C import _cuda_getCurrentRawStream as _current_raw_stream
+except ImportError:
+    def _current_raw_stream(dev):
+        return torch.cuda.current_stream(dev).cuda_stream
+
+
 def _arg(name, t, dev, dtype, shape):
     """Address of a contiguous tensor of this type and shape on device `dev`."""
     if (t.get_device() != dev or t.dtype is not dtype or t.shape != shape
@@ -870,6 +880,14 @@ def _arg(name, t, dev, dtype, shape):
             f"{name}: expected a contiguous {dtype} tensor {list(shape)} on cuda:{dev}, got "
             f"{t.dtype} {list(t.shape)} with strides {list(t.stride())} on {t.device}")
     return t.data_ptr()
+
+
+def _out(name, t, dev, dtype, shape, device):
+    """(output, its address): the caller's, checked, or a new one."""
+    if t is not None:
+        return t, _arg(name, t, dev, dtype, shape)
+    t = torch.empty(shape, dtype=dtype, device=device)
+    return t, t.data_ptr()
 
 
 def _flat(name, t, dev, n):
@@ -882,26 +900,29 @@ def _flat(name, t, dev, n):
 
 
 def _rows(name, t, dev, dtype, shape):
-    """(address, elements between tokens) of [..., heads, D] whose rows of one token are
-    contiguous and whose tokens are evenly spaced (a slice of a fused projection, say)."""
-    st, sh = t.stride(), t.shape
+    """(address, elements between tokens; 0: contiguous) of [..., heads, D] whose rows of one
+    token are contiguous and whose tokens are evenly spaced (a slice of a fused projection)."""
+    sh = t.shape
     if t.get_device() != dev or t.dtype is not dtype or sh != shape:
         raise ValueError(f"{name}: expected a {dtype} tensor {list(shape)} on cuda:{dev}, got "
                          f"{t.dtype} {list(sh)} on {t.device}")
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    st = t.stride()
     heads, D = sh[-2], sh[-1]
     ok = (st[-1] == 1 or D == 1) and (st[-2] == D or heads == 1)
-    step, span = None, 1
+    step, span = 0, 1
     for n, s in zip(reversed(sh[:-2]), reversed(st[:-2])):
         if n == 1:
             continue
-        if step is None:
+        if span == 1:
             step = s
         ok = ok and s == step * span
         span *= n
-    if not ok and t.numel():
+    if not ok:
         raise ValueError(f"{name}: the elements of a token have to be contiguous and the tokens "
                          f"evenly spaced, got strides {list(st)} for {list(sh)}")
-    return t.data_ptr(), (step if step is not None and t.numel() else 0)
+    return t.data_ptr(), step
 
 
 def _device_of(t):
@@ -912,17 +933,19 @@ def _device_of(t):
 
 
 def _call(name, dev, *args):
-    """Call a library function with the raw stream appended, `dev` current meanwhile."""
+    """Call a library function with `dev` current meanwhile."""
     fn = getattr(_lib or load_library(), name)
     if torch.cuda.current_device() == dev:
-        _check(name, fn(*args))
+        status = fn(*args)
     else:
         with torch.cuda.device(dev):
-            _check(name, fn(*args))
+            status = fn(*args)
+    if status != GDN_OK:
+        raise GDNError(name, status)
 
 
 def _raw_stream(stream, dev):
-    return (stream or torch.cuda.current_stream(dev)).cuda_stream
+    return _current_raw_stream(dev) if stream is None else stream.cuda_stream
 
 
 def status_word(device="cuda") -> torch.Tensor:
@@ -948,26 +971,22 @@ def gdn_step(q, k, v, a, b, A_log, dt_bias, state, slots=None, *, l2norm=True, e
     if T != 1:
         raise ValueError(f"gdn_step takes one token per row, got {T}")
     p = Problem(_dtype_code(dt), 64, B, 1, 0, Hqk, H, dk, dv, 1 if l2norm else 0, eps, scale, 0)
-    gates = (B, 1, H)
-    if o is None:
-        o = torch.empty((B, 1, H, dv), dtype=dt, device=q.device)
+    qk, vs, gates, f32 = (B, 1, Hqk, dk), (B, 1, H, dv), (B, 1, H), torch.float32
+    o, op = _out("o", o, dev, dt, vs, q.device)
     _call("gdn_step", dev, p, n,
           None if slots is None else _arg("slots", slots, dev, torch.int32, (B,)),
-          _arg("q", q, dev, dt, (B, 1, Hqk, dk)), _arg("k", k, dev, dt, (B, 1, Hqk, dk)),
-          _arg("v", v, dev, dt, (B, 1, H, dv)), _arg("a", a, dev, dt, gates),
-          _arg("b", b, dev, dt, gates), _arg("A_log", A_log, dev, torch.float32, (H,)),
-          _arg("dt_bias", dt_bias, dev, torch.float32, (H,)),
-          _arg("state", state, dev, torch.float32, (n, H, dk, dv)),
-          _arg("o", o, dev, dt, (B, 1, H, dv)), _status(status, dev), _raw_stream(stream, dev))
+          _arg("q", q, dev, dt, qk), _arg("k", k, dev, dt, qk), _arg("v", v, dev, dt, vs),
+          _arg("a", a, dev, dt, gates), _arg("b", b, dev, dt, gates),
+          _arg("A_log", A_log, dev, f32, (H,)), _arg("dt_bias", dt_bias, dev, f32, (H,)),
+          _arg("state", state, dev, f32, (n, H, dk, dv)), op, _status(status, dev),
+          _raw_stream(stream, dev))
     return o
 
 
 def _rope_problem(q, k, v, dev, inv_freq, T, interleaved, eps, rope_scale):
     """(problem, addresses of q, k and v) for q [..., Hq, D], k, v [..., Hk, D]."""
     lead, D = q.shape[:-2], q.shape[-1]
-    N = 1
-    for n in lead:
-        N *= n
+    N = lead[0] if len(lead) == 1 else lead.numel()
     Hq, Hk = q.shape[-2], k.shape[-2]
     qp, qs = _rows("q", q, dev, q.dtype, q.shape)
     kp, ks = _rows("k", k, dev, q.dtype, lead + (Hk, D))
@@ -995,14 +1014,10 @@ def gdn_qk_norm_rope_fwd(q, k, wq, wk, inv_freq, positions=None, *, T=None, inte
     at n).  q and k may be slices of one projection.  Returns (q_out, k_out), contiguous."""
     dev, dt = _device_of(q), q.dtype
     p, qp, kp, _ = _rope_problem(q, k, None, dev, inv_freq, T, interleaved, eps, rope_scale)
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=dt, device=q.device)
-    if k_out is None:
-        k_out = torch.empty(k.shape, dtype=dt, device=q.device)
+    q_out, qo = _out("q_out", q_out, dev, dt, q.shape, q.device)
+    k_out, ko = _out("k_out", k_out, dev, dt, k.shape, q.device)
     _call("gdn_qk_norm_rope_fwd", dev, p, qp, kp,
-          *_rope_tables(wq, wk, inv_freq, positions, p, dev),
-          _arg("q_out", q_out, dev, dt, q.shape), _arg("k_out", k_out, dev, dt, k.shape),
-          _raw_stream(stream, dev))
+          *_rope_tables(wq, wk, inv_freq, positions, p, dev), qo, ko, _raw_stream(stream, dev))
     return q_out, k_out
 
 
@@ -1019,19 +1034,16 @@ def gdn_qk_norm_rope_bwd(q, k, wq, wk, inv_freq, positions, dq_out, dk_out, *, T
     """Backward of gdn_qk_norm_rope_fwd: (dq, dk contiguous in q's type, dwq, dwk [D] fp32)."""
     dev, dt, f32 = _device_of(q), q.dtype, torch.float32
     p, qp, kp, _ = _rope_problem(q, k, None, dev, inv_freq, T, interleaved, eps, rope_scale)
-    dq = torch.empty(q.shape, dtype=dt, device=q.device) if dq is None else dq
-    dk = torch.empty(k.shape, dtype=dt, device=q.device) if dk is None else dk
-    dwq = torch.empty(p.D, dtype=f32, device=q.device) if dwq is None else dwq
-    dwk = torch.empty(p.D, dtype=f32, device=q.device) if dwk is None else dwk
-    if ws is None:
-        ws = torch.empty(max(gdn_qk_norm_rope_bwd_workspace_size(p), 16), dtype=torch.uint8,
-                         device=q.device)
+    dq, dqp = _out("dq", dq, dev, dt, q.shape, q.device)
+    dk, dkp = _out("dk", dk, dev, dt, k.shape, q.device)
+    dwq, wqp = _out("dwq", dwq, dev, f32, (p.D,), q.device)
+    dwk, wkp = _out("dwk", dwk, dev, f32, (p.D,), q.device)
+    n = gdn_qk_norm_rope_bwd_workspace_size(p) if ws is None else ws.numel()
+    ws, wsp = _out("ws", ws, dev, torch.uint8, (n,), q.device)
     _call("gdn_qk_norm_rope_bwd", dev, p, qp, kp,
           *_rope_tables(wq, wk, inv_freq, positions, p, dev),
           _arg("dq_out", dq_out, dev, dt, q.shape), _arg("dk_out", dk_out, dev, dt, k.shape),
-          _arg("dq", dq, dev, dt, q.shape), _arg("dk", dk, dev, dt, k.shape),
-          _arg("dwq", dwq, dev, f32, (p.D,)), _arg("dwk", dwk, dev, f32, (p.D,)),
-          _arg("ws", ws, dev, torch.uint8, ws.shape), ws.numel(), _raw_stream(stream, dev))
+          dqp, dkp, wqp, wkp, wsp, n, _raw_stream(stream, dev))
     return dq, dk, dwq, dwk
 
 
@@ -1043,17 +1055,13 @@ def gdn_qk_norm_rope_cache(q, k, v, wq, wk, inv_freq, positions, slots, k_cache,
     [pages, page_size, Hk, D].  Returns q_out."""
     dev, dt = _device_of(q), q.dtype
     p, qp, kp, vp = _rope_problem(q, k, v, dev, inv_freq, T, interleaved, eps, rope_scale)
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=dt, device=q.device)
+    q_out, qo = _out("q_out", q_out, dev, dt, q.shape, q.device)
     cache = k_cache.shape[:-2] + (p.Hk, p.D)
-    n_slots = 1
-    for n in cache[:-2]:
-        n_slots *= n
     _call("gdn_qk_norm_rope_cache", dev, p, qp, kp, vp,
-          *_rope_tables(wq, wk, inv_freq, positions, p, dev), n_slots,
-          _flat("slots", slots, dev, p.N), _arg("q_out", q_out, dev, dt, q.shape),
-          _arg("k_cache", k_cache, dev, dt, cache), _arg("v_cache", v_cache, dev, dt, cache),
-          _status(status, dev), _raw_stream(stream, dev))
+          *_rope_tables(wq, wk, inv_freq, positions, p, dev), k_cache.shape[:-2].numel(),
+          _flat("slots", slots, dev, p.N), qo, _arg("k_cache", k_cache, dev, dt, cache),
+          _arg("v_cache", v_cache, dev, dt, cache), _status(status, dev),
+          _raw_stream(stream, dev))
     return q_out
 
 
@@ -1076,20 +1084,18 @@ def gdn_attn_decode(q, k_cache, v_cache, block_table, seq_len, *, scale=0.0, o=N
     qp, qs = _rows("q", q, dev, dt, q.shape)
     blocks = block_table.shape[1]
     p = AttnProblem(_dtype_code(dt), D, P, scale, B, Hq, Hk, pages, blocks, qs)
-    if o is None:
-        o = torch.empty((B, Hq, D), dtype=dt, device=q.device)
-    if lse is None and want_lse:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device)
-    if ws is None:
-        ws = torch.empty(gdn_attn_decode_workspace_size(p), dtype=torch.uint8, device=q.device)
+    o, op = _out("o", o, dev, dt, (B, Hq, D), q.device)
+    lp = None
+    if lse is not None or want_lse:
+        lse, lp = _out("lse", lse, dev, torch.float32, (B, Hq), q.device)
+    n = gdn_attn_decode_workspace_size(p) if ws is None else ws.numel()
+    ws, wsp = _out("ws", ws, dev, torch.uint8, (n,), q.device)
     cache = (pages, P, Hk, D)
     _call("gdn_attn_decode", dev, p, qp, _arg("k_cache", k_cache, dev, dt, cache),
           _arg("v_cache", v_cache, dev, dt, cache),
           _arg("block_table", block_table, dev, torch.int32, (B, blocks)),
-          _arg("seq_len", seq_len, dev, torch.int32, (B,)), _arg("o", o, dev, dt, (B, Hq, D)),
-          None if lse is None else _arg("lse", lse, dev, torch.float32, (B, Hq)),
-          _arg("ws", ws, dev, torch.uint8, ws.shape), ws.numel(), _status(status, dev),
-          _raw_stream(stream, dev))
+          _arg("seq_len", seq_len, dev, torch.int32, (B,)), op, lp, wsp, n,
+          _status(status, dev), _raw_stream(stream, dev))
     return o, lse
 
 
@@ -1103,19 +1109,16 @@ def gdn_slot_map(ctx_len, new_len, free_pages, block_table, *, page_size, pages,
     B, blocks = block_table.shape
     n_free = free_pages.numel()
 
-    def out(t, n):
-        return torch.empty(n, dtype=i32, device=ctx_len.device) if t is None else t
-
-    seq_len, cu_seqlens, used = out(seq_len, B), out(cu_seqlens, B + 1), out(used, 1)
-    positions, slots = out(positions, n_tokens), out(slots, n_tokens)
+    d = ctx_len.device
+    seq_len, sp = _out("seq_len", seq_len, dev, i32, (B,), d)
+    cu_seqlens, cp = _out("cu_seqlens", cu_seqlens, dev, i32, (B + 1,), d)
+    positions, pp = _out("positions", positions, dev, i32, (n_tokens,), d)
+    slots, lp = _out("slots", slots, dev, i32, (n_tokens,), d)
+    used, up = _out("used", used, dev, i32, (1,), d)
     p = SlotProblem(page_size, 0, B, blocks, pages, n_free, n_tokens)
     _call("gdn_slot_map", dev, p, _arg("ctx_len", ctx_len, dev, i32, (B,)),
           _arg("new_len", new_len, dev, i32, (B,)),
           _arg("free_pages", free_pages, dev, i32, (n_free,)),
-          _arg("block_table", block_table, dev, i32, (B, blocks)),
-          _arg("seq_len", seq_len, dev, i32, (B,)),
-          _arg("cu_seqlens", cu_seqlens, dev, i32, (B + 1,)),
-          _arg("positions", positions, dev, i32, (n_tokens,)),
-          _arg("slots", slots, dev, i32, (n_tokens,)), _arg("used", used, dev, i32, (1,)),
+          _arg("block_table", block_table, dev, i32, (B, blocks)), sp, cp, pp, lp, up,
           _status(status, dev), _raw_stream(stream, dev))
     return seq_len, cu_seqlens, positions, slots, used

@@ -40,6 +40,9 @@ constexpr int AT_W = 4;            // warps per CTA
 constexpr int AT_NT = 32 * AT_W;
 constexpr int AT_G = 8;            // query heads per piece
 constexpr int AT_SMS = 152;
+// What a piece costs beside its tiles, in units (its first loads and its end): without it a
+// CTA with many short requests lags (61 ragged requests 128 against 102 us; 2 to 5 units: the same).
+constexpr int AT_START = 1;
 
 // Keys per warp tile and CTAs per SM: the K and V tiles and the accumulators of D x 8 fill
 // most of a CTA's share of the registers.
@@ -508,7 +511,10 @@ __global__ void __launch_bounds__(AT_NT, Cfg<D, T>::kCtas) k_attn_decode(AttnArg
     return (int)(n < 0 ? 0 : n > cap ? cap : n);
   };
   auto tiles = [&](int n) { return n > 0 ? (n - 1) / TK + 1 : 0; };
-  auto units = [&](int64_t b) { return tiles(length(b)) * per; };
+  auto units = [&](int64_t b) {
+    const int n = tiles(length(b));
+    return n > 0 ? (n + AT_START) * per : 0;
+  };
   // the units of all requests, and this CTA's share of them
   int64_t W = 0, first = 0;
   for (int64_t b0 = 0; b0 < ar.B; b0 += AT_NT) {
@@ -545,67 +551,182 @@ __global__ void __launch_bounds__(AT_NT, Cfg<D, T>::kCtas) k_attn_decode(AttnArg
     }
     __syncthreads();
     int64_t b = s_b, u = u0;
-    int n = length(b), nt = tiles(n);
-    int h = (int)(s_r / nt), t0 = (int)(s_r % nt);  // piece of the request, unit in it
+    int n = length(b), nt = tiles(n), w = nt + AT_START;
+    int h = (int)(s_r / w), r0 = (int)(s_r % w);  // piece of the request, unit in it
     while (u < u1) {
-      const int t1 = (int)(u1 - u < nt - t0 ? t0 + (u1 - u) : nt);
-      const int hk = h / ar.HG, hg = h % ar.HG, heads = min(AT_G, ar.G - hg * AT_G);
-      const int h0 = hk * ar.G + hg * AT_G;
-      Acc<D> a;
-      piece<D, T>(ar, smem, b, n, hk, hg, t0, t1, a, &bad);
-      const int64_t slot = t0 == 0 && t1 == nt ? -1 : t0 == 0 ? 2 * c + 1 : 2 * c;
-      finish<D, T>(ar, smem, ml, b, h0, heads, a, slot);
-      if (t0 == 0 && t1 < nt && tid == 0) {
-        const int64_t end = u + nt - 1;  // its last unit: the CTA with W c / C <= end
-        ar.join[c] = Join{(int32_t)b, h0, heads, (int32_t)(((end + 1) * C - 1) / W)};
+      const int r1 = (int)(u1 - u < w - r0 ? r0 + (u1 - u) : w);
+      const int t0 = max(0, r0 - AT_START), t1 = max(0, r1 - AT_START);
+      if (t0 < t1) {
+        const int hk = h / ar.HG, hg = h % ar.HG, heads = min(AT_G, ar.G - hg * AT_G);
+        const int h0 = hk * ar.G + hg * AT_G;
+        Acc<D> a;
+        piece<D, T>(ar, smem, b, n, hk, hg, t0, t1, a, &bad);
+        const int64_t slot = t0 == 0 && t1 == nt ? -1 : t0 == 0 ? 2 * c + 1 : 2 * c;
+        finish<D, T>(ar, smem, ml, b, h0, heads, a, slot);
+        if (t0 == 0 && t1 < nt && tid == 0) {
+          const int64_t end = u - r0 + w - 1;  // its last unit: of the CTA with W c / C <= end
+          ar.join[c] = Join{(int32_t)b, h0, heads, (int32_t)(((end + 1) * C - 1) / W)};
+        }
       }
-      u += t1 - t0;
-      t0 = 0;
+      u += r1 - r0;
+      r0 = 0;
       if (u < u1 && ++h == per) {
         h = 0;
         do n = length(++b); while (n == 0);
         nt = tiles(n);
+        w = nt + AT_START;
       }
     }
   }
   if (bad && ar.status) atomicOr(ar.status, kStatusClamped);
 }
 
-// Adds up the partial pieces of one (request, key head): CTA (c, h) for the piece that began in
-// CTA c of the pass above, query head h of it.  4 groups of D threads take every fourth part.
-template <int D, typename T>
-__global__ void __launch_bounds__(4 * D) k_attn_join(AttnArgs ar) {
-  __shared__ float s_o[4][D], s_m[4], s_l[4];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t c = blockIdx.x;
-  const int h = blockIdx.y, d = threadIdx.x % D, w = threadIdx.x / D;
-  const Join j = ar.join[c];
-  if (j.h < 0 || h >= j.heads) return;
-  const int n = (int)(j.last - c) + 1;  // parts: slot 2c + 1, then slot 2i of the CTAs behind
-  auto slot = [&](int i) { return (i == 0 ? 2 * c + 1 : 2 * (c + i)) * AT_G + h; };
-  float m = -INFINITY, l = 0.f, o = 0.f;
-  for (int i = w; i < n; i += 4) m = fmaxf(m, ar.ml[slot(i)].x);
-  if (d == 0) s_m[w] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll 4
-  for (int i = w; i < n; i += 4) {
-    const float2 x = ar.ml[slot(i)];
-    const float f = ex2(x.x - base);
-    l = fmaf(x.y, f, l);
-    o = fmaf(ar.acc[slot(i) * D + d], f, o);
+constexpr int AJ_NT = 256;
+constexpr int AJ_FEW = 8;   // parts that one warp adds up by itself
+constexpr int AJ_DC = 64;   // columns of a CTA's item
+constexpr int AJ_CTAS = 2 * AT_SMS;
+
+template <typename T>
+__device__ __forceinline__ void store_o(T* o, float4 x, float r) {
+  if constexpr (sizeof(T) == 2) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x.x * r, x.y * r);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x.z * r, x.w * r);
+    *reinterpret_cast<uint2*>(o) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                              *reinterpret_cast<const uint32_t*>(&b));
+  } else {
+    *reinterpret_cast<float4*>(o) = make_float4(x.x * r, x.y * r, x.z * r, x.w * r);
   }
-  s_o[w][d] = o;
-  if (d == 0) s_l[w] = l;
-  __syncthreads();
-  if (w > 0) return;
-  o = (s_o[0][d] + s_o[1][d]) + (s_o[2][d] + s_o[3][d]);
-  l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
-  const float r = l != 0.f ? 1.f / l : 0.f;
-  const int64_t row = (int64_t)j.b * ar.Hq + j.h + h;
-  reinterpret_cast<T*>(ar.o)[row * D + d] = (T)(o * r);
-  if (d == 0 && ar.lse) ar.lse[row] = (base + log2f(l)) * 0.69314718055994531f;
+}
+__device__ __forceinline__ void add_scaled(float4& a, const float4& x, float f) {
+  a.x = fmaf(x.x, f, a.x);
+  a.y = fmaf(x.y, f, a.y);
+  a.z = fmaf(x.z, f, a.z);
+  a.w = fmaf(x.w, f, a.w);
+}
+
+// Adds up the parts of the pieces that were split.  Each CTA collects the list of those pieces
+// (at most one begins in a CTA of the pass above).  A piece of few parts (a batch: hundreds of
+// pieces of 2 or 3) takes one warp per query head; one of many parts (a few long requests)
+// takes a CTA per query head and AJ_DC columns, 16 threads a row of columns, 16 parts at a time.
+template <int D, typename T>
+__global__ void __launch_bounds__(AJ_NT) k_attn_join(AttnArgs ar, int ctas) {
+  constexpr int MAXC = AT_SMS * 4, NW = AJ_NT / 32;
+  __shared__ Join s_list[MAXC];
+  __shared__ int16_t s_c[MAXC];
+  __shared__ int2 s_n[NW];
+  __shared__ float s_w[MAXC + 1], s_red[NW][2];
+  __shared__ float4 s_o[AJ_NT / 16][AJ_DC / 4];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // pieces of few parts from the front of the list, of many from its end, in the order of the CTAs
+  // (every CTA here makes the same list)
+  int n_few = 0, n_many = 0;
+  for (int c0 = 0; c0 < ctas; c0 += AJ_NT) {
+    const int c = c0 + tid;
+    const Join j = c < ctas ? ar.join[c] : Join{0, -1, 0, 0};
+    const bool few = j.h >= 0 && j.last - c < AJ_FEW, many = j.h >= 0 && !few;
+    const unsigned bf = __ballot_sync(0xffffffffu, few), bm = __ballot_sync(0xffffffffu, many);
+    if (lane == 0) s_n[warp] = make_int2(__popc(bf), __popc(bm));
+    __syncthreads();
+    const unsigned below = (1u << lane) - 1u;
+    int2 at = make_int2(n_few + __popc(bf & below), n_many + __popc(bm & below));
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const int2 y = s_n[w];
+      if (w < warp) {
+        at.x += y.x;
+        at.y += y.y;
+      }
+      n_few += y.x;
+      n_many += y.y;
+    }
+    if (j.h >= 0) {
+      const int i = few ? at.x : MAXC - 1 - at.y;
+      s_list[i] = j;
+      s_c[i] = (int16_t)c;
+    }
+    __syncthreads();
+  }
+  const int few = n_few * AT_G, many = n_many * AT_G * (D / AJ_DC);
+  // parts: slot 2c + 1 of the piece's first CTA c, slot 2i of the CTAs behind it
+  for (int x = blockIdx.x * NW + warp; x < few; x += gridDim.x * NW) {
+    const Join j = s_list[x / AT_G];
+    const int c = s_c[x / AT_G], h = x % AT_G, n = j.last - c + 1;
+    if (h >= j.heads) continue;
+    auto slot = [&](int i) { return (int64_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * AT_G + h; };
+    const float2 ml = lane < n ? ar.ml[slot(lane)] : make_float2(-INFINITY, 0.f);
+    float m = ml.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float base = m == -INFINITY ? 0.f : m, f = ex2(ml.x - base);
+    float l = ml.y * f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    constexpr int V = D >= 128 ? D / 128 : 1;  // columns 4 lane + 128 v
+    const bool in = D >= 128 || lane * 4 < D;
+    float4 a[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) a[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < AJ_FEW; ++i) {
+      const float fi = __shfl_sync(0xffffffffu, f, i);
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+        if (i < n && in)
+          add_scaled(a[v], *reinterpret_cast<const float4*>(ar.acc + slot(i) * D + lane * 4 + v * 128),
+                     fi);
+    }
+    const int64_t row = (int64_t)j.b * ar.Hq + j.h + h;
+    const float r = l != 0.f ? 1.f / l : 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (in) store_o(reinterpret_cast<T*>(ar.o) + row * D + lane * 4 + v * 128, a[v], r);
+    if (lane == 0 && ar.lse) ar.lse[row] = (base + log2f(l)) * 0.69314718055994531f;
+  }
+  for (int x = blockIdx.x; x < many; x += gridDim.x) {
+    const int p = MAXC - 1 - x / (AT_G * (D / AJ_DC)), h = x / (D / AJ_DC) % AT_G;
+    const int d0 = x % (D / AJ_DC) * AJ_DC, col = tid % 16, row0 = tid / 16;
+    const Join j = s_list[p];
+    const int c = s_c[p], n = j.last - c + 1;
+    if (h >= j.heads) continue;
+    auto slot = [&](int i) { return (int64_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * AT_G + h; };
+    float m = -INFINITY, l = 0.f;
+    for (int i = tid; i < n; i += AJ_NT) m = fmaxf(m, ar.ml[slot(i)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    __syncthreads();  // the last item's readers are done
+    if (lane == 0) s_red[warp][0] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NW; ++w) m = fmaxf(m, s_red[w][0]);
+    const float base = m == -INFINITY ? 0.f : m;
+    for (int i = tid; i < n; i += AJ_NT) {
+      const float2 y = ar.ml[slot(i)];
+      const float f = ex2(y.x - base);
+      s_w[i] = f;
+      l = fmaf(y.y, f, l);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) s_red[warp][1] = l;
+    __syncthreads();
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = row0; i < n; i += AJ_NT / 16)
+      add_scaled(a, *reinterpret_cast<const float4*>(ar.acc + slot(i) * D + d0 + col * 4), s_w[i]);
+    s_o[row0][col] = a;
+    __syncthreads();
+    if (tid < AJ_DC / 4) {
+      a = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i = 0; i < AJ_NT / 16; ++i) add_scaled(a, s_o[i][tid], 1.f);
+      l = 0.f;
+      for (int w = 0; w < NW; ++w) l += s_red[w][1];
+      const int64_t row = (int64_t)j.b * ar.Hq + j.h + h;
+      store_o(reinterpret_cast<T*>(ar.o) + row * D + d0 + tid * 4, a, l != 0.f ? 1.f / l : 0.f);
+      if (tid == 0 && d0 == 0 && ar.lse)
+        ar.lse[row] = (base + log2f(l)) * 0.69314718055994531f;
+    }
+  }
 }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
@@ -672,15 +793,15 @@ cudaError_t launch(AttnArgs ar, char* ws, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   // the join starts as the pass's CTAs leave and waits for its end on the device
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(pl.ctas, ar.G < AT_G ? ar.G : AT_G);
-  cfg.blockDim = dim3(4 * D);
+  cfg.gridDim = dim3(AJ_CTAS);
+  cfg.blockDim = dim3(AJ_NT);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_attn_join<D, T>, ar);
+  return cudaLaunchKernelEx(&cfg, k_attn_join<D, T>, ar, pl.ctas);
 }
 
 }  // namespace

@@ -23,7 +23,7 @@ constexpr int SM_NT = 256;      // threads per CTA, requests per scan step
 constexpr int SM_TOK = 1024;    // tokens per CTA
 
 struct SlotArgs {
-  int P;
+  uint32_t P;
   int64_t B, max_blocks, pages, n_free, n_tokens;
   const int32_t* ctx;
   const int32_t* nw;
@@ -39,6 +39,10 @@ struct SlotArgs {
 
 __device__ __forceinline__ int32_t sat31(int64_t x) {
   return x > 0x7fffffff ? 0x7fffffff : (int32_t)x;
+}
+
+__device__ __forceinline__ uint32_t ceil_div(uint32_t x, uint32_t d) {
+  return x == 0 ? 0 : (x - 1) / d + 1;
 }
 
 // inclusive sums of two values over the CTA's threads, in thread order
@@ -66,25 +70,24 @@ __device__ __forceinline__ void scan2(int64_t& x, int64_t& y, int64_t (*part)[2]
 __global__ void __launch_bounds__(SM_NT) k_slot_map(SlotArgs ar) {
   __shared__ int64_t part[SM_NT / 32][2];
   __shared__ int64_t s_cu[SM_NT + 1], s_first[SM_NT + 1];
-  __shared__ int32_t s_ctx[SM_NT];
+  __shared__ uint32_t s_ctx[SM_NT];
   const int tid = threadIdx.x;
   const int64_t t0 = (int64_t)blockIdx.x * SM_TOK;
   const int64_t t1 = t0 + SM_TOK < ar.n_tokens ? t0 + SM_TOK : ar.n_tokens;
-  const int64_t cap = ar.max_blocks * ar.P;
+  const uint32_t cap = (uint32_t)(ar.max_blocks * ar.P);  // below 2^31
   const bool lead = blockIdx.x == 0;
   int bad = 0;
   int64_t cu0 = 0, first0 = 0;  // sums over the requests of earlier steps
   for (int64_t b0 = 0; b0 < ar.B && (lead || cu0 < t1); b0 += SM_NT) {
     const int64_t b = b0 + tid;
-    int64_t c = 0, n = 0;
+    uint32_t c = 0, n = 0;  // below 2^31 each: their sum fits 32 bits, and divides in 32
     if (b < ar.B) {
-      c = ar.ctx[b];
-      n = ar.nw[b];
-      if (c < 0 || n < 0 || c + n > cap) bad = 1;
-      c = c < 0 ? 0 : c;
-      n = n < 0 ? 0 : n;
+      const int32_t ci = ar.ctx[b], ni = ar.nw[b];
+      c = ci < 0 ? 0 : ci;
+      n = ni < 0 ? 0 : ni;
+      if (ci < 0 || ni < 0 || c + n > cap) bad = 1;
     }
-    const int64_t need = (c + n + ar.P - 1) / ar.P - (c + ar.P - 1) / ar.P;
+    const int64_t need = ceil_div(c + n, ar.P) - ceil_div(c, ar.P);
     int64_t cu = n, first = need;
     scan2(cu, first, part);
     if (tid == 0) {
@@ -93,9 +96,9 @@ __global__ void __launch_bounds__(SM_NT) k_slot_map(SlotArgs ar) {
     }
     s_cu[tid + 1] = cu0 + cu;
     s_first[tid + 1] = first0 + first;
-    s_ctx[tid] = (int32_t)c;
+    s_ctx[tid] = c;
     if (lead && b < ar.B) {
-      ar.seq_len[b] = (int32_t)(c + n < cap ? c + n : cap);
+      ar.seq_len[b] = (int32_t)min(c + n, cap);
       ar.cu[b + 1] = sat31(cu0 + cu);
     }
     __syncthreads();
@@ -107,15 +110,15 @@ __global__ void __launch_bounds__(SM_NT) k_slot_map(SlotArgs ar) {
         const int m = (l + r) >> 1;
         if (s_cu[m] <= t) l = m; else r = m;
       }
-      const int64_t p = s_ctx[l] + (t - s_cu[l]), i = p / ar.P;
-      const int64_t held = ((int64_t)s_ctx[l] + ar.P - 1) / ar.P;
+      const uint32_t p = s_ctx[l] + (uint32_t)(t - s_cu[l]), i = p / ar.P;
+      const uint32_t held = ceil_div(s_ctx[l], ar.P);
       int32_t page = -1;
       if (i < ar.max_blocks) {
         int32_t* entry = ar.table + (b0 + l) * ar.max_blocks + i;
         if (i < held) {
           page = *entry;
         } else {
-          const int64_t f = s_first[l] + i - held;
+          const int64_t f = s_first[l] + (i - held);
           if (f < ar.n_free) page = ar.free_pages[f];
           if (page < 0 || page >= ar.pages) page = -1;
           if (p == i * ar.P) *entry = page;
@@ -124,7 +127,7 @@ __global__ void __launch_bounds__(SM_NT) k_slot_map(SlotArgs ar) {
       const bool ok = page >= 0 && page < ar.pages;
       if (!ok) bad = 1;
       ar.pos[t] = sat31(p);
-      ar.slots[t] = ok ? (int32_t)(page * (int64_t)ar.P + (p - i * ar.P)) : -1;
+      ar.slots[t] = ok ? (int32_t)((uint32_t)page * ar.P + (p - i * ar.P)) : -1;
     }
     cu0 = s_cu[SM_NT];
     first0 = s_first[SM_NT];
@@ -171,7 +174,7 @@ extern "C" gdn_status gdn_slot_map(const gdn_slot_problem* p, const int32_t* ctx
     return GDN_ERR_INVALID_ARG;
   SlotArgs ar;
   memset(&ar, 0, sizeof(ar));
-  ar.P = p->page_size;
+  ar.P = (uint32_t)p->page_size;
   ar.B = p->B;
   ar.max_blocks = p->max_blocks;
   ar.pages = p->pages;
