@@ -1110,15 +1110,19 @@ def gdn_slot_map(ctx_len, new_len, free_pages, block_table, *, page_size, pages,
     n_free = free_pages.numel()
 
     d = ctx_len.device
-    seq_len, sp = _out("seq_len", seq_len, dev, i32, (B,), d)
-    cu_seqlens, cp = _out("cu_seqlens", cu_seqlens, dev, i32, (B + 1,), d)
-    positions, pp = _out("positions", positions, dev, i32, (n_tokens,), d)
-    slots, lp = _out("slots", slots, dev, i32, (n_tokens,), d)
-    used, up = _out("used", used, dev, i32, (1,), d)
+    sizes = (B, B + 1, n_tokens, n_tokens, 1)
+    outs = (seq_len, cu_seqlens, positions, slots, used)
+    if all(t is None for t in outs):  # one allocation, five views of it
+        outs = torch.empty(sum(sizes), dtype=i32, device=d).split(sizes)
+        addr = [t.data_ptr() for t in outs]
+    else:
+        pairs = [_out(name, t, dev, i32, (n,), d) for name, t, n in
+                 zip(("seq_len", "cu_seqlens", "positions", "slots", "used"), outs, sizes)]
+        outs, addr = tuple(t for t, _ in pairs), [x for _, x in pairs]
     p = SlotProblem(page_size, 0, B, blocks, pages, n_free, n_tokens)
     _call("gdn_slot_map", dev, p, _arg("ctx_len", ctx_len, dev, i32, (B,)),
           _arg("new_len", new_len, dev, i32, (B,)),
           _arg("free_pages", free_pages, dev, i32, (n_free,)),
-          _arg("block_table", block_table, dev, i32, (B, blocks)), sp, cp, pp, lp, up,
-          _status(status, dev), _raw_stream(stream, dev))
-    return seq_len, cu_seqlens, positions, slots, used
+          _arg("block_table", block_table, dev, i32, (B, blocks)), *addr, _status(status, dev),
+          _raw_stream(stream, dev))
+    return outs

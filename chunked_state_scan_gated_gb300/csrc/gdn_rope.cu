@@ -36,9 +36,9 @@ constexpr int RO_NT = 256;     // 8 warps
 constexpr int RO_W = RO_NT / 32;
 constexpr int RO_CTAS = 152 * 2;  // CTAs at most: one wave of 2 per SM of a 152-SM GPU
 constexpr int RO_MAXD = 256;   // 8 elements per lane
-constexpr int RO_RING = 12288;  // bytes of a warp's ring
-constexpr int RO_FU = 4, RO_GU = 2;  // sets of heads per group, forward and backward
-constexpr int RO_SMEM = RO_W * (RO_RING + RO_MAXD * 4);  // rings, cos and sin
+constexpr int RO_RING = 8192;  // bytes of a warp's ring
+constexpr int RO_FU = 2, RO_GU = 1;  // sets of heads per group, forward and backward
+constexpr int RO_SMEM = RO_W * (RO_RING + (RO_MAXD + 16) * 4);  // rings, cos and sin
 
 struct RopeArgs {
   int64_t N, T, qs, ks, vs, n_slots;
@@ -65,23 +65,28 @@ __device__ __forceinline__ void ld8(const float* p, float (&v)[8]) {
     v[j + 4] = b[j];
   }
 }
-// cos and sin of t * f, t any int32, f fp32.  In revolutions u = t f / (2 pi), with
-// 1/(2 pi) as the sum of two fp32 numbers: t is split into two parts that are exact in fp32
-// and f / (2 pi) into hi + lo, the product with hi is exact as value and remainder of an
-// fma, and only the fraction goes into sincospi.  What is left is the rounding of the
-// fraction (2^-24 revolutions) and of lo (t f 2^-51 revolutions: 2^-22 at t = 2^29).
-__device__ __forceinline__ void angle(int32_t t, float f, float* c, float* s) {
+// A frequency in revolutions per position, f / (2 pi) = hi + lo, with 1/(2 pi) as the sum of two
+// fp32 numbers.
+struct Freq {
+  float hi, lo;
+};
+__device__ __forceinline__ Freq freq(float f) {
   constexpr float kHi = 0x1.45f306p-3f, kLo = 0x1.b9391p-28f;  // 1/(2 pi) = kHi + kLo
   const float hi = __fmul_rn(f, kHi);
-  const float lo = fmaf(f, kHi, -hi) + f * kLo;
-  const int32_t th = t & ~0xffff, tl = t & 0xffff;  // t = th + tl, both exact in fp32
-  float u = 0.f;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const float x = (float)(k ? tl : th);
-    const float p = __fmul_rn(x, hi);  // not contracted: its remainder is added below
-    u += (p - rintf(p)) + fmaf(x, hi, -p) + x * lo;
-  }
+  return Freq{hi, fmaf(f, kHi, -hi) + f * kLo};
+}
+// Revolutions of position x (exact in fp32), less whole ones.  The product with hi is exact as
+// value and remainder of an fma.
+__device__ __forceinline__ float turns(float x, Freq f) {
+  const float p = __fmul_rn(x, f.hi);  // not contracted: its remainder is added here
+  return (p - rintf(p)) + fmaf(x, f.hi, -p) + x * f.lo;
+}
+// cos and sin of t * f, t any int32, f fp32: t is split into two parts that are exact in fp32, and
+// only the fraction goes into sincospi.  What is left is the rounding of the fraction (2^-24
+// revolutions) and of lo (t f 2^-51 revolutions: 2^-22 at t = 2^29).
+__device__ __forceinline__ void angle(int32_t t, Freq f, float* c, float* s) {
+  float u = turns((float)(t & 0xffff), f);
+  if (t & ~0xffff) u += turns((float)(t & ~0xffff), f);
   u -= rintf(u);
   sincospif(2.f * u, s, c);
 }
@@ -153,32 +158,72 @@ __device__ __forceinline__ void copy8(T* dst, const T* src, bool in) {
   if constexpr (sizeof(T) == 4) copy16(dst + 4, src + 4, in);
 }
 
-// cos and sin of the token's angles into the warp's cs[0 .. R/2) and cs[RO_MAXD / 2 ..)
-__device__ __forceinline__ void angles(const RopeArgs& ar, int64_t n, float* cs) {
-  const int lane = threadIdx.x & 31;
-  const int32_t t = ar.pos ? ar.pos[n] : (int32_t)(n % ar.T);
-  __syncwarp();  // the last token's readers are done
-  for (int i = lane; i < ar.R / 2; i += 32) {
-    float c, s;
-    angle(t, ar.inv_freq[i], &c, &s);
-    cs[i] = c * ar.rscale;
-    cs[RO_MAXD / 2 + i] = s * ar.rscale;
+// The warp's table of the token's cos and sin, RO_MAXD / 2 of each, followed by 8 ones and 8
+// zeros (no rotation).
+constexpr int RO_CS = RO_MAXD + 16;
+constexpr int RO_Z = RO_MAXD / 2 / 32;  // angles per lane at most
+struct Angles {
+  Freq f[RO_Z];  // of angles lane, lane + 32, ...
+  int32_t t;     // position of the next token to be filled in, read ahead
+  __device__ __forceinline__ void fetch(const RopeArgs& ar, int n) {
+    t = n >= ar.N ? 0 : ar.pos ? ar.pos[n] : (int32_t)(n % ar.T);
   }
-  __syncwarp();
-}
+  __device__ __forceinline__ void init(const RopeArgs& ar, int n, float* cs) {
+    const int lane = threadIdx.x & 31;
+    fetch(ar, n);
+#pragma unroll
+    for (int z = 0; z < RO_Z; ++z)
+      f[z] = freq(lane + 32 * z < ar.R / 2 ? ar.inv_freq[lane + 32 * z] : 0.f);
+    if (lane < 16) cs[RO_MAXD + lane] = lane < 8 ? 1.f : 0.f;
+  }
+  // fills in the token whose position was read before; reads that of `next`
+  __device__ __forceinline__ void fill(const RopeArgs& ar, int next, float* cs) {
+    const int lane = threadIdx.x & 31;
+    const int32_t at = t;
+    fetch(ar, next);
+    __syncwarp();  // the last token's readers are done
+#pragma unroll
+    for (int z = 0; z < RO_Z; ++z) {
+      const int i = lane + 32 * z;
+      if (i < ar.R / 2) {
+        float c, s;
+        angle(at, f[z], &c, &s);
+        cs[i] = c * ar.rscale;
+        cs[RO_MAXD / 2 + i] = s * ar.rscale;
+      }
+    }
+    __syncwarp();
+  }
+};
 
 // A lane's view of the rotation: y_j = x_j c_j + xp_j s_j with xp the partner elements and the
 // sign of the pair's side in s (sgn = -1: the transposed rotation); c = 1, s = 0 past R.
 template <bool INTER>
 __device__ __forceinline__ void turn(const RopeArgs& ar, const float* cs, int e, float sgn,
-                                     float (&c)[8], float (&s)[8]) {
+                                     F2 (&c)[4], F2 (&s)[4]) {
   const bool in = e < ar.R, first = e < ar.R / 2;
+  const int at = !in ? RO_MAXD : INTER ? e / 2 : first ? e : e - ar.R / 2;
+  const float4* cp = reinterpret_cast<const float4*>(cs + at);
+  const float4* sp = reinterpret_cast<const float4*>(cs + (in ? at + RO_MAXD / 2 : at + 8));
+  const float4 c0 = cp[0], s0 = sp[0];
+  if constexpr (INTER) {  // 4 pairs (c, c), (-s, s)
+    const float cc[4] = {c0.x, c0.y, c0.z, c0.w}, ss[4] = {s0.x, s0.y, s0.z, s0.w};
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int i = INTER ? (e + j) / 2 : first ? e + j : e + j - ar.R / 2;
-    c[j] = in ? cs[i] : 1.f;
-    const bool neg = INTER ? !(j & 1) : first;
-    s[j] = in ? (neg ? -sgn : sgn) * cs[RO_MAXD / 2 + i] : 0.f;
+    for (int j = 0; j < 4; ++j) {
+      c[j] = f2(cc[j], cc[j]);
+      s[j] = f2(-sgn * ss[j], sgn * ss[j]);
+    }
+  } else {
+    const float4 c1 = cp[1], s1 = sp[1];
+    const float g = first ? -sgn : sgn;
+    c[0] = f2(c0.x, c0.y);
+    c[1] = f2(c0.z, c0.w);
+    c[2] = f2(c1.x, c1.y);
+    c[3] = f2(c1.z, c1.w);
+    s[0] = f2(g * s0.x, g * s0.y);
+    s[1] = f2(g * s0.z, g * s0.w);
+    s[2] = f2(g * s1.x, g * s1.y);
+    s[3] = f2(g * s1.z, g * s1.w);
   }
 }
 // The lane (of LPR) that holds the partner elements: its own past R (where they do not count).
@@ -187,37 +232,115 @@ __device__ __forceinline__ int other_lane(const RopeArgs& ar, int e) {
   return (e < ar.R / 2 ? e + ar.R / 2 : e - ar.R / 2) / 8;
 }
 
-// A place in the sequence of groups: token, group of its heads.
-struct Place {
-  int64_t n;
-  int g;
-  __device__ __forceinline__ void next(int groups) {
-    if (++g == groups) {
-      g = 0;
-      ++n;
-    }
+// A warp's share of the groups: of the N tokens, as many whole rounds of one token per warp as
+// there are (neighbouring warps read neighbouring tokens: 98 us against 109 for each warp its own
+// stretch of 32768 tokens), then an even part of the groups of the tokens that are left, from
+// group tail_g of token tail_n.  Tokens fit 31 bits and groups 32 (checked on the host).
+struct Share {
+  int warps, full, tail_n, tail_g, groups;  // full: tokens in whole rounds
+  unsigned todo;                            // groups of this warp
+  __device__ __forceinline__ Share(const RopeArgs& ar, int g) {
+    const unsigned w = blockIdx.x * RO_W + (threadIdx.x >> 5);
+    groups = g;
+    warps = (int)(gridDim.x * RO_W);
+    const int rounds = (int)(ar.N / warps);
+    full = rounds * warps;
+    const uint64_t rest = (uint64_t)(ar.N - full) * g;
+    const unsigned first = (unsigned)(rest * w / warps);
+    todo = rounds * g + (unsigned)(rest * (w + 1) / warps) - first;
+    tail_n = full + (int)(first / g);
+    tail_g = (int)(first % g);
   }
 };
-// A group: kind 0 query, 1 key, 2 value; this lane's first head of that kind (the others
-// follow 32 / LPR apart) and how many heads the kind has (0 for a lane past D).
-struct Heads {
-  int kind, h, end;
+
+// A run of groups of one token and kind (0 query, 1 key, 2 value).
+struct Run {
+  int n;
+  int g;     // group of the token
+  int kind;
+  int i;     // group of the kind
+  int stop;  // group of the token behind the kind's last
+  int left;  // groups of the kind from here on
+  __device__ __forceinline__ void set(const RopeArgs& ar) {
+    kind = g < ar.gq ? 0 : g < ar.gq + ar.gk ? 1 : 2;
+    stop = kind == 0 ? ar.gq : kind == 1 ? ar.gq + ar.gk : ar.gq + ar.gk + ar.gv;
+    left = stop - g;
+    i = g - (kind == 0 ? 0 : kind == 1 ? ar.gq : ar.gq + ar.gk);
+  }
+  __device__ __forceinline__ void tail(const Share& sh) {
+    n = sh.tail_n;
+    g = sh.tail_g;
+  }
+  __device__ __forceinline__ void start(const RopeArgs& ar, const Share& sh) {
+    n = (int)(blockIdx.x * RO_W + (threadIdx.x >> 5));
+    g = 0;
+    if (n >= sh.full) tail(sh);
+    set(ar);
+  }
+  // the token behind n
+  __device__ __forceinline__ int behind(const Share& sh) const {
+    if (n >= sh.full) return n + 1;
+    return n + sh.warps < sh.full ? n + sh.warps : sh.tail_n;
+  }
+  // the run behind this one
+  __device__ __forceinline__ void next(const RopeArgs& ar, const Share& sh) {
+    g = stop;
+    if (g >= sh.groups) {
+      g = 0;
+      if (n >= sh.full) ++n;
+      else if ((n += sh.warps) >= sh.full) tail(sh);
+    }
+    set(ar);
+  }
 };
-template <int LPR, int U>
-__device__ __forceinline__ Heads heads_of(const RopeArgs& ar, int g) {
-  const int lane = threadIdx.x & 31, e = (lane & (LPR - 1)) * 8;
-  const int kind = g < ar.gq ? 0 : g < ar.gq + ar.gk ? 1 : 2;
-  const int i = g - (kind == 0 ? 0 : kind == 1 ? ar.gq : ar.gq + ar.gk);
-  return Heads{kind, i * U * (32 / LPR) + lane / LPR, e < ar.D ? kind == 0 ? ar.Hq : ar.Hk : 0};
-}
-// This warp's share [first, last) of the groups.
-__device__ __forceinline__ void share(const RopeArgs& ar, int groups, int64_t* first,
-                                      int64_t* last) {
-  const int64_t all = ar.N * groups, w = (int64_t)blockIdx.x * RO_W + (threadIdx.x >> 5);
-  const int64_t warps = (int64_t)gridDim.x * RO_W;
-  *first = all * w / warps;
-  *last = all * (w + 1) / warps;
-}
+
+// Issues the groups of a warp's share one after another, NP rows (x, and dy backward) a head.
+template <int LPR, int U, int NP, int NST, typename T>
+struct Loader {
+  static constexpr int RPL = 32 / LPR, SE = 32 * 8;
+  Run run;
+  unsigned todo;
+  int h, end, step;   // this lane's first head, heads of the kind (0 past D), elements per set
+  const T* p[NP];
+  T* ring;            // this lane's place in stage 0
+  __device__ __forceinline__ void set(const RopeArgs& ar) {
+    const int lane = threadIdx.x & 31, e = (lane & (LPR - 1)) * 8;
+    h = run.i * U * RPL + lane / LPR;
+    end = e < ar.D ? (run.kind == 0 ? ar.Hq : ar.Hk) : 0;
+    const int64_t at = (int64_t)h * ar.D + e;
+    if (run.kind == 0) {
+      p[0] = reinterpret_cast<const T*>(ar.q) + run.n * ar.qs + at;
+      if constexpr (NP == 2) p[1] = reinterpret_cast<const T*>(ar.dq_out) + (int64_t)run.n * ar.Hq * ar.D + at;
+    } else if (NP == 2 || run.kind == 1) {
+      p[0] = reinterpret_cast<const T*>(ar.k) + run.n * ar.ks + at;
+      if constexpr (NP == 2) p[1] = reinterpret_cast<const T*>(ar.dk_out) + (int64_t)run.n * ar.Hk * ar.D + at;
+    } else {
+      p[0] = reinterpret_cast<const T*>(ar.v) + run.n * ar.vs + at;
+    }
+  }
+  __device__ __forceinline__ void issue(const RopeArgs& ar, const Share& sh, int stage) {
+    if (todo > 0) {
+      T* dst = ring + stage * U * NP * SE;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool in = h + u * RPL < end;
+#pragma unroll
+        for (int z = 0; z < NP; ++z)
+          copy8(dst + (u * NP + z) * SE, in ? p[z] + u * step : p[z], in);
+      }
+      --todo;
+      if (--run.left > 0) {
+        h += U * RPL;
+#pragma unroll
+        for (int z = 0; z < NP; ++z) p[z] += U * step;
+      } else if (todo > 0) {
+        run.next(ar, sh);
+        set(ar);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+};
 
 // CACHE: k and v rows go to the caches
 template <bool CACHE, bool INTER, int LPR, typename T>
@@ -227,118 +350,113 @@ __global__ void __launch_bounds__(RO_NT, 2) k_qk_norm_rope_fwd(RopeArgs ar) {
   constexpr int NST = RO_RING / (U * SE * (int)sizeof(T));
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = (lane & (LPR - 1)) * 8;
   T* ring = reinterpret_cast<T*>(smem + warp * RO_RING);
-  float* cs = reinterpret_cast<float*>(smem + RO_W * RO_RING) + warp * RO_MAXD;
+  float* cs = reinterpret_cast<float*>(smem + RO_W * RO_RING) + warp * RO_CS;
   const int groups = ar.gq + ar.gk + (CACHE ? ar.gv : 0);
-  int64_t left, last;
-  share(ar, groups, &left, &last);
-  Place load{left / groups, (int)(left % groups)}, at = load;
-  left = last - left;
-  int64_t ahead = left;  // groups still to be issued
   const int other = INTER ? 0 : other_lane(ar, e);
   const int mine = lane * 8, theirs = (lane / LPR * LPR + other) * 8;
-  auto issue = [&](int stage) {
-    if (ahead-- > 0) {
-      const Heads x = heads_of<LPR, U>(ar, load.g);
-      const T* src = reinterpret_cast<const T*>(x.kind == 0 ? ar.q : x.kind == 1 ? ar.k : ar.v);
-      const int64_t stride = x.kind == 0 ? ar.qs : x.kind == 1 ? ar.ks : ar.vs;
-      const T* row = src + load.n * stride + x.h * ar.D + e;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const bool in = x.h + u * RPL < x.end;
-        copy8(ring + (stage * U + u) * SE + mine, in ? row + u * RPL * ar.D : src, in);
-      }
-      load.next(groups);
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  for (int i = 0; i < NST - 1; ++i) issue(i);
-  F2 A[4], B[4];
-  int64_t n = -1, dst = -1;
-  int kind = -1, stage = 0;
-  for (; left > 0; --left, at.next(groups)) {
-    const Heads x = heads_of<LPR, U>(ar, at.g);
-    if (at.n != n || x.kind != kind) {
-      if (at.n != n) {
-        angles(ar, at.n, cs);
-        if constexpr (CACHE) {
-          dst = ar.slots[at.n];
-          if (dst < 0 || dst >= ar.n_slots) {
-            if (dst != -1 && lane == 0 && ar.status) atomicOr(ar.status, kStatusClamped);
-            dst = -1;
-          }
-        } else {
-          dst = at.n;
-        }
-      }
-      n = at.n;
-      kind = x.kind;
-      if (!CACHE || kind < 2) {
-        const float* w = kind == 0 ? ar.wq : ar.wk;
-        float c[8], s[8], wv[8] = {}, wp[8] = {};
-        turn<INTER>(ar, cs, e, 1.f, c, s);
-        if (e < ar.D) {
-          ld8(w + e, wv);
-          if constexpr (!INTER) ld8(w + other * 8, wp);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float p0 = INTER ? wv[2 * j + 1] : wp[2 * j];
-          const float p1 = INTER ? wv[2 * j] : wp[2 * j + 1];
-          A[j] = f2(wv[2 * j] * c[2 * j], wv[2 * j + 1] * c[2 * j + 1]);
-          B[j] = f2(p0 * s[2 * j], p1 * s[2 * j + 1]);
+  const Share sh(ar, groups);
+  if (sh.todo == 0) return;
+  Loader<LPR, U, 1, NST, T> ld;
+  ld.run.start(ar, sh);
+  ld.todo = sh.todo;
+  ld.step = RPL * ar.D;
+  ld.ring = ring + mine;
+  ld.set(ar);
+  Run run = ld.run;
+  for (int i = 0; i < NST - 1; ++i) ld.issue(ar, sh, i);
+  Angles an;
+  an.init(ar, run.n, cs);
+  unsigned left = sh.todo;
+  int64_t dst = -1;
+  int stage = 0;
+  for (int token = -1; left > 0; run.next(ar, sh)) {
+    if (run.n != token) {
+      token = run.n;
+      an.fill(ar, run.behind(sh), cs);
+      dst = run.n;
+      if constexpr (CACHE) {
+        dst = ar.slots[run.n];
+        if (dst < 0 || dst >= ar.n_slots) {
+          if (dst != -1 && lane == 0 && ar.status) atomicOr(ar.status, kStatusClamped);
+          dst = -1;
         }
       }
     }
-    asm volatile("cp.async.wait_group %0;" ::"n"(NST - 2) : "memory");
-    __syncwarp();  // every lane's part has arrived, and the stage before this one is read
-    issue(stage == 0 ? NST - 1 : stage - 1);
-    const T* in = ring + stage * U * SE;
-    stage = stage == NST - 1 ? 0 : stage + 1;
-    F2 v[U][4];
-    float ss[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      get(in + u * SE + mine, v[u]);
-      F2 sq = mul(v[u][0], v[u][0]);
-#pragma unroll
-      for (int j = 1; j < 4; ++j) sq = fma(v[u][j], v[u][j], sq);
-      const float2 s2 = un(sq);
-      ss[u] = s2.x + s2.y;
-    }
+    const int kind = run.kind;
+    const unsigned count = min((unsigned)run.left, left);
+    left -= count;
+    F2 A[4], B[4];
     if (!CACHE || kind < 2) {
+      const float* w = kind == 0 ? ar.wq : ar.wk;
+      float wv[8] = {}, wp[8] = {};
+      turn<INTER>(ar, cs, e, 1.f, A, B);
+      if (e < ar.D) {
+        ld8(w + e, wv);
+        if constexpr (!INTER) ld8(w + other * 8, wp);
+      }
 #pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1)
-#pragma unroll
-        for (int u = 0; u < U; ++u) ss[u] += __shfl_xor_sync(0xffffffffu, ss[u], o);
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        F2 y[4];
-        if constexpr (INTER) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 a = un(v[u][j]);
-            y[j] = f2(a.y, a.x);
-          }
-        } else {
-          get(in + u * SE + theirs, y);
-        }
-        const float f = rsqrtf(fmaf(ss[u], ar.inv_d, ar.eps));
-        const F2 ff = f2(f, f);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[u][j] = mul(fma(y[j], B[j], mul(v[u][j], A[j])), ff);
+      for (int j = 0; j < 4; ++j) {
+        A[j] = mul(A[j], f2(wv[2 * j], wv[2 * j + 1]));
+        B[j] = mul(B[j], INTER ? f2(wv[2 * j + 1], wv[2 * j]) : f2(wp[2 * j], wp[2 * j + 1]));
       }
     }
-    if (CACHE && kind > 0 && dst < 0) continue;
-    T* out = reinterpret_cast<T*>(kind == 0 ? ar.q_out : kind == 1 ? ar.k_out : ar.v_out);
-    out += ((kind == 0 ? at.n * ar.Hq : dst * ar.Hk) + x.h) * ar.D + e;
+    int h = run.i * U * RPL + lane / LPR;
+    int end = e < ar.D ? (kind == 0 ? ar.Hq : ar.Hk) : 0;
+    if (CACHE && kind > 0 && dst < 0) end = 0;
+    T* out = reinterpret_cast<T*>(kind == 0 ? ar.q_out : kind == 1 ? ar.k_out : ar.v_out) +
+             ((kind == 0 ? (int64_t)run.n * ar.Hq : dst * ar.Hk) + h) * ar.D + e;
+#pragma unroll 1
+    for (unsigned i = 0; i < count; ++i) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(NST - 2) : "memory");
+      __syncwarp();  // every lane's part has arrived, and the stage before this one is read
+      ld.issue(ar, sh, stage == 0 ? NST - 1 : stage - 1);
+      const T* in = ring + stage * U * SE;
+      stage = stage == NST - 1 ? 0 : stage + 1;
+      F2 v[U][4];
+      float ss[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (x.h + u * RPL < x.end) put(out + u * RPL * ar.D, v[u]);
+      for (int u = 0; u < U; ++u) {
+        get(in + u * SE + mine, v[u]);
+        F2 sq = mul(v[u][0], v[u][0]);
+#pragma unroll
+        for (int j = 1; j < 4; ++j) sq = fma(v[u][j], v[u][j], sq);
+        const float2 s2 = un(sq);
+        ss[u] = s2.x + s2.y;
+      }
+      if (!CACHE || kind < 2) {
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1)
+#pragma unroll
+          for (int u = 0; u < U; ++u) ss[u] += __shfl_xor_sync(0xffffffffu, ss[u], o);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          F2 y[4];
+          if constexpr (INTER) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 a = un(v[u][j]);
+              y[j] = f2(a.y, a.x);
+            }
+          } else {
+            get(in + u * SE + theirs, y);
+          }
+          const float f = rsqrtf(fmaf(ss[u], ar.inv_d, ar.eps));
+          const F2 ff = f2(f, f);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[u][j] = mul(fma(y[j], B[j], mul(v[u][j], A[j])), ff);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (h + u * RPL < end) put(out + u * RPL * ar.D, v[u]);
+      h += U * RPL;
+      out += U * RPL * ar.D;
+    }
   }
 }
 
 // dx = f w dn - x f^3 sum(dn x w) / D,  dw += f dn x  with dn the turned dy.  The ring's stages
-// hold a group of x and of dy; a warp keeps its lanes' dwq, dwk in registers.
+// hold a group's rows of x and dy; a warp keeps its lanes' dwq, dwk in registers.
 template <bool INTER, int LPR, typename T>
 __global__ void __launch_bounds__(RO_NT, 2) k_qk_norm_rope_bwd(RopeArgs ar) {
   extern __shared__ __align__(16) char smem[];
@@ -347,120 +465,113 @@ __global__ void __launch_bounds__(RO_NT, 2) k_qk_norm_rope_bwd(RopeArgs ar) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LPR;
   const int e = (lane & (LPR - 1)) * 8;
   T* ring = reinterpret_cast<T*>(smem + warp * RO_RING);
-  float* cs = reinterpret_cast<float*>(smem + RO_W * RO_RING) + warp * RO_MAXD;
+  float* cs = reinterpret_cast<float*>(smem + RO_W * RO_RING) + warp * RO_CS;
   const int groups = ar.gq + ar.gk;
-  int64_t left, last;
-  share(ar, groups, &left, &last);
-  Place load{left / groups, (int)(left % groups)}, at = load;
-  left = last - left;
-  int64_t ahead = left;
   const int other = INTER ? 0 : other_lane(ar, e);
   const int mine = lane * 8, theirs = (lane / LPR * LPR + other) * 8;
-  auto issue = [&](int stage) {
-    if (ahead-- > 0) {
-      const Heads x = heads_of<LPR, U>(ar, load.g);
-      const bool isq = x.kind == 0;
-      const T* xs = reinterpret_cast<const T*>(isq ? ar.q : ar.k);
-      const T* gs = reinterpret_cast<const T*>(isq ? ar.dq_out : ar.dk_out);
-      const T* xr = xs + load.n * (isq ? ar.qs : ar.ks) + x.h * ar.D + e;
-      const T* gr = gs + (load.n * (isq ? ar.Hq : ar.Hk) + x.h) * ar.D + e;
-      T* dst = ring + stage * 2 * U * SE + mine;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const bool in = x.h + u * RPL < x.end;
-        copy8(dst + 2 * u * SE, in ? xr + u * RPL * ar.D : xs, in);
-        copy8(dst + (2 * u + 1) * SE, in ? gr + u * RPL * ar.D : gs, in);
-      }
-      load.next(groups);
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  for (int i = 0; i < NST - 1; ++i) issue(i);
-  F2 C[4], S[4], W[4], dw[2][4];
+  asm volatile("griddepcontrol.launch_dependents;");
+  F2 dw[2][4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) dw[0][j] = dw[1][j] = f2(0.f, 0.f);
-  int64_t n = -1;
-  int kind = -1, stage = 0;
-  for (; left > 0; --left, at.next(groups)) {
-    const Heads hd = heads_of<LPR, U>(ar, at.g);
-    if (at.n != n || hd.kind != kind) {
-      if (at.n != n) {
-        angles(ar, at.n, cs);
-        float c[8], s[8];
-        turn<INTER>(ar, cs, e, -1.f, c, s);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          C[j] = f2(c[2 * j], c[2 * j + 1]);
-          S[j] = f2(s[2 * j], s[2 * j + 1]);
-        }
+  const Share sh(ar, groups);
+  if (sh.todo > 0) {
+    Loader<LPR, U, 2, NST, T> ld;
+    ld.run.start(ar, sh);
+    ld.todo = sh.todo;
+    ld.step = RPL * ar.D;
+    ld.ring = ring + mine;
+    ld.set(ar);
+    Run run = ld.run;
+    for (int i = 0; i < NST - 1; ++i) ld.issue(ar, sh, i);
+    Angles an;
+    an.init(ar, run.n, cs);
+    unsigned left = sh.todo;
+    int stage = 0;
+    F2 C[4], S[4];
+    for (int token = -1; left > 0; run.next(ar, sh)) {
+      if (run.n != token) {
+        token = run.n;
+        an.fill(ar, run.behind(sh), cs);
+        turn<INTER>(ar, cs, e, -1.f, C, S);
       }
-      if (hd.kind != kind) {
-        float wv[8] = {};
-        if (e < ar.D) ld8((hd.kind == 0 ? ar.wq : ar.wk) + e, wv);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) W[j] = f2(wv[2 * j], wv[2 * j + 1]);
-      }
-      n = at.n;
-      kind = hd.kind;
-    }
-    asm volatile("cp.async.wait_group %0;" ::"n"(NST - 2) : "memory");
-    __syncwarp();
-    issue(stage == 0 ? NST - 1 : stage - 1);
-    const T* in = ring + stage * 2 * U * SE;
-    stage = stage == NST - 1 ? 0 : stage + 1;
-    F2 x[U][4], g[U][4], t[U][4];
-    float ss[U], dot[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      F2 y[4];
-      get(in + 2 * u * SE + mine, x[u]);
-      get(in + (2 * u + 1) * SE + mine, g[u]);
-      if constexpr (INTER) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 a = un(g[u][j]);
-          y[j] = f2(a.y, a.x);
-        }
-      } else {
-        get(in + (2 * u + 1) * SE + theirs, y);
-      }
-      F2 sq = f2(0.f, 0.f), dt = sq;
+      const int kind = run.kind;
+    const unsigned count = min((unsigned)run.left, left);
+      left -= count;
+      float wv[8] = {};
+      if (e < ar.D) ld8((kind == 0 ? ar.wq : ar.wk) + e, wv);
+      F2 W[4], d[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        sq = fma(x[u][j], x[u][j], sq);
-        g[u][j] = fma(y[j], S[j], mul(g[u][j], C[j]));  // dn
-        t[u][j] = mul(g[u][j], x[u][j]);
-        g[u][j] = mul(g[u][j], W[j]);
-        dt = fma(g[u][j], x[u][j], dt);
+        W[j] = f2(wv[2 * j], wv[2 * j + 1]);
+        d[j] = kind == 0 ? dw[0][j] : dw[1][j];
       }
-      const float2 s2 = un(sq), d2 = un(dt);
-      ss[u] = s2.x + s2.y;
-      dot[u] = d2.x + d2.y;
-    }
+      const int heads = kind == 0 ? ar.Hq : ar.Hk, end = e < ar.D ? heads : 0;
+      int h = run.i * U * RPL + sub;
+      T* out = reinterpret_cast<T*>(kind == 0 ? ar.q_out : ar.k_out) +
+               ((int64_t)run.n * heads + h) * ar.D + e;
+#pragma unroll 1
+      for (unsigned i = 0; i < count; ++i) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(NST - 2) : "memory");
+        __syncwarp();
+        ld.issue(ar, sh, stage == 0 ? NST - 1 : stage - 1);
+        const T* in = ring + stage * 2 * U * SE;
+        stage = stage == NST - 1 ? 0 : stage + 1;
+        F2 x[U][4], g[U][4], t[U][4];
+        float ss[U], dot[U];
 #pragma unroll
-    for (int o = LPR / 2; o > 0; o >>= 1)
+        for (int u = 0; u < U; ++u) {
+          F2 y[4];
+          get(in + 2 * u * SE + mine, x[u]);
+          get(in + (2 * u + 1) * SE + mine, g[u]);
+          if constexpr (INTER) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        ss[u] += __shfl_xor_sync(0xffffffffu, ss[u], o);
-        dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], o);
+            for (int j = 0; j < 4; ++j) {
+              const float2 a = un(g[u][j]);
+              y[j] = f2(a.y, a.x);
+            }
+          } else {
+            get(in + (2 * u + 1) * SE + theirs, y);
+          }
+          F2 sq = f2(0.f, 0.f), dt = sq;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            sq = fma(x[u][j], x[u][j], sq);
+            g[u][j] = fma(y[j], S[j], mul(g[u][j], C[j]));  // dn
+            t[u][j] = mul(g[u][j], x[u][j]);
+            g[u][j] = mul(g[u][j], W[j]);
+            dt = fma(g[u][j], x[u][j], dt);
+          }
+          const float2 s2 = un(sq), d2 = un(dt);
+          ss[u] = s2.x + s2.y;
+          dot[u] = d2.x + d2.y;
+        }
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1)
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            ss[u] += __shfl_xor_sync(0xffffffffu, ss[u], o);
+            dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], o);
+          }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float f = rsqrtf(fmaf(ss[u], ar.inv_d, ar.eps));
+          const float m = -(dot[u] * ar.inv_d) * f * f * f;
+          const F2 ff = f2(f, f), mm = f2(m, m);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            d[j] = fma(t[u][j], ff, d[j]);  // lanes without a head hold zeros
+            g[u][j] = fma(x[u][j], mm, mul(g[u][j], ff));
+          }
+          if (h + u * RPL < end) put(out + u * RPL * ar.D, g[u]);
+        }
+        h += U * RPL;
+        out += U * RPL * ar.D;
       }
-    T* out = reinterpret_cast<T*>(kind == 0 ? ar.q_out : ar.k_out);
-    out += (at.n * (kind == 0 ? ar.Hq : ar.Hk) + hd.h) * ar.D + e;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const float f = rsqrtf(fmaf(ss[u], ar.inv_d, ar.eps));
-      const float m = -(dot[u] * ar.inv_d) * f * f * f;
-      const F2 ff = f2(f, f), mm = f2(m, m);
-      if (kind == 0) {  // lanes without a head hold zeros
-#pragma unroll
-        for (int j = 0; j < 4; ++j) dw[0][j] = fma(t[u][j], ff, dw[0][j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) dw[1][j] = fma(t[u][j], ff, dw[1][j]);
+      for (int j = 0; j < 4; ++j) {
+        if (kind == 0) dw[0][j] = d[j];
+        else dw[1][j] = d[j];
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) g[u][j] = fma(x[u][j], mm, mul(g[u][j], ff));
-      if (hd.h + u * RPL < hd.end) put(out + u * RPL * ar.D, g[u]);
     }
   }
   // this CTA's dwq, dwk: lanes of equal elements, then the warps in order (cs is free now)
@@ -488,25 +599,26 @@ __global__ void __launch_bounds__(RO_NT, 2) k_qk_norm_rope_bwd(RopeArgs ar) {
   }
 }
 
-// dwq, dwk = sums over the n_part CTA partials in fp64: 32 columns per CTA, warp w adds the
-// partials w, w + 8, ... in order, then warp 0 adds the 8 warp sums in order.
-__global__ void __launch_bounds__(RO_NT) k_qk_norm_rope_dw(int n_part, int D,
-                                                           const float* __restrict__ part,
+// dwq, dwk = sums over the n_part CTA partials in fp64: 8 columns (one sector) per CTA, thread row
+// r adds the partials r, r + 32, ... in order, then one thread per column the 32 row sums.
+constexpr int RD_COLS = 8, RD_ROWS = RO_NT / RD_COLS;
+__global__ void __launch_bounds__(RO_NT) k_qk_norm_rope_dw(int n_part, int D, const float* part,
                                                            float* dwq, float* dwk) {
-  __shared__ double acc[RO_NT / 32][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int e = blockIdx.x * 32 + lane;
+  __shared__ double acc[RD_ROWS][RD_COLS];
+  const int col = threadIdx.x % RD_COLS, row = threadIdx.x / RD_COLS;
+  const int e = blockIdx.x * RD_COLS + col;  // D is a multiple of 8: e < 2 D
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   double s = 0.0;
-  if (e < 2 * D)
-    for (int p = warp; p < n_part; p += RO_NT / 32) s += part[(int64_t)p * 2 * D + e];
-  acc[warp][lane] = s;
+#pragma unroll 5
+  for (int p = row; p < n_part; p += RD_ROWS) s += part[(int64_t)p * 2 * D + e];
+  acc[row][col] = s;
   __syncthreads();
-  if (warp == 0 && e < 2 * D) {
-    double t = 0.0;
+  if (row == 0) {
+    s = 0.0;
 #pragma unroll
-    for (int w = 0; w < RO_NT / 32; ++w) t += acc[w][lane];
+    for (int r = 0; r < RD_ROWS; ++r) s += acc[r][col];
     float* out = e < D ? dwq : dwk;
-    if (out) out[e < D ? e : e - D] = (float)t;
+    if (out) out[e < D ? e : e - D] = (float)s;
   }
 }
 
@@ -709,9 +821,20 @@ gdn_status gdn_qk_norm_rope_bwd(const gdn_rope_problem* p, const void* q, const 
     });
     if (e != cudaSuccess) return GDN_ERR_CUDA;
   }
-  k_qk_norm_rope_dw<<<(unsigned)((2 * ar.D + 31) / 32), RO_NT, 0, st>>>(
-      (int)ctas, ar.D, (const float*)workspace, ar.Hq ? dwq : nullptr, ar.Hk ? dwk : nullptr);
-  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  // starts as the pass's CTAs leave and waits for its end on the device
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(2 * ar.D / RD_COLS));
+  cfg.blockDim = dim3(RO_NT);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e =
+      cudaLaunchKernelEx(&cfg, k_qk_norm_rope_dw, (int)ctas, ar.D, (const float*)workspace,
+                         ar.Hq ? dwq : (float*)nullptr, ar.Hk ? dwk : (float*)nullptr);
+  return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -296,6 +296,9 @@ ROPE = [  # N, Hq, Hk, D, R, dtype, far
     (129, 5, 5, 128, 16, BF, 2 ** 31 - 1), (1000, 16, 4, 64, 32, BF, 0),
     (1, 2, 1, 16, 16, F32, 0), (50, 4, 2, 128, 64, F32, 2 ** 20), (17, 1, 1, 256, 256, F32, 7),
     (200, 3, 3, 72, 48, F32, 2 ** 31 - 1), (65, 8, 2, 248, 240, F32, 0),
+    # several tokens and kinds per warp
+    (4001, 17, 3, 128, 64, BF, 0), (3001, 13, 5, 64, 64, BF, 9000), (2500, 12, 1, 256, 64, BF, 0),
+    (3003, 16, 9, 64, 32, F32, 70000),
 ]
 ROPE_IDS = [f"N{c[0]}_h{c[1]}x{c[2]}_d{c[3]}_r{c[4]}_{'bf16' if c[5] == BF else 'f32'}_p{c[6]}"
             for c in ROPE]
