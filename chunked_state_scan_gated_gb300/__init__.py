@@ -1072,6 +1072,9 @@ def gdn_attn_decode_workspace_size(problem: AttnProblem) -> int:
     return n.value
 
 
+_attn_ws = {}  # workspace bytes by (head dim, type)
+
+
 def gdn_attn_decode(q, k_cache, v_cache, block_table, seq_len, *, scale=0.0, o=None, lse=None,
                     want_lse=True, ws=None, status=None, stream=None):
     """Attention of one new token per request, q [B,Hq,D], over the paged caches
@@ -1088,7 +1091,10 @@ def gdn_attn_decode(q, k_cache, v_cache, block_table, seq_len, *, scale=0.0, o=N
     lp = None
     if lse is not None or want_lse:
         lse, lp = _out("lse", lse, dev, torch.float32, (B, Hq), q.device)
-    n = gdn_attn_decode_workspace_size(p) if ws is None else ws.numel()
+    if ws is not None:
+        n = ws.numel()
+    else:  # the size goes by D and the type alone
+        n = _attn_ws.get((D, dt)) or _attn_ws.setdefault((D, dt), gdn_attn_decode_workspace_size(p))
     ws, wsp = _out("ws", ws, dev, torch.uint8, (n,), q.device)
     cache = (pages, P, Hk, D)
     _call("gdn_attn_decode", dev, p, qp, _arg("k_cache", k_cache, dev, dt, cache),
@@ -1110,19 +1116,15 @@ def gdn_slot_map(ctx_len, new_len, free_pages, block_table, *, page_size, pages,
     n_free = free_pages.numel()
 
     d = ctx_len.device
-    sizes = (B, B + 1, n_tokens, n_tokens, 1)
-    outs = (seq_len, cu_seqlens, positions, slots, used)
-    if all(t is None for t in outs):  # one allocation, five views of it
-        outs = torch.empty(sum(sizes), dtype=i32, device=d).split(sizes)
-        addr = [t.data_ptr() for t in outs]
-    else:
-        pairs = [_out(name, t, dev, i32, (n,), d) for name, t, n in
-                 zip(("seq_len", "cu_seqlens", "positions", "slots", "used"), outs, sizes)]
-        outs, addr = tuple(t for t, _ in pairs), [x for _, x in pairs]
+    seq_len, sp = _out("seq_len", seq_len, dev, i32, (B,), d)
+    cu_seqlens, cp = _out("cu_seqlens", cu_seqlens, dev, i32, (B + 1,), d)
+    positions, pp = _out("positions", positions, dev, i32, (n_tokens,), d)
+    slots, lp = _out("slots", slots, dev, i32, (n_tokens,), d)
+    used, up = _out("used", used, dev, i32, (1,), d)
     p = SlotProblem(page_size, 0, B, blocks, pages, n_free, n_tokens)
     _call("gdn_slot_map", dev, p, _arg("ctx_len", ctx_len, dev, i32, (B,)),
           _arg("new_len", new_len, dev, i32, (B,)),
           _arg("free_pages", free_pages, dev, i32, (n_free,)),
-          _arg("block_table", block_table, dev, i32, (B, blocks)), *addr, _status(status, dev),
-          _raw_stream(stream, dev))
-    return outs
+          _arg("block_table", block_table, dev, i32, (B, blocks)), sp, cp, pp, lp, up,
+          _status(status, dev), _raw_stream(stream, dev))
+    return seq_len, cu_seqlens, positions, slots, used

@@ -32,6 +32,7 @@
 #include <type_traits>
 
 #include "gdn_internal.h"
+#include "gdn_launch.cuh"
 
 namespace gdn {
 namespace {
@@ -40,6 +41,7 @@ constexpr int AT_W = 4;            // warps per CTA
 constexpr int AT_NT = 32 * AT_W;
 constexpr int AT_G = 8;            // query heads per piece
 constexpr int AT_SMS = 152;
+constexpr float AT_LAZY = 8.f;     // log2 units
 // What a piece costs beside its tiles, in units (its first loads and its end): without it a
 // CTA with many short requests lags (61 ragged requests 128 against 102 us; 2 to 5 units: the same).
 constexpr int AT_START = 1;
@@ -67,12 +69,13 @@ struct AttnArgs {
   int64_t B, Hq, Hk, pages, max_blocks, qs;
   int P, G, HG;   // tokens per page, query heads per key head, pieces of AT_G of them
   float sl;       // scale log2(e)
+  float lazy;     // AT_LAZY in units of the unscaled scores
   const void *q, *kc, *vc;
   const int32_t *table, *len;
   void* o;
   float* lse;
   Join* join;     // [CTAs]
-  float2* ml;     // [CTAs][2][AT_G] maximum (log2 units) and sum
+  float2* ml;     // [CTAs][2][AT_G] reference score (unscaled) and sum
   float* acc;     // [CTAs][2][AT_G][D]
   int32_t* status;
 };
@@ -145,7 +148,7 @@ template <int D, typename T> struct Smem {
 // What a warp keeps of its piece.
 template <int D> struct Acc {
   float o[D / 16][4];  // O^T tiles
-  float m[2], l[2];    // of heads 2t, 2t + 1: maximum (log2 units), this lane's part of the sum
+  float m[2], l[2];    // of heads 2t, 2t + 1: reference score (unscaled), this lane's part of the sum
 };
 
 // NK blocks of 16 keys by DP elements.
@@ -257,7 +260,8 @@ __device__ __forceinline__ void weigh(const Tile<DP, float, NK>& v, const float 
     }
 }
 
-template <int DP, typename T, int NK>
+// FULL: every row counts.
+template <bool FULL, int DP, typename T, int NK>
 __device__ __forceinline__ void load_k(Tile<DP, T, NK>& k, const T* base, const Block (&blk)[NK],
                                        int64_t row) {
   constexpr int EL = 16 / (int)sizeof(T);
@@ -265,7 +269,7 @@ __device__ __forceinline__ void load_k(Tile<DP, T, NK>& k, const T* base, const 
 #pragma unroll
   for (int i = 0; i < NK; ++i) {
     const T* p = base + blk[i].off + g * row + t * EL;
-    const bool in0 = g < blk[i].n, in1 = g + 8 < blk[i].n;
+    const bool in0 = FULL || g < blk[i].n, in1 = FULL || g + 8 < blk[i].n;
 #pragma unroll
     for (int c = 0; c < DP / (4 * EL); ++c) {
       const uint4 z = make_uint4(0, 0, 0, 0);
@@ -274,7 +278,7 @@ __device__ __forceinline__ void load_k(Tile<DP, T, NK>& k, const T* base, const 
     }
   }
 }
-template <int DP, typename T, int NK>
+template <bool FULL, int DP, typename T, int NK>
 __device__ __forceinline__ void load_v(Tile<DP, T, NK>& v, const T* base, const Block (&blk)[NK],
                                        int64_t row) {
   constexpr int EL = 16 / (int)sizeof(T);
@@ -286,11 +290,23 @@ __device__ __forceinline__ void load_v(Tile<DP, T, NK>& v, const T* base, const 
       // the fragment's keys: 2t, 2t + 1, 2t + 8, 2t + 9 (bf16), t, t + 4, t + 8, t + 12 (fp32)
       const int key = sizeof(T) == 2 ? 2 * t + (z & 1) + 8 * (z >> 1) : t + 4 * z;
       const T* p = base + blk[i].off + key * row + g * EL;
-      const bool in = key < blk[i].n;
+      const bool in = FULL || key < blk[i].n;
 #pragma unroll
       for (int c = 0; c < DP / (8 * EL); ++c)
         v.r[i][z][c] = in ? ldg16(p + c * 8 * EL) : make_uint4(0, 0, 0, 0);
     }
+}
+template <int DP, typename T, int NK>
+__device__ __forceinline__ void load_k(Tile<DP, T, NK>& k, const T* base, const Block (&blk)[NK],
+                                       int64_t row, bool full) {
+  if (full) load_k<true>(k, base, blk, row);
+  else load_k<false>(k, base, blk, row);
+}
+template <int DP, typename T, int NK>
+__device__ __forceinline__ void load_v(Tile<DP, T, NK>& v, const T* base, const Block (&blk)[NK],
+                                       int64_t row, bool full) {
+  if (full) load_v<true>(v, base, blk, row);
+  else load_v<false>(v, base, blk, row);
 }
 
 // Tokens [0, n) of request b, units [t0, t1) of CTA tiles.
@@ -331,67 +347,91 @@ __device__ void piece(const AttnArgs& ar, char* smem, int64_t b, int n, int hk, 
   const T* kc = reinterpret_cast<const T*>(ar.kc) + (int64_t)hk * D;
   const T* vc = reinterpret_cast<const T*>(ar.vc) + (int64_t)hk * D;
   const int32_t* table = ar.table + b * ar.max_blocks;
-  const int pb = ar.P / 16, nb = (n - 1) / 16 + 1;  // 16-key blocks per page, and in all
-  auto page_of = [&](int tile, int i) {
-    const int blk = (tile * AT_W + warp) * NK + i;
-    return blk < nb && tile < t1 ? table[blk / pb] : -1;
-  };
-  auto place = [&](int tile, int i, int32_t page) {
-    const int blk = (tile * AT_W + warp) * NK + i;
-    Block x;
-    x.n = blk < nb && tile < t1 ? min(16, n - blk * 16) : 0;
-    if (x.n > 0 && (page < 0 || page >= ar.pages)) {
-      *bad = 1;
-      x.n = 0;
+  // A warp's next blocks of 16 keys: number, page of the table and block in the page, moved on
+  // by the blocks of a CTA tile without dividing.
+  constexpr int STEP = AT_W * NK;
+  const int pb = ar.P / 16, end = min((n - 1) / 16 + 1, t1 * STEP);
+  const int dpi = STEP / pb, dpo = STEP % pb;
+  int blk = t0 * STEP + warp * NK, pi = blk / pb, po = blk % pb;
+  int32_t pg[NK];  // pages of the blocks that were looked up, one tile ahead
+  int pofs[NK], cnt[NK];
+  auto look_up = [&]() {
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      const bool wrap = po + i >= pb;
+      const bool live = blk + i < end;
+      pg[i] = live ? table[pi + wrap] : -1;
+      pofs[i] = (po + i - (wrap ? pb : 0)) * 16;
+      cnt[i] = live ? min(16, n - (blk + i) * 16) : 0;
     }
-    x.off = x.n > 0 ? ((int64_t)page * ar.P + (blk % pb) * 16) * row : 0;
-    return x;
+    blk += STEP;
+    pi += dpi;
+    po += dpo;
+    if (po >= pb) {
+      po -= pb;
+      ++pi;
+    }
+  };
+  // their places; whether all 16 rows of all of them count
+  auto place = [&](Block (&x)[NK]) {
+    bool full = true;
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      x[i].n = cnt[i];
+      if (cnt[i] > 0 && (pg[i] < 0 || pg[i] >= ar.pages)) {
+        *bad = 1;
+        x[i].n = 0;
+      }
+      x[i].off = x[i].n > 0 ? ((int64_t)pg[i] * ar.P + pofs[i]) * row : 0;
+      full = full && x[i].n == 16;
+    }
+    return full;
   };
   Tile<DP, T, NK> k, v;
   Block cur[NK];
-  int32_t page[NK];
-#pragma unroll
-  for (int i = 0; i < NK; ++i) cur[i] = place(t0, i, page_of(t0, i));
+  look_up();
+  bool full = place(cur);
   if constexpr (kParts == 1) {
-    load_k(k, kc, cur, row);
-    load_v(v, vc, cur, row);
+    load_k(k, kc, cur, row, full);
+    load_v(v, vc, cur, row, full);
   }
-#pragma unroll
-  for (int i = 0; i < NK; ++i) page[i] = page_of(t0 + 1, i);
+  look_up();
   __syncthreads();  // Q is there
 #pragma unroll 1
   for (int tile = t0; tile < t1; ++tile) {
     Block nxt[NK];
-#pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      nxt[i] = place(tile + 1, i, page[i]);
-      page[i] = page_of(tile + 2, i);
-    }
+    const bool nfull = place(nxt);
+    look_up();
     float s[NK][4] = {};
 #pragma unroll
     for (int z = 0; z < kParts; ++z) {
-      if constexpr (kParts > 1) load_k(k, kc + z * DP, cur, row);
+      if constexpr (kParts > 1) load_k(k, kc + z * DP, cur, row, full);
       scores<D, DP, NK>(k, smem + z * DP * sizeof(T), s);
     }
-    if constexpr (kParts == 1) load_k(k, kc, nxt, row);
-    float mx[2] = {a.m[0], a.m[1]};
+    if constexpr (kParts == 1) load_k(k, kc, nxt, row, nfull);
+    if (!full)
+#pragma unroll
+      for (int i = 0; i < NK; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (g + 8 * (j >> 1) >= cur[i].n) s[i][j] = -INFINITY;
+    float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
     for (int i = 0; i < NK; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s[i][j] = g + 8 * (j >> 1) < cur[i].n ? s[i][j] * ar.sl : -INFINITY;
-        mx[j & 1] = fmaxf(mx[j & 1], s[i][j]);
-      }
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], o));
-    if (__any_sync(0xffffffffu, mx[0] > a.m[0] || mx[1] > a.m[1])) {
+      for (int j = 0; j < 4; ++j) mx[j & 1] = fmaxf(mx[j & 1], s[i][j]);
+    // The reference value m of a head follows the maximum only when a score is above it by
+    // AT_LAZY: weights up to 2^AT_LAZY lose nothing in fp32 sums or in bf16's relative rounding,
+    // and most tiles need one vote in place of six shuffles and a pass over the accumulators.
+    if (__any_sync(0xffffffffu, mx[0] > a.m[0] + ar.lazy || mx[1] > a.m[1] + ar.lazy)) {
       float f[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        f[j] = ex2(a.m[j] - mx[j]);  // 0 from -inf; mx is finite or above m where it is used
-        if (mx[j] == a.m[j]) f[j] = 1.f;
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1)
+          mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], o));
+        mx[j] = fmaxf(mx[j], a.m[j]);
+        f[j] = mx[j] == a.m[j] ? 1.f : ex2((a.m[j] - mx[j]) * ar.sl);  // 0 from -inf
         a.l[j] *= f[j];
         a.m[j] = mx[j];
       }
@@ -405,17 +445,19 @@ __device__ void piece(const AttnArgs& ar, char* smem, int64_t b, int n, int hk, 
     for (int i = 0; i < NK; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        s[i][j] = ex2(s[i][j] - base[j & 1]);
+        // the difference first: equal scores weigh the same whatever their size
+        s[i][j] = ex2((s[i][j] - base[j & 1]) * ar.sl);
         a.l[j & 1] += s[i][j];
       }
 #pragma unroll
     for (int z = 0; z < kParts; ++z) {
-      if constexpr (kParts > 1) load_v(v, vc + z * DP, cur, row);
+      if constexpr (kParts > 1) load_v(v, vc + z * DP, cur, row, full);
       weigh<D, DP, NK>(v, s, a, z);
     }
-    if constexpr (kParts == 1) load_v(v, vc, nxt, row);
+    if constexpr (kParts == 1) load_v(v, vc, nxt, row, nfull);
 #pragma unroll
     for (int i = 0; i < NK; ++i) cur[i] = nxt[i];
+    full = nfull;
   }
 #pragma unroll
   for (int j = 0; j < 2; ++j)
@@ -453,7 +495,7 @@ __device__ void finish(const AttnArgs& ar, char* smem, float2 (*ml)[AT_G], int64
     const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
     for (int w = 0; w < AT_W; ++w) {
-      const float f = ex2(ml[w][h].x - base);
+      const float f = ex2((ml[w][h].x - base) * ar.sl);
       const float2 y = *reinterpret_cast<const float2*>(so + (w * AT_G + h) * kORow + d);
       l = fmaf(ml[w][h].y, f, l);
       o.x = fmaf(y.x, f, o.x);
@@ -471,7 +513,7 @@ __device__ void finish(const AttnArgs& ar, char* smem, float2 (*ml)[AT_G], int64
     else
       *reinterpret_cast<float2*>(out) = make_float2(o.x * r, o.y * r);
     if (d == 0 && ar.lse)
-      ar.lse[b * ar.Hq + h0 + h] = (base + log2f(l)) * 0.69314718055994531f;
+      ar.lse[b * ar.Hq + h0 + h] = (base * ar.sl + log2f(l)) * 0.69314718055994531f;
   }
 }
 
@@ -504,7 +546,8 @@ __global__ void __launch_bounds__(AT_NT, Cfg<D, T>::kCtas) k_attn_decode(AttnArg
   constexpr int TK = Cfg<D, T>::kKeys * AT_W;  // keys per unit
   const int tid = threadIdx.x;
   const int64_t c = blockIdx.x, cap = ar.max_blocks * ar.P, per = ar.Hk * ar.HG;
-  asm volatile("griddepcontrol.launch_dependents;");
+  after_previous();
+  before_next();
   int bad = 0;
   auto length = [&](int64_t b) {
     const int32_t n = ar.len[b];
@@ -617,7 +660,8 @@ __global__ void __launch_bounds__(AJ_NT) k_attn_join(AttnArgs ar, int ctas) {
   __shared__ float s_w[MAXC + 1], s_red[NW][2];
   __shared__ float4 s_o[AJ_NT / 16][AJ_DC / 4];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  after_previous();
+  before_next();
   // pieces of few parts from the front of the list, of many from its end, in the order of the CTAs
   // (every CTA here makes the same list)
   int n_few = 0, n_many = 0;
@@ -658,7 +702,7 @@ __global__ void __launch_bounds__(AJ_NT) k_attn_join(AttnArgs ar, int ctas) {
     float m = ml.x;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float base = m == -INFINITY ? 0.f : m, f = ex2(ml.x - base);
+    const float base = m == -INFINITY ? 0.f : m, f = ex2((ml.x - base) * ar.sl);
     float l = ml.y * f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -681,7 +725,7 @@ __global__ void __launch_bounds__(AJ_NT) k_attn_join(AttnArgs ar, int ctas) {
 #pragma unroll
     for (int v = 0; v < V; ++v)
       if (in) store_o(reinterpret_cast<T*>(ar.o) + row * D + lane * 4 + v * 128, a[v], r);
-    if (lane == 0 && ar.lse) ar.lse[row] = (base + log2f(l)) * 0.69314718055994531f;
+    if (lane == 0 && ar.lse) ar.lse[row] = (base * ar.sl + log2f(l)) * 0.69314718055994531f;
   }
   for (int x = blockIdx.x; x < many; x += gridDim.x) {
     const int p = MAXC - 1 - x / (AT_G * (D / AJ_DC)), h = x / (D / AJ_DC) % AT_G;
@@ -702,7 +746,7 @@ __global__ void __launch_bounds__(AJ_NT) k_attn_join(AttnArgs ar, int ctas) {
     const float base = m == -INFINITY ? 0.f : m;
     for (int i = tid; i < n; i += AJ_NT) {
       const float2 y = ar.ml[slot(i)];
-      const float f = ex2(y.x - base);
+      const float f = ex2((y.x - base) * ar.sl);
       s_w[i] = f;
       l = fmaf(y.y, f, l);
     }
@@ -724,7 +768,7 @@ __global__ void __launch_bounds__(AJ_NT) k_attn_join(AttnArgs ar, int ctas) {
       const int64_t row = (int64_t)j.b * ar.Hq + j.h + h;
       store_o(reinterpret_cast<T*>(ar.o) + row * D + d0 + tid * 4, a, l != 0.f ? 1.f / l : 0.f);
       if (tid == 0 && d0 == 0 && ar.lse)
-        ar.lse[row] = (base + log2f(l)) * 0.69314718055994531f;
+        ar.lse[row] = (base * ar.sl + log2f(l)) * 0.69314718055994531f;
     }
   }
 }
@@ -788,20 +832,10 @@ cudaError_t launch(AttnArgs ar, char* ws, cudaStream_t st) {
   ar.join = (Join*)(ws + pl.join);
   ar.ml = (float2*)(ws + pl.ml);
   ar.acc = (float*)(ws + pl.acc);
-  k_attn_decode<D, T><<<pl.ctas, AT_NT, Smem<D, T>::kBytes, st>>>(ar);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_behind(k_attn_decode<D, T>, dim3(pl.ctas), AT_NT,
+                                      Smem<D, T>::kBytes, st, ar);
   if (e != cudaSuccess) return e;
-  // the join starts as the pass's CTAs leave and waits for its end on the device
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(AJ_CTAS);
-  cfg.blockDim = dim3(AJ_NT);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_attn_join<D, T>, ar, pl.ctas);
+  return launch_behind(k_attn_join<D, T>, dim3(AJ_CTAS), AJ_NT, 0, st, ar, pl.ctas);
 }
 
 }  // namespace
@@ -845,6 +879,7 @@ gdn_status gdn_attn_decode(const gdn_attn_problem* p, const void* q, const void*
   ar.G = (int)(p->Hq / p->Hk);
   ar.HG = (ar.G + AT_G - 1) / AT_G;
   ar.sl = (p->scale > 0.f ? p->scale : 1.0f / sqrtf((float)p->D)) * 1.4426950408889634f;
+  ar.lazy = fminf(AT_LAZY / ar.sl, 1e30f);
   ar.q = q;
   ar.kc = k_cache;
   ar.vc = v_cache;

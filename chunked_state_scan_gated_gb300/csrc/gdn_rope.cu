@@ -25,6 +25,7 @@
 #include <type_traits>
 
 #include "gdn_internal.h"
+#include "gdn_launch.cuh"
 #include "gdn_vec.cuh"
 
 namespace gdn {
@@ -346,6 +347,8 @@ struct Loader {
 template <bool CACHE, bool INTER, int LPR, typename T>
 __global__ void __launch_bounds__(RO_NT, 2) k_qk_norm_rope_fwd(RopeArgs ar) {
   extern __shared__ __align__(16) char smem[];
+  after_previous();
+  before_next();
   constexpr int U = RO_FU, RPL = 32 / LPR, SE = 32 * 8;
   constexpr int NST = RO_RING / (U * SE * (int)sizeof(T));
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = (lane & (LPR - 1)) * 8;
@@ -469,7 +472,8 @@ __global__ void __launch_bounds__(RO_NT, 2) k_qk_norm_rope_bwd(RopeArgs ar) {
   const int groups = ar.gq + ar.gk;
   const int other = INTER ? 0 : other_lane(ar, e);
   const int mine = lane * 8, theirs = (lane / LPR * LPR + other) * 8;
-  asm volatile("griddepcontrol.launch_dependents;");
+  after_previous();
+  before_next();
   F2 dw[2][4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) dw[0][j] = dw[1][j] = f2(0.f, 0.f);
@@ -607,7 +611,8 @@ __global__ void __launch_bounds__(RO_NT) k_qk_norm_rope_dw(int n_part, int D, co
   __shared__ double acc[RD_ROWS][RD_COLS];
   const int col = threadIdx.x % RD_COLS, row = threadIdx.x / RD_COLS;
   const int e = blockIdx.x * RD_COLS + col;  // D is a multiple of 8: e < 2 D
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  after_previous();
+  before_next();
   double s = 0.0;
 #pragma unroll 5
   for (int p = row; p < n_part; p += RD_ROWS) s += part[(int64_t)p * 2 * D + e];
@@ -685,8 +690,7 @@ template <typename K>
 cudaError_t launch(K kernel, const RopeArgs& ar, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RO_SMEM);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)ctas_of(ar), RO_NT, RO_SMEM, st>>>(ar);
-  return cudaGetLastError();
+  return launch_behind(kernel, dim3((unsigned)ctas_of(ar)), RO_NT, RO_SMEM, st, ar);
 }
 
 // Runs f with the lanes per row, the pairing and the type as template arguments.
@@ -821,19 +825,10 @@ gdn_status gdn_qk_norm_rope_bwd(const gdn_rope_problem* p, const void* q, const 
     });
     if (e != cudaSuccess) return GDN_ERR_CUDA;
   }
-  // starts as the pass's CTAs leave and waits for its end on the device
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(2 * ar.D / RD_COLS));
-  cfg.blockDim = dim3(RO_NT);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
   const cudaError_t e =
-      cudaLaunchKernelEx(&cfg, k_qk_norm_rope_dw, (int)ctas, ar.D, (const float*)workspace,
-                         ar.Hq ? dwq : (float*)nullptr, ar.Hk ? dwk : (float*)nullptr);
+      launch_behind(k_qk_norm_rope_dw, dim3((unsigned)(2 * ar.D / RD_COLS)), RO_NT, 0, st,
+                    (int)ctas, ar.D, (const float*)workspace, ar.Hq ? dwq : nullptr,
+                    ar.Hk ? dwk : nullptr);
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 

@@ -15,6 +15,7 @@
 #include <string.h>
 
 #include "gdn_internal.h"
+#include "gdn_launch.cuh"
 
 namespace gdn {
 namespace {
@@ -71,6 +72,8 @@ __global__ void __launch_bounds__(SM_NT) k_slot_map(SlotArgs ar) {
   __shared__ int64_t part[SM_NT / 32][2];
   __shared__ int64_t s_cu[SM_NT + 1], s_first[SM_NT + 1];
   __shared__ uint32_t s_ctx[SM_NT];
+  after_previous();
+  before_next();
   const int tid = threadIdx.x;
   const int64_t t0 = (int64_t)blockIdx.x * SM_TOK;
   const int64_t t1 = t0 + SM_TOK < ar.n_tokens ? t0 + SM_TOK : ar.n_tokens;
@@ -191,6 +194,7 @@ extern "C" gdn_status gdn_slot_map(const gdn_slot_problem* p, const int32_t* ctx
   ar.used = used;
   ar.status = status;
   const int64_t ctas = p->n_tokens > 0 ? (p->n_tokens + SM_TOK - 1) / SM_TOK : 1;
-  k_slot_map<<<(unsigned)ctas, SM_NT, 0, (cudaStream_t)stream>>>(ar);
-  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  const cudaError_t e =
+      launch_behind(k_slot_map, dim3((unsigned)ctas), SM_NT, 0, (cudaStream_t)stream, ar);
+  return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }

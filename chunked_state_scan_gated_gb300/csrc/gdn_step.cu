@@ -15,6 +15,7 @@
 #include <string.h>
 
 #include "gdn_internal.h"
+#include "gdn_launch.cuh"
 #include "gdn_vec.cuh"
 
 namespace gdn {
@@ -57,6 +58,8 @@ template <typename T, bool FULL>
 __global__ void __launch_bounds__(ST_NT) k_step(StepArgs ar) {
   __shared__ float s_q[ST_NT / 32][kMaxHeadDim], s_k[ST_NT / 32][kMaxHeadDim];
   __shared__ float4 s_u[ST_NT / 32][2][ST_LANES];
+  after_previous();
+  before_next();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const unsigned head = blockIdx.x / ar.slices;  // row and V head
   const int64_t b = head / (unsigned)ar.H, h = head % (unsigned)ar.H;
@@ -220,9 +223,9 @@ extern "C" gdn_status gdn_step(const gdn_problem* p, int64_t n_slots, const int3
   cudaStream_t st = (cudaStream_t)stream;
   ar.slices = (unsigned)((pr.dv + ST_COLS - 1) / ST_COLS);
   const unsigned ctas = (unsigned)(pr.B * pr.H * ar.slices);
-  if (pr.dtype == GDN_BF16)  // dk = dv = 128
-    k_step<__nv_bfloat16, true><<<ctas, ST_NT, 0, st>>>(ar);
-  else
-    k_step<float, false><<<ctas, ST_NT, 0, st>>>(ar);
-  return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+  const cudaError_t e =
+      pr.dtype == GDN_BF16  // dk = dv = 128
+          ? launch_behind(k_step<__nv_bfloat16, true>, dim3(ctas), ST_NT, 0, st, ar)
+          : launch_behind(k_step<float, false>, dim3(ctas), ST_NT, 0, st, ar);
+  return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
