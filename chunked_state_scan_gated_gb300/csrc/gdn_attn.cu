@@ -19,7 +19,9 @@
 // data: a warp's next K tile is on its way while it does the softmax and V's product, and the
 // next V tile during the next K product; 8 to 16 such warps per SM keep 64 to 128 KB in flight.
 // fp32 caches use tf32 products of the two-term split x = hi + lo (hi hi + hi lo + lo hi:
-// 2^-21 of each product's size), which keeps fp32 accuracy at the same layout.
+// 2^-21 of each product's size), which keeps fp32 accuracy at the same layout.  The split is
+// done with integer and fp32 instructions at full rate (131001 tokens of 8 heads of 128: 167 us
+// against 234 us with conversion instructions and a test of every value for infinities).
 //
 // Split: the unit is a CTA tile of one (request, key head); the units of all requests in a
 // row are divided evenly over the CTAs of one wave, whatever the lengths: no tail, and one long
@@ -48,14 +50,14 @@ constexpr int AT_START = 1;
 
 // Keys per warp tile and CTAs per SM: the K and V tiles and the accumulators of D x 8 fill
 // most of a CTA's share of the registers.
-// kParts > 1: the two tiles do not fit; they are loaded that many parts of D at a time, as used.
+// kParts > 1: the two tiles do not fit; they go by that many parts of D.
 template <int D, typename T> struct Cfg;
 template <> struct Cfg<64, __nv_bfloat16> { static constexpr int kKeys = 32, kCtas = 4, kParts = 1; };
 template <> struct Cfg<128, __nv_bfloat16> { static constexpr int kKeys = 16, kCtas = 3, kParts = 1; };
 template <> struct Cfg<256, __nv_bfloat16> { static constexpr int kKeys = 16, kCtas = 2, kParts = 1; };
 template <> struct Cfg<64, float> { static constexpr int kKeys = 16, kCtas = 3, kParts = 1; };
 template <> struct Cfg<128, float> { static constexpr int kKeys = 16, kCtas = 2, kParts = 1; };
-template <> struct Cfg<256, float> { static constexpr int kKeys = 16, kCtas = 2, kParts = 4; };
+template <> struct Cfg<256, float> { static constexpr int kKeys = 16, kCtas = 2, kParts = 2; };
 
 // A partial piece in the workspace: slot 2c of CTA c is the piece that began before it, slot
 // 2c + 1 the one that goes on behind it.
@@ -113,17 +115,29 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-// x = hi + lo with hi, lo in tf32 (lo's own rounding is 2^-23 of x).  An infinite or NaN x (or one
-// that hi's rounding would make infinite) goes into lo alone: mma_split multiplies lo only with the
-// other operand's hi, so that no 0 * inf arises beside the product itself.
+// x = hi + lo with hi, lo in tf32: hi is x rounded to nearest (ties away), lo what is left, cut
+// after its 11 bits (2^-22 of x, of either sign).  SAFE: an infinite or NaN x, or one that hi's
+// rounding could make infinite, goes into lo alone: mma_split multiplies lo only with the other
+// operand's hi, so that no 0 * inf arises beside the product itself.
+template <bool SAFE>
 __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t* hi, uint32_t* lo) {
-  uint32_t h, l;
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(h) : "f"(__uint_as_float(x)));
-  const float r = __uint_as_float(x) - __uint_as_float(h);
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(l) : "f"(r));
-  const bool huge = (x & 0x7f800000u) >= 0x7f000000u;
+  const uint32_t h = (x + 0x1000u) & 0xffffe000u;
+  const uint32_t l = __float_as_uint(__uint_as_float(x) - __uint_as_float(h)) & 0xffffe000u;
+  const bool huge = SAFE && (x & 0x7f800000u) >= 0x7f000000u;
   *hi = huge ? 0u : h;
   *lo = huge ? x : l;
+}
+// acc += 4 v: not finite once any value is not, or is as large as 2^126 (a sum that overflows
+// only takes the SAFE form without need)
+__device__ __forceinline__ void probe(const uint4& v, uint64_t* acc) {
+  asm("{\n\t.reg .b64 a, b, f;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+      "mov.b64 f, 0x4080000040800000;\n\tfma.rn.f32x2 %0, a, f, %0;\n\t"
+      "fma.rn.f32x2 %0, b, f, %0;\n\t}"
+      : "+l"(*acc) : "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w));
+}
+__device__ __forceinline__ bool plain(uint64_t acc) {  // for every lane of the warp
+  const float x = __uint_as_float((uint32_t)acc), y = __uint_as_float((uint32_t)(acc >> 32));
+  return !__any_sync(0xffffffffu, !(fabsf(x) + fabsf(y) < INFINITY));
 }
 // c += A B with A and B given as split values
 __device__ __forceinline__ void mma_split(float (&c)[4], const uint32_t (&ah)[4],
@@ -158,6 +172,18 @@ struct Tile {
   uint4 r[NK][4][DP / (8 * EL)];  // K: rows g, g + 8 of even, then odd chunks; V: 4 keys
 };
 
+template <int DP, int NK>
+__device__ __forceinline__ bool plain(const Tile<DP, float, NK>& x) {
+  uint64_t acc = 0;
+#pragma unroll
+  for (int i = 0; i < NK; ++i)
+#pragma unroll
+    for (int z = 0; z < 4; ++z)
+#pragma unroll
+      for (int c = 0; c < DP / 32; ++c) probe(x.r[i][z][c], &acc);
+  return plain(acc);
+}
+
 // One 16-key block's place in the cache: rows kept, and the block's first row.
 struct Block {
   int64_t off;  // element offset of its first row
@@ -182,9 +208,9 @@ __device__ __forceinline__ void scores(const Tile<DP, __nv_bfloat16, NK>& k, con
     }
   }
 }
-template <int D, int DP, int NK>
-__device__ __forceinline__ void scores(const Tile<DP, float, NK>& k, const char* qs,
-                                       float (&s)[NK][4]) {
+template <bool SAFE, int D, int DP, int NK>
+__device__ __forceinline__ void scores_split(const Tile<DP, float, NK>& k, const char* qs,
+                                             float (&s)[NK][4]) {
   constexpr int kRow = Smem<D, float>::kRow;
   const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
 #pragma unroll
@@ -197,16 +223,23 @@ __device__ __forceinline__ void scores(const Tile<DP, float, NK>& k, const char*
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         uint32_t ah[4], al[4];
-        split_tf32(word(a0, 2 * u), &ah[0], &al[0]);
-        split_tf32(word(a1, 2 * u), &ah[1], &al[1]);
-        split_tf32(word(a0, 2 * u + 1), &ah[2], &al[2]);
-        split_tf32(word(a1, 2 * u + 1), &ah[3], &al[3]);
+        split_tf32<SAFE>(word(a0, 2 * u), &ah[0], &al[0]);
+        split_tf32<SAFE>(word(a1, 2 * u), &ah[1], &al[1]);
+        split_tf32<SAFE>(word(a0, 2 * u + 1), &ah[2], &al[2]);
+        split_tf32<SAFE>(word(a1, 2 * u + 1), &ah[3], &al[3]);
         const uint32_t h[2] = {word(bh, 2 * u), word(bh, 2 * u + 1)};
         const uint32_t l[2] = {word(bl, 2 * u), word(bl, 2 * u + 1)};
         mma_split(s[i], ah, al, h, l);
       }
     }
   }
+}
+
+template <int D, int DP, int NK>
+__device__ __forceinline__ void scores(const Tile<DP, float, NK>& k, const char* qs,
+                                       float (&s)[NK][4]) {
+  if (plain(k)) scores_split<false, D>(k, qs, s);
+  else scores_split<true, D>(k, qs, s);
 }
 
 // O^T += V^T P^T over part `part` of D; p holds the weights in the scores' layout.
@@ -231,9 +264,9 @@ __device__ __forceinline__ void weigh(const Tile<DP, __nv_bfloat16, NK>& v,
       }
   }
 }
-template <int D, int DP, int NK>
-__device__ __forceinline__ void weigh(const Tile<DP, float, NK>& v, const float (&p)[NK][4],
-                                      Acc<D>& a, int part) {
+template <bool SAFE, int D, int DP, int NK>
+__device__ __forceinline__ void weigh_split(const Tile<DP, float, NK>& v, const float (&p)[NK][4],
+                                            Acc<D>& a, int part) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int i = 0; i < NK; ++i)
@@ -245,7 +278,7 @@ __device__ __forceinline__ void weigh(const Tile<DP, float, NK>& v, const float 
         const int src = (t + 4 * z) * 4 + (g >> 1);
         const float e = __shfl_sync(0xffffffffu, p[i][2 * u], src);
         const float f = __shfl_sync(0xffffffffu, p[i][2 * u + 1], src);
-        split_tf32(__float_as_uint(g & 1 ? f : e), &bh[z], &bl[z]);
+        split_tf32<true>(__float_as_uint(g & 1 ? f : e), &bh[z], &bl[z]);
       }
 #pragma unroll
       for (int c = 0; c < DP / 32; ++c)
@@ -254,10 +287,18 @@ __device__ __forceinline__ void weigh(const Tile<DP, float, NK>& v, const float 
           uint32_t ah[4], al[4];
 #pragma unroll
           for (int z = 0; z < 4; ++z)
-            split_tf32(word(v.r[i][2 * u + (z >> 1)][c], 2 * w + (z & 1)), &ah[z], &al[z]);
+            split_tf32<SAFE>(word(v.r[i][2 * u + (z >> 1)][c], 2 * w + (z & 1)), &ah[z],
+                             &al[z]);
           mma_split(a.o[part * (DP / 16) + c * 2 + w], ah, al, bh, bl);
         }
     }
+}
+
+template <int D, int DP, int NK>
+__device__ __forceinline__ void weigh(const Tile<DP, float, NK>& v, const float (&p)[NK][4],
+                                      Acc<D>& a, int part) {
+  if (plain(v)) weigh_split<false>(v, p, a, part);
+  else weigh_split<true>(v, p, a, part);
 }
 
 // FULL: every row counts.
@@ -327,10 +368,10 @@ __device__ void piece(const AttnArgs& ar, char* smem, int64_t b, int n, int hk, 
     char* dst = smem + h * kRow + c * 16;
     if constexpr (sizeof(T) == 4) {
       uint4 hi, lo;
-      split_tf32(x.x, &hi.x, &lo.x);
-      split_tf32(x.y, &hi.y, &lo.y);
-      split_tf32(x.z, &hi.z, &lo.z);
-      split_tf32(x.w, &hi.w, &lo.w);
+      split_tf32<true>(x.x, &hi.x, &lo.x);
+      split_tf32<true>(x.y, &hi.y, &lo.y);
+      split_tf32<true>(x.z, &hi.z, &lo.z);
+      split_tf32<true>(x.w, &hi.w, &lo.w);
       *reinterpret_cast<uint4*>(dst) = hi;
       *reinterpret_cast<uint4*>(dst + AT_G * kRow) = lo;
     } else {
@@ -387,14 +428,14 @@ __device__ void piece(const AttnArgs& ar, char* smem, int64_t b, int n, int hk, 
     }
     return full;
   };
+  // kParts = 1: k and v in turn; else the parts K 0, 1, .., V 0, 1, .. of a tile alternate between
+  // the two buffers, each loaded one step ahead
   Tile<DP, T, NK> k, v;
   Block cur[NK];
   look_up();
   bool full = place(cur);
-  if constexpr (kParts == 1) {
-    load_k(k, kc, cur, row, full);
-    load_v(v, vc, cur, row, full);
-  }
+  load_k(k, kc, cur, row, full);
+  if constexpr (kParts == 1) load_v(v, vc, cur, row, full);
   look_up();
   __syncthreads();  // Q is there
 #pragma unroll 1
@@ -403,12 +444,18 @@ __device__ void piece(const AttnArgs& ar, char* smem, int64_t b, int n, int hk, 
     const bool nfull = place(nxt);
     look_up();
     float s[NK][4] = {};
+    if constexpr (kParts == 1) {
+      scores<D, DP, NK>(k, smem, s);
+      load_k(k, kc, nxt, row, nfull);
+    } else {
 #pragma unroll
-    for (int z = 0; z < kParts; ++z) {
-      if constexpr (kParts > 1) load_k(k, kc + z * DP, cur, row, full);
-      scores<D, DP, NK>(k, smem + z * DP * sizeof(T), s);
+      for (int z = 0; z < kParts; ++z) {
+        Tile<DP, T, NK>&x = z & 1 ? v : k, &y = z & 1 ? k : v;
+        if (z + 1 < kParts) load_k(y, kc + (z + 1) * DP, cur, row, full);
+        else load_v(y, vc, cur, row, full);
+        scores<D, DP, NK>(x, smem + z * DP * sizeof(T), s);
+      }
     }
-    if constexpr (kParts == 1) load_k(k, kc, nxt, row, nfull);
     if (!full)
 #pragma unroll
       for (int i = 0; i < NK; ++i)
@@ -449,12 +496,19 @@ __device__ void piece(const AttnArgs& ar, char* smem, int64_t b, int n, int hk, 
         s[i][j] = ex2((s[i][j] - base[j & 1]) * ar.sl);
         a.l[j & 1] += s[i][j];
       }
+    if constexpr (kParts == 1) {
+      weigh<D, DP, NK>(v, s, a, 0);
+      load_v(v, vc, nxt, row, nfull);
+    } else {
+      static_assert(kParts == 1 || kParts % 2 == 0, "V's first part goes where K's does");
 #pragma unroll
-    for (int z = 0; z < kParts; ++z) {
-      if constexpr (kParts > 1) load_v(v, vc + z * DP, cur, row, full);
-      weigh<D, DP, NK>(v, s, a, z);
+      for (int z = 0; z < kParts; ++z) {
+        Tile<DP, T, NK>&x = z & 1 ? v : k, &y = z & 1 ? k : v;
+        if (z + 1 < kParts) load_v(y, vc + (z + 1) * DP, cur, row, full);
+        else load_k(y, kc, nxt, row, nfull);
+        weigh<D, DP, NK>(x, s, a, z);
+      }
     }
-    if constexpr (kParts == 1) load_v(v, vc, nxt, row, nfull);
 #pragma unroll
     for (int i = 0; i < NK; ++i) cur[i] = nxt[i];
     full = nfull;
