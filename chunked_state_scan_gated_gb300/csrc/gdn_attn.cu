@@ -59,14 +59,8 @@ template <> struct Cfg<64, float> { static constexpr int kKeys = 16, kCtas = 3, 
 template <> struct Cfg<128, float> { static constexpr int kKeys = 16, kCtas = 2, kParts = 1; };
 template <> struct Cfg<256, float> { static constexpr int kKeys = 16, kCtas = 2, kParts = 2; };
 
-// A partial piece in the workspace: slot 2c of CTA c is the piece that began before it, slot
+// Parts of pieces in the workspace: slot 2c of CTA c is the piece that began before it, slot
 // 2c + 1 the one that goes on behind it.
-struct Join {
-  int32_t b, h;   // request, first query head (h < 0: no piece begins in this CTA and goes on)
-  int32_t heads;  // query heads of the piece
-  int32_t last;   // CTA that ends it
-};
-
 struct AttnArgs {
   int64_t B, Hq, Hk, pages, max_blocks, qs;
   int P, G, HG;   // tokens per page, query heads per key head, pieces of AT_G of them
@@ -76,7 +70,6 @@ struct AttnArgs {
   const int32_t *table, *len;
   void* o;
   float* lse;
-  Join* join;     // [CTAs]
   float2* ml;     // [CTAs][2][AT_G] reference score (unscaled) and sum
   float* acc;     // [CTAs][2][AT_G][D]
   int32_t* status;
@@ -571,106 +564,117 @@ __device__ void finish(const AttnArgs& ar, char* smem, float2 (*ml)[AT_G], int64
   }
 }
 
-__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* part, int64_t* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+// How the work is divided, the same for every caller.  The units of request b are those of its
+// pieces (key head x group of AT_G query heads) in a row, each its CTA tiles behind AT_START; the
+// W units of all requests are divided over C CTAs, CTA c taking [W c / C, W (c + 1) / C).
+// Each warp finds its way by itself: a lane sums up a run of requests, one scan over the lanes.
+template <int D, typename T>
+struct Schedule {
+  static constexpr int TK = Cfg<D, T>::kKeys * AT_W;  // keys per CTA tile
+  const AttnArgs& ar;
+  int64_t W, incl, excl;  // all units; up to and before this lane's run
+  int C, run, per;        // CTAs with work, requests per run, pieces per request
+
+  __device__ __forceinline__ int length(int64_t b) const {
+    const int32_t n = ar.len[b];
+    const int64_t cap = ar.max_blocks * ar.P;
+    return (int)(n < 0 ? 0 : n > cap ? cap : n);
   }
-  __syncthreads();
-  if (lane == 31) part[warp] = x;
-  __syncthreads();
-  int64_t sum = 0;
-#pragma unroll
-  for (int w = 0; w < AT_W; ++w) {
-    if (w < warp) x += part[w];
-    sum += part[w];
+  static __device__ __forceinline__ int tiles(int n) { return n > 0 ? (n - 1) / TK + 1 : 0; }
+  __device__ __forceinline__ int64_t units(int64_t b) const {
+    const int n = tiles(length(b));
+    return n > 0 ? (int64_t)(n + AT_START) * per : 0;
   }
-  *total = sum;
-  return x;  // inclusive
-}
+  static __device__ __forceinline__ int64_t scan(int64_t x) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    return x;
+  }
+  __device__ __forceinline__ Schedule(const AttnArgs& a, int ctas) : ar(a) {
+    const int lane = threadIdx.x & 31;
+    per = (int)ar.Hk * ar.HG;
+    run = (int)((ar.B + 31) / 32);
+    const int64_t b0 = (int64_t)lane * run, b1 = min(ar.B, b0 + run);
+    int64_t sum = 0;
+#pragma unroll 4
+    for (int64_t b = b0; b < b1; ++b) sum += units(b);
+    incl = scan(sum);
+    excl = incl - sum;
+    W = __shfl_sync(0xffffffffu, incl, 31);
+    C = (int)(W < ctas ? W : ctas);
+  }
+  __device__ __forceinline__ int64_t first(int c) const { return W * c / C; }
+  // the CTA of unit u: the last c with first(c) <= u
+  __device__ __forceinline__ int cta_of(int64_t u) const { return (int)(((u + 1) * C - 1) / W); }
+  // the request of unit u (0 <= u < W) and the unit's number in it
+  __device__ __forceinline__ void find(int64_t u, int64_t* b, int64_t* r) const {
+    const int lane = threadIdx.x & 31;
+    const int own = __ffs(__ballot_sync(0xffffffffu, incl > u)) - 1;
+    int64_t at = __shfl_sync(0xffffffffu, excl, own), b0 = (int64_t)own * run;
+    if (run > 1) {
+      const int64_t end = min(ar.B, b0 + run);
+      for (;; b0 += 32) {
+        const int64_t n = b0 + lane < end ? units(b0 + lane) : 0, x = scan(n);
+        const unsigned over = __ballot_sync(0xffffffffu, at + x > u);
+        if (over) {
+          const int i = __ffs(over) - 1;
+          at += __shfl_sync(0xffffffffu, x - n, i);
+          b0 += i;
+          break;
+        }
+        at += __shfl_sync(0xffffffffu, x, 31);
+      }
+    }
+    *b = b0;
+    *r = u - at;
+  }
+};
 
 template <int D, typename T>
 __global__ void __launch_bounds__(AT_NT, Cfg<D, T>::kCtas) k_attn_decode(AttnArgs ar) {
   extern __shared__ __align__(16) char smem[];
-  __shared__ int64_t part[AT_W];
   __shared__ float2 ml[AT_W][AT_G];
-  __shared__ int64_t s_b, s_r;
-  constexpr int TK = Cfg<D, T>::kKeys * AT_W;  // keys per unit
-  const int tid = threadIdx.x;
-  const int64_t c = blockIdx.x, cap = ar.max_blocks * ar.P, per = ar.Hk * ar.HG;
   after_previous();
   before_next();
+  const int tid = threadIdx.x, c = blockIdx.x;
+  const Schedule<D, T> sc(ar, gridDim.x);
   int bad = 0;
-  auto length = [&](int64_t b) {
-    const int32_t n = ar.len[b];
-    return (int)(n < 0 ? 0 : n > cap ? cap : n);
-  };
-  auto tiles = [&](int n) { return n > 0 ? (n - 1) / TK + 1 : 0; };
-  auto units = [&](int64_t b) {
-    const int n = tiles(length(b));
-    return n > 0 ? (n + AT_START) * per : 0;
-  };
-  // the units of all requests, and this CTA's share of them
-  int64_t W = 0, first = 0;
-  for (int64_t b0 = 0; b0 < ar.B; b0 += AT_NT) {
-    int64_t sum;
-    const int64_t b = b0 + tid;
-    first = block_scan(b < ar.B ? units(b) : 0, part, &sum);
-    if (c == 0 && b < ar.B && length(b) != ar.len[b]) bad = 1;
-    W += sum;
-  }
-  const int64_t C = W < gridDim.x ? W : gridDim.x;
-  const int64_t u0 = c < C ? W * c / C : 0, u1 = c < C ? W * (c + 1) / C : 0;
+  if (c == 0)
+    for (int64_t b = tid; b < ar.B; b += AT_NT) bad |= sc.length(b) != ar.len[b];
   // requests without tokens
   for (int64_t b = c; b < ar.B; b += gridDim.x)
-    if (length(b) == 0) {
+    if (sc.length(b) == 0) {
       T* o = reinterpret_cast<T*>(ar.o) + b * ar.Hq * D;
       for (int64_t i = tid; i < ar.Hq * D; i += AT_NT) o[i] = (T)0.f;
       if (ar.lse)
         for (int64_t i = tid; i < ar.Hq; i += AT_NT) ar.lse[b * ar.Hq + i] = -INFINITY;
     }
-  if (tid == 0) ar.join[c] = Join{0, -1, 0, 0};
-  if (u0 < u1) {
-    // the request that unit u0 falls in
-    int64_t done = 0;
-    for (int64_t b0 = 0; b0 < ar.B && done <= u0; b0 += AT_NT) {
-      int64_t sum;
-      const int64_t b = b0 + tid, n = b < ar.B ? units(b) : 0;
-      if (ar.B > AT_NT) first = block_scan(n, part, &sum);
-      else sum = W;
-      if (u0 >= done + first - n && u0 < done + first) {
-        s_b = b;
-        s_r = u0 - (done + first - n);
-      }
-      done += sum;
-    }
-    __syncthreads();
-    int64_t b = s_b, u = u0;
-    int n = length(b), nt = tiles(n), w = nt + AT_START;
-    int h = (int)(s_r / w), r0 = (int)(s_r % w);  // piece of the request, unit in it
+  if (c < sc.C) {
+    int64_t u = sc.first(c), b, r;
+    const int64_t u1 = sc.first(c + 1);
+    sc.find(u, &b, &r);
+    int n = sc.length(b), nt = sc.tiles(n), w = nt + AT_START;
+    int h = (int)(r / w), r0 = (int)(r % w);  // piece of the request, unit in it
     while (u < u1) {
       const int r1 = (int)(u1 - u < w - r0 ? r0 + (u1 - u) : w);
       const int t0 = max(0, r0 - AT_START), t1 = max(0, r1 - AT_START);
       if (t0 < t1) {
         const int hk = h / ar.HG, hg = h % ar.HG, heads = min(AT_G, ar.G - hg * AT_G);
-        const int h0 = hk * ar.G + hg * AT_G;
         Acc<D> a;
         piece<D, T>(ar, smem, b, n, hk, hg, t0, t1, a, &bad);
         const int64_t slot = t0 == 0 && t1 == nt ? -1 : t0 == 0 ? 2 * c + 1 : 2 * c;
-        finish<D, T>(ar, smem, ml, b, h0, heads, a, slot);
-        if (t0 == 0 && t1 < nt && tid == 0) {
-          const int64_t end = u - r0 + w - 1;  // its last unit: of the CTA with W c / C <= end
-          ar.join[c] = Join{(int32_t)b, h0, heads, (int32_t)(((end + 1) * C - 1) / W)};
-        }
+        finish<D, T>(ar, smem, ml, b, hk * ar.G + hg * AT_G, heads, a, slot);
       }
       u += r1 - r0;
       r0 = 0;
-      if (u < u1 && ++h == per) {
+      if (u < u1 && ++h == sc.per) {
         h = 0;
-        do n = length(++b); while (n == 0);
-        nt = tiles(n);
+        do n = sc.length(++b); while (n == 0);
+        nt = sc.tiles(n);
         w = nt + AT_START;
       }
     }
@@ -678,10 +682,9 @@ __global__ void __launch_bounds__(AT_NT, Cfg<D, T>::kCtas) k_attn_decode(AttnArg
   if (bad && ar.status) atomicOr(ar.status, kStatusClamped);
 }
 
-constexpr int AJ_NT = 256;
-constexpr int AJ_FEW = 8;   // parts that one warp adds up by itself
-constexpr int AJ_DC = 64;   // columns of a CTA's item
-constexpr int AJ_CTAS = 2 * AT_SMS;
+constexpr int AJ_NT = 32 * AT_G;  // a warp per query head
+constexpr int AJ_FEW = 8;        // parts that one warp adds up by itself
+constexpr int AJ_DC = 64;         // columns per item of a CTA
 
 template <typename T>
 __device__ __forceinline__ void store_o(T* o, float4 x, float r) {
@@ -701,57 +704,42 @@ __device__ __forceinline__ void add_scaled(float4& a, const float4& x, float f) 
   a.w = fmaf(x.w, f, a.w);
 }
 
-// Adds up the parts of the pieces that were split.  Each CTA collects the list of those pieces
-// (at most one begins in a CTA of the pass above).  A piece of few parts (a batch: hundreds of
-// pieces of 2 or 3) takes one warp per query head; one of many parts (a few long requests)
-// takes a CTA per query head and AJ_DC columns, 16 threads a row of columns, 16 parts at a time.
+// Adds up the parts of the pieces that were split.  CTA x serves the piece that goes on from CTA
+// x of the pass above to CTA x + 1: a piece of n parts has n - 1 CTAs.  They share its items (a
+// query head and AJ_DC columns), 16 parts at a time; or, with up to AJ_FEW parts (a batch: hundreds
+// of pieces of 2 or 3), or up to 32 where the CTAs would have to take several items each, the
+// first of them does it alone, a warp per query head (517 tokens, 9 parts, 32 items: 9.4 us for
+// the whole call against 12.7 shared; 10 parts of 3 items: 13.4 shared, 14.3 alone).  The schedule is worked out again from the lengths, which the kernels in front of the pass wrote;
+// only then does the CTA wait for the pass.
 template <int D, typename T>
-__global__ void __launch_bounds__(AJ_NT) k_attn_join(AttnArgs ar, int ctas) {
-  constexpr int MAXC = AT_SMS * 4, NW = AJ_NT / 32;
-  __shared__ Join s_list[MAXC];
-  __shared__ int16_t s_c[MAXC];
-  __shared__ int2 s_n[NW];
-  __shared__ float s_w[MAXC + 1], s_red[NW][2];
+__global__ void __launch_bounds__(AJ_NT) k_attn_join(AttnArgs ar) {
+  constexpr int NW = AJ_NT / 32, MAXC = AT_SMS * Cfg<D, T>::kCtas;
+  __shared__ float s_w[MAXC], s_red[NW][2];
   __shared__ float4 s_o[AJ_NT / 16][AJ_DC / 4];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int x = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const Schedule<D, T> sc(ar, gridDim.x);
+  int64_t b = 0, r = 0;
+  int c = 0, last = 0, h = 0;  // first and last CTA of the piece
+  if (x < sc.C) {
+    const int64_t u = sc.first(x + 1) - 1;  // CTA x's last unit, in piece [start, start + w)
+    sc.find(u, &b, &r);
+    const int w = sc.tiles(sc.length(b)) + AT_START;
+    h = (int)(r / w);
+    const int64_t start = u - r % w;
+    c = sc.cta_of(start + AT_START);
+    last = sc.cta_of(start + w - 1);
+  }
+  const int hk = h / ar.HG, hg = h % ar.HG, heads = min(AT_G, ar.G - hg * AT_G);
+  const int64_t row0 = b * ar.Hq + hk * ar.G + hg * AT_G;
+  const int n = last - c + 1;
   after_previous();
   before_next();
-  // pieces of few parts from the front of the list, of many from its end, in the order of the CTAs
-  // (every CTA here makes the same list)
-  int n_few = 0, n_many = 0;
-  for (int c0 = 0; c0 < ctas; c0 += AJ_NT) {
-    const int c = c0 + tid;
-    const Join j = c < ctas ? ar.join[c] : Join{0, -1, 0, 0};
-    const bool few = j.h >= 0 && j.last - c < AJ_FEW, many = j.h >= 0 && !few;
-    const unsigned bf = __ballot_sync(0xffffffffu, few), bm = __ballot_sync(0xffffffffu, many);
-    if (lane == 0) s_n[warp] = make_int2(__popc(bf), __popc(bm));
-    __syncthreads();
-    const unsigned below = (1u << lane) - 1u;
-    int2 at = make_int2(n_few + __popc(bf & below), n_many + __popc(bm & below));
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      const int2 y = s_n[w];
-      if (w < warp) {
-        at.x += y.x;
-        at.y += y.y;
-      }
-      n_few += y.x;
-      n_many += y.y;
-    }
-    if (j.h >= 0) {
-      const int i = few ? at.x : MAXC - 1 - at.y;
-      s_list[i] = j;
-      s_c[i] = (int16_t)c;
-    }
-    __syncthreads();
-  }
-  const int few = n_few * AT_G, many = n_many * AT_G * (D / AJ_DC);
+  if (x < c || x >= last) return;
   // parts: slot 2c + 1 of the piece's first CTA c, slot 2i of the CTAs behind it
-  for (int x = blockIdx.x * NW + warp; x < few; x += gridDim.x * NW) {
-    const Join j = s_list[x / AT_G];
-    const int c = s_c[x / AT_G], h = x % AT_G, n = j.last - c + 1;
-    if (h >= j.heads) continue;
-    auto slot = [&](int i) { return (int64_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * AT_G + h; };
+  if (n <= AJ_FEW || (n <= 32 && heads * (D / AJ_DC) > n - 1)) {
+    const int g = warp;
+    if (x > c || g >= heads) return;
+    auto slot = [&](int i) { return (int64_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * AT_G + g; };
     const float2 ml = lane < n ? ar.ml[slot(lane)] : make_float2(-INFINITY, 0.f);
     float m = ml.x;
 #pragma unroll
@@ -765,29 +753,26 @@ __global__ void __launch_bounds__(AJ_NT) k_attn_join(AttnArgs ar, int ctas) {
     float4 a[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) a[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < n; i0 += AJ_FEW)
 #pragma unroll
-    for (int i = 0; i < AJ_FEW; ++i) {
-      const float fi = __shfl_sync(0xffffffffu, f, i);
+      for (int j = 0; j < AJ_FEW; ++j) {
+        const int i = i0 + j;
+        const float fi = __shfl_sync(0xffffffffu, f, i);
+        const float* part = ar.acc + slot(i) * D + lane * 4;
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (i < n && in)
-          add_scaled(a[v], *reinterpret_cast<const float4*>(ar.acc + slot(i) * D + lane * 4 + v * 128),
-                     fi);
-    }
-    const int64_t row = (int64_t)j.b * ar.Hq + j.h + h;
-    const float r = l != 0.f ? 1.f / l : 0.f;
+        for (int v = 0; v < V; ++v)
+          if (i < n && in) add_scaled(a[v], *reinterpret_cast<const float4*>(part + v * 128), fi);
+      }
+    const float q = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v)
-      if (in) store_o(reinterpret_cast<T*>(ar.o) + row * D + lane * 4 + v * 128, a[v], r);
-    if (lane == 0 && ar.lse) ar.lse[row] = (base * ar.sl + log2f(l)) * 0.69314718055994531f;
+      if (in) store_o(reinterpret_cast<T*>(ar.o) + (row0 + g) * D + lane * 4 + v * 128, a[v], q);
+    if (lane == 0 && ar.lse) ar.lse[row0 + g] = (base * ar.sl + log2f(l)) * 0.69314718055994531f;
+    return;
   }
-  for (int x = blockIdx.x; x < many; x += gridDim.x) {
-    const int p = MAXC - 1 - x / (AT_G * (D / AJ_DC)), h = x / (D / AJ_DC) % AT_G;
-    const int d0 = x % (D / AJ_DC) * AJ_DC, col = tid % 16, row0 = tid / 16;
-    const Join j = s_list[p];
-    const int c = s_c[p], n = j.last - c + 1;
-    if (h >= j.heads) continue;
-    auto slot = [&](int i) { return (int64_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * AT_G + h; };
+  for (int item = x - c; item < heads * (D / AJ_DC); item += n - 1) {
+    const int g = item % heads, d0 = item / heads * AJ_DC, col = tid % 16, first = tid / 16;
+    auto slot = [&](int i) { return (int64_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * AT_G + g; };
     float m = -INFINITY, l = 0.f;
     for (int i = tid; i < n; i += AJ_NT) m = fmaxf(m, ar.ml[slot(i)].x);
 #pragma unroll
@@ -809,20 +794,22 @@ __global__ void __launch_bounds__(AJ_NT) k_attn_join(AttnArgs ar, int ctas) {
     if (lane == 0) s_red[warp][1] = l;
     __syncthreads();
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = row0; i < n; i += AJ_NT / 16)
+#pragma unroll 8
+    for (int i = first; i < n; i += AJ_NT / 16)
       add_scaled(a, *reinterpret_cast<const float4*>(ar.acc + slot(i) * D + d0 + col * 4), s_w[i]);
-    s_o[row0][col] = a;
+    s_o[first][col] = a;
     __syncthreads();
     if (tid < AJ_DC / 4) {
       a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
       for (int i = 0; i < AJ_NT / 16; ++i) add_scaled(a, s_o[i][tid], 1.f);
       l = 0.f;
+#pragma unroll
       for (int w = 0; w < NW; ++w) l += s_red[w][1];
-      const int64_t row = (int64_t)j.b * ar.Hq + j.h + h;
-      store_o(reinterpret_cast<T*>(ar.o) + row * D + d0 + tid * 4, a, l != 0.f ? 1.f / l : 0.f);
+      store_o(reinterpret_cast<T*>(ar.o) + (row0 + g) * D + d0 + tid * 4, a,
+              l != 0.f ? 1.f / l : 0.f);
       if (tid == 0 && d0 == 0 && ar.lse)
-        ar.lse[row] = (base * ar.sl + log2f(l)) * 0.69314718055994531f;
+        ar.lse[row0 + g] = (base * ar.sl + log2f(l)) * 0.69314718055994531f;
     }
   }
 }
@@ -853,16 +840,14 @@ gdn_status check_problem(const gdn_attn_problem* p) {
 // not depend on the device).
 struct Plan {
   int ctas;
-  size_t join, ml, acc, total;
+  size_t acc, total;
 };
 template <int D, typename T>
 Plan plan_of() {
   Plan pl;
   pl.ctas = AT_SMS * Cfg<D, T>::kCtas;
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-  pl.join = 0;
-  pl.ml = up(pl.ctas * sizeof(Join));
-  pl.acc = pl.ml + up((size_t)pl.ctas * 2 * AT_G * sizeof(float2));
+  pl.acc = up((size_t)pl.ctas * 2 * AT_G * sizeof(float2));
   pl.total = pl.acc + (size_t)pl.ctas * 2 * AT_G * D * sizeof(float);
   return pl;
 }
@@ -883,13 +868,12 @@ auto with_types(const gdn_attn_problem* p, F f) {
 template <int D, typename T>
 cudaError_t launch(AttnArgs ar, char* ws, cudaStream_t st) {
   const Plan pl = plan_of<D, T>();
-  ar.join = (Join*)(ws + pl.join);
-  ar.ml = (float2*)(ws + pl.ml);
+  ar.ml = (float2*)ws;
   ar.acc = (float*)(ws + pl.acc);
   const cudaError_t e = launch_behind(k_attn_decode<D, T>, dim3(pl.ctas), AT_NT,
                                       Smem<D, T>::kBytes, st, ar);
   if (e != cudaSuccess) return e;
-  return launch_behind(k_attn_join<D, T>, dim3(AJ_CTAS), AJ_NT, 0, st, ar, pl.ctas);
+  return launch_behind(k_attn_join<D, T>, dim3(pl.ctas), AJ_NT, 0, st, ar);
 }
 
 }  // namespace
