@@ -82,7 +82,7 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ uint4 ldg16(const void* p) {
   uint4 v;
-  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
@@ -568,7 +568,9 @@ __device__ void finish(const AttnArgs& ar, char* smem, float2 (*ml)[AT_G], int64
 // pieces (key head x group of AT_G query heads) in a row, each its CTA tiles behind AT_START; the
 // W units of all requests are divided over C CTAs, CTA c taking [W c / C, W (c + 1) / C).
 // Each warp finds its way by itself: a lane sums up a run of requests, one scan over the lanes.
-template <int D, typename T>
+// AHEAD: read past the first-level cache, for a caller that has not waited for the kernel before it
+// (the lengths were written before that one began).
+template <int D, typename T, bool AHEAD>
 struct Schedule {
   static constexpr int TK = Cfg<D, T>::kKeys * AT_W;  // keys per CTA tile
   const AttnArgs& ar;
@@ -576,7 +578,7 @@ struct Schedule {
   int C, run, per;        // CTAs with work, requests per run, pieces per request
 
   __device__ __forceinline__ int length(int64_t b) const {
-    const int32_t n = ar.len[b];
+    const int32_t n = AHEAD ? __ldcg(ar.len + b) : ar.len[b];
     const int64_t cap = ar.max_blocks * ar.P;
     return (int)(n < 0 ? 0 : n > cap ? cap : n);
   }
@@ -641,7 +643,7 @@ __global__ void __launch_bounds__(AT_NT, Cfg<D, T>::kCtas) k_attn_decode(AttnArg
   after_previous();
   before_next();
   const int tid = threadIdx.x, c = blockIdx.x;
-  const Schedule<D, T> sc(ar, gridDim.x);
+  const Schedule<D, T, false> sc(ar, gridDim.x);
   int bad = 0;
   if (c == 0)
     for (int64_t b = tid; b < ar.B; b += AT_NT) bad |= sc.length(b) != ar.len[b];
@@ -717,7 +719,7 @@ __global__ void __launch_bounds__(AJ_NT) k_attn_join(AttnArgs ar) {
   __shared__ float s_w[MAXC], s_red[NW][2];
   __shared__ float4 s_o[AJ_NT / 16][AJ_DC / 4];
   const int x = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const Schedule<D, T> sc(ar, gridDim.x);
+  const Schedule<D, T, true> sc(ar, gridDim.x);
   int64_t b = 0, r = 0;
   int c = 0, last = 0, h = 0;  // first and last CTA of the piece
   if (x < sc.C) {
@@ -822,7 +824,7 @@ gdn_status check_problem(const gdn_attn_problem* p) {
   if (!p) return GDN_ERR_INVALID_ARG;
   if (p->dtype != GDN_BF16 && p->dtype != GDN_FP32) return GDN_ERR_INVALID_ARG;
   if (p->B < 0 || p->Hq < 1 || p->Hk < 1 || p->Hq % p->Hk != 0 || p->pages < 0 ||
-      p->max_blocks < 0 || p->page_size < 1 || p->D < 1 || p->scale != p->scale)
+      p->max_blocks < 0 || p->page_size < 1 || p->D < 1 || !isfinite(p->scale))
     return GDN_ERR_INVALID_ARG;
   const int64_t unit = p->dtype == GDN_BF16 ? 8 : 4;  // elements in 16 bytes
   if (p->q_stride != 0 && (p->q_stride < p->Hq * p->D || p->q_stride % unit != 0))

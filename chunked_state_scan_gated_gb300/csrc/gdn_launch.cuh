@@ -30,7 +30,9 @@ cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t s
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+  if (e != cudaSuccess) cudaGetLastError();  // reported here: not left for the next call
+  return e;
 }
 
 }  // namespace gdn

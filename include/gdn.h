@@ -609,11 +609,12 @@ gdn_status gdn_qk_norm_rope_cache(const gdn_rope_problem* p, const void* q, cons
  *  - seq_len int32 [B]; a length outside [0, max_blocks page_size] is clamped, a used page
  *    outside [0, pages) has its tokens left out; both are recorded in `status`.
  *  - Workspace: gdn_attn_decode_workspace_size, 256-byte aligned: the pieces of requests whose
- *    cache is split over several CTAs.  Its size depends on p only through D and dtype.
+ *    cache is split over several CTAs.  Its size depends on p only through D and dtype.  Calls
+ *    that can run at the same time need workspaces of their own.
  * The split is chosen on the device from seq_len (the host reads nothing) and depends on the
  * lengths alone: deterministic.  Two launches.
  * Errors: null or misaligned pointer, sizes < 0, Hq % Hk != 0, q_stride < Hq D or no multiple
- * of 16 bytes: GDN_ERR_INVALID_ARG; D other than 64, 128 or 256, page_size no multiple of 16,
+ * of 16 bytes, a scale that is not finite: GDN_ERR_INVALID_ARG; D other than 64, 128 or 256, page_size no multiple of 16,
  * pages page_size or max_blocks page_size >= 2^31, B Hq >= 2^31: GDN_ERR_UNSUPPORTED.
  */
 typedef struct gdn_attn_problem {

@@ -158,7 +158,7 @@ def attn(lib, prob=None, ws=A, ws_bytes=1 << 40, status=A, **over):
 @pytest.mark.parametrize("kw,status", [
     ({"dtype": 2}, BAD), ({"B": -1}, BAD), ({"Hq": 0}, BAD), ({"Hk": 0}, BAD), ({"Hk": 3}, BAD),
     ({"pages": -1}, BAD), ({"max_blocks": -1}, BAD), ({"page_size": 0}, BAD), ({"D": 0}, BAD),
-    ({"scale": float("nan")}, BAD), ({"q_stride": 1016}, BAD), ({"q_stride": 1028}, BAD),
+    ({"scale": float("nan")}, BAD), ({"scale": float("inf")}, BAD), ({"q_stride": 1016}, BAD), ({"q_stride": 1028}, BAD),
     ({"D": 96}, UNSUP), ({"page_size": 24}, UNSUP), ({"pages": 1 << 27}, UNSUP),
     ({"max_blocks": 1 << 27}, UNSUP), ({"B": 1 << 28}, UNSUP),
 ])

@@ -128,6 +128,10 @@ ATTN = [  # lens, Hq, Hk, D, page, dtype
     ([0, 0, 0], 8, 2, 128, 16, BF), ([0], 8, 2, 256, 16, F32),
     (list(range(1, 200, 3)), 10, 2, 128, 16, BF),
     ([2] * 700, 8, 1, 64, 16, BF),
+    # parts joined: 11 and 24 by one warp per head, hundreds shared; many requests per lane
+    ([700], 8, 1, 256, 16, BF), ([1500], 8, 1, 256, 16, BF), ([1500], 8, 1, 256, 16, F32),
+    ([60011], 2, 1, 64, 64, BF), ([i % 7 for i in range(3000)], 2, 1, 64, 16, BF),
+    ([(i * 37) % 301 for i in range(1111)], 2, 1, 64, 16, F32),
 ]
 
 
@@ -240,6 +244,82 @@ def test_attention_graph_replay_and_streams():
         check_attn(q, kc, vc, table, lens, o, lse)
         for x in got:
             assert torch.equal(x[0], ref_other[0]) and torch.equal(x[1], ref_other[1])
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_attention_scores_that_rise_and_fall_slowly(dt):
+    """The running maximum creeps up by less than a factor 2^8 of weight from tile to tile, then
+    falls."""
+    q, kc, vc, table, lens = attn_inputs([2000], 2, 1, 64, 16, dt, seed=14)
+    ramp = 6 * torch.sin(torch.linspace(0, 3, 2000, device="cuda"))
+    ids = table[0, :125].long()
+    q.fill_(1.0)
+    kc[ids] = (ramp.view(125, 16, 1, 1) + 0.1 * torch.randn(125, 16, 1, 64, device="cuda")).to(dt)
+    o, lse = gdn.gdn_attn_decode(q, kc, vc, table, lens)
+    check_attn(q, kc, vc, table, lens, o, lse)
+
+
+def test_attention_without_lse_and_into_given_outputs():
+    inp = attn_inputs([300, 0, 5], 8, 2, 128, 16, BF, seed=15)
+    o, lse = gdn.gdn_attn_decode(*inp)
+    mine, ws = torch.empty_like(o), torch.empty(8 << 20, dtype=torch.uint8, device="cuda")
+    got = gdn.gdn_attn_decode(*inp, o=mine, want_lse=False, ws=ws)
+    assert got[0] is mine and got[1] is None and torch.equal(mine, o)
+    with pytest.raises(gdn.GDNError):
+        gdn.gdn_attn_decode(*inp, ws=ws[:512])
+
+
+def test_binding_refuses_wrong_types_and_shapes():
+    q, kc, vc, table, lens = attn_inputs([30, 5], 8, 2, 128, 16, BF, seed=16)
+    for bad in ((q.float(), kc, vc, table, lens), (q, kc, vc[:-1], table, lens),
+                (q, kc, vc, table.long(), lens), (q, kc, vc, table, lens[:1]),
+                (q, kc, vc, table.t(), lens), (q.transpose(0, 1), kc, vc, table, lens),
+                (q, kc.transpose(1, 2), vc, table, lens)):
+        with pytest.raises(ValueError):
+            gdn.gdn_attn_decode(*bad)
+    d, state = step_inputs(2, 1, 2, 128, 128, BF, 4)
+    for kw in (dict(slots=torch.zeros(2, dtype=torch.int64, device="cuda")),
+               dict(slots=i32([0])), dict(state=state.bfloat16()), dict(state=state[:, :1])):
+        with pytest.raises(ValueError):
+            gdn.gdn_step(**(d | dict(state=state) | kw))
+    with pytest.raises(gdn.GDNError):
+        gdn.gdn_step(**d, state=state[:1])  # no slots, fewer states than rows
+
+
+def test_calls_captured_behind_copies_memsets_and_other_streams():
+    """Each call as the first kernel behind a memset, a device copy and a join of two streams, in
+    a captured graph: they are launched behind what comes before them, whatever that is."""
+    q, kc, vc, table, lens = attn_inputs([500, 70], 8, 2, 128, 16, BF, seed=17)
+    d, state = step_inputs(2, 2, 4, 128, 128, BF, 2, seed=18)
+    rq, rk, _, wq, wk, f, _ = rope_inputs(300, 4, 2, 128, 64, BF, seed=19)
+    dyq, dyk = torch.randn(300, 4, 128, device="cuda").to(BF), torch.ones(300, 2, 128, device="cuda").to(BF)
+    want_o = gdn.gdn_attn_decode(q, kc, vc, table, lens)[0]
+    keep = state.clone()
+    want_s = gdn.gdn_step(**d, state=keep)
+    want_g = gdn.gdn_qk_norm_rope_bwd(rq, rk, wq, wk, f, None, dyq, dyk)
+    lens2, state2, dyq2 = torch.empty_like(lens), torch.empty_like(state), torch.empty_like(dyq)
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        lens2.zero_()
+        empty = gdn.gdn_attn_decode(q, kc, vc, table, lens2)[0]
+        lens2.copy_(lens)
+        got_o = gdn.gdn_attn_decode(q, kc, vc, table, lens2)[0]
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            state2.copy_(state)
+            dyq2.copy_(dyq)
+        busy = torch.ones(1000, device="cuda") + 1
+        main.wait_stream(side)
+        got_s = gdn.gdn_step(**d, state=state2)
+        got_g = gdn.gdn_qk_norm_rope_bwd(rq, rk, wq, wk, f, None, dyq2, dyk)
+    for _ in range(3):
+        g.replay()
+        torch.cuda.synchronize()
+        assert (empty == 0).all() and torch.equal(got_o, want_o) and torch.equal(got_s, want_s)
+        assert torch.equal(state2, keep) and all(torch.equal(a, b) for a, b in zip(got_g, want_g))
+        assert (busy == 2).all()
 
 
 def test_attention_empty_batch():
@@ -394,11 +474,18 @@ def test_rope_positions_of_batch_rows_and_contiguous_inputs():
 
 
 def test_rope_zero_rows_and_one_kind_of_heads():
-    """A zero row normalises to zero (and its gradient stays finite); Hk = 0 and N = 0."""
+    """A zero row normalises to zero (and its gradient stays finite); Hk = 0, Hq = 0 and N = 0."""
     w, f = torch.ones(64, device="cuda"), torch.ones(8, device="cuda")
     q, none = torch.zeros(3, 2, 64, device="cuda"), torch.zeros(3, 0, 64, device="cuda")
     y, e = gdn.gdn_qk_norm_rope_fwd(q, none, w, w, f)
     assert (y == 0).all() and e.shape == (3, 0, 64)
+    x = torch.randn(700, 5, 64, device="cuda")
+    a = gdn.gdn_qk_norm_rope_fwd(x, x[:, :0], w, w, f)[0]
+    b = gdn.gdn_qk_norm_rope_fwd(x[:, :0], x, w, w, f)[1]
+    assert torch.equal(a, b)
+    ga = gdn.gdn_qk_norm_rope_bwd(x, x[:, :0], w, w, f, None, x, x[:, :0].contiguous())
+    gb = gdn.gdn_qk_norm_rope_bwd(x[:, :0], x, w, w, f, None, x[:, :0].contiguous(), x)
+    assert torch.equal(ga[0], gb[1]) and torch.equal(ga[2], gb[3])
     dq, _, dw, _ = gdn.gdn_qk_norm_rope_bwd(q, none, w, w, f, None, torch.ones_like(q), none)
     check_grads("q", dq, dw, q, w, np.arange(3), f, False, torch.ones_like(q), F32)
     z = q[:0]
@@ -532,6 +619,18 @@ def test_step_padded_bad_and_repeated_slots():
     assert torch.equal(o, good[0]) and torch.equal(state, good[1])
     assert gdn.gdn_step(**{k: (x[:0] if x.dim() > 1 else x) for k, x in d.items()},
                         state=state, slots=i32([])).shape == (0, 1, 4, 128)
+
+
+def test_step_offsets_past_32_bits():
+    """States behind 2^31 elements of the pool."""
+    d, small = step_inputs(3, 2, 32, 128, 128, BF, 3, seed=22)
+    pool = torch.empty((1 << 32) // (32 * 128 * 128) + 3, 32, 128, 128, device="cuda")
+    at = torch.tensor([pool.shape[0] - 1, 0, pool.shape[0] - 2], device="cuda")
+    pool[at] = small
+    o = gdn.gdn_step(**d, state=pool, slots=at.int())
+    assert torch.equal(o, gdn.gdn_step(**d, state=small)) and torch.equal(pool[at], small)
+    del pool
+    torch.cuda.empty_cache()
 
 
 @pytest.mark.parametrize("dt,tol", [(BF, 1e-2), (F32, 1e-5)])
