@@ -909,6 +909,8 @@ def _rows(name, t, dev, dtype, shape):
     if t.is_contiguous():
         return t.data_ptr(), 0
     st = t.stride()
+    if len(st) == 3 and st[2] == 1 and st[1] == sh[2] and sh[0] > 1:
+        return t.data_ptr(), st[0]
     heads, D = sh[-2], sh[-1]
     ok = (st[-1] == 1 or D == 1) and (st[-2] == D or heads == 1)
     step, span = 0, 1

@@ -7,17 +7,19 @@
 // The angle is formed in revolutions: t * (inv_freq / 2 pi) as an exact two-term product, its
 // integer part dropped, so positions past 2^20 lose nothing (angle()).
 //
-// Bound by HBM (2 row accesses forward, 3 backward).  A row is held 8 elements per lane (16
-// bytes of bf16) by LPR = 8, 16 or 32 lanes, so a warp holds 32 / LPR heads at a time and takes U
-// such sets together (independent chains of shuffles: one at a time was bound by their latency,
-// 154 against 100 us for 32768 tokens of 18 heads of 256).  All these groups of all tokens, in order, are divided evenly over one wave of
-// warps, from a decode step's few (each warp one group) to a training batch: no tail.  A warp
-// streams its groups through a ring of its own in shared memory (16-byte asynchronous copies, RO_RING bytes in
-// flight) with warp barriers only; a rotated element's partner in the other half is read from
-// the ring.  The token's R/2 angles are computed once and folded with the weights:
+// Bound by HBM (2 row accesses forward, 3 backward).  A row is held 8 elements per lane (16 bytes
+// of bf16) by LPR = 8, 16 or 32 lanes, so a warp holds 32 / LPR heads at a time; a group is U such
+// sets, whose chains of shuffles are independent (32768 tokens of 18 heads of 256: 96 us with U =
+// 2, 107 with 1).  The groups of all tokens are divided evenly over one wave of warps, from a decode
+// step's few (each warp one group) to a training batch: no tail.  A warp streams its groups
+// through a ring of its own in shared memory (16-byte asynchronous copies) with warp barriers
+// only; a rotated element's partner in the other half is read from the ring.  The token's R/2
+// angles are computed once and folded with the weights:
 //   y = r (x (w c) + xp (w_p s)),  xp the partner elements, s with the sign of the pair's side
-// and the arithmetic is packed two fp32 numbers at a time: 2 (3) row accesses leave about
-// 44 issue slots of an SM's scheduler per 512-byte row.
+// and the arithmetic is packed two fp32 numbers at a time (237 instructions per row without
+// either, 113 now).  Measured: forward of those 32768 tokens 96 us (6.3 TB/s), backward of 16001
+// tokens of 40 heads of 128 85 us (5.8 TB/s).  Two CTAs of 8 warps per SM with 4 KB in flight per
+// warp are the best of 2 to 4 CTAs and 4 to 16 KB (3 CTAs: 108 us; 8 KB: 100 us).
 #include <cuda_bf16.h>
 #include <math.h>
 #include <string.h>
@@ -37,7 +39,7 @@ constexpr int RO_NT = 256;     // 8 warps
 constexpr int RO_W = RO_NT / 32;
 constexpr int RO_CTAS = 152 * 2;  // CTAs at most: one wave of 2 per SM of a 152-SM GPU
 constexpr int RO_MAXD = 256;   // 8 elements per lane
-constexpr int RO_RING = 8192;  // bytes of a warp's ring
+constexpr int RO_RING = 4096;  // bytes of a warp's ring
 constexpr int RO_FU = 2, RO_GU = 1;  // sets of heads per group, forward and backward
 constexpr int RO_SMEM = RO_W * (RO_RING + (RO_MAXD + 16) * 4);  // rings, cos and sin
 
@@ -234,8 +236,8 @@ __device__ __forceinline__ int other_lane(const RopeArgs& ar, int e) {
 }
 
 // A warp's share of the groups: of the N tokens, as many whole rounds of one token per warp as
-// there are (neighbouring warps read neighbouring tokens: 98 us against 109 for each warp its own
-// stretch of 32768 tokens), then an even part of the groups of the tokens that are left, from
+// there are (neighbouring warps read neighbouring tokens: a stretch of its own for each warp
+// took a tenth longer), then an even part of the groups of the tokens that are left, from
 // group tail_g of token tail_n.  Tokens fit 31 bits and groups 32 (checked on the host).
 struct Share {
   int warps, full, tail_n, tail_g, groups;  // full: tokens in whole rounds
@@ -351,6 +353,7 @@ __global__ void __launch_bounds__(RO_NT, 2) k_qk_norm_rope_fwd(RopeArgs ar) {
   before_next();
   constexpr int U = RO_FU, RPL = 32 / LPR, SE = 32 * 8;
   constexpr int NST = RO_RING / (U * SE * (int)sizeof(T));
+  static_assert(NST >= 2, "the stage being read is not the one being filled");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = (lane & (LPR - 1)) * 8;
   T* ring = reinterpret_cast<T*>(smem + warp * RO_RING);
   float* cs = reinterpret_cast<float*>(smem + RO_W * RO_RING) + warp * RO_CS;
@@ -465,6 +468,7 @@ __global__ void __launch_bounds__(RO_NT, 2) k_qk_norm_rope_bwd(RopeArgs ar) {
   extern __shared__ __align__(16) char smem[];
   constexpr int U = RO_GU, RPL = 32 / LPR, SE = 32 * 8;
   constexpr int NST = RO_RING / (2 * U * SE * (int)sizeof(T));
+  static_assert(NST >= 2, "the stage being read is not the one being filled");
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / LPR;
   const int e = (lane & (LPR - 1)) * 8;
   T* ring = reinterpret_cast<T*>(smem + warp * RO_RING);
@@ -684,12 +688,9 @@ int64_t ctas_of(const RopeArgs& ar) {
   return n < RO_CTAS ? n : RO_CTAS;
 }
 
-// The kernels' dynamic shared memory is above the default limit: raised per kernel and call (a
-// host-side attribute of the current device's function, set to the same value every time).
+static_assert(RO_SMEM <= 48 * 1024, "above this a kernel has to ask for its shared memory");
 template <typename K>
 cudaError_t launch(K kernel, const RopeArgs& ar, cudaStream_t st) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RO_SMEM);
-  if (e != cudaSuccess) return e;
   return launch_behind(kernel, dim3((unsigned)ctas_of(ar)), RO_NT, RO_SMEM, st, ar);
 }
 
