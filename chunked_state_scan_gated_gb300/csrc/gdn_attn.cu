@@ -6,9 +6,11 @@
 // Bound by HBM: every K and V row is read once.  A piece of work is (request, key head, range
 // of tokens); the query heads of a key head are the 8 columns of the products
 //   S^T [16 keys x 8 heads] = K [16 x D] Q^T,   O^T [D x 8] += V^T [D x 16 keys] P^T
-// so a group of 8 query heads fills mma.sync's tile and K, V need no transposition: both are
-// the products' A operand, whose fragments are loaded from global memory straight into
-// registers, 16 bytes per lane.  That works because the contraction index of the first
+// so a group of 8 query heads fills mma.sync's tile (more than 8 per key head go 16 to a pass over the
+// cache, two products per fragment: 131001 tokens with 16 query heads to each of 8 key heads of
+// 128: 92 us against 158 in two passes) and K, V need no transposition: both are the products' A
+// operand, whose fragments are loaded from global memory straight into registers, 16 bytes per
+// lane.  That works because the contraction index of the first
 // product (the head's elements) and the output rows of the second may be permuted freely:
 //   K: lane (g, t) = (lane / 4, lane % 4) loads 16-byte chunk t + 4c of key rows g and g + 8,
 //      and the 4 (2) words of a chunk serve 2 products, Q's fragment being the same chunk;
@@ -41,37 +43,47 @@ namespace {
 
 constexpr int AT_W = 4;            // warps per CTA
 constexpr int AT_NT = 32 * AT_W;
-constexpr int AT_G = 8;            // query heads per piece
+constexpr int AT_G = 8;            // query heads per product
 constexpr int AT_SMS = 152;
 constexpr float AT_LAZY = 8.f;     // log2 units
 // What a piece costs beside its tiles, in units (its first loads and its end): without it a
 // CTA with many short requests lags (61 ragged requests 128 against 102 us; 2 to 5 units: the same).
 constexpr int AT_START = 1;
 
-// Keys per warp tile and CTAs per SM: the K and V tiles and the accumulators of D x 8 fill
-// most of a CTA's share of the registers.
+// Keys per warp tile, CTAs per SM and parts, for NG groups of AT_G query heads per piece: the K and V
+// tiles and the accumulators of D x 8 NG fill most of a CTA's share of the registers.
 // kParts > 1: the two tiles do not fit; they go by that many parts of D.
-template <int D, typename T> struct Cfg;
-template <> struct Cfg<64, __nv_bfloat16> { static constexpr int kKeys = 32, kCtas = 4, kParts = 1; };
-template <> struct Cfg<128, __nv_bfloat16> { static constexpr int kKeys = 16, kCtas = 3, kParts = 1; };
-template <> struct Cfg<256, __nv_bfloat16> { static constexpr int kKeys = 16, kCtas = 2, kParts = 1; };
-template <> struct Cfg<64, float> { static constexpr int kKeys = 16, kCtas = 3, kParts = 1; };
-template <> struct Cfg<128, float> { static constexpr int kKeys = 16, kCtas = 2, kParts = 1; };
-template <> struct Cfg<256, float> { static constexpr int kKeys = 16, kCtas = 2, kParts = 2; };
+template <int KEYS, int CTAS, int PARTS>
+struct Fit {
+  static constexpr int kKeys = KEYS, kCtas = CTAS, kParts = PARTS;
+};
+template <int D, typename T, int NG> struct Cfg;
+template <> struct Cfg<64, __nv_bfloat16, 1> : Fit<32, 4, 1> {};
+template <> struct Cfg<128, __nv_bfloat16, 1> : Fit<16, 3, 1> {};
+template <> struct Cfg<256, __nv_bfloat16, 1> : Fit<16, 2, 1> {};
+template <> struct Cfg<64, float, 1> : Fit<16, 3, 1> {};
+template <> struct Cfg<128, float, 1> : Fit<16, 2, 1> {};
+template <> struct Cfg<256, float, 1> : Fit<16, 2, 2> {};
+template <> struct Cfg<64, __nv_bfloat16, 2> : Fit<32, 3, 1> {};
+template <> struct Cfg<128, __nv_bfloat16, 2> : Fit<16, 2, 1> {};
+template <> struct Cfg<256, __nv_bfloat16, 2> : Fit<16, 2, 2> {};
+template <> struct Cfg<64, float, 2> : Fit<16, 2, 1> {};
+template <> struct Cfg<128, float, 2> : Fit<16, 2, 2> {};
+template <> struct Cfg<256, float, 2> : Fit<16, 2, 4> {};
 
 // Parts of pieces in the workspace: slot 2c of CTA c is the piece that began before it, slot
 // 2c + 1 the one that goes on behind it.
 struct AttnArgs {
   int64_t B, Hq, Hk, pages, max_blocks, qs;
-  int P, G, HG;   // tokens per page, query heads per key head, pieces of AT_G of them
+  int P, G, HG;   // tokens per page, query heads per key head, pieces of them
   float sl;       // scale log2(e)
   float lazy;     // AT_LAZY in units of the unscaled scores
   const void *q, *kc, *vc;
   const int32_t *table, *len;
   void* o;
   float* lse;
-  float2* ml;     // [CTAs][2][AT_G] reference score (unscaled) and sum
-  float* acc;     // [CTAs][2][AT_G][D]
+  float2* ml;     // [CTAs][2][AT_G NG] reference score (unscaled) and sum
+  float* acc;     // [CTAs][2][AT_G NG][D]
   int32_t* status;
 };
 
@@ -141,21 +153,21 @@ __device__ __forceinline__ void mma_split(float (&c)[4], const uint32_t (&ah)[4]
   mma_tf32(c, ah, bh[0], bh[1]);
 }
 
-// Q of the piece in shared memory: AT_G rows (zeros past the piece's heads); rows are 64 bytes
+// Q of the piece in shared memory: AT_G NG rows (zeros past the piece's heads); rows are 64 bytes
 // longer than D elements, so that the 8 lanes of a 16-byte read phase (2 rows x 4 chunks)
 // fall on different banks.  fp32: hi rows, then lo rows.
-template <int D, typename T> struct Smem {
+template <int D, typename T, int NG> struct Smem {
   static constexpr int kRow = D * (int)sizeof(T) + 64;  // bytes
-  static constexpr int kQ = AT_G * kRow * (sizeof(T) == 4 ? 2 : 1);
+  static constexpr int kQ = AT_G * NG * kRow * (sizeof(T) == 4 ? 2 : 1);
   static constexpr int kORow = D + 2;                   // floats
   static constexpr int kO = AT_W * AT_G * kORow * 4;
   static constexpr int kBytes = kQ > kO ? kQ : kO;      // Q and O take turns
 };
 
 // What a warp keeps of its piece.
-template <int D> struct Acc {
-  float o[D / 16][4];  // O^T tiles
-  float m[2], l[2];    // of heads 2t, 2t + 1: reference score (unscaled), this lane's part of the sum
+template <int D, int NG> struct Acc {
+  float o[NG][D / 16][4];      // O^T tiles
+  float m[NG][2], l[NG][2];    // of heads 2t, 2t + 1: reference score (unscaled), this lane's part of the sum
 };
 
 // NK blocks of 16 keys by DP elements.
@@ -185,31 +197,39 @@ struct Block {
 
 // s += the scores of NK blocks over one part of D, for heads 2t, 2t + 1 of the lane's rows g, g + 8;
 // qs points at the part in Q's rows.
-template <int D, int DP, int NK>
+template <int D, int DP, int NK, int NG>
 __device__ __forceinline__ void scores(const Tile<DP, __nv_bfloat16, NK>& k, const char* qs,
-                                       float (&s)[NK][4]) {
-  constexpr int kRow = Smem<D, __nv_bfloat16>::kRow;
+                                       float (&s)[NG][NK][4]) {
+  constexpr int kRow = Smem<D, __nv_bfloat16, NG>::kRow;
   const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
 #pragma unroll
-  for (int c = 0; c < DP / 32; ++c) {
-    const uint4 b = *reinterpret_cast<const uint4*>(qs + g * kRow + (t + 4 * c) * 16);
+  for (int c = 0; c < DP / 32; ++c)
 #pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      const uint4 a0 = k.r[i][(c & 1) * 2][c >> 1], a1 = k.r[i][(c & 1) * 2 + 1][c >> 1];
-      mma_bf16(s[i], a0.x, a1.x, a0.y, a1.y, b.x, b.y);
-      mma_bf16(s[i], a0.z, a1.z, a0.w, a1.w, b.z, b.w);
+    for (int q = 0; q < NG; ++q) {
+      const uint4 b =
+          *reinterpret_cast<const uint4*>(qs + (q * AT_G + g) * kRow + (t + 4 * c) * 16);
+#pragma unroll
+      for (int i = 0; i < NK; ++i) {
+        const uint4 a0 = k.r[i][(c & 1) * 2][c >> 1], a1 = k.r[i][(c & 1) * 2 + 1][c >> 1];
+        mma_bf16(s[q][i], a0.x, a1.x, a0.y, a1.y, b.x, b.y);
+        mma_bf16(s[q][i], a0.z, a1.z, a0.w, a1.w, b.z, b.w);
+      }
     }
-  }
 }
-template <bool SAFE, int D, int DP, int NK>
+template <bool SAFE, int D, int DP, int NK, int NG>
 __device__ __forceinline__ void scores_split(const Tile<DP, float, NK>& k, const char* qs,
-                                             float (&s)[NK][4]) {
-  constexpr int kRow = Smem<D, float>::kRow;
+                                             float (&s)[NG][NK][4]) {
+  constexpr int kRow = Smem<D, float, NG>::kRow;
   const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
 #pragma unroll
   for (int c = 0; c < DP / 16; ++c) {
-    const uint4 bh = *reinterpret_cast<const uint4*>(qs + g * kRow + (t + 4 * c) * 16);
-    const uint4 bl = *reinterpret_cast<const uint4*>(qs + (AT_G + g) * kRow + (t + 4 * c) * 16);
+    uint4 bh[NG], bl[NG];
+#pragma unroll
+    for (int q = 0; q < NG; ++q) {
+      const char* at = qs + (q * AT_G + g) * kRow + (t + 4 * c) * 16;
+      bh[q] = *reinterpret_cast<const uint4*>(at);
+      bl[q] = *reinterpret_cast<const uint4*>(at + AT_G * NG * kRow);
+    }
 #pragma unroll
     for (int i = 0; i < NK; ++i) {
       const uint4 a0 = k.r[i][(c & 1) * 2][c >> 1], a1 = k.r[i][(c & 1) * 2 + 1][c >> 1];
@@ -220,59 +240,71 @@ __device__ __forceinline__ void scores_split(const Tile<DP, float, NK>& k, const
         split_tf32<SAFE>(word(a1, 2 * u), &ah[1], &al[1]);
         split_tf32<SAFE>(word(a0, 2 * u + 1), &ah[2], &al[2]);
         split_tf32<SAFE>(word(a1, 2 * u + 1), &ah[3], &al[3]);
-        const uint32_t h[2] = {word(bh, 2 * u), word(bh, 2 * u + 1)};
-        const uint32_t l[2] = {word(bl, 2 * u), word(bl, 2 * u + 1)};
-        mma_split(s[i], ah, al, h, l);
+#pragma unroll
+        for (int q = 0; q < NG; ++q) {
+          const uint32_t h[2] = {word(bh[q], 2 * u), word(bh[q], 2 * u + 1)};
+          const uint32_t l[2] = {word(bl[q], 2 * u), word(bl[q], 2 * u + 1)};
+          mma_split(s[q][i], ah, al, h, l);
+        }
       }
     }
   }
 }
 
-template <int D, int DP, int NK>
+template <int D, int DP, int NK, int NG>
 __device__ __forceinline__ void scores(const Tile<DP, float, NK>& k, const char* qs,
-                                       float (&s)[NK][4]) {
+                                       float (&s)[NG][NK][4]) {
   if (plain(k)) scores_split<false, D>(k, qs, s);
   else scores_split<true, D>(k, qs, s);
 }
 
 // O^T += V^T P^T over part `part` of D; p holds the weights in the scores' layout.
-template <int D, int DP, int NK>
+template <int D, int DP, int NK, int NG>
 __device__ __forceinline__ void weigh(const Tile<DP, __nv_bfloat16, NK>& v,
-                                      const float (&p)[NK][4], Acc<D>& a, int part) {
+                                      const float (&p)[NG][NK][4], Acc<D, NG>& a, int part) {
 #pragma unroll
   for (int i = 0; i < NK; ++i) {
-    // the weights' one rounding: half a bf16 step each, of random sign over the keys
-    const __nv_bfloat162 p0 = __floats2bfloat162_rn(p[i][0], p[i][1]);
-    const __nv_bfloat162 p1 = __floats2bfloat162_rn(p[i][2], p[i][3]);
-    const uint32_t b0 = transpose8x8(*reinterpret_cast<const uint32_t*>(&p0));
-    const uint32_t b1 = transpose8x8(*reinterpret_cast<const uint32_t*>(&p1));
+    uint32_t b0[NG], b1[NG];
+#pragma unroll
+    for (int q = 0; q < NG; ++q) {
+      // the weights' one rounding: half a bf16 step each, of random sign over the keys
+      const __nv_bfloat162 p0 = __floats2bfloat162_rn(p[q][i][0], p[q][i][1]);
+      const __nv_bfloat162 p1 = __floats2bfloat162_rn(p[q][i][2], p[q][i][3]);
+      b0[q] = transpose8x8(*reinterpret_cast<const uint32_t*>(&p0));
+      b1[q] = transpose8x8(*reinterpret_cast<const uint32_t*>(&p1));
+    }
 #pragma unroll
     for (int c = 0; c < DP / 64; ++c)
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         const uint32_t x0 = word(v.r[i][0][c], w), x1 = word(v.r[i][1][c], w);
         const uint32_t x2 = word(v.r[i][2][c], w), x3 = word(v.r[i][3][c], w);
-        mma_bf16(a.o[part * (DP / 16) + c * 4 + w], __byte_perm(x0, x1, 0x5410), __byte_perm(x0, x1, 0x7632),
-                 __byte_perm(x2, x3, 0x5410), __byte_perm(x2, x3, 0x7632), b0, b1);
+        const uint32_t a0 = __byte_perm(x0, x1, 0x5410), a1 = __byte_perm(x0, x1, 0x7632);
+        const uint32_t a2 = __byte_perm(x2, x3, 0x5410), a3 = __byte_perm(x2, x3, 0x7632);
+#pragma unroll
+        for (int q = 0; q < NG; ++q)
+          mma_bf16(a.o[q][part * (DP / 16) + c * 4 + w], a0, a1, a2, a3, b0[q], b1[q]);
       }
   }
 }
-template <bool SAFE, int D, int DP, int NK>
-__device__ __forceinline__ void weigh_split(const Tile<DP, float, NK>& v, const float (&p)[NK][4],
-                                            Acc<D>& a, int part) {
+template <bool SAFE, int D, int DP, int NK, int NG>
+__device__ __forceinline__ void weigh_split(const Tile<DP, float, NK>& v,
+                                            const float (&p)[NG][NK][4], Acc<D, NG>& a, int part) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int i = 0; i < NK; ++i)
 #pragma unroll
     for (int u = 0; u < 2; ++u) {  // keys 8u .. 8u + 7
-      uint32_t bh[2], bl[2];
+      uint32_t bh[NG][2], bl[NG][2];
 #pragma unroll
-      for (int z = 0; z < 2; ++z) {  // P[key 8u + t + 4z][head g] from lane (t + 4z, g / 2)
-        const int src = (t + 4 * z) * 4 + (g >> 1);
-        const float e = __shfl_sync(0xffffffffu, p[i][2 * u], src);
-        const float f = __shfl_sync(0xffffffffu, p[i][2 * u + 1], src);
-        split_tf32<true>(__float_as_uint(g & 1 ? f : e), &bh[z], &bl[z]);
-      }
+      for (int q = 0; q < NG; ++q)
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {  // P[key 8u + t + 4z][head g] from lane (t + 4z, g / 2)
+          const int src = (t + 4 * z) * 4 + (g >> 1);
+          const float e = __shfl_sync(0xffffffffu, p[q][i][2 * u], src);
+          const float f = __shfl_sync(0xffffffffu, p[q][i][2 * u + 1], src);
+          split_tf32<true>(__float_as_uint(g & 1 ? f : e), &bh[q][z], &bl[q][z]);
+        }
 #pragma unroll
       for (int c = 0; c < DP / 32; ++c)
 #pragma unroll
@@ -282,14 +314,15 @@ __device__ __forceinline__ void weigh_split(const Tile<DP, float, NK>& v, const 
           for (int z = 0; z < 4; ++z)
             split_tf32<SAFE>(word(v.r[i][2 * u + (z >> 1)][c], 2 * w + (z & 1)), &ah[z],
                              &al[z]);
-          mma_split(a.o[part * (DP / 16) + c * 2 + w], ah, al, bh, bl);
+#pragma unroll
+          for (int q = 0; q < NG; ++q)
+            mma_split(a.o[q][part * (DP / 16) + c * 2 + w], ah, al, bh[q], bl[q]);
         }
     }
 }
-
-template <int D, int DP, int NK>
-__device__ __forceinline__ void weigh(const Tile<DP, float, NK>& v, const float (&p)[NK][4],
-                                      Acc<D>& a, int part) {
+template <int D, int DP, int NK, int NG>
+__device__ __forceinline__ void weigh(const Tile<DP, float, NK>& v, const float (&p)[NG][NK][4],
+                                      Acc<D, NG>& a, int part) {
   if (plain(v)) weigh_split<false>(v, p, a, part);
   else weigh_split<true>(v, p, a, part);
 }
@@ -344,17 +377,17 @@ __device__ __forceinline__ void load_v(Tile<DP, T, NK>& v, const T* base, const 
 }
 
 // Tokens [0, n) of request b, units [t0, t1) of CTA tiles.
-template <int D, typename T>
+template <int D, typename T, int NG>
 __device__ void piece(const AttnArgs& ar, char* smem, int64_t b, int n, int hk, int hg, int t0,
-                      int t1, Acc<D>& a, int* bad) {
-  constexpr int KT = Cfg<D, T>::kKeys, NK = KT / 16, EL = 16 / (int)sizeof(T);
-  constexpr int kRow = Smem<D, T>::kRow;
+                      int t1, Acc<D, NG>& a, int* bad) {
+  constexpr int GP = AT_G * NG, KT = Cfg<D, T, NG>::kKeys, NK = KT / 16, EL = 16 / (int)sizeof(T);
+  constexpr int kRow = Smem<D, T, NG>::kRow;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2;
-  const int heads = min(AT_G, ar.G - hg * AT_G);
+  const int heads = min(GP, ar.G - hg * GP);
   // Q (the barrier in front: other warps may still read what was there)
   __syncthreads();
-  const T* q = reinterpret_cast<const T*>(ar.q) + b * ar.qs + ((int64_t)hk * ar.G + hg * AT_G) * D;
-  for (int i = threadIdx.x; i < AT_G * D / EL; i += AT_NT) {
+  const T* q = reinterpret_cast<const T*>(ar.q) + b * ar.qs + ((int64_t)hk * ar.G + hg * GP) * D;
+  for (int i = threadIdx.x; i < GP * D / EL; i += AT_NT) {
     const int h = i / (D / EL), c = i % (D / EL);
     uint4 x = make_uint4(0, 0, 0, 0);
     if (h < heads) x = *reinterpret_cast<const uint4*>(q + (int64_t)h * D + c * EL);
@@ -366,17 +399,20 @@ __device__ void piece(const AttnArgs& ar, char* smem, int64_t b, int n, int hk, 
       split_tf32<true>(x.z, &hi.z, &lo.z);
       split_tf32<true>(x.w, &hi.w, &lo.w);
       *reinterpret_cast<uint4*>(dst) = hi;
-      *reinterpret_cast<uint4*>(dst + AT_G * kRow) = lo;
+      *reinterpret_cast<uint4*>(dst + GP * kRow) = lo;
     } else {
       *reinterpret_cast<uint4*>(dst) = x;
     }
   }
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i) a.o[i][0] = a.o[i][1] = a.o[i][2] = a.o[i][3] = 0.f;
-  a.m[0] = a.m[1] = -INFINITY;
-  a.l[0] = a.l[1] = 0.f;
-
-  constexpr int kParts = Cfg<D, T>::kParts, DP = D / kParts;
+  for (int q = 0; q < NG; ++q) {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+      a.o[q][i][0] = a.o[q][i][1] = a.o[q][i][2] = a.o[q][i][3] = 0.f;
+    a.m[q][0] = a.m[q][1] = -INFINITY;
+    a.l[q][0] = a.l[q][1] = 0.f;
+  }
+  constexpr int kParts = Cfg<D, T, NG>::kParts, DP = D / kParts;
   const int64_t row = ar.Hk * D;  // elements between a page's rows
   const T* kc = reinterpret_cast<const T*>(ar.kc) + (int64_t)hk * D;
   const T* vc = reinterpret_cast<const T*>(ar.vc) + (int64_t)hk * D;
@@ -436,9 +472,9 @@ __device__ void piece(const AttnArgs& ar, char* smem, int64_t b, int n, int hk, 
     Block nxt[NK];
     const bool nfull = place(nxt);
     look_up();
-    float s[NK][4] = {};
+    float s[NG][NK][4] = {};
     if constexpr (kParts == 1) {
-      scores<D, DP, NK>(k, smem, s);
+      scores<D>(k, smem, s);
       load_k(k, kc, nxt, row, nfull);
     } else {
 #pragma unroll
@@ -446,51 +482,65 @@ __device__ void piece(const AttnArgs& ar, char* smem, int64_t b, int n, int hk, 
         Tile<DP, T, NK>&x = z & 1 ? v : k, &y = z & 1 ? k : v;
         if (z + 1 < kParts) load_k(y, kc + (z + 1) * DP, cur, row, full);
         else load_v(y, vc, cur, row, full);
-        scores<D, DP, NK>(x, smem + z * DP * sizeof(T), s);
+        scores<D>(x, smem + z * DP * sizeof(T), s);
       }
     }
     if (!full)
 #pragma unroll
+      for (int q = 0; q < NG; ++q)
+#pragma unroll
+        for (int i = 0; i < NK; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (g + 8 * (j >> 1) >= cur[i].n) s[q][i][j] = -INFINITY;
+    float mx[NG][2];
+    bool up = false;
+#pragma unroll
+    for (int q = 0; q < NG; ++q) {
+      mx[q][0] = mx[q][1] = -INFINITY;
+#pragma unroll
       for (int i = 0; i < NK; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (g + 8 * (j >> 1) >= cur[i].n) s[i][j] = -INFINITY;
-    float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-    for (int i = 0; i < NK; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) mx[j & 1] = fmaxf(mx[j & 1], s[i][j]);
+        for (int j = 0; j < 4; ++j) mx[q][j & 1] = fmaxf(mx[q][j & 1], s[q][i][j]);
+      up = up || mx[q][0] > a.m[q][0] + ar.lazy || mx[q][1] > a.m[q][1] + ar.lazy;
+    }
     // The reference value m of a head follows the maximum only when a score is above it by
     // AT_LAZY: weights up to 2^AT_LAZY lose nothing in fp32 sums or in bf16's relative rounding,
     // and most tiles need one vote in place of six shuffles and a pass over the accumulators.
-    if (__any_sync(0xffffffffu, mx[0] > a.m[0] + ar.lazy || mx[1] > a.m[1] + ar.lazy)) {
-      float f[2];
+    if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int q = 0; q < NG; ++q) {
+        float f[2];
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1)
-          mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], o));
-        mx[j] = fmaxf(mx[j], a.m[j]);
-        f[j] = mx[j] == a.m[j] ? 1.f : ex2((a.m[j] - mx[j]) * ar.sl);  // 0 from -inf
-        a.l[j] *= f[j];
-        a.m[j] = mx[j];
+        for (int j = 0; j < 2; ++j) {
+          float m = mx[q][j];
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          m = fmaxf(m, a.m[q][j]);
+          f[j] = m == a.m[q][j] ? 1.f : ex2((a.m[q][j] - m) * ar.sl);  // 0 from -inf
+          a.l[q][j] *= f[j];
+          a.m[q][j] = m;
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) a.o[q][i][j] *= f[j & 1];
       }
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) a.o[i][j] *= f[j & 1];
     }
-    const float base[2] = {a.m[0] == -INFINITY ? 0.f : a.m[0], a.m[1] == -INFINITY ? 0.f : a.m[1]};
 #pragma unroll
-    for (int i = 0; i < NK; ++i)
+    for (int q = 0; q < NG; ++q)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        // the difference first: equal scores weigh the same whatever their size
-        s[i][j] = ex2((s[i][j] - base[j & 1]) * ar.sl);
-        a.l[j & 1] += s[i][j];
+        const float base = a.m[q][j & 1] == -INFINITY ? 0.f : a.m[q][j & 1];
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+          // the difference first: equal scores weigh the same whatever their size
+          s[q][i][j] = ex2((s[q][i][j] - base) * ar.sl);
+          a.l[q][j & 1] += s[q][i][j];
+        }
       }
     if constexpr (kParts == 1) {
-      weigh<D, DP, NK>(v, s, a, 0);
+      weigh(v, s, a, 0);
       load_v(v, vc, nxt, row, nfull);
     } else {
       static_assert(kParts == 1 || kParts % 2 == 0, "V's first part goes where K's does");
@@ -499,7 +549,7 @@ __device__ void piece(const AttnArgs& ar, char* smem, int64_t b, int n, int hk, 
         Tile<DP, T, NK>&x = z & 1 ? v : k, &y = z & 1 ? k : v;
         if (z + 1 < kParts) load_v(y, vc + (z + 1) * DP, cur, row, full);
         else load_k(y, kc, nxt, row, nfull);
-        weigh<D, DP, NK>(x, s, a, z);
+        weigh(x, s, a, z);
       }
     }
 #pragma unroll
@@ -507,72 +557,81 @@ __device__ void piece(const AttnArgs& ar, char* smem, int64_t b, int n, int hk, 
     full = nfull;
   }
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
+  for (int q = 0; q < NG; ++q)
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1) a.l[j] += __shfl_xor_sync(0xffffffffu, a.l[j], o);
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1)
+        a.l[q][j] += __shfl_xor_sync(0xffffffffu, a.l[q][j], o);
 }
 
-// The 4 warps' results joined: to o and lse (slot < 0), or as the partial piece `slot`.
-template <int D, typename T>
+// The 4 warps' results joined, AT_G heads at a time: to o and lse (slot < 0), or as the partial
+// piece `slot`.
+template <int D, typename T, int NG>
 __device__ void finish(const AttnArgs& ar, char* smem, float2 (*ml)[AT_G], int64_t b, int h0,
-                       int heads, const Acc<D>& a, int64_t slot) {
-  constexpr int kORow = Smem<D, T>::kORow, EL = 16 / (int)sizeof(T);
+                       int heads, const Acc<D, NG>& a, int64_t slot) {
+  constexpr int kORow = Smem<D, T, NG>::kORow, EL = 16 / (int)sizeof(T);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  __syncthreads();  // every warp is done with Q
   float* so = reinterpret_cast<float*>(smem);
-  if (g == 0) {
-    ml[warp][2 * t] = make_float2(a.m[0], a.l[0]);
-    ml[warp][2 * t + 1] = make_float2(a.m[1], a.l[1]);
-  }
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i) {
-    const int d = EL * (g + 8 * (i / (EL / 2))) + 2 * (i % (EL / 2));
-    *reinterpret_cast<float2*>(so + (warp * AT_G + 2 * t) * kORow + d) =
-        make_float2(a.o[i][0], a.o[i][2]);
-    *reinterpret_cast<float2*>(so + (warp * AT_G + 2 * t + 1) * kORow + d) =
-        make_float2(a.o[i][1], a.o[i][3]);
-  }
-  __syncthreads();
-  for (int x = threadIdx.x; x < heads * (D / 2); x += AT_NT) {
-    const int h = x / (D / 2), d = (x % (D / 2)) * 2;
-    float m = -INFINITY, l = 0.f;
-    float2 o = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < AT_W; ++w) m = fmaxf(m, ml[w][h].x);
-    const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll
-    for (int w = 0; w < AT_W; ++w) {
-      const float f = ex2((ml[w][h].x - base) * ar.sl);
-      const float2 y = *reinterpret_cast<const float2*>(so + (w * AT_G + h) * kORow + d);
-      l = fmaf(ml[w][h].y, f, l);
-      o.x = fmaf(y.x, f, o.x);
-      o.y = fmaf(y.y, f, o.y);
+  for (int q = 0; q < NG; ++q) {
+    __syncthreads();  // every warp is done with Q, or with the heads before these
+    if (g == 0) {
+      ml[warp][2 * t] = make_float2(a.m[q][0], a.l[q][0]);
+      ml[warp][2 * t + 1] = make_float2(a.m[q][1], a.l[q][1]);
     }
-    if (slot >= 0) {
-      *reinterpret_cast<float2*>(ar.acc + (slot * AT_G + h) * D + d) = o;
-      if (d == 0) ar.ml[slot * AT_G + h] = make_float2(m, l);
-      continue;
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      const int d = EL * (g + 8 * (i / (EL / 2))) + 2 * (i % (EL / 2));
+      *reinterpret_cast<float2*>(so + (warp * AT_G + 2 * t) * kORow + d) =
+          make_float2(a.o[q][i][0], a.o[q][i][2]);
+      *reinterpret_cast<float2*>(so + (warp * AT_G + 2 * t + 1) * kORow + d) =
+          make_float2(a.o[q][i][1], a.o[q][i][3]);
     }
-    const float r = l != 0.f ? 1.f / l : 0.f;  // nothing counted: zero, not 0 / 0
-    T* out = reinterpret_cast<T*>(ar.o) + (b * ar.Hq + h0 + h) * D + d;
-    if constexpr (sizeof(T) == 2)
-      *reinterpret_cast<__nv_bfloat162*>(out) = __floats2bfloat162_rn(o.x * r, o.y * r);
-    else
-      *reinterpret_cast<float2*>(out) = make_float2(o.x * r, o.y * r);
-    if (d == 0 && ar.lse)
-      ar.lse[b * ar.Hq + h0 + h] = (base * ar.sl + log2f(l)) * 0.69314718055994531f;
+    __syncthreads();
+    for (int x = threadIdx.x; x < min(AT_G, heads - q * AT_G) * (D / 2); x += AT_NT) {
+      const int h = x / (D / 2), d = (x % (D / 2)) * 2, hp = q * AT_G + h;
+      float m = -INFINITY, l = 0.f;
+      float2 o = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < AT_W; ++w) m = fmaxf(m, ml[w][h].x);
+      const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int w = 0; w < AT_W; ++w) {
+        const float f = ex2((ml[w][h].x - base) * ar.sl);
+        const float2 y = *reinterpret_cast<const float2*>(so + (w * AT_G + h) * kORow + d);
+        l = fmaf(ml[w][h].y, f, l);
+        o.x = fmaf(y.x, f, o.x);
+        o.y = fmaf(y.y, f, o.y);
+      }
+      if (slot >= 0) {
+        const int64_t at = slot * (AT_G * NG) + hp;
+        *reinterpret_cast<float2*>(ar.acc + at * D + d) = o;
+        if (d == 0) ar.ml[at] = make_float2(m, l);
+        continue;
+      }
+      const float r = l != 0.f ? 1.f / l : 0.f;  // nothing counted: zero, not 0 / 0
+      const int64_t row = b * ar.Hq + h0 + hp;
+      T* out = reinterpret_cast<T*>(ar.o) + row * D + d;
+      if constexpr (sizeof(T) == 2)
+        *reinterpret_cast<__nv_bfloat162*>(out) = __floats2bfloat162_rn(o.x * r, o.y * r);
+      else
+        *reinterpret_cast<float2*>(out) = make_float2(o.x * r, o.y * r);
+      if (d == 0 && ar.lse)
+        ar.lse[row] = (base * ar.sl + log2f(l)) * 0.69314718055994531f;
+    }
   }
 }
 
 // How the work is divided, the same for every caller.  The units of request b are those of its
-// pieces (key head x group of AT_G query heads) in a row, each its CTA tiles behind AT_START; the
+// pieces (key head x AT_G NG query heads) in a row, each its CTA tiles behind AT_START; the
 // W units of all requests are divided over C CTAs, CTA c taking [W c / C, W (c + 1) / C).
 // Each warp finds its way by itself: a lane sums up a run of requests, one scan over the lanes.
 // AHEAD: read past the first-level cache, for a caller that has not waited for the kernel before it
 // (the lengths were written before that one began).
-template <int D, typename T, bool AHEAD>
+template <int D, typename T, int NG, bool AHEAD>
 struct Schedule {
-  static constexpr int TK = Cfg<D, T>::kKeys * AT_W;  // keys per CTA tile
+  static constexpr int TK = Cfg<D, T, NG>::kKeys * AT_W;  // keys per CTA tile
   const AttnArgs& ar;
   int64_t W, incl, excl;  // all units; up to and before this lane's run
   int C, run, per;        // CTAs with work, requests per run, pieces per request
@@ -636,14 +695,15 @@ struct Schedule {
   }
 };
 
-template <int D, typename T>
-__global__ void __launch_bounds__(AT_NT, Cfg<D, T>::kCtas) k_attn_decode(AttnArgs ar) {
+template <int D, typename T, int NG>
+__global__ void __launch_bounds__(AT_NT, Cfg<D, T, NG>::kCtas) k_attn_decode(AttnArgs ar) {
+  constexpr int GP = AT_G * NG;
   extern __shared__ __align__(16) char smem[];
   __shared__ float2 ml[AT_W][AT_G];
   after_previous();
   before_next();
   const int tid = threadIdx.x, c = blockIdx.x;
-  const Schedule<D, T, false> sc(ar, gridDim.x);
+  const Schedule<D, T, NG, false> sc(ar, gridDim.x);
   int bad = 0;
   if (c == 0)
     for (int64_t b = tid; b < ar.B; b += AT_NT) bad |= sc.length(b) != ar.len[b];
@@ -665,11 +725,11 @@ __global__ void __launch_bounds__(AT_NT, Cfg<D, T>::kCtas) k_attn_decode(AttnArg
       const int r1 = (int)(u1 - u < w - r0 ? r0 + (u1 - u) : w);
       const int t0 = max(0, r0 - AT_START), t1 = max(0, r1 - AT_START);
       if (t0 < t1) {
-        const int hk = h / ar.HG, hg = h % ar.HG, heads = min(AT_G, ar.G - hg * AT_G);
-        Acc<D> a;
-        piece<D, T>(ar, smem, b, n, hk, hg, t0, t1, a, &bad);
+        const int hk = h / ar.HG, hg = h % ar.HG, heads = min(GP, ar.G - hg * GP);
+        Acc<D, NG> a;
+        piece<D, T, NG>(ar, smem, b, n, hk, hg, t0, t1, a, &bad);
         const int64_t slot = t0 == 0 && t1 == nt ? -1 : t0 == 0 ? 2 * c + 1 : 2 * c;
-        finish<D, T>(ar, smem, ml, b, hk * ar.G + hg * AT_G, heads, a, slot);
+        finish<D, T, NG>(ar, smem, ml, b, hk * ar.G + hg * GP, heads, a, slot);
       }
       u += r1 - r0;
       r0 = 0;
@@ -713,13 +773,13 @@ __device__ __forceinline__ void add_scaled(float4& a, const float4& x, float f) 
 // first of them does it alone, a warp per query head (517 tokens, 9 parts, 32 items: 9.4 us for
 // the whole call against 12.7 shared; 10 parts of 3 items: 13.4 shared, 14.3 alone).  The schedule is worked out again from the lengths, which the kernels in front of the pass wrote;
 // only then does the CTA wait for the pass.
-template <int D, typename T>
+template <int D, typename T, int NG>
 __global__ void __launch_bounds__(AJ_NT) k_attn_join(AttnArgs ar) {
-  constexpr int NW = AJ_NT / 32, MAXC = AT_SMS * Cfg<D, T>::kCtas;
+  constexpr int GP = AT_G * NG, NW = AJ_NT / 32, MAXC = AT_SMS * Cfg<D, T, NG>::kCtas;
   __shared__ float s_w[MAXC], s_red[NW][2];
   __shared__ float4 s_o[AJ_NT / 16][AJ_DC / 4];
   const int x = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const Schedule<D, T, true> sc(ar, gridDim.x);
+  const Schedule<D, T, NG, true> sc(ar, gridDim.x);
   int64_t b = 0, r = 0;
   int c = 0, last = 0, h = 0;  // first and last CTA of the piece
   if (x < sc.C) {
@@ -731,50 +791,51 @@ __global__ void __launch_bounds__(AJ_NT) k_attn_join(AttnArgs ar) {
     c = sc.cta_of(start + AT_START);
     last = sc.cta_of(start + w - 1);
   }
-  const int hk = h / ar.HG, hg = h % ar.HG, heads = min(AT_G, ar.G - hg * AT_G);
-  const int64_t row0 = b * ar.Hq + hk * ar.G + hg * AT_G;
+  const int hk = h / ar.HG, hg = h % ar.HG, heads = min(GP, ar.G - hg * GP);
+  const int64_t row0 = b * ar.Hq + hk * ar.G + hg * GP;
   const int n = last - c + 1;
   after_previous();
   before_next();
   if (x < c || x >= last) return;
   // parts: slot 2c + 1 of the piece's first CTA c, slot 2i of the CTAs behind it
   if (n <= AJ_FEW || (n <= 32 && heads * (D / AJ_DC) > n - 1)) {
-    const int g = warp;
-    if (x > c || g >= heads) return;
-    auto slot = [&](int i) { return (int64_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * AT_G + g; };
-    const float2 ml = lane < n ? ar.ml[slot(lane)] : make_float2(-INFINITY, 0.f);
-    float m = ml.x;
+    if (x > c) return;
+    for (int g = warp; g < heads; g += NW) {
+      auto slot = [&](int i) { return (int64_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * GP + g; };
+      const float2 ml = lane < n ? ar.ml[slot(lane)] : make_float2(-INFINITY, 0.f);
+      float m = ml.x;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float base = m == -INFINITY ? 0.f : m, f = ex2((ml.x - base) * ar.sl);
-    float l = ml.y * f;
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const float base = m == -INFINITY ? 0.f : m, f = ex2((ml.x - base) * ar.sl);
+      float l = ml.y * f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    constexpr int V = D >= 128 ? D / 128 : 1;  // columns 4 lane + 128 v
-    const bool in = D >= 128 || lane * 4 < D;
-    float4 a[V];
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      constexpr int V = D >= 128 ? D / 128 : 1;  // columns 4 lane + 128 v
+      const bool in = D >= 128 || lane * 4 < D;
+      float4 a[V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) a[v] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < n; i0 += AJ_FEW)
+      for (int v = 0; v < V; ++v) a[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int i0 = 0; i0 < n; i0 += AJ_FEW)
 #pragma unroll
-      for (int j = 0; j < AJ_FEW; ++j) {
-        const int i = i0 + j;
-        const float fi = __shfl_sync(0xffffffffu, f, i);
-        const float* part = ar.acc + slot(i) * D + lane * 4;
+        for (int j = 0; j < AJ_FEW; ++j) {
+          const int i = i0 + j;
+          const float fi = __shfl_sync(0xffffffffu, f, i);
+          const float* part = ar.acc + slot(i) * D + lane * 4;
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-          if (i < n && in) add_scaled(a[v], *reinterpret_cast<const float4*>(part + v * 128), fi);
-      }
-    const float q = l != 0.f ? 1.f / l : 0.f;
+          for (int v = 0; v < V; ++v)
+            if (i < n && in) add_scaled(a[v], *reinterpret_cast<const float4*>(part + v * 128), fi);
+        }
+      const float q = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (in) store_o(reinterpret_cast<T*>(ar.o) + (row0 + g) * D + lane * 4 + v * 128, a[v], q);
-    if (lane == 0 && ar.lse) ar.lse[row0 + g] = (base * ar.sl + log2f(l)) * 0.69314718055994531f;
+      for (int v = 0; v < V; ++v)
+        if (in) store_o(reinterpret_cast<T*>(ar.o) + (row0 + g) * D + lane * 4 + v * 128, a[v], q);
+      if (lane == 0 && ar.lse) ar.lse[row0 + g] = (base * ar.sl + log2f(l)) * 0.69314718055994531f;
+    }
     return;
   }
   for (int item = x - c; item < heads * (D / AJ_DC); item += n - 1) {
     const int g = item % heads, d0 = item / heads * AJ_DC, col = tid % 16, first = tid / 16;
-    auto slot = [&](int i) { return (int64_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * AT_G + g; };
+    auto slot = [&](int i) { return (int64_t)(i == 0 ? 2 * c + 1 : 2 * (c + i)) * GP + g; };
     float m = -INFINITY, l = 0.f;
     for (int i = tid; i < n; i += AJ_NT) m = fmaxf(m, ar.ml[slot(i)].x);
 #pragma unroll
@@ -838,20 +899,25 @@ gdn_status check_problem(const gdn_attn_problem* p) {
   return GDN_OK;
 }
 
-// CTAs of the pass and the workspace's parts (a fixed count per D and type, so that results do
-// not depend on the device).
+// CTAs of the pass and the workspace's parts (a fixed count per kind, so that results do not
+// depend on the device).
 struct Plan {
   int ctas;
   size_t acc, total;
 };
-template <int D, typename T>
+template <int D, typename T, int NG>
 Plan plan_of() {
   Plan pl;
-  pl.ctas = AT_SMS * Cfg<D, T>::kCtas;
-  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-  pl.acc = up((size_t)pl.ctas * 2 * AT_G * sizeof(float2));
-  pl.total = pl.acc + (size_t)pl.ctas * 2 * AT_G * D * sizeof(float);
+  pl.ctas = AT_SMS * Cfg<D, T, NG>::kCtas;
+  const size_t parts = (size_t)pl.ctas * 2 * AT_G * NG;
+  pl.acc = (parts * sizeof(float2) + 255) & ~(size_t)255;
+  pl.total = pl.acc + parts * D * sizeof(float);
   return pl;
+}
+template <int D, typename T>
+size_t workspace_of() {
+  const size_t a = plan_of<D, T, 1>().total, b = plan_of<D, T, 2>().total;
+  return a > b ? a : b;
 }
 
 // Runs f with the call's head dim and type as template arguments.
@@ -867,15 +933,16 @@ auto with_types(const gdn_attn_problem* p, F f) {
   return p->D == 64 ? f(D64(), 0.f) : p->D == 128 ? f(D128(), 0.f) : f(D256(), 0.f);
 }
 
-template <int D, typename T>
+template <int D, typename T, int NG>
 cudaError_t launch(AttnArgs ar, char* ws, cudaStream_t st) {
-  const Plan pl = plan_of<D, T>();
+  const Plan pl = plan_of<D, T, NG>();
+  ar.HG = (ar.G + AT_G * NG - 1) / (AT_G * NG);
   ar.ml = (float2*)ws;
   ar.acc = (float*)(ws + pl.acc);
-  const cudaError_t e = launch_behind(k_attn_decode<D, T>, dim3(pl.ctas), AT_NT,
-                                      Smem<D, T>::kBytes, st, ar);
+  const cudaError_t e = launch_behind(k_attn_decode<D, T, NG>, dim3(pl.ctas), AT_NT,
+                                      Smem<D, T, NG>::kBytes, st, ar);
   if (e != cudaSuccess) return e;
-  return launch_behind(k_attn_join<D, T>, dim3(pl.ctas), AJ_NT, 0, st, ar);
+  return launch_behind(k_attn_join<D, T, NG>, dim3(pl.ctas), AJ_NT, 0, st, ar);
 }
 
 }  // namespace
@@ -889,7 +956,7 @@ gdn_status gdn_attn_decode_workspace_size(const gdn_attn_problem* p, size_t* byt
   if (!bytes) return GDN_ERR_INVALID_ARG;
   gdn_status s = check_problem(p);
   if (s != GDN_OK) return s;
-  *bytes = with_types(p, [](auto d, auto t) { return plan_of<d(), decltype(t)>().total; });
+  *bytes = with_types(p, [](auto d, auto t) { return workspace_of<d(), decltype(t)>(); });
   return GDN_OK;
 }
 
@@ -917,7 +984,6 @@ gdn_status gdn_attn_decode(const gdn_attn_problem* p, const void* q, const void*
   ar.qs = p->q_stride ? p->q_stride : p->Hq * p->D;
   ar.P = p->page_size;
   ar.G = (int)(p->Hq / p->Hk);
-  ar.HG = (ar.G + AT_G - 1) / AT_G;
   ar.sl = (p->scale > 0.f ? p->scale : 1.0f / sqrtf((float)p->D)) * 1.4426950408889634f;
   ar.lazy = fminf(AT_LAZY / ar.sl, 1e30f);
   ar.q = q;
@@ -930,7 +996,9 @@ gdn_status gdn_attn_decode(const gdn_attn_problem* p, const void* q, const void*
   ar.status = status;
   cudaStream_t st = (cudaStream_t)stream;
   const cudaError_t e = with_types(p, [&](auto d, auto t) {
-    return launch<d(), decltype(t)>(ar, (char*)workspace, st);
+    // one pass over the cache serves 8 query heads of a key head, or 16
+    return ar.G <= AT_G ? launch<d(), decltype(t), 1>(ar, (char*)workspace, st)
+                        : launch<d(), decltype(t), 2>(ar, (char*)workspace, st);
   });
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }

@@ -132,6 +132,11 @@ ATTN = [  # lens, Hq, Hk, D, page, dtype
     ([700], 8, 1, 256, 16, BF), ([1500], 8, 1, 256, 16, BF), ([1500], 8, 1, 256, 16, F32),
     ([60011], 2, 1, 64, 64, BF), ([i % 7 for i in range(3000)], 2, 1, 64, 16, BF),
     ([(i * 37) % 301 for i in range(1111)], 2, 1, 64, 16, F32),
+    # more than 8 query heads to a key head: 16 to a pass, the last pass not full
+    ([300, 0, 17, 1100], 9, 1, 64, 16, BF), ([300, 0, 17, 1100], 32, 2, 256, 16, BF),
+    ([300, 0, 17, 1100], 20, 1, 128, 32, BF), ([3000], 48, 2, 128, 16, BF),
+    ([300, 0, 17, 700], 17, 1, 128, 16, F32), ([300, 0, 17, 700], 24, 2, 256, 16, F32),
+    ([300, 0, 17, 700], 40, 1, 64, 16, F32), ([2500], 13, 1, 256, 48, BF),
 ]
 
 
