@@ -608,24 +608,35 @@ __global__ void __launch_bounds__(RO_NT, 2) k_qk_norm_rope_bwd(RopeArgs ar) {
 }
 
 // dwq, dwk = sums over the n_part CTA partials in fp64: 8 columns (one sector) per CTA, thread row
-// r adds the partials r, r + 32, ... in order, then one thread per column the 32 row sums.
+// r adds the partials r, r + 32, ... in order (at most 10, read at once), then the 32 rows in a
+// fixed tree.
 constexpr int RD_COLS = 8, RD_ROWS = RO_NT / RD_COLS;
+constexpr int RD_MOST = (RO_CTAS + RD_ROWS - 1) / RD_ROWS;
 __global__ void __launch_bounds__(RO_NT) k_qk_norm_rope_dw(int n_part, int D, const float* part,
                                                            float* dwq, float* dwk) {
-  __shared__ double acc[RD_ROWS][RD_COLS];
+  __shared__ double acc[RO_W][RD_COLS];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = threadIdx.x % RD_COLS, row = threadIdx.x / RD_COLS;
   const int e = blockIdx.x * RD_COLS + col;  // D is a multiple of 8: e < 2 D
   after_previous();
   before_next();
+  float x[RD_MOST];
+#pragma unroll
+  for (int i = 0; i < RD_MOST; ++i) {
+    const int p = row + i * RD_ROWS;
+    x[i] = p < n_part ? part[(int64_t)p * 2 * D + e] : 0.f;
+  }
   double s = 0.0;
-#pragma unroll 5
-  for (int p = row; p < n_part; p += RD_ROWS) s += part[(int64_t)p * 2 * D + e];
-  acc[row][col] = s;
+#pragma unroll
+  for (int i = 0; i < RD_MOST; ++i) s += x[i];
+#pragma unroll
+  for (int o = RD_COLS; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane < RD_COLS) acc[warp][lane] = s;
   __syncthreads();
   if (row == 0) {
     s = 0.0;
 #pragma unroll
-    for (int r = 0; r < RD_ROWS; ++r) s += acc[r][col];
+    for (int w = 0; w < RO_W; ++w) s += acc[w][col];
     float* out = e < D ? dwq : dwk;
     if (out) out[e < D ? e : e - D] = (float)s;
   }
