@@ -20,10 +20,10 @@
 // (bf16) or shuffles (fp32).  No shared memory, barrier or copy wait is on the path of the
 // data: a warp's next K tile is on its way while it does the softmax and V's product, and the
 // next V tile during the next K product; 8 to 16 such warps per SM keep 64 to 128 KB in flight.
-// fp32 caches use tf32 products of the two-term split x = hi + lo (hi hi + hi lo + lo hi:
-// 2^-21 of each product's size), which keeps fp32 accuracy at the same layout.  The split is
-// done with integer and fp32 instructions at full rate (131001 tokens of 8 heads of 128: 167 us
-// against 234 us with conversion instructions and a test of every value for infinities).
+// fp32 caches use tf32 products of the two-term split x = hi + lo (2^-23 of x; all four products),
+// which keeps fp32 accuracy at the same layout.  The split is done with integer and fp32
+// instructions at full rate (131001 tokens of 8 heads of 128: 181 us against 234 with conversion
+// instructions and a test of every value for infinities).
 //
 // Split: the unit is a CTA tile of one (request, key head); the units of all requests in a
 // row are divided evenly over the CTAs of one wave, whatever the lengths: no tail, and one long
@@ -120,14 +120,15 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-// x = hi + lo with hi, lo in tf32: hi is x rounded to nearest (ties away), lo what is left, cut
-// after its 11 bits (2^-22 of x, of either sign).  SAFE: an infinite or NaN x, or one that hi's
-// rounding could make infinite, goes into lo alone: mma_split multiplies lo only with the other
-// operand's hi, so that no 0 * inf arises beside the product itself.
+// x = hi + lo with hi, lo in tf32: hi is x rounded to nearest (ties away), lo what is left, rounded
+// too (2^-23 of x).  SAFE: an infinite or NaN x, or one that hi's rounding could make infinite, goes
+// into lo alone, and mma_split<SAFE> multiplies lo only with the other operand's hi, so that no
+// 0 * inf arises beside the product itself.
 template <bool SAFE>
 __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t* hi, uint32_t* lo) {
   const uint32_t h = (x + 0x1000u) & 0xffffe000u;
-  const uint32_t l = __float_as_uint(__uint_as_float(x) - __uint_as_float(h)) & 0xffffe000u;
+  const uint32_t l =
+      (__float_as_uint(__uint_as_float(x) - __uint_as_float(h)) + 0x1000u) & 0xffffe000u;
   const bool huge = SAFE && (x & 0x7f800000u) >= 0x7f000000u;
   *hi = huge ? 0u : h;
   *lo = huge ? x : l;
@@ -144,13 +145,19 @@ __device__ __forceinline__ bool plain(uint64_t acc) {  // for every lane of the 
   const float x = __uint_as_float((uint32_t)acc), y = __uint_as_float((uint32_t)(acc >> 32));
   return !__any_sync(0xffffffffu, !(fabsf(x) + fabsf(y) < INFINITY));
 }
-// c += A B with A and B given as split values
-__device__ __forceinline__ void mma_split(float (&c)[4], const uint32_t (&ah)[4],
+// hi + lo += A B with A and B given as split values; lo lo is left out where a value is in lo alone
+// (with an infinity there the other's lo could only add to or spoil what its hi gives).  The
+// tensor cores cut an accumulator's low bits off at every product, so the small products have an
+// accumulator of their own, and both are kept for a few products only and then added up with
+// rounded fp32 additions (one accumulator throughout: 2.6e-6 off at D = 256, 3.1e-7 now).
+template <bool SAFE>
+__device__ __forceinline__ void mma_split(float (&hi)[4], float (&lo)[4], const uint32_t (&ah)[4],
                                           const uint32_t (&al)[4], const uint32_t (&bh)[2],
                                           const uint32_t (&bl)[2]) {
-  mma_tf32(c, al, bh[0], bh[1]);
-  mma_tf32(c, ah, bl[0], bl[1]);
-  mma_tf32(c, ah, bh[0], bh[1]);
+  if constexpr (!SAFE) mma_tf32(lo, al, bl[0], bl[1]);
+  mma_tf32(lo, al, bh[0], bh[1]);
+  mma_tf32(lo, ah, bl[0], bl[1]);
+  mma_tf32(hi, ah, bh[0], bh[1]);
 }
 
 // Q of the piece in shared memory: AT_G NG rows (zeros past the piece's heads); rows are 64 bytes
@@ -199,7 +206,7 @@ struct Block {
 // qs points at the part in Q's rows.
 template <int D, int DP, int NK, int NG>
 __device__ __forceinline__ void scores(const Tile<DP, __nv_bfloat16, NK>& k, const char* qs,
-                                       float (&s)[NG][NK][4]) {
+                                       bool /*qplain*/, float (&s)[NG][NK][4]) {
   constexpr int kRow = Smem<D, __nv_bfloat16, NG>::kRow;
   const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
 #pragma unroll
@@ -222,39 +229,49 @@ __device__ __forceinline__ void scores_split(const Tile<DP, float, NK>& k, const
   constexpr int kRow = Smem<D, float, NG>::kRow;
   const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
 #pragma unroll
-  for (int c = 0; c < DP / 16; ++c) {
-    uint4 bh[NG], bl[NG];
+  for (int c0 = 0; c0 < DP / 16; c0 += 4) {  // 64 elements: 8 products of hi
+    float hi[NG][NK][4] = {}, lo[NG][NK][4] = {};
 #pragma unroll
-    for (int q = 0; q < NG; ++q) {
-      const char* at = qs + (q * AT_G + g) * kRow + (t + 4 * c) * 16;
-      bh[q] = *reinterpret_cast<const uint4*>(at);
-      bl[q] = *reinterpret_cast<const uint4*>(at + AT_G * NG * kRow);
-    }
+    for (int c = c0; c < c0 + 4; ++c) {
+      uint4 bh[NG], bl[NG];
 #pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      const uint4 a0 = k.r[i][(c & 1) * 2][c >> 1], a1 = k.r[i][(c & 1) * 2 + 1][c >> 1];
+      for (int q = 0; q < NG; ++q) {
+        const char* at = qs + (q * AT_G + g) * kRow + (t + 4 * c) * 16;
+        bh[q] = *reinterpret_cast<const uint4*>(at);
+        bl[q] = *reinterpret_cast<const uint4*>(at + AT_G * NG * kRow);
+      }
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        uint32_t ah[4], al[4];
-        split_tf32<SAFE>(word(a0, 2 * u), &ah[0], &al[0]);
-        split_tf32<SAFE>(word(a1, 2 * u), &ah[1], &al[1]);
-        split_tf32<SAFE>(word(a0, 2 * u + 1), &ah[2], &al[2]);
-        split_tf32<SAFE>(word(a1, 2 * u + 1), &ah[3], &al[3]);
+      for (int i = 0; i < NK; ++i) {
+        const uint4 a0 = k.r[i][(c & 1) * 2][c >> 1], a1 = k.r[i][(c & 1) * 2 + 1][c >> 1];
 #pragma unroll
-        for (int q = 0; q < NG; ++q) {
-          const uint32_t h[2] = {word(bh[q], 2 * u), word(bh[q], 2 * u + 1)};
-          const uint32_t l[2] = {word(bl[q], 2 * u), word(bl[q], 2 * u + 1)};
-          mma_split(s[q][i], ah, al, h, l);
+        for (int u = 0; u < 2; ++u) {
+          uint32_t ah[4], al[4];
+          split_tf32<SAFE>(word(a0, 2 * u), &ah[0], &al[0]);
+          split_tf32<SAFE>(word(a1, 2 * u), &ah[1], &al[1]);
+          split_tf32<SAFE>(word(a0, 2 * u + 1), &ah[2], &al[2]);
+          split_tf32<SAFE>(word(a1, 2 * u + 1), &ah[3], &al[3]);
+#pragma unroll
+          for (int q = 0; q < NG; ++q) {
+            const uint32_t h[2] = {word(bh[q], 2 * u), word(bh[q], 2 * u + 1)};
+            const uint32_t l[2] = {word(bl[q], 2 * u), word(bl[q], 2 * u + 1)};
+            mma_split<SAFE>(hi[q][i], lo[q][i], ah, al, h, l);
+          }
         }
       }
     }
+#pragma unroll
+    for (int q = 0; q < NG; ++q)
+#pragma unroll
+      for (int i = 0; i < NK; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[q][i][j] += hi[q][i][j] + lo[q][i][j];
   }
 }
 
 template <int D, int DP, int NK, int NG>
-__device__ __forceinline__ void scores(const Tile<DP, float, NK>& k, const char* qs,
+__device__ __forceinline__ void scores(const Tile<DP, float, NK>& k, const char* qs, bool qplain,
                                        float (&s)[NG][NK][4]) {
-  if (plain(k)) scores_split<false, D>(k, qs, s);
+  if (plain(k) && qplain) scores_split<false, D>(k, qs, s);
   else scores_split<true, D>(k, qs, s);
 }
 
@@ -292,10 +309,10 @@ __device__ __forceinline__ void weigh_split(const Tile<DP, float, NK>& v,
                                             const float (&p)[NG][NK][4], Acc<D, NG>& a, int part) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-  for (int i = 0; i < NK; ++i)
+  for (int i = 0; i < NK; ++i) {
+    uint32_t bh[2][NG][2], bl[2][NG][2];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {  // keys 8u .. 8u + 7
-      uint32_t bh[NG][2], bl[NG][2];
+    for (int u = 0; u < 2; ++u)  // keys 8u .. 8u + 7
 #pragma unroll
       for (int q = 0; q < NG; ++q)
 #pragma unroll
@@ -303,22 +320,30 @@ __device__ __forceinline__ void weigh_split(const Tile<DP, float, NK>& v,
           const int src = (t + 4 * z) * 4 + (g >> 1);
           const float e = __shfl_sync(0xffffffffu, p[q][i][2 * u], src);
           const float f = __shfl_sync(0xffffffffu, p[q][i][2 * u + 1], src);
-          split_tf32<true>(__float_as_uint(g & 1 ? f : e), &bh[q][z], &bl[q][z]);
+          split_tf32<true>(__float_as_uint(g & 1 ? f : e), &bh[u][q][z], &bl[u][q][z]);
         }
 #pragma unroll
-      for (int c = 0; c < DP / 32; ++c)
+    for (int c = 0; c < DP / 32; ++c)
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
+      for (int w = 0; w < 2; ++w) {
+        float hi[NG][4] = {}, lo[NG][4] = {};
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
           uint32_t ah[4], al[4];
 #pragma unroll
           for (int z = 0; z < 4; ++z)
             split_tf32<SAFE>(word(v.r[i][2 * u + (z >> 1)][c], 2 * w + (z & 1)), &ah[z],
                              &al[z]);
 #pragma unroll
-          for (int q = 0; q < NG; ++q)
-            mma_split(a.o[q][part * (DP / 16) + c * 2 + w], ah, al, bh[q], bl[q]);
+          for (int q = 0; q < NG; ++q) mma_split<SAFE>(hi[q], lo[q], ah, al, bh[u][q], bl[u][q]);
         }
-    }
+#pragma unroll
+        for (int q = 0; q < NG; ++q)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            a.o[q][part * (DP / 16) + c * 2 + w][j] += hi[q][j] + lo[q][j];
+      }
+  }
 }
 template <int D, int DP, int NK, int NG>
 __device__ __forceinline__ void weigh(const Tile<DP, float, NK>& v, const float (&p)[NG][NK][4],
@@ -387,6 +412,7 @@ __device__ void piece(const AttnArgs& ar, char* smem, int64_t b, int n, int hk, 
   // Q (the barrier in front: other warps may still read what was there)
   __syncthreads();
   const T* q = reinterpret_cast<const T*>(ar.q) + b * ar.qs + ((int64_t)hk * ar.G + hg * GP) * D;
+  uint64_t qacc = 0;
   for (int i = threadIdx.x; i < GP * D / EL; i += AT_NT) {
     const int h = i / (D / EL), c = i % (D / EL);
     uint4 x = make_uint4(0, 0, 0, 0);
@@ -394,6 +420,7 @@ __device__ void piece(const AttnArgs& ar, char* smem, int64_t b, int n, int hk, 
     char* dst = smem + h * kRow + c * 16;
     if constexpr (sizeof(T) == 4) {
       uint4 hi, lo;
+      probe(x, &qacc);
       split_tf32<true>(x.x, &hi.x, &lo.x);
       split_tf32<true>(x.y, &hi.y, &lo.y);
       split_tf32<true>(x.z, &hi.z, &lo.z);
@@ -466,7 +493,8 @@ __device__ void piece(const AttnArgs& ar, char* smem, int64_t b, int n, int hk, 
   load_k(k, kc, cur, row, full);
   if constexpr (kParts == 1) load_v(v, vc, cur, row, full);
   look_up();
-  __syncthreads();  // Q is there
+  // Q is there; fp32: whether all of it is finite
+  const bool qplain = __syncthreads_and(sizeof(T) == 2 || plain(qacc));
 #pragma unroll 1
   for (int tile = t0; tile < t1; ++tile) {
     Block nxt[NK];
@@ -474,7 +502,7 @@ __device__ void piece(const AttnArgs& ar, char* smem, int64_t b, int n, int hk, 
     look_up();
     float s[NG][NK][4] = {};
     if constexpr (kParts == 1) {
-      scores<D>(k, smem, s);
+      scores<D>(k, smem, qplain, s);
       load_k(k, kc, nxt, row, nfull);
     } else {
 #pragma unroll
@@ -482,7 +510,7 @@ __device__ void piece(const AttnArgs& ar, char* smem, int64_t b, int n, int hk, 
         Tile<DP, T, NK>&x = z & 1 ? v : k, &y = z & 1 ? k : v;
         if (z + 1 < kParts) load_k(y, kc + (z + 1) * DP, cur, row, full);
         else load_v(y, vc, cur, row, full);
-        scores<D>(x, smem + z * DP * sizeof(T), s);
+        scores<D>(x, smem + z * DP * sizeof(T), qplain, s);
       }
     }
     if (!full)
