@@ -882,11 +882,16 @@ def _arg(name, t, dev, dtype, shape):
     return t.data_ptr()
 
 
-def _out(name, t, dev, dtype, shape, device):
-    """(output, its address): the caller's, checked, or a new one."""
+def _out(name, t, dev, dtype, shape, device, stream):
+    """(output, its address): the caller's, checked, or a new one, allocated for the stream that
+    the call runs on."""
     if t is not None:
         return t, _arg(name, t, dev, dtype, shape)
-    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+    else:
+        with torch.cuda.stream(stream):
+            t = torch.empty(shape, dtype=dtype, device=device)
     return t, t.data_ptr()
 
 
@@ -974,7 +979,7 @@ def gdn_step(q, k, v, a, b, A_log, dt_bias, state, slots=None, *, l2norm=True, e
         raise ValueError(f"gdn_step takes one token per row, got {T}")
     p = Problem(_dtype_code(dt), 64, B, 1, 0, Hqk, H, dk, dv, 1 if l2norm else 0, eps, scale, 0)
     qk, vs, gates, f32 = (B, 1, Hqk, dk), (B, 1, H, dv), (B, 1, H), torch.float32
-    o, op = _out("o", o, dev, dt, vs, q.device)
+    o, op = _out("o", o, dev, dt, vs, q.device, stream)
     _call("gdn_step", dev, p, n,
           None if slots is None else _arg("slots", slots, dev, torch.int32, (B,)),
           _arg("q", q, dev, dt, qk), _arg("k", k, dev, dt, qk), _arg("v", v, dev, dt, vs),
@@ -1016,8 +1021,8 @@ def gdn_qk_norm_rope_fwd(q, k, wq, wk, inv_freq, positions=None, *, T=None, inte
     at n).  q and k may be slices of one projection.  Returns (q_out, k_out), contiguous."""
     dev, dt = _device_of(q), q.dtype
     p, qp, kp, _ = _rope_problem(q, k, None, dev, inv_freq, T, interleaved, eps, rope_scale)
-    q_out, qo = _out("q_out", q_out, dev, dt, q.shape, q.device)
-    k_out, ko = _out("k_out", k_out, dev, dt, k.shape, q.device)
+    q_out, qo = _out("q_out", q_out, dev, dt, q.shape, q.device, stream)
+    k_out, ko = _out("k_out", k_out, dev, dt, k.shape, q.device, stream)
     _call("gdn_qk_norm_rope_fwd", dev, p, qp, kp,
           *_rope_tables(wq, wk, inv_freq, positions, p, dev), qo, ko, _raw_stream(stream, dev))
     return q_out, k_out
@@ -1036,12 +1041,12 @@ def gdn_qk_norm_rope_bwd(q, k, wq, wk, inv_freq, positions, dq_out, dk_out, *, T
     """Backward of gdn_qk_norm_rope_fwd: (dq, dk contiguous in q's type, dwq, dwk [D] fp32)."""
     dev, dt, f32 = _device_of(q), q.dtype, torch.float32
     p, qp, kp, _ = _rope_problem(q, k, None, dev, inv_freq, T, interleaved, eps, rope_scale)
-    dq, dqp = _out("dq", dq, dev, dt, q.shape, q.device)
-    dk, dkp = _out("dk", dk, dev, dt, k.shape, q.device)
-    dwq, wqp = _out("dwq", dwq, dev, f32, (p.D,), q.device)
-    dwk, wkp = _out("dwk", dwk, dev, f32, (p.D,), q.device)
+    dq, dqp = _out("dq", dq, dev, dt, q.shape, q.device, stream)
+    dk, dkp = _out("dk", dk, dev, dt, k.shape, q.device, stream)
+    dwq, wqp = _out("dwq", dwq, dev, f32, (p.D,), q.device, stream)
+    dwk, wkp = _out("dwk", dwk, dev, f32, (p.D,), q.device, stream)
     n = gdn_qk_norm_rope_bwd_workspace_size(p) if ws is None else ws.numel()
-    ws, wsp = _out("ws", ws, dev, torch.uint8, (n,), q.device)
+    ws, wsp = _out("ws", ws, dev, torch.uint8, (n,), q.device, stream)
     _call("gdn_qk_norm_rope_bwd", dev, p, qp, kp,
           *_rope_tables(wq, wk, inv_freq, positions, p, dev),
           _arg("dq_out", dq_out, dev, dt, q.shape), _arg("dk_out", dk_out, dev, dt, k.shape),
@@ -1057,7 +1062,7 @@ def gdn_qk_norm_rope_cache(q, k, v, wq, wk, inv_freq, positions, slots, k_cache,
     [pages, page_size, Hk, D].  Returns q_out."""
     dev, dt = _device_of(q), q.dtype
     p, qp, kp, vp = _rope_problem(q, k, v, dev, inv_freq, T, interleaved, eps, rope_scale)
-    q_out, qo = _out("q_out", q_out, dev, dt, q.shape, q.device)
+    q_out, qo = _out("q_out", q_out, dev, dt, q.shape, q.device, stream)
     cache = k_cache.shape[:-2] + (p.Hk, p.D)
     _call("gdn_qk_norm_rope_cache", dev, p, qp, kp, vp,
           *_rope_tables(wq, wk, inv_freq, positions, p, dev), k_cache.shape[:-2].numel(),
@@ -1089,15 +1094,15 @@ def gdn_attn_decode(q, k_cache, v_cache, block_table, seq_len, *, scale=0.0, o=N
     qp, qs = _rows("q", q, dev, dt, q.shape)
     blocks = block_table.shape[1]
     p = AttnProblem(_dtype_code(dt), D, P, scale, B, Hq, Hk, pages, blocks, qs)
-    o, op = _out("o", o, dev, dt, (B, Hq, D), q.device)
+    o, op = _out("o", o, dev, dt, (B, Hq, D), q.device, stream)
     lp = None
     if lse is not None or want_lse:
-        lse, lp = _out("lse", lse, dev, torch.float32, (B, Hq), q.device)
+        lse, lp = _out("lse", lse, dev, torch.float32, (B, Hq), q.device, stream)
     if ws is not None:
         n = ws.numel()
     else:  # the size goes by D and the type alone
         n = _attn_ws.get((D, dt)) or _attn_ws.setdefault((D, dt), gdn_attn_decode_workspace_size(p))
-    ws, wsp = _out("ws", ws, dev, torch.uint8, (n,), q.device)
+    ws, wsp = _out("ws", ws, dev, torch.uint8, (n,), q.device, stream)
     cache = (pages, P, Hk, D)
     _call("gdn_attn_decode", dev, p, qp, _arg("k_cache", k_cache, dev, dt, cache),
           _arg("v_cache", v_cache, dev, dt, cache),
@@ -1118,11 +1123,11 @@ def gdn_slot_map(ctx_len, new_len, free_pages, block_table, *, page_size, pages,
     n_free = free_pages.numel()
 
     d = ctx_len.device
-    seq_len, sp = _out("seq_len", seq_len, dev, i32, (B,), d)
-    cu_seqlens, cp = _out("cu_seqlens", cu_seqlens, dev, i32, (B + 1,), d)
-    positions, pp = _out("positions", positions, dev, i32, (n_tokens,), d)
-    slots, lp = _out("slots", slots, dev, i32, (n_tokens,), d)
-    used, up = _out("used", used, dev, i32, (1,), d)
+    seq_len, sp = _out("seq_len", seq_len, dev, i32, (B,), d, stream)
+    cu_seqlens, cp = _out("cu_seqlens", cu_seqlens, dev, i32, (B + 1,), d, stream)
+    positions, pp = _out("positions", positions, dev, i32, (n_tokens,), d, stream)
+    slots, lp = _out("slots", slots, dev, i32, (n_tokens,), d, stream)
+    used, up = _out("used", used, dev, i32, (1,), d, stream)
     p = SlotProblem(page_size, 0, B, blocks, pages, n_free, n_tokens)
     _call("gdn_slot_map", dev, p, _arg("ctx_len", ctx_len, dev, i32, (B,)),
           _arg("new_len", new_len, dev, i32, (B,)),

@@ -327,6 +327,25 @@ def test_calls_captured_behind_copies_memsets_and_other_streams():
         assert (busy == 2).all()
 
 
+def test_calls_on_a_given_stream():
+    """`stream` runs the call there, allocations included; many calls in a row keep their outputs."""
+    inp = attn_inputs([700, 90], 8, 2, 128, 16, BF, seed=23)
+    want = gdn.gdn_attn_decode(*inp)
+    rq, rk, _, wq, wk, f, _ = rope_inputs(200, 4, 2, 128, 64, BF, seed=24)
+    dy = torch.randn(200, 4, 128, device="cuda").to(BF), torch.ones(200, 2, 128, device="cuda").to(BF)
+    grads = gdn.gdn_qk_norm_rope_bwd(rq, rk, wq, wk, f, None, *dy)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = [(gdn.gdn_attn_decode(*inp, stream=side),
+            gdn.gdn_qk_norm_rope_bwd(rq, rk, wq, wk, f, None, *dy, stream=side))
+           for _ in range(20)]
+    filler = [torch.full((1 << 20,), 7.0, device="cuda") for _ in range(20)]
+    torch.cuda.synchronize()
+    for a, g in got:
+        assert all(torch.equal(x, y) for x, y in zip(a + g, want + grads))
+    assert all((x == 7).all() for x in filler)
+
+
 def test_attention_empty_batch():
     q, kc, vc, table, lens = attn_inputs([5], 8, 2, 128, 16, BF)
     o, lse = gdn.gdn_attn_decode(q[:0], kc, vc, table[:0], lens[:0])
