@@ -907,19 +907,18 @@ def _flat(name, t, dev, n):
 def _rows(name, t, dev, dtype, shape):
     """(address, elements between tokens; 0: contiguous) of [..., heads, D] whose rows of one
     token are contiguous and whose tokens are evenly spaced (a slice of a fused projection)."""
-    sh = t.shape
-    if t.get_device() != dev or t.dtype is not dtype or sh != shape:
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name}: expected a {dtype} tensor {list(shape)} on cuda:{dev}, got "
-                         f"{t.dtype} {list(sh)} on {t.device}")
+                         f"{t.dtype} {list(t.shape)} on {t.device}")
+    st = t.stride()
+    heads, D = shape[-2], shape[-1]
+    if len(st) == 3 and st[2] == 1 and st[1] == D and shape[0] > 1:
+        return t.data_ptr(), st[0]
     if t.is_contiguous():
         return t.data_ptr(), 0
-    st = t.stride()
-    if len(st) == 3 and st[2] == 1 and st[1] == sh[2] and sh[0] > 1:
-        return t.data_ptr(), st[0]
-    heads, D = sh[-2], sh[-1]
     ok = (st[-1] == 1 or D == 1) and (st[-2] == D or heads == 1)
     step, span = 0, 1
-    for n, s in zip(reversed(sh[:-2]), reversed(st[:-2])):
+    for n, s in zip(reversed(shape[:-2]), reversed(st[:-2])):
         if n == 1:
             continue
         if span == 1:
@@ -928,7 +927,7 @@ def _rows(name, t, dev, dtype, shape):
         span *= n
     if not ok:
         raise ValueError(f"{name}: the elements of a token have to be contiguous and the tokens "
-                         f"evenly spaced, got strides {list(st)} for {list(sh)}")
+                         f"evenly spaced, got strides {list(st)} for {list(shape)}")
     return t.data_ptr(), step
 
 
@@ -991,26 +990,31 @@ def gdn_step(q, k, v, a, b, A_log, dt_bias, state, slots=None, *, l2norm=True, e
 
 
 def _rope_problem(q, k, v, dev, inv_freq, T, interleaved, eps, rope_scale):
-    """(problem, addresses of q, k and v) for q [..., Hq, D], k, v [..., Hk, D]."""
-    lead, D = q.shape[:-2], q.shape[-1]
-    N = lead[0] if len(lead) == 1 else lead.numel()
-    Hq, Hk = q.shape[-2], k.shape[-2]
-    qp, qs = _rows("q", q, dev, q.dtype, q.shape)
-    kp, ks = _rows("k", k, dev, q.dtype, lead + (Hk, D))
-    vp, vs = (None, 0) if v is None else _rows("v", v, dev, q.dtype, lead + (Hk, D))
-    if T is None:
-        T = lead[-1] if len(lead) > 1 else 0
-    R = 2 * inv_freq.numel()
-    return RopeProblem(_dtype_code(q.dtype), D, R, 1 if interleaved else 0, N, T, Hq, Hk, qs, ks,
-                       vs, eps, rope_scale), qp, kp, vp
+    """(problem, addresses of q, k and v, shapes of q and k) for q [..., Hq, D], k, v [..., Hk,
+    D]."""
+    dt, sq, sk = q.dtype, q.shape, k.shape
+    Hq, D = sq[-2:]
+    Hk = sk[-2]
+    if len(sq) == 3:
+        N, lead = sq[0], sq[:1]
+    else:
+        lead = sq[:-2]
+        N = lead.numel()
+        if T is None:
+            T = lead[-1]
+    want = lead + (Hk, D)
+    qp, qs = _rows("q", q, dev, dt, sq)
+    kp, ks = _rows("k", k, dev, dt, want)
+    vp, vs = (None, 0) if v is None else _rows("v", v, dev, dt, want)
+    return RopeProblem(_dtype_code(dt), D, 2 * inv_freq.numel(), 1 if interleaved else 0, N,
+                       T or 0, Hq, Hk, qs, ks, vs, eps, rope_scale), qp, kp, vp, sq, sk
 
 
-def _rope_tables(wq, wk, inv_freq, positions, p, dev):
-    f32 = torch.float32
-    return (_arg("wq", wq, dev, f32, (p.D,)), _arg("wk", wk, dev, f32, (p.D,)),
-            _arg("inv_freq", inv_freq, dev, f32, (p.R // 2,)),
-            None if positions is None else
-            _flat("positions", positions, dev, p.N))
+def _rope_tables(wq, wk, inv_freq, positions, D, N, dev):
+    f32, w = torch.float32, (D,)
+    return (_arg("wq", wq, dev, f32, w), _arg("wk", wk, dev, f32, w),
+            _arg("inv_freq", inv_freq, dev, f32, (inv_freq.numel(),)),
+            None if positions is None else _flat("positions", positions, dev, N))
 
 
 def gdn_qk_norm_rope_fwd(q, k, wq, wk, inv_freq, positions=None, *, T=None, interleaved=False,
@@ -1020,11 +1024,13 @@ def gdn_qk_norm_rope_fwd(q, k, wq, wk, inv_freq, positions=None, *, T=None, inte
     positions int32, one per token; None: token n of q's [B, T, ...] is at n % T ([N, ...]:
     at n).  q and k may be slices of one projection.  Returns (q_out, k_out), contiguous."""
     dev, dt = _device_of(q), q.dtype
-    p, qp, kp, _ = _rope_problem(q, k, None, dev, inv_freq, T, interleaved, eps, rope_scale)
-    q_out, qo = _out("q_out", q_out, dev, dt, q.shape, q.device, stream)
-    k_out, ko = _out("k_out", k_out, dev, dt, k.shape, q.device, stream)
+    p, qp, kp, _, sq, sk = _rope_problem(q, k, None, dev, inv_freq, T, interleaved, eps,
+                                         rope_scale)
+    q_out, qo = _out("q_out", q_out, dev, dt, sq, q.device, stream)
+    k_out, ko = _out("k_out", k_out, dev, dt, sk, q.device, stream)
     _call("gdn_qk_norm_rope_fwd", dev, p, qp, kp,
-          *_rope_tables(wq, wk, inv_freq, positions, p, dev), qo, ko, _raw_stream(stream, dev))
+          *_rope_tables(wq, wk, inv_freq, positions, p.D, p.N, dev), qo, ko,
+          _raw_stream(stream, dev))
     return q_out, k_out
 
 
@@ -1040,16 +1046,17 @@ def gdn_qk_norm_rope_bwd(q, k, wq, wk, inv_freq, positions, dq_out, dk_out, *, T
                          dwk=None, ws=None, stream=None):
     """Backward of gdn_qk_norm_rope_fwd: (dq, dk contiguous in q's type, dwq, dwk [D] fp32)."""
     dev, dt, f32 = _device_of(q), q.dtype, torch.float32
-    p, qp, kp, _ = _rope_problem(q, k, None, dev, inv_freq, T, interleaved, eps, rope_scale)
-    dq, dqp = _out("dq", dq, dev, dt, q.shape, q.device, stream)
-    dk, dkp = _out("dk", dk, dev, dt, k.shape, q.device, stream)
+    p, qp, kp, _, sq, sk = _rope_problem(q, k, None, dev, inv_freq, T, interleaved, eps,
+                                         rope_scale)
+    dq, dqp = _out("dq", dq, dev, dt, sq, q.device, stream)
+    dk, dkp = _out("dk", dk, dev, dt, sk, q.device, stream)
     dwq, wqp = _out("dwq", dwq, dev, f32, (p.D,), q.device, stream)
     dwk, wkp = _out("dwk", dwk, dev, f32, (p.D,), q.device, stream)
     n = gdn_qk_norm_rope_bwd_workspace_size(p) if ws is None else ws.numel()
     ws, wsp = _out("ws", ws, dev, torch.uint8, (n,), q.device, stream)
     _call("gdn_qk_norm_rope_bwd", dev, p, qp, kp,
-          *_rope_tables(wq, wk, inv_freq, positions, p, dev),
-          _arg("dq_out", dq_out, dev, dt, q.shape), _arg("dk_out", dk_out, dev, dt, k.shape),
+          *_rope_tables(wq, wk, inv_freq, positions, p.D, p.N, dev),
+          _arg("dq_out", dq_out, dev, dt, sq), _arg("dk_out", dk_out, dev, dt, sk),
           dqp, dkp, wqp, wkp, wsp, n, _raw_stream(stream, dev))
     return dq, dk, dwq, dwk
 
@@ -1061,12 +1068,13 @@ def gdn_qk_norm_rope_cache(q, k, v, wq, wk, inv_freq, positions, slots, k_cache,
     (int32, one per token; -1: nowhere; the others have to differ) of k_cache, v_cache
     [pages, page_size, Hk, D].  Returns q_out."""
     dev, dt = _device_of(q), q.dtype
-    p, qp, kp, vp = _rope_problem(q, k, v, dev, inv_freq, T, interleaved, eps, rope_scale)
-    q_out, qo = _out("q_out", q_out, dev, dt, q.shape, q.device, stream)
+    p, qp, kp, vp, sq, _ = _rope_problem(q, k, v, dev, inv_freq, T, interleaved, eps, rope_scale)
+    N = p.N
+    q_out, qo = _out("q_out", q_out, dev, dt, sq, q.device, stream)
     cache = k_cache.shape[:-2] + (p.Hk, p.D)
     _call("gdn_qk_norm_rope_cache", dev, p, qp, kp, vp,
-          *_rope_tables(wq, wk, inv_freq, positions, p, dev), k_cache.shape[:-2].numel(),
-          _flat("slots", slots, dev, p.N), qo, _arg("k_cache", k_cache, dev, dt, cache),
+          *_rope_tables(wq, wk, inv_freq, positions, p.D, p.N, dev), k_cache.shape[:-2].numel(),
+          _flat("slots", slots, dev, N), qo, _arg("k_cache", k_cache, dev, dt, cache),
           _arg("v_cache", v_cache, dev, dt, cache), _status(status, dev),
           _raw_stream(stream, dev))
     return q_out

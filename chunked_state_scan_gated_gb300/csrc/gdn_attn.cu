@@ -6,12 +6,12 @@
 // Bound by HBM: every K and V row is read once.  A piece of work is (request, key head, range
 // of tokens); the query heads of a key head are the 8 columns of the products
 //   S^T [16 keys x 8 heads] = K [16 x D] Q^T,   O^T [D x 8] += V^T [D x 16 keys] P^T
-// so a group of 8 query heads fills mma.sync's tile (more than 8 per key head go 16 to a pass over the
-// cache, two products per fragment: 131001 tokens with 16 query heads to each of 8 key heads of
-// 128: 92 us against 158 in two passes) and K, V need no transposition: both are the products' A
-// operand, whose fragments are loaded from global memory straight into registers, 16 bytes per
-// lane.  That works because the contraction index of the first
-// product (the head's elements) and the output rows of the second may be permuted freely:
+// so a group of 8 query heads fills mma.sync's tile (more than 8 per key head go 16 to a pass over
+// the cache, two products per fragment: 131001 tokens with 16 query heads to each of 8 key heads
+// of 128: 92 us against 158 in two passes) and K, V need no transposition: both are the products'
+// A operand, whose fragments are loaded from global memory straight into registers, 16 bytes per
+// lane.  That works because the contraction index of the first product (the head's elements) and
+// the output rows of the second may be permuted freely:
 //   K: lane (g, t) = (lane / 4, lane % 4) loads 16-byte chunk t + 4c of key rows g and g + 8,
 //      and the 4 (2) words of a chunk serve 2 products, Q's fragment being the same chunk;
 //   V: the lane loads chunk g + 8c of the rows of the 4 keys of its fragment; the pairs of
@@ -46,12 +46,12 @@ constexpr int AT_NT = 32 * AT_W;
 constexpr int AT_G = 8;            // query heads per product
 constexpr int AT_SMS = 152;
 constexpr float AT_LAZY = 8.f;     // log2 units
-// What a piece costs beside its tiles, in units (its first loads and its end): without it a
-// CTA with many short requests lags (61 ragged requests 128 against 102 us; 2 to 5 units: the same).
+// What a piece costs beside its tiles, in units (its first loads and its end): without it a CTA
+// with many short requests lags (61 ragged requests 128 against 102 us; 2 to 5: the same).
 constexpr int AT_START = 1;
 
-// Keys per warp tile, CTAs per SM and parts, for NG groups of AT_G query heads per piece: the K and V
-// tiles and the accumulators of D x 8 NG fill most of a CTA's share of the registers.
+// Keys per warp tile, CTAs per SM and parts, for NG groups of AT_G query heads per piece: the K
+// and V tiles and the accumulators of D x 8 NG fill most of a CTA's share of the registers.
 // kParts > 1: the two tiles do not fit; they go by that many parts of D.
 template <int KEYS, int CTAS, int PARTS>
 struct Fit {
@@ -121,9 +121,9 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 // x = hi + lo with hi, lo in tf32: hi is x rounded to nearest (ties away), lo what is left, rounded
-// too (2^-23 of x).  SAFE: an infinite or NaN x, or one that hi's rounding could make infinite, goes
-// into lo alone, and mma_split<SAFE> multiplies lo only with the other operand's hi, so that no
-// 0 * inf arises beside the product itself.
+// too (2^-23 of x).  SAFE: an infinite or NaN x, or one that hi's rounding could make infinite,
+// goes into lo alone, and mma_split<SAFE> multiplies lo only with the other operand's hi, so that
+// no 0 * inf arises beside the product itself.
 template <bool SAFE>
 __device__ __forceinline__ void split_tf32(uint32_t x, uint32_t* hi, uint32_t* lo) {
   const uint32_t h = (x + 0x1000u) & 0xffffe000u;
@@ -173,8 +173,8 @@ template <int D, typename T, int NG> struct Smem {
 
 // What a warp keeps of its piece.
 template <int D, int NG> struct Acc {
-  float o[NG][D / 16][4];      // O^T tiles
-  float m[NG][2], l[NG][2];    // of heads 2t, 2t + 1: reference score (unscaled), this lane's part of the sum
+  float o[NG][D / 16][4];    // O^T tiles
+  float m[NG][2], l[NG][2];  // heads 2t, 2t + 1: reference score (unscaled), this lane's sum
 };
 
 // NK blocks of 16 keys by DP elements.
@@ -202,8 +202,8 @@ struct Block {
   int n;        // rows that count (0..16)
 };
 
-// s += the scores of NK blocks over one part of D, for heads 2t, 2t + 1 of the lane's rows g, g + 8;
-// qs points at the part in Q's rows.
+// s += the scores of NK blocks over one part of D, for heads 2t, 2t + 1 of the lane's rows g and
+// g + 8; qs points at the part in Q's rows.
 template <int D, int DP, int NK, int NG>
 __device__ __forceinline__ void scores(const Tile<DP, __nv_bfloat16, NK>& k, const char* qs,
                                        bool /*qplain*/, float (&s)[NG][NK][4]) {
@@ -799,8 +799,9 @@ __device__ __forceinline__ void add_scaled(float4& a, const float4& x, float f) 
 // query head and AJ_DC columns), 16 parts at a time; or, with up to AJ_FEW parts (a batch: hundreds
 // of pieces of 2 or 3), or up to 32 where the CTAs would have to take several items each, the
 // first of them does it alone, a warp per query head (517 tokens, 9 parts, 32 items: 9.4 us for
-// the whole call against 12.7 shared; 10 parts of 3 items: 13.4 shared, 14.3 alone).  The schedule is worked out again from the lengths, which the kernels in front of the pass wrote;
-// only then does the CTA wait for the pass.
+// the whole call against 12.7 shared; 10 parts of 3 items: 13.4 shared, 14.3 alone).  The schedule
+// is worked out again from the lengths, which the kernels in front of the pass wrote; only then
+// does the CTA wait for the pass.
 template <int D, typename T, int NG>
 __global__ void __launch_bounds__(AJ_NT) k_attn_join(AttnArgs ar) {
   constexpr int GP = AT_G * NG, NW = AJ_NT / 32, MAXC = AT_SMS * Cfg<D, T, NG>::kCtas;

@@ -10,8 +10,8 @@
 // Bound by HBM (2 row accesses forward, 3 backward).  A row is held 8 elements per lane (16 bytes
 // of bf16) by LPR = 8, 16 or 32 lanes, so a warp holds 32 / LPR heads at a time; a group is U such
 // sets, whose chains of shuffles are independent (32768 tokens of 18 heads of 256: 96 us with U =
-// 2, 107 with 1).  The groups of all tokens are divided evenly over one wave of warps, from a decode
-// step's few (each warp one group) to a training batch: no tail.  A warp streams its groups
+// 2, 107 with 1).  The groups of all tokens are divided evenly over one wave of warps, from a
+// decode step's few (each warp one group) to a training batch: no tail.  A warp streams its groups
 // through a ring of its own in shared memory (16-byte asynchronous copies) with warp barriers
 // only; a rotated element's partner in the other half is read from the ring.  The token's R/2
 // angles are computed once and folded with the weights:
@@ -128,7 +128,8 @@ __device__ __forceinline__ void get(const __nv_bfloat16* p, F2 (&v)[4]) {
     v[j] = f2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
 }
 __device__ __forceinline__ void get(const float* p, F2 (&v)[4]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *(reinterpret_cast<const float4*>(p) + 1);
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  const float4 b = *(reinterpret_cast<const float4*>(p) + 1);
   v[0] = f2(a.x, a.y);
   v[1] = f2(a.z, a.w);
   v[2] = f2(b.x, b.y);
@@ -311,14 +312,17 @@ struct Loader {
     h = run.i * U * RPL + lane / LPR;
     end = e < ar.D ? (run.kind == 0 ? ar.Hq : ar.Hk) : 0;
     const int64_t at = (int64_t)h * ar.D + e;
+    const int64_t n = run.n;
     if (run.kind == 0) {
-      p[0] = reinterpret_cast<const T*>(ar.q) + run.n * ar.qs + at;
-      if constexpr (NP == 2) p[1] = reinterpret_cast<const T*>(ar.dq_out) + (int64_t)run.n * ar.Hq * ar.D + at;
+      p[0] = reinterpret_cast<const T*>(ar.q) + n * ar.qs + at;
+      if constexpr (NP == 2)
+        p[1] = reinterpret_cast<const T*>(ar.dq_out) + n * ar.Hq * ar.D + at;
     } else if (NP == 2 || run.kind == 1) {
-      p[0] = reinterpret_cast<const T*>(ar.k) + run.n * ar.ks + at;
-      if constexpr (NP == 2) p[1] = reinterpret_cast<const T*>(ar.dk_out) + (int64_t)run.n * ar.Hk * ar.D + at;
+      p[0] = reinterpret_cast<const T*>(ar.k) + n * ar.ks + at;
+      if constexpr (NP == 2)
+        p[1] = reinterpret_cast<const T*>(ar.dk_out) + n * ar.Hk * ar.D + at;
     } else {
-      p[0] = reinterpret_cast<const T*>(ar.v) + run.n * ar.vs + at;
+      p[0] = reinterpret_cast<const T*>(ar.v) + n * ar.vs + at;
     }
   }
   __device__ __forceinline__ void issue(const RopeArgs& ar, const Share& sh, int stage) {
