@@ -72,7 +72,13 @@ template <> struct Cfg<128, float, 2> : Fit<16, 2, 2> {};
 template <> struct Cfg<256, float, 2> : Fit<16, 2, 4> {};
 
 // Parts of pieces in the workspace: slot 2c of CTA c is the piece that began before it, slot
-// 2c + 1 the one that goes on behind it.
+// 2c + 1 the one that goes on behind it.  Join c tells of the piece that goes on from CTA c to
+// CTA c + 1, if one does.
+struct __align__(16) Join {
+  int32_t b, h;         // request, piece of it
+  int32_t first, last;  // CTAs that it begins and ends in (last < 0: none goes on)
+};
+
 struct AttnArgs {
   int64_t B, Hq, Hk, pages, max_blocks, qs;
   int P, G, HG;   // tokens per page, query heads per key head, pieces of them
@@ -82,6 +88,7 @@ struct AttnArgs {
   const int32_t *table, *len;
   void* o;
   float* lse;
+  Join* join;     // [CTAs]
   float2* ml;     // [CTAs][2][AT_G NG] reference score (unscaled) and sum
   float* acc;     // [CTAs][2][AT_G NG][D]
   int32_t* status;
@@ -651,12 +658,12 @@ __device__ void finish(const AttnArgs& ar, char* smem, float2 (*ml)[AT_G], int64
   }
 }
 
-// How the work is divided, the same for every caller.  The units of request b are those of its
+// How the work is divided.  The units of request b are those of its
 // pieces (key head x AT_G NG query heads) in a row, each its CTA tiles behind AT_START; the
 // W units of all requests are divided over C CTAs, CTA c taking [W c / C, W (c + 1) / C).
 // Each warp finds its way by itself: a lane sums up a run of requests, one scan over the lanes.
-// AHEAD: read past the first-level cache, for a caller that has not waited for the kernel before it
-// (the lengths were written before that one began).
+// AHEAD: read past the first-level cache, for a caller that has not waited for the kernel before
+// it (the lengths were written before that one began).
 template <int D, typename T, int NG, bool AHEAD>
 struct Schedule {
   static constexpr int TK = Cfg<D, T, NG>::kKeys * AT_W;  // keys per CTA tile
@@ -743,6 +750,7 @@ __global__ void __launch_bounds__(AT_NT, Cfg<D, T, NG>::kCtas) k_attn_decode(Att
       if (ar.lse)
         for (int64_t i = tid; i < ar.Hq; i += AT_NT) ar.lse[b * ar.Hq + i] = -INFINITY;
     }
+  Join goes_on{0, 0, 0, -1};
   if (c < sc.C) {
     int64_t u = sc.first(c), b, r;
     const int64_t u1 = sc.first(c + 1);
@@ -758,6 +766,10 @@ __global__ void __launch_bounds__(AT_NT, Cfg<D, T, NG>::kCtas) k_attn_decode(Att
         piece<D, T, NG>(ar, smem, b, n, hk, hg, t0, t1, a, &bad);
         const int64_t slot = t0 == 0 && t1 == nt ? -1 : t0 == 0 ? 2 * c + 1 : 2 * c;
         finish<D, T, NG>(ar, smem, ml, b, hk * ar.G + hg * GP, heads, a, slot);
+        if (t1 < nt) {  // the share ends in this piece, whose tile 0 is unit u - r0 + AT_START
+          const int64_t tile0 = u - r0 + AT_START;
+          goes_on = Join{(int32_t)b, h, sc.cta_of(tile0), sc.cta_of(tile0 + nt - 1)};
+        }
       }
       u += r1 - r0;
       r0 = 0;
@@ -769,6 +781,7 @@ __global__ void __launch_bounds__(AT_NT, Cfg<D, T, NG>::kCtas) k_attn_decode(Att
       }
     }
   }
+  if (tid == 0) ar.join[c] = goes_on;
   if (bad && ar.status) atomicOr(ar.status, kStatusClamped);
 }
 
@@ -799,33 +812,39 @@ __device__ __forceinline__ void add_scaled(float4& a, const float4& x, float f) 
 // query head and AJ_DC columns), 16 parts at a time; or, with up to AJ_FEW parts (a batch: hundreds
 // of pieces of 2 or 3), or up to 32 where the CTAs would have to take several items each, the
 // first of them does it alone, a warp per query head (517 tokens, 9 parts, 32 items: 9.4 us for
-// the whole call against 12.7 shared; 10 parts of 3 items: 13.4 shared, 14.3 alone).  The schedule
-// is worked out again from the lengths, which the kernels in front of the pass wrote; only then
-// does the CTA wait for the pass.
+// the whole call against 12.7 shared; 10 parts of 3 items: 13.4 shared, 14.3 alone).  Which piece
+// it is, a CTA works out from the lengths while the pass still runs where one load per warp tells
+// them (the kernels in front of the pass wrote them; 8 requests of 1000 tokens 11.9 against 12.8
+// us); with more requests all CTAs together would wait for the same few lines of L2 (400 requests
+// of 100 tokens 102 us), and it reads what the pass wrote down (44 us).
 template <int D, typename T, int NG>
 __global__ void __launch_bounds__(AJ_NT) k_attn_join(AttnArgs ar) {
   constexpr int GP = AT_G * NG, NW = AJ_NT / 32, MAXC = AT_SMS * Cfg<D, T, NG>::kCtas;
   __shared__ float s_w[MAXC], s_red[NW][2];
   __shared__ float4 s_o[AJ_NT / 16][AJ_DC / 4];
   const int x = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const Schedule<D, T, NG, true> sc(ar, gridDim.x);
-  int64_t b = 0, r = 0;
-  int c = 0, last = 0, h = 0;  // first and last CTA of the piece
-  if (x < sc.C) {
-    const int64_t u = sc.first(x + 1) - 1;  // CTA x's last unit, in piece [start, start + w)
-    sc.find(u, &b, &r);
-    const int w = sc.tiles(sc.length(b)) + AT_START;
-    h = (int)(r / w);
-    const int64_t start = u - r % w;
-    c = sc.cta_of(start + AT_START);
-    last = sc.cta_of(start + w - 1);
+  Join j{0, 0, 0, -1};
+  if (ar.B <= 32) {
+    const Schedule<D, T, NG, true> sc(ar, gridDim.x);
+    if (x < sc.C) {
+      int64_t b, r;
+      const int64_t u = sc.first(x + 1) - 1;  // CTA x's last unit, in piece [start, start + w)
+      sc.find(u, &b, &r);
+      const int w = sc.tiles(sc.length(b)) + AT_START;
+      const int64_t tile0 = u - r % w + AT_START;
+      j = Join{(int32_t)b, (int32_t)(r / w), sc.cta_of(tile0), sc.cta_of(tile0 + w - AT_START - 1)};
+    }
+    after_previous();
+    if (x < j.first || x >= j.last) return;
+  } else {
+    after_previous();
+    j = ar.join[x];
+    if (j.last < 0) return;
   }
-  const int hk = h / ar.HG, hg = h % ar.HG, heads = min(GP, ar.G - hg * GP);
-  const int64_t row0 = b * ar.Hq + hk * ar.G + hg * GP;
-  const int n = last - c + 1;
-  after_previous();
   before_next();
-  if (x < c || x >= last) return;
+  const int c = j.first, n = j.last - c + 1;
+  const int hk = j.h / ar.HG, hg = j.h % ar.HG, heads = min(GP, ar.G - hg * GP);
+  const int64_t row0 = (int64_t)j.b * ar.Hq + hk * ar.G + hg * GP;
   // parts: slot 2c + 1 of the piece's first CTA c, slot 2i of the CTAs behind it
   if (n <= AJ_FEW || (n <= 32 && heads * (D / AJ_DC) > n - 1)) {
     if (x > c) return;
@@ -932,14 +951,15 @@ gdn_status check_problem(const gdn_attn_problem* p) {
 // depend on the device).
 struct Plan {
   int ctas;
-  size_t acc, total;
+  size_t ml, acc, total;
 };
 template <int D, typename T, int NG>
 Plan plan_of() {
   Plan pl;
   pl.ctas = AT_SMS * Cfg<D, T, NG>::kCtas;
   const size_t parts = (size_t)pl.ctas * 2 * AT_G * NG;
-  pl.acc = (parts * sizeof(float2) + 255) & ~(size_t)255;
+  pl.ml = (pl.ctas * sizeof(Join) + 255) & ~(size_t)255;
+  pl.acc = pl.ml + ((parts * sizeof(float2) + 255) & ~(size_t)255);
   pl.total = pl.acc + parts * D * sizeof(float);
   return pl;
 }
@@ -966,7 +986,8 @@ template <int D, typename T, int NG>
 cudaError_t launch(AttnArgs ar, char* ws, cudaStream_t st) {
   const Plan pl = plan_of<D, T, NG>();
   ar.HG = (ar.G + AT_G * NG - 1) / (AT_G * NG);
-  ar.ml = (float2*)ws;
+  ar.join = (Join*)ws;
+  ar.ml = (float2*)(ws + pl.ml);
   ar.acc = (float*)(ws + pl.acc);
   const cudaError_t e = launch_behind(k_attn_decode<D, T, NG>, dim3(pl.ctas), AT_NT,
                                       Smem<D, T, NG>::kBytes, st, ar);
