@@ -18,7 +18,7 @@
 //   y = r (x (w c) + xp (w_p s)),  xp the partner elements, s with the sign of the pair's side
 // and the arithmetic is packed two fp32 numbers at a time (237 instructions per row without
 // either, 113 now).  Measured: forward of those 32768 tokens 96 us (6.3 TB/s), backward of 16001
-// tokens of 40 heads of 128 85 us (5.8 TB/s).  Two CTAs of 8 warps per SM with 4 KB in flight per
+// tokens of 40 heads of 128 80 us (6.1 TB/s).  Two CTAs of 8 warps per SM with 4 KB in flight per
 // warp are the best of 2 to 4 CTAs and 4 to 16 KB (3 CTAs: 108 us; 8 KB: 100 us).
 #include <cuda_bf16.h>
 #include <math.h>
@@ -480,8 +480,9 @@ __global__ void __launch_bounds__(RO_NT, 2) k_qk_norm_rope_bwd(RopeArgs ar) {
   const int groups = ar.gq + ar.gk;
   const int other = INTER ? 0 : other_lane(ar, e);
   const int mine = lane * 8, theirs = (lane / LPR * LPR + other) * 8;
+  // No before_next(): with the sums' CTAs placed early a call of more than about 150 CTAs took 5 us
+  // longer (16001 tokens, 32 + 8 heads of 128: 85.2 against 80.3 us); smaller ones take the same.
   after_previous();
-  before_next();
   F2 dw[2][4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) dw[0][j] = dw[1][j] = f2(0.f, 0.f);
@@ -507,7 +508,7 @@ __global__ void __launch_bounds__(RO_NT, 2) k_qk_norm_rope_bwd(RopeArgs ar) {
         turn<INTER>(ar, cs, e, -1.f, C, S);
       }
       const int kind = run.kind;
-    const unsigned count = min((unsigned)run.left, left);
+      const unsigned count = min((unsigned)run.left, left);
       left -= count;
       float wv[8] = {};
       if (e < ar.D) ld8((kind == 0 ? ar.wq : ar.wk) + e, wv);
