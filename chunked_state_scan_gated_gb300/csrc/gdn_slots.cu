@@ -173,7 +173,8 @@ extern "C" gdn_status gdn_slot_map(const gdn_slot_problem* p, const int32_t* ctx
   if (!ok4(ctx_len, p->B) || !ok4(new_len, p->B) || !ok4(free_pages, p->n_free) ||
       !ok4(block_table, p->B * p->max_blocks) || !ok4(seq_len, p->B) || !ok4(cu_seqlens, 1) ||
       !ok4(positions, p->n_tokens) || !ok4(slots, p->n_tokens) || !ok4(used, 1) ||
-      ((uintptr_t)status & 255u) != 0)
+      ((uintptr_t)status & 255u) != 0 ||
+      (p->B > 0 && (seq_len == ctx_len || seq_len == new_len)))  // CTAs read them as others write
     return GDN_ERR_INVALID_ARG;
   SlotArgs ar;
   memset(&ar, 0, sizeof(ar));

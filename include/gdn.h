@@ -614,8 +614,9 @@ gdn_status gdn_qk_norm_rope_cache(const gdn_rope_problem* p, const void* q, cons
  * The split is chosen on the device from seq_len (the host reads nothing) and depends on the
  * lengths alone: deterministic.  Two launches.
  * Errors: null or misaligned pointer, sizes < 0, Hq % Hk != 0, q_stride < Hq D or no multiple
- * of 16 bytes, a scale that is not finite: GDN_ERR_INVALID_ARG; D other than 64, 128 or 256, page_size no multiple of 16,
- * pages page_size or max_blocks page_size >= 2^31, B Hq >= 2^31: GDN_ERR_UNSUPPORTED.
+ * of 16 bytes, a scale that is not finite: GDN_ERR_INVALID_ARG; D other than 64, 128 or 256,
+ * page_size no multiple of 16, pages page_size or max_blocks page_size >= 2^31, B Hq >= 2^31:
+ * GDN_ERR_UNSUPPORTED.
  */
 typedef struct gdn_attn_problem {
   int32_t dtype;      /* GDN_BF16 or GDN_FP32: q, both caches, o */
@@ -650,8 +651,9 @@ gdn_status gdn_attn_decode(const gdn_attn_problem* p, const void* q, const void*
  * outside [0, pages).  That, a negative length (taken as 0) and packed tokens past n_tokens
  * (dropped) are recorded in `status`; seq_len stops at max_blocks page_size.  One launch, no
  * workspace; all outputs int32.
- * Errors: null or misaligned pointer, sizes < 0, page_size < 1: GDN_ERR_INVALID_ARG;
- * pages page_size, max_blocks page_size, n_tokens, n_free or B >= 2^31: GDN_ERR_UNSUPPORTED.
+ * Errors: null or misaligned pointer, sizes < 0, page_size < 1, seq_len that is ctx_len or
+ * new_len: GDN_ERR_INVALID_ARG; pages page_size, max_blocks page_size, n_tokens, n_free or
+ * B >= 2^31: GDN_ERR_UNSUPPORTED.
  */
 typedef struct gdn_slot_problem {
   int32_t page_size;  /* tokens per page, >= 1 */

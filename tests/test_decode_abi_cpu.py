@@ -214,6 +214,11 @@ def test_slot_map_pointer_refusals(lib):
             assert slot_map(lib, **{k: None}) == BAD
 
 
+def test_slot_map_lengths_in_place_are_refused(lib):
+    assert slot_map(lib, ctx_len=2 * A, seq_len=2 * A) == BAD
+    assert slot_map(lib, new_len=2 * A, seq_len=2 * A) == BAD
+
+
 def test_binding_refuses_host_tensors_and_wrong_layouts():
     """The binding's own checks, on the CPU: no address reaches the library."""
     q, k = torch.zeros(3, 4, 64), torch.zeros(3, 2, 64)
