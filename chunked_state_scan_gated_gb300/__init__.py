@@ -912,7 +912,7 @@ def _rows(name, t, dev, dtype, shape):
                          f"{t.dtype} {list(t.shape)} on {t.device}")
     st = t.stride()
     heads, D = shape[-2], shape[-1]
-    if len(st) == 3 and st[2] == 1 and st[1] == D and shape[0] > 1:
+    if len(st) == 3 and st[2] == 1 and st[1] == D and shape[0] > 1 and st[0] > 0:
         return t.data_ptr(), st[0]
     if t.is_contiguous():
         return t.data_ptr(), 0
@@ -923,7 +923,7 @@ def _rows(name, t, dev, dtype, shape):
             continue
         if span == 1:
             step = s
-        ok = ok and s == step * span
+        ok = ok and s == step * span and s > 0  # 0: one token expanded
         span *= n
     if not ok:
         raise ValueError(f"{name}: the elements of a token have to be contiguous and the tokens "
@@ -1000,7 +1000,7 @@ def _rope_problem(q, k, v, dev, inv_freq, T, interleaved, eps, rope_scale):
     else:
         lead = sq[:-2]
         N = lead.numel()
-        if T is None:
+        if T is None and lead:
             T = lead[-1]
     want = lead + (Hk, D)
     qp, qs = _rows("q", q, dev, dt, sq)

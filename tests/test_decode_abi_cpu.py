@@ -242,3 +242,19 @@ def test_binding_refuses_host_tensors_and_wrong_layouts():
     for bad in (x[:, :2, 2:6], x[:, :, ::2], x[..., ::2], x.transpose(1, 2)):
         with pytest.raises(ValueError):
             gdn._rows("q", bad, -1, torch.float32, bad.shape)
+
+
+def test_binding_refuses_an_expanded_token():
+    """A stride of zero between tokens is no layout of the library's (its 0 means contiguous)."""
+    x = torch.zeros(1, 4, 64)
+    for bad in (x.expand(5, 4, 64), x.expand(2, 5, 4, 64), x[:, :2].expand(5, 2, 64),
+                torch.zeros(1, 1, 4, 64).expand(6, 1, 4, 64), torch.zeros(5, 1, 64).expand(5, 4, 64)):
+        with pytest.raises(ValueError):
+            gdn._rows("q", bad, -1, torch.float32, bad.shape)
+    assert gdn._rows("q", x, -1, torch.float32, (1, 4, 64))[1] == 0
+
+
+def test_binding_takes_one_token_without_leading_sizes():
+    q, k = torch.zeros(4, 64), torch.zeros(2, 64)
+    p = gdn._rope_problem(q, k, None, -1, torch.zeros(8), None, False, 1e-6, 1.0)[0]
+    assert (p.N, p.T, p.Hq, p.Hk, p.D, p.q_stride) == (1, 0, 4, 2, 64, 0)

@@ -497,6 +497,23 @@ def test_rope_positions_of_batch_rows_and_contiguous_inputs():
                    (pos - 5).reshape(-1).cpu().numpy(), f, False, BF)
 
 
+def test_rope_of_one_token_without_leading_sizes():
+    gen = torch.Generator().manual_seed(8)
+    q, k, w = rand(gen, (4, 64), BF), rand(gen, (2, 64), BF), torch.ones(64, device="cuda")
+    f, pos = torch.ones(8, device="cuda"), torch.full((1,), 9, dtype=torch.int32, device="cuda")
+    for p in (None, pos):
+        a = gdn.gdn_qk_norm_rope_fwd(q, k, w, w, f, p)
+        b = gdn.gdn_qk_norm_rope_fwd(q[None], k[None], w, w, f, p)
+        for x, y in zip(a, b):
+            assert torch.equal(x, y[0])
+
+
+def test_attention_refuses_one_query_row_expanded():
+    q, kc, vc, table, lens = attn_inputs([30, 5], 8, 2, 128, 16, BF, seed=16)
+    with pytest.raises(ValueError):
+        gdn.gdn_attn_decode(q[:1].expand(2, 8, 128), kc, vc, table, lens)
+
+
 def test_rope_zero_rows_and_one_kind_of_heads():
     """A zero row normalises to zero (and its gradient stays finite); Hk = 0, Hq = 0 and N = 0."""
     w, f = torch.ones(64, device="cuda"), torch.ones(8, device="cuda")
