@@ -408,44 +408,66 @@ __device__ __forceinline__ void load_v(Tile<DP, T, NK>& v, const T* base, const 
   else load_v<false>(v, base, blk, row);
 }
 
+// Q of `heads` query heads from q on, to shared memory (fp32: split).  Returns the sum of probe()s.
+template <int D, typename T, int NG>
+__device__ __forceinline__ uint64_t stage_q(char* smem, const T* q, int heads) {
+  constexpr int EL = 16 / (int)sizeof(T), ROW = D / EL, N = AT_G * NG * ROW;  // 16-byte chunks
+  constexpr int kRow = Smem<D, T, NG>::kRow;
+  uint64_t acc = 0;
+  if constexpr (sizeof(T) == 2 && NG == 1) {
+    constexpr int PER = (N + AT_NT - 1) / AT_NT;  // all loads at once, before the barrier
+    uint4 x[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int i = threadIdx.x + j * AT_NT;
+      x[j] = make_uint4(0, 0, 0, 0);
+      if (i / ROW < heads) x[j] = *reinterpret_cast<const uint4*>(q + (int64_t)i * EL);
+    }
+    __syncthreads();  // other warps may still read what was there
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int i = threadIdx.x + j * AT_NT;
+      if (i < N) *reinterpret_cast<uint4*>(smem + i / ROW * kRow + i % ROW * 16) = x[j];
+    }
+  } else {
+    __syncthreads();
+    for (int i = threadIdx.x; i < N; i += AT_NT) {
+      uint4 x = make_uint4(0, 0, 0, 0), hi, lo;
+      if (i / ROW < heads) x = *reinterpret_cast<const uint4*>(q + (int64_t)i * EL);
+      char* dst = smem + i / ROW * kRow + i % ROW * 16;
+      if constexpr (sizeof(T) == 4) {
+        probe(x, &acc);
+        split_tf32<true>(x.x, &hi.x, &lo.x);
+        split_tf32<true>(x.y, &hi.y, &lo.y);
+        split_tf32<true>(x.z, &hi.z, &lo.z);
+        split_tf32<true>(x.w, &hi.w, &lo.w);
+        *reinterpret_cast<uint4*>(dst) = hi;
+        *reinterpret_cast<uint4*>(dst + AT_G * NG * kRow) = lo;
+      } else {
+        *reinterpret_cast<uint4*>(dst) = x;
+      }
+    }
+  }
+  return acc;
+}
+
 // Tokens [0, n) of request b, units [t0, t1) of CTA tiles.
 template <int D, typename T, int NG>
 __device__ void piece(const AttnArgs& ar, char* smem, int64_t b, int n, int hk, int hg, int t0,
                       int t1, Acc<D, NG>& a, int* bad) {
-  constexpr int GP = AT_G * NG, KT = Cfg<D, T, NG>::kKeys, NK = KT / 16, EL = 16 / (int)sizeof(T);
-  constexpr int kRow = Smem<D, T, NG>::kRow;
+  constexpr int GP = AT_G * NG, KT = Cfg<D, T, NG>::kKeys, NK = KT / 16;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2;
   const int heads = min(GP, ar.G - hg * GP);
-  // Q (the barrier in front: other warps may still read what was there)
-  __syncthreads();
-  const T* q = reinterpret_cast<const T*>(ar.q) + b * ar.qs + ((int64_t)hk * ar.G + hg * GP) * D;
+  // Q goes to shared memory with the numbers of the first pages on their way where the registers
+  // allow it (517 tokens, 16 on 2 heads of 256: 8.5 us against 9.0; 400 requests of 50 to 150: 31.1
+  // against 33.1; the others spill), in front of everything else where not.  Its address is worked
+  // out there and not before: kept meanwhile, it costs D = 128 a twentieth.
+  constexpr bool kEarly = sizeof(T) == 2 && NG == 1;
+  auto queries = [&]() {
+    return reinterpret_cast<const T*>(ar.q) + b * ar.qs + ((int64_t)hk * ar.G + hg * GP) * D;
+  };
   uint64_t qacc = 0;
-  for (int i = threadIdx.x; i < GP * D / EL; i += AT_NT) {
-    const int h = i / (D / EL), c = i % (D / EL);
-    uint4 x = make_uint4(0, 0, 0, 0);
-    if (h < heads) x = *reinterpret_cast<const uint4*>(q + (int64_t)h * D + c * EL);
-    char* dst = smem + h * kRow + c * 16;
-    if constexpr (sizeof(T) == 4) {
-      uint4 hi, lo;
-      probe(x, &qacc);
-      split_tf32<true>(x.x, &hi.x, &lo.x);
-      split_tf32<true>(x.y, &hi.y, &lo.y);
-      split_tf32<true>(x.z, &hi.z, &lo.z);
-      split_tf32<true>(x.w, &hi.w, &lo.w);
-      *reinterpret_cast<uint4*>(dst) = hi;
-      *reinterpret_cast<uint4*>(dst + GP * kRow) = lo;
-    } else {
-      *reinterpret_cast<uint4*>(dst) = x;
-    }
-  }
-#pragma unroll
-  for (int q = 0; q < NG; ++q) {
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i)
-      a.o[q][i][0] = a.o[q][i][1] = a.o[q][i][2] = a.o[q][i][3] = 0.f;
-    a.m[q][0] = a.m[q][1] = -INFINITY;
-    a.l[q][0] = a.l[q][1] = 0.f;
-  }
+  if constexpr (!kEarly) qacc = stage_q<D, T, NG>(smem, queries(), heads);
   constexpr int kParts = Cfg<D, T, NG>::kParts, DP = D / kParts;
   const int64_t row = ar.Hk * D;  // elements between a page's rows
   const T* kc = reinterpret_cast<const T*>(ar.kc) + (int64_t)hk * D;
@@ -496,9 +518,18 @@ __device__ void piece(const AttnArgs& ar, char* smem, int64_t b, int n, int hk, 
   Tile<DP, T, NK> k, v;
   Block cur[NK];
   look_up();
+  if constexpr (kEarly) stage_q<D, T, NG>(smem, queries(), heads);
   bool full = place(cur);
   load_k(k, kc, cur, row, full);
   if constexpr (kParts == 1) load_v(v, vc, cur, row, full);
+#pragma unroll
+  for (int q = 0; q < NG; ++q) {
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+      a.o[q][i][0] = a.o[q][i][1] = a.o[q][i][2] = a.o[q][i][3] = 0.f;
+    a.m[q][0] = a.m[q][1] = -INFINITY;
+    a.l[q][0] = a.l[q][1] = 0.f;
+  }
   look_up();
   // Q is there; fp32: whether all of it is finite
   const bool qplain = __syncthreads_and(sizeof(T) == 2 || plain(qacc));
