@@ -8,7 +8,7 @@
 //   S^T [16 keys x 8 heads] = K [16 x D] Q^T,   O^T [D x 8] += V^T [D x 16 keys] P^T
 // so a group of 8 query heads fills mma.sync's tile (more than 8 per key head go 16 to a pass over
 // the cache, two products per fragment: 131001 tokens with 16 query heads to each of 8 key heads
-// of 128: 92 us against 158 in two passes) and K, V need no transposition: both are the products'
+// of 128: 94 us against 158 in two passes) and K, V need no transposition: both are the products'
 // A operand, whose fragments are loaded from global memory straight into registers, 16 bytes per
 // lane.  That works because the contraction index of the first product (the head's elements) and
 // the output rows of the second may be permuted freely:
@@ -17,7 +17,9 @@
 //   V: the lane loads chunk g + 8c of the rows of the 4 keys of its fragment; the pairs of
 //      keys are put together with byte permutes.
 // P^T comes out of the first product transposed (keys by heads) and is turned with movmatrix
-// (bf16) or shuffles (fp32).  No shared memory, barrier or copy wait is on the path of the
+// (bf16) or shuffles (fp32).  On bf16 the weights go into V's product as two bf16 terms each, so
+// that o has no rounding but its own (one term: 2^-9 of a weight, a third more error in o; two
+// cost 0 to 4% of the time, the tensor pipe being far from full).  No shared memory, barrier or copy wait is on the path of the
 // data: a warp's next K tile is on its way while it does the softmax and V's product, and the
 // next V tile during the next K product; 8 to 16 such warps per SM keep 64 to 128 KB in flight.
 // fp32 caches use tf32 products of the two-term split x = hi + lo (2^-23 of x; all four products),
@@ -122,10 +124,22 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// volatile: kept in place, or the weights of several blocks are turned early and spill what they
+// displace (12 or 16 query heads on 2 of 256: 336 us against 295; 517 tokens 9.5 against 9.0)
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
+}
+// Two weights (at least 0, or NaN) as sums hi + lo of bf16 numbers, x in the low halves: hi is cut
+// off and lo, what is left, rounded (2^-15 of the weight).  lo is not zero where hi is not, so that
+// an infinite v gives the infinity that hi v is, not 0 * inf beside it.
+__device__ __forceinline__ void split_bf16(float x, float y, uint32_t* hi, uint32_t* lo) {
+  const uint32_t a = __float_as_uint(x), b = __float_as_uint(y), h = __byte_perm(a, b, 0x7632);
+  const __nv_bfloat162 l = __floats2bfloat162_rn(x - __uint_as_float(a & 0xffff0000u),
+                                                 y - __uint_as_float(b & 0xffff0000u));
+  *hi = h;
+  *lo = __vmaxu2(*reinterpret_cast<const uint32_t*>(&l), __vminu2(h, 0x00010001u));
 }
 // x = hi + lo with hi, lo in tf32: hi is x rounded to nearest (ties away), lo what is left, rounded
 // too (2^-23 of x).  SAFE: an infinite or NaN x, or one that hi's rounding could make infinite,
@@ -288,14 +302,15 @@ __device__ __forceinline__ void weigh(const Tile<DP, __nv_bfloat16, NK>& v,
                                       const float (&p)[NG][NK][4], Acc<D, NG>& a, int part) {
 #pragma unroll
   for (int i = 0; i < NK; ++i) {
-    uint32_t b0[NG], b1[NG];
+    uint32_t h0[NG], h1[NG], l0[NG], l1[NG];
 #pragma unroll
     for (int q = 0; q < NG; ++q) {
-      // the weights' one rounding: half a bf16 step each, of random sign over the keys
-      const __nv_bfloat162 p0 = __floats2bfloat162_rn(p[q][i][0], p[q][i][1]);
-      const __nv_bfloat162 p1 = __floats2bfloat162_rn(p[q][i][2], p[q][i][3]);
-      b0[q] = transpose8x8(*reinterpret_cast<const uint32_t*>(&p0));
-      b1[q] = transpose8x8(*reinterpret_cast<const uint32_t*>(&p1));
+      split_bf16(p[q][i][0], p[q][i][1], &h0[q], &l0[q]);
+      split_bf16(p[q][i][2], p[q][i][3], &h1[q], &l1[q]);
+      h0[q] = transpose8x8(h0[q]);
+      h1[q] = transpose8x8(h1[q]);
+      l0[q] = transpose8x8(l0[q]);
+      l1[q] = transpose8x8(l1[q]);
     }
 #pragma unroll
     for (int c = 0; c < DP / 64; ++c)
@@ -306,8 +321,10 @@ __device__ __forceinline__ void weigh(const Tile<DP, __nv_bfloat16, NK>& v,
         const uint32_t a0 = __byte_perm(x0, x1, 0x5410), a1 = __byte_perm(x0, x1, 0x7632);
         const uint32_t a2 = __byte_perm(x2, x3, 0x5410), a3 = __byte_perm(x2, x3, 0x7632);
 #pragma unroll
-        for (int q = 0; q < NG; ++q)
-          mma_bf16(a.o[q][part * (DP / 16) + c * 4 + w], a0, a1, a2, a3, b0[q], b1[q]);
+        for (int q = 0; q < NG; ++q) {
+          mma_bf16(a.o[q][part * (DP / 16) + c * 4 + w], a0, a1, a2, a3, l0[q], l1[q]);
+          mma_bf16(a.o[q][part * (DP / 16) + c * 4 + w], a0, a1, a2, a3, h0[q], h1[q]);
+        }
       }
   }
 }

@@ -605,7 +605,7 @@ gdn_status gdn_qk_norm_rope_cache(const gdn_rope_problem* p, const void* q, cons
  * o [B,Hq,D] in p->dtype; lse [B,Hq] fp32, nullable.  seq_len[b] = 0: o = 0, lse = -inf.
  * Cache rows past seq_len are never used, whatever they hold.  Entries of block_table behind
  * the last used page are not read.  fp32 sums and softmax; on bf16 the weights exp(s_j - m)
- * are rounded to bf16 for their product with v, and lse is taken before that rounding.
+ * go into their product with v as sums of two bf16 numbers (2^-15 of a weight).
  *  - seq_len int32 [B]; a length outside [0, max_blocks page_size] is clamped, a used page
  *    outside [0, pages) has its tokens left out; both are recorded in `status`.
  *  - Workspace: gdn_attn_decode_workspace_size, 256-byte aligned: the pieces of requests whose
