@@ -567,12 +567,13 @@ __global__ void __launch_bounds__(RO_NT, 2) k_qk_norm_rope_bwd(RopeArgs ar) {
           }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const float f = rsqrtf(fmaf(ss[u], ar.inv_d, ar.eps));
+          // places past the last head hold zeros: 0 for them, not the 1 / 0 of eps = 0
+          const float f = h + u * RPL < heads ? rsqrtf(fmaf(ss[u], ar.inv_d, ar.eps)) : 0.f;
           const float m = -(dot[u] * ar.inv_d) * f * f * f;
           const F2 ff = f2(f, f), mm = f2(m, m);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            d[j] = fma(t[u][j], ff, d[j]);  // lanes without a head hold zeros
+            d[j] = fma(t[u][j], ff, d[j]);  // zero for lanes without a head
             g[u][j] = fma(x[u][j], mm, mul(g[u][j], ff));
           }
           if (h + u * RPL < end) put(out + u * RPL * ar.D, g[u]);

@@ -1,11 +1,14 @@
 """GPU tests of the decode-step calls at places where a definition is easily missed: softmax weights
-that a short type cannot hold, infinite values.  Bounds are counted as in test_decode_gpu.py."""
+that a short type cannot hold, infinite values, an epsilon of zero or
+above the rows' size.  Bounds are counted as in test_decode_gpu.py."""
 import numpy as np
 import pytest
 import torch
 
 import chunked_state_scan_gated_gb300 as gdn
-from test_decode_gpu import BF, F32, U, attn_inputs, half, n64, within
+from oracle import decode
+from test_decode_gpu import (BF, F32, U, angle_err, attn_inputs, half, n64, rand, rope_inputs, terms,
+                             within)
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +80,52 @@ def test_attention_infinite_and_largest_values(dt, D, Hq, n):
         o, _ = gdn.gdn_attn_decode(q, kc, vc, table, lens)
         within("o", o[0], np.full((Hq, D), 3.0),
                3 * (half(dt) + (n + 16) * 2.0 ** -22 + 2.0 ** -20))
+
+
+# ------------------------------------------------------------------ norm + rotation
+
+# A lane adds the rows of its warp's groups one after another: at most 2 tokens of 9 groups and a
+# part of a token's in the cases here; then 2 or 4 lanes, 8 warps; the CTAs' partials in fp64.
+CHAIN = 64
+
+
+def norm_bounds(x, w, f, inter, eps, angle):
+    """(|n| of each rotated pair, its relative error) as check_rows of test_decode_gpu.py."""
+    n = x / np.sqrt(np.mean(x * x, -1, keepdims=True) + eps) * w
+    return terms(n, inter, 2 * len(f)), 20 * U + angle
+
+
+EPS = [(3, 3, 1, 64, 32, BF), (50, 5, 2, 64, 64, F32), (7, 1, 3, 128, 0, BF), (300, 7, 5, 128, 64, F32),
+       (40, 3, 1, 256, 64, BF), (21, 9, 2, 80, 32, F32), (9, 1, 1, 8, 0, F32)]
+
+
+@pytest.mark.parametrize("eps", [0.0, 0.1, 30.0])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("case", EPS, ids=["x".join(map(str, c[:5])) + (
+    "_bf16" if c[5] == BF else "_f32") for c in EPS])
+def test_rope_epsilon(case, inter, eps):
+    """Forward and backward with an epsilon of zero (rows are not zero; the warp's places past the
+    last head are) and with some that change the result."""
+    N, Hq, Hk, D, R, dt = case
+    q, k, _, wq, wk, f, _ = rope_inputs(N, Hq, Hk, D, R, dt, seed=33)
+    gen = torch.Generator().manual_seed(34)
+    dyq, dyk = rand(gen, (N, Hq, D), dt), rand(gen, (N, Hk, D), dt)
+    eps32 = float(np.float32(eps))
+    t = np.arange(N)
+    yq, yk = gdn.gdn_qk_norm_rope_fwd(q, k, wq, wk, f, interleaved=inter, eps=eps)
+    dq, dk, dwq, dwk = gdn.gdn_qk_norm_rope_bwd(q, k, wq, wk, f, None, dyq, dyk, interleaved=inter,
+                                                eps=eps)
+    ang = angle_err(t, n64(f))
+    for name, x, w, y, dy, dx, dw in (("q", q, wq, yq, dyq, dq, dwq), ("k", k, wk, yk, dyk, dk, dwk)):
+        x, w, dy = n64(x), n64(w), n64(dy)
+        ref = decode.norm_rope_fwd(x, w, t, n64(f), inter, eps=eps32)
+        A, e = norm_bounds(x, w, f, inter, eps32, ang)
+        within(name, y, ref, half(dt) * np.abs(ref) + A * e * (1 + half(dt)))
+        rdx, rdw = decode.norm_rope_bwd(x, w, t, n64(f), dy, inter, eps=eps32)
+        r = 1 / np.sqrt(np.mean(x * x, -1, keepdims=True) + eps32)
+        A, xr = terms(dy, inter, R), np.abs(x * r)
+        e = 40 * U + ang
+        tol = e * r * (A * np.abs(w) + xr * np.mean(A * np.abs(w) * xr, -1, keepdims=True))
+        within("d" + name, dx, rdx, half(dt) * np.abs(rdx) + tol * (1 + half(dt)))
+        tol = ((e + (CHAIN + 16) * U) * A * xr).sum((0, 1))
+        within("dw" + name, dw, rdw, tol + U * np.abs(rdw))
