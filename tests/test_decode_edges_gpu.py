@@ -1,6 +1,7 @@
 """GPU tests of the decode-step calls at places where a definition is easily missed: softmax weights
-that a short type cannot hold, infinite values, an epsilon of zero or
-above the rows' size.  Bounds are counted as in test_decode_gpu.py."""
+that a short type cannot hold, infinite values, fp32 accuracy in the norm, an epsilon of zero or
+above the rows' size, weight gradients that lose or double a token.  Bounds are counted as in
+test_decode_gpu.py."""
 import numpy as np
 import pytest
 import torch
@@ -82,6 +83,28 @@ def test_attention_infinite_and_largest_values(dt, D, Hq, n):
                3 * (half(dt) + (n + 16) * 2.0 ** -22 + 2.0 ** -20))
 
 
+FP32 = [([65], 8, 1, 64), ([3000], 8, 2, 64), ([3000], 12, 1, 64), ([65], 8, 1, 128),
+        ([5000, 70], 4, 2, 128), ([3000], 40, 2, 128), ([65], 8, 1, 256), ([5000, 70], 6, 2, 256),
+        ([3000], 16, 1, 256), ([700, 1, 90], 26, 2, 256)]
+
+
+@pytest.mark.parametrize("lens,Hq,Hk,D", FP32)
+def test_attention_fp32_accuracy_in_the_norm(lens, Hq, Hk, D):
+    """Two-term splits leave 2^-23 of an operand, a product 2^-22, a score (its terms' errors of
+    random sign, sum |q k| scale up to 0.64 sqrt(D)) less than 2^-20, and a weight as much beside
+    exp's 2^-21: relative errors of o that average out over keys and columns, 2^-19 in the norm
+    with a factor to spare.  A tf32 product without its small terms is off by 2^-11."""
+    inp = attn_inputs(lens, Hq, Hk, D, 16, F32, seed=32)
+    o, lse = gdn.gdn_attn_decode(*inp)
+    ro, rl = decode.attn_decode(*[n64(x) for x in inp[:3]], inp[3].cpu().numpy(),
+                                inp[4].cpu().numpy())
+    for b in range(len(lens)):
+        for h in range(Hq):
+            err = np.linalg.norm(n64(o[b, h]) - ro[b, h]) / np.linalg.norm(ro[b, h])
+            assert err <= 2.0 ** -19, (b, h, err)
+    assert np.abs(n64(lse) - rl).max() <= 2.0 ** -18
+
+
 # ------------------------------------------------------------------ norm + rotation
 
 # A lane adds the rows of its warp's groups one after another: at most 2 tokens of 9 groups and a
@@ -129,3 +152,45 @@ def test_rope_epsilon(case, inter, eps):
         within("d" + name, dx, rdx, half(dt) * np.abs(rdx) + tol * (1 + half(dt)))
         tol = ((e + (CHAIN + 16) * U) * A * xr).sum((0, 1))
         within("dw" + name, dw, rdw, tol + U * np.abs(rdw))
+
+
+TOKENS = [(4001, 17, 3, 128, 64, BF), (3001, 13, 5, 64, 64, BF), (2500, 12, 1, 256, 64, BF),
+          (3003, 16, 9, 64, 32, F32), (2433, 3, 1, 64, 0, F32), (300, 1, 1, 128, 16, BF)]
+TOKEN_IDS = ["x".join(map(str, c[:5])) for c in TOKENS]
+
+
+@pytest.mark.parametrize("case", TOKENS, ids=TOKEN_IDS)
+def test_rope_weight_gradient_counts_every_row_once(case):
+    """Elements of size 1 with eps = 3: x r = x / 2 exactly (rsqrt: 2 units of 2^-23 at most).
+    dy = x or 2 x without rotation: every row adds 1/2 or 1 to every column, so sums of small
+    halves, exact in fp32 but for rsqrt's error: a row lost or counted twice is 1/2 at least."""
+    N, Hq, Hk, D, _, dt = case
+    gen = torch.Generator().manual_seed(N)
+    w, none = torch.ones(D, device="cuda"), torch.empty(0, device="cuda")
+    x = [torch.randint(0, 2, (N, H, D), generator=gen).mul(2).sub(1).to(dt).cuda() for H in (Hq, Hk)]
+    m = [torch.randint(1, 3, (N, H, D), generator=gen).to(dt).cuda() for H in (Hq, Hk)]
+    got = gdn.gdn_qk_norm_rope_bwd(*x, w, w, none, None, x[0] * m[0], x[1] * m[1], eps=3.0)[2:]
+    for dw, y in zip(got, m):
+        want = n64(y).sum((0, 1)) / 2
+        tol = want.max() * (2.0 ** -22 + CHAIN * U)
+        assert tol < 0.5
+        within("dw", dw, want, tol)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("case", TOKENS, ids=TOKEN_IDS)
+def test_rope_weight_gradient_to_its_own_roundings(case, inter):
+    N, Hq, Hk, D, R, dt = case
+    q, k, _, wq, wk, f, _ = rope_inputs(N, Hq, Hk, D, R, dt, seed=N + 1)
+    gen = torch.Generator().manual_seed(N)
+    dyq, dyk = rand(gen, (N, Hq, D), dt), rand(gen, (N, Hk, D), dt)
+    _, _, dwq, dwk = gdn.gdn_qk_norm_rope_bwd(q, k, wq, wk, f, None, dyq, dyk, interleaved=inter)
+    t = np.arange(N)
+    for dw, x, w, dy in ((dwq, q, wq, dyq), (dwk, k, wk, dyk)):
+        x, dy = n64(x), n64(dy)
+        _, ref = decode.norm_rope_bwd(x, n64(w), t, n64(f), dy, inter)
+        xr = np.abs(x) / np.sqrt(np.mean(x * x, -1, keepdims=True) + 1e-6)
+        tol = ((40 * U + angle_err(t, n64(f)) + (CHAIN + 16) * U) * terms(dy, inter, R) * xr)
+        tol = tol.sum((0, 1)) + U * np.abs(ref)
+        assert np.median(tol) < 0.02 * np.sqrt(np.mean(ref * ref))  # it would notice
+        within("dw", dw, ref, tol)
