@@ -11,7 +11,8 @@
 // a scan kernel: the lengths come from L2.  A token finds its request by a binary search in
 // shared memory.  The token at the first row of a new page writes the page's entry of
 // block_table (each new page has exactly one such token); CTA 0 writes the per-request
-// outputs.
+// outputs.  Pages are numbered by the requests before, so that a cut at the last token row
+// changes only the request that it falls on and those behind it, which have no token here.
 #include <string.h>
 
 #include "gdn_internal.h"
@@ -101,8 +102,17 @@ __global__ void __launch_bounds__(SM_NT) k_slot_map(SlotArgs ar) {
     s_first[tid + 1] = first0 + first;
     s_ctx[tid] = c;
     if (lead && b < ar.B) {
-      ar.seq_len[b] = (int32_t)min(c + n, cap);
-      ar.cu[b + 1] = sat31(cu0 + cu);
+      // tokens past n_tokens have no row: the step is the one without them, lengths and pages too
+      const int64_t room = ar.n_tokens - (cu0 + cu - n);
+      const uint32_t kept = room < (int64_t)n ? (uint32_t)(room > 0 ? room : 0) : n;
+      ar.seq_len[b] = (int32_t)min(c + kept, cap);
+      ar.cu[b + 1] = (int32_t)min(cu0 + cu, ar.n_tokens);
+      if (room >= 0 && kept < n) {  // the one request that the end falls on
+        const int64_t taken =
+            first0 + first - need + ceil_div(c + kept, ar.P) - ceil_div(c, ar.P);
+        ar.used[0] = sat31(taken);
+        bad = 1;
+      }
     }
     __syncthreads();
     const int64_t lo = s_cu[0] > t0 ? s_cu[0] : t0;
@@ -143,8 +153,10 @@ __global__ void __launch_bounds__(SM_NT) k_slot_map(SlotArgs ar) {
   }
   if (lead && tid == 0) {
     ar.cu[0] = 0;
-    ar.used[0] = sat31(first0);
-    if (cu0 > ar.n_tokens || first0 > ar.n_free) bad = 1;
+    if (cu0 <= ar.n_tokens) {
+      ar.used[0] = sat31(first0);
+      if (first0 > ar.n_free) bad = 1;
+    }
   }
   if (bad && ar.status) atomicOr(ar.status, kStatusClamped);
 }

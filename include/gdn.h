@@ -648,9 +648,11 @@ gdn_status gdn_attn_decode(const gdn_attn_problem* p, const void* q, const void*
  *  - positions[t], slots[t] of packed token t: its position in its request and its cache row
  *    page * page_size + position % page_size; padding rows get position 0 and slot -1.
  * A token whose page is missing gets slot -1: past max_blocks, past the free list, or a page
- * outside [0, pages).  That, a negative length (taken as 0) and packed tokens past n_tokens
- * (dropped) are recorded in `status`; seq_len stops at max_blocks page_size.  One launch, no
- * workspace; all outputs int32.
+ * outside [0, pages).  Packed tokens past n_tokens are left out of the step: every output is
+ * that of new_len cut to the tokens that have a row, so that seq_len counts no cache row that
+ * nothing writes and no page is taken for them.  These and a negative length (taken as 0) are
+ * recorded in `status`; seq_len stops at max_blocks page_size.  One launch, no workspace; all
+ * outputs int32.
  * Errors: null or misaligned pointer, sizes < 0, page_size < 1, seq_len that is ctx_len or
  * new_len: GDN_ERR_INVALID_ARG; pages page_size, max_blocks page_size, n_tokens, n_free or
  * B >= 2^31: GDN_ERR_UNSUPPORTED.

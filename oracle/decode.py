@@ -77,6 +77,7 @@ def slot_map(ctx_len, new_len, free_pages, block_table, page_size, pages, n_toke
     cap = table.shape[1] * P
     for b, (c, n) in enumerate(zip(ctx_len, new_len)):
         c, n = max(int(c), 0), max(int(n), 0)
+        n = min(n, n_tokens - t)  # tokens without a row are not part of the step
         held = -(-c // P)
         for p in range(c, c + n):
             i = p // P
@@ -85,12 +86,11 @@ def slot_map(ctx_len, new_len, free_pages, block_table, page_size, pages, n_toke
                 taken += 1
                 if not 0 <= page < pages:
                     page = -1
-                if i < table.shape[1] and t < n_tokens:
+                if i < table.shape[1]:
                     table[b, i] = page
-            if t < n_tokens:
-                page = int(table[b, i]) if i < table.shape[1] else -1
-                pos[t] = p
-                slots[t] = page * P + p % P if 0 <= page < pages else -1
+            page = int(table[b, i]) if i < table.shape[1] else -1
+            pos[t] = p
+            slots[t] = page * P + p % P if 0 <= page < pages else -1
             t += 1
         assert held <= -(-(c + n) // P)
         seq.append(min(c + n, cap))

@@ -1,15 +1,15 @@
 """GPU tests of the decode-step calls at places where a definition is easily missed: softmax weights
 that a short type cannot hold, infinite values, fp32 accuracy in the norm, an epsilon of zero or
-above the rows' size, weight gradients that lose or double a token.  Bounds are counted as in
-test_decode_gpu.py."""
+above the rows' size, weight gradients that lose or double a token, and steps with fewer token rows
+than their requests need.  Bounds are counted as in test_decode_gpu.py."""
 import numpy as np
 import pytest
 import torch
 
 import chunked_state_scan_gated_gb300 as gdn
 from oracle import decode
-from test_decode_gpu import (BF, F32, U, angle_err, attn_inputs, half, n64, rand, rope_inputs, terms,
-                             within)
+from test_decode_gpu import (BF, F32, U, angle_err, attn_inputs, check_attn, check_slots, half, n64,
+                             rand, rope_inputs, slot_inputs, terms, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -194,3 +194,67 @@ def test_rope_weight_gradient_to_its_own_roundings(case, inter):
         tol = tol.sum((0, 1)) + U * np.abs(ref)
         assert np.median(tol) < 0.02 * np.sqrt(np.mean(ref * ref))  # it would notice
         within("dw", dw, ref, tol)
+
+
+# ------------------------------------------------------------------------------- slot map
+
+def stale(table, pages, seed=0):
+    """The table with its unused entries holding pages of other requests."""
+    other = torch.from_numpy(np.random.default_rng(seed).integers(0, pages, tuple(table.shape)))
+    return torch.where(table < 0, other.int().cuda(), table)
+
+
+def check_step_is_whole(ctx, new, free, table, P, pages, n_tokens, ok):
+    """Against the definition, and by itself: every length counts only tokens that have a row, every
+    page that a length reaches was held before or is one of the first `used` free ones, none twice."""
+    before = table.cpu().numpy()
+    check_slots(ctx, new, free, table.clone(), P, pages, n_tokens, ok=ok)
+    seq, cu, _, slots, used = (x.tolist() for x in gdn.gdn_slot_map(
+        ctx, new, free, table, page_size=P, pages=pages, n_tokens=n_tokens))
+    cap = table.shape[1] * P
+    given, after = free.tolist()[:used[0]], table.cpu().numpy()
+    assert len(given) == used[0] and cu[-1] <= n_tokens
+    for b, c in enumerate(ctx.tolist()):
+        assert min(c, cap) <= seq[b] <= min(c + cu[b + 1] - cu[b], cap)
+        held = min(-(-c // P), table.shape[1])
+        assert (after[b, :held] == before[b, :held]).all()
+        fresh = after[b, held:-(-seq[b] // P)].tolist()
+        assert fresh == given[:len(fresh)]
+        del given[:len(fresh)]
+    assert not given  # every page that was taken is in a table
+
+
+@pytest.mark.parametrize("n_tokens", [0, 1, 6, 7, 29, 30, 31, 35, 41, 49, 50, 51, 59, 60, 61])
+def test_slot_map_with_fewer_token_rows_than_tokens(n_tokens):
+    c, w, free, table, pages = slot_inputs([10, 3, 40], [30, 20, 10], 8, 10, seed=1)
+    check_step_is_whole(c, w, free, stale(table, pages), 8, pages, n_tokens, n_tokens >= 60)
+
+
+@pytest.mark.parametrize("n_tokens", [0, 100, 767, 768, 769, 1023, 1024, 1025, 2000, 2047, 2100])
+def test_slot_map_of_many_requests_cut_at_the_last_row(n_tokens):
+    """2100 tokens of 700 requests: the cut falls on any of several blocks of requests and rows."""
+    ctx, new = [(7 * b) % 50 for b in range(700)], [(b * 5) % 7 for b in range(700)]
+    c, w, free, table, pages = slot_inputs(ctx, new, 4, 16, seed=2)
+    assert sum(new) == 2100
+    check_step_is_whole(c, w, free, stale(table, pages), 4, pages, n_tokens, n_tokens >= 2100)
+
+
+def test_dropped_tokens_bring_no_other_request_into_the_attention():
+    """Rows of the cache that the step does not write hold NaN; the tables' unused entries name
+    such pages.  The attention over seq_len is over the rows that were written."""
+    Hq, Hk, D, P, rows = 4, 2, 128, 16, 41
+    c, w, free, table, pages = slot_inputs([0, 0, 0], [20, 30, 10], P, 4, seed=3)
+    table = stale(table, pages)
+    gen = torch.Generator().manual_seed(4)
+    qkv, one = rand(gen, (rows, Hq + 2 * Hk, D), BF), torch.ones(D, device="cuda")
+    kc, vc = (torch.full((pages, P, Hk, D), float("nan"), dtype=BF, device="cuda") for _ in range(2))
+    word = gdn.status_word()
+    seq, cu, pos, slots, _ = gdn.gdn_slot_map(c, w, free, table, page_size=P, pages=pages,
+                                              n_tokens=rows, status=word)
+    q = gdn.gdn_qk_norm_rope_cache(qkv[:, :Hq], qkv[:, Hq:Hq + Hk], qkv[:, Hq + Hk:], one, one,
+                                   torch.ones(8, device="cuda"), pos, slots, kc, vc, status=word)
+    o, lse = gdn.gdn_attn_decode(q[:3].contiguous(), kc, vc, table, seq, status=word)
+    assert gdn.gdn_check_device_status(word) == gdn.GDN_ERR_INVALID_ARG
+    assert seq.tolist() == [20, 21, 0] and cu.tolist() == [0, 20, 41, 41]
+    assert torch.isfinite(o).all() and torch.isfinite(lse[:2]).all()
+    check_attn(q[:3].contiguous(), kc, vc, table, seq, o, lse)
