@@ -2,9 +2,9 @@
 // Request b has ctx_b cached tokens and new_b new ones; with P tokens per page
 //   cu_b    = sum_{i<b} new_i                                  (packed token offsets)
 //   need_b  = ceil((ctx_b + new_b) / P) - ceil(ctx_b / P),  first_b = sum_{i<b} need_i
-// and token j of request b is at position ctx_b + j, on the request's page number
-// i = position / P: an old page (block_table) below ceil(ctx_b / P), else entry
-// first_b + i - ceil(ctx_b / P) of the free list.
+// (both lengths at most what a row of the table holds) and token j of request b is at position
+// ctx_b + j, on the request's page number i = position / P: an old page (block_table) below
+// ceil(ctx_b / P), else entry first_b + i - ceil(ctx_b / P) of the free list.
 //
 // Integer work on a few KB: bound by latency, so one launch.  Every CTA scans the lengths
 // itself (SM_NT at a time, 64-bit sums) up to the tokens that it owns, rather than wait for
@@ -91,7 +91,8 @@ __global__ void __launch_bounds__(SM_NT) k_slot_map(SlotArgs ar) {
       n = ni < 0 ? 0 : ni;
       if (ci < 0 || ni < 0 || c + n > cap) bad = 1;
     }
-    const int64_t need = ceil_div(c + n, ar.P) - ceil_div(c, ar.P);
+    const auto pages_of = [&](uint32_t x) { return ceil_div(min(x, cap), ar.P); };
+    const int64_t need = pages_of(c + n) - pages_of(c);  // the table takes no others
     int64_t cu = n, first = need;
     scan2(cu, first, part);
     if (tid == 0) {
@@ -108,8 +109,7 @@ __global__ void __launch_bounds__(SM_NT) k_slot_map(SlotArgs ar) {
       ar.seq_len[b] = (int32_t)min(c + kept, cap);
       ar.cu[b + 1] = (int32_t)min(cu0 + cu, ar.n_tokens);
       if (room >= 0 && kept < n) {  // the one request that the end falls on
-        const int64_t taken =
-            first0 + first - need + ceil_div(c + kept, ar.P) - ceil_div(c, ar.P);
+        const int64_t taken = first0 + first - need + pages_of(c + kept) - pages_of(c);
         ar.used[0] = sat31(taken);
         bad = 1;
       }

@@ -641,9 +641,10 @@ gdn_status gdn_attn_decode(const gdn_attn_problem* p, const void* q, const void*
  * request after another in n_tokens token rows (rows behind the last are padding).
  *  - seq_len[b] = ctx_len[b] + new_len[b]; cu_seqlens [B+1]: offsets of the packed tokens (as
  *    gdn_fwd_varlen takes).
- *  - Request b needs ceil(seq_len/page_size) - ceil(ctx_len/page_size) new pages; they are
- *    taken from the front of free_pages [n_free] in the order of the requests and written to
- *    block_table [B][max_blocks] behind the pages it has; the other entries stay as they are.
+ *  - Request b needs ceil(seq_len/page_size) - ceil(ctx_len/page_size) new pages, none past
+ *    max_blocks; they are taken from the front of free_pages [n_free] in the order of the
+ *    requests and written to block_table [B][max_blocks] behind the pages it has; the other
+ *    entries stay as they are.
  *    used[0] = the pages the step needs (more than n_free: not all could be given).
  *  - positions[t], slots[t] of packed token t: its position in its request and its cache row
  *    page * page_size + position % page_size; padding rows get position 0 and slot -1.

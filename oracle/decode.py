@@ -81,13 +81,10 @@ def slot_map(ctx_len, new_len, free_pages, block_table, page_size, pages, n_toke
         held = -(-c // P)
         for p in range(c, c + n):
             i = p // P
-            if p % P == 0:  # the first row of a page that the request does not have yet
+            if p % P == 0 and i < table.shape[1]:  # the first row of a page that it does not have
                 page = int(free_pages[taken]) if taken < len(free_pages) else -1
                 taken += 1
-                if not 0 <= page < pages:
-                    page = -1
-                if i < table.shape[1]:
-                    table[b, i] = page
+                table[b, i] = page if 0 <= page < pages else -1
             page = int(table[b, i]) if i < table.shape[1] else -1
             pos[t] = p
             slots[t] = page * P + p % P if 0 <= page < pages else -1

@@ -1,7 +1,7 @@
 """GPU tests of the decode-step calls at places where a definition is easily missed: softmax weights
 that a short type cannot hold, infinite values, fp32 accuracy in the norm, an epsilon of zero or
 above the rows' size, weight gradients that lose or double a token, and steps with fewer token rows
-than their requests need.  Bounds are counted as in test_decode_gpu.py."""
+or narrower tables than their requests need.  Bounds are counted as in test_decode_gpu.py."""
 import numpy as np
 import pytest
 import torch
@@ -237,6 +237,15 @@ def test_slot_map_of_many_requests_cut_at_the_last_row(n_tokens):
     c, w, free, table, pages = slot_inputs(ctx, new, 4, 16, seed=2)
     assert sum(new) == 2100
     check_step_is_whole(c, w, free, stale(table, pages), 4, pages, n_tokens, n_tokens >= 2100)
+
+
+@pytest.mark.parametrize("blocks", [0, 1, 2, 5, 6, 7, 8])
+@pytest.mark.parametrize("n_tokens", [64, 45])
+def test_slot_map_takes_no_page_past_the_table(blocks, n_tokens):
+    """A request that its row of the table cannot hold takes no page that it has no entry for."""
+    c, w, free, table, pages = slot_inputs([10, 40, 3, 0], [30, 15, 10, 5], 8, 8, seed=5)
+    table = stale(table, pages)[:, :blocks].contiguous()
+    check_step_is_whole(c, w, free, table, 8, pages, n_tokens, n_tokens == 64 and blocks >= 7)
 
 
 def test_dropped_tokens_bring_no_other_request_into_the_attention():
