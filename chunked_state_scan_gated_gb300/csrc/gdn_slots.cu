@@ -164,6 +164,19 @@ __global__ void __launch_bounds__(SM_NT) k_slot_map(SlotArgs ar) {
 bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 bool ok4(const void* p, int64_t n) { return n == 0 || (p && aligned4(p)); }
 
+// An array of n int32 in memory.
+struct Span {
+  uintptr_t first, last;  // bytes; empty: first > last
+  Span(const void* p, int64_t n) {
+    first = n > 0 ? (uintptr_t)p : 1;
+    const uintptr_t left = (UINTPTR_MAX - first) / 4;
+    last = n > 0 ? first + 4 * ((uint64_t)n < left ? (uintptr_t)n : left) - 1 : 0;
+  }
+  bool meets(const Span& o) const {
+    return first <= last && o.first <= o.last && first <= o.last && o.first <= last;
+  }
+};
+
 }  // namespace
 }  // namespace gdn
 
@@ -185,9 +198,19 @@ extern "C" gdn_status gdn_slot_map(const gdn_slot_problem* p, const int32_t* ctx
   if (!ok4(ctx_len, p->B) || !ok4(new_len, p->B) || !ok4(free_pages, p->n_free) ||
       !ok4(block_table, p->B * p->max_blocks) || !ok4(seq_len, p->B) || !ok4(cu_seqlens, 1) ||
       !ok4(positions, p->n_tokens) || !ok4(slots, p->n_tokens) || !ok4(used, 1) ||
-      ((uintptr_t)status & 255u) != 0 ||
-      (p->B > 0 && (seq_len == ctx_len || seq_len == new_len)))  // CTAs read them as others write
+      ((uintptr_t)status & 255u) != 0)
     return GDN_ERR_INVALID_ARG;
+  // CTAs read lengths, pages and table entries while others write: nothing may lie on anything
+  const Span in[] = {{ctx_len, p->B}, {new_len, p->B}, {free_pages, p->n_free}};
+  const Span out[] = {{block_table, p->B * p->max_blocks}, {seq_len, p->B},
+                      {cu_seqlens, p->B + 1}, {positions, p->n_tokens},
+                      {slots, p->n_tokens}, {used, 1}};
+  for (const Span& o : out) {
+    for (const Span& i : in)
+      if (o.meets(i)) return GDN_ERR_INVALID_ARG;
+    for (const Span& other : out)
+      if (&other != &o && o.meets(other)) return GDN_ERR_INVALID_ARG;
+  }
   SlotArgs ar;
   memset(&ar, 0, sizeof(ar));
   ar.P = (uint32_t)p->page_size;

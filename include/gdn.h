@@ -654,9 +654,9 @@ gdn_status gdn_attn_decode(const gdn_attn_problem* p, const void* q, const void*
  * nothing writes and no page is taken for them.  These and a negative length (taken as 0) are
  * recorded in `status`; seq_len stops at max_blocks page_size.  One launch, no workspace; all
  * outputs int32.
- * Errors: null or misaligned pointer, sizes < 0, page_size < 1, seq_len that is ctx_len or
- * new_len: GDN_ERR_INVALID_ARG; pages page_size, max_blocks page_size, n_tokens, n_free or
- * B >= 2^31: GDN_ERR_UNSUPPORTED.
+ * Errors: null or misaligned pointer, sizes < 0, page_size < 1, an output (block_table among
+ * them) that overlaps an input or another output, in part or whole: GDN_ERR_INVALID_ARG; pages
+ * page_size, max_blocks page_size, n_tokens, n_free or B >= 2^31: GDN_ERR_UNSUPPORTED.
  */
 typedef struct gdn_slot_problem {
   int32_t page_size;  /* tokens per page, >= 1 */

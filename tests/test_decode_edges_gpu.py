@@ -248,6 +248,29 @@ def test_slot_map_takes_no_page_past_the_table(blocks, n_tokens):
     check_step_is_whole(c, w, free, table, 8, pages, n_tokens, n_tokens == 64 and blocks >= 7)
 
 
+def test_slot_map_arrays_side_by_side_in_one_block():
+    """Arrays of one int32 block that touch and do not overlap, empty ones anywhere."""
+    c, w, free, table, pages = slot_inputs([10, 3, 40], [30, 20, 10], 8, 10, seed=6)
+    want = gdn.gdn_slot_map(c, w, free, table.clone(), page_size=8, pages=pages, n_tokens=64)
+    sizes = [3, 3, free.numel(), table.numel(), 3, 4, 64, 64, 1]
+    parts = list(torch.empty(sum(sizes), dtype=torch.int32, device="cuda").split(sizes))
+    for p, x in zip(parts, (c, w, free, table.view(-1))):
+        p.copy_(x)
+    ctx, new, fr, tb, seq, cu, pos, slots, used = parts
+    kw = dict(page_size=8, pages=pages, n_tokens=64)
+    got = gdn.gdn_slot_map(ctx, new, fr, tb.view(3, 10), seq_len=seq, cu_seqlens=cu, positions=pos,
+                           slots=slots, used=used, **kw)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    new.zero_()
+    got = gdn.gdn_slot_map(ctx, new, fr, tb.view(3, 10), seq_len=seq, cu_seqlens=cu,
+                           positions=used[:0], slots=used[:0], used=used, page_size=8, pages=pages,
+                           n_tokens=0)
+    assert torch.equal(got[0], ctx) and used.tolist() == [0] and not cu.any()
+    with pytest.raises(gdn.GDNError):
+        gdn.gdn_slot_map(ctx, new, fr, tb.view(3, 10), seq_len=seq, cu_seqlens=cu, positions=pos,
+                         slots=slots, used=cu[3:], **kw)
+
+
 def test_dropped_tokens_bring_no_other_request_into_the_attention():
     """Rows of the cache that the step does not write hold NaN; the tables' unused entries name
     such pages.  The attention over seq_len is over the rows that were written."""
