@@ -48,6 +48,7 @@ constexpr int AT_NT = 32 * AT_W;
 constexpr int AT_G = 8;            // query heads per product
 constexpr int AT_SMS = 152;
 constexpr float AT_LAZY = 8.f;     // log2 units
+constexpr float AT_LOG2E = 1.4426950408889634f;
 // What a piece costs beside its tiles, in units (its first loads and its end): without it a CTA
 // with many short requests lags (61 ragged requests 128 against 102 us; 2 to 5: the same).
 constexpr int AT_START = 1;
@@ -981,7 +982,8 @@ gdn_status check_problem(const gdn_attn_problem* p) {
   if (!p) return GDN_ERR_INVALID_ARG;
   if (p->dtype != GDN_BF16 && p->dtype != GDN_FP32) return GDN_ERR_INVALID_ARG;
   if (p->B < 0 || p->Hq < 1 || p->Hk < 1 || p->Hq % p->Hk != 0 || p->pages < 0 ||
-      p->max_blocks < 0 || p->page_size < 1 || p->D < 1 || !isfinite(p->scale))
+      p->max_blocks < 0 || p->page_size < 1 || p->D < 1 || !isfinite(p->scale) ||
+      !isfinite(fmaxf(p->scale, 0.f) * AT_LOG2E))
     return GDN_ERR_INVALID_ARG;
   const int64_t unit = p->dtype == GDN_BF16 ? 8 : 4;  // elements in 16 bytes
   if (p->q_stride != 0 && (p->q_stride < p->Hq * p->D || p->q_stride % unit != 0))
@@ -1082,7 +1084,7 @@ gdn_status gdn_attn_decode(const gdn_attn_problem* p, const void* q, const void*
   ar.qs = p->q_stride ? p->q_stride : p->Hq * p->D;
   ar.P = p->page_size;
   ar.G = (int)(p->Hq / p->Hk);
-  ar.sl = (p->scale > 0.f ? p->scale : 1.0f / sqrtf((float)p->D)) * 1.4426950408889634f;
+  ar.sl = (p->scale > 0.f ? p->scale : 1.0f / sqrtf((float)p->D)) * AT_LOG2E;
   ar.lazy = fminf(AT_LAZY / ar.sl, 1e30f);
   ar.q = q;
   ar.kc = k_cache;

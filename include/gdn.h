@@ -614,9 +614,9 @@ gdn_status gdn_qk_norm_rope_cache(const gdn_rope_problem* p, const void* q, cons
  * The split is chosen on the device from seq_len (the host reads nothing) and depends on the
  * lengths alone: deterministic.  Two launches.
  * Errors: null or misaligned pointer, sizes < 0, Hq % Hk != 0, q_stride < Hq D or no multiple
- * of 16 bytes, a scale that is not finite: GDN_ERR_INVALID_ARG; D other than 64, 128 or 256,
- * page_size no multiple of 16, pages page_size or max_blocks page_size >= 2^31, B Hq >= 2^31:
- * GDN_ERR_UNSUPPORTED.
+ * of 16 bytes, a scale that is not finite or whose product with log2(e) is not:
+ * GDN_ERR_INVALID_ARG; D other than 64, 128 or 256, page_size no multiple of 16, pages page_size
+ * or max_blocks page_size >= 2^31, B Hq >= 2^31: GDN_ERR_UNSUPPORTED.
  */
 typedef struct gdn_attn_problem {
   int32_t dtype;      /* GDN_BF16 or GDN_FP32: q, both caches, o */

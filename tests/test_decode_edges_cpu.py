@@ -1,5 +1,7 @@
 """CPU tests of refusals that the decode-step calls owe at their edges: arrays of one call that lie on
-one another.  Validation fails before any launch, so the addresses are stand-ins."""
+one another, a scale that only overflows once it is in base 2.  Validation fails before any launch,
+so the addresses are stand-ins."""
+import ctypes
 import itertools
 
 import pytest
@@ -33,3 +35,13 @@ def test_slot_map_arrays_that_overlap_are_refused(lib, x, y):
         at = {k: A * (i + 1) for i, k in enumerate(SIZES)}
         at[y] = at[x] + 4 * shift
         assert lib.gdn_slot_map(p, *[at[k] for k in SIZES], None, None) == BAD, shift
+
+
+@pytest.mark.parametrize("scale,status", [(2.3e38, gdn.GDN_OK), (2.4e38, BAD), (3.4e38, BAD),
+                                          (-3.4e38, gdn.GDN_OK), (1e-45, gdn.GDN_OK)])
+def test_attention_scale_has_to_be_finite_in_base_2(lib, scale, status):
+    """exp(scale x) is taken as 2^(scale log2(e) x): an infinite factor makes 0 * inf of equal
+    scores.  Below 0 the scale means the default."""
+    p = gdn.AttnProblem(gdn.GDN_BF16, 128, 16, scale, 3, 8, 2, 100, 10, 0)
+    n = ctypes.c_size_t(0)
+    assert lib.gdn_attn_decode_workspace_size(p, ctypes.byref(n)) == status
