@@ -8,8 +8,8 @@ import torch
 
 import chunked_state_scan_gated_gb300 as gdn
 from oracle import decode
-from test_decode_gpu import (BF, F32, U, angle_err, attn_inputs, check_attn, check_slots, half, n64,
-                             rand, rope_inputs, slot_inputs, terms, within)
+from test_decode_gpu import (BF, F32, U, angle_err, attn_inputs, check_attn, check_slots, half, i32,
+                             n64, rand, rope_inputs, slot_inputs, terms, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -81,6 +81,36 @@ def test_attention_infinite_and_largest_values(dt, D, Hq, n):
         o, _ = gdn.gdn_attn_decode(q, kc, vc, table, lens)
         within("o", o[0], np.full((Hq, D), 3.0),
                3 * (half(dt) + (n + 16) * 2.0 ** -22 + 2.0 ** -20))
+
+
+@pytest.mark.parametrize("D,Hq", [(64, 2), (64, 9), (128, 8), (128, 16), (256, 8), (256, 11)])
+def test_attention_fp32_of_the_largest_numbers(D, Hq):
+    """fp32 keys and values up to the type's largest are as exact as others: one key, whose weight is
+    1, gives v; 8 keys of that size on queries that bring the scores back to 2 .. 16 (one product
+    each, queries of 4 bits) weigh as they should: both splits cut off leave 2^-21 of an operand,
+    scores 2^-21 and 3 U of the difference, exp 2^-21, in the weight and in the sum; o has its
+    values' 2^-21 and 16 additions of 2^-22."""
+    q, kc, vc, table, lens = attn_inputs([8], Hq, 1, D, 16, F32, seed=35)
+    top = torch.finfo(F32).max
+    page = table[0, 0].long()
+    gen = torch.Generator().manual_seed(36)
+    v = (0.5 + 0.5 * torch.rand((8, D), generator=gen)).cuda()
+    vc[page, :8, 0] = v * top
+    vc[page, 0, 0, 0] = -top
+    o, _ = gdn.gdn_attn_decode(q, kc, vc, table, i32([1]))
+    ref = n64(vc[page, 0, 0])[None].repeat(Hq, 0)
+    within("o", o[0], ref, np.abs(ref) * (half(F32) + 2.0 ** -21))
+    q.zero_()
+    kc[page, :8] = 0.0
+    row, at = torch.arange(8, device="cuda"), torch.arange(8, device="cuda") * 7
+    kc[page, row, 0, at] = v[:, 0] * top
+    q[0][:, at] = 2.0 ** -125 * (1 + torch.randint(0, 8, (Hq, 8), generator=gen) / 8).cuda()
+    vc[page, :8, 0] = v
+    o, lse = gdn.gdn_attn_decode(q, kc, vc, table, lens, scale=1.0)
+    ro, rl = decode.attn_decode(n64(q), n64(kc), n64(vc), table.cpu().numpy(), [8], 1.0)
+    e = 2 * (16 * (2.0 ** -21 + 3 * U) + 2.0 ** -21) + 2.0 ** -21 + 16 * 2.0 ** -22
+    within("o", o, ro, e * np.abs(ro) + half(F32) * np.abs(ro))
+    within("lse", lse, rl, e + 4 * U * np.abs(rl))
 
 
 FP32 = [([65], 8, 1, 64), ([3000], 8, 2, 64), ([3000], 12, 1, 64), ([65], 8, 1, 128),
