@@ -24,8 +24,8 @@
 // next V tile during the next K product; 8 to 16 such warps per SM keep 64 to 128 KB in flight.
 // fp32 caches use tf32 products of the two-term split x = hi + lo (2^-23 of x; all four products),
 // which keeps fp32 accuracy at the same layout.  The split is done with integer and fp32
-// instructions at full rate (131001 tokens of 8 heads of 128: 176 us against 234 with conversion
-// instructions and a test of every value for infinities).
+// instructions at full rate (131001 tokens of 8 heads of 128: 181 us against 234 with conversion
+// instructions and a test of every value for infinities; 176 with the accumulators of mma_split).
 //
 // Split: the unit is a CTA tile of one (request, key head); the units of all requests in a
 // row are divided evenly over the CTAs of one wave, whatever the lengths: no tail, and one long

@@ -2,8 +2,8 @@
 // (programmatic stream serialization): the next grid's CTAs are placed while the last CTAs of
 // the one before run out, and wait on the device for its end.  A kernel launched so calls
 // after_previous() before it touches memory; before_next() lets the one behind it start being
-// placed once every CTA has called it (or left).  Saves 1 to 2 us per launch of a decode step,
-// captured or not.
+// placed once every CTA has called it (or left).  Saves 1 to 3 us per call of a decode step (one
+// or two launches), captured or not.
 #pragma once
 
 #include <cuda_runtime.h>

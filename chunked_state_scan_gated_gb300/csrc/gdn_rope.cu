@@ -18,7 +18,8 @@
 //   y = r (x (w c) + xp (w_p s)),  xp the partner elements, s with the sign of the pair's side
 // and the arithmetic is packed two fp32 numbers at a time (237 instructions per row without
 // either, 113 now).  Measured: forward of those 32768 tokens 96 us (6.3 TB/s), backward of 16001
-// tokens of 40 heads of 128 80 us (6.1 TB/s).  Two CTAs of 8 warps per SM with 4 KB in flight per
+// tokens of 40 heads of 128 81 us (6.1 TB/s); fp32, 16384 and 16001 tokens: 93 and 158 us (6.5 and
+// 6.2 TB/s).  Two CTAs of 8 warps per SM with 4 KB in flight per
 // warp are the best of 2 to 4 CTAs and 4 to 16 KB (3 CTAs: 108 us; 8 KB: 100 us).
 #include <cuda_bf16.h>
 #include <math.h>
@@ -86,7 +87,7 @@ __device__ __forceinline__ float turns(float x, Freq f) {
 }
 // cos and sin of t * f, t any int32, f fp32: t is split into two parts that are exact in fp32, and
 // only the fraction goes into sincospi.  What is left is the rounding of the fraction (2^-24
-// revolutions) and of lo (t f 2^-51 revolutions: 2^-22 at t = 2^29).
+// revolutions) and, past 2^24 revolutions, of lo and of the remainders (t f 2^-50: 2^-21 at t = 2^29).
 __device__ __forceinline__ void angle(int32_t t, Freq f, float* c, float* s) {
   float u = turns((float)(t & 0xffff), f);
   if (t & ~0xffff) u += turns((float)(t & ~0xffff), f);

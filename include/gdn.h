@@ -546,7 +546,8 @@ gdn_status gdn_step(const gdn_problem* p, int64_t n_slots, const int32_t* slots,
  *   (n[2i], n[2i+1]) when interleaved;  y = n for the elements from R on.
  * w is wq for the Hq query heads, wk for the Hk key heads.  Long-context scalings of the
  * rotation are given through inv_freq (scaled frequencies) and rope_scale (their factor on
- * cos and sin).  The angle's product is exact before it is reduced, for any int32 position.
+ * cos and sin).  The angle's product is formed in two fp32 terms before it is reduced: off by at
+ * most 2^-23 + |t inv_freq| 2^-50 revolutions, for any int32 position.
  *  - q [N,Hq,D], k, v [N,Hk,D] in p->dtype with q_stride, k_stride, v_stride elements between
  *    tokens (0: contiguous; they may be slices of one fused projection); q_out [N,Hq,D],
  *    k_out [N,Hk,D], dq_out, dk_out, dq, dk contiguous.
