@@ -9,7 +9,7 @@ The functions keep the C names (``gdn_fwd``, ``gdn_bwd``, ``gdn_summary``,
 ``gdn_summary_bwd``, ``gdn_compose``, ``gdn_prefix_compose``,
 ``gdn_prefix_compose_bwd``, ``gdn_apply_state``, ``gdn_apply_state_bwd``,
 ``gdn_gate_param_bwd``, ``gdn_query_support``, ``gdn_resolved_segments``, ``gdn_workspace_size``,
-``gdn_check_device_status``, and the decode-step calls at the end) and
+``gdn_check_device_status``, and the decode-step and full-attention calls at the end) and
 take torch tensors in the token-major layouts of the header: q, k
 [B,T,Hqk,dk]; v [B,T,H,dv]; a, b [B,T,H]; A_log, dt_bias [H] fp32; states
 [B,H,dk,dv] fp32.
@@ -47,6 +47,8 @@ EXPORTS = (
     "gdn_step", "gdn_qk_norm_rope_fwd", "gdn_qk_norm_rope_bwd_workspace_size",
     "gdn_qk_norm_rope_bwd", "gdn_qk_norm_rope_cache", "gdn_attn_decode_workspace_size",
     "gdn_attn_decode", "gdn_slot_map",
+    "gdn_attn_fwd_workspace_size", "gdn_attn_fwd", "gdn_attn_bwd_workspace_size", "gdn_attn_bwd",
+    "gdn_cache_write8", "gdn_cache_read8", "gdn_attn_decode8_workspace_size", "gdn_attn_decode8",
 )
 
 
@@ -116,6 +118,26 @@ class SlotProblem(ctypes.Structure):
                 ("n_tokens", ctypes.c_int64)]
 
 
+class AttnSeqProblem(ctypes.Structure):
+    """Mirror of ``gdn_attn_seq_problem`` (include/gdn.h)."""
+
+    _fields_ = [("dtype", ctypes.c_int32), ("D", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("n_seqs", ctypes.c_int64), ("Nq", ctypes.c_int64),
+                ("Nk", ctypes.c_int64), ("Hq", ctypes.c_int64), ("Hk", ctypes.c_int64),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64)]
+
+
+class Cache8Problem(ctypes.Structure):
+    """Mirror of ``gdn_cache8_problem`` (include/gdn.h)."""
+
+    _fields_ = [("dtype", ctypes.c_int32), ("D", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("B", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("Hk", ctypes.c_int64), ("pages", ctypes.c_int64),
+                ("max_blocks", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64)]
+
+
 _lock = threading.Lock()
 _lib = None
 _VP = ctypes.c_void_p
@@ -125,6 +147,8 @@ _CPP = ctypes.POINTER(ConvProblem)
 _RPP = ctypes.POINTER(RmsNormProblem)
 _ROPP = ctypes.POINTER(RopeProblem)
 _APP = ctypes.POINTER(AttnProblem)
+_ASP = ctypes.POINTER(AttnSeqProblem)
+_C8P = ctypes.POINTER(Cache8Problem)
 
 
 def load_library(path: str | None = None):
@@ -206,6 +230,17 @@ def load_library(path: str | None = None):
                                                ctypes.c_int),
             "gdn_attn_decode": ([_APP] + [_VP] * 8 + [ctypes.c_size_t, _VP, _VP], ctypes.c_int),
             "gdn_slot_map": ([ctypes.POINTER(SlotProblem)] + [_VP] * 11, ctypes.c_int),
+            "gdn_attn_fwd_workspace_size": ([_ASP, ctypes.POINTER(ctypes.c_size_t)],
+                                            ctypes.c_int),
+            "gdn_attn_fwd": ([_ASP] + [_VP] * 8 + [ctypes.c_size_t, _VP, _VP], ctypes.c_int),
+            "gdn_attn_bwd_workspace_size": ([_ASP, ctypes.POINTER(ctypes.c_size_t)],
+                                            ctypes.c_int),
+            "gdn_attn_bwd": ([_ASP] + [_VP] * 12 + [ctypes.c_size_t, _VP, _VP], ctypes.c_int),
+            "gdn_cache_write8": ([_C8P] + [_VP] * 11, ctypes.c_int),
+            "gdn_cache_read8": ([_C8P] + [_VP] * 10, ctypes.c_int),
+            "gdn_attn_decode8_workspace_size": ([_APP, ctypes.POINTER(ctypes.c_size_t)],
+                                                ctypes.c_int),
+            "gdn_attn_decode8": ([_APP] + [_VP] * 10 + [ctypes.c_size_t, _VP, _VP], ctypes.c_int),
         }
         for name, (args, res) in sig.items():
             fn = getattr(lib, name)
@@ -1143,3 +1178,185 @@ def gdn_slot_map(ctx_len, new_len, free_pages, block_table, *, page_size, pages,
           _arg("block_table", block_table, dev, i32, (B, blocks)), sp, cp, pp, lp, up,
           _status(status, dev), _raw_stream(stream, dev))
     return seq_len, cu_seqlens, positions, slots, used
+
+
+# ------------------------------- the full-attention layers over whole prompts, a cache in 8 bits
+
+CACHE8_BLOCK = 16  # tokens of a head that share a scale
+
+
+def _seq_problem(q, k, v, cu, cu_k, dev, causal, scale):
+    """(problem, addresses of q, k, v, cu_seqlens and cu_seqlens_k) for q [..., Hq, D] and k, v
+    [..., Hk, D], packed along their leading axes or, without offsets, a sequence per row."""
+    dt, sq, sk = q.dtype, q.shape, k.shape
+    if len(sq) not in (3, 4) or len(sk) != len(sq):
+        raise ValueError(f"expected q and k [tokens, heads, D] or [B, T, heads, D], got {list(sq)} "
+                         f"and {list(sk)}")
+    Hq, D = sq[-2:]
+    Hk = sk[-2]
+    Nq, Nk = sq[:-2].numel(), sk[:-2].numel()
+    cup = ckp = None
+    if cu is None:
+        if cu_k is not None:
+            raise ValueError("cu_seqlens_k without cu_seqlens")
+        n = sq[0] if len(sq) == 4 else 1
+        if len(sq) == 4 and sk[0] != n:
+            raise ValueError(f"q has {n} rows, k {sk[0]}")
+    else:
+        n = cu.numel() - 1
+        if n < 0:
+            raise ValueError("cu_seqlens: one offset at least")
+        cup = _flat("cu_seqlens", cu, dev, n + 1)
+        ckp = None if cu_k is None else _flat("cu_seqlens_k", cu_k, dev, n + 1)
+    qp, qs = _rows("q", q, dev, dt, sq)
+    kp, ks = _rows("k", k, dev, dt, sk[:-1] + (D,))
+    vp, vs = _rows("v", v, dev, dt, sk[:-1] + (D,))
+    return AttnSeqProblem(_dtype_code(dt), D, 1 if causal else 0, scale, n, Nq, Nk, Hq, Hk, qs,
+                          ks, vs), qp, kp, vp, cup, ckp
+
+
+def gdn_attn_fwd_workspace_size(problem: AttnSeqProblem) -> int:
+    n = ctypes.c_size_t(0)
+    _check("gdn_attn_fwd_workspace_size",
+           load_library().gdn_attn_fwd_workspace_size(problem, ctypes.byref(n)))
+    return n.value
+
+
+def gdn_attn_bwd_workspace_size(problem: AttnSeqProblem) -> int:
+    n = ctypes.c_size_t(0)
+    _check("gdn_attn_bwd_workspace_size",
+           load_library().gdn_attn_bwd_workspace_size(problem, ctypes.byref(n)))
+    return n.value
+
+
+def gdn_attn_fwd(q, k, v, cu_seqlens=None, cu_seqlens_k=None, *, causal=True, scale=0.0, o=None,
+                 lse=None, want_lse=True, ws=None, status=None, stream=None):
+    """Attention of packed sequences: q [Nq, Hq, D], k, v [Nk, Hk, D]; sequence b is the rows
+    cu_seqlens[b] .. cu_seqlens[b+1]-1 of q and those of cu_seqlens_k (None: the same) of k and v
+    (int32 on the device).  causal: the queries are the last of the sequence's keys, and see none
+    behind their own place.  Without offsets: one sequence, or q [B, T, Hq, D] and k, v
+    [B, Tk, Hk, D].  q, k, v may be slices of one projection.  Returns (o like q, contiguous, lse
+    [..., Hq] fp32 or None); rows behind the last sequence are left as they are."""
+    dev, dt = _device_of(q), q.dtype
+    p, qp, kp, vp, cup, ckp = _seq_problem(q, k, v, cu_seqlens, cu_seqlens_k, dev, causal, scale)
+    o, op = _out("o", o, dev, dt, q.shape, q.device, stream)
+    lp = None
+    if lse is not None or want_lse:
+        lse, lp = _out("lse", lse, dev, torch.float32, q.shape[:-1], q.device, stream)
+    n = gdn_attn_fwd_workspace_size(p) if ws is None else ws.numel()
+    ws, wsp = _out("ws", ws, dev, torch.uint8, (n,), q.device, stream)
+    _call("gdn_attn_fwd", dev, p, qp, kp, vp, cup, ckp, op, lp, wsp, n, _status(status, dev),
+          _raw_stream(stream, dev))
+    return o, lse
+
+
+def gdn_attn_bwd(q, k, v, o, lse, dO, cu_seqlens=None, cu_seqlens_k=None, *, causal=True,
+                 scale=0.0, dq=None, dk=None, dv=None, ws=None, status=None, stream=None):
+    """Backward of gdn_attn_fwd from its o and lse: (dq like q, dk, dv like k), contiguous."""
+    dev, dt = _device_of(q), q.dtype
+    p, qp, kp, vp, cup, ckp = _seq_problem(q, k, v, cu_seqlens, cu_seqlens_k, dev, causal, scale)
+    dq, dqp = _out("dq", dq, dev, dt, q.shape, q.device, stream)
+    dk, dkp = _out("dk", dk, dev, dt, k.shape, q.device, stream)
+    dv, dvp = _out("dv", dv, dev, dt, k.shape, q.device, stream)
+    n = gdn_attn_bwd_workspace_size(p) if ws is None else ws.numel()
+    ws, wsp = _out("ws", ws, dev, torch.uint8, (n,), q.device, stream)
+    _call("gdn_attn_bwd", dev, p, qp, kp, vp, _arg("o", o, dev, dt, q.shape),
+          _arg("lse", lse, dev, torch.float32, q.shape[:-1]), _arg("dO", dO, dev, dt, q.shape),
+          cup, ckp, dqp, dkp, dvp, wsp, n, _status(status, dev), _raw_stream(stream, dev))
+    return dq, dk, dv
+
+
+def _cache8(dev, k_cache, v_cache, k_scale, v_scale):
+    """(pages, page size, key heads, D, addresses of the caches and their scales)."""
+    pages, P, Hk, D = k_cache.shape
+    f8, sc = torch.float8_e4m3fn, (pages, P // CACHE8_BLOCK, Hk)
+    return pages, P, Hk, D, (_arg("k_cache", k_cache, dev, f8, k_cache.shape),
+                             _arg("v_cache", v_cache, dev, f8, k_cache.shape),
+                             _arg("k_scale", k_scale, dev, torch.float32, sc),
+                             _arg("v_scale", v_scale, dev, torch.float32, sc))
+
+
+def gdn_cache_write8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, ctx_len, cu_seqlens,
+                     *, status=None, stream=None):
+    """Quantises a step's keys and values, packed k, v [N, Hk, D], into the 8-bit paged caches
+    (float8_e4m3fn [pages, page_size, Hk, D], scales fp32 [pages, page_size / 16, Hk]), in place:
+    request b's rows cu_seqlens[b] .. cu_seqlens[b+1]-1 become its tokens from ctx_len[b] on,
+    in the pages of block_table (int32 [B, max_blocks]); the arguments and outputs of
+    gdn_slot_map.  k and v may be slices of one projection."""
+    dev, dt = _device_of(k), k.dtype
+    pages, P, Hk, D, cache = _cache8(dev, k_cache, v_cache, k_scale, v_scale)
+    N = k.shape[:-2].numel()
+    want = k.shape[:-2] + (Hk, D)
+    kp, ks = _rows("k", k, dev, dt, want)
+    vp, vs = _rows("v", v, dev, dt, want)
+    B, blocks = block_table.shape
+    p = Cache8Problem(_dtype_code(dt), D, P, 0, B, N, Hk, pages, blocks, ks, vs)
+    _call("gdn_cache_write8", dev, p, kp, vp,
+          _arg("block_table", block_table, dev, torch.int32, (B, blocks)),
+          _arg("ctx_len", ctx_len, dev, torch.int32, (B,)),
+          _arg("cu_seqlens", cu_seqlens, dev, torch.int32, (B + 1,)), *cache,
+          _status(status, dev), _raw_stream(stream, dev))
+
+
+def gdn_cache_read8(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, *, n_tokens=None,
+                    dtype=torch.bfloat16, k=None, v=None, status=None, stream=None):
+    """The cached keys and values of every request, from its first token on, in packed rows:
+    token j of request b in row cu_seqlens[b] + j of (k, v) [n_tokens, Hk, D] (the caller's, or new
+    ones of `dtype`; rows behind the last are left as they are)."""
+    dev = _device_of(k_cache)
+    pages, P, Hk, D, cache = _cache8(dev, k_cache, v_cache, k_scale, v_scale)
+    if k is not None:
+        n_tokens, dtype = k.shape[0], k.dtype
+    elif v is not None:
+        n_tokens, dtype = v.shape[0], v.dtype
+    elif n_tokens is None:
+        raise ValueError("gdn_cache_read8: n_tokens, or k or v, has to be given")
+    shape = (n_tokens, Hk, D)
+    k, kp = _out("k", k, dev, dtype, shape, k_cache.device, stream)
+    v, vp = _out("v", v, dev, dtype, shape, k_cache.device, stream)
+    B, blocks = block_table.shape
+    p = Cache8Problem(_dtype_code(dtype), D, P, 0, B, n_tokens, Hk, pages, blocks, 0, 0)
+    _call("gdn_cache_read8", dev, p, *cache,
+          _arg("block_table", block_table, dev, torch.int32, (B, blocks)),
+          _arg("cu_seqlens", cu_seqlens, dev, torch.int32, (B + 1,)), kp, vp,
+          _status(status, dev), _raw_stream(stream, dev))
+    return k, v
+
+
+def gdn_attn_decode8_workspace_size(problem: AttnProblem) -> int:
+    n = ctypes.c_size_t(0)
+    _check("gdn_attn_decode8_workspace_size",
+           load_library().gdn_attn_decode8_workspace_size(problem, ctypes.byref(n)))
+    return n.value
+
+
+_attn8_ws = {}  # workspace bytes by (head dim, type)
+
+
+def gdn_attn_decode8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len, *, scale=0.0,
+                     o=None, lse=None, want_lse=True, ws=None, status=None, stream=None):
+    """gdn_attn_decode over the 8-bit caches of gdn_cache_write8: q [B,Hq,D] bf16 or fp32.
+    Returns (o [B,Hq,D] in q's type, lse [B,Hq] fp32 or None)."""
+    dev, dt = _device_of(q), q.dtype
+    B, Hq, D = q.shape
+    qp, qs = _rows("q", q, dev, dt, q.shape)
+    pages, P, Hk, Dc, cache = _cache8(dev, k_cache, v_cache, k_scale, v_scale)
+    if Dc != D:
+        raise ValueError(f"q has heads of {D}, the caches of {Dc}")
+    blocks = block_table.shape[1]
+    p = AttnProblem(_dtype_code(dt), D, P, scale, B, Hq, Hk, pages, blocks, qs)
+    o, op = _out("o", o, dev, dt, (B, Hq, D), q.device, stream)
+    lp = None
+    if lse is not None or want_lse:
+        lse, lp = _out("lse", lse, dev, torch.float32, (B, Hq), q.device, stream)
+    if ws is not None:
+        n = ws.numel()
+    else:  # the size goes by D and the type alone
+        n = (_attn8_ws.get((D, dt))
+             or _attn8_ws.setdefault((D, dt), gdn_attn_decode8_workspace_size(p)))
+    ws, wsp = _out("ws", ws, dev, torch.uint8, (n,), q.device, stream)
+    _call("gdn_attn_decode8", dev, p, qp, *cache,
+          _arg("block_table", block_table, dev, torch.int32, (B, blocks)),
+          _arg("seq_len", seq_len, dev, torch.int32, (B,)), op, lp, wsp, n,
+          _status(status, dev), _raw_stream(stream, dev))
+    return o, lse

@@ -674,6 +674,130 @@ gdn_status gdn_slot_map(const gdn_slot_problem* p, const int32_t* ctx_len,
                         int32_t* seq_len, int32_t* cu_seqlens, int32_t* positions,
                         int32_t* slots, int32_t* used, int32_t* status, void* stream);
 
+/*
+ * ---- The full-attention layers over whole prompts, and a cache in 8 bits ----
+ *
+ * The full-attention layers of the hybrid model train on whole rows and take whole prompts in
+ * when they serve (gdn_attn_fwd, gdn_attn_bwd: between gdn_qk_norm_rope_fwd and its backward);
+ * served, their keys and values can be kept in 8 bits (gdn_cache_write8 behind
+ * gdn_qk_norm_rope_fwd, gdn_attn_decode8 for the single tokens, gdn_cache_read8 where a prompt
+ * goes on behind a cached context).  Alignment, indices in device memory and `status` as in the
+ * decode-step calls above.
+ */
+
+/*
+ * Attention of packed sequences.  Sequence b is the query rows cu_q[b] .. cu_q[b+1]-1 and the key
+ * rows cu_k[b] .. cu_k[b+1]-1; its query i (of nq) sees key j (of nk) when not causal, or when
+ * j <= i + nk - nq: the queries are the last tokens of a context of nk.  Query head h reads key
+ * head h / (Hq/Hk).  With s_ij = scale q_i.k_j over the keys that i sees:
+ *   lse_i = log sum_j exp(s_ij),   o_i = sum_j exp(s_ij - lse_i) v_j
+ * A query that sees no key: o = 0, lse = -inf.
+ * Backward, from the forward's o and lse:  p_ij = exp(s_ij - lse_i), delta_i = dO_i.o_i,
+ *   ds_ij = p_ij (dO_i.v_j - delta_i),  dq_i = scale sum_j ds_ij k_j,
+ *   dk_j = scale sum_i ds_ij q_i,  dv_j = sum_i p_ij dO_i   (i over the group's query heads too)
+ *  - q [Nq,Hq,D], k, v [Nk,Hk,D] in p->dtype with q_stride, k_stride, v_stride elements between
+ *    tokens (0: contiguous); o, dO, dq [Nq,Hq,D], dk, dv [Nk,Hk,D] contiguous; lse [Nq,Hq] fp32
+ *    (nullable in the forward).
+ *  - cu_q, cu_k int32 [n_seqs+1] in device memory; cu_k NULL: cu_q (Nk = Nq).  cu_q NULL (cu_k
+ *    too): the rows of q are n_seqs sequences of Nq / n_seqs, those of k n_seqs of Nk / n_seqs.
+ *    An offset outside the rows, or below the one before it, is raised or cut to the nearest that
+ *    is neither, and recorded in `status`.
+ *  - Rows of q, k, v that belong to no sequence have no influence, whatever they hold; rows of the
+ *    outputs that belong to no sequence are left as they were.  (A NaN or infinity in a key or
+ *    value row of a sequence may reach the queries of the same sequence that do not see it.)
+ *  - fp32 softmax and sums.  On bf16, p and ds are rounded to bf16 for their products.
+ *  - Deterministic: the same bits for the same call.
+ *  - Workspace 256-byte aligned; calls that can run at the same time need one each.
+ * Errors: null or misaligned pointer, sizes < 0, Hq % Hk != 0, n_seqs < 1 with rows given, cu_q
+ * NULL with rows that n_seqs does not divide or with a cu_k, cu_k NULL with Nk != Nq and cu_q
+ * given, a stride smaller than a token or no multiple of 16 bytes, a scale that is not finite or
+ * whose product with log2(e) is not: GDN_ERR_INVALID_ARG; D other than 64, 128 or 256, Nq Hq or
+ * Nk Hk >= 2^31, n_seqs > 2^20, a token stride of 2^31 elements or more: GDN_ERR_UNSUPPORTED;
+ * workspace smaller than asked: GDN_ERR_WORKSPACE.
+ */
+typedef struct gdn_attn_seq_problem {
+  int32_t dtype;   /* GDN_BF16 or GDN_FP32: every tensor but lse */
+  int32_t D;       /* head dim: 64, 128 or 256 */
+  int32_t causal;  /* 1: j <= i + nk - nq; 0: every key of the sequence */
+  float scale;     /* of the scores; <= 0 means 1/sqrt(D) */
+  int64_t n_seqs;
+  int64_t Nq, Nk;  /* token rows of q; of k and v */
+  int64_t Hq, Hk;  /* query heads; key and value heads */
+  int64_t q_stride, k_stride, v_stride;  /* elements between tokens; 0: contiguous */
+} gdn_attn_seq_problem;
+
+gdn_status gdn_attn_fwd_workspace_size(const gdn_attn_seq_problem* p, size_t* bytes);
+gdn_status gdn_attn_fwd(const gdn_attn_seq_problem* p, const void* q, const void* k,
+                        const void* v, const int32_t* cu_q, const int32_t* cu_k, void* o,
+                        float* lse, void* workspace, size_t workspace_bytes, int32_t* status,
+                        void* stream);
+gdn_status gdn_attn_bwd_workspace_size(const gdn_attn_seq_problem* p, size_t* bytes);
+gdn_status gdn_attn_bwd(const gdn_attn_seq_problem* p, const void* q, const void* k,
+                        const void* v, const void* o, const float* lse, const void* dO,
+                        const int32_t* cu_q, const int32_t* cu_k, void* dq, void* dk, void* dv,
+                        void* workspace, size_t workspace_bytes, int32_t* status, void* stream);
+
+/*
+ * A paged cache in 8 bits: k_cache, v_cache [pages][page_size][Hk][D] of e4m3 numbers and
+ * k_scale, v_scale [pages][page_size/16][Hk] fp32, one scale for 16 tokens of a head; the value of
+ * an element is its e4m3 number times the scale.
+ *
+ * gdn_cache_write8 writes a step's tokens: request b has ctx_len[b] tokens in the cache already
+ * and the packed rows cu_seqlens[b] .. cu_seqlens[b+1]-1 of k, v [N,Hk,D] (p->dtype) are its next
+ * ones; token j is row j % page_size of page block_table[b][j / page_size] (gdn_slot_map's ctx_len,
+ * cu_seqlens and block_table).  A block's scale is the smallest power of two, 2^-100 at least,
+ * with 448 scale >= |x| for every new element x of the block and head.  If the block holds earlier
+ * tokens of the request, it is at least the scale that they have; if it grew, they are requantised
+ * (a power of two: exact but for numbers that fall below e4m3's smallest normal one).  Elements
+ * are rounded to the nearest, ties to even.  One that is not finite is stored as NaN and does not
+ * count for the scale.  No other row or scale is written.
+ *
+ * gdn_cache_read8 reads it back: token j of request b to row cu_seqlens[b] + j of k, v [N,Hk,D],
+ * cu_seqlens[b+1] - cu_seqlens[b] tokens of each request from its first (exact in p->dtype, but
+ * that numbers from 248 2^120 on, stored as 2^128, are infinite); rows behind the last are left as
+ * they were.
+ *  - A token of write8 whose page is missing (past max_blocks, or a page outside [0, pages)) is
+ *    left out, in read8 it reads zeros; both are recorded in `status`, as are offsets outside
+ *    [0, N] or below the one before them (raised or cut) and a negative ctx_len (taken as 0).
+ *  - Pages that a call writes belong to one request each.
+ *  - One launch, no workspace.
+ * Errors: null or misaligned pointer, sizes < 0, page_size < 1, a stride smaller than a token or
+ * no multiple of 16 bytes: GDN_ERR_INVALID_ARG; D other than 64, 128 or 256, page_size no multiple
+ * of 16, pages page_size or max_blocks page_size >= 2^31, N Hk >= 2^31, B > 2^20:
+ * GDN_ERR_UNSUPPORTED.
+ */
+typedef struct gdn_cache8_problem {
+  int32_t dtype;      /* GDN_BF16 or GDN_FP32: k and v */
+  int32_t D;          /* head dim: 64, 128 or 256 */
+  int32_t page_size;  /* tokens per page, a multiple of 16 */
+  int32_t reserved;   /* 0 */
+  int64_t B, N, Hk;   /* requests, packed token rows, key heads */
+  int64_t pages;      /* pages of each cache */
+  int64_t max_blocks; /* entries per row of block_table */
+  int64_t k_stride, v_stride; /* write8: elements between tokens; 0: contiguous */
+} gdn_cache8_problem;
+
+gdn_status gdn_cache_write8(const gdn_cache8_problem* p, const void* k, const void* v,
+                            const int32_t* block_table, const int32_t* ctx_len,
+                            const int32_t* cu_seqlens, void* k_cache, void* v_cache,
+                            float* k_scale, float* v_scale, int32_t* status, void* stream);
+gdn_status gdn_cache_read8(const gdn_cache8_problem* p, const void* k_cache, const void* v_cache,
+                           const float* k_scale, const float* v_scale,
+                           const int32_t* block_table, const int32_t* cu_seqlens, void* k,
+                           void* v, int32_t* status, void* stream);
+
+/*
+ * gdn_attn_decode over that cache: the same call with k_cache and v_cache in e4m3 and their
+ * scales; q and o in p->dtype.  The softmax weights go into their product with v in f16, rounded
+ * (bf16 q: 2^-11 of a weight) or as two terms (fp32 q).  Errors as gdn_attn_decode.
+ */
+gdn_status gdn_attn_decode8_workspace_size(const gdn_attn_problem* p, size_t* bytes);
+gdn_status gdn_attn_decode8(const gdn_attn_problem* p, const void* q, const void* k_cache,
+                            const void* v_cache, const float* k_scale, const float* v_scale,
+                            const int32_t* block_table, const int32_t* seq_len, void* o,
+                            float* lse, void* workspace, size_t workspace_bytes,
+                            int32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
