@@ -532,7 +532,8 @@ Layout layout(const gdn_attn_seq_problem* p, bool bwd, int rq, int rk) {
 Layout layout_of(const gdn_attn_seq_problem* p, bool bwd) {
   if (p->dtype != GDN_BF16) return layout(p, bwd, ST, ST);
   const TcPlan tp = tc_plan(p->D);
-  return bwd ? layout(p, true, tp.dq_rows, tp.dkv_rows) : layout(p, false, tp.fwd_rows, ST);
+  return bwd ? layout(p, true, tp.dq_rows, tp.dkv_rows)
+             : layout(p, false, tp.fwd_rows / tc_pack(p->Hq / p->Hk), ST);
 }
 
 // Arguments that both calls share, their checks, and the schedule's launch.
@@ -557,7 +558,8 @@ gdn_status begin(const gdn_attn_seq_problem* p, bool bwd, const int32_t* cu_q,
   const Layout y = layout_of(p, bwd);
   const bool bf16 = p->dtype == GDN_BF16;
   const TcPlan tp = tc_plan(p->D);
-  a->tq.rows = bf16 ? (bwd ? tp.dq_rows : tp.fwd_rows) : ST;
+  a->pack = tc_pack(a->G);
+  a->tq.rows = bf16 ? (bwd ? tp.dq_rows : tp.fwd_rows / a->pack) : ST;
   a->tk.rows = bf16 ? tp.dkv_rows : ST;
   a->tq.most = y.mq;
   a->tk.most = y.mk;

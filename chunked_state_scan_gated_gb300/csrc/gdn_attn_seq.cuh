@@ -34,6 +34,7 @@ struct Tiles {
 struct SeqArgs {
   int64_t Nq, Nk, qs, ks, vs;  // rows; elements between tokens
   int n_seqs, Hq, Hk, G, causal;
+  int pack;  // bf16 forward: query heads of a key head that share a tile, a row per token and head
   float scale, sl;  // of the scores; times log2(e)
   const void *q, *k, *v, *o, *dO;
   const int32_t *cuq, *cuk;
@@ -111,6 +112,8 @@ __device__ __forceinline__ float ex2(float x) {
 struct TcPlan {
   int fwd_rows, dq_rows, dkv_rows;  // rows per tile
 };
+// Query heads that share a tile of the forward: the largest power of two, up to 16, in the group.
+inline int tc_pack(int64_t G) { return G % 16 == 0 ? 16 : G % 8 == 0 ? 8 : G % 4 == 0 ? 4 : G % 2 == 0 ? 2 : 1; }
 TcPlan tc_plan(int D);
 cudaError_t launch_fwd_tc(const SeqArgs& a, int D, cudaStream_t st);
 cudaError_t launch_bwd_tc(const SeqArgs& a, int D, cudaStream_t st);

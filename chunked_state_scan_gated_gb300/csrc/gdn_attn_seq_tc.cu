@@ -25,7 +25,7 @@
 namespace gdn {
 
 bool tc_make_map_tokens(CUtensorMap* m, const void* ptr, int64_t N, int64_t stride, int64_t heads,
-                        int D, int rows);
+                        int D, int rows, int pack);
 
 namespace seq {
 namespace {
@@ -38,6 +38,39 @@ constexpr float kLazy = 8.f;                // log2 units
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// A shared-memory descriptor as its two words: steps along an operand change the low one only.
+struct Desc {
+  uint32_t lo, hi;
+  __device__ __forceinline__ explicit Desc(uint64_t d) : lo((uint32_t)d), hi((uint32_t)(d >> 32)) {}
+  __device__ __forceinline__ uint64_t at(uint32_t bytes) const {
+    return ((uint64_t)hi << 32) | (lo + (bytes >> 4));
+  }
+};
+
+// K columns of two K-major operands, whose groups of 64 columns are A and B bytes apart.
+template <int K, int A, int B>
+__device__ __forceinline__ void mma_rows(uint32_t to, const Desc& a, uint32_t a0, const Desc& b,
+                                         uint32_t b0, uint32_t id, bool more, uint32_t issue) {
+#pragma unroll
+  for (int k = 0; k < K / 16; ++k)
+    mma_ss(to, a.at(a0 + (k >> 2) * A + (k & 3) * 32), b.at(b0 + (k >> 2) * B + (k & 3) * 32), id,
+           k > 0 || more, issue);
+}
+// Steps [K0, K1) of 16 rows of an MN-major operand (of `steps` in all), weighed with the weights in
+// TMEM.
+template <int K0, int K1>
+__device__ __forceinline__ void mma_weights(uint32_t to, uint32_t w, const Desc& b, uint32_t b0,
+                                            uint32_t id, int steps, bool more, uint32_t issue) {
+  if (steps >= K1) {
+#pragma unroll
+    for (int k = K0; k < K1; ++k) mma_ts(to, w + k * 8, b.at(b0 + k * 2048), id, k > 0 || more, issue);
+  } else {
+#pragma unroll 1
+    for (int k = K0; k < steps; ++k)
+      mma_ts(to, w + k * 8, b.at(b0 + k * 2048), id, k > 0 || more, issue);
+  }
 }
 
 // Rows [from, to) of a streamed block set to zero: rows of another sequence (or of none) whose
@@ -53,11 +86,30 @@ __device__ __forceinline__ void zero_rows(uint8_t* block, int atoms, int atom_by
   fence_proxy_async();
 }
 
+struct Bars {
+  uint64_t r_full, r_empty, full[8], empty[8], s_full[2], p_full[2], p_rest[2], pv[2], o_full[2],
+      o_empty[2], l_full[2], drained;
+  uint32_t tmem;
+  int gave_up;
+};
+static_assert(sizeof(Bars) <= 512, "");
+
+// A CTA that gave up ends only when its copies have landed: those of its last own tile, and the
+// ring's stages, of which those up to `stage` were filled in this turn, the others in the last.
+__device__ inline void drain(Bars& bar, int works, int stages, int stage, int turn) {
+  if (works > 0) mbar_wait(&bar.r_full, (works - 1) & 1, nullptr, 0);
+  for (int i = 0; i < stages; ++i)
+    if (i < stage || turn > 0)
+      mbar_wait(&bar.full[i], (i < stage ? turn : turn - 1) & 1, nullptr, 0);
+}
+
 // ------------------------------------------------------------------------- forward and dv
 
 // D <= 128: two tiles share every streamed block, each with one buffer of S: while one tile's
 // softmax runs, the tensor cores work for the other.  D = 256: the accumulator of one tile leaves
-// room for two buffers of S, which alternate.
+// room for two buffers of S, which alternate.  Two warpgroups do the softmax (one for each tile, or
+// for half of the tile's columns each), one writes results, one issues copies and products.
+// setmaxnreg: the registers of a thread, which sum up to no more than the launch's.
 template <int D>
 struct Flash {
   static constexpr int kTiles = D <= 128 ? 2 : 1;
@@ -68,25 +120,92 @@ struct Flash {
   static constexpr int kTile = TR * D * 2;
   static constexpr int kRaw = (kSmem - kHead - kTiles * kTile) / kStage;
   static constexpr int kStages = kRaw < 8 ? kRaw : 8;
-  static constexpr int kThreads = kTiles * 128 + 64;
+  static constexpr int kThreads = 512;
   static constexpr int kBytes = kHead + kTiles * kTile + kStages * kStage;
+  static constexpr int kSoftRegs = 192, kEndRegs = 64, kIssueRegs = 64;  // of 4 x 128
 };
-
-struct Bars {
-  uint64_t r_full, full[10], empty[10], s_full[2], p_full[2], pv[2], o_full[2], drained;
-  uint32_t tmem;
-  int gave_up;
-};
-static_assert(sizeof(Bars) <= 512, "");
-
-// A CTA that gave up ends only when its copies have landed: the ring's stages up to `stage` were
-// filled in this turn, the others in the one before.
-__device__ inline void drain(Bars& bar, int stages, int stage, int turn) {
-  mbar_wait(&bar.r_full, 0, nullptr, 0);
-  for (int i = 0; i < stages; ++i)
-    if (i < stage || turn > 0)
-      mbar_wait(&bar.full[i], (i < stage ? turn : turn - 1) & 1, nullptr, 0);
+template <int N> __device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
+template <int N> __device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// (x, y) = (x, y) m + c, two at once.
+__device__ __forceinline__ void fma2(float& x, float& y, float m, float c) {
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %2};\n"
+      " mov.b64 d, {%3, %3};\n fma.rn.f32x2 a, a, b, d;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "+f"(x), "+f"(y) : "f"(m), "f"(c));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n"
+      " add.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "+f"(x), "+f"(y) : "f"(a), "f"(b));
+}
+
+// One CTA's share of the work: items of the sorted list, in turns that change direction, so that
+// the CTAs end together.
+struct Turns {
+  int round = -1, total;
+  __device__ __forceinline__ explicit Turns(int n) : total(n) {}
+  __device__ __forceinline__ int next() {  // -1: none left
+    while (true) {
+      ++round;
+      const int64_t first = (int64_t)round * gridDim.x;
+      if (first >= total) return -1;
+      const int64_t i = first + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      if (i < total) return (int)i;
+    }
+  }
+};
+
+// An item of k_flash: kTiles tiles of one sequence and head (or key head), the blocks that they
+// stream and those [lo, hi) that each tile takes.
+template <int D, bool FWD>
+struct Item {
+  using F = Flash<D>;
+  Tile t;
+  int head, hk;    // the first query head (FWD), the key head
+  int n, per, j0;  // iterations; of one query head; the first block
+  int lo0, lo1, hi0, hi1;
+  __device__ __forceinline__ int lo(int i) const { return i ? lo1 : lo0; }
+  __device__ __forceinline__ int hi(int i) const { return i ? hi1 : hi0; }
+  __device__ __forceinline__ bool find(const SeqArgs& a, int idx) {
+    const int groups = FWD ? a.Hq / a.pack : a.Hk, part = idx % groups;
+    if (!tile_of<!FWD>(a, idx / groups, &t)) return false;
+    head = FWD ? part * a.pack : part * a.G;
+    hk = head / a.G;
+    const int side = FWD ? t.nq : t.nk, rows = FWD ? TR / a.pack : TR;
+    lo0 = lo1 = hi0 = hi1 = 0;
+#pragma unroll
+    for (int i = 0; i < F::kTiles; ++i) {
+      Tile x = t;
+      x.at += i * rows;
+      if (x.at >= side) continue;
+      int from = 0, to;
+      if (FWD) {
+        to = (keys_seen(a, x, rows) + 127) / 128;
+      } else {
+        to = (t.nq + 127) / 128;
+        from = min(to, first_query(a, x) / 128);
+      }
+      (i ? lo1 : lo0) = from;
+      (i ? hi1 : hi0) = to;
+    }
+    j0 = lo0;
+    per = max(hi0, hi1) - j0;
+    n = FWD ? per : per * a.G;
+    return true;
+  }
+  __device__ __forceinline__ void make_uniform() {
+    for (int* v : {&t.q0, &t.nq, &t.k0, &t.nk, &t.at, &n, &per, &j0, &lo0, &lo1, &hi0, &hi1})
+      *v = uniform(*v);
+  }
+  // whether tile i takes block j (of the sequence's)
+  __device__ __forceinline__ bool takes(int i, int j) const { return j >= lo(i) && j < hi(i); }
+  __device__ __forceinline__ bool works(int i) const { return lo(i) < hi(i); }
+  __device__ __forceinline__ int after(int j) const { return j + 1 == j0 + per ? j0 : j + 1; }
+};
 
 template <int D, bool FWD>
 __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
@@ -94,14 +213,18 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
             const __grid_constant__ CUtensorMap m2, SeqArgs a) {
   using F = Flash<D>;
   constexpr int NT = F::kTiles, NC = F::kChunks, ST = F::kStages;
+  static_assert(FWD || NT == 1, "row_values");
   extern __shared__ __align__(1024) uint8_t sm[];
   Bars& bar = *reinterpret_cast<Bars*>(sm);
-  float* row_values = reinterpret_cast<float*>(sm + 512);  // dv: [tile][2][128] lse2
+  float* row_values = reinterpret_cast<float*>(sm + 512);  // dv: [2][128] lse2
+  float* row_tops = row_values;                            // forward, D = 256: [2][half][128]
+  float* row_factors = reinterpret_cast<float*>(sm + (NT == 1 ? 2560 : 512));  // [tile][128] 1 / l
   uint8_t *own = sm + kHead, *ring = own + NT * F::kTile;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31, group = warp >> 2;
 
   if (tid == 0) {
     mbar_init(&bar.r_full, 1);
+    mbar_init(&bar.r_empty, 1);
     for (int i = 0; i < ST; ++i) {
       mbar_init(&bar.full[i], 1);
       mbar_init(&bar.empty[i], 1);
@@ -109,8 +232,11 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.s_full[i], 1);
       mbar_init(&bar.p_full[i], 4);
+      mbar_init(&bar.p_rest[i], 4);
       mbar_init(&bar.pv[i], 1);
       mbar_init(&bar.o_full[i], 1);
+      mbar_init(&bar.o_empty[i], 4);
+      mbar_init(&bar.l_full[i], 4);
     }
     mbar_init(&bar.drained, 1);
     bar.gave_up = 0;
@@ -122,311 +248,426 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
   before_next();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = bar.tmem;
+  const uint32_t tmem = uniform(bar.tmem);
   // columns: S 0 and 1 at 0 and 128, then the accumulators
   auto acc_of = [&](int t) { return tmem + 256 + t * D; };
   auto wait = [&](uint64_t* b, uint32_t parity) { wait_for(b, parity, a.status, &bar.gave_up); };
-
   if (FWD && blockIdx.x == 0 && tid == 0) check_single(a);
-  const int heads = FWD ? a.Hq : a.Hk, hh = blockIdx.x % heads, hk = FWD ? hh / a.G : hh;
-  Tile t;
-  int n = 0, per = 0;            // iterations; of one query head
-  int j0 = 0, lo[2] = {0, 0}, hi[2] = {0, 0};  // blocks: the first, and a tile's [lo, hi)
-  const bool some = tile_of<!FWD>(a, blockIdx.x / heads, &t);
-  if (some) {
-    const int side = FWD ? t.nq : t.nk;
-#pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      Tile x = t;
-      x.at += i * TR;
-      if (x.at >= side) continue;
-      if (FWD) {
-        hi[i] = (keys_seen(a, x, TR) + 127) / 128;
-      } else {
-        lo[i] = first_query(a, x) / 128;
-        hi[i] = (t.nq + 127) / 128;
-        if (lo[i] > hi[i]) lo[i] = hi[i];
-      }
-    }
-    j0 = lo[0];
-    per = (FWD && NT == 2 ? max(hi[0], hi[1]) : hi[0]) - j0;
-    n = FWD ? per : per * a.G;
-  }
-  const int xrows = FWD ? t.nk : t.nq, xfirst = FWD ? t.k0 : t.q0;  // the streamed side
-  // whether tile i takes part in block j (of the sequence's)
-  auto takes = [&](int i, int j) { return j >= lo[i] && j < hi[i]; };
-  // the place of an iteration's second operand in the ring, in blocks
-  auto place2 = [&](int it) { return NT == 2 || it == n - 1 ? 2 * it + 1 : 2 * it + 2; };
+  Turns turns((FWD ? a.tq.most : a.tk.most) * (FWD ? a.Hq / a.pack : a.Hk));
+  Item<D, FWD> x;
 
-  if (warp == NT * 4 && lane == 0 && n > 0) {
-    // ---- copies
-    const int row0 = (FWD ? t.q0 : t.k0) + t.at;
-    mbar_arrive_expect_tx(&bar.r_full, NT * F::kTile);
-    for (int i = 0; i < NT; ++i)
-      for (int c = 0; c < D / 64; ++c)
-        tma_load_3d(own + i * F::kTile + c * 16384, &mr, c * 64, hh, row0 + i * TR, &bar.r_full);
-    int stage = 0, turn = 0;
-    auto block = [&](const CUtensorMap* m, int g, int j) {
-      for (int c = 0; c < NC; ++c) {
-        if (turn > 0) wait(&bar.empty[stage], (turn - 1) & 1);
-        if (bar.gave_up) return;
-        mbar_arrive_expect_tx(&bar.full[stage], F::kStage);
-        for (int x = 0; x < F::kAtoms; ++x)
-          tma_load_3d(ring + stage * F::kStage + x * 16384, m, c * F::kCols + x * 64,
-                      FWD ? hk : hh * a.G + g, xfirst + j * 128, &bar.full[stage]);
+  if (group == 3) {
+    fewer_registers<F::kIssueRegs>();
+    if (warp == 12 && lane == 0) {
+      // ---- copies
+      int stage = 0, turn = 0, works = 0;
+      for (int idx; (idx = turns.next()) >= 0 && !bar.gave_up;) {
+        if (!x.find(a, idx) || x.n == 0) continue;
+        const int rows = FWD ? TR / a.pack : TR;
+        if (works > 0) wait(&bar.r_empty, (works - 1) & 1);
+        ++works;
+        mbar_arrive_expect_tx(&bar.r_full, NT * F::kTile);
+        for (int i = 0; i < NT; ++i)
+          for (int c = 0; c < D / 64; ++c)
+            tma_load_3d(own + i * F::kTile + c * 16384, &mr, c * 64, FWD ? x.head : x.hk,
+                        (FWD ? x.t.q0 : x.t.k0) + x.t.at + i * rows, &bar.r_full);
+        auto block = [&](const CUtensorMap* m, int g, int j) {
+          for (int c = 0; c < NC; ++c) {
+            if (turn > 0) wait(&bar.empty[stage], (turn - 1) & 1);
+            if (bar.gave_up) return;
+            mbar_arrive_expect_tx(&bar.full[stage], F::kStage);
+            for (int y = 0; y < F::kAtoms; ++y)
+              tma_load_3d(ring + stage * F::kStage + y * 16384, m, c * F::kCols + y * 64,
+                          FWD ? x.hk : x.head + g, (FWD ? x.t.k0 : x.t.q0) + j * 128,
+                          &bar.full[stage]);
+            if (++stage == ST) stage = 0, ++turn;
+          }
+        };
+        int g1 = 0, j1 = x.j0, g2 = 0, j2 = x.j0;
+        auto first = [&]() {
+          block(&m1, g1, j1);
+          if ((j1 = x.after(j1)) == x.j0) ++g1;
+        };
+        auto second = [&]() {
+          block(&m2, g2, j2);
+          if ((j2 = x.after(j2)) == x.j0) ++g2;
+        };
+        for (int it = 0; it <= x.n; ++it) {
+          if (NT == 2 && it > 0) second();
+          if (it < x.n) first();
+          if (NT == 1 && it > 0) second();
+        }
+      }
+      if (bar.gave_up) drain(bar, works, ST, stage, turn);
+    } else if (warp == 13) {
+      // ---- products
+      const uint32_t issue = elected();
+      const uint32_t base = smem_u32(sm);
+      const Desc kmaj(sdesc(base, 16, 1024)), mnmaj(sdesc(base, 16384, 1024));
+      constexpr uint32_t kOwn = kHead, kRing = kHead + NT * F::kTile;
+      int stage = 0, turn = 0, items = 0, works = 0;
+      int weights[2] = {0, 0}, scored = 0;  // parities of a tile's weights; blocks (NT = 1)
+      auto next = [&]() {
         if (++stage == ST) stage = 0, ++turn;
-      }
-    };
-    int g1 = 0, j1 = j0, g2 = 0, j2 = j0;
-    auto first = [&]() {
-      block(&m1, g1, j1);
-      if (++j1 == j0 + per) j1 = j0, ++g1;
-    };
-    auto second = [&]() {
-      block(&m2, g2, j2);
-      if (++j2 == j0 + per) j2 = j0, ++g2;
-    };
-    for (int it = 0; it <= n; ++it) {
-      if (NT == 2 && it > 0) second();
-      if (it < n) first();
-      if (NT == 1 && it > 0) second();
-    }
-    if (bar.gave_up) drain(bar, ST, stage, turn);
-  } else if (warp == NT * 4 + 1 && lane == 0 && n > 0) {
-    // ---- products
-    const uint32_t base = smem_u32(sm);
-    const uint64_t kmaj = sdesc(base, 16, 1024), mnmaj = sdesc(base, 16384, 1024);
-    auto at = [&](const uint8_t* p) { return (uint64_t)((smem_u32(p) - base) >> 4); };
-    int stage = 0, turn = 0;
-    auto next = [&]() {
-      if (++stage == ST) stage = 0, ++turn;
-    };
-    wait(&bar.r_full, 0);
-    // 16-row steps of block j that hold rows of the sequence
-    auto steps = [&](int j) { return min(8, (xrows - j * 128 + 15) / 16); };
-    auto scores = [&](int i, int buf, int c, int j) {  // the contraction's columns c kCols ..
-      const uint32_t id = idesc_bf16(128, steps(j) * 16, 0, 0);
-#pragma unroll
-      for (int k = 0; k < F::kCols / 16; ++k)
-        mma_bf16(tmem + buf * 128,
-                 kmaj + at(own + i * F::kTile + c * F::kAtoms * 16384) +
-                     (((k >> 2) * 16384 + (k & 3) * 32) >> 4),
-                 kmaj + at(ring + stage * F::kStage) + (((k >> 2) * 16384 + (k & 3) * 32) >> 4),
-                 id, c > 0 || k > 0);
-    };
-    auto weigh = [&](int i, int buf, int c, int j, bool more) {  // output columns c kCols ..
-      const int ks = steps(j);
-      for (int k = 0; k < ks; ++k)
-        mma_bf16_ts(acc_of(i) + c * F::kCols, tmem + buf * 128 + k * 8,
-                    mnmaj + at(ring + stage * F::kStage) + ((k * 2048) >> 4),
-                    idesc_bf16(128, F::kCols, 0, 1), more || k > 0);
-    };
-    if constexpr (NT == 2) {
-      int ps[2] = {0, 0};  // weights consumed
-      int j = j0;          // of iteration it
-      int before = j0;     // of iteration it - 1
-      for (int it = 0; it <= n; ++it) {
-        const int s2 = stage, t2 = turn;
-        if (it > 0) next();
-        const int s1 = stage, t1 = turn;
-        if (it < n) next();
-        const int s_end = stage, t_end = turn;
-        if (it > 0) wait(&bar.full[s2], t2 & 1);
-        for (int i = 0; i < 2; ++i) {
-          if (it > 0 && takes(i, before)) {
-            wait(&bar.p_full[i], ps[i] & 1);
-            tc_fence_after();
-            stage = s2;
-            weigh(i, i, 0, before, ps[i] > 0);
-            ++ps[i];
-            const bool last = FWD ? before == hi[i] - 1 : it == n;
-            if (last) mma_commit(&bar.o_full[i]);
-          }
-          if (it < n && takes(i, j)) {
-            wait(&bar.full[s1], t1 & 1);
-            stage = s1;
+      };
+      for (int idx; (idx = turns.next()) >= 0;) {
+        if (!uniform(x.find(a, idx))) continue;
+        x.make_uniform();
+        ++items;
+        if (x.n == 0) continue;
+        const int xrows = FWD ? x.t.nk : x.t.nq;
+        wait(&bar.r_full, works & 1);
+        ++works;
+        // 16-row steps of block j that hold rows of the sequence
+        auto steps = [&](int j) { return min(8, (xrows - j * 128 + 15) / 16); };
+        auto scores = [&](int i, int buf, int c, int j) {  // the contraction's columns c kCols ..
+          mma_rows<F::kCols, 16384, 16384>(tmem + buf * 128, kmaj,
+                                           kOwn + i * F::kTile + c * F::kAtoms * 16384, kmaj,
+                                           kRing + stage * F::kStage,
+                                           idesc_bf16(128, steps(j) * 16, 0, 0), c > 0, issue);
+        };
+        // output columns c kCols .., by the first half of the weights or the rest
+        constexpr uint32_t kId = idesc_bf16(128, F::kCols, 0, 1);
+        auto weigh0 = [&](int i, int buf, int c, int ks, bool more) {
+          mma_weights<0, 4>(acc_of(i) + c * F::kCols, tmem + buf * 128, mnmaj,
+                            kRing + stage * F::kStage, kId, ks, more, issue);
+        };
+        auto weigh1 = [&](int i, int buf, int c, int ks) {
+          mma_weights<4, 8>(acc_of(i) + c * F::kCols, tmem + buf * 128, mnmaj,
+                            kRing + stage * F::kStage, kId, ks, true, issue);
+        };
+        if constexpr (NT == 2) {
+          // forward: tile i takes the blocks [0, last[i]); the ring holds K 0, V 0, K 1, V 1, ..
+          const int last[2] = {x.hi0, x.hi1};
+          auto score = [&](int i, int j) {
             scores(i, i, 0, j);
-            mma_commit(&bar.s_full[i]);
+            commit_to(&bar.s_full[i], issue);
+          };
+          wait(&bar.full[stage], turn & 1);
+          if (last[0] > 0) score(0, 0);
+          if (last[1] > 0) score(1, 0);
+          commit_to(&bar.empty[stage], issue);
+          if (x.n == 1) commit_to(&bar.r_empty, issue);
+          next();
+          if (items > 1) {  // the accumulators of the item before have been read
+            wait(&bar.o_empty[0], items & 1);
+            wait(&bar.o_empty[1], items & 1);
           }
-        }
-        if (it > 0) mma_commit(&bar.empty[s2]);
-        if (it < n) mma_commit(&bar.empty[s1]);
-        stage = s_end;
-        turn = t_end;
-        before = j;
-        if (++j == j0 + per) j = j0;
-      }
-    } else {
-      int j = j0, before = j0;
-      for (int it = 0; it <= n; ++it) {
-        if (it < n) {
-          for (int c = 0; c < NC; ++c) {
-            wait(&bar.full[stage], turn & 1);
-            scores(0, it & 1, c, j);
-            mma_commit(&bar.empty[stage]);
+          for (int it = 0; it < x.n; ++it) {
+            const int sv = stage, ks = steps(it);
+            wait(&bar.full[sv], turn & 1);
             next();
-          }
-          mma_commit(&bar.s_full[it & 1]);
-        }
-        if (it > 0) {
-          const int w = it - 1;
-          wait(&bar.p_full[w & 1], (w >> 1) & 1);
-          tc_fence_after();
-          for (int c = 0; c < NC; ++c) {
-            wait(&bar.full[stage], turn & 1);
-            weigh(0, w & 1, c, before, w > 0);
-            mma_commit(&bar.empty[stage]);
-            next();
-          }
-          mma_commit(it == n ? &bar.o_full[0] : &bar.pv[w & 1]);
-        }
-        before = j;
-        if (++j == j0 + per) j = j0;
-      }
-    }
-    if (bar.gave_up) {  // products in flight end before the TMEM is given back
-      mma_commit(&bar.drained);
-      mbar_wait(&bar.drained, 0, nullptr, 0);
-    }
-  } else if (warp < NT * 4 && some) {
-    // ---- softmax: a thread per row
-    const int i = warp >> 2, r = tid & 127, at = t.at + i * TR;  // tile, row of it
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const int off = t.nk - t.nq, first_row = at + (warp & 3) * 32, row = at + r;
-    float m = -INFINITY, l = 0.f;  // reference (log2 units) and this row's sum
-    float ahead = 0.f;             // dv: the next block's lse2 of query r
-    int done = 0, g = 0, j = j0;
-    auto value = [&](int gg, int jj) {
-      const int q = jj * 128 + r;
-      return q < t.nq ? a.lse2[(int64_t)(hh * a.G + gg) * a.Nq + t.q0 + q] : INFINITY;
-    };
-    if (!FWD && n > 0 && lo[i] < hi[i]) ahead = value(0, lo[i]);
-    for (int it = 0; it < n; ++it) {
-      const int jj = j, gg = g;
-      if (++j == j0 + per) j = j0, ++g;
-      if (!takes(i, jj)) continue;
-      const int buf = NT == 2 ? i : done & 1, kb = jj * 128;
-      const uint32_t parity = NT == 2 ? done & 1 : (done >> 1) & 1;
-      float* lv = row_values + (i * 2 + (done & 1)) * 128;
-      if (!FWD) {
-        lv[r] = ahead;
-        bar_sync(1 + i, 128);
-        if (it + 1 < n) ahead = jj + 1 < hi[i] ? value(gg, jj + 1) : value(gg + 1, lo[i]);
-      }
-      wait(&bar.s_full[buf], parity);
-      tc_fence_after();
-      float s[128];
-      tmem_ld128(tmem + lanes + buf * 128, s);
-      // columns [c0, c1) of the row count
-      int c0 = 0, c1 = 128;
-      bool whole;
-      if (FWD) {
-        c1 = (a.causal ? min(t.nk, row + off + 1) : t.nk) - kb;
-        whole = kb + 128 <= (a.causal ? min(t.nk, first_row + off + 1) : t.nk);
-      } else {
-        c1 = t.nq - kb;
-        if (a.causal) c0 = row - off - kb;
-        whole = kb + 128 <= t.nq && (!a.causal || first_row + 31 - off <= kb);
-      }
-      if (!whole) {
+            const int sk = stage, tk = turn;
+            const bool ahead = it + 1 < x.n;
 #pragma unroll
-        for (int c = 0; c < 128; ++c) s[c] = c >= c0 && c < c1 ? s[c] : -INFINITY;
-      }
-      uint32_t p[64];
-      if (FWD) {
-        float mx = s[0];
-#pragma unroll
-        for (int c = 1; c < 128; ++c) mx = fmaxf(mx, s[c]);
-        mx *= a.sl;
-        // The reference follows the maximum only when a score is above it by kLazy: weights up to
-        // 2^kLazy lose nothing, and the accumulator stays where it is for most blocks.
-        const bool up = mx > m + kLazy;
-        if (__any_sync(0xffffffffu, up)) {
-          const float to = up ? mx : m, f = up ? ex2(m - to) : 1.f;
-          l *= f;
-          m = to;
-          if (done > 0) {
-            if (NT == 1) wait(&bar.pv[(done - 1) & 1], ((done - 1) >> 1) & 1);
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              float x[32];
-              tmem_ld32(acc_of(i) + lanes + c, x);
-              uint32_t y[32];
-#pragma unroll
-              for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(x[e] * f);
-              tmem_st32(acc_of(i) + lanes + c, y);
+            for (int i = 0; i < 2; ++i) {
+              if (it >= last[i]) continue;
+              wait(&bar.p_full[i], weights[i]);
+              tc_fence_after();
+              stage = sv;
+              weigh0(i, i, 0, ks, it > 0);
+              wait(&bar.p_rest[i], weights[i]);
+              weights[i] ^= 1;
+              tc_fence_after();
+              weigh1(i, i, 0, ks);
+              if (it + 1 < last[i]) {
+                wait(&bar.full[sk], tk & 1);
+                stage = sk;
+                score(i, it + 1);
+              } else {
+                commit_to(&bar.o_full[i], issue);
+              }
+            }
+            commit_to(&bar.empty[sv], issue);
+            stage = sk;
+            if (ahead) {
+              commit_to(&bar.empty[sk], issue);
+              if (it + 2 == x.n) commit_to(&bar.r_empty, issue);
+              next();
             }
           }
-        }
-        const float base = m == -INFINITY ? 0.f : m;
-        float sum0 = 0.f, sum1 = 0.f;
+        } else {
+          // the ring holds X1 0, X1 1, X2 0, X1 2, X2 1, ..
+          int ahead = x.j0, j = x.j0;  // blocks of the next S and of the next accumulation
+          auto score = [&](int it) {
+            const int buf = (scored + it) & 1;
 #pragma unroll
-        for (int c = 0; c < 128; c += 2) {
-          const float x = ex2(fmaf(s[c], a.sl, -base)), y = ex2(fmaf(s[c + 1], a.sl, -base));
-          sum0 += x;
-          sum1 += y;
-          p[c / 2] = bf16x2(x, y);
-        }
-        l += sum0 + sum1;
-      } else {
+            for (int c = 0; c < NC; ++c) {
+              wait(&bar.full[stage], turn & 1);
+              scores(0, buf, c, ahead);
+              commit_to(&bar.empty[stage], issue);
+              next();
+            }
+            commit_to(&bar.s_full[buf], issue);
+            if (it == x.n - 1) commit_to(&bar.r_empty, issue);
+            ahead = x.after(ahead);
+          };
+          score(0);
+          if (x.n > 1) score(1);
+          if (items > 1) wait(&bar.o_empty[0], items & 1);  // the item before has been read
+          for (int it = 0; it < x.n; ++it) {
+            const int w = scored + it, buf = w & 1, ks = steps(j);
+            wait(&bar.p_full[buf], (w >> 1) & 1);
+            wait(&bar.p_rest[buf], (w >> 1) & 1);
+            tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < 128; c += 4) {
-          const float4 v = *reinterpret_cast<const float4*>(lv + c);
-          const float x = ex2(fmaf(s[c], a.sl, -v.x)), y = ex2(fmaf(s[c + 1], a.sl, -v.y));
-          const float z = ex2(fmaf(s[c + 2], a.sl, -v.z)), w = ex2(fmaf(s[c + 3], a.sl, -v.w));
-          p[c / 2] = bf16x2(x, y);
-          p[c / 2 + 1] = bf16x2(z, w);
+            for (int c = 0; c < NC; ++c) {
+              wait(&bar.full[stage], turn & 1);
+              mma_weights<0, 8>(acc_of(0) + c * F::kCols, tmem + buf * 128, mnmaj,
+                                kRing + stage * F::kStage, kId, ks, it > 0, issue);
+              commit_to(&bar.empty[stage], issue);
+              next();
+            }
+            commit_to(&bar.pv[buf], issue);
+            if (it == x.n - 1) commit_to(&bar.o_full[0], issue);
+            if (it + 2 < x.n) score(it + 2);
+            j = x.after(j);
+          }
+          scored += x.n;
         }
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t y[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e) y[e] = p[h * 32 + e];
-        tmem_st32(tmem + lanes + buf * 128 + h * 32, y);
+      if (bar.gave_up) {  // products in flight end before the TMEM is given back
+        commit_to(&bar.drained, issue);
+        mbar_wait(&bar.drained, 0, nullptr, 0);
       }
-      if (kb + 128 > xrows && (xrows & 15)) {  // rows behind the sequence in its last 16
-        const int from = xrows - kb, to = (from + 15) & ~15;
-        for (int c = 0; c < NC; ++c) {
-          const int x = place2(it) * NC + c;
-          wait(&bar.full[x % ST], (x / ST) & 1);
-          zero_rows<128>(ring + (x % ST) * F::kStage, F::kAtoms, 16384, from, to, r);
-        }
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.p_full[buf]);
-      ++done;
     }
-    // ---- the row's result
-    if (done > 0) {
-      wait(&bar.o_full[i], 0);
-      tc_fence_after();
-    }
-    const int side = FWD ? t.nq : t.nk;
-    const int64_t out = (int64_t)((FWD ? t.q0 : t.k0) + row) * heads + hh;
-    const float f = FWD ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
-    __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(FWD ? a.out : a.dv) + out * D;
+  } else if (group == 2) {
+    // ---- results: a thread per row
+    fewer_registers<F::kEndRegs>();
+    const int r = tid & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    int items = 0, works[2] = {0, 0};
+    for (int idx; (idx = turns.next()) >= 0;) {
+      if (!x.find(a, idx)) continue;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const int row = FWD ? x.t.at + (i * TR + r) / a.pack : x.t.at + i * TR + r;
+        const int side = FWD ? x.t.nq : x.t.nk;
+        const int64_t out =
+            FWD ? (int64_t)(x.t.q0 + row) * a.Hq + x.head + (a.pack > 1 ? r % a.pack : 0)
+                : (int64_t)(x.t.k0 + row) * a.Hk + x.hk;
+        float f = 1.f;
+        if (FWD) {
+          wait(&bar.l_full[i], items & 1);
+          f = row_factors[i * 128 + r];
+        }
+        const bool work = x.works(i);
+        if (work) {
+          wait(&bar.o_full[i], works[i] & 1);
+          ++works[i];
+          tc_fence_after();
+        }
+        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(FWD ? a.out : a.dv) + out * D;
 #pragma unroll 1
-    for (int c = 0; c < D; c += 32) {
-      float x[32];
-      if (done > 0) {
-        tmem_ld32(acc_of(i) + lanes + c, x);
-      } else {
+        for (int c = 0; c < D; c += 32) {
+          float y[32];
+          if (work) {
+            tmem_ld32(acc_of(i) + lanes + c, y);
+          } else {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = 0.f;
+            for (int e = 0; e < 32; ++e) y[e] = 0.f;
+          }
+          if (c == D - 32) {  // read: the next item may accumulate
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.o_empty[i]);
+          }
+          if (row < side)
+#pragma unroll
+            for (int e = 0; e < 32; e += 8)
+              *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(
+                  bf16x2(y[e] * f, y[e + 1] * f), bf16x2(y[e + 2] * f, y[e + 3] * f),
+                  bf16x2(y[e + 4] * f, y[e + 5] * f), bf16x2(y[e + 6] * f, y[e + 7] * f));
+        }
       }
-      if (row < side)
-#pragma unroll
-        for (int e = 0; e < 32; e += 8)
-          *reinterpret_cast<uint4*>(dst + c + e) =
-              make_uint4(bf16x2(x[e] * f, x[e + 1] * f), bf16x2(x[e + 2] * f, x[e + 3] * f),
-                         bf16x2(x[e + 4] * f, x[e + 5] * f), bf16x2(x[e + 6] * f, x[e + 7] * f));
+      ++items;
     }
-    if (FWD && a.lse && row < side)
-      a.lse[out] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  } else {
+    // ---- softmax: a thread per row, or per row and half of its columns
+    more_registers<F::kSoftRegs>();
+    constexpr int N = NT == 2 ? 128 : 64;  // columns of a thread
+    const int i = NT == 2 ? group : 0, half = NT == 2 ? 0 : group;
+    const int r = tid & 127;  // row of the tile
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    int items = 0, done = 0;  // done: blocks of the tile so far, of all items
+    int placed = 0;           // blocks of the ring in front of this item
+    for (int idx; (idx = turns.next()) >= 0;) {
+      if (!x.find(a, idx)) continue;
+      const int rows = FWD ? TR / a.pack : TR, at = x.t.at + i * rows, off = x.t.nk - x.t.nq;
+      const int w0 = (warp & 3) * 32;  // the warp's rows: tokens first .. last
+      const int first = FWD ? at + w0 / a.pack : at + w0;
+      const int last = FWD ? at + (w0 + 31) / a.pack : first + 31;
+      const int row = FWD ? at + r / a.pack : at + r;
+      const int xrows = FWD ? x.t.nk : x.t.nq;
+      float m = -INFINITY, l = 0.f;  // reference (log2 units) and the sum of this thread's weights
+      float ahead = 0.f;             // dv: the next block's lse2 of query r
+      auto value = [&](int g, int j) {
+        const int q = j * 128 + r;
+        return q < x.t.nq ? a.lse2[(int64_t)(x.head + g) * a.Nq + x.t.q0 + q] : INFINITY;
+      };
+      if (!FWD && x.n > 0) ahead = value(0, x.lo(i));
+      int g = 0, j = x.j0;
+      bool begun = false;
+      for (int it = 0; it < x.n; ++it) {
+        const int jj = j;
+        if ((j = x.after(j)) == x.j0) ++g;
+        if (!x.takes(i, jj)) continue;
+        const int buf = NT == 2 ? i : done & 1, kb = jj * 128;
+        const uint32_t parity = NT == 2 ? done & 1 : (done >> 1) & 1;
+        const uint32_t ts = tmem + lanes + buf * 128;
+        float* lv = row_values + (done & 1) * 128;
+        if (!FWD) {
+          if (half == 0) lv[r] = ahead;
+          bar_sync(1, 256);
+          if (it + 1 < x.n) ahead = value(g, j);
+        }
+        wait(&bar.s_full[buf], parity);
+        tc_fence_after();
+        float s[N];
+        {
+          float s0[64];
+          tmem_ld_begin(ts + half * 64, s0);
+          if constexpr (N == 128) {
+            float s1[64];
+            tmem_ld_begin(ts + 64, s1);
+            tmem_ld_end(s0);
+            tmem_ld_end(s1);
+#pragma unroll
+            for (int c = 0; c < 64; ++c) s[64 + c] = s1[c];
+          } else {
+            tmem_ld_end(s0);
+          }
+#pragma unroll
+          for (int c = 0; c < 64; ++c) s[c] = s0[c];
+        }
+        // columns [c0, c1) of the row count
+        int c0 = 0, c1 = 128;
+        bool whole;
+        if (FWD) {
+          c1 = (a.causal ? min(x.t.nk, row + off + 1) : x.t.nk) - kb;
+          whole = kb + 128 <= (a.causal ? min(x.t.nk, first + off + 1) : x.t.nk);
+        } else {
+          c1 = x.t.nq - kb;
+          if (a.causal) c0 = row - off - kb;
+          whole = kb + 128 <= x.t.nq && (!a.causal || last - off <= kb);
+        }
+        if (!whole) {
+#pragma unroll
+          for (int c = 0; c < N; ++c)
+            s[c] = half * 64 + c >= c0 && half * 64 + c < c1 ? s[c] : -INFINITY;
+        }
+        float base = 0.f, sum0 = 0.f, sum1 = 0.f, sum2 = 0.f, sum3 = 0.f;
+        if (FWD) {
+          float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int c = 4; c < N - 4; c += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[e] = fmaxf(fmaxf(mx[e], s[c + e]), s[c + e + 4]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[N - 4 + e]);
+          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.sl;
+          if constexpr (NT == 1) {  // the other half's; both halves of S have been read then
+            float* tops = row_tops + (done & 1) * 256;
+            tops[half * 128 + r] = top;
+            bar_sync(1 + (warp & 3), 64);
+            top = fmaxf(top, tops[(1 - half) * 128 + r]);
+          }
+          // The reference follows the maximum only when a score is above it by kLazy: weights up
+          // to 2^kLazy lose nothing, and the accumulator stays where it is for most blocks.
+          const bool up = top > m + kLazy;
+          if (__any_sync(0xffffffffu, up)) {
+            const float to = up ? top : m, f = up ? ex2(m - to) : 1.f;
+            l *= f;
+            m = to;
+            if (begun) {
+              if (NT == 1) wait(&bar.pv[(done - 1) & 1], ((done - 1) >> 1) & 1);
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = half * (D / 2); c < (NT == 1 ? (half + 1) * (D / 2) : D); c += 16) {
+                float y[16];
+                uint32_t z[16];
+                tmem_ld16(acc_of(i) + lanes + c, y);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) z[e] = __float_as_uint(y[e] * f);
+                tmem_st16(acc_of(i) + lanes + c, z);
+              }
+            }
+          }
+          base = m == -INFINITY ? 0.f : m;
+        } else {
+          bar_sync(2 + (warp & 3), 64);  // both halves of S have been read
+        }
+        if (kb + 128 > xrows && (xrows & 15)) {  // rows behind the sequence in its last 16
+          const int from = xrows - kb, to = (from + 15) & ~15;
+          const int place = placed + (NT == 2 || it == x.n - 1 ? 2 * it + 1 : 2 * it + 2);
+          for (int c = 0; c < NC; ++c) {
+            const int y = place * NC + c;
+            wait(&bar.full[y % ST], (y / ST) & 1);
+            zero_rows<NT == 2 ? 128 : 256>(ring + (y % ST) * F::kStage, F::kAtoms, 16384, from, to,
+                                           NT == 2 ? r : tid);
+          }
+        }
+        // the weights, 32 columns at a time; the product begins when the first 64 are there
+#pragma unroll
+        for (int q = 0; q < N / 32; ++q) {
+          uint32_t y[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            float* z = s + q * 32 + e;
+            if (FWD) {
+              fma2(z[0], z[1], a.sl, -base);
+              fma2(z[2], z[3], a.sl, -base);
+            } else {
+              const float4 v = *reinterpret_cast<const float4*>(lv + half * 64 + q * 32 + e);
+              z[0] = fmaf(z[0], a.sl, -v.x);
+              z[1] = fmaf(z[1], a.sl, -v.y);
+              z[2] = fmaf(z[2], a.sl, -v.z);
+              z[3] = fmaf(z[3], a.sl, -v.w);
+            }
+            z[0] = ex2(z[0]);
+            z[1] = ex2(z[1]);
+            z[2] = ex2(z[2]);
+            z[3] = ex2(z[3]);
+            if (FWD) {
+              add2(sum0, sum1, z[0], z[1]);
+              add2(sum2, sum3, z[2], z[3]);
+            }
+            y[e / 2] = bf16x2(z[0], z[1]);
+            y[e / 2 + 1] = bf16x2(z[2], z[3]);
+          }
+          tmem_st16(ts + half * 32 + q * 16, y);
+          if (q & 1) {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q == 1 && half == 0 ? &bar.p_full[buf] : &bar.p_rest[buf]);
+          }
+        }
+        l += (sum0 + sum1) + (sum2 + sum3);
+        begun = true;
+        ++done;
+      }
+      placed += 2 * x.n;
+      if (FWD) {
+        if constexpr (NT == 1) {  // the other half's sum, with no block left to use the place
+          float* tops = row_tops + (done & 1) * 256;
+          tops[half * 128 + r] = l;
+          bar_sync(1 + (warp & 3), 64);
+          l += tops[(1 - half) * 128 + r];
+          bar_sync(1 + (warp & 3), 64);
+        }
+        if (half == 0) {
+          if (items > 0) wait(&bar.o_empty[i], (items - 1) & 1);  // the last one's were read
+          row_factors[i * 128 + r] = l != 0.f ? 1.f / l : 0.f;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.l_full[i]);
+          if (a.lse && row < x.t.nq)
+            a.lse[(int64_t)(x.t.q0 + row) * a.Hq + x.head + r % a.pack] =
+                l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        }
+      }
+      ++items;
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -483,7 +724,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
   Bars& bar = *reinterpret_cast<Bars*>(sm);
   float* row_values = reinterpret_cast<float*>(sm + 512);  // dk: [2][lse2, delta][BN]
   uint8_t *own = sm + kHead, *ring = own + 2 * F::kTile;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
 
   if (tid == 0) {
     mbar_init(&bar.r_full, 1);
@@ -507,14 +748,15 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   // columns: S (two buffers, or one), dP, the accumulators
-  const uint32_t tmem = bar.tmem, t_dp = tmem + (BOTH ? 1 : 2) * BN, t_acc = t_dp + BN;
+  const uint32_t tmem = uniform(bar.tmem), t_dp = tmem + (BOTH ? 1 : 2) * BN, t_acc = t_dp + BN;
   auto wait = [&](uint64_t* b, uint32_t parity) { wait_for(b, parity, a.status, &bar.gave_up); };
 
   const int heads = DQ ? a.Hq : a.Hk, hh = blockIdx.x % heads, hk = DQ ? hh / a.G : hh;
   Tile t;
   int n = 0, per = 0, j0 = 0;
-  const bool some = tile_of<!DQ>(a, blockIdx.x / heads, &t);
+  const bool some = uniform(tile_of<!DQ>(a, blockIdx.x / heads, &t));
   if (some) {
+    for (int* v : {&t.q0, &t.nq, &t.k0, &t.nk, &t.at}) *v = uniform(*v);
     if (DQ) {
       per = (keys_seen(a, t, TR) + BN - 1) / BN;
     } else {
@@ -548,45 +790,39 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
       for (int i = max(0, it - ST); i < it; ++i)
         for (int x = 0; x < 2; ++x) mbar_wait(&bar.full[F::stage(x, i)], F::parity(x, i), nullptr, 0);
     }
-  } else if ((warp == 9 || warp == 10) && lane == 0 && n > 0) {
+  } else if ((warp == 9 || warp == 10) && n > 0) {
+    const uint32_t issue = elected();
     const uint32_t base = smem_u32(sm);
-    const uint64_t kmaj = sdesc(base, 16, 1024), mnmaj = sdesc(base, F::kAtom, 1024);
-    auto at = [&](const uint8_t* p) { return (uint64_t)((smem_u32(p) - base) >> 4); };
+    const Desc kmaj(sdesc(base, 16, 1024)), mnmaj(sdesc(base, F::kAtom, 1024));
+    constexpr uint32_t kOwn = kHead, kRing = kHead + 2 * F::kTile;
     auto steps = [&](int j) { return min(BN / 16, (xrows - j * BN + 15) / 16); };
     wait(&bar.r_full, 0);
     // S (x = 0) or dP (x = 1) of iteration it: the own tile x with the streamed operand x
     auto scores = [&](uint32_t to, int x, int it, int j) {
       const int stage = F::stage(x, it);
       wait(&bar.full[stage], F::parity(x, it));
-      const uint32_t id = idesc_bf16(128, steps(j) * 16, 0, 0);
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        mma_bf16(to, kmaj + at(own + x * F::kTile) + (((k >> 2) * 16384 + (k & 3) * 32) >> 4),
-                 kmaj + at(ring + stage * F::kStage) +
-                     (((k >> 2) * F::kAtom + (k & 3) * 32) >> 4),
-                 id, k > 0);
+      mma_rows<D, 16384, F::kAtom>(to, kmaj, kOwn + x * F::kTile, kmaj, kRing + stage * F::kStage,
+                                   idesc_bf16(128, steps(j) * 16, 0, 0), false, issue);
     };
     // an accumulation: the bf16 weights at `w` with the streamed operand x of iteration it, whose
     // last use it is
     auto weigh = [&](uint32_t to, uint32_t w, int x, int it, int j) {
       const int ks = steps(j), stage = F::stage(x, it);
-      for (int k = 0; k < ks; ++k)
-        mma_bf16_ts(to, w + k * 8,
-                    mnmaj + at(ring + stage * F::kStage) + ((k * 2048) >> 4),
-                    idesc_bf16(128, D, 0, 1), it > 0 || k > 0);
-      mma_commit(&bar.empty[stage]);
+      mma_weights<0, BN / 16>(to, w, mnmaj, kRing + stage * F::kStage, idesc_bf16(128, D, 0, 1), ks,
+                              it > 0, issue);
+      commit_to(&bar.empty[stage], issue);
     };
     int j = j0;
     auto after = [&](int j) { return j + 1 == j0 + per ? j0 : j + 1; };
     auto score0 = [&](int it, int j) {  // S, in its buffer
       const int buf = BOTH ? 0 : it & 1;
       scores(tmem + buf * BN, 0, it, j);
-      mma_commit(&bar.s_full[buf]);
+      commit_to(&bar.s_full[buf], issue);
     };
     auto score1 = [&](int it, int j) {  // dP
       scores(t_dp, 1, it, j);
-      mma_commit(&bar.pv[0]);
-      if (!BOTH) mma_commit(&bar.empty[F::stage(1, it)]);
+      commit_to(&bar.pv[0], issue);
+      if (!BOTH) commit_to(&bar.empty[F::stage(1, it)], issue);
     };
     if constexpr (BOTH) {
       if (warp == 9) {
@@ -602,7 +838,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
           tc_fence_after();
           weigh(t_acc, t_dp, 0, it, j);
           if (it + 1 < n) score1(it + 1, j1);
-          else mma_commit(&bar.o_full[0]);
+          else commit_to(&bar.o_full[0], issue);
           j = j1;
         }
       }
@@ -620,13 +856,13 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
         tc_fence_after();
         if (it + 1 < n) score1(it + 1, j1);
         weigh(t_acc, tmem + (it & 1) * BN, 0, it, j);
-        if (it + 1 == n) mma_commit(&bar.o_full[0]);
+        if (it + 1 == n) commit_to(&bar.o_full[0], issue);
         if (!F::kTight && it + 2 < n) score0(it + 2, after(j1));
         j = j1;
       }
     }
     if (bar.gave_up) {
-      mma_commit(&bar.drained);
+      commit_to(&bar.drained, issue);
       mbar_wait(&bar.drained, 0, nullptr, 0);
     }
   } else if (warp < 8 && some) {
@@ -789,20 +1025,26 @@ struct Maps {
   CUtensorMap q, k, v, d;
 };
 bool make(CUtensorMap* m, const void* p, int64_t n, int64_t stride, int64_t heads, int D,
-          int rows) {
-  return tc_make_map_tokens(m, p, n, stride, heads, D, rows);
+          int rows, int pack = 1) {
+  return tc_make_map_tokens(m, p, n, stride, heads, D, rows, pack);
+}
+
+// CTAs of k_flash, one per SM, each of which takes several items.
+int64_t ctas_of(int64_t items) {
+  const int64_t sms = device_sms();
+  return items < sms ? items : sms;
 }
 
 template <int D>
 cudaError_t fwd(const SeqArgs& a, cudaStream_t st) {
   CUtensorMap q, k, v;
-  if (!make(&q, a.q, a.Nq, a.qs, a.Hq, D, 128)) return cudaErrorInvalidValue;
+  if (!make(&q, a.q, a.Nq, a.qs, a.Hq, D, TR / a.pack, a.pack)) return cudaErrorInvalidValue;
   k = v = q;
   if (a.Nk > 0 && (!make(&k, a.k, a.Nk, a.ks, a.Hk, D, 128) ||
                    !make(&v, a.v, a.Nk, a.vs, a.Hk, D, 128)))
     return cudaErrorInvalidValue;
-  return launch(k_flash<D, true>, (int64_t)a.tq.most * a.Hq, Flash<D>::kThreads,
-                Flash<D>::kBytes, st, q, k, v, a);
+  return launch(k_flash<D, true>, ctas_of((int64_t)a.tq.most * (a.Hq / a.pack)),
+                Flash<D>::kThreads, Flash<D>::kBytes, st, q, k, v, a);
 }
 
 template <int D>
@@ -828,7 +1070,7 @@ cudaError_t bwd(const SeqArgs& a, cudaStream_t st) {
                            Slope<D>::kBytes, st, k, v, qb, db, a);
     if (e != cudaSuccess) return e;
     if constexpr (D == 256) {
-      e = launch(k_flash<D, false>, ctas, Flash<D>::kThreads, Flash<D>::kBytes, st, k, q, d, a);
+      e = launch(k_flash<D, false>, ctas_of(ctas), Flash<D>::kThreads, Flash<D>::kBytes, st, k, q, d, a);
       if (e != cudaSuccess) return e;
     }
   }
@@ -841,7 +1083,7 @@ cudaError_t bwd(const SeqArgs& a, cudaStream_t st) {
 
 TcPlan tc_plan(int D) {
   const int two = D == 64 ? Flash<64>::kTiles : D == 128 ? Flash<128>::kTiles : Flash<256>::kTiles;
-  return TcPlan{two * TR, TR, TR};
+  return TcPlan{two * TR, TR, TR};  // fwd: rows, of which `pack` belong to a token
 }
 cudaError_t launch_fwd_tc(const SeqArgs& a, int D, cudaStream_t st) {
   return D == 64 ? fwd<64>(a, st) : D == 128 ? fwd<128>(a, st) : fwd<256>(a, st);

@@ -68,15 +68,15 @@ bool tc_make_map_rows(CUtensorMap* m, const void* ptr, int64_t B, int64_t T, int
              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Token-major rows [N][heads][D] with `stride` elements between tokens, boxes of `rows` tokens x 64
-// columns of one head, 128-byte swizzle.
+// Token-major rows [N][heads][D] with `stride` elements between tokens, boxes of `rows` tokens x
+// `pack` heads x 64 columns (a row per token and head), 128-byte swizzle.
 bool tc_make_map_tokens(CUtensorMap* m, const void* ptr, int64_t N, int64_t stride, int64_t heads,
-                        int D, int rows) {
+                        int D, int rows, int pack) {
   EncodeTiledFn enc = encode_fn();
-  if (!enc || rows < 1 || rows > 256) return false;
+  if (!enc || rows < 1 || rows > 256 || pack < 1 || pack > 256) return false;
   cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)N};
   cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
-  cuuint32_t box[3] = {64, 1, (cuuint32_t)rows};
+  cuuint32_t box[3] = {64, (cuuint32_t)pack, (cuuint32_t)rows};
   cuuint32_t es[3] = {1, 1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box,
              es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
