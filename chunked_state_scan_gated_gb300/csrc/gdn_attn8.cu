@@ -32,10 +32,13 @@ struct Cache<Q8<TO>> {
   template <int D> static constexpr int el() { return D == 64 ? 8 : 16; }
 };
 
-template <typename TO> struct Cfg<64, Q8<TO>, 1> : Fit<64, 4, 1> {};
-template <typename TO> struct Cfg<128, Q8<TO>, 1> : Fit<32, 3, 1> {};
-template <typename TO> struct Cfg<256, Q8<TO>, 1> : Fit<16, 2, 1> {};
-template <typename TO> struct Cfg<64, Q8<TO>, 2> : Fit<64, 3, 1> {};
+// 4 KB of K and of V to a warp's tile (8 KB at D = 256): what is on its way per SM, 64 KB, and the
+// work per tile weigh against each other (131001 tokens, 8 heads of 128: 16 keys and 4 CTAs 56.3 us,
+// 32 and 3 57.8, 32 and 2 55.0; 812,553 tokens, 2 heads of 256: 16 and 2 159, 32 and 2 149).
+template <typename TO> struct Cfg<64, Q8<TO>, 1> : Fit<32, 4, 1> {};
+template <typename TO> struct Cfg<128, Q8<TO>, 1> : Fit<32, 2, 1> {};
+template <typename TO> struct Cfg<256, Q8<TO>, 1> : Fit<32, 2, 1> {};
+template <typename TO> struct Cfg<64, Q8<TO>, 2> : Fit<32, 3, 1> {};
 template <typename TO> struct Cfg<128, Q8<TO>, 2> : Fit<32, 2, 1> {};
 template <typename TO> struct Cfg<256, Q8<TO>, 2> : Fit<16, 2, 1> {};
 

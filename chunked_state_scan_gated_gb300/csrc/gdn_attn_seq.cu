@@ -519,12 +519,13 @@ struct Layout {
 Layout layout(const gdn_attn_seq_problem* p, bool bwd, int rq, int rk) {
   Layout y;
   const int64_t n = p->n_seqs;
+  const bool lists = n > 1;  // one sequence needs none
   // every sequence ends in one tile that may be partly empty
   y.mq = (int)(p->Nq / rq + (n < p->Nq ? n : p->Nq));
   y.mk = (int)(p->Nk / rk + (n < p->Nk ? n : p->Nk));
-  y.lq = 256;
-  y.lk = up(y.lq + y.mq * sizeof(Tile));
-  y.lse2 = bwd ? up(y.lk + y.mk * sizeof(Tile)) : y.lk;
+  y.lq = lists ? 256 : 0;
+  y.lk = lists ? up(y.lq + y.mq * sizeof(Tile)) : 0;
+  y.lse2 = lists && bwd ? up(y.lk + y.mk * sizeof(Tile)) : y.lk;
   y.delta = y.lse2 + (bwd ? up((size_t)p->Nq * p->Hq * 4) : 0);
   y.total = y.delta + (bwd ? up((size_t)p->Nq * p->Hq * 4) : 0);
   return y;
@@ -596,17 +597,13 @@ auto with_dim(int D, F f) {
   return D == 64 ? f(D64()) : D == 128 ? f(D128()) : f(D256());
 }
 
-template <typename K>
-cudaError_t launch_simt(K kernel, int64_t grid, int threads, size_t smem, cudaStream_t st,
+template <auto kKernel>
+cudaError_t launch_simt(int64_t grid, int threads, size_t smem, cudaStream_t st,
                         const SeqArgs& a) {
   if (grid == 0) return cudaSuccess;
-  cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return e;
-  }
-  return launch_behind(kernel, dim3((unsigned)grid), threads, smem, st, a);
+  const cudaError_t e = allow_smem<kKernel>(smem);
+  if (e != cudaSuccess) return e;
+  return launch_behind(kKernel, dim3((unsigned)grid), threads, smem, st, a);
 }
 
 }  // namespace
@@ -637,7 +634,7 @@ gdn_status gdn_attn_fwd(const gdn_attn_seq_problem* p, const void* q, const void
   if (!ok16(q, p->Nq) || !ok16(o, p->Nq) || !ok16(k, p->Nk) || !ok16(v, p->Nk) ||
       !aligned16(lse) || ((uintptr_t)workspace & 255u) != 0 || ((uintptr_t)status & 255u) != 0)
     return GDN_ERR_INVALID_ARG;
-  if (!workspace || workspace_bytes < need) return GDN_ERR_WORKSPACE;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
   if (p->Nq == 0) return GDN_OK;
   cudaStream_t st = (cudaStream_t)stream;
   SeqArgs a;
@@ -649,8 +646,8 @@ gdn_status gdn_attn_fwd(const gdn_attn_seq_problem* p, const void* q, const void
   a.lse = lse;
   const cudaError_t e = p->dtype == GDN_BF16 ? launch_fwd_tc(a, p->D, st)
                                              : with_dim(p->D, [&](auto d) {
-    return launch_simt(k_attn_fwd_simt<d(), float>, (int64_t)a.tq.most * a.Hq, F_NT,
-                       fwd_smem<d()>(), st, a);
+    return launch_simt<k_attn_fwd_simt<d(), float>>((int64_t)a.tq.most * a.Hq, F_NT,
+                                                    fwd_smem<d()>(), st, a);
   });
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
@@ -675,7 +672,7 @@ gdn_status gdn_attn_bwd(const gdn_attn_seq_problem* p, const void* q, const void
       !ok16(dq, p->Nq) || !ok16(k, p->Nk) || !ok16(v, p->Nk) || !ok16(dk, p->Nk) ||
       !ok16(dv, p->Nk) || ((uintptr_t)workspace & 255u) != 0 || ((uintptr_t)status & 255u) != 0)
     return GDN_ERR_INVALID_ARG;
-  if (!workspace || workspace_bytes < need) return GDN_ERR_WORKSPACE;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return GDN_ERR_WORKSPACE;
   if (p->Nq + p->Nk == 0) return GDN_OK;
   cudaStream_t st = (cudaStream_t)stream;
   SeqArgs a;
@@ -701,11 +698,11 @@ gdn_status gdn_attn_bwd(const gdn_attn_seq_problem* p, const void* q, const void
                : launch_behind(k_attn_rows<D, float>, dim3(grid), 256, 0, st, a);
     if (e != cudaSuccess) return e;
     if (bf16) return launch_bwd_tc(a, D, st);
-    e = launch_simt(k_attn_bwd_simt<D, float, true>, (int64_t)a.tk.most * a.Hk, B_NT,
-                    bwd_smem<D, true>(), st, a);
+    e = launch_simt<k_attn_bwd_simt<D, float, true>>((int64_t)a.tk.most * a.Hk, B_NT,
+                                                     bwd_smem<D, true>(), st, a);
     if (e != cudaSuccess) return e;
-    return launch_simt(k_attn_bwd_simt<D, float, false>, (int64_t)a.tq.most * a.Hq, B_NT,
-                       bwd_smem<D, false>(), st, a);
+    return launch_simt<k_attn_bwd_simt<D, float, false>>((int64_t)a.tq.most * a.Hq, B_NT,
+                                                         bwd_smem<D, false>(), st, a);
   });
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }

@@ -686,48 +686,79 @@ struct Slope {
   static constexpr int kRaw = (kSmem - kHead - 2 * kTile) / kStage;
   static constexpr int kStages = kRaw < 8 ? kRaw : 8;
   // Three stages only (D = 256): two for X1 and one for X2, in place of one ring for both; S is
-  // then issued by a thread of its own, as its X1 arrives last.
+  // then issued by a warp of its own, as its X1 arrives last.
   static constexpr bool kTight = kStages < 4;
-  static constexpr int kThreads = 256 + (kTight ? 96 : 64);
+  static constexpr int kThreads = 512;
   static constexpr int kBytes = kHead + 2 * kTile + kStages * kStage;
-  // stage and parity of operand x (0: X1, 1: X2) of iteration it
-  static __device__ __forceinline__ int stage(int x, int it) {
-    return kTight ? (x ? 2 : it & 1) : (2 * it + x) % kStages;
-  }
-  static __device__ __forceinline__ uint32_t parity(int x, int it) {
-    return (kTight ? (x ? it : it >> 1) : (2 * it + x) / kStages) & 1;
-  }
-  // whether the stage held something before
-  static __device__ __forceinline__ bool used(int x, int it) {
-    return kTight ? it >= 2 - x : 2 * it + x >= kStages;
-  }
 };
 
 // What a call computes: dq of queries; dk of keys; dk and dv of keys, where TMEM has room for both
 // accumulators (D <= 128): one pass of four products in place of 3 + 2.
 enum Kind { kDq, kDk, kDkv };
 
+// An item of k_slope: a tile of one sequence and head (or key head), and its iterations.
+template <int D, bool DQ>
+struct SlopeItem {
+  Tile t;
+  int head, hk;    // the (first) query head, the key head
+  int n, per, j0;  // iterations; of one query head; the first block
+  __device__ __forceinline__ bool find(const SeqArgs& a, int idx) {
+    constexpr int BN = Slope<D>::kBlock;
+    const int heads = DQ ? a.Hq : a.Hk, part = idx % heads;
+    if (!tile_of<!DQ>(a, idx / heads, &t)) return false;
+    head = DQ ? part : part * a.G;
+    hk = DQ ? part / a.G : part;
+    j0 = 0;
+    if (DQ) {
+      per = (keys_seen(a, t, TR) + BN - 1) / BN;
+    } else {
+      j0 = first_query(a, t) / BN;
+      per = max(0, (t.nq + BN - 1) / BN - j0);
+    }
+    n = DQ ? per : per * a.G;
+    return true;
+  }
+  __device__ __forceinline__ void make_uniform() {
+    for (int* v : {&t.q0, &t.nq, &t.k0, &t.nk, &t.at, &n, &per, &j0}) *v = uniform(*v);
+  }
+  __device__ __forceinline__ int after(int j) const { return j + 1 == j0 + per ? j0 : j + 1; }
+};
+
+// A place in the ring: stage and parity.
+struct Place {
+  int stage;
+  uint32_t parity;
+  template <int N> __device__ __forceinline__ Place on(int by) const {
+    Place p{stage + by, parity};
+    if (p.stage >= N) p.stage -= N, p.parity ^= 1;
+    return p;
+  }
+};
+
 // Order of the products.  dq, dk: S 0, dP 0, S 1, then for every block j, once its dS is there:
 // dP j+1, the accumulation of j, S j+2.  S has two buffers, dS goes over its own S, dP has one: the
 // exponentials of block j+1 need S j+1 alone and run while the tensor cores work on dP j+1.
 // dk and dv: S 0, dP 0, then for every block j: once its P is there (over its S) dv's part and
 // S j+1, once its dS is there (over its dP) dk's part and dP j+1.
+// The warpgroups are those of k_flash; both softmax ones work on the tile, for half of a block's
+// columns each.
 template <int D, int KIND>
 __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
     k_slope(const __grid_constant__ CUtensorMap mr1, const __grid_constant__ CUtensorMap mr2,
             const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUtensorMap m2,
             SeqArgs a) {
   using F = Slope<D>;
-  constexpr bool DQ = KIND == kDq, BOTH = KIND == kDkv;
+  constexpr bool DQ = KIND == kDq, BOTH = KIND == kDkv, TIGHT = F::kTight;
   constexpr int BN = F::kBlock, ST = F::kStages, HN = BN / 2;
   extern __shared__ __align__(1024) uint8_t sm[];
   Bars& bar = *reinterpret_cast<Bars*>(sm);
   float* row_values = reinterpret_cast<float*>(sm + 512);  // dk: [2][lse2, delta][BN]
   uint8_t *own = sm + kHead, *ring = own + 2 * F::kTile;
-  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31, group = warp >> 2;
 
   if (tid == 0) {
     mbar_init(&bar.r_full, 1);
+    mbar_init(&bar.r_empty, TIGHT ? 2 : 1);
     for (int i = 0; i < ST; ++i) {
       mbar_init(&bar.full[i], 1);
       mbar_init(&bar.empty[i], 1);
@@ -737,7 +768,8 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
     mbar_init(&bar.p_full[0], 8);  // dS is there, dP has been read
     mbar_init(&bar.p_full[1], 8);  // dk and dv: P is there
     mbar_init(&bar.o_full[0], 1);
-    mbar_init(&bar.drained, F::kTight ? 2 : 1);
+    mbar_init(&bar.o_empty[0], 4);
+    mbar_init(&bar.drained, TIGHT ? 2 : 1);
     bar.gave_up = 0;
     fence_barrier_init();
   }
@@ -750,144 +782,223 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
   // columns: S (two buffers, or one), dP, the accumulators
   const uint32_t tmem = uniform(bar.tmem), t_dp = tmem + (BOTH ? 1 : 2) * BN, t_acc = t_dp + BN;
   auto wait = [&](uint64_t* b, uint32_t parity) { wait_for(b, parity, a.status, &bar.gave_up); };
+  Turns turns((DQ ? a.tq.most : a.tk.most) * (DQ ? a.Hq : a.Hk));
+  SlopeItem<D, DQ> x;
+  // the places of X1 and X2 of iteration c of all items
+  auto place1 = [&](int c) { return Place{c & 1, (uint32_t)(c >> 1) & 1}; };      // TIGHT
+  auto place2 = [&](int c) { return Place{2, (uint32_t)c & 1}; };                 // TIGHT
 
-  const int heads = DQ ? a.Hq : a.Hk, hh = blockIdx.x % heads, hk = DQ ? hh / a.G : hh;
-  Tile t;
-  int n = 0, per = 0, j0 = 0;
-  const bool some = uniform(tile_of<!DQ>(a, blockIdx.x / heads, &t));
-  if (some) {
-    for (int* v : {&t.q0, &t.nq, &t.k0, &t.nk, &t.at}) *v = uniform(*v);
-    if (DQ) {
-      per = (keys_seen(a, t, TR) + BN - 1) / BN;
-    } else {
-      j0 = first_query(a, t) / BN;
-      per = max(0, (t.nq + BN - 1) / BN - j0);
-    }
-    n = DQ ? per : per * a.G;
-  }
-  const int xrows = DQ ? t.nk : t.nq, xfirst = DQ ? t.k0 : t.q0;
-  if (warp == 8 && lane == 0 && n > 0) {
-    const int row0 = (DQ ? t.q0 : t.k0) + t.at;
-    mbar_arrive_expect_tx(&bar.r_full, 2 * F::kTile);
-    for (int c = 0; c < D / 64; ++c) {
-      tma_load_3d(own + c * 16384, &mr1, c * 64, hh, row0, &bar.r_full);
-      tma_load_3d(own + F::kTile + c * 16384, &mr2, c * 64, hh, row0, &bar.r_full);
-    }
-    int g = 0, j = j0, it = 0;
-    for (; it < n && !bar.gave_up; ++it) {
-      for (int x = 0; x < 2; ++x) {
-        const int stage = F::stage(x, it);
-        if (F::used(x, it)) wait(&bar.empty[stage], F::parity(x, it) ^ 1);
-        mbar_arrive_expect_tx(&bar.full[stage], F::kStage);
-        for (int c = 0; c < D / 64; ++c)
-          tma_load_3d(ring + stage * F::kStage + c * F::kAtom, x ? &m2 : &m1, c * 64,
-                      DQ ? hk : hh * a.G + g, xfirst + j * BN, &bar.full[stage]);
-      }
-      if (++j == j0 + per) j = j0, ++g;
-    }
-    if (bar.gave_up) {  // the copies have to land before the CTA ends
-      mbar_wait(&bar.r_full, 0, nullptr, 0);
-      for (int i = max(0, it - ST); i < it; ++i)
-        for (int x = 0; x < 2; ++x) mbar_wait(&bar.full[F::stage(x, i)], F::parity(x, i), nullptr, 0);
-    }
-  } else if ((warp == 9 || warp == 10) && n > 0) {
-    const uint32_t issue = elected();
-    const uint32_t base = smem_u32(sm);
-    const Desc kmaj(sdesc(base, 16, 1024)), mnmaj(sdesc(base, F::kAtom, 1024));
-    constexpr uint32_t kOwn = kHead, kRing = kHead + 2 * F::kTile;
-    auto steps = [&](int j) { return min(BN / 16, (xrows - j * BN + 15) / 16); };
-    wait(&bar.r_full, 0);
-    // S (x = 0) or dP (x = 1) of iteration it: the own tile x with the streamed operand x
-    auto scores = [&](uint32_t to, int x, int it, int j) {
-      const int stage = F::stage(x, it);
-      wait(&bar.full[stage], F::parity(x, it));
-      mma_rows<D, 16384, F::kAtom>(to, kmaj, kOwn + x * F::kTile, kmaj, kRing + stage * F::kStage,
-                                   idesc_bf16(128, steps(j) * 16, 0, 0), false, issue);
-    };
-    // an accumulation: the bf16 weights at `w` with the streamed operand x of iteration it, whose
-    // last use it is
-    auto weigh = [&](uint32_t to, uint32_t w, int x, int it, int j) {
-      const int ks = steps(j), stage = F::stage(x, it);
-      mma_weights<0, BN / 16>(to, w, mnmaj, kRing + stage * F::kStage, idesc_bf16(128, D, 0, 1), ks,
-                              it > 0, issue);
-      commit_to(&bar.empty[stage], issue);
-    };
-    int j = j0;
-    auto after = [&](int j) { return j + 1 == j0 + per ? j0 : j + 1; };
-    auto score0 = [&](int it, int j) {  // S, in its buffer
-      const int buf = BOTH ? 0 : it & 1;
-      scores(tmem + buf * BN, 0, it, j);
-      commit_to(&bar.s_full[buf], issue);
-    };
-    auto score1 = [&](int it, int j) {  // dP
-      scores(t_dp, 1, it, j);
-      commit_to(&bar.pv[0], issue);
-      if (!BOTH) commit_to(&bar.empty[F::stage(1, it)], issue);
-    };
-    if constexpr (BOTH) {
-      if (warp == 9) {
-        score0(0, j);
-        score1(0, j);
-        for (int it = 0; it < n; ++it) {
-          const int j1 = after(j);
-          wait(&bar.p_full[1], it & 1);
-          tc_fence_after();
-          weigh(t_acc + D, tmem, 1, it, j);
-          if (it + 1 < n) score0(it + 1, j1);
-          wait(&bar.p_full[0], it & 1);
-          tc_fence_after();
-          weigh(t_acc, t_dp, 0, it, j);
-          if (it + 1 < n) score1(it + 1, j1);
-          else commit_to(&bar.o_full[0], issue);
-          j = j1;
+  if (group == 3) {
+    fewer_registers<64>();
+    if (warp == 12 && lane == 0) {
+      // ---- copies
+      int works = 0, c = 0;
+      Place at{0, 0};
+      for (int idx; (idx = turns.next()) >= 0 && !bar.gave_up;) {
+        if (!x.find(a, idx) || x.n == 0) continue;
+        const int row0 = (DQ ? x.t.q0 : x.t.k0) + x.t.at;
+        if (works > 0) wait(&bar.r_empty, (works - 1) & 1);
+        ++works;
+        mbar_arrive_expect_tx(&bar.r_full, 2 * F::kTile);
+        for (int i = 0; i < D / 64; ++i) {
+          tma_load_3d(own + i * 16384, &mr1, i * 64, DQ ? x.head : x.hk, row0, &bar.r_full);
+          tma_load_3d(own + F::kTile + i * 16384, &mr2, i * 64, DQ ? x.head : x.hk, row0,
+                      &bar.r_full);
+        }
+        int g = 0, j = x.j0;
+        for (int it = 0; it < x.n && !bar.gave_up; ++it, ++c) {
+          for (int y = 0; y < 2; ++y) {
+            const Place to = TIGHT ? (y ? place2(c) : place1(c)) : at;
+            if (TIGHT ? c >= 2 - y : 2 * c + y >= ST) wait(&bar.empty[to.stage], to.parity ^ 1);
+            mbar_arrive_expect_tx(&bar.full[to.stage], F::kStage);
+            for (int i = 0; i < D / 64; ++i)
+              tma_load_3d(ring + to.stage * F::kStage + i * F::kAtom, y ? &m2 : &m1, i * 64,
+                          DQ ? x.hk : x.head + g, (DQ ? x.t.k0 : x.t.q0) + j * BN,
+                          &bar.full[to.stage]);
+            at = at.template on<ST>(1);
+          }
+          if ((j = x.after(j)) == x.j0) ++g;
         }
       }
-    } else if (F::kTight && warp == 10) {
-      // X1 of iteration it comes into the stage of it - 2 once that one's accumulation has ended,
-      // which had read the S buffer that is written here
-      for (int it = 0; it < n; ++it, j = after(j)) score0(it, j);
-    } else if (warp == 9) {
-      if (!F::kTight) score0(0, j);
-      score1(0, j);
-      if (!F::kTight && n > 1) score0(1, after(j));
-      for (int it = 0; it < n; ++it) {
-        const int j1 = after(j);
-        wait(&bar.p_full[0], it & 1);
-        tc_fence_after();
-        if (it + 1 < n) score1(it + 1, j1);
-        weigh(t_acc, tmem + (it & 1) * BN, 0, it, j);
-        if (it + 1 == n) commit_to(&bar.o_full[0], issue);
-        if (!F::kTight && it + 2 < n) score0(it + 2, after(j1));
-        j = j1;
+      if (bar.gave_up) {  // the copies have to land before the CTA ends
+        if (works > 0) mbar_wait(&bar.r_full, (works - 1) & 1, nullptr, 0);
+        for (int i = max(0, c - ST); i < c; ++i)
+          for (int y = 0; y < 2; ++y) {
+            const int p = 2 * i + y;
+            const Place to = TIGHT ? (y ? place2(i) : place1(i)) : Place{p % ST, (uint32_t)(p / ST) & 1};
+            mbar_wait(&bar.full[to.stage], to.parity, nullptr, 0);
+          }
+      }
+    } else if (warp == 13 || (TIGHT && warp == 14)) {
+      // ---- products
+      const uint32_t issue = elected();
+      const uint32_t base = smem_u32(sm);
+      const Desc kmaj(sdesc(base, 16, 1024)), mnmaj(sdesc(base, F::kAtom, 1024));
+      constexpr uint32_t kOwn = kHead, kRing = kHead + 2 * F::kTile;
+      int items = 0, works = 0, c = 0;
+      Place p1{0, 0}, p2{1, 0};  // of X1 and X2 of iteration c
+      for (int idx; (idx = turns.next()) >= 0;) {
+        if (!uniform(x.find(a, idx))) continue;
+        x.make_uniform();
+        ++items;
+        if (x.n == 0) continue;
+        const int xrows = DQ ? x.t.nk : x.t.nq;
+        wait(&bar.r_full, works & 1);
+        ++works;
+        auto steps = [&](int j) { return min(BN / 16, (xrows - j * BN + 15) / 16); };
+        // S (y = 0) or dP (y = 1): the own tile y with the streamed operand at `at`
+        auto scores = [&](uint32_t to, int y, const Place& at, int j) {
+          wait(&bar.full[at.stage], at.parity);
+          mma_rows<D, 16384, F::kAtom>(to, kmaj, kOwn + y * F::kTile, kmaj,
+                                       kRing + at.stage * F::kStage,
+                                       idesc_bf16(128, steps(j) * 16, 0, 0), false, issue);
+        };
+        // an accumulation: the bf16 weights at `w` with a streamed operand, whose last use it is
+        auto weigh = [&](uint32_t to, uint32_t w, const Place& at, int j, bool more) {
+          mma_weights<0, BN / 16>(to, w, mnmaj, kRing + at.stage * F::kStage,
+                                  idesc_bf16(128, D, 0, 1), steps(j), more, issue);
+          commit_to(&bar.empty[at.stage], issue);
+        };
+        auto next = [&](const Place& p) { return p.template on<ST>(2); };
+        // the accumulators of the item before have been read
+        auto vacant = [&](int it) {
+          if (it == 0 && items > 1) wait(&bar.o_empty[0], items & 1);
+        };
+        int j = x.j0;
+        if constexpr (BOTH) {
+          scores(tmem, 0, p1, j);
+          commit_to(&bar.s_full[0], issue);
+          scores(t_dp, 1, p2, j);
+          commit_to(&bar.pv[0], issue);
+          if (x.n == 1) commit_to(&bar.r_empty, issue);
+          for (int it = 0; it < x.n; ++it, ++c) {
+            const int j1 = x.after(j);
+            const bool ahead = it + 1 < x.n;
+            const Place n1 = next(p1), n2 = next(p2);
+            vacant(it);
+            wait(&bar.p_full[1], c & 1);
+            tc_fence_after();
+            weigh(t_acc + D, tmem, p2, j, it > 0);
+            if (ahead) {
+              scores(tmem, 0, n1, j1);
+              commit_to(&bar.s_full[0], issue);
+            }
+            wait(&bar.p_full[0], c & 1);
+            tc_fence_after();
+            weigh(t_acc, t_dp, p1, j, it > 0);
+            if (ahead) {
+              scores(t_dp, 1, n2, j1);
+              commit_to(&bar.pv[0], issue);
+              if (it + 2 == x.n) commit_to(&bar.r_empty, issue);
+            } else {
+              commit_to(&bar.o_full[0], issue);
+            }
+            p1 = n1;
+            p2 = n2;
+            j = j1;
+          }
+        } else if (TIGHT && warp == 14) {
+          // X1 of iteration c comes into the stage of c - 2 once that one's accumulation has ended,
+          // which had read the S buffer that is written here
+          for (int it = 0; it < x.n; ++it, ++c, j = x.after(j)) {
+            scores(tmem + (c & 1) * BN, 0, place1(c), j);
+            commit_to(&bar.s_full[c & 1], issue);
+          }
+          commit_to(&bar.r_empty, issue);
+        } else {
+          auto at1 = [&](int c) { return TIGHT ? place1(c) : p1; };
+          auto slope = [&](int c, const Place& at, int j) {
+            scores(t_dp, 1, at, j);
+            commit_to(&bar.pv[0], issue);
+            commit_to(&bar.empty[at.stage], issue);
+          };
+          auto score = [&](int c, const Place& at, int j) {
+            scores(tmem + (c & 1) * BN, 0, at, j);
+            commit_to(&bar.s_full[c & 1], issue);
+          };
+          if (!TIGHT) score(c, p1, j);
+          slope(c, TIGHT ? place2(c) : p2, j);
+          if (x.n == 1) commit_to(&bar.r_empty, issue);
+          if (!TIGHT && x.n > 1) score(c + 1, next(p1), x.after(j));
+          for (int it = 0; it < x.n; ++it, ++c) {
+            const int j1 = x.after(j);
+            const Place n1 = next(p1), n2 = next(p2);
+            vacant(it);
+            wait(&bar.p_full[0], c & 1);
+            tc_fence_after();
+            if (it + 1 < x.n) {
+              slope(c + 1, TIGHT ? place2(c + 1) : n2, j1);
+              if (it + 2 == x.n) commit_to(&bar.r_empty, issue);
+            }
+            weigh(t_acc, tmem + (c & 1) * BN, at1(c), j, it > 0);
+            if (it + 1 == x.n) commit_to(&bar.o_full[0], issue);
+            if (!TIGHT && it + 2 < x.n) score(c, next(n1), x.after(j1));
+            p1 = n1;
+            p2 = n2;
+            j = j1;
+          }
+        }
+      }
+      if (bar.gave_up) {
+        commit_to(&bar.drained, issue);
+        mbar_wait(&bar.drained, 0, nullptr, 0);
       }
     }
-    if (bar.gave_up) {
-      commit_to(&bar.drained, issue);
-      mbar_wait(&bar.drained, 0, nullptr, 0);
-    }
-  } else if (warp < 8 && some) {
-    // ---- a thread per row and half of the block's columns
-    const int half = warp >> 2, r = tid & 127;
+  } else if (group == 2) {
+    // ---- results: a thread per row
+    fewer_registers<64>();
+    const int r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const int off = t.nk - t.nq, first_row = t.at + (warp & 3) * 32, row = t.at + r;
-    float lse2 = INFINITY, delta = 0.f, ahead = 0.f;
-    if (DQ && row < t.nq) {
-      lse2 = a.lse2[(int64_t)hh * a.Nq + t.q0 + row];
-      delta = a.delta[(int64_t)hh * a.Nq + t.q0 + row];
+    int works = 0;
+    for (int idx; (idx = turns.next()) >= 0;) {
+      if (!x.find(a, idx)) continue;
+      const int row = x.t.at + r, side = DQ ? x.t.nq : x.t.nk;
+      const int64_t out = DQ ? ((int64_t)(x.t.q0 + row) * a.Hq + x.head) * D
+                             : ((int64_t)(x.t.k0 + row) * a.Hk + x.hk) * D;
+      if (x.n > 0) {
+        wait(&bar.o_full[0], works & 1);
+        ++works;
+        tc_fence_after();
+      }
+      constexpr int kAll = BOTH ? 2 * D : D;
+#pragma unroll 1
+      for (int c = 0; c < kAll; c += 32) {
+        float y[32];
+        if (x.n > 0) {
+          tmem_ld32(t_acc + lanes + c, y);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = 0.f;
+        }
+        if (c == kAll - 32) {  // read: the next item may accumulate
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.o_empty[0]);
+        }
+        const bool second = c >= D;  // dv
+        const float f = second ? 1.f : a.scale;
+        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(DQ ? a.dq : second ? a.dv : a.dk) +
+                             out + (second ? c - D : c);
+        if (row < side)
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            *reinterpret_cast<uint4*>(dst + e) = make_uint4(
+                bf16x2(y[e] * f, y[e + 1] * f), bf16x2(y[e + 2] * f, y[e + 3] * f),
+                bf16x2(y[e + 4] * f, y[e + 5] * f), bf16x2(y[e + 6] * f, y[e + 7] * f));
+      }
     }
-    // dk: thread tid < 2 BN fetches value tid % BN of lse2 or delta, one block ahead
-    auto value = [&](int g, int j) {
-      const int q = j * BN + tid % BN;
-      const float* src = tid < BN ? a.lse2 : a.delta;
-      return tid < 2 * BN && q < t.nq ? src[(int64_t)(hh * a.G + g) * a.Nq + t.q0 + q] : 0.f;
-    };
+  } else {
+    // ---- a thread per row and half of the block's columns
+    more_registers<192>();
+    const int half = group, r = tid & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     // the weights of this thread's columns, as bf16 over the columns that the row's two threads
     // have read
-    auto put = [&](uint32_t to, const float (&x)[HN]) {
+    auto put = [&](uint32_t to, const float (&w)[HN]) {
       bar_sync(2 + (warp & 3), 64);
       uint32_t y[HN / 2];
 #pragma unroll
-      for (int e = 0; e < HN / 2; ++e) y[e] = bf16x2(x[2 * e], x[2 * e + 1]);
+      for (int e = 0; e < HN / 2; ++e) y[e] = bf16x2(w[2 * e], w[2 * e + 1]);
       if constexpr (HN == 64) tmem_st32(to + lanes + half * 32, y);
       else tmem_st16(to + lanes + half * 16, y);
     };
@@ -897,108 +1008,107 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(b);
     };
-    int g = 0, j = j0;
-    if (!DQ && n > 0) ahead = value(0, j0);
-    for (int it = 0; it < n; ++it) {
-      const int kb = j * BN;
-      if (++j == j0 + per) j = j0, ++g;
-      float* lv = row_values + (it & 1) * 2 * BN;
-      if (!DQ) {
-        if (tid < 2 * BN) lv[tid] = ahead;
-        bar_sync(1, 256);
-        if (it + 1 < n) ahead = value(g, j);
+    int c = 0;  // iterations of all items
+    for (int idx; (idx = turns.next()) >= 0;) {
+      if (!x.find(a, idx)) continue;
+      const int off = x.t.nk - x.t.nq, first_row = x.t.at + (warp & 3) * 32, row = x.t.at + r;
+      const int xrows = DQ ? x.t.nk : x.t.nq;
+      float lse2 = INFINITY, delta = 0.f, ahead = 0.f;
+      if (DQ && row < x.t.nq) {
+        lse2 = a.lse2[(int64_t)x.head * a.Nq + x.t.q0 + row];
+        delta = a.delta[(int64_t)x.head * a.Nq + x.t.q0 + row];
       }
-      int c0 = 0, c1;  // columns [c0, c1) of the row count
-      bool whole;
-      if (DQ) {
-        c1 = (a.causal ? min(t.nk, row + off + 1) : t.nk) - kb;
-        whole = kb + BN <= (a.causal ? min(t.nk, first_row + off + 1) : t.nk);
-      } else {
-        c1 = t.nq - kb;
-        if (a.causal) c0 = row - off - kb;
-        whole = kb + BN <= t.nq && (!a.causal || first_row + 31 - off <= kb);
-      }
-      auto mask = [&](float (&x)[HN]) {
-        if (whole) return;
-#pragma unroll
-        for (int c = 0; c < HN; ++c)
-          x[c] = half * HN + c >= c0 && half * HN + c < c1 ? x[c] : 0.f;
+      // dk: thread tid < 2 BN fetches value tid % BN of lse2 or delta, one block ahead
+      auto value = [&](int g, int j) {
+        const int q = j * BN + tid % BN;
+        const float* src = tid < BN ? a.lse2 : a.delta;
+        return tid < 2 * BN && q < x.t.nq ? src[(int64_t)(x.head + g) * a.Nq + x.t.q0 + q] : 0.f;
       };
-      // rows of a block behind the sequence, in its last 16
-      const bool ragged = kb + BN > xrows && (xrows & 15);
-      auto zero = [&](int x) {
-        if (!ragged) return;
-        const int stage = F::stage(x, it);
-        if (x) wait(&bar.full[stage], F::parity(x, it));  // X2: dP may not have read it yet
-        zero_rows<256>(ring + stage * F::kStage, D / 64, F::kAtom, xrows - kb,
-                       (xrows - kb + 15) & ~15, tid);
-      };
-      const int buf = BOTH ? 0 : it & 1;
-      const uint32_t ts = tmem + buf * BN;
-      wait(&bar.s_full[buf], (BOTH ? it : it >> 1) & 1);
-      tc_fence_after();
-      float s[HN], dp[HN];
-      if constexpr (HN == 64) tmem_ld64(ts + lanes + half * HN, s);
-      else tmem_ld32(ts + lanes + half * HN, s);
+      int g = 0, j = x.j0;
+      if (!DQ && x.n > 0) ahead = value(0, x.j0);
+      for (int it = 0; it < x.n; ++it, ++c) {
+        const int kb = j * BN;
+        if ((j = x.after(j)) == x.j0) ++g;
+        float* lv = row_values + (c & 1) * 2 * BN;
+        if (!DQ) {
+          if (tid < 2 * BN) lv[tid] = ahead;
+          bar_sync(1, 256);
+          if (it + 1 < x.n) ahead = value(g, j);
+        }
+        int c0 = 0, c1;  // columns [c0, c1) of the row count
+        bool whole;
+        if (DQ) {
+          c1 = (a.causal ? min(x.t.nk, row + off + 1) : x.t.nk) - kb;
+          whole = kb + BN <= (a.causal ? min(x.t.nk, first_row + off + 1) : x.t.nk);
+        } else {
+          c1 = x.t.nq - kb;
+          if (a.causal) c0 = row - off - kb;
+          whole = kb + BN <= x.t.nq && (!a.causal || first_row + 31 - off <= kb);
+        }
+        auto mask = [&](float (&w)[HN]) {
+          if (whole) return;
 #pragma unroll
-      for (int c = 0; c < HN; c += 4) {
-        float4 v = make_float4(lse2, lse2, lse2, lse2);
-        if (!DQ) v = *reinterpret_cast<const float4*>(lv + half * HN + c);
-        s[c] = ex2(fmaf(s[c], a.sl, -v.x));
-        s[c + 1] = ex2(fmaf(s[c + 1], a.sl, -v.y));
-        s[c + 2] = ex2(fmaf(s[c + 2], a.sl, -v.z));
-        s[c + 3] = ex2(fmaf(s[c + 3], a.sl, -v.w));
-      }
-      if (BOTH) {
+          for (int e = 0; e < HN; ++e)
+            w[e] = half * HN + e >= c0 && half * HN + e < c1 ? w[e] : 0.f;
+        };
+        // rows of a block behind the sequence, in its last 16
+        const bool ragged = kb + BN > xrows && (xrows & 15);
+        auto zero = [&](int y) {
+          if (!ragged) return;
+          const int p = 2 * c + y;
+          const Place at = TIGHT ? (y ? place2(c) : place1(c)) : Place{p % ST, (uint32_t)(p / ST) & 1};
+          if (y) wait(&bar.full[at.stage], at.parity);  // X2: dP may not have read it yet
+          zero_rows<256>(ring + at.stage * F::kStage, D / 64, F::kAtom, xrows - kb,
+                         (xrows - kb + 15) & ~15, tid);
+        };
+        const int buf = BOTH ? 0 : c & 1;
+        const uint32_t ts = tmem + buf * BN;
+        wait(&bar.s_full[buf], (BOTH ? c : c >> 1) & 1);
+        tc_fence_after();
+        float s[HN], dp[HN];
+        if constexpr (HN == 64) tmem_ld64(ts + lanes + half * HN, s);
+        else tmem_ld32(ts + lanes + half * HN, s);
+#pragma unroll
+        for (int e = 0; e < HN; e += 4) {
+          if (DQ) {
+            fma2(s[e], s[e + 1], a.sl, -lse2);
+            fma2(s[e + 2], s[e + 3], a.sl, -lse2);
+          } else {
+            const float4 v = *reinterpret_cast<const float4*>(lv + half * HN + e);
+            s[e] = fmaf(s[e], a.sl, -v.x);
+            s[e + 1] = fmaf(s[e + 1], a.sl, -v.y);
+            s[e + 2] = fmaf(s[e + 2], a.sl, -v.z);
+            s[e + 3] = fmaf(s[e + 3], a.sl, -v.w);
+          }
+          s[e] = ex2(s[e]);
+          s[e + 1] = ex2(s[e + 1]);
+          s[e + 2] = ex2(s[e + 2]);
+          s[e + 3] = ex2(s[e + 3]);
+        }
+        if (BOTH) {
+          mask(s);
+          put(ts, s);
+          zero(1);
+          tell(&bar.p_full[1]);
+        }
+        wait(&bar.pv[0], c & 1);
+        tc_fence_after();
+        if constexpr (HN == 64) tmem_ld64(t_dp + lanes + half * HN, dp);
+        else tmem_ld32(t_dp + lanes + half * HN, dp);
+#pragma unroll
+        for (int e = 0; e < HN; e += 4) {
+          float4 v = make_float4(delta, delta, delta, delta);
+          if (!DQ) v = *reinterpret_cast<const float4*>(lv + BN + half * HN + e);
+          s[e] *= dp[e] - v.x;
+          s[e + 1] *= dp[e + 1] - v.y;
+          s[e + 2] *= dp[e + 2] - v.z;
+          s[e + 3] *= dp[e + 3] - v.w;
+        }
         mask(s);
-        put(ts, s);
-        zero(1);
-        tell(&bar.p_full[1]);
+        put(BOTH ? t_dp : ts, s);
+        zero(0);
+        tell(&bar.p_full[0]);
       }
-      wait(&bar.pv[0], it & 1);
-      tc_fence_after();
-      if constexpr (HN == 64) tmem_ld64(t_dp + lanes + half * HN, dp);
-      else tmem_ld32(t_dp + lanes + half * HN, dp);
-#pragma unroll
-      for (int c = 0; c < HN; c += 4) {
-        float4 v = make_float4(delta, delta, delta, delta);
-        if (!DQ) v = *reinterpret_cast<const float4*>(lv + BN + half * HN + c);
-        s[c] *= dp[c] - v.x;
-        s[c + 1] *= dp[c + 1] - v.y;
-        s[c + 2] *= dp[c + 2] - v.z;
-        s[c + 3] *= dp[c + 3] - v.w;
-      }
-      mask(s);
-      put(BOTH ? t_dp : ts, s);
-      zero(0);
-      tell(&bar.p_full[0]);
-    }
-    if (n > 0) {
-      wait(&bar.o_full[0], 0);
-      tc_fence_after();
-    }
-    const int side = DQ ? t.nq : t.nk;
-    const int64_t out = ((int64_t)((DQ ? t.q0 : t.k0) + row) * heads + hh) * D;
-#pragma unroll 1
-    for (int x0 = 0; x0 < (BOTH ? D : D / 2); x0 += 32) {
-      const bool second = BOTH && x0 >= D / 2;  // dv
-      const int c = half * (D / 2) + x0 % (D / 2);
-      float x[32];
-      if (n > 0) {
-        tmem_ld32(t_acc + lanes + (second ? D : 0) + c, x);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = 0.f;
-      }
-      const float f = second ? 1.f : a.scale;
-      __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(DQ ? a.dq : second ? a.dv : a.dk) +
-                           out + c;
-      if (row < side)
-#pragma unroll
-        for (int e = 0; e < 32; e += 8)
-          *reinterpret_cast<uint4*>(dst + e) =
-              make_uint4(bf16x2(x[e] * f, x[e + 1] * f), bf16x2(x[e + 2] * f, x[e + 3] * f),
-                         bf16x2(x[e + 4] * f, x[e + 5] * f), bf16x2(x[e + 6] * f, x[e + 7] * f));
     }
   }
   tc_fence_before();
@@ -1008,28 +1118,21 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
 
 // ---------------------------------------------------------------------------------- host
 
-template <typename K, typename... M>
-cudaError_t launch(K kernel, int64_t grid, int threads, int smem, cudaStream_t st, M... maps_args) {
+template <auto kKernel, typename... M>
+cudaError_t launch(int64_t grid, int threads, int smem, cudaStream_t st, const M&... args) {
   if (grid == 0) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return e;
-  }
-  return launch_behind(kernel, dim3((unsigned)grid), threads, smem, st, maps_args...);
+  const cudaError_t e = allow_smem<kKernel>(smem);
+  if (e != cudaSuccess) return e;
+  return launch_behind(kKernel, dim3((unsigned)grid), threads, smem, st, args...);
 }
 
-// Maps of q, k, v (and dO); rows that do not exist are never loaded (a map of one row of another
-// tensor stands in).
-struct Maps {
-  CUtensorMap q, k, v, d;
-};
+// Maps; rows that do not exist are never loaded (a map of another tensor stands in).
 bool make(CUtensorMap* m, const void* p, int64_t n, int64_t stride, int64_t heads, int D,
           int rows, int pack = 1) {
   return tc_make_map_tokens(m, p, n, stride, heads, D, rows, pack);
 }
 
-// CTAs of k_flash, one per SM, each of which takes several items.
+// CTAs, one per SM, each of which takes several items.
 int64_t ctas_of(int64_t items) {
   const int64_t sms = device_sms();
   return items < sms ? items : sms;
@@ -1043,7 +1146,7 @@ cudaError_t fwd(const SeqArgs& a, cudaStream_t st) {
   if (a.Nk > 0 && (!make(&k, a.k, a.Nk, a.ks, a.Hk, D, 128) ||
                    !make(&v, a.v, a.Nk, a.vs, a.Hk, D, 128)))
     return cudaErrorInvalidValue;
-  return launch(k_flash<D, true>, ctas_of((int64_t)a.tq.most * (a.Hq / a.pack)),
+  return launch<k_flash<D, true>>(ctas_of((int64_t)a.tq.most * (a.Hq / a.pack)),
                 Flash<D>::kThreads, Flash<D>::kBytes, st, q, k, v, a);
 }
 
@@ -1066,16 +1169,16 @@ cudaError_t bwd(const SeqArgs& a, cudaStream_t st) {
   if (a.Nk == 0) k = v = kb = vb = q;
   if (a.Nk > 0) {
     const int64_t ctas = (int64_t)a.tk.most * a.Hk;
-    cudaError_t e = launch(k_slope<D, D == 256 ? kDk : kDkv>, ctas, Slope<D>::kThreads,
+    cudaError_t e = launch<k_slope<D, D == 256 ? kDk : kDkv>>(ctas_of(ctas), Slope<D>::kThreads,
                            Slope<D>::kBytes, st, k, v, qb, db, a);
     if (e != cudaSuccess) return e;
     if constexpr (D == 256) {
-      e = launch(k_flash<D, false>, ctas_of(ctas), Flash<D>::kThreads, Flash<D>::kBytes, st, k, q, d, a);
+      e = launch<k_flash<D, false>>(ctas_of(ctas), Flash<D>::kThreads, Flash<D>::kBytes, st, k, q, d, a);
       if (e != cudaSuccess) return e;
     }
   }
   if (a.Nq == 0) return cudaSuccess;
-  return launch(k_slope<D, kDq>, (int64_t)a.tq.most * a.Hq, Slope<D>::kThreads,
+  return launch<k_slope<D, kDq>>(ctas_of((int64_t)a.tq.most * a.Hq), Slope<D>::kThreads,
                 Slope<D>::kBytes, st, q, d, kb, vb, a);
 }
 

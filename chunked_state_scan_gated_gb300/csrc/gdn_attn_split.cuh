@@ -488,8 +488,11 @@ cudaError_t launch(AttnArgs ar, char* ws, cudaStream_t st) {
   ar.join = (Join*)ws;
   ar.ml = (float2*)(ws + pl.ml);
   ar.acc = (float*)(ws + pl.acc);
-  const cudaError_t e = launch_behind(k_attn_decode<D, T, NG>, dim3(pl.ctas), AT_NT,
-                                      Smem<D, T, NG>::kBytes, st, ar);
+  cudaError_t e = cudaSuccess;
+  if constexpr (Smem<D, T, NG>::kBytes > 48 * 1024)
+    e = allow_smem<k_attn_decode<D, T, NG>>(Smem<D, T, NG>::kBytes);
+  if (e == cudaSuccess)
+    e = launch_behind(k_attn_decode<D, T, NG>, dim3(pl.ctas), AT_NT, Smem<D, T, NG>::kBytes, st, ar);
   if (e != cudaSuccess) return e;
   return launch_behind(k_attn_join<D, T, NG>, dim3(pl.ctas), AJ_NT, 0, st, ar);
 }

@@ -7,6 +7,9 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
 
 namespace gdn {
 
@@ -32,6 +35,21 @@ cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, int threads, size_t s
   cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, P(args)...);
   if (e != cudaSuccess) cudaGetLastError();  // reported here: not left for the next call
+  return e;
+}
+
+// Lets the kernel have `bytes` of shared memory, once per device (two threads that both ask do no
+// harm).
+template <auto kKernel>
+cudaError_t allow_smem(size_t bytes) {
+  static std::atomic<uint64_t> done{0};  // a bit per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess && dev < 64 && (done.load() >> dev & 1)) return e;
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e != cudaSuccess) cudaGetLastError();
+  else if (dev < 64) done.fetch_or(1ull << dev);
   return e;
 }
 

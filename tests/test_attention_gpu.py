@@ -337,7 +337,8 @@ def test_attention_argument_checks():
     with pytest.raises(gdn.GDNError):
         gdn.gdn_attn_fwd(q, k[:5], k[:5], cu)  # one set of offsets, two lengths
     with pytest.raises(gdn.GDNError):
-        gdn.gdn_attn_fwd(q, k, k, cu, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        gdn.gdn_attn_fwd(q, k, k, i32([0, 4, 10]),
+                         ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(gdn.GDNError):
         gdn.gdn_attn_fwd(q[:, :3], k, k, cu)
     empty = gdn.gdn_attn_fwd(q[:0], k[:0], k[:0], cu * 0)
