@@ -513,8 +513,9 @@ size_t up(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Workspace: the lists' counts, the lists, the backward's rows of lse and delta.
 struct Layout {
-  size_t lq, lk, lse2, delta, total;
+  size_t lq, lk, lse2, delta, part_k, part_v, total;
   int mq, mk;  // upper bounds of the tiles
+  int splits;  // parts that a key head's query heads are divided into, for dk and dv
 };
 Layout layout(const gdn_attn_seq_problem* p, bool bwd, int rq, int rk) {
   Layout y;
@@ -527,7 +528,18 @@ Layout layout(const gdn_attn_seq_problem* p, bool bwd, int rq, int rk) {
   y.lk = lists ? up(y.lq + y.mq * sizeof(Tile)) : 0;
   y.lse2 = lists && bwd ? up(y.lk + y.mk * sizeof(Tile)) : y.lk;
   y.delta = y.lse2 + (bwd ? up((size_t)p->Nq * p->Hq * 4) : 0);
-  y.total = y.delta + (bwd ? up((size_t)p->Nq * p->Hq * 4) : 0);
+  y.part_k = y.delta + (bwd ? up((size_t)p->Nq * p->Hq * 4) : 0);
+  // bf16: a key tile's query heads go to several CTAs where there are fewer tiles than 4 per SM; each
+  // writes a part of dk and dv in fp32, which k_attn_sum adds up (16001 tokens, 16 on 2 heads of 256:
+  // one part 7.9 ms, 8: see the kernels' file; the parts cost 16 bytes per element and part).
+  y.splits = 1;
+  const int64_t G = p->Hq / p->Hk, tiles = (int64_t)y.mk * p->Hk * (rk / 128);
+  if (bwd && p->dtype == GDN_BF16 && tiles > 0)
+    for (int64_t s = 2; s <= G && tiles * y.splits < 608; ++s)
+      if (G % s == 0) y.splits = (int)s;
+  const size_t part = y.splits > 1 ? up((size_t)y.splits * p->Nk * p->Hk * p->D * 4) : 0;
+  y.part_v = y.part_k + part;
+  y.total = y.part_v + part;
   return y;
 }
 Layout layout_of(const gdn_attn_seq_problem* p, bool bwd) {
@@ -566,6 +578,9 @@ gdn_status begin(const gdn_attn_seq_problem* p, bool bwd, const int32_t* cu_q,
   a->tk.most = y.mk;
   a->lse2 = (float*)(ws + y.lse2);
   a->delta = (float*)(ws + y.delta);
+  a->part_k = (float*)(ws + y.part_k);
+  a->part_v = (float*)(ws + y.part_v);
+  a->splits = y.splits;
   if (cu_q && p->n_seqs > 1) {
     int* count = (int*)ws;
     PlanSide sq{(Tile*)(ws + y.lq), count, a->tq.rows, y.mq};

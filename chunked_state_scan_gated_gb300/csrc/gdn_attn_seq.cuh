@@ -43,7 +43,7 @@ struct SeqArgs {
   float *lse2, *delta; // [Hq][Nq]: lse log2(e) (+inf where no key is seen), dO.o
   Tiles tq, tk;
   float *part_k, *part_v;  // [splits][Nk][Hk][D]: dk, dv of a part of a key head's query heads
-  int splits;
+  int splits;              // 1: none, dk and dv are written themselves
   int32_t* status;
 };
 

@@ -103,6 +103,35 @@ __device__ inline void drain(Bars& bar, int works, int stages, int stage, int tu
       mbar_wait(&bar.full[i], (i < stage ? turn : turn - 1) & 1, nullptr, 0);
 }
 
+// 32 columns of an output row, times f, as bf16 or (a part of dk or dv) as fp32.
+__device__ __forceinline__ void write_row(__nv_bfloat16* dst, const float (&y)[32], float f) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 8)
+    *reinterpret_cast<uint4*>(dst + e) =
+        make_uint4(bf16x2(y[e] * f, y[e + 1] * f), bf16x2(y[e + 2] * f, y[e + 3] * f),
+                   bf16x2(y[e + 4] * f, y[e + 5] * f), bf16x2(y[e + 6] * f, y[e + 7] * f));
+}
+__device__ __forceinline__ void write_row(float* dst, const float (&y)[32], float f) {
+#pragma unroll
+  for (int e = 0; e < 32; e += 4)
+    *reinterpret_cast<float4*>(dst + e) =
+        make_float4(y[e] * f, y[e + 1] * f, y[e + 2] * f, y[e + 3] * f);
+}
+// Columns c .. c + 31 of row `row` (of all key rows) of dk (dv: second), of the query heads from
+// `head` on.
+template <int D>
+__device__ __forceinline__ void write_dkv(const SeqArgs& a, bool second, int64_t row, int hk,
+                                          int head, int c, const float (&y)[32]) {
+  const float f = second ? 1.f : a.scale;
+  const int64_t at = (row * a.Hk + hk) * D + c;
+  if (a.splits == 1) {
+    write_row(reinterpret_cast<__nv_bfloat16*>(second ? a.dv : a.dk) + at, y, f);
+  } else {
+    const int part = (head - hk * a.G) / (a.G / a.splits);
+    write_row((second ? a.part_v : a.part_k) + (int64_t)part * a.Nk * a.Hk * D + at, y, f);
+  }
+}
+
 // ------------------------------------------------------------------------- forward and dv
 
 // D <= 128: two tiles share every streamed block, each with one buffer of S: while one tile's
@@ -146,14 +175,15 @@ __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
 // One CTA's share of the work: items of the sorted list, in turns that change direction, so that
 // the CTAs end together.
 struct Turns {
-  int round = -1, total;
-  __device__ __forceinline__ explicit Turns(int n) : total(n) {}
+  int round = -1, total, ctas, cta;
+  __device__ __forceinline__ explicit Turns(int n, int per = 1)
+      : total(n), ctas(gridDim.x / per), cta(blockIdx.x / per) {}
   __device__ __forceinline__ int next() {  // -1: none left
     while (true) {
       ++round;
-      const int64_t first = (int64_t)round * gridDim.x;
+      const int64_t first = (int64_t)round * ctas;
       if (first >= total) return -1;
-      const int64_t i = first + (round & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      const int64_t i = first + (round & 1 ? ctas - 1 - cta : cta);
       if (i < total) return (int)i;
     }
   }
@@ -171,9 +201,11 @@ struct Item {
   __device__ __forceinline__ int lo(int i) const { return i ? lo1 : lo0; }
   __device__ __forceinline__ int hi(int i) const { return i ? hi1 : hi0; }
   __device__ __forceinline__ bool find(const SeqArgs& a, int idx) {
-    const int groups = FWD ? a.Hq / a.pack : a.Hk, part = idx % groups;
-    if (!tile_of<!FWD>(a, idx / groups, &t)) return false;
-    head = FWD ? part * a.pack : part * a.G;
+    const int groups = FWD ? a.Hq / a.pack : a.Hk * a.splits, part = idx % groups;
+    const int subs = FWD ? 1 : a.tk.rows / TR, tile = idx / groups;
+    if (!tile_of<!FWD>(a, tile / subs, &t)) return false;
+    if (!FWD) t.at += tile % subs * TR;  // dv: 128 rows of one of the list's tiles
+    head = part * (FWD ? a.pack : a.G / a.splits);
     hk = head / a.G;
     const int side = FWD ? t.nq : t.nk, rows = FWD ? TR / a.pack : TR;
     lo0 = lo1 = hi0 = hi1 = 0;
@@ -194,7 +226,7 @@ struct Item {
     }
     j0 = lo0;
     per = max(hi0, hi1) - j0;
-    n = FWD ? per : per * a.G;
+    n = FWD ? per : per * (a.G / a.splits);
     return true;
   }
   __device__ __forceinline__ void make_uniform() {
@@ -253,7 +285,7 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
   auto acc_of = [&](int t) { return tmem + 256 + t * D; };
   auto wait = [&](uint64_t* b, uint32_t parity) { wait_for(b, parity, a.status, &bar.gave_up); };
   if (FWD && blockIdx.x == 0 && tid == 0) check_single(a);
-  Turns turns((FWD ? a.tq.most : a.tk.most) * (FWD ? a.Hq / a.pack : a.Hk));
+  Turns turns(FWD ? a.tq.most * (a.Hq / a.pack) : a.tk.most * (a.tk.rows / TR) * a.Hk * a.splits);
   Item<D, FWD> x;
 
   if (group == 3) {
@@ -444,8 +476,7 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
         const int row = FWD ? x.t.at + (i * TR + r) / a.pack : x.t.at + i * TR + r;
         const int side = FWD ? x.t.nq : x.t.nk;
         const int64_t out =
-            FWD ? (int64_t)(x.t.q0 + row) * a.Hq + x.head + (a.pack > 1 ? r % a.pack : 0)
-                : (int64_t)(x.t.k0 + row) * a.Hk + x.hk;
+            (int64_t)(x.t.q0 + row) * a.Hq + x.head + (a.pack > 1 ? r % a.pack : 0);  // forward
         float f = 1.f;
         if (FWD) {
           wait(&bar.l_full[i], items & 1);
@@ -457,7 +488,6 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
           ++works[i];
           tc_fence_after();
         }
-        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(FWD ? a.out : a.dv) + out * D;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float y[32];
@@ -472,12 +502,10 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.o_empty[i]);
           }
-          if (row < side)
-#pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(
-                  bf16x2(y[e] * f, y[e + 1] * f), bf16x2(y[e + 2] * f, y[e + 3] * f),
-                  bf16x2(y[e + 4] * f, y[e + 5] * f), bf16x2(y[e + 6] * f, y[e + 7] * f));
+          if (row < side) {
+            if (FWD) write_row(reinterpret_cast<__nv_bfloat16*>(a.out) + out * D + c, y, f);
+            else write_dkv<D>(a, true, x.t.k0 + row, x.hk, x.head, c, y);
+          }
         }
       }
       ++items;
@@ -676,46 +704,41 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
 
 // ------------------------------------------------------------------------- dq, dk (and dv)
 
-// Blocks of 128 rows of the streamed side; of 64 with D = 256, whose own tiles take 128 KB.
 template <int D>
 struct Slope {
-  static constexpr int kBlock = D == 256 ? 64 : 128;
+  static constexpr int kBlock = 128;            // rows of a streamed block
   static constexpr int kStage = kBlock * D * 2;
-  static constexpr int kAtom = kBlock * 128;  // bytes of 64 columns
+  static constexpr int kAtom = kBlock * 128;    // bytes of 64 columns
   static constexpr int kTile = TR * D * 2;
   static constexpr int kRaw = (kSmem - kHead - 2 * kTile) / kStage;
   static constexpr int kStages = kRaw < 8 ? kRaw : 8;
-  // Three stages only (D = 256): two for X1 and one for X2, in place of one ring for both; S is
-  // then issued by a warp of its own, as its X1 arrives last.
-  static constexpr bool kTight = kStages < 4;
   static constexpr int kThreads = 512;
   static constexpr int kBytes = kHead + 2 * kTile + kStages * kStage;
 };
 
-// What a call computes: dq of queries; dk of keys; dk and dv of keys, where TMEM has room for both
-// accumulators (D <= 128): one pass of four products in place of 3 + 2.
-enum Kind { kDq, kDk, kDkv };
+// What a launch computes: dq of queries; dk and dv of keys, where TMEM has room for both accumulators
+// (D <= 128): one pass of four products in place of 3 + 2; dk of keys.
+enum Kind { kDq, kDkv, kDk };
 
 // An item of k_slope: a tile of one sequence and head (or key head), and its iterations.
-template <int D, bool DQ>
+template <bool DQ, int BN, int ROWS>
 struct SlopeItem {
   Tile t;
   int head, hk;    // the (first) query head, the key head
   int n, per, j0;  // iterations; of one query head; the first block
   __device__ __forceinline__ bool find(const SeqArgs& a, int idx) {
-    constexpr int BN = Slope<D>::kBlock;
-    const int heads = DQ ? a.Hq : a.Hk, part = idx % heads;
-    if (!tile_of<!DQ>(a, idx / heads, &t)) return false;
-    head = DQ ? part : part * a.G;
-    hk = DQ ? part / a.G : part;
+    const int groups = DQ ? a.Hq : a.Hk * a.splits, part = idx % groups;
+    if (!tile_of<!DQ>(a, idx / groups, &t)) return false;
+    head = DQ ? part : part * (a.G / a.splits);
+    hk = head / a.G;
     j0 = 0;
     if (DQ) {
-      per = (keys_seen(a, t, TR) + BN - 1) / BN;
+      per = (keys_seen(a, t, ROWS) + BN - 1) / BN;
     } else {
       j0 = first_query(a, t) / BN;
       per = max(0, (t.nq + BN - 1) / BN - j0);
     }
-    n = DQ ? per : per * a.G;
+    n = DQ ? per : per * (a.G / a.splits);
     return true;
   }
   __device__ __forceinline__ void make_uniform() {
@@ -735,11 +758,11 @@ struct Place {
   }
 };
 
-// Order of the products.  dq, dk: S 0, dP 0, S 1, then for every block j, once its dS is there:
-// dP j+1, the accumulation of j, S j+2.  S has two buffers, dS goes over its own S, dP has one: the
-// exponentials of block j+1 need S j+1 alone and run while the tensor cores work on dP j+1.
-// dk and dv: S 0, dP 0, then for every block j: once its P is there (over its S) dv's part and
-// S j+1, once its dS is there (over its dP) dk's part and dP j+1.
+// Heads of 64 and 128.  Order of the products.  dq: S 0, dP 0, S 1, then for every block j, once its
+// dS is there: dP j+1, the accumulation of j, S j+2.  S has two buffers, dS goes over its own S, dP
+// has one: the exponentials of block j+1 need S j+1 alone and run while the tensor cores work on
+// dP j+1.  dk and dv: S 0, dP 0, then for every block j: once its P is there (over its S) dv's part
+// and S j+1, once its dS is there (over its dP) dk's part and dP j+1.
 // The warpgroups are those of k_flash; both softmax ones work on the tile, for half of a block's
 // columns each.
 template <int D, int KIND>
@@ -748,7 +771,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
             const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUtensorMap m2,
             SeqArgs a) {
   using F = Slope<D>;
-  constexpr bool DQ = KIND == kDq, BOTH = KIND == kDkv, TIGHT = F::kTight;
+  constexpr bool DQ = KIND == kDq;
   constexpr int BN = F::kBlock, ST = F::kStages, HN = BN / 2;
   extern __shared__ __align__(1024) uint8_t sm[];
   Bars& bar = *reinterpret_cast<Bars*>(sm);
@@ -758,7 +781,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
 
   if (tid == 0) {
     mbar_init(&bar.r_full, 1);
-    mbar_init(&bar.r_empty, TIGHT ? 2 : 1);
+    mbar_init(&bar.r_empty, 1);
     for (int i = 0; i < ST; ++i) {
       mbar_init(&bar.full[i], 1);
       mbar_init(&bar.empty[i], 1);
@@ -769,7 +792,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
     mbar_init(&bar.p_full[1], 8);  // dk and dv: P is there
     mbar_init(&bar.o_full[0], 1);
     mbar_init(&bar.o_empty[0], 4);
-    mbar_init(&bar.drained, TIGHT ? 2 : 1);
+    mbar_init(&bar.drained, 1);
     bar.gave_up = 0;
     fence_barrier_init();
   }
@@ -780,13 +803,12 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   // columns: S (two buffers, or one), dP, the accumulators
-  const uint32_t tmem = uniform(bar.tmem), t_dp = tmem + (BOTH ? 1 : 2) * BN, t_acc = t_dp + BN;
+  const uint32_t tmem = uniform(bar.tmem), t_dp = tmem + (DQ ? 2 : 1) * BN, t_acc = t_dp + BN;
   auto wait = [&](uint64_t* b, uint32_t parity) { wait_for(b, parity, a.status, &bar.gave_up); };
-  Turns turns((DQ ? a.tq.most : a.tk.most) * (DQ ? a.Hq : a.Hk));
-  SlopeItem<D, DQ> x;
-  // the places of X1 and X2 of iteration c of all items
-  auto place1 = [&](int c) { return Place{c & 1, (uint32_t)(c >> 1) & 1}; };      // TIGHT
-  auto place2 = [&](int c) { return Place{2, (uint32_t)c & 1}; };                 // TIGHT
+  Turns turns((DQ ? a.tq.most : a.tk.most) * (DQ ? a.Hq : a.Hk * a.splits));
+  SlopeItem<DQ, BN, TR> x;
+  // X1 0, X2 0, X1 1, X2 1, .. of all items follow each other in the ring
+  auto place = [&](int p) { return Place{p % ST, (uint32_t)(p / ST) & 1}; };
 
   if (group == 3) {
     fewer_registers<64>();
@@ -808,13 +830,12 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
         int g = 0, j = x.j0;
         for (int it = 0; it < x.n && !bar.gave_up; ++it, ++c) {
           for (int y = 0; y < 2; ++y) {
-            const Place to = TIGHT ? (y ? place2(c) : place1(c)) : at;
-            if (TIGHT ? c >= 2 - y : 2 * c + y >= ST) wait(&bar.empty[to.stage], to.parity ^ 1);
-            mbar_arrive_expect_tx(&bar.full[to.stage], F::kStage);
+            if (2 * c + y >= ST) wait(&bar.empty[at.stage], at.parity ^ 1);
+            mbar_arrive_expect_tx(&bar.full[at.stage], F::kStage);
             for (int i = 0; i < D / 64; ++i)
-              tma_load_3d(ring + to.stage * F::kStage + i * F::kAtom, y ? &m2 : &m1, i * 64,
+              tma_load_3d(ring + at.stage * F::kStage + i * F::kAtom, y ? &m2 : &m1, i * 64,
                           DQ ? x.hk : x.head + g, (DQ ? x.t.k0 : x.t.q0) + j * BN,
-                          &bar.full[to.stage]);
+                          &bar.full[at.stage]);
             at = at.template on<ST>(1);
           }
           if ((j = x.after(j)) == x.j0) ++g;
@@ -822,14 +843,10 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
       }
       if (bar.gave_up) {  // the copies have to land before the CTA ends
         if (works > 0) mbar_wait(&bar.r_full, (works - 1) & 1, nullptr, 0);
-        for (int i = max(0, c - ST); i < c; ++i)
-          for (int y = 0; y < 2; ++y) {
-            const int p = 2 * i + y;
-            const Place to = TIGHT ? (y ? place2(i) : place1(i)) : Place{p % ST, (uint32_t)(p / ST) & 1};
-            mbar_wait(&bar.full[to.stage], to.parity, nullptr, 0);
-          }
+        for (int p = max(0, 2 * c - ST); p < 2 * c; ++p)
+          mbar_wait(&bar.full[place(p).stage], place(p).parity, nullptr, 0);
       }
-    } else if (warp == 13 || (TIGHT && warp == 14)) {
+    } else if (warp == 13) {
       // ---- products
       const uint32_t issue = elected();
       const uint32_t base = smem_u32(sm);
@@ -865,7 +882,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
           if (it == 0 && items > 1) wait(&bar.o_empty[0], items & 1);
         };
         int j = x.j0;
-        if constexpr (BOTH) {
+        if constexpr (!DQ) {
           scores(tmem, 0, p1, j);
           commit_to(&bar.s_full[0], issue);
           scores(t_dp, 1, p2, j);
@@ -897,17 +914,8 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
             p2 = n2;
             j = j1;
           }
-        } else if (TIGHT && warp == 14) {
-          // X1 of iteration c comes into the stage of c - 2 once that one's accumulation has ended,
-          // which had read the S buffer that is written here
-          for (int it = 0; it < x.n; ++it, ++c, j = x.after(j)) {
-            scores(tmem + (c & 1) * BN, 0, place1(c), j);
-            commit_to(&bar.s_full[c & 1], issue);
-          }
-          commit_to(&bar.r_empty, issue);
         } else {
-          auto at1 = [&](int c) { return TIGHT ? place1(c) : p1; };
-          auto slope = [&](int c, const Place& at, int j) {
+          auto slope = [&](const Place& at, int j) {
             scores(t_dp, 1, at, j);
             commit_to(&bar.pv[0], issue);
             commit_to(&bar.empty[at.stage], issue);
@@ -916,10 +924,10 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
             scores(tmem + (c & 1) * BN, 0, at, j);
             commit_to(&bar.s_full[c & 1], issue);
           };
-          if (!TIGHT) score(c, p1, j);
-          slope(c, TIGHT ? place2(c) : p2, j);
+          score(c, p1, j);
+          slope(p2, j);
           if (x.n == 1) commit_to(&bar.r_empty, issue);
-          if (!TIGHT && x.n > 1) score(c + 1, next(p1), x.after(j));
+          if (x.n > 1) score(c + 1, next(p1), x.after(j));
           for (int it = 0; it < x.n; ++it, ++c) {
             const int j1 = x.after(j);
             const Place n1 = next(p1), n2 = next(p2);
@@ -927,12 +935,12 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
             wait(&bar.p_full[0], c & 1);
             tc_fence_after();
             if (it + 1 < x.n) {
-              slope(c + 1, TIGHT ? place2(c + 1) : n2, j1);
+              slope(n2, j1);
               if (it + 2 == x.n) commit_to(&bar.r_empty, issue);
             }
-            weigh(t_acc, tmem + (c & 1) * BN, at1(c), j, it > 0);
+            weigh(t_acc, tmem + (c & 1) * BN, p1, j, it > 0);
             if (it + 1 == x.n) commit_to(&bar.o_full[0], issue);
-            if (!TIGHT && it + 2 < x.n) score(c, next(n1), x.after(j1));
+            if (it + 2 < x.n) score(c, next(n1), x.after(j1));
             p1 = n1;
             p2 = n2;
             j = j1;
@@ -953,14 +961,12 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
     for (int idx; (idx = turns.next()) >= 0;) {
       if (!x.find(a, idx)) continue;
       const int row = x.t.at + r, side = DQ ? x.t.nq : x.t.nk;
-      const int64_t out = DQ ? ((int64_t)(x.t.q0 + row) * a.Hq + x.head) * D
-                             : ((int64_t)(x.t.k0 + row) * a.Hk + x.hk) * D;
       if (x.n > 0) {
         wait(&bar.o_full[0], works & 1);
         ++works;
         tc_fence_after();
       }
-      constexpr int kAll = BOTH ? 2 * D : D;
+      constexpr int kAll = DQ ? D : 2 * D;
 #pragma unroll 1
       for (int c = 0; c < kAll; c += 32) {
         float y[32];
@@ -975,16 +981,13 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.o_empty[0]);
         }
-        const bool second = c >= D;  // dv
-        const float f = second ? 1.f : a.scale;
-        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(DQ ? a.dq : second ? a.dv : a.dk) +
-                             out + (second ? c - D : c);
-        if (row < side)
-#pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            *reinterpret_cast<uint4*>(dst + e) = make_uint4(
-                bf16x2(y[e] * f, y[e + 1] * f), bf16x2(y[e + 2] * f, y[e + 3] * f),
-                bf16x2(y[e + 4] * f, y[e + 5] * f), bf16x2(y[e + 6] * f, y[e + 7] * f));
+        if (row < side) {
+          if (DQ)
+            write_row(reinterpret_cast<__nv_bfloat16*>(a.dq) +
+                          ((int64_t)(x.t.q0 + row) * a.Hq + x.head) * D + c, y, a.scale);
+          else
+            write_dkv<D>(a, c >= D, x.t.k0 + row, x.hk, x.head, c >= D ? c - D : c, y);
+        }
       }
     }
   } else {
@@ -999,8 +1002,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
       uint32_t y[HN / 2];
 #pragma unroll
       for (int e = 0; e < HN / 2; ++e) y[e] = bf16x2(w[2 * e], w[2 * e + 1]);
-      if constexpr (HN == 64) tmem_st32(to + lanes + half * 32, y);
-      else tmem_st16(to + lanes + half * 16, y);
+      tmem_st32(to + lanes + half * 32, y);
     };
     auto tell = [&](uint64_t* b) {
       tmem_st_wait();
@@ -1018,11 +1020,11 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
         lse2 = a.lse2[(int64_t)x.head * a.Nq + x.t.q0 + row];
         delta = a.delta[(int64_t)x.head * a.Nq + x.t.q0 + row];
       }
-      // dk: thread tid < 2 BN fetches value tid % BN of lse2 or delta, one block ahead
+      // dk, dv: a thread fetches value tid % BN of lse2 or delta, one block ahead
       auto value = [&](int g, int j) {
         const int q = j * BN + tid % BN;
         const float* src = tid < BN ? a.lse2 : a.delta;
-        return tid < 2 * BN && q < x.t.nq ? src[(int64_t)(x.head + g) * a.Nq + x.t.q0 + q] : 0.f;
+        return q < x.t.nq ? src[(int64_t)(x.head + g) * a.Nq + x.t.q0 + q] : 0.f;
       };
       int g = 0, j = x.j0;
       if (!DQ && x.n > 0) ahead = value(0, x.j0);
@@ -1031,7 +1033,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
         if ((j = x.after(j)) == x.j0) ++g;
         float* lv = row_values + (c & 1) * 2 * BN;
         if (!DQ) {
-          if (tid < 2 * BN) lv[tid] = ahead;
+          lv[tid] = ahead;
           bar_sync(1, 256);
           if (it + 1 < x.n) ahead = value(g, j);
         }
@@ -1055,19 +1057,17 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
         const bool ragged = kb + BN > xrows && (xrows & 15);
         auto zero = [&](int y) {
           if (!ragged) return;
-          const int p = 2 * c + y;
-          const Place at = TIGHT ? (y ? place2(c) : place1(c)) : Place{p % ST, (uint32_t)(p / ST) & 1};
+          const Place at = place(2 * c + y);
           if (y) wait(&bar.full[at.stage], at.parity);  // X2: dP may not have read it yet
           zero_rows<256>(ring + at.stage * F::kStage, D / 64, F::kAtom, xrows - kb,
                          (xrows - kb + 15) & ~15, tid);
         };
-        const int buf = BOTH ? 0 : c & 1;
+        const int buf = DQ ? c & 1 : 0;
         const uint32_t ts = tmem + buf * BN;
-        wait(&bar.s_full[buf], (BOTH ? c : c >> 1) & 1);
+        wait(&bar.s_full[buf], (DQ ? c >> 1 : c) & 1);
         tc_fence_after();
         float s[HN], dp[HN];
-        if constexpr (HN == 64) tmem_ld64(ts + lanes + half * HN, s);
-        else tmem_ld32(ts + lanes + half * HN, s);
+        tmem_ld64(ts + lanes + half * HN, s);
 #pragma unroll
         for (int e = 0; e < HN; e += 4) {
           if (DQ) {
@@ -1085,7 +1085,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
           s[e + 2] = ex2(s[e + 2]);
           s[e + 3] = ex2(s[e + 3]);
         }
-        if (BOTH) {
+        if (!DQ) {
           mask(s);
           put(ts, s);
           zero(1);
@@ -1093,8 +1093,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
         }
         wait(&bar.pv[0], c & 1);
         tc_fence_after();
-        if constexpr (HN == 64) tmem_ld64(t_dp + lanes + half * HN, dp);
-        else tmem_ld32(t_dp + lanes + half * HN, dp);
+        tmem_ld64(t_dp + lanes + half * HN, dp);
 #pragma unroll
         for (int e = 0; e < HN; e += 4) {
           float4 v = make_float4(delta, delta, delta, delta);
@@ -1105,7 +1104,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
           s[e + 3] *= dp[e + 3] - v.w;
         }
         mask(s);
-        put(BOTH ? t_dp : ts, s);
+        put(DQ ? ts : t_dp, s);
         zero(0);
         tell(&bar.p_full[0]);
       }
@@ -1114,6 +1113,391 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+// ----------------------------------------------------------------- dq and dk, heads of 256
+
+// A pair of CTAs takes 256 own rows, 128 each, and products of 256 x 128 x 16: each CTA's shared
+// memory holds its own rows of both operands (128 KB), half of a block's 128 rows of X1 and X2 for S
+// and dP, and half of X1's columns for the accumulation (32 KB each).  With one CTA alone there is
+// room for blocks of 64 rows only, whose products take almost as long as those of 128 (59 of 64
+// cycles: the first operand's rows have to be read all the same), and for three of them, which is
+// too few to hide the copies.
+struct Pair {
+  static constexpr int D = 256, kBlock = 128;
+  static constexpr int kTile = TR * D * 2;  // own rows, of each operand
+  static constexpr int kPart = 32 * 1024;   // of X1 and X2 by rows, of X1 by columns
+  static constexpr int kThreads = 512;
+  static constexpr int kBytes = kHead + 2 * kTile + 3 * kPart;
+};
+struct PairBars {
+  uint64_t r_full, r_empty, full[3], empty[3], s_full, dp_full, o_full;  // of this CTA
+  uint64_t peer[4], s_read, ds_full, o_empty;  // of the first CTA: what the other's copies bring
+                                               // (full[3], r_full), what both have read or written
+  uint64_t drained;
+  uint32_t tmem;
+  int gave_up;
+};
+static_assert(sizeof(PairBars) <= 512, "");
+
+// Order of the products: S 0, dP 0, then for every block j: S j+1 once S j has been read, the
+// accumulation of j once its dS is there (over its dP), dP j+1.  So the tensor cores have S j+1 to do
+// while dS j is worked out, and every copy has the time of two products to arrive.
+template <int KIND>
+__global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
+    k_slope_pair(const __grid_constant__ CUtensorMap mr1, const __grid_constant__ CUtensorMap mr2,
+                 const __grid_constant__ CUtensorMap m1, const __grid_constant__ CUtensorMap m2,
+                 const __grid_constant__ CUtensorMap m1c, SeqArgs a) {
+  using F = Pair;
+  constexpr bool DQ = KIND == kDq;
+  constexpr int D = F::D, BN = F::kBlock, HN = 64;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  PairBars& bar = *reinterpret_cast<PairBars*>(sm);
+  float* row_values = reinterpret_cast<float*>(sm + 512);  // dk: [2][lse2, delta][BN]
+  uint8_t *own = sm + kHead, *parts = own + 2 * F::kTile;
+  const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31, group = warp >> 2;
+  const int rank = uniform(pair_rank());
+
+  if (tid == 0) {
+    for (uint64_t* b : {&bar.r_full, &bar.r_empty, &bar.s_full, &bar.dp_full, &bar.o_full,
+                        &bar.drained})
+      mbar_init(b, 1);
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&bar.full[i], 1);
+      mbar_init(&bar.empty[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) mbar_init(&bar.peer[i], 1);
+    mbar_init(&bar.s_read, 16);
+    mbar_init(&bar.ds_full, 16);
+    mbar_init(&bar.o_empty, 8);
+    bar.gave_up = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) pair_tmem_alloc(&bar.tmem);
+  tc_fence_before();
+  after_previous();
+  before_next();
+  __syncthreads();
+  pair_sync();
+  tc_fence_after();
+  const uint32_t tmem = uniform(bar.tmem), t_dp = tmem + BN, t_acc = tmem + 2 * BN;
+  auto wait = [&](uint64_t* b, uint32_t parity) { wait_for(b, parity, a.status, &bar.gave_up); };
+  Turns turns((DQ ? a.tq.most : a.tk.most) * (DQ ? a.Hq : a.Hk * a.splits), 2);
+  SlopeItem<DQ, BN, 2 * TR> x;
+
+  if (group == 3) {
+    fewer_registers<64>();
+    if (warp == 12 && lane == 0) {
+      // ---- copies: parts 0 X1 by rows, 1 X2 by rows, 2 X1 by columns
+      int works = 0, c = 0;
+      for (int idx; (idx = turns.next()) >= 0 && !bar.gave_up;) {
+        if (!x.find(a, idx) || x.n == 0) continue;
+        const int row0 = (DQ ? x.t.q0 : x.t.k0) + x.t.at + rank * TR;
+        if (works > 0) wait(&bar.r_empty, (works - 1) & 1);
+        ++works;
+        mbar_arrive_expect_tx(&bar.r_full, 2 * F::kTile);
+        for (int i = 0; i < D / 64; ++i) {
+          tma_load_3d(own + i * 16384, &mr1, i * 64, DQ ? x.head : x.hk, row0, &bar.r_full);
+          tma_load_3d(own + F::kTile + i * 16384, &mr2, i * 64, DQ ? x.head : x.hk, row0,
+                      &bar.r_full);
+        }
+        int g = 0, j = x.j0;
+        for (int it = 0; it < x.n && !bar.gave_up; ++it, ++c) {
+          const int head = DQ ? x.hk : x.head + g, row = (DQ ? x.t.k0 : x.t.q0) + j * BN;
+          for (int y = 0; y < 3; ++y) {
+            if (c > 0) wait(&bar.empty[y], (c - 1) & 1);
+            mbar_arrive_expect_tx(&bar.full[y], F::kPart);
+            uint8_t* to = parts + y * F::kPart;
+            if (y < 2) {
+              for (int i = 0; i < 4; ++i)
+                tma_load_3d(to + i * 8192, y ? &m2 : &m1, i * 64, head, row + rank * 64,
+                            &bar.full[y]);
+            } else {
+              for (int i = 0; i < 2; ++i)
+                tma_load_3d(to + i * 16384, &m1c, rank * 128 + i * 64, head, row, &bar.full[y]);
+            }
+          }
+          if ((j = x.after(j)) == x.j0) ++g;
+        }
+      }
+      if (bar.gave_up) {  // the copies have to land before the CTA ends
+        if (works > 0) mbar_wait(&bar.r_full, (works - 1) & 1, nullptr, 0);
+        if (c > 0)
+          for (int y = 0; y < 3; ++y) mbar_wait(&bar.full[y], (c - 1) & 1, nullptr, 0);
+      }
+    } else if (warp == 13 && rank == 1) {
+      // ---- tells the first CTA what has arrived here, in the order in which it is used
+      int works = 0, c = 0;
+      auto tell = [&](uint64_t* b, uint32_t parity, int to) {
+        wait(b, parity);
+        if (lane == 0) arrive_first(&bar.peer[to]);
+      };
+      for (int idx; (idx = turns.next()) >= 0 && !bar.gave_up;) {
+        if (!uniform(x.find(a, idx)) || uniform(x.n) == 0) continue;
+        tell(&bar.r_full, works & 1, 3);
+        ++works;
+        const int n = uniform(x.n);
+        tell(&bar.full[0], c & 1, 0);
+        tell(&bar.full[1], c & 1, 1);
+        for (int it = 0; it < n; ++it, ++c) {
+          if (it + 1 < n) tell(&bar.full[0], (c + 1) & 1, 0);
+          tell(&bar.full[2], c & 1, 2);
+          if (it + 1 < n) tell(&bar.full[1], (c + 1) & 1, 1);
+        }
+      }
+    } else if (warp == 13) {
+      // ---- products
+      const uint32_t issue = elected();
+      const uint32_t base = smem_u32(sm);
+      const Desc kmaj(sdesc(base, 16, 1024)), mnmaj(sdesc(base, 16384, 1024));
+      constexpr uint32_t kOwn = kHead, kParts = kHead + 2 * F::kTile;
+      int items = 0, works = 0, c = 0;
+      for (int idx; (idx = turns.next()) >= 0;) {
+        if (!uniform(x.find(a, idx))) continue;
+        x.make_uniform();
+        ++items;
+        if (x.n == 0) continue;
+        const int xrows = DQ ? x.t.nk : x.t.nq;
+        wait(&bar.r_full, works & 1);
+        wait(&bar.peer[3], works & 1);
+        ++works;
+        // S (y = 0) or dP (y = 1) of iteration c
+        auto scores = [&](uint32_t to, int y, int c) {
+          wait(&bar.full[y], c & 1);
+          wait(&bar.peer[y], c & 1);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            pair_mma_ss(to, kmaj.at(kOwn + y * F::kTile + (k >> 2) * 16384 + (k & 3) * 32),
+                        kmaj.at(kParts + y * F::kPart + (k >> 2) * 8192 + (k & 3) * 32),
+                        idesc_bf16(256, BN, 0, 0), k > 0, issue);
+          pair_commit(&bar.empty[y], issue);
+          pair_commit(y ? &bar.dp_full : &bar.s_full, issue);
+        };
+        int j = x.j0;
+        scores(tmem, 0, c);
+        scores(t_dp, 1, c);
+        if (x.n == 1) pair_commit(&bar.r_empty, issue);
+        for (int it = 0; it < x.n; ++it, ++c) {
+          const bool ahead = it + 1 < x.n;
+          if (ahead) {
+            wait(&bar.s_read, c & 1);
+            tc_fence_after();
+            scores(tmem, 0, c + 1);
+          } else {
+            wait(&bar.s_read, c & 1);
+          }
+          if (it == 0 && items > 1) wait(&bar.o_empty, items & 1);  // the item before was read
+          wait(&bar.full[2], c & 1);
+          wait(&bar.peer[2], c & 1);
+          wait(&bar.ds_full, c & 1);
+          tc_fence_after();
+          const int steps = min(BN / 16, (xrows - j * BN + 15) / 16);
+          if (steps == BN / 16) {
+#pragma unroll
+            for (int k = 0; k < BN / 16; ++k)
+              pair_mma_ts(t_acc, t_dp + k * 8, mnmaj.at(kParts + 2 * F::kPart + k * 2048),
+                          idesc_bf16(256, D, 0, 1), it > 0 || k > 0, issue);
+          } else {
+#pragma unroll 1
+            for (int k = 0; k < steps; ++k)
+              pair_mma_ts(t_acc, t_dp + k * 8, mnmaj.at(kParts + 2 * F::kPart + k * 2048),
+                          idesc_bf16(256, D, 0, 1), it > 0 || k > 0, issue);
+          }
+          pair_commit(&bar.empty[2], issue);
+          if (ahead) {
+            scores(t_dp, 1, c + 1);
+            if (it + 2 == x.n) pair_commit(&bar.r_empty, issue);
+          } else {
+            pair_commit(&bar.o_full, issue);
+          }
+          j = x.after(j);
+        }
+      }
+      if (bar.gave_up) {
+        pair_commit(&bar.drained, issue);
+        mbar_wait(&bar.drained, 0, nullptr, 0);
+      }
+    }
+  } else if (group == 2) {
+    // ---- results: a thread per row
+    fewer_registers<64>();
+    const int r = tid & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    int works = 0;
+    for (int idx; (idx = turns.next()) >= 0;) {
+      if (!x.find(a, idx)) continue;
+      const int row = x.t.at + rank * TR + r, side = DQ ? x.t.nq : x.t.nk;
+      if (x.n > 0) {
+        wait(&bar.o_full, works & 1);
+        ++works;
+        tc_fence_after();
+      }
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float y[32];
+        if (x.n > 0) {
+          tmem_ld32(t_acc + lanes + c, y);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = 0.f;
+        }
+        if (c == D - 32) {  // read: the next item may accumulate
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_first(&bar.o_empty);
+        }
+        if (row < side) {
+          if (DQ)
+            write_row(reinterpret_cast<__nv_bfloat16*>(a.dq) +
+                          ((int64_t)(x.t.q0 + row) * a.Hq + x.head) * D + c, y, a.scale);
+          else
+            write_dkv<D>(a, false, x.t.k0 + row, x.hk, x.head, c, y);
+        }
+      }
+    }
+  } else {
+    // ---- a thread per row and half of the block's columns
+    more_registers<192>();
+    const int half = group, r = tid & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    int c = 0;  // iterations of all items
+    for (int idx; (idx = turns.next()) >= 0;) {
+      if (!x.find(a, idx)) continue;
+      const int off = x.t.nk - x.t.nq, at = x.t.at + rank * TR;
+      const int first_row = at + (warp & 3) * 32, row = at + r;
+      const int xrows = DQ ? x.t.nk : x.t.nq;
+      float lse2 = INFINITY, delta = 0.f, ahead = 0.f;
+      if (DQ && row < x.t.nq) {
+        lse2 = a.lse2[(int64_t)x.head * a.Nq + x.t.q0 + row];
+        delta = a.delta[(int64_t)x.head * a.Nq + x.t.q0 + row];
+      }
+      // dk: the first 128 threads fetch lse2 of the next block's queries, the others delta
+      auto value = [&](int g, int j) {
+        const int q = j * BN + r;
+        const float* src = half == 0 ? a.lse2 : a.delta;
+        return q < x.t.nq ? src[(int64_t)(x.head + g) * a.Nq + x.t.q0 + q] : 0.f;
+      };
+      int g = 0, j = x.j0;
+      if (!DQ && x.n > 0) ahead = value(0, x.j0);
+      for (int it = 0; it < x.n; ++it, ++c) {
+        const int kb = j * BN;
+        if ((j = x.after(j)) == x.j0) ++g;
+        float* lv = row_values + (c & 1) * 2 * BN;
+        if (!DQ) {
+          lv[tid] = ahead;
+          bar_sync(1, 256);
+          if (it + 1 < x.n) ahead = value(g, j);
+        }
+        int c0 = 0, c1;  // columns [c0, c1) of the row count
+        bool whole;
+        if (DQ) {
+          c1 = (a.causal ? min(x.t.nk, row + off + 1) : x.t.nk) - kb;
+          whole = kb + BN <= (a.causal ? min(x.t.nk, first_row + off + 1) : x.t.nk);
+        } else {
+          c1 = x.t.nq - kb;
+          if (a.causal) c0 = row - off - kb;
+          whole = kb + BN <= x.t.nq && (!a.causal || first_row + 31 - off <= kb);
+        }
+        wait(&bar.s_full, c & 1);
+        tc_fence_after();
+        float s[HN], dp[HN];
+        tmem_ld64(tmem + lanes + half * HN, s);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_first(&bar.s_read);
+#pragma unroll
+        for (int e = 0; e < HN; e += 4) {
+          if (DQ) {
+            fma2(s[e], s[e + 1], a.sl, -lse2);
+            fma2(s[e + 2], s[e + 3], a.sl, -lse2);
+          } else {
+            const float4 v = *reinterpret_cast<const float4*>(lv + half * HN + e);
+            s[e] = fmaf(s[e], a.sl, -v.x);
+            s[e + 1] = fmaf(s[e + 1], a.sl, -v.y);
+            s[e + 2] = fmaf(s[e + 2], a.sl, -v.z);
+            s[e + 3] = fmaf(s[e + 3], a.sl, -v.w);
+          }
+          s[e] = ex2(s[e]);
+          s[e + 1] = ex2(s[e + 1]);
+          s[e + 2] = ex2(s[e + 2]);
+          s[e + 3] = ex2(s[e + 3]);
+        }
+        wait(&bar.dp_full, c & 1);
+        tc_fence_after();
+        tmem_ld64(t_dp + lanes + half * HN, dp);
+#pragma unroll
+        for (int e = 0; e < HN; e += 4) {
+          float4 v = make_float4(delta, delta, delta, delta);
+          if (!DQ) v = *reinterpret_cast<const float4*>(lv + BN + half * HN + e);
+          s[e] *= dp[e] - v.x;
+          s[e + 1] *= dp[e + 1] - v.y;
+          s[e + 2] *= dp[e + 2] - v.z;
+          s[e + 3] *= dp[e + 3] - v.w;
+        }
+        if (!whole) {
+#pragma unroll
+          for (int e = 0; e < HN; ++e)
+            s[e] = half * HN + e >= c0 && half * HN + e < c1 ? s[e] : 0.f;
+        }
+        bar_sync(2 + (warp & 3), 64);  // both halves of dP have been read
+        uint32_t y[HN / 2];
+#pragma unroll
+        for (int e = 0; e < HN / 2; ++e) y[e] = bf16x2(s[2 * e], s[2 * e + 1]);
+        tmem_st32(t_dp + lanes + half * 32, y);
+        if (kb + BN > xrows && (xrows & 15)) {  // rows behind the sequence in its last 16
+          wait(&bar.full[2], c & 1);
+          zero_rows<256>(parts + 2 * F::kPart, 2, 16384, xrows - kb, (xrows - kb + 15) & ~15, tid);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_first(&bar.ds_full);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  __syncwarp();
+  pair_sync();  // neither CTA's barriers or TMEM are used any more
+  if (warp == 0) pair_tmem_dealloc(tmem);
+}
+
+// dk and dv from their parts, which are added in their order: a CTA takes SUM_ROWS rows of a key tile
+// and head.  Bound by HBM.
+constexpr int SUM_ROWS = 16;
+template <int D>
+__global__ void __launch_bounds__(256) k_attn_sum(SeqArgs a) {
+  after_previous();
+  before_next();
+  Tile t;
+  const int per = a.tk.rows / SUM_ROWS, hk = blockIdx.x % a.Hk, x = blockIdx.x / a.Hk;
+  if (!tile_of<true>(a, x / per, &t)) return;
+  t.at += x % per * SUM_ROWS;
+  const int rows = min(SUM_ROWS, t.nk - t.at);
+  const int64_t step = a.Nk * a.Hk * D;
+#pragma unroll 2
+  for (int i = threadIdx.x; i < rows * (D / 4); i += 256) {
+    const int64_t at = ((int64_t)(t.k0 + t.at + i / (D / 4)) * a.Hk + hk) * D + i % (D / 4) * 4;
+    const float *pk = a.part_k + at, *pv = a.part_v + at;
+    float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
+#pragma unroll 4
+    for (int q = 0; q < a.splits; ++q) {
+      const float4 y = *reinterpret_cast<const float4*>(pk + q * step);
+      const float4 z = *reinterpret_cast<const float4*>(pv + q * step);
+      k.x += y.x;
+      k.y += y.y;
+      k.z += y.z;
+      k.w += y.w;
+      v.x += z.x;
+      v.y += z.y;
+      v.z += z.z;
+      v.w += z.w;
+    }
+    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.dk) + at) =
+        make_uint2(bf16x2(k.x, k.y), bf16x2(k.z, k.w));
+    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.dv) + at) =
+        make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
+  }
 }
 
 // ---------------------------------------------------------------------------------- host
@@ -1138,6 +1522,12 @@ int64_t ctas_of(int64_t items) {
   return items < sms ? items : sms;
 }
 
+// The same in pairs.
+int64_t pairs_of(int64_t items) {
+  const int64_t sms = device_sms() / 2;
+  return 2 * (items < sms ? items : sms);
+}
+
 template <int D>
 cudaError_t fwd(const SeqArgs& a, cudaStream_t st) {
   CUtensorMap q, k, v;
@@ -1152,41 +1542,60 @@ cudaError_t fwd(const SeqArgs& a, cudaStream_t st) {
 
 template <int D>
 cudaError_t bwd(const SeqArgs& a, cudaStream_t st) {
-  constexpr int BN = Slope<D>::kBlock;
   const int64_t os = (int64_t)a.Hq * D;
-  CUtensorMap q, d, k, v, qb, db, kb, vb;  // boxes of 128 rows, and of the blocks' rows
+  CUtensorMap q, d, k, v;  // boxes of 128 rows
   if (a.Nq > 0 && (!make(&q, a.q, a.Nq, a.qs, a.Hq, D, 128) ||
-                   !make(&d, a.dO, a.Nq, os, a.Hq, D, 128) ||
-                   !make(&qb, a.q, a.Nq, a.qs, a.Hq, D, BN) ||
-                   !make(&db, a.dO, a.Nq, os, a.Hq, D, BN)))
+                   !make(&d, a.dO, a.Nq, os, a.Hq, D, 128)))
     return cudaErrorInvalidValue;
   if (a.Nk > 0 && (!make(&k, a.k, a.Nk, a.ks, a.Hk, D, 128) ||
-                   !make(&v, a.v, a.Nk, a.vs, a.Hk, D, 128) ||
-                   !make(&kb, a.k, a.Nk, a.ks, a.Hk, D, BN) ||
-                   !make(&vb, a.v, a.Nk, a.vs, a.Hk, D, BN)))
+                   !make(&v, a.v, a.Nk, a.vs, a.Hk, D, 128)))
     return cudaErrorInvalidValue;
-  if (a.Nq == 0) q = d = qb = db = k;
-  if (a.Nk == 0) k = v = kb = vb = q;
-  if (a.Nk > 0) {
-    const int64_t ctas = (int64_t)a.tk.most * a.Hk;
-    cudaError_t e = launch<k_slope<D, D == 256 ? kDk : kDkv>>(ctas_of(ctas), Slope<D>::kThreads,
-                           Slope<D>::kBytes, st, k, v, qb, db, a);
-    if (e != cudaSuccess) return e;
-    if constexpr (D == 256) {
-      e = launch<k_flash<D, false>>(ctas_of(ctas), Flash<D>::kThreads, Flash<D>::kBytes, st, k, q, d, a);
+  if (a.Nq == 0) q = d = k;
+  if (a.Nk == 0) k = v = q;
+  const int64_t key_items = (int64_t)a.tk.most * a.Hk * a.splits;
+  const int64_t query_items = (int64_t)a.tq.most * a.Hq;
+  cudaError_t e = cudaSuccess;
+  if constexpr (D == 256) {
+    CUtensorMap qh, dh, kh, vh;  // boxes of 64 rows
+    if (a.Nq > 0 && (!make(&qh, a.q, a.Nq, a.qs, a.Hq, D, 64) ||
+                     !make(&dh, a.dO, a.Nq, os, a.Hq, D, 64)))
+      return cudaErrorInvalidValue;
+    if (a.Nk > 0 && (!make(&kh, a.k, a.Nk, a.ks, a.Hk, D, 64) ||
+                     !make(&vh, a.v, a.Nk, a.vs, a.Hk, D, 64)))
+      return cudaErrorInvalidValue;
+    if (a.Nq == 0) qh = dh = kh;
+    if (a.Nk == 0) kh = vh = qh;
+    if (a.Nk > 0) {
+      e = launch<k_slope_pair<kDk>>(pairs_of(key_items), Pair::kThreads, Pair::kBytes, st, k, v, qh,
+                                    dh, q, a);
       if (e != cudaSuccess) return e;
+      e = launch<k_flash<D, false>>(ctas_of(2 * key_items), Flash<D>::kThreads, Flash<D>::kBytes, st,
+                                    k, q, d, a);
     }
+    if (e == cudaSuccess && a.Nq > 0)
+      e = launch<k_slope_pair<kDq>>(pairs_of(query_items), Pair::kThreads, Pair::kBytes, st, q, d,
+                                    kh, vh, k, a);
+  } else {
+    if (a.Nk > 0)
+      e = launch<k_slope<D, kDkv>>(ctas_of(key_items), Slope<D>::kThreads, Slope<D>::kBytes, st, k,
+                                   v, q, d, a);
+    if (e == cudaSuccess && a.Nq > 0)
+      e = launch<k_slope<D, kDq>>(ctas_of(query_items), Slope<D>::kThreads, Slope<D>::kBytes, st,
+                                  q, d, k, v, a);
   }
-  if (a.Nq == 0) return cudaSuccess;
-  return launch<k_slope<D, kDq>>(ctas_of((int64_t)a.tq.most * a.Hq), Slope<D>::kThreads,
-                Slope<D>::kBytes, st, q, d, kb, vb, a);
+  if (e == cudaSuccess && a.Nk > 0 && a.splits > 1)
+    e = launch_behind(k_attn_sum<D>,
+                      dim3((unsigned)((int64_t)a.tk.most * a.Hk * (a.tk.rows / SUM_ROWS))), 256, 0,
+                      st, a);
+  return e;
 }
 
 }  // namespace
 
 TcPlan tc_plan(int D) {
   const int two = D == 64 ? Flash<64>::kTiles : D == 128 ? Flash<128>::kTiles : Flash<256>::kTiles;
-  return TcPlan{two * TR, TR, TR};  // fwd: rows, of which `pack` belong to a token
+  const int own = D == 256 ? 2 * TR : TR;
+  return TcPlan{two * TR, own, own};  // fwd: rows, of which `pack` belong to a token
 }
 cudaError_t launch_fwd_tc(const SeqArgs& a, int D, cudaStream_t st) {
   return D == 64 ? fwd<64>(a, st) : D == 128 ? fwd<128>(a, st) : fwd<256>(a, st);
