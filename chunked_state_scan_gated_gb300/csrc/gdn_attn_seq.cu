@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(256) k_attn_rows(SeqArgs a) {
 
 constexpr int ST = 64;   // rows and columns of a tile
 constexpr int LT = 68;   // a transposed operand's row in shared memory: 16-byte aligned
-constexpr int F_NT = 128, F_DC = 32, F_KC = 16;
+constexpr int F_HALF = 128, F_NT = 2 * F_HALF, F_DC = 32, F_KC = 16;
 
 template <typename T>
 __device__ __forceinline__ float4 ld4(const T* p) {
@@ -209,10 +209,10 @@ __device__ __forceinline__ void st4(T* p, float x, float y, float z, float w) {
   }
 }
 
-// dst[c][row] = columns [c0, c0 + C) of rows [0, 64) of src (zeros from row n on).
+// By NT threads: dst[c][row] = columns [c0, c0 + C) of rows [0, 64) of src (zeros from row n on).
 template <int C, int NT, typename T>
 __device__ __forceinline__ void load_t(float* dst, const T* src, int64_t stride, int n, int c0) {
-  for (int i = threadIdx.x; i < ST * (C / 4); i += NT) {
+  for (int i = threadIdx.x % NT; i < ST * (C / 4); i += NT) {
     const int r = i % ST, c = i / ST * 4;  // a warp's stores fall on different banks
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < n) x = ld4(src + (int64_t)r * stride + c0 + c);
@@ -225,7 +225,7 @@ __device__ __forceinline__ void load_t(float* dst, const T* src, int64_t stride,
 // dst[row][D] = rows [r0, r0 + R) of src (zeros from row n on).
 template <int D, int R, int NT, typename T>
 __device__ __forceinline__ void load_r(float* dst, const T* src, int64_t stride, int r0, int n) {
-  for (int i = threadIdx.x; i < R * (D / 4); i += NT) {
+  for (int i = threadIdx.x % NT; i < R * (D / 4); i += NT) {
     const int r = i / (D / 4), c = i % (D / 4) * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r0 + r < n) x = ld4(src + (int64_t)(r0 + r) * stride + c);
@@ -234,23 +234,33 @@ __device__ __forceinline__ void load_r(float* dst, const T* src, int64_t stride,
 }
 
 template <int D>
+constexpr int fwd_half() {  // floats of a half's buffers: K's chunk, P, V's chunk
+  return F_DC * LT + ST * LT + F_KC * D;
+}
+template <int D>
 constexpr size_t fwd_smem() {
-  return (size_t)(D * LT + F_DC * LT + ST * LT + F_KC * D) * 4;
+  return (size_t)(D * LT + 2 * fwd_half<D>() + 2 * ST) * 4;
 }
 
-// 64 queries of one head; a thread has 8 rows x 4 keys of the scores, 8 rows x D/16 columns of o.
+// 64 queries of one head.  Two halves of the CTA take the blocks of 64 keys in turn, each with a
+// softmax of its own, and are joined at the end: a prompt's last tile, which takes the longest, is
+// done in half the time (9 prompts up to 700 tokens, 12 heads of 64: 121 us with one half).  A thread
+// has 8 rows x 4 keys of the scores, 8 rows x D/16 columns of o.
 template <int D, typename T>
 __global__ void __launch_bounds__(F_NT) k_attn_fwd_simt(SeqArgs a) {
   extern __shared__ __align__(16) float sm[];
-  float *Qt = sm, *Kt = Qt + D * LT, *Pt = Kt + F_DC * LT, *Vc = Pt + ST * LT;
   constexpr int NV = D / 64;
+  const int half = threadIdx.x / F_HALF, tid = threadIdx.x % F_HALF;
+  float *Qt = sm, *Kt = Qt + D * LT + half * fwd_half<D>(), *Pt = Kt + F_DC * LT;
+  float *Vc = Pt + ST * LT, *ml = sm + D * LT + 2 * fwd_half<D>();
+  auto sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + half), "n"(F_HALF) : "memory"); };
   after_previous();
   before_next();
   if (blockIdx.x == 0 && threadIdx.x == 0) check_single(a);
   const int h = blockIdx.x % a.Hq, hk = h / a.G;
   Tile t;
   if (!tile_of<false>(a, blockIdx.x / a.Hq, &t)) return;
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  const int ty = tid / 16, tx = tid % 16;
   const int rows = min(ST, t.nq - t.at), end = keys_seen(a, t, ST), off = t.nk - t.nq;
   const T* q = (const T*)a.q + (int64_t)(t.q0 + t.at) * a.qs + (int64_t)h * D;
   const T* k = (const T*)a.k + (int64_t)t.k0 * a.ks + (int64_t)hk * D;
@@ -264,12 +274,13 @@ __global__ void __launch_bounds__(F_NT) k_attn_fwd_simt(SeqArgs a) {
 #pragma unroll
     for (int c = 0; c < NV; ++c) o[i][c][0] = o[i][c][1] = o[i][c][2] = o[i][c][3] = 0.f;
   }
-  for (int kb = 0; kb < end; kb += ST) {
+  __syncthreads();
+  for (int kb = half * ST; kb < end; kb += 2 * ST) {
     float s[8][4] = {};
     for (int dc = 0; dc < D; dc += F_DC) {
-      __syncthreads();
-      load_t<F_DC, F_NT>(Kt, k + (int64_t)kb * a.ks, a.ks, t.nk - kb, dc);
-      __syncthreads();
+      sync();
+      load_t<F_DC, F_HALF>(Kt, k + (int64_t)kb * a.ks, a.ks, t.nk - kb, dc);
+      sync();
 #pragma unroll 8
       for (int d = 0; d < F_DC; ++d) {
         const float4 x0 = *reinterpret_cast<const float4*>(Qt + (dc + d) * LT + ty * 8);
@@ -314,9 +325,9 @@ __global__ void __launch_bounds__(F_NT) k_attn_fwd_simt(SeqArgs a) {
       *reinterpret_cast<float4*>(at + 4) = make_float4(s[4][j], s[5][j], s[6][j], s[7][j]);
     }
     for (int kc = 0; kc < min(ST, end - kb); kc += F_KC) {
-      __syncthreads();
-      load_r<D, F_KC, F_NT>(Vc, v + (int64_t)kb * a.vs, a.vs, kc, t.nk - kb);
-      __syncthreads();
+      sync();
+      load_r<D, F_KC, F_HALF>(Vc, v + (int64_t)kb * a.vs, a.vs, kc, t.nk - kb);
+      sync();
 #pragma unroll 4
       for (int j = 0; j < F_KC; ++j) {
         const float4 x0 = *reinterpret_cast<const float4*>(Pt + (kc + j) * LT + ty * 8);
@@ -337,18 +348,41 @@ __global__ void __launch_bounds__(F_NT) k_attn_fwd_simt(SeqArgs a) {
     }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int x = 1; x < 16; x <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
-    if (ty * 8 + i >= rows) continue;
-    const int64_t row = (int64_t)(t.q0 + t.at + ty * 8 + i) * a.Hq + h;
-    const float r = l[i] != 0.f ? 1.f / l[i] : 0.f;
+  // the second half's o goes over Q, its m and l behind the buffers
+  __syncthreads();
+  if (half == 1) {
 #pragma unroll
-    for (int c = 0; c < NV; ++c)
-      st4((T*)a.out + row * D + c * 64 + tx * 4, o[i][c][0] * r, o[i][c][1] * r, o[i][c][2] * r,
-          o[i][c][3] * r);
-    if (tx == 0 && a.lse)
-      a.lse[row] = l[i] != 0.f ? (m[i] + log2f(l[i])) * kLn2 : m[i] == m[i] ? -INFINITY : m[i];
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+      for (int c = 0; c < NV; ++c)
+        *reinterpret_cast<float4*>(Qt + (ty * 8 + i) * D + c * 64 + tx * 4) =
+            make_float4(o[i][c][0], o[i][c][1], o[i][c][2], o[i][c][3]);
+      if (tx == 0) {
+        ml[ty * 8 + i] = m[i];
+        ml[ST + ty * 8 + i] = l[i];
+      }
+    }
+  }
+  __syncthreads();
+  if (half == 1) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (ty * 8 + i >= rows) continue;
+    const float m1 = ml[ty * 8 + i], l1 = ml[ST + ty * 8 + i], top = fmaxf(m[i], m1);
+    const float base = top == -INFINITY ? 0.f : top, f0 = ex2(m[i] - base), f1 = ex2(m1 - base);
+    const float sum = l[i] * f0 + l1 * f1, r = sum != 0.f ? 1.f / sum : 0.f;
+    const int64_t row = (int64_t)(t.q0 + t.at + ty * 8 + i) * a.Hq + h;
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+      const float4 y = *reinterpret_cast<const float4*>(Qt + (ty * 8 + i) * D + c * 64 + tx * 4);
+      st4((T*)a.out + row * D + c * 64 + tx * 4, (o[i][c][0] * f0 + y.x * f1) * r,
+          (o[i][c][1] * f0 + y.y * f1) * r, (o[i][c][2] * f0 + y.z * f1) * r,
+          (o[i][c][3] * f0 + y.w * f1) * r);
+    }
+    if (tx == 0 && a.lse) a.lse[row] = sum != 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
   }
 }
 
@@ -513,9 +547,10 @@ size_t up(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Workspace: the lists' counts, the lists, the backward's rows of lse and delta.
 struct Layout {
-  size_t lq, lk, lse2, delta, part_k, part_v, total;
+  size_t lq, lk, lse2, delta, part_k, part_v, part_o, part_lse, total;
   int mq, mk;  // upper bounds of the tiles
   int splits;  // parts that a key head's query heads are divided into, for dk and dv
+  int parts;   // .. and the keys of the forward
 };
 Layout layout(const gdn_attn_seq_problem* p, bool bwd, int rq, int rk) {
   Layout y;
@@ -539,7 +574,22 @@ Layout layout(const gdn_attn_seq_problem* p, bool bwd, int rq, int rk) {
       if (G % s == 0) y.splits = (int)s;
   const size_t part = y.splits > 1 ? up((size_t)y.splits * p->Nk * p->Hk * p->D * 4) : 0;
   y.part_v = y.part_k + part;
-  y.total = y.part_v + part;
+  y.part_o = y.part_v + part;
+  // bf16 forward: tiles for less than one wave over many keys (a few new tokens behind a long
+  // context) leave SMs idle, so the keys of every tile are divided, 512 at least to a part on average;
+  // the parts of o are fp32 and k_attn_merge joins them (64 tokens behind 31936, 32 on 8 heads of 128:
+  // 338 us without, 80 with; 256 tiles of 9 sequences behind up to 16000 tokens: 308 and 330).
+  y.parts = 1;
+  const int64_t items = (int64_t)y.mq * (p->Hq / tc_pack(G));
+  if (!bwd && p->dtype == GDN_BF16 && items > 0) {
+    int64_t s = items < 152 ? (2 * 152 + items - 1) / items : 1;
+    const int64_t keys = p->Nk / (n > 0 ? n : 1);
+    if (s > keys / 512) s = keys / 512;
+    y.parts = (int)(s < 1 ? 1 : s > kMaxParts ? kMaxParts : s);
+  }
+  const size_t rows = y.parts > 1 ? (size_t)y.parts * p->Nq * p->Hq * 4 : 0;
+  y.part_lse = y.part_o + up(rows * p->D);
+  y.total = y.part_lse + up(rows);
   return y;
 }
 Layout layout_of(const gdn_attn_seq_problem* p, bool bwd) {
@@ -581,6 +631,9 @@ gdn_status begin(const gdn_attn_seq_problem* p, bool bwd, const int32_t* cu_q,
   a->part_k = (float*)(ws + y.part_k);
   a->part_v = (float*)(ws + y.part_v);
   a->splits = y.splits;
+  a->part_o = (float*)(ws + y.part_o);
+  a->part_lse = (float*)(ws + y.part_lse);
+  a->parts = y.parts;
   if (cu_q && p->n_seqs > 1) {
     int* count = (int*)ws;
     PlanSide sq{(Tile*)(ws + y.lq), count, a->tq.rows, y.mq};

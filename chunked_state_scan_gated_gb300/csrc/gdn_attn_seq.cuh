@@ -44,8 +44,12 @@ struct SeqArgs {
   Tiles tq, tk;
   float *part_k, *part_v;  // [splits][Nk][Hk][D]: dk, dv of a part of a key head's query heads
   int splits;              // 1: none, dk and dv are written themselves
+  float *part_o, *part_lse;  // [parts][Nq][Hq](D): o and log2-sum over a part of the keys
+  int parts;               // 1: none, o and lse are written themselves
   int32_t* status;
 };
+
+constexpr int kMaxParts = 32;
 
 __device__ __forceinline__ int clamp_row(int64_t x, int64_t n) {
   return (int)(x < 0 ? 0 : x > n ? n : x);

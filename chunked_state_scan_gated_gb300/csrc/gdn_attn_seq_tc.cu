@@ -196,16 +196,22 @@ struct Item {
   using F = Flash<D>;
   Tile t;
   int head, hk;    // the first query head (FWD), the key head
+  int part;        // of the keys (FWD)
   int n, per, j0;  // iterations; of one query head; the first block
   int lo0, lo1, hi0, hi1;
   __device__ __forceinline__ int lo(int i) const { return i ? lo1 : lo0; }
   __device__ __forceinline__ int hi(int i) const { return i ? hi1 : hi0; }
   __device__ __forceinline__ bool find(const SeqArgs& a, int idx) {
-    const int groups = FWD ? a.Hq / a.pack : a.Hk * a.splits, part = idx % groups;
+    part = 0;
+    if (FWD && a.parts > 1) {
+      part = idx % a.parts;
+      idx /= a.parts;
+    }
+    const int groups = FWD ? a.Hq / a.pack : a.Hk * a.splits, g = idx % groups;
     const int subs = FWD ? 1 : a.tk.rows / TR, tile = idx / groups;
     if (!tile_of<!FWD>(a, tile / subs, &t)) return false;
     if (!FWD) t.at += tile % subs * TR;  // dv: 128 rows of one of the list's tiles
-    head = part * (FWD ? a.pack : a.G / a.splits);
+    head = g * (FWD ? a.pack : a.G / a.splits);
     hk = head / a.G;
     const int side = FWD ? t.nq : t.nk, rows = FWD ? TR / a.pack : TR;
     lo0 = lo1 = hi0 = hi1 = 0;
@@ -223,6 +229,13 @@ struct Item {
       }
       (i ? lo1 : lo0) = from;
       (i ? hi1 : hi0) = to;
+    }
+    if (FWD && a.parts > 1) {  // this part's share of the blocks
+      const int all = max(hi0, hi1), from = (int)((int64_t)all * part / a.parts);
+      const int to = (int)((int64_t)all * (part + 1) / a.parts);
+      lo0 = lo1 = from;
+      hi0 = max(from, min(hi0, to));
+      hi1 = max(from, min(hi1, to));
     }
     j0 = lo0;
     per = max(hi0, hi1) - j0;
@@ -285,7 +298,7 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
   auto acc_of = [&](int t) { return tmem + 256 + t * D; };
   auto wait = [&](uint64_t* b, uint32_t parity) { wait_for(b, parity, a.status, &bar.gave_up); };
   if (FWD && blockIdx.x == 0 && tid == 0) check_single(a);
-  Turns turns(FWD ? a.tq.most * (a.Hq / a.pack) : a.tk.most * (a.tk.rows / TR) * a.Hk * a.splits);
+  Turns turns(FWD ? a.tq.most * (a.Hq / a.pack) * a.parts : a.tk.most * (a.tk.rows / TR) * a.Hk * a.splits);
   Item<D, FWD> x;
 
   if (group == 3) {
@@ -369,10 +382,10 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
                             kRing + stage * F::kStage, kId, ks, true, issue);
         };
         if constexpr (NT == 2) {
-          // forward: tile i takes the blocks [0, last[i]); the ring holds K 0, V 0, K 1, V 1, ..
-          const int last[2] = {x.hi0, x.hi1};
-          auto score = [&](int i, int j) {
-            scores(i, i, 0, j);
+          // forward: tile i takes the first last[i] blocks; the ring holds K 0, V 0, K 1, V 1, ..
+          const int last[2] = {x.hi0 - x.j0, x.hi1 - x.j0};
+          auto score = [&](int i, int it) {
+            scores(i, i, 0, x.j0 + it);
             commit_to(&bar.s_full[i], issue);
           };
           wait(&bar.full[stage], turn & 1);
@@ -386,7 +399,7 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
             wait(&bar.o_empty[1], items & 1);
           }
           for (int it = 0; it < x.n; ++it) {
-            const int sv = stage, ks = steps(it);
+            const int sv = stage, ks = steps(x.j0 + it);
             wait(&bar.full[sv], turn & 1);
             next();
             const int sk = stage, tk = turn;
@@ -503,7 +516,8 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
             if (lane == 0) mbar_arrive(&bar.o_empty[i]);
           }
           if (row < side) {
-            if (FWD) write_row(reinterpret_cast<__nv_bfloat16*>(a.out) + out * D + c, y, f);
+            if (FWD && a.parts > 1) write_row(a.part_o + (x.part * a.Nq * a.Hq + out) * D + c, y, f);
+            else if (FWD) write_row(reinterpret_cast<__nv_bfloat16*>(a.out) + out * D + c, y, f);
             else write_dkv<D>(a, true, x.t.k0 + row, x.hk, x.head, c, y);
           }
         }
@@ -689,9 +703,12 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
           row_factors[i * 128 + r] = l != 0.f ? 1.f / l : 0.f;
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.l_full[i]);
-          if (a.lse && row < x.t.nq)
-            a.lse[(int64_t)(x.t.q0 + row) * a.Hq + x.head + r % a.pack] =
-                l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+          if (row < x.t.nq) {
+            const int64_t out = (int64_t)(x.t.q0 + row) * a.Hq + x.head + r % a.pack;
+            const float lse2 = l != 0.f ? m + log2f(l) : -INFINITY;
+            if (a.parts > 1) a.part_lse[x.part * a.Nq * a.Hq + out] = lse2;
+            else if (a.lse) a.lse[out] = lse2 * kLn2;
+          }
         }
       }
       ++items;
@@ -1500,6 +1517,61 @@ __global__ void __launch_bounds__(256) k_attn_sum(SeqArgs a) {
   }
 }
 
+// o and lse from the parts of the keys: a CTA takes SUM_ROWS rows of a tile.  With L_p the part's
+// log2-sum and o_p its average: w_p = 2^(L_p - max L), o = sum w_p o_p / sum w_p.  A part without
+// keys has L_p = -inf and counts nothing.
+template <int D>
+__global__ void __launch_bounds__(256) k_attn_merge(SeqArgs a) {
+  constexpr int PER = D / 4;  // threads of a row
+  __shared__ float s_w[SUM_ROWS][kMaxParts];
+  after_previous();
+  before_next();
+  Tile t;
+  const int groups = a.Hq / a.pack, rows = a.tq.rows * a.pack, per = rows / SUM_ROWS;
+  const int head = blockIdx.x % groups * a.pack, y = blockIdx.x / groups;
+  if (!tile_of<false>(a, y / per, &t)) return;
+  const int r0 = y % per * SUM_ROWS;
+  const int64_t step = a.Nq * a.Hq;
+  auto row_of = [&](int r, int64_t* at) {  // row r0 + r of the tile: whether it exists, its place
+    const int token = t.at + (r0 + r) / a.pack;
+    *at = (int64_t)(t.q0 + token) * a.Hq + head + (r0 + r) % a.pack;
+    return token < t.nq;
+  };
+  if (threadIdx.x < SUM_ROWS) {
+    int64_t at;
+    if (row_of(threadIdx.x, &at)) {
+      float m = -INFINITY, l = 0.f;
+      for (int p = 0; p < a.parts; ++p) m = fmaxf(m, a.part_lse[p * step + at]);
+      const float base = m == -INFINITY ? 0.f : m;
+      for (int p = 0; p < a.parts; ++p) {
+        const float w = ex2(a.part_lse[p * step + at] - base);
+        s_w[threadIdx.x][p] = w;
+        l += w;
+      }
+      for (int p = 0; p < a.parts; ++p) s_w[threadIdx.x][p] = l != 0.f ? s_w[threadIdx.x][p] / l : 0.f;
+      if (a.lse) a.lse[at] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < SUM_ROWS * PER; i += 256) {
+    int64_t at;
+    if (!row_of(i / PER, &at)) continue;
+    const float* src = a.part_o + at * D + i % PER * 4;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int p = 0; p < a.parts; ++p) {
+      const float4 x = *reinterpret_cast<const float4*>(src + p * step * D);
+      const float w = s_w[i / PER][p];
+      o.x = fmaf(x.x, w, o.x);
+      o.y = fmaf(x.y, w, o.y);
+      o.z = fmaf(x.z, w, o.z);
+      o.w = fmaf(x.w, w, o.w);
+    }
+    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + at * D + i % PER * 4) =
+        make_uint2(bf16x2(o.x, o.y), bf16x2(o.z, o.w));
+  }
+}
+
 // ---------------------------------------------------------------------------------- host
 
 template <auto kKernel, typename... M>
@@ -1536,8 +1608,12 @@ cudaError_t fwd(const SeqArgs& a, cudaStream_t st) {
   if (a.Nk > 0 && (!make(&k, a.k, a.Nk, a.ks, a.Hk, D, 128) ||
                    !make(&v, a.v, a.Nk, a.vs, a.Hk, D, 128)))
     return cudaErrorInvalidValue;
-  return launch<k_flash<D, true>>(ctas_of((int64_t)a.tq.most * (a.Hq / a.pack)),
-                Flash<D>::kThreads, Flash<D>::kBytes, st, q, k, v, a);
+  const int64_t tiles = (int64_t)a.tq.most * (a.Hq / a.pack);
+  const cudaError_t e = launch<k_flash<D, true>>(ctas_of(tiles * a.parts), Flash<D>::kThreads,
+                                                 Flash<D>::kBytes, st, q, k, v, a);
+  if (e != cudaSuccess || a.parts == 1) return e;
+  return launch_behind(k_attn_merge<D>,
+                       dim3((unsigned)(tiles * (a.tq.rows * a.pack / SUM_ROWS))), 256, 0, st, a);
 }
 
 template <int D>

@@ -707,7 +707,7 @@ gdn_status gdn_slot_map(const gdn_slot_problem* p, const int32_t* ctx_len,
  *    value row of a sequence may reach the queries of the same sequence that do not see it.)
  *  - fp32 softmax and sums.  On bf16, p and ds are rounded to bf16 for their products.
  *  - Deterministic: the same bits for the same call.
- *  - Workspace 256-byte aligned (none in the forward of one sequence, whose size is 0); calls that
+ *  - Workspace 256-byte aligned (none in most forwards of one sequence, whose size is 0); calls that
  *    can run at the same time need one each.
  * Errors: null or misaligned pointer, sizes < 0, Hq % Hk != 0, n_seqs < 1 with rows given, cu_q
  * NULL with rows that n_seqs does not divide or with a cu_k, cu_k NULL with Nk != Nq and cu_q
