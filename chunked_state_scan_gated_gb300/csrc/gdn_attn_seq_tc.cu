@@ -86,7 +86,23 @@ __device__ __forceinline__ void zero_rows(uint8_t* block, int atoms, int atom_by
   fence_proxy_async();
 }
 
+// Items on their way to a CTA's warps: one warp finds them (a list's entry and a few divisions, 1 us)
+// while the others work on those before.
+constexpr int kItemWords = 16;
+constexpr int kTakers = 14;  // warps: 8 softmax, 4 results, copies, products
+struct Feed {
+  alignas(16) int item[2][kItemWords];
+  uint64_t full[2], empty[2];
+  __device__ __forceinline__ void init() {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], kTakers);
+    }
+  }
+};
+
 struct Bars {
+  Feed feed;
   uint64_t r_full, r_empty, full[8], empty[8], s_full[2], p_full[2], p_rest[2], pv[2], o_full[2],
       o_empty[2], l_full[2], drained;
   uint32_t tmem;
@@ -189,6 +205,39 @@ struct Turns {
   }
 };
 
+// The finder's side: every item there is, then one with n = -1.
+template <typename ITEM, typename W>
+__device__ __forceinline__ void feed_items(Feed& f, Turns turns, const SeqArgs& a, W wait) {
+  static_assert(sizeof(ITEM) <= sizeof(f.item[0]), "");
+  int turn = 0;
+  auto put = [&](const ITEM& x) {
+    const int s = turn & 1;
+    if (turn >= 2) wait(&f.empty[s], ((turn >> 1) - 1) & 1);
+    *reinterpret_cast<ITEM*>(f.item[s]) = x;
+    mbar_arrive(&f.full[s]);
+    ++turn;
+  };
+  ITEM x;
+  for (int idx; (idx = turns.next()) >= 0;)
+    if (x.find(a, idx)) put(x);
+  x.n = -1;
+  put(x);
+}
+// The others': the next item; false: there is none, or the CTA gave up.  By whole warps, or (ALONE) by
+// one lane.
+template <bool ALONE, typename ITEM, typename W>
+__device__ __forceinline__ bool take_item(Feed& f, int& turn, ITEM& x, W wait,
+                                          volatile int* gave_up) {
+  const int s = turn & 1;
+  wait(&f.full[s], (turn >> 1) & 1);
+  ++turn;
+  if (*gave_up) return false;
+  x = *reinterpret_cast<const ITEM*>(f.item[s]);
+  if (!ALONE) __syncwarp();
+  if (ALONE || (threadIdx.x & 31) == 0) mbar_arrive(&f.empty[s]);
+  return x.n >= 0;
+}
+
 // An item of k_flash: kTiles tiles of one sequence and head (or key head), the blocks that they
 // stream and those [lo, hi) that each tile takes.
 template <int D, bool FWD>
@@ -284,6 +333,7 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
       mbar_init(&bar.l_full[i], 4);
     }
     mbar_init(&bar.drained, 1);
+    bar.feed.init();
     bar.gave_up = 0;
     fence_barrier_init();
   }
@@ -300,14 +350,15 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
   if (FWD && blockIdx.x == 0 && tid == 0) check_single(a);
   Turns turns(FWD ? a.tq.most * (a.Hq / a.pack) * a.parts : a.tk.most * (a.tk.rows / TR) * a.Hk * a.splits);
   Item<D, FWD> x;
+  int taken = 0;
 
   if (group == 3) {
     fewer_registers<F::kIssueRegs>();
     if (warp == 12 && lane == 0) {
       // ---- copies
       int stage = 0, turn = 0, works = 0;
-      for (int idx; (idx = turns.next()) >= 0 && !bar.gave_up;) {
-        if (!x.find(a, idx) || x.n == 0) continue;
+      while (take_item<true>(bar.feed, taken, x, wait, &bar.gave_up)) {
+        if (x.n == 0) continue;
         const int rows = FWD ? TR / a.pack : TR;
         if (works > 0) wait(&bar.r_empty, (works - 1) & 1);
         ++works;
@@ -355,8 +406,7 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
       auto next = [&]() {
         if (++stage == ST) stage = 0, ++turn;
       };
-      for (int idx; (idx = turns.next()) >= 0;) {
-        if (!uniform(x.find(a, idx))) continue;
+      while (take_item<false>(bar.feed, taken, x, wait, &bar.gave_up)) {
         x.make_uniform();
         ++items;
         if (x.n == 0) continue;
@@ -475,6 +525,8 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
         commit_to(&bar.drained, issue);
         mbar_wait(&bar.drained, 0, nullptr, 0);
       }
+    } else if (warp == 14 && lane == 0) {
+      feed_items<Item<D, FWD>>(bar.feed, turns, a, wait);
     }
   } else if (group == 2) {
     // ---- results: a thread per row
@@ -482,8 +534,7 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
     const int r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     int items = 0, works[2] = {0, 0};
-    for (int idx; (idx = turns.next()) >= 0;) {
-      if (!x.find(a, idx)) continue;
+    while (take_item<false>(bar.feed, taken, x, wait, &bar.gave_up)) {
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         const int row = FWD ? x.t.at + (i * TR + r) / a.pack : x.t.at + i * TR + r;
@@ -533,8 +584,7 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     int items = 0, done = 0;  // done: blocks of the tile so far, of all items
     int placed = 0;           // blocks of the ring in front of this item
-    for (int idx; (idx = turns.next()) >= 0;) {
-      if (!x.find(a, idx)) continue;
+    while (take_item<false>(bar.feed, taken, x, wait, &bar.gave_up)) {
       const int rows = FWD ? TR / a.pack : TR, at = x.t.at + i * rows, off = x.t.nk - x.t.nq;
       const int w0 = (warp & 3) * 32;  // the warp's rows: tokens first .. last
       const int first = FWD ? at + w0 / a.pack : at + w0;
@@ -810,6 +860,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
     mbar_init(&bar.o_full[0], 1);
     mbar_init(&bar.o_empty[0], 4);
     mbar_init(&bar.drained, 1);
+    bar.feed.init();
     bar.gave_up = 0;
     fence_barrier_init();
   }
@@ -824,6 +875,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
   auto wait = [&](uint64_t* b, uint32_t parity) { wait_for(b, parity, a.status, &bar.gave_up); };
   Turns turns((DQ ? a.tq.most : a.tk.most) * (DQ ? a.Hq : a.Hk * a.splits));
   SlopeItem<DQ, BN, TR> x;
+  int taken = 0;
   // X1 0, X2 0, X1 1, X2 1, .. of all items follow each other in the ring
   auto place = [&](int p) { return Place{p % ST, (uint32_t)(p / ST) & 1}; };
 
@@ -833,8 +885,8 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
       // ---- copies
       int works = 0, c = 0;
       Place at{0, 0};
-      for (int idx; (idx = turns.next()) >= 0 && !bar.gave_up;) {
-        if (!x.find(a, idx) || x.n == 0) continue;
+      while (take_item<true>(bar.feed, taken, x, wait, &bar.gave_up)) {
+        if (x.n == 0) continue;
         const int row0 = (DQ ? x.t.q0 : x.t.k0) + x.t.at;
         if (works > 0) wait(&bar.r_empty, (works - 1) & 1);
         ++works;
@@ -871,8 +923,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
       constexpr uint32_t kOwn = kHead, kRing = kHead + 2 * F::kTile;
       int items = 0, works = 0, c = 0;
       Place p1{0, 0}, p2{1, 0};  // of X1 and X2 of iteration c
-      for (int idx; (idx = turns.next()) >= 0;) {
-        if (!uniform(x.find(a, idx))) continue;
+      while (take_item<false>(bar.feed, taken, x, wait, &bar.gave_up)) {
         x.make_uniform();
         ++items;
         if (x.n == 0) continue;
@@ -968,6 +1019,8 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
         commit_to(&bar.drained, issue);
         mbar_wait(&bar.drained, 0, nullptr, 0);
       }
+    } else if (warp == 14 && lane == 0) {
+      feed_items<SlopeItem<DQ, BN, TR>>(bar.feed, turns, a, wait);
     }
   } else if (group == 2) {
     // ---- results: a thread per row
@@ -975,8 +1028,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
     const int r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     int works = 0;
-    for (int idx; (idx = turns.next()) >= 0;) {
-      if (!x.find(a, idx)) continue;
+    while (take_item<false>(bar.feed, taken, x, wait, &bar.gave_up)) {
       const int row = x.t.at + r, side = DQ ? x.t.nq : x.t.nk;
       if (x.n > 0) {
         wait(&bar.o_full[0], works & 1);
@@ -1028,8 +1080,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
       if (lane == 0) mbar_arrive(b);
     };
     int c = 0;  // iterations of all items
-    for (int idx; (idx = turns.next()) >= 0;) {
-      if (!x.find(a, idx)) continue;
+    while (take_item<false>(bar.feed, taken, x, wait, &bar.gave_up)) {
       const int off = x.t.nk - x.t.nq, first_row = x.t.at + (warp & 3) * 32, row = x.t.at + r;
       const int xrows = DQ ? x.t.nk : x.t.nq;
       float lse2 = INFINITY, delta = 0.f, ahead = 0.f;
@@ -1148,6 +1199,7 @@ struct Pair {
   static constexpr int kBytes = kHead + 2 * kTile + 3 * kPart;
 };
 struct PairBars {
+  Feed feed;
   uint64_t r_full, r_empty, full[3], empty[3], s_full, dp_full, o_full;  // of this CTA
   uint64_t peer[4], s_read, ds_full, o_empty;  // of the first CTA: what the other's copies bring
                                                // (full[3], r_full), what both have read or written
@@ -1187,6 +1239,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
     mbar_init(&bar.s_read, 16);
     mbar_init(&bar.ds_full, 16);
     mbar_init(&bar.o_empty, 8);
+    bar.feed.init();
     bar.gave_up = 0;
     fence_barrier_init();
   }
@@ -1198,17 +1251,20 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
   pair_sync();
   tc_fence_after();
   const uint32_t tmem = uniform(bar.tmem), t_dp = tmem + BN, t_acc = tmem + 2 * BN;
-  auto wait = [&](uint64_t* b, uint32_t parity) { wait_for(b, parity, a.status, &bar.gave_up); };
+  auto wait = [&](uint64_t* b, uint32_t parity) {
+    wait_for<true>(b, parity, a.status, &bar.gave_up);
+  };
   Turns turns((DQ ? a.tq.most : a.tk.most) * (DQ ? a.Hq : a.Hk * a.splits), 2);
   SlopeItem<DQ, BN, 2 * TR> x;
+  int taken = 0;
 
   if (group == 3) {
     fewer_registers<64>();
     if (warp == 12 && lane == 0) {
       // ---- copies: parts 0 X1 by rows, 1 X2 by rows, 2 X1 by columns
       int works = 0, c = 0;
-      for (int idx; (idx = turns.next()) >= 0 && !bar.gave_up;) {
-        if (!x.find(a, idx) || x.n == 0) continue;
+      while (take_item<true>(bar.feed, taken, x, wait, &bar.gave_up)) {
+        if (x.n == 0) continue;
         const int row0 = (DQ ? x.t.q0 : x.t.k0) + x.t.at + rank * TR;
         if (works > 0) wait(&bar.r_empty, (works - 1) & 1);
         ++works;
@@ -1249,8 +1305,8 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
         wait(b, parity);
         if (lane == 0) arrive_first(&bar.peer[to]);
       };
-      for (int idx; (idx = turns.next()) >= 0 && !bar.gave_up;) {
-        if (!uniform(x.find(a, idx)) || uniform(x.n) == 0) continue;
+      while (take_item<false>(bar.feed, taken, x, wait, &bar.gave_up)) {
+        if (x.n == 0) continue;
         tell(&bar.r_full, works & 1, 3);
         ++works;
         const int n = uniform(x.n);
@@ -1269,8 +1325,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
       const Desc kmaj(sdesc(base, 16, 1024)), mnmaj(sdesc(base, 16384, 1024));
       constexpr uint32_t kOwn = kHead, kParts = kHead + 2 * F::kTile;
       int items = 0, works = 0, c = 0;
-      for (int idx; (idx = turns.next()) >= 0;) {
-        if (!uniform(x.find(a, idx))) continue;
+      while (take_item<false>(bar.feed, taken, x, wait, &bar.gave_up)) {
         x.make_uniform();
         ++items;
         if (x.n == 0) continue;
@@ -1334,6 +1389,8 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
         pair_commit(&bar.drained, issue);
         mbar_wait(&bar.drained, 0, nullptr, 0);
       }
+    } else if (warp == 14 && lane == 0) {
+      feed_items<SlopeItem<DQ, BN, 2 * TR>>(bar.feed, turns, a, wait);
     }
   } else if (group == 2) {
     // ---- results: a thread per row
@@ -1341,8 +1398,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
     const int r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     int works = 0;
-    for (int idx; (idx = turns.next()) >= 0;) {
-      if (!x.find(a, idx)) continue;
+    while (take_item<false>(bar.feed, taken, x, wait, &bar.gave_up)) {
       const int row = x.t.at + rank * TR + r, side = DQ ? x.t.nq : x.t.nk;
       if (x.n > 0) {
         wait(&bar.o_full, works & 1);
@@ -1378,8 +1434,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
     const int half = group, r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     int c = 0;  // iterations of all items
-    for (int idx; (idx = turns.next()) >= 0;) {
-      if (!x.find(a, idx)) continue;
+    while (take_item<false>(bar.feed, taken, x, wait, &bar.gave_up)) {
       const int off = x.t.nk - x.t.nq, at = x.t.at + rank * TR;
       const int first_row = at + (warp & 3) * 32, row = at + r;
       const int xrows = DQ ? x.t.nk : x.t.nq;

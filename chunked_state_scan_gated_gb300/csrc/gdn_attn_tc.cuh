@@ -119,14 +119,24 @@ __device__ __forceinline__ void bar_sync(int id, int threads) {
 
 // A wait of at most kWaitLimitNs; once one has run out (status, *gave_up), the others of the CTA
 // give up at once, so that it ends.
+// PAIR: what the other CTA of a pair did before it arrived is seen too.
+template <bool PAIR = false>
 __device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, int32_t* status,
                                          volatile int* gave_up) {
   const uint32_t addr = smem_u32(bar);
   uint64_t t0 = 0;
   for (uint32_t it = 0;; ++it) {
     uint32_t done;
-    asm volatile(
+    if constexpr (PAIR)
+      asm volatile(
         "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(addr), "r"(parity)
+        : "memory");
+    else
+      asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
         " selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(done)
         : "r"(addr), "r"(parity)
