@@ -46,6 +46,7 @@ struct SeqArgs {
   int splits;              // 1: none, dk and dv are written themselves
   float *part_o, *part_lse;  // [parts][Nq][Hq](D): o and log2-sum over a part of the keys
   int parts;               // 1: none, o and lse are written themselves
+  int late;                // 1: the kernel waits for the one before it at its end, not first
   int32_t* status;
 };
 

@@ -316,6 +316,11 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
   uint8_t *own = sm + kHead, *ring = own + NT * F::kTile;
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31, group = warp >> 2;
 
+  if (tid == 32) {
+    prefetch_map(&mr);
+    prefetch_map(&m1);
+    prefetch_map(&m2);
+  }
   if (tid == 0) {
     mbar_init(&bar.r_full, 1);
     mbar_init(&bar.r_empty, 1);
@@ -339,7 +344,7 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
   }
   if (warp == 0) tmem_alloc(&bar.tmem, 512);
   tc_fence_before();
-  after_previous();
+  if (!a.late) after_previous();
   before_next();
   __syncthreads();
   tc_fence_after();
@@ -767,6 +772,7 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == 0) tmem_dealloc(tmem, 512);
+  if (a.late) after_previous();
 }
 
 // ------------------------------------------------------------------------- dq, dk (and dv)
@@ -846,6 +852,12 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
   uint8_t *own = sm + kHead, *ring = own + 2 * F::kTile;
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31, group = warp >> 2;
 
+  if (tid == 32) {
+    prefetch_map(&mr1);
+    prefetch_map(&mr2);
+    prefetch_map(&m1);
+    prefetch_map(&m2);
+  }
   if (tid == 0) {
     mbar_init(&bar.r_full, 1);
     mbar_init(&bar.r_empty, 1);
@@ -866,7 +878,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
   }
   if (warp == 0) tmem_alloc(&bar.tmem, 512);
   tc_fence_before();
-  after_previous();
+  if (!a.late) after_previous();
   before_next();
   __syncthreads();
   tc_fence_after();
@@ -1181,6 +1193,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (warp == 0) tmem_dealloc(tmem, 512);
+  if (a.late) after_previous();
 }
 
 // ----------------------------------------------------------------- dq and dk, heads of 256
@@ -1227,6 +1240,13 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31, group = warp >> 2;
   const int rank = uniform(pair_rank());
 
+  if (tid == 32) {
+    prefetch_map(&mr1);
+    prefetch_map(&mr2);
+    prefetch_map(&m1);
+    prefetch_map(&m2);
+    prefetch_map(&m1c);
+  }
   if (tid == 0) {
     for (uint64_t* b : {&bar.r_full, &bar.r_empty, &bar.s_full, &bar.dp_full, &bar.o_full,
                         &bar.drained})
@@ -1245,7 +1265,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
   }
   if (warp == 0) pair_tmem_alloc(&bar.tmem);
   tc_fence_before();
-  after_previous();
+  if (!a.late) after_previous();
   before_next();
   __syncthreads();
   pair_sync();
@@ -1532,6 +1552,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
   __syncwarp();
   pair_sync();  // neither CTA's barriers or TMEM are used any more
   if (warp == 0) pair_tmem_dealloc(tmem);
+  if (a.late) after_previous();
 }
 
 // dk and dv from their parts, which are added in their order: a CTA takes SUM_ROWS rows of a key tile
@@ -1672,7 +1693,7 @@ cudaError_t fwd(const SeqArgs& a, cudaStream_t st) {
 }
 
 template <int D>
-cudaError_t bwd(const SeqArgs& a, cudaStream_t st) {
+cudaError_t bwd(SeqArgs a, cudaStream_t st) {
   const int64_t os = (int64_t)a.Hq * D;
   CUtensorMap q, d, k, v;  // boxes of 128 rows
   if (a.Nq > 0 && (!make(&q, a.q, a.Nq, a.qs, a.Hq, D, 128) ||
@@ -1683,6 +1704,9 @@ cudaError_t bwd(const SeqArgs& a, cudaStream_t st) {
     return cudaErrorInvalidValue;
   if (a.Nq == 0) q = d = k;
   if (a.Nk == 0) k = v = q;
+  // The first launch waits for what came before it; the others read nothing that it writes and begin
+  // as its CTAs end (late), and wait for it before they end themselves, so that the last one's end is
+  // the end of all.
   const int64_t key_items = (int64_t)a.tk.most * a.Hk * a.splits;
   const int64_t query_items = (int64_t)a.tq.most * a.Hq;
   cudaError_t e = cudaSuccess;
@@ -1700,6 +1724,7 @@ cudaError_t bwd(const SeqArgs& a, cudaStream_t st) {
       e = launch<k_slope_pair<kDk>>(pairs_of(key_items), Pair::kThreads, Pair::kBytes, st, k, v, qh,
                                     dh, q, a);
       if (e != cudaSuccess) return e;
+      a.late = 1;
       e = launch<k_flash<D, false>>(ctas_of(2 * key_items), Flash<D>::kThreads, Flash<D>::kBytes, st,
                                     k, q, d, a);
     }
@@ -1710,6 +1735,7 @@ cudaError_t bwd(const SeqArgs& a, cudaStream_t st) {
     if (a.Nk > 0)
       e = launch<k_slope<D, kDkv>>(ctas_of(key_items), Slope<D>::kThreads, Slope<D>::kBytes, st, k,
                                    v, q, d, a);
+    a.late = a.Nk > 0;
     if (e == cudaSuccess && a.Nq > 0)
       e = launch<k_slope<D, kDq>>(ctas_of(query_items), Slope<D>::kThreads, Slope<D>::kBytes, st,
                                   q, d, k, v, a);
