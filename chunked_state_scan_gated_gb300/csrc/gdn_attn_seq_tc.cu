@@ -182,6 +182,18 @@ __device__ __forceinline__ void fma2(float& x, float& y, float m, float c) {
       " mov.b64 d, {%3, %3};\n fma.rn.f32x2 a, a, b, d;\n mov.b64 {%0, %1}, a;\n}\n"
       : "+f"(x), "+f"(y) : "f"(m), "f"(c));
 }
+__device__ __forceinline__ void fma2(float& x, float& y, float m, float c, float d) {
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %2};\n"
+      " mov.b64 d, {%3, %4};\n fma.rn.f32x2 a, a, b, d;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "+f"(x), "+f"(y) : "f"(m), "f"(c), "f"(d));
+}
+// (x, y) = (x, y) (a + c, b + d)
+__device__ __forceinline__ void mul_sum2(float& x, float& y, float a, float b, float c, float d) {
+  asm("{\n .reg .b64 p, q, r;\n mov.b64 p, {%0, %1};\n mov.b64 q, {%2, %3};\n"
+      " mov.b64 r, {%4, %5};\n add.rn.f32x2 q, q, r;\n mul.rn.f32x2 p, p, q;\n"
+      " mov.b64 {%0, %1}, p;\n}\n"
+      : "+f"(x), "+f"(y) : "f"(a), "f"(b), "f"(c), "f"(d));
+}
 __device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
   asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n"
       " add.rn.f32x2 a, a, b;\n mov.b64 {%0, %1}, a;\n}\n"
@@ -310,7 +322,7 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
   static_assert(FWD || NT == 1, "row_values");
   extern __shared__ __align__(1024) uint8_t sm[];
   Bars& bar = *reinterpret_cast<Bars*>(sm);
-  float* row_values = reinterpret_cast<float*>(sm + 512);  // dv: [2][128] lse2
+  float* row_values = reinterpret_cast<float*>(sm + 512);  // dv: [2][128] -lse2
   float* row_tops = row_values;                            // forward, D = 256: [2][half][128]
   float* row_factors = reinterpret_cast<float*>(sm + (NT == 1 ? 2560 : 512));  // [tile][128] 1 / l
   uint8_t *own = sm + kHead, *ring = own + NT * F::kTile;
@@ -614,7 +626,7 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
         const uint32_t ts = tmem + lanes + buf * 128;
         float* lv = row_values + (done & 1) * 128;
         if (!FWD) {
-          if (half == 0) lv[r] = ahead;
+          if (half == 0) lv[r] = -ahead;
           bar_sync(1, 256);
           if (it + 1 < x.n) ahead = value(g, j);
         }
@@ -716,10 +728,8 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
               fma2(z[2], z[3], a.sl, -base);
             } else {
               const float4 v = *reinterpret_cast<const float4*>(lv + half * 64 + q * 32 + e);
-              z[0] = fmaf(z[0], a.sl, -v.x);
-              z[1] = fmaf(z[1], a.sl, -v.y);
-              z[2] = fmaf(z[2], a.sl, -v.z);
-              z[3] = fmaf(z[3], a.sl, -v.w);
+              fma2(z[0], z[1], a.sl, v.x, v.y);
+              fma2(z[2], z[3], a.sl, v.z, v.w);
             }
             z[0] = ex2(z[0]);
             z[1] = ex2(z[1]);
@@ -848,7 +858,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
   constexpr int BN = F::kBlock, ST = F::kStages, HN = BN / 2;
   extern __shared__ __align__(1024) uint8_t sm[];
   Bars& bar = *reinterpret_cast<Bars*>(sm);
-  float* row_values = reinterpret_cast<float*>(sm + 512);  // dk: [2][lse2, delta][BN]
+  float* row_values = reinterpret_cast<float*>(sm + 512);  // dk: [2][-lse2, -delta][BN]
   uint8_t *own = sm + kHead, *ring = own + 2 * F::kTile;
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31, group = warp >> 2;
 
@@ -1113,7 +1123,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
         if ((j = x.after(j)) == x.j0) ++g;
         float* lv = row_values + (c & 1) * 2 * BN;
         if (!DQ) {
-          lv[tid] = ahead;
+          lv[tid] = -ahead;
           bar_sync(1, 256);
           if (it + 1 < x.n) ahead = value(g, j);
         }
@@ -1155,10 +1165,8 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
             fma2(s[e + 2], s[e + 3], a.sl, -lse2);
           } else {
             const float4 v = *reinterpret_cast<const float4*>(lv + half * HN + e);
-            s[e] = fmaf(s[e], a.sl, -v.x);
-            s[e + 1] = fmaf(s[e + 1], a.sl, -v.y);
-            s[e + 2] = fmaf(s[e + 2], a.sl, -v.z);
-            s[e + 3] = fmaf(s[e + 3], a.sl, -v.w);
+            fma2(s[e], s[e + 1], a.sl, v.x, v.y);
+            fma2(s[e + 2], s[e + 3], a.sl, v.z, v.w);
           }
           s[e] = ex2(s[e]);
           s[e + 1] = ex2(s[e + 1]);
@@ -1176,12 +1184,10 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
         tmem_ld64(t_dp + lanes + half * HN, dp);
 #pragma unroll
         for (int e = 0; e < HN; e += 4) {
-          float4 v = make_float4(delta, delta, delta, delta);
+          float4 v = make_float4(-delta, -delta, -delta, -delta);
           if (!DQ) v = *reinterpret_cast<const float4*>(lv + BN + half * HN + e);
-          s[e] *= dp[e] - v.x;
-          s[e + 1] *= dp[e + 1] - v.y;
-          s[e + 2] *= dp[e + 2] - v.z;
-          s[e + 3] *= dp[e + 3] - v.w;
+          mul_sum2(s[e], s[e + 1], dp[e], dp[e + 1], v.x, v.y);
+          mul_sum2(s[e + 2], s[e + 3], dp[e + 2], dp[e + 3], v.z, v.w);
         }
         mask(s);
         put(DQ ? ts : t_dp, s);
@@ -1235,7 +1241,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
   constexpr int D = F::D, BN = F::kBlock, HN = 64;
   extern __shared__ __align__(1024) uint8_t sm[];
   PairBars& bar = *reinterpret_cast<PairBars*>(sm);
-  float* row_values = reinterpret_cast<float*>(sm + 512);  // dk: [2][lse2, delta][BN]
+  float* row_values = reinterpret_cast<float*>(sm + 512);  // dk: [2][-lse2, -delta][BN]
   uint8_t *own = sm + kHead, *parts = own + 2 * F::kTile;
   const int tid = threadIdx.x, warp = uniform(tid >> 5), lane = tid & 31, group = warp >> 2;
   const int rank = uniform(pair_rank());
@@ -1476,7 +1482,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
         if ((j = x.after(j)) == x.j0) ++g;
         float* lv = row_values + (c & 1) * 2 * BN;
         if (!DQ) {
-          lv[tid] = ahead;
+          lv[tid] = -ahead;
           bar_sync(1, 256);
           if (it + 1 < x.n) ahead = value(g, j);
         }
@@ -1504,10 +1510,8 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
             fma2(s[e + 2], s[e + 3], a.sl, -lse2);
           } else {
             const float4 v = *reinterpret_cast<const float4*>(lv + half * HN + e);
-            s[e] = fmaf(s[e], a.sl, -v.x);
-            s[e + 1] = fmaf(s[e + 1], a.sl, -v.y);
-            s[e + 2] = fmaf(s[e + 2], a.sl, -v.z);
-            s[e + 3] = fmaf(s[e + 3], a.sl, -v.w);
+            fma2(s[e], s[e + 1], a.sl, v.x, v.y);
+            fma2(s[e + 2], s[e + 3], a.sl, v.z, v.w);
           }
           s[e] = ex2(s[e]);
           s[e + 1] = ex2(s[e + 1]);
@@ -1519,12 +1523,10 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
         tmem_ld64(t_dp + lanes + half * HN, dp);
 #pragma unroll
         for (int e = 0; e < HN; e += 4) {
-          float4 v = make_float4(delta, delta, delta, delta);
+          float4 v = make_float4(-delta, -delta, -delta, -delta);
           if (!DQ) v = *reinterpret_cast<const float4*>(lv + BN + half * HN + e);
-          s[e] *= dp[e] - v.x;
-          s[e + 1] *= dp[e + 1] - v.y;
-          s[e + 2] *= dp[e + 2] - v.z;
-          s[e + 3] *= dp[e + 3] - v.w;
+          mul_sum2(s[e], s[e + 1], dp[e], dp[e + 1], v.x, v.y);
+          mul_sum2(s[e + 2], s[e + 3], dp[e + 2], dp[e + 3], v.z, v.w);
         }
         if (!whole) {
 #pragma unroll
