@@ -56,6 +56,20 @@ __device__ __forceinline__ int clamp_row(int64_t x, int64_t n) {
   return (int)(x < 0 ? 0 : x > n ? n : x);
 }
 
+// The tiles that there are, at most `most`.
+template <bool KEYS>
+__device__ __forceinline__ int tiles_there(const SeqArgs& a) {
+  const Tiles& ts = KEYS ? a.tk : a.tq;
+  if (ts.list) return *ts.count;
+  int rows = (int)((KEYS ? a.Nk : a.Nq) / a.n_seqs);
+  if (a.cuq) {
+    const int32_t* cu = KEYS && a.cuk ? a.cuk : a.cuq;
+    const int64_t n = KEYS ? a.Nk : a.Nq;
+    rows = max(0, clamp_row(cu[1], n) - clamp_row(cu[0], n));
+  }
+  return (rows + ts.rows - 1) / ts.rows * a.n_seqs;
+}
+
 // The idx-th tile; false: there is none.  KEYS: tiles of the key side.
 template <bool KEYS>
 __device__ __forceinline__ bool tile_of(const SeqArgs& a, int idx, Tile* t) {

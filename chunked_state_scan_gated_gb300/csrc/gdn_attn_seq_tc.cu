@@ -365,7 +365,8 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
   auto acc_of = [&](int t) { return tmem + 256 + t * D; };
   auto wait = [&](uint64_t* b, uint32_t parity) { wait_for(b, parity, a.status, &bar.gave_up); };
   if (FWD && blockIdx.x == 0 && tid == 0) check_single(a);
-  Turns turns(FWD ? a.tq.most * (a.Hq / a.pack) * a.parts : a.tk.most * (a.tk.rows / TR) * a.Hk * a.splits);
+  const int per_tile =
+      FWD ? a.Hq / a.pack * a.parts : a.tk.rows / TR * a.Hk * a.splits;  // items
   Item<D, FWD> x;
   int taken = 0;
 
@@ -543,7 +544,7 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
         mbar_wait(&bar.drained, 0, nullptr, 0);
       }
     } else if (warp == 14 && lane == 0) {
-      feed_items<Item<D, FWD>>(bar.feed, turns, a, wait);
+      feed_items<Item<D, FWD>>(bar.feed, Turns(tiles_there<!FWD>(a) * per_tile), a, wait);
     }
   } else if (group == 2) {
     // ---- results: a thread per row
@@ -895,7 +896,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
   // columns: S (two buffers, or one), dP, the accumulators
   const uint32_t tmem = uniform(bar.tmem), t_dp = tmem + (DQ ? 2 : 1) * BN, t_acc = t_dp + BN;
   auto wait = [&](uint64_t* b, uint32_t parity) { wait_for(b, parity, a.status, &bar.gave_up); };
-  Turns turns((DQ ? a.tq.most : a.tk.most) * (DQ ? a.Hq : a.Hk * a.splits));
+  const int per_tile = DQ ? a.Hq : a.Hk * a.splits;  // items
   SlopeItem<DQ, BN, TR> x;
   int taken = 0;
   // X1 0, X2 0, X1 1, X2 1, .. of all items follow each other in the ring
@@ -1042,7 +1043,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
         mbar_wait(&bar.drained, 0, nullptr, 0);
       }
     } else if (warp == 14 && lane == 0) {
-      feed_items<SlopeItem<DQ, BN, TR>>(bar.feed, turns, a, wait);
+      feed_items<SlopeItem<DQ, BN, TR>>(bar.feed, Turns(tiles_there<!DQ>(a) * per_tile), a, wait);
     }
   } else if (group == 2) {
     // ---- results: a thread per row
@@ -1280,7 +1281,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
   auto wait = [&](uint64_t* b, uint32_t parity) {
     wait_for<true>(b, parity, a.status, &bar.gave_up);
   };
-  Turns turns((DQ ? a.tq.most : a.tk.most) * (DQ ? a.Hq : a.Hk * a.splits), 2);
+  const int per_tile = DQ ? a.Hq : a.Hk * a.splits;  // items
   SlopeItem<DQ, BN, 2 * TR> x;
   int taken = 0;
 
@@ -1416,7 +1417,8 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
         mbar_wait(&bar.drained, 0, nullptr, 0);
       }
     } else if (warp == 14 && lane == 0) {
-      feed_items<SlopeItem<DQ, BN, 2 * TR>>(bar.feed, turns, a, wait);
+      feed_items<SlopeItem<DQ, BN, 2 * TR>>(bar.feed, Turns(tiles_there<!DQ>(a) * per_tile, 2), a,
+                                            wait);
     }
   } else if (group == 2) {
     // ---- results: a thread per row

@@ -229,6 +229,73 @@ def test_attention_rows_of_one_length_need_no_offsets(dt):
     assert gdn.gdn_attn_fwd(q, k, v, want_lse=False)[1] is None
 
 
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_of_a_sequence_beside_one_of_nan(D, dt):
+    """A packed sequence whose every number is NaN leaves its neighbours as they are without it."""
+    lens = [40, 133, 55, 250, 7]
+    q, k, v, cu, ck = seq_inputs(lens, [50, 133, 70, 300, 19], 4, 2, D, dt, seed=20)
+    gen = torch.Generator().manual_seed(21)
+    dO = rand(gen, q.shape, dt)
+    cuq, cuk = i32(cu), i32(ck)
+    want = gdn.gdn_attn_fwd(q, k, v, cuq, cuk)
+    grads = gdn.gdn_attn_bwd(q, k, v, *want, dO, cuq, cuk)
+    for b in (1, 3):
+        for x, c in ((q, cu), (dO, cu), (k, ck), (v, ck)):
+            x[c[b]:c[b + 1]] = float("nan")
+    o, lse = gdn.gdn_attn_fwd(q, k, v, cuq, cuk)
+    got = gdn.gdn_attn_bwd(q, k, v, o, lse, dO, cuq, cuk)
+    for b in (0, 2, 4):
+        rows, keys = slice(cu[b], cu[b + 1]), slice(ck[b], ck[b + 1])
+        assert torch.equal(o[rows], want[0][rows]) and torch.equal(lse[rows], want[1][rows])
+        for x, y, r in zip(got, grads, (rows, keys, keys)):
+            assert torch.isfinite(y[r]).all() and torch.equal(x[r], y[r])
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("D", [64, 256])
+def test_attention_without_keys_or_without_queries(D, dt):
+    q = torch.randn(70, 4, D, device="cuda").to(dt)
+    none = q[:0, :2]
+    cu, zero = i32([0, 30, 70]), i32([0, 0, 0])
+    o, lse = gdn.gdn_attn_fwd(q, none, none, cu, zero)
+    assert not o.any() and torch.isneginf(lse).all()
+    dq, dk, dv = gdn.gdn_attn_bwd(q, none, none, o, lse, q, cu, zero)
+    assert not dq.any() and dk.shape == dv.shape == none.shape
+    k = q[:, :2].contiguous()
+    o, lse = gdn.gdn_attn_fwd(q[:0], k, k, zero, cu)
+    dq, dk, dv = gdn.gdn_attn_bwd(q[:0], k, k, o, lse, o, zero, cu)
+    assert dq.numel() == 0 and not dk.any() and not dv.any()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_few_new_tokens_behind_a_long_context(D):
+    """The keys of every tile divided over several CTAs, and their parts joined."""
+    check_seq([40, 3, 90], [3000, 9000, 90], 8, 2, D, BF, True, seed=22)
+    check_seq([5], [5000], 4, 4, D, BF, False, seed=23)
+
+
+@pytest.mark.parametrize("dt,D", [(BF, 128), (BF, 256), (F32, 64)])
+def test_attention_rows_far_apart(dt, D):
+    """Tokens 2^25 bytes apart: offsets past 2^32."""
+    N, step = 150, 2 ** 25 // (2 if dt == BF else 4)
+    big = torch.empty((N, step), dtype=dt, device="cuda")
+    gen = torch.Generator().manual_seed(24)
+    parts = [rand(gen, (N, h, D), dt) for h in (4, 2, 2)]
+    views, at = [], 0
+    for x in parts:
+        y = big[:, at:at + x[0].numel()].view(x.shape)
+        y.copy_(x)
+        views.append(y)
+        at += x[0].numel()
+    cu, dO = i32([0, 60, 150]), rand(gen, parts[0].shape, dt)
+    want = gdn.gdn_attn_fwd(*parts, cu)
+    got = gdn.gdn_attn_fwd(*views, cu)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for x, y in zip(gdn.gdn_attn_bwd(*views, *got, dO, cu), gdn.gdn_attn_bwd(*parts, *want, dO, cu)):
+        assert torch.equal(x, y)
+
+
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("n_seqs", [1, 3])
 def test_attention_offsets_out_of_order_are_cut(dt, n_seqs):
@@ -482,6 +549,31 @@ def test_cache_offsets_that_are_not_ordered_write_nothing_outside(cu):
     gdn.gdn_cache_read8(kc, vc, ks, vs, i32(table), i32(cu), k=out, v=out.clone(), status=word)
     if fine:
         assert (out == 7).all() and (u8(kc) == before).all()
+
+
+def test_cache_past_2_32_bytes():
+    """The last pages of a cache of 4.5 GB: written, read back and attended to."""
+    P, Hk, D, pages = 128, 8, 256, 18000
+    gen = torch.Generator().manual_seed(25)
+    kc, vc = (torch.empty((pages, P, Hk, D), dtype=F8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros((pages, P // 16, Hk), device="cuda") for _ in range(2))
+    table, ctx, cu = np.array([[pages - 1, 3], [pages - 2, pages - 5]]), [0, 0], [0, 150, 350]
+    k, v = rand(gen, (350, Hk, D), BF), rand(gen, (350, Hk, D), BF)
+    gdn.gdn_cache_write8(k, v, kc, vc, ks, vs, i32(table), i32(ctx), i32(cu))
+    back = gdn.gdn_cache_read8(kc, vc, ks, vs, i32(table), i32(cu), n_tokens=350)
+    small = np.array([[0, 1], [2, 3]])
+    args = []
+    for x in (k, v):
+        zero = np.zeros((4, P, Hk, D), np.uint8), np.zeros((4, P // 16, Hk))
+        args.append(attention.cache_write8(n64(x), *zero, small, ctx, cu))
+    for x, c in zip(back, args):
+        np.testing.assert_array_equal(n64(x), attention.cache_read8(*c, small, cu, 350))
+    q = rand(gen, (2, 16, D), BF)
+    o, lse = gdn.gdn_attn_decode8(q, kc, vc, ks, vs, i32(table), i32([150, 200]))
+    near = [torch.from_numpy(c[0]).cuda().view(F8) for c in args]
+    sc = [torch.from_numpy(c[1]).float().cuda() for c in args]
+    want = gdn.gdn_attn_decode8(q, *near, *sc, i32(small), i32([150, 200]))
+    assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
 
 
 # ------------------------------------------------------------------ decode over the 8-bit cache
