@@ -104,7 +104,7 @@ struct Feed {
 struct Bars {
   Feed feed;
   uint64_t r_full, r_empty, full[8], empty[8], s_full[2], p_full[2], p_rest[2], pv[2], o_full[2],
-      o_empty[2], l_full[2], drained;
+      o_empty[2], l_full[2], l_empty[2], drained;
   uint32_t tmem;
   int gave_up;
 };
@@ -348,6 +348,7 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
       mbar_init(&bar.o_full[i], 1);
       mbar_init(&bar.o_empty[i], 4);
       mbar_init(&bar.l_full[i], 4);
+      mbar_init(&bar.l_empty[i], 4);
     }
     mbar_init(&bar.drained, 1);
     bar.feed.init();
@@ -419,14 +420,19 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
       const uint32_t base = smem_u32(sm);
       const Desc kmaj(sdesc(base, 16, 1024)), mnmaj(sdesc(base, 16384, 1024));
       constexpr uint32_t kOwn = kHead, kRing = kHead + NT * F::kTile;
-      int stage = 0, turn = 0, items = 0, works = 0;
+      int stage = 0, turn = 0, works = 0;  // works: items that have blocks
+      int filled[2] = {0, 0};              // items of which a tile has some
+      // tile i's accumulator has been read, if it held something
+      auto vacant = [&](int i) {
+        if (filled[i] > 0) wait(&bar.o_empty[i], (filled[i] - 1) & 1);
+        ++filled[i];
+      };
       int weights[2] = {0, 0}, scored = 0;  // parities of a tile's weights; blocks (NT = 1)
       auto next = [&]() {
         if (++stage == ST) stage = 0, ++turn;
       };
       while (take_item<false>(bar.feed, taken, x, wait, &bar.gave_up)) {
         x.make_uniform();
-        ++items;
         if (x.n == 0) continue;
         const int xrows = FWD ? x.t.nk : x.t.nq;
         wait(&bar.r_full, works & 1);
@@ -462,10 +468,8 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
           commit_to(&bar.empty[stage], issue);
           if (x.n == 1) commit_to(&bar.r_empty, issue);
           next();
-          if (items > 1) {  // the accumulators of the item before have been read
-            wait(&bar.o_empty[0], items & 1);
-            wait(&bar.o_empty[1], items & 1);
-          }
+          if (last[0] > 0) vacant(0);
+          if (last[1] > 0) vacant(1);
           for (int it = 0; it < x.n; ++it) {
             const int sv = stage, ks = steps(x.j0 + it);
             wait(&bar.full[sv], turn & 1);
@@ -517,7 +521,7 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
           };
           score(0);
           if (x.n > 1) score(1);
-          if (items > 1) wait(&bar.o_empty[0], items & 1);  // the item before has been read
+          vacant(0);
           for (int it = 0; it < x.n; ++it) {
             const int w = scored + it, buf = w & 1, ks = steps(j);
             wait(&bar.p_full[buf], (w >> 1) & 1);
@@ -563,6 +567,8 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
         if (FWD) {
           wait(&bar.l_full[i], items & 1);
           f = row_factors[i * 128 + r];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar.l_empty[i]);
         }
         const bool work = x.works(i);
         if (work) {
@@ -579,7 +585,7 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; ++e) y[e] = 0.f;
           }
-          if (c == D - 32) {  // read: the next item may accumulate
+          if (c == D - 32 && work) {  // read: the next item may accumulate
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar.o_empty[i]);
@@ -709,6 +715,10 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
         }
         if (kb + 128 > xrows && (xrows & 15)) {  // rows behind the sequence in its last 16
           const int from = xrows - kb, to = (from + 15) & ~15;
+          // D = 256: a stage's wait below is for one turn of the ring, so the turn before has to be
+          // over, which it is once the block before has been accumulated (with two tiles that came
+          // before this block's scores)
+          if (NT == 1 && done > 0) wait(&bar.pv[(done - 1) & 1], ((done - 1) >> 1) & 1);
           const int place = placed + (NT == 2 || it == x.n - 1 ? 2 * it + 1 : 2 * it + 2);
           for (int c = 0; c < NC; ++c) {
             const int y = place * NC + c;
@@ -765,7 +775,7 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
           bar_sync(1 + (warp & 3), 64);
         }
         if (half == 0) {
-          if (items > 0) wait(&bar.o_empty[i], (items - 1) & 1);  // the last one's were read
+          if (items > 0) wait(&bar.l_empty[i], (items - 1) & 1);  // the last one's was read
           row_factors[i * 128 + r] = l != 0.f ? 1.f / l : 0.f;
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.l_full[i]);
@@ -944,11 +954,10 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
       const uint32_t base = smem_u32(sm);
       const Desc kmaj(sdesc(base, 16, 1024)), mnmaj(sdesc(base, F::kAtom, 1024));
       constexpr uint32_t kOwn = kHead, kRing = kHead + 2 * F::kTile;
-      int items = 0, works = 0, c = 0;
+      int works = 0, c = 0;
       Place p1{0, 0}, p2{1, 0};  // of X1 and X2 of iteration c
       while (take_item<false>(bar.feed, taken, x, wait, &bar.gave_up)) {
         x.make_uniform();
-        ++items;
         if (x.n == 0) continue;
         const int xrows = DQ ? x.t.nk : x.t.nq;
         wait(&bar.r_full, works & 1);
@@ -968,9 +977,9 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
           commit_to(&bar.empty[at.stage], issue);
         };
         auto next = [&](const Place& p) { return p.template on<ST>(2); };
-        // the accumulators of the item before have been read
+        // before an item's first accumulation: that of the one before has been read
         auto vacant = [&](int it) {
-          if (it == 0 && items > 1) wait(&bar.o_empty[0], items & 1);
+          if (it == 0 && works > 1) wait(&bar.o_empty[0], works & 1);
         };
         int j = x.j0;
         if constexpr (!DQ) {
@@ -1068,7 +1077,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) y[e] = 0.f;
         }
-        if (c == kAll - 32) {  // read: the next item may accumulate
+        if (c == kAll - 32 && x.n > 0) {  // read: the next item may accumulate
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar.o_empty[0]);
@@ -1351,10 +1360,9 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
       const uint32_t base = smem_u32(sm);
       const Desc kmaj(sdesc(base, 16, 1024)), mnmaj(sdesc(base, 16384, 1024));
       constexpr uint32_t kOwn = kHead, kParts = kHead + 2 * F::kTile;
-      int items = 0, works = 0, c = 0;
+      int works = 0, c = 0;
       while (take_item<false>(bar.feed, taken, x, wait, &bar.gave_up)) {
         x.make_uniform();
-        ++items;
         if (x.n == 0) continue;
         const int xrows = DQ ? x.t.nk : x.t.nq;
         wait(&bar.r_full, works & 1);
@@ -1385,7 +1393,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
           } else {
             wait(&bar.s_read, c & 1);
           }
-          if (it == 0 && items > 1) wait(&bar.o_empty, items & 1);  // the item before was read
+          if (it == 0 && works > 1) wait(&bar.o_empty, works & 1);  // the item before was read
           wait(&bar.full[2], c & 1);
           wait(&bar.peer[2], c & 1);
           wait(&bar.ds_full, c & 1);
@@ -1442,7 +1450,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) y[e] = 0.f;
         }
-        if (c == D - 32) {  // read: the next item may accumulate
+        if (c == D - 32 && x.n > 0) {  // read: the next item may accumulate
           tc_fence_before();
           __syncwarp();
           if (lane == 0) arrive_first(&bar.o_empty);

@@ -275,6 +275,17 @@ def test_attention_few_new_tokens_behind_a_long_context(D):
     check_seq([5], [5000], 4, 4, D, BF, False, seed=23)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_sequences_without_work_among_others(D):
+    """Beside one long context, sequences of a few keys and of none: they share a class of work, so
+    that a CTA meets tiles without keys between others."""
+    klens = [8000] + [(0, 5, 0, 16, 3, 0, 0)[i % 7] for i in range(450)]
+    for seed in range(3):
+        check_seq([1] * 451, klens, 4, 2, D, BF, True, seed=seed)
+    check_seq([700] + [1 - i % 2 for i in range(450)], [700] + [(9, 4, 0, 16)[i % 4] for i in range(450)],
+              4, 2, D, BF, True, seed=3)
+
+
 @pytest.mark.parametrize("dt,D", [(BF, 128), (BF, 256), (F32, 64)])
 def test_attention_rows_far_apart(dt, D):
     """Tokens 2^25 bytes apart: offsets past 2^32."""
