@@ -142,8 +142,8 @@ __global__ void __launch_bounds__(PL_NT) k_attn_plan(SeqArgs a, PlanSide s0, Pla
 
 // ------------------------------------------------------------------- backward: row values
 
-// lse2 = lse log2(e), +inf for a row that sees no key (its p is 0), and delta = dO.o, by rows of
-// heads: what the other kernels read along the tokens.  Bound by HBM.
+// lse2 = lse log2(e) (fp32: lse), +inf for a row that sees no key (its p is 0), and delta = dO.o, by
+// rows of heads: what the other kernels read along the tokens.  Bound by HBM.
 template <int D, typename T>
 __global__ void __launch_bounds__(256) k_attn_rows(SeqArgs a) {
   constexpr int EL = 16 / (int)sizeof(T), CH = D / EL, LR = CH < 32 ? CH : 32, CPL = CH / LR;
@@ -177,172 +177,226 @@ __global__ void __launch_bounds__(256) k_attn_rows(SeqArgs a) {
   if (r < rows && sub == 0) {
     const int64_t n = r / a.Hq, h = r % a.Hq;
     const float l = a.lse[r];
-    a.lse2[h * a.Nq + n] = l == -INFINITY ? INFINITY : l * kLog2e;
+    a.lse2[h * a.Nq + n] = l == -INFINITY ? INFINITY : sizeof(T) == 2 ? l * kLog2e : l;
     a.delta[h * a.Nq + n] = s;
   }
 }
 
 // ----------------------------------------------------------------------- fp32, CUDA cores
 
-constexpr int ST = 64;   // rows and columns of a tile
-constexpr int LT = 68;   // a transposed operand's row in shared memory: 16-byte aligned
-constexpr int F_HALF = 128, F_NT = 2 * F_HALF, F_DC = 32, F_KC = 16;
+// The other side's operands come as chunks of 8 to 10 KB through a ring in shared memory (cp.async, a
+// chunk is about 1000 clocks of products), in two shapes: columns of 64 rows for the products over
+// D, whole rows for those over tokens.  A product over D keeps two sums, of the even and of the odd
+// columns, one over tokens two rows: either way two numbers to an instruction.
+constexpr int ST = 64;  // rows and columns of a tile
+constexpr int LT = 68;  // floats between the columns of the weights: 16-byte aligned
 
-template <typename T>
-__device__ __forceinline__ float4 ld4(const T* p) {
-  if constexpr (sizeof(T) == 4) {
-    return *reinterpret_cast<const float4*>(p);
-  } else {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
-                       __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
-  }
+typedef unsigned long long f32x2;
+
+__device__ __forceinline__ void fma2(f32x2& c, f32x2 x, f32x2 y) {
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(x), "l"(y));
 }
-template <typename T>
-__device__ __forceinline__ void st4(T* p, float x, float y, float z, float w) {
-  if constexpr (sizeof(T) == 4) {
-    *reinterpret_cast<float4*>(p) = make_float4(x, y, z, w);
-  } else {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(x, y), b = __floats2bfloat162_rn(z, w);
-    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
-                                              *reinterpret_cast<const uint32_t*>(&b));
+__device__ __forceinline__ f32x2 pair(float x, float y) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 parts_of(f32x2 x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ float sum_of(f32x2 x) {
+  const float2 r = parts_of(x);
+  return r.x + r.y;
+}
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src), "r"(in ? 16 : 0)
+               : "memory");  // zeros where it is not in
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {  // for all groups but the last N
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// By NT threads: R rows of C floats of src, zeros from row n on.
+template <int R, int C, int PITCH, int NT>
+__device__ __forceinline__ void copy_rows(float* dst, const float* src, int64_t stride, int n) {
+#pragma unroll
+  for (int z = 0; z < R * (C / 4) / NT; ++z) {
+    const int i = threadIdx.x % NT + z * NT, r = i / (C / 4), c = i % (C / 4) * 4;
+    const bool in = r < n;
+    copy16(dst + r * PITCH + c, src + (in ? r * stride + c : 0), in);
   }
 }
 
-// By NT threads: dst[c][row] = columns [c0, c0 + C) of rows [0, 64) of src (zeros from row n on).
-template <int C, int NT, typename T>
-__device__ __forceinline__ void load_t(float* dst, const T* src, int64_t stride, int n, int c0) {
-  for (int i = threadIdx.x % NT; i < ST * (C / 4); i += NT) {
-    const int r = i % ST, c = i / ST * 4;  // a warp's stores fall on different banks
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < n) x = ld4(src + (int64_t)r * stride + c0 + c);
-    dst[c * LT + r] = x.x;
-    dst[(c + 1) * LT + r] = x.y;
-    dst[(c + 2) * LT + r] = x.z;
-    dst[(c + 3) * LT + r] = x.w;
-  }
-}
-// dst[row][D] = rows [r0, r0 + R) of src (zeros from row n on).
-template <int D, int R, int NT, typename T>
-__device__ __forceinline__ void load_r(float* dst, const T* src, int64_t stride, int r0, int n) {
-  for (int i = threadIdx.x % NT; i < R * (D / 4); i += NT) {
-    const int r = i / (D / 4), c = i % (D / 4) * 4;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r0 + r < n) x = ld4(src + (int64_t)(r0 + r) * stride + c);
-    *reinterpret_cast<float4*>(dst + r * D + c) = x;
-  }
-}
+constexpr int F_HALF = 128, F_NT = 2 * F_HALF, F_STAGES = 3;
+constexpr int F_KC = 32, F_KP = F_KC + 4;  // columns of a chunk of K, floats between its rows
+constexpr int F_SLOT = ST * F_KP;
 
 template <int D>
-constexpr int fwd_half() {  // floats of a half's buffers: K's chunk, P, V's chunk
-  return F_DC * LT + ST * LT + F_KC * D;
+constexpr int fwd_half() {  // floats of a half's buffers: the ring, P
+  return F_STAGES * F_SLOT + ST * LT;
 }
 template <int D>
 constexpr size_t fwd_smem() {
-  return (size_t)(D * LT + 2 * fwd_half<D>() + 2 * ST) * 4;
+  return (size_t)(ST * (D + 4) + 2 * fwd_half<D>() + 2 * ST) * 4;
 }
 
 // 64 queries of one head.  Two halves of the CTA take the blocks of 64 keys in turn, each with a
 // softmax of its own, and are joined at the end: a prompt's last tile, which takes the longest, is
-// done in half the time (9 prompts up to 700 tokens, 12 heads of 64: 121 us with one half).  A thread
-// has 8 rows x 4 keys of the scores, 8 rows x D/16 columns of o.
-template <int D, typename T>
+// done in half the time.  A thread has 8 rows (ty, ty + 8, ..) x 4 keys (tx, tx + 16, ..) of the
+// scores, 8 rows x D/16 columns of o.
+template <int D>
 __global__ void __launch_bounds__(F_NT) k_attn_fwd_simt(SeqArgs a) {
   extern __shared__ __align__(16) float sm[];
-  constexpr int NV = D / 64;
+  constexpr int NV = D / 64, QP = D + 4, NK = D / F_KC, VR = 2048 / D;
   const int half = threadIdx.x / F_HALF, tid = threadIdx.x % F_HALF;
-  float *Qt = sm, *Kt = Qt + D * LT + half * fwd_half<D>(), *Pt = Kt + F_DC * LT;
-  float *Vc = Pt + ST * LT, *ml = sm + D * LT + 2 * fwd_half<D>();
-  auto sync = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + half), "n"(F_HALF) : "memory"); };
+  float *Q = sm, *ring = Q + ST * QP + half * fwd_half<D>(), *Pt = ring + F_STAGES * F_SLOT;
+  float* ml = sm + ST * QP + 2 * fwd_half<D>();
   after_previous();
   before_next();
   if (blockIdx.x == 0 && threadIdx.x == 0) check_single(a);
-  const int h = blockIdx.x % a.Hq, hk = h / a.G;
+  const int part = blockIdx.x % a.parts, item = blockIdx.x / a.parts;
+  const int h = item % a.Hq, hk = h / a.G;
   Tile t;
-  if (!tile_of<false>(a, blockIdx.x / a.Hq, &t)) return;
+  if (!tile_of<false>(a, item / a.Hq, &t)) return;
   const int ty = tid / 16, tx = tid % 16;
-  const int rows = min(ST, t.nq - t.at), end = keys_seen(a, t, ST), off = t.nk - t.nq;
-  const T* q = (const T*)a.q + (int64_t)(t.q0 + t.at) * a.qs + (int64_t)h * D;
-  const T* k = (const T*)a.k + (int64_t)t.k0 * a.ks + (int64_t)hk * D;
-  const T* v = (const T*)a.v + (int64_t)t.k0 * a.vs + (int64_t)hk * D;
-  load_t<D, F_NT>(Qt, q, a.qs, rows, 0);
-  float o[8][NV][4], m[8], l[8];
+  const int rows = min(ST, t.nq - t.at), off = t.nk - t.nq, seen = keys_seen(a, t, ST);
+  // this part's share of the blocks, and this half's of those
+  const int64_t blocks = (seen + ST - 1) / ST;
+  const int from = (int)(blocks * part / a.parts), to = (int)(blocks * (part + 1) / a.parts);
+  const int end = min(seen, to * ST), mine = max(0, (to - from - half + 1) / 2);
+  const float* q = (const float*)a.q + (t.q0 + t.at) * a.qs + (int64_t)h * D;
+  const float* k = (const float*)a.k + t.k0 * a.ks + (int64_t)hk * D;
+  const float* v = (const float*)a.v + t.k0 * a.vs + (int64_t)hk * D;
+  auto first_of = [&](int b) { return (from + half + 2 * b) * ST; };
+  auto v_chunks = [&](int b) { return (min(ST, end - first_of(b)) + VR - 1) / VR; };
+  int fb = 0, fc = 0, fs = 0;  // the next chunk to be fetched, its place in the ring
+  auto fetch = [&]() {
+    if (fb < mine) {
+      const int kb = first_of(fb);
+      float* to_ = ring + fs * F_SLOT;
+      if (fc < NK) {
+        copy_rows<ST, F_KC, F_KP, F_HALF>(to_, k + kb * a.ks + fc * F_KC, a.ks, end - kb);
+      } else {
+        const int at = kb + (fc - NK) * VR;
+        copy_rows<VR, D, D, F_HALF>(to_, v + at * a.vs, a.vs, end - at);
+      }
+      fs = fs + 1 == F_STAGES ? 0 : fs + 1;
+      if (++fc == NK + v_chunks(fb)) {
+        fc = 0;
+        ++fb;
+      }
+    }
+    copies_end();  // a group without copies past the last one
+  };
+  int slot = 0;
+  auto next = [&]() {  // the next chunk is there; the one before it is no longer read
+    copies_wait<F_STAGES - 2>();
+    asm volatile("bar.sync %0, %1;" ::"r"(1 + half), "n"(F_HALF) : "memory");
+    fetch();
+    const float* x = ring + slot * F_SLOT;
+    slot = slot + 1 == F_STAGES ? 0 : slot + 1;
+    return x;
+  };
+  copy_rows<ST, D, QP, F_NT>(Q, q, a.qs, rows);
+  copies_end();
+#pragma unroll
+  for (int i = 0; i < F_STAGES - 1; ++i) fetch();
+  f32x2 o[4][NV][4];  // rows 2i and 2i + 1 of the thread's
+  float m[8], l[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     m[i] = -INFINITY;
     l[i] = 0.f;
-#pragma unroll
-    for (int c = 0; c < NV; ++c) o[i][c][0] = o[i][c][1] = o[i][c][2] = o[i][c][3] = 0.f;
   }
-  __syncthreads();
-  for (int kb = half * ST; kb < end; kb += 2 * ST) {
-    float s[8][4] = {};
-    for (int dc = 0; dc < D; dc += F_DC) {
-      sync();
-      load_t<F_DC, F_HALF>(Kt, k + (int64_t)kb * a.ks, a.ks, t.nk - kb, dc);
-      sync();
-#pragma unroll 8
-      for (int d = 0; d < F_DC; ++d) {
-        const float4 x0 = *reinterpret_cast<const float4*>(Qt + (dc + d) * LT + ty * 8);
-        const float4 x1 = *reinterpret_cast<const float4*>(Qt + (dc + d) * LT + ty * 8 + 4);
-        const float4 y = *reinterpret_cast<const float4*>(Kt + d * LT + tx * 4);
-        const float xs[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-        const float ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int c = 0; c < NV; ++c) o[i][c][0] = o[i][c][1] = o[i][c][2] = o[i][c][3] = 0;
+  copies_wait<F_STAGES - 1>();
+  __syncthreads();  // Q is there
+  for (int b = 0; b < mine; ++b) {
+    const int kb = first_of(b);
+    f32x2 s2[8][4] = {};
+#pragma unroll 1
+    for (int c = 0; c < NK; ++c) {
+      const float* K = next();
+#pragma unroll 4
+      for (int d = 0; d < F_KC; d += 4) {
+        ulonglong2 x[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
+          x[i] = *reinterpret_cast<const ulonglong2*>(Q + (ty + 8 * i) * QP + c * F_KC + d);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[i][j] = fmaf(xs[i], ys[j], s[i][j]);
+        for (int j = 0; j < 4; ++j) {
+          const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(K + (tx + 16 * j) * F_KP + d);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            fma2(s2[i][j], x[i].x, y.x);
+            fma2(s2[i][j], x[i].y, y.y);
+          }
+        }
       }
     }
+    float f[8], s[8][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int top = a.causal ? min(t.nk, t.at + ty * 8 + i + off + 1) : t.nk;  // keys seen
+      const int top = a.causal ? min(end, t.at + ty + 8 * i + off + 1) : end;  // keys seen
       float mx = m[i];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        s[i][j] = kb + tx * 4 + j < top ? s[i][j] * a.sl : -INFINITY;
+        s[i][j] = kb + tx + 16 * j < top ? sum_of(s2[i][j]) * a.sl : -INFINITY;
         mx = fmaxf(mx, s[i][j]);
       }
 #pragma unroll
       for (int x = 1; x < 16; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-      const float base = mx == -INFINITY ? 0.f : mx, f = ex2(m[i] - base);
+      const float base = mx == -INFINITY ? 0.f : mx;
+      f[i] = ex2(m[i] - base);
       m[i] = mx;
-      l[i] *= f;
+      l[i] *= f[i];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         s[i][j] = ex2(s[i][j] - base);
         l[i] += s[i][j];
       }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int c = 0; c < NV; ++c)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[i][c][j] *= f;
-    }
+        for (int j = 0; j < 4; ++j) {
+          const float2 x = parts_of(o[i][c][j]);
+          o[i][c][j] = pair(x.x * f[2 * i], x.y * f[2 * i + 1]);
+        }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float* at = Pt + (tx * 4 + j) * LT + ty * 8;
+      float* at = Pt + (tx + 16 * j) * LT + ty * 8;
       *reinterpret_cast<float4*>(at) = make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
       *reinterpret_cast<float4*>(at + 4) = make_float4(s[4][j], s[5][j], s[6][j], s[7][j]);
     }
-    for (int kc = 0; kc < min(ST, end - kb); kc += F_KC) {
-      sync();
-      load_r<D, F_KC, F_HALF>(Vc, v + (int64_t)kb * a.vs, a.vs, kc, t.nk - kb);
-      sync();
+    const int nv = v_chunks(b);
+#pragma unroll 1
+    for (int c = 0; c < nv; ++c) {
+      const float* V = next();
+      const float* P = Pt + c * VR * LT + ty * 8;
 #pragma unroll 4
-      for (int j = 0; j < F_KC; ++j) {
-        const float4 x0 = *reinterpret_cast<const float4*>(Pt + (kc + j) * LT + ty * 8);
-        const float4 x1 = *reinterpret_cast<const float4*>(Pt + (kc + j) * LT + ty * 8 + 4);
-        const float xs[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+      for (int j = 0; j < VR; ++j) {
+        const ulonglong2 x0 = *reinterpret_cast<const ulonglong2*>(P + j * LT);
+        const ulonglong2 x1 = *reinterpret_cast<const ulonglong2*>(P + j * LT + 4);
+        const f32x2 x[4] = {x0.x, x0.y, x1.x, x1.y};
 #pragma unroll
-        for (int c = 0; c < NV; ++c) {
-          const float4 y = *reinterpret_cast<const float4*>(Vc + j * D + c * 64 + tx * 4);
+        for (int w = 0; w < NV; ++w) {
+          const float4 y = *reinterpret_cast<const float4*>(V + j * D + w * 64 + tx * 4);
+          const f32x2 ys[4] = {pair(y.x, y.x), pair(y.y, y.y), pair(y.z, y.z), pair(y.w, y.w)};
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            o[i][c][0] = fmaf(xs[i], y.x, o[i][c][0]);
-            o[i][c][1] = fmaf(xs[i], y.y, o[i][c][1]);
-            o[i][c][2] = fmaf(xs[i], y.z, o[i][c][2]);
-            o[i][c][3] = fmaf(xs[i], y.w, o[i][c][3]);
-          }
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int z = 0; z < 4; ++z) fma2(o[i][w][z], x[i], ys[z]);
         }
       }
     }
@@ -357,141 +411,224 @@ __global__ void __launch_bounds__(F_NT) k_attn_fwd_simt(SeqArgs a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
 #pragma unroll
-      for (int c = 0; c < NV; ++c)
-        *reinterpret_cast<float4*>(Qt + (ty * 8 + i) * D + c * 64 + tx * 4) =
-            make_float4(o[i][c][0], o[i][c][1], o[i][c][2], o[i][c][3]);
+      for (int c = 0; c < NV; ++c) {
+        float x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          x[j] = i % 2 ? parts_of(o[i / 2][c][j]).y : parts_of(o[i / 2][c][j]).x;
+        *reinterpret_cast<float4*>(Q + (ty + 8 * i) * D + c * 64 + tx * 4) =
+            make_float4(x[0], x[1], x[2], x[3]);
+      }
       if (tx == 0) {
-        ml[ty * 8 + i] = m[i];
-        ml[ST + ty * 8 + i] = l[i];
+        ml[ty + 8 * i] = m[i];
+        ml[ST + ty + 8 * i] = l[i];
       }
     }
   }
   __syncthreads();
   if (half == 1) return;
+  float* out = a.parts > 1 ? a.part_o + part * a.Nq * a.Hq * D : (float*)a.out;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    if (ty * 8 + i >= rows) continue;
-    const float m1 = ml[ty * 8 + i], l1 = ml[ST + ty * 8 + i], top = fmaxf(m[i], m1);
+    const int at = ty + 8 * i;
+    if (at >= rows) continue;
+    const float m1 = ml[at], l1 = ml[ST + at], top = fmaxf(m[i], m1);
     const float base = top == -INFINITY ? 0.f : top, f0 = ex2(m[i] - base), f1 = ex2(m1 - base);
     const float sum = l[i] * f0 + l1 * f1, r = sum != 0.f ? 1.f / sum : 0.f;
-    const int64_t row = (int64_t)(t.q0 + t.at + ty * 8 + i) * a.Hq + h;
+    const int64_t row = (int64_t)(t.q0 + t.at + at) * a.Hq + h;
 #pragma unroll
     for (int c = 0; c < NV; ++c) {
-      const float4 y = *reinterpret_cast<const float4*>(Qt + (ty * 8 + i) * D + c * 64 + tx * 4);
-      st4((T*)a.out + row * D + c * 64 + tx * 4, (o[i][c][0] * f0 + y.x * f1) * r,
-          (o[i][c][1] * f0 + y.y * f1) * r, (o[i][c][2] * f0 + y.z * f1) * r,
-          (o[i][c][3] * f0 + y.w * f1) * r);
+      const float4 y = *reinterpret_cast<const float4*>(Q + at * D + c * 64 + tx * 4);
+      float x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        x[j] = i % 2 ? parts_of(o[i / 2][c][j]).y : parts_of(o[i / 2][c][j]).x;
+      *reinterpret_cast<float4*>(out + row * D + c * 64 + tx * 4) =
+          make_float4((x[0] * f0 + y.x * f1) * r, (x[1] * f0 + y.y * f1) * r,
+                      (x[2] * f0 + y.z * f1) * r, (x[3] * f0 + y.w * f1) * r);
     }
-    if (tx == 0 && a.lse) a.lse[row] = sum != 0.f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+    if (tx == 0) {
+      const float lse2 = sum != 0.f ? top + log2f(sum) : -INFINITY;
+      if (a.parts > 1)
+        a.part_lse[part * a.Nq * a.Hq + row] = lse2;
+      else if (a.lse)
+        a.lse[row] = lse2 * kLn2;
+    }
   }
 }
 
-constexpr int B_NT = 256, B_DC = 16, B_XC = 8;
+constexpr int B_NT = 256;
+constexpr int B_CC = 16, B_CP = B_CC + 4;  // columns of a chunk, floats between its rows
+constexpr int B_SLOT = 2 * ST * B_CP;
 
+// Chunks on their way or in use: 2 where that lets two CTAs share an SM.
+template <int D, bool KV>
+constexpr int bwd_stages() {
+  return D == 128 && !KV ? 2 : 3;
+}
 template <int D, bool KV>
 constexpr size_t bwd_smem() {
-  return (size_t)(2 * D * LT + 2 * B_DC * LT + (KV ? 2 : 1) * ST * LT + (KV ? 2 : 1) * B_XC * D) * 4;
+  return (size_t)(2 * ST * (D + 4) + bwd_stages<D, KV>() * B_SLOT + (KV ? 2 : 1) * ST * LT) * 4;
+}
+template <int D, bool KV>
+constexpr int bwd_ctas() {
+  return 2 * (bwd_smem<D, KV>() + 1024) <= 228 * 1024 ? 2 : 1;
 }
 
 // KV: 64 keys of one key head, dk and dv over all queries of its query heads; else 64 queries of
-// one head, dq over the keys that they see.  A thread has 4 x 4 scores and 4 rows x D/16 columns of
-// each gradient.  The own side's two operands (k, v or q, dO) stay in shared memory.
-template <int D, typename T, bool KV>
-__global__ void __launch_bounds__(B_NT) k_attn_bwd_simt(SeqArgs a) {
+// one head, dq over the keys that they see.  A thread has 4 rows x 4 columns (tx, tx + 16, ..) of
+// the scores and 4 rows x D/16 columns of each gradient.  The own side's two operands (k, v or q,
+// dO) stay in shared memory.
+template <int D, bool KV>
+__global__ void __launch_bounds__(B_NT, bwd_ctas<D, KV>()) k_attn_bwd_simt(SeqArgs a) {
   extern __shared__ __align__(16) float sm[];
-  constexpr int NV = D / 64, NP = KV ? 2 : 1;
-  float *R1 = sm, *R2 = R1 + D * LT, *C1 = R2 + D * LT, *C2 = C1 + B_DC * LT;
-  float *dS = C2 + B_DC * LT, *P = dS + ST * LT, *X1 = dS + NP * ST * LT, *X2 = X1 + B_XC * D;
-  after_previous();
+  constexpr int NV = D / 64, NP = KV ? 2 : 1, RP = D + 4, STAGES = bwd_stages<D, KV>();
+  constexpr int C1 = D / B_CC, XR = 2048 / (D * NP);  // chunks of columns; rows of a chunk of rows
+  float *R1 = sm, *R2 = R1 + ST * RP, *ring = R2 + ST * RP, *dS = ring + STAGES * B_SLOT;
+  float* P = dS + (KV ? ST * LT : 0);
+  if (!a.late) after_previous();
   before_next();
-  const int heads = KV ? a.Hk : a.Hq, hh = blockIdx.x % heads, hk = KV ? hh : hh / a.G;
+  const int heads = KV ? a.Hk : a.Hq, part = KV ? blockIdx.x % a.splits : 0;
+  const int item = KV ? blockIdx.x / a.splits : blockIdx.x, hh = item % heads, hk = KV ? hh : hh / a.G;
   Tile t;
-  if (!tile_of<KV>(a, blockIdx.x / heads, &t)) return;
+  if (!tile_of<KV>(a, item / heads, &t)) {
+    if (a.late) after_previous();
+    return;
+  }
   const int ty = threadIdx.x / 16, tx = threadIdx.x % 16, off = t.nk - t.nq;
   const int rows = min(ST, (KV ? t.nk : t.nq) - t.at);
-  const int first = KV ? first_query(a, t) / ST * ST : 0, end = KV ? t.nq : keys_seen(a, t, ST);
-  const T* kv_k = (const T*)a.k + (int64_t)t.k0 * a.ks + (int64_t)hk * D;
-  const T* kv_v = (const T*)a.v + (int64_t)t.k0 * a.vs + (int64_t)hk * D;
+  const int first = KV ? first_query(a, t) : 0, end = KV ? t.nq : keys_seen(a, t, ST);
+  const float* kv_k = (const float*)a.k + t.k0 * a.ks + (int64_t)hk * D;
+  const float* kv_v = (const float*)a.v + t.k0 * a.vs + (int64_t)hk * D;
   const int64_t os = (int64_t)a.Hq * D;  // between tokens of dO
-  auto q_of = [&](int h) { return (const T*)a.q + (int64_t)t.q0 * a.qs + (int64_t)h * D; };
-  auto do_of = [&](int h) { return (const T*)a.dO + t.q0 * os + (int64_t)h * D; };
-  if (KV) {
-    load_t<D, B_NT>(R1, kv_k + (int64_t)t.at * a.ks, a.ks, rows, 0);
-    load_t<D, B_NT>(R2, kv_v + (int64_t)t.at * a.vs, a.vs, rows, 0);
-  } else {
-    load_t<D, B_NT>(R1, q_of(hh) + (int64_t)t.at * a.qs, a.qs, rows, 0);
-    load_t<D, B_NT>(R2, do_of(hh) + (int64_t)t.at * os, os, rows, 0);
-  }
-  float acc[NP][4][NV][4] = {};
-  for (int h = KV ? hh * a.G : hh; h < (KV ? (hh + 1) * a.G : hh + 1); ++h) {
-    const float* lse2 = a.lse2 + (int64_t)h * a.Nq + t.q0;
+  auto q_of = [&](int h) { return (const float*)a.q + t.q0 * a.qs + (int64_t)h * D; };
+  auto do_of = [&](int h) { return (const float*)a.dO + t.q0 * os + (int64_t)h * D; };
+  const int64_t s1 = KV ? a.qs : a.ks, s2 = KV ? os : a.vs;
+  const int mine = KV ? a.G / a.splits : 1, h0 = KV ? hh * a.G + part * mine : hh;
+  const int h1 = first < end ? h0 + mine : h0;
+  auto x_chunks = [&](int b) { return (min(ST, end - b) + XR - 1) / XR; };
+  int fh = h0, fb = first, fc = 0, fs = 0;  // the next chunk to be fetched, its place in the ring
+  auto fetch = [&]() {
+    if (fh < h1) {
+      const float *x1 = KV ? q_of(fh) : kv_k, *x2 = KV ? do_of(fh) : kv_v;
+      float* to = ring + fs * B_SLOT;
+      if (fc < C1) {
+        copy_rows<ST, B_CC, B_CP, B_NT>(to, x1 + fb * s1 + fc * B_CC, s1, end - fb);
+        copy_rows<ST, B_CC, B_CP, B_NT>(to + ST * B_CP, x2 + fb * s2 + fc * B_CC, s2, end - fb);
+      } else {
+        const int at = fb + (fc - C1) * XR;
+        copy_rows<XR, D, D, B_NT>(to, x1 + at * s1, s1, end - at);
+        if (KV) copy_rows<XR, D, D, B_NT>(to + XR * D, x2 + at * s2, s2, end - at);
+      }
+      fs = fs + 1 == STAGES ? 0 : fs + 1;
+      if (++fc == C1 + x_chunks(fb)) {
+        fc = 0;
+        fb += ST;
+        if (fb >= end) {
+          fb = first;
+          ++fh;
+        }
+      }
+    }
+    copies_end();  // a group without copies past the last one
+  };
+  int slot = 0;
+  auto next = [&]() {  // the next chunk is there; the one before it is no longer read
+    copies_wait<STAGES - 2>();
+    __syncthreads();
+    fetch();
+    const float* x = ring + slot * B_SLOT;
+    slot = slot + 1 == STAGES ? 0 : slot + 1;
+    return x;
+  };
+  copy_rows<ST, D, RP, B_NT>(R1, (KV ? kv_k : q_of(hh)) + t.at * (KV ? a.ks : a.qs),
+                             KV ? a.ks : a.qs, rows);
+  copy_rows<ST, D, RP, B_NT>(R2, (KV ? kv_v : do_of(hh)) + t.at * (KV ? a.vs : os),
+                             KV ? a.vs : os, rows);
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) fetch();  // the first group holds R1 and R2 too
+  f32x2 acc[NP][2][NV][4];                       // rows 2i and 2i + 1 of the thread's
+#pragma unroll
+  for (int z = 0; z < NP; ++z)
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int c = 0; c < NV; ++c)
+        acc[z][i][c][0] = acc[z][i][c][1] = acc[z][i][c][2] = acc[z][i][c][3] = 0;
+  for (int h = h0; h < h1; ++h) {
+    const float* lse = a.lse2 + (int64_t)h * a.Nq + t.q0;
     const float* delta = a.delta + (int64_t)h * a.Nq + t.q0;
-    const T *x1 = KV ? q_of(h) : kv_k, *x2 = KV ? do_of(h) : kv_v;
-    const int64_t s1 = KV ? a.qs : a.ks, s2 = KV ? os : a.vs;
-    const int all = KV ? t.nq : t.nk;
     for (int b = first; b < end; b += ST) {
-      float s[4][4] = {}, dp[4][4] = {};
-      for (int dc = 0; dc < D; dc += B_DC) {
-        __syncthreads();
-        load_t<B_DC, B_NT>(C1, x1 + (int64_t)b * s1, s1, all - b, dc);
-        load_t<B_DC, B_NT>(C2, x2 + (int64_t)b * s2, s2, all - b, dc);
-        __syncthreads();
+      float ls[4], de[4];  // of the queries: the thread's columns, or its rows
 #pragma unroll
-        for (int d = 0; d < B_DC; ++d) {
-          const float4 r1 = *reinterpret_cast<const float4*>(R1 + (dc + d) * LT + ty * 4);
-          const float4 r2 = *reinterpret_cast<const float4*>(R2 + (dc + d) * LT + ty * 4);
-          const float4 c1 = *reinterpret_cast<const float4*>(C1 + d * LT + tx * 4);
-          const float4 c2 = *reinterpret_cast<const float4*>(C2 + d * LT + tx * 4);
-          const float r1s[4] = {r1.x, r1.y, r1.z, r1.w}, r2s[4] = {r2.x, r2.y, r2.z, r2.w};
-          const float c1s[4] = {c1.x, c1.y, c1.z, c1.w}, c2s[4] = {c2.x, c2.y, c2.z, c2.w};
+      for (int j = 0; j < 4; ++j) {
+        const int qi = KV ? b + tx + 16 * j : t.at + ty * 4 + j;
+        ls[j] = qi < t.nq ? lse[qi] : INFINITY;
+        de[j] = qi < t.nq ? delta[qi] : 0.f;
+      }
+      f32x2 s[4][4] = {}, dp[4][4] = {};
+#pragma unroll 1
+      for (int c = 0; c < C1; ++c) {
+        const float* x = next();
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+        for (int z = 0; z < 2; ++z)
+#pragma unroll
+          for (int d = 0; d < B_CC; d += 4) {
+            const float* own = (z ? R2 : R1) + ty * 4 * RP + c * B_CC + d;
+            ulonglong2 r[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              r[i] = *reinterpret_cast<const ulonglong2*>(own + i * RP);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              s[i][j] = fmaf(r1s[i], c1s[j], s[i][j]);
-              dp[i][j] = fmaf(r2s[i], c2s[j], dp[i][j]);
+              const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(
+                  x + z * ST * B_CP + (tx + 16 * j) * B_CP + d);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                fma2((z ? dp : s)[i][j], r[i].x, y.x);
+                fma2((z ? dp : s)[i][j], r[i].y, y.y);
+              }
             }
-        }
+          }
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         float p[4], ds[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int row = t.at + ty * 4 + i, col = b + tx * 4 + j;
+          const int row = t.at + ty * 4 + i, col = b + tx + 16 * j, w = KV ? j : i;
           const int qi = KV ? col : row, kj = KV ? row : col;
           const bool in = qi < t.nq && kj < t.nk && (!a.causal || kj <= qi + off);
-          p[i] = in ? ex2(fmaf(s[i][j], a.sl, -lse2[qi])) : 0.f;
-          ds[i] = in ? p[i] * (dp[i][j] - delta[qi]) : 0.f;
+          // the exponent is rounded once, where it is small: p is at most 1
+          p[i] = in ? ex2(fmaf(sum_of(s[i][j]), a.scale, -ls[w]) * kLog2e) : 0.f;
+          ds[i] = in ? p[i] * (sum_of(dp[i][j]) - de[w]) : 0.f;
         }
-        *reinterpret_cast<float4*>(dS + (tx * 4 + j) * LT + ty * 4) =
+        *reinterpret_cast<float4*>(dS + (tx + 16 * j) * LT + ty * 4) =
             make_float4(ds[0], ds[1], ds[2], ds[3]);
         if (KV)
-          *reinterpret_cast<float4*>(P + (tx * 4 + j) * LT + ty * 4) =
+          *reinterpret_cast<float4*>(P + (tx + 16 * j) * LT + ty * 4) =
               make_float4(p[0], p[1], p[2], p[3]);
       }
-      for (int xc = 0; xc < min(ST, end - b); xc += B_XC) {
-        __syncthreads();
-        load_r<D, B_XC, B_NT>(X1, x1 + (int64_t)b * s1, s1, xc, all - b);
-        if (KV) load_r<D, B_XC, B_NT>(X2, x2 + (int64_t)b * s2, s2, xc, all - b);
-        __syncthreads();
+      const int nx = x_chunks(b);
+#pragma unroll 1
+      for (int c = 0; c < nx; ++c) {
+        const float* x = next();
 #pragma unroll
-        for (int j = 0; j < B_XC; ++j)
+        for (int j = 0; j < XR; ++j)
 #pragma unroll
           for (int z = 0; z < NP; ++z) {
-            const float4 w =
-                *reinterpret_cast<const float4*>((z ? P : dS) + (xc + j) * LT + ty * 4);
-            const float ws[4] = {w.x, w.y, w.z, w.w};
+            const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(
+                (z ? P : dS) + (c * XR + j) * LT + ty * 4);
 #pragma unroll
-            for (int c = 0; c < NV; ++c) {
+            for (int v = 0; v < NV; ++v) {
               const float4 y =
-                  *reinterpret_cast<const float4*>((z ? X2 : X1) + j * D + c * 64 + tx * 4);
+                  *reinterpret_cast<const float4*>(x + (z * XR + j) * D + v * 64 + tx * 4);
+              const f32x2 ys[4] = {pair(y.x, y.x), pair(y.y, y.y), pair(y.z, y.z),
+                                   pair(y.w, y.w)};
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                acc[z][i][c][0] = fmaf(ws[i], y.x, acc[z][i][c][0]);
-                acc[z][i][c][1] = fmaf(ws[i], y.y, acc[z][i][c][1]);
-                acc[z][i][c][2] = fmaf(ws[i], y.z, acc[z][i][c][2]);
-                acc[z][i][c][3] = fmaf(ws[i], y.w, acc[z][i][c][3]);
+              for (int e = 0; e < 4; ++e) {
+                fma2(acc[z][0][v][e], w.x, ys[e]);
+                fma2(acc[z][1][v][e], w.y, ys[e]);
               }
             }
           }
@@ -503,16 +640,22 @@ __global__ void __launch_bounds__(B_NT) k_attn_bwd_simt(SeqArgs a) {
     if (ty * 4 + i >= rows) continue;
     const int64_t row = (int64_t)((KV ? t.k0 : t.q0) + t.at + ty * 4 + i) * heads + hh;
 #pragma unroll
-    for (int c = 0; c < NV; ++c) {
-      const float* x = acc[0][i][c];
-      st4((T*)(KV ? a.dk : a.dq) + row * D + c * 64 + tx * 4, x[0] * a.scale, x[1] * a.scale,
-          x[2] * a.scale, x[3] * a.scale);
-      if constexpr (KV) {
-        const float* y = acc[1][i][c];
-        st4((T*)a.dv + row * D + c * 64 + tx * 4, y[0], y[1], y[2], y[3]);
+    for (int z = 0; z < NP; ++z)
+#pragma unroll
+      for (int c = 0; c < NV; ++c) {
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 y = parts_of(acc[z][i / 2][c][e]);
+          x[e] = (i % 2 ? y.y : y.x) * (z ? 1.f : a.scale);
+        }
+        float* to = (float*)(z ? a.dv : KV ? a.dk : a.dq);
+        if (KV && a.splits > 1) to = (z ? a.part_v : a.part_k) + part * a.Nk * a.Hk * D;
+        to += row * D + c * 64 + tx * 4;
+        *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
       }
-    }
   }
+  if (a.late) after_previous();
 }
 
 // -------------------------------------------------------------------------------- host
@@ -564,13 +707,14 @@ Layout layout(const gdn_attn_seq_problem* p, bool bwd, int rq, int rk) {
   y.lse2 = lists && bwd ? up(y.lk + y.mk * sizeof(Tile)) : y.lk;
   y.delta = y.lse2 + (bwd ? up((size_t)p->Nq * p->Hq * 4) : 0);
   y.part_k = y.delta + (bwd ? up((size_t)p->Nq * p->Hq * 4) : 0);
-  // bf16: a key tile's query heads go to several CTAs where there are fewer tiles than 4 per SM; each
-  // writes a part of dk and dv in fp32, which k_attn_sum adds up (16001 tokens, 16 on 2 heads of 256:
-  // one part 7.9 ms, 8: see the kernels' file; the parts cost 16 bytes per element and part).
+  // A key tile's query heads go to several CTAs where there are fewer tiles than 4 per SM (fp32: 2, its
+  // tiles are smaller); each writes a part of dk and dv in fp32, which k_attn_sum adds up (16001 tokens,
+  // 16 on 2 heads of 256, bf16: one part 7.9 ms, 8: 6.0; the parts cost 16 bytes per element and part).
   y.splits = 1;
-  const int64_t G = p->Hq / p->Hk, tiles = (int64_t)y.mk * p->Hk * (rk / 128);
-  if (bwd && p->dtype == GDN_BF16 && tiles > 0)
-    for (int64_t s = 2; s <= G && tiles * y.splits < 608; ++s)
+  const bool bf16 = p->dtype == GDN_BF16;
+  const int64_t G = p->Hq / p->Hk, tiles = (int64_t)y.mk * p->Hk * (bf16 ? rk / 128 : 1);
+  if (bwd && tiles > 0)
+    for (int64_t s = 2; s <= G && tiles * y.splits < (bf16 ? 608 : 304); ++s)
       if (G % s == 0) y.splits = (int)s;
   const size_t part = y.splits > 1 ? up((size_t)y.splits * p->Nk * p->Hk * p->D * 4) : 0;
   y.part_v = y.part_k + part;
@@ -580,11 +724,11 @@ Layout layout(const gdn_attn_seq_problem* p, bool bwd, int rq, int rk) {
   // the parts of o are fp32 and k_attn_merge joins them (64 tokens behind 31936, 32 on 8 heads of 128:
   // 338 us without, 80 with; 256 tiles of 9 sequences behind up to 16000 tokens: 308 and 330).
   y.parts = 1;
-  const int64_t items = (int64_t)y.mq * (p->Hq / tc_pack(G));
-  if (!bwd && p->dtype == GDN_BF16 && items > 0) {
+  const int64_t items = (int64_t)y.mq * (p->Hq / (bf16 ? tc_pack(G) : 1));
+  if (!bwd && items > 0) {
     int64_t s = items < 152 ? (2 * 152 + items - 1) / items : 1;
-    const int64_t keys = p->Nk / (n > 0 ? n : 1);
-    if (s > keys / 512) s = keys / 512;
+    const int64_t keys = p->Nk / (n > 0 ? n : 1), least = bf16 ? 512 : 256;
+    if (s > keys / least) s = keys / least;
     y.parts = (int)(s < 1 ? 1 : s > kMaxParts ? kMaxParts : s);
   }
   const size_t rows = y.parts > 1 ? (size_t)y.parts * p->Nq * p->Hq * 4 : 0;
@@ -621,7 +765,7 @@ gdn_status begin(const gdn_attn_seq_problem* p, bool bwd, const int32_t* cu_q,
   const Layout y = layout_of(p, bwd);
   const bool bf16 = p->dtype == GDN_BF16;
   const TcPlan tp = tc_plan(p->D);
-  a->pack = tc_pack(a->G);
+  a->pack = bf16 ? tc_pack(a->G) : 1;
   a->tq.rows = bf16 ? (bwd ? tp.dq_rows : tp.fwd_rows / a->pack) : ST;
   a->tk.rows = bf16 ? tp.dkv_rows : ST;
   a->tq.most = y.mq;
@@ -714,8 +858,9 @@ gdn_status gdn_attn_fwd(const gdn_attn_seq_problem* p, const void* q, const void
   a.lse = lse;
   const cudaError_t e = p->dtype == GDN_BF16 ? launch_fwd_tc(a, p->D, st)
                                              : with_dim(p->D, [&](auto d) {
-    return launch_simt<k_attn_fwd_simt<d(), float>>((int64_t)a.tq.most * a.Hq, F_NT,
-                                                    fwd_smem<d()>(), st, a);
+    const cudaError_t e = launch_simt<k_attn_fwd_simt<d()>>((int64_t)a.tq.most * a.Hq * a.parts,
+                                                            F_NT, fwd_smem<d()>(), st, a);
+    return e == cudaSuccess && a.parts > 1 ? launch_merge(a, d(), true, st) : e;
   });
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
@@ -766,11 +911,13 @@ gdn_status gdn_attn_bwd(const gdn_attn_seq_problem* p, const void* q, const void
                : launch_behind(k_attn_rows<D, float>, dim3(grid), 256, 0, st, a);
     if (e != cudaSuccess) return e;
     if (bf16) return launch_bwd_tc(a, D, st);
-    e = launch_simt<k_attn_bwd_simt<D, float, true>>((int64_t)a.tk.most * a.Hk, B_NT,
-                                                     bwd_smem<D, true>(), st, a);
+    e = launch_simt<k_attn_bwd_simt<D, true>>((int64_t)a.tk.most * a.Hk * a.splits, B_NT,
+                                              bwd_smem<D, true>(), st, a);
     if (e != cudaSuccess) return e;
-    return launch_simt<k_attn_bwd_simt<D, float, false>>((int64_t)a.tq.most * a.Hq, B_NT,
-                                                         bwd_smem<D, false>(), st, a);
+    a.late = a.tk.most > 0;  // reads nothing of the launch before
+    e = launch_simt<k_attn_bwd_simt<D, false>>((int64_t)a.tq.most * a.Hq, B_NT,
+                                               bwd_smem<D, false>(), st, a);
+    return e == cudaSuccess && a.Nk > 0 && a.splits > 1 ? launch_sum(a, D, true, st) : e;
   });
   return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }

@@ -136,6 +136,9 @@ inline int tc_pack(int64_t G) { return G % 16 == 0 ? 16 : G % 8 == 0 ? 8 : G % 4
 TcPlan tc_plan(int D);
 cudaError_t launch_fwd_tc(const SeqArgs& a, int D, cudaStream_t st);
 cudaError_t launch_bwd_tc(const SeqArgs& a, int D, cudaStream_t st);
+// dk and dv from their parts, o and lse from the parts of the keys, in either type.
+cudaError_t launch_sum(const SeqArgs& a, int D, bool fp32, cudaStream_t st);
+cudaError_t launch_merge(const SeqArgs& a, int D, bool fp32, cudaStream_t st);
 
 }  // namespace seq
 }  // namespace gdn

@@ -1567,10 +1567,17 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
   if (a.late) after_previous();
 }
 
+__device__ __forceinline__ void write4(__nv_bfloat16* to, float4 x) {
+  *reinterpret_cast<uint2*>(to) = make_uint2(bf16x2(x.x, x.y), bf16x2(x.z, x.w));
+}
+__device__ __forceinline__ void write4(float* to, float4 x) {
+  *reinterpret_cast<float4*>(to) = x;
+}
+
 // dk and dv from their parts, which are added in their order: a CTA takes SUM_ROWS rows of a key tile
 // and head.  Bound by HBM.
 constexpr int SUM_ROWS = 16;
-template <int D>
+template <int D, typename T>
 __global__ void __launch_bounds__(256) k_attn_sum(SeqArgs a) {
   after_previous();
   before_next();
@@ -1598,17 +1605,15 @@ __global__ void __launch_bounds__(256) k_attn_sum(SeqArgs a) {
       v.z += z.z;
       v.w += z.w;
     }
-    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.dk) + at) =
-        make_uint2(bf16x2(k.x, k.y), bf16x2(k.z, k.w));
-    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.dv) + at) =
-        make_uint2(bf16x2(v.x, v.y), bf16x2(v.z, v.w));
+    write4(reinterpret_cast<T*>(a.dk) + at, k);
+    write4(reinterpret_cast<T*>(a.dv) + at, v);
   }
 }
 
 // o and lse from the parts of the keys: a CTA takes SUM_ROWS rows of a tile.  With L_p the part's
 // log2-sum and o_p its average: w_p = 2^(L_p - max L), o = sum w_p o_p / sum w_p.  A part without
 // keys has L_p = -inf and counts nothing.
-template <int D>
+template <int D, typename T>
 __global__ void __launch_bounds__(256) k_attn_merge(SeqArgs a) {
   constexpr int PER = D / 4;  // threads of a row
   __shared__ float s_w[SUM_ROWS][kMaxParts];
@@ -1655,8 +1660,7 @@ __global__ void __launch_bounds__(256) k_attn_merge(SeqArgs a) {
       o.z = fmaf(x.z, w, o.z);
       o.w = fmaf(x.w, w, o.w);
     }
-    *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.out) + at * D + i % PER * 4) =
-        make_uint2(bf16x2(o.x, o.y), bf16x2(o.z, o.w));
+    write4(reinterpret_cast<T*>(a.out) + at * D + i % PER * 4, o);
   }
 }
 
@@ -1699,9 +1703,7 @@ cudaError_t fwd(const SeqArgs& a, cudaStream_t st) {
   const int64_t tiles = (int64_t)a.tq.most * (a.Hq / a.pack);
   const cudaError_t e = launch<k_flash<D, true>>(ctas_of(tiles * a.parts), Flash<D>::kThreads,
                                                  Flash<D>::kBytes, st, q, k, v, a);
-  if (e != cudaSuccess || a.parts == 1) return e;
-  return launch_behind(k_attn_merge<D>,
-                       dim3((unsigned)(tiles * (a.tq.rows * a.pack / SUM_ROWS))), 256, 0, st, a);
+  return e == cudaSuccess && a.parts > 1 ? launch_merge(a, D, false, st) : e;
 }
 
 template <int D>
@@ -1752,15 +1754,34 @@ cudaError_t bwd(SeqArgs a, cudaStream_t st) {
       e = launch<k_slope<D, kDq>>(ctas_of(query_items), Slope<D>::kThreads, Slope<D>::kBytes, st,
                                   q, d, k, v, a);
   }
-  if (e == cudaSuccess && a.Nk > 0 && a.splits > 1)
-    e = launch_behind(k_attn_sum<D>,
-                      dim3((unsigned)((int64_t)a.tk.most * a.Hk * (a.tk.rows / SUM_ROWS))), 256, 0,
-                      st, a);
-  return e;
+  return e == cudaSuccess && a.Nk > 0 && a.splits > 1 ? launch_sum(a, D, false, st) : e;
 }
 
 }  // namespace
 
+cudaError_t launch_sum(const SeqArgs& a, int D, bool fp32, cudaStream_t st) {
+  const dim3 grid((unsigned)((int64_t)a.tk.most * a.Hk * (a.tk.rows / SUM_ROWS)));
+  auto go = [&](auto kernel) { return launch_behind(kernel, grid, 256, 0, st, a); };
+  if (fp32)
+    return D == 64    ? go(k_attn_sum<64, float>)
+           : D == 128 ? go(k_attn_sum<128, float>)
+                      : go(k_attn_sum<256, float>);
+  return D == 64    ? go(k_attn_sum<64, __nv_bfloat16>)
+         : D == 128 ? go(k_attn_sum<128, __nv_bfloat16>)
+                    : go(k_attn_sum<256, __nv_bfloat16>);
+}
+cudaError_t launch_merge(const SeqArgs& a, int D, bool fp32, cudaStream_t st) {
+  const dim3 grid((unsigned)((int64_t)a.tq.most * (a.Hq / a.pack) *
+                             (a.tq.rows * a.pack / SUM_ROWS)));
+  auto go = [&](auto kernel) { return launch_behind(kernel, grid, 256, 0, st, a); };
+  if (fp32)
+    return D == 64    ? go(k_attn_merge<64, float>)
+           : D == 128 ? go(k_attn_merge<128, float>)
+                      : go(k_attn_merge<256, float>);
+  return D == 64    ? go(k_attn_merge<64, __nv_bfloat16>)
+         : D == 128 ? go(k_attn_merge<128, __nv_bfloat16>)
+                    : go(k_attn_merge<256, __nv_bfloat16>);
+}
 TcPlan tc_plan(int D) {
   const int two = D == 64 ? Flash<64>::kTiles : D == 128 ? Flash<128>::kTiles : Flash<256>::kTiles;
   const int own = D == 256 ? 2 * TR : TR;
