@@ -32,7 +32,7 @@ namespace {
 
 constexpr int TR = 128;                     // rows of a tile
 constexpr int kSmem = 227 * 1024;
-constexpr int kHead = 3072;                 // barriers and row values in front of the tiles
+constexpr int kHead = 3 * 1024;             // barriers and row values in front of the tiles
 constexpr float kLazy = 8.f;                // log2 units
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
@@ -217,33 +217,32 @@ struct Turns {
   }
 };
 
-// The finder's side: every item there is, then one with n = -1.
-template <typename ITEM, typename W>
-__device__ __forceinline__ void feed_items(Feed& f, Turns turns, const SeqArgs& a, W wait) {
+// The finder's side: every item there is, then one with n = -1.  Where the CTA gave up, that one at
+// once: all others see it after the same items, so that their barriers of some warps stay matched.
+template <typename ITEM>
+__device__ __forceinline__ void feed_items(Feed& f, Turns turns, const SeqArgs& a,
+                                           volatile int* gave_up) {
   static_assert(sizeof(ITEM) <= sizeof(f.item[0]), "");
   int turn = 0;
   auto put = [&](const ITEM& x) {
     const int s = turn & 1;
-    if (turn >= 2) wait(&f.empty[s], ((turn >> 1) - 1) & 1);
+    if (turn >= 2) wait_alone(&f.empty[s], ((turn >> 1) - 1) & 1, gave_up);
     *reinterpret_cast<ITEM*>(f.item[s]) = x;
     mbar_arrive(&f.full[s]);
     ++turn;
   };
   ITEM x;
-  for (int idx; (idx = turns.next()) >= 0;)
+  for (int idx; !*gave_up && (idx = turns.next()) >= 0;)
     if (x.find(a, idx)) put(x);
   x.n = -1;
   put(x);
 }
-// The others': the next item; false: there is none, or the CTA gave up.  By whole warps, or (ALONE) by
-// one lane.
-template <bool ALONE, typename ITEM, typename W>
-__device__ __forceinline__ bool take_item(Feed& f, int& turn, ITEM& x, W wait,
-                                          volatile int* gave_up) {
+// The others': the next item; false: there is none.  By whole warps, or (ALONE) by one lane.
+template <bool ALONE, typename ITEM>
+__device__ __forceinline__ bool take_item(Feed& f, int& turn, ITEM& x, volatile int* gave_up) {
   const int s = turn & 1;
-  wait(&f.full[s], (turn >> 1) & 1);
+  if (!wait_alone(&f.full[s], (turn >> 1) & 1, gave_up)) return false;
   ++turn;
-  if (*gave_up) return false;
   x = *reinterpret_cast<const ITEM*>(f.item[s]);
   if (!ALONE) __syncwarp();
   if (ALONE || (threadIdx.x & 31) == 0) mbar_arrive(&f.empty[s]);
@@ -376,10 +375,11 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
     if (warp == 12 && lane == 0) {
       // ---- copies
       int stage = 0, turn = 0, works = 0;
-      while (take_item<true>(bar.feed, taken, x, wait, &bar.gave_up)) {
+      while (take_item<true>(bar.feed, taken, x, &bar.gave_up)) {
         if (x.n == 0) continue;
         const int rows = FWD ? TR / a.pack : TR;
         if (works > 0) wait(&bar.r_empty, (works - 1) & 1);
+        if (bar.gave_up) continue;
         ++works;
         mbar_arrive_expect_tx(&bar.r_full, NT * F::kTile);
         for (int i = 0; i < NT; ++i)
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
       auto next = [&]() {
         if (++stage == ST) stage = 0, ++turn;
       };
-      while (take_item<false>(bar.feed, taken, x, wait, &bar.gave_up)) {
+      while (take_item<false>(bar.feed, taken, x, &bar.gave_up)) {
         x.make_uniform();
         if (x.n == 0) continue;
         const int xrows = FWD ? x.t.nk : x.t.nq;
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
         mbar_wait(&bar.drained, 0, nullptr, 0);
       }
     } else if (warp == 14 && lane == 0) {
-      feed_items<Item<D, FWD>>(bar.feed, Turns(tiles_there<!FWD>(a) * per_tile), a, wait);
+      feed_items<Item<D, FWD>>(bar.feed, Turns(tiles_there<!FWD>(a) * per_tile), a, &bar.gave_up);
     }
   } else if (group == 2) {
     // ---- results: a thread per row
@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
     const int r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     int items = 0, works[2] = {0, 0};
-    while (take_item<false>(bar.feed, taken, x, wait, &bar.gave_up)) {
+    while (take_item<false>(bar.feed, taken, x, &bar.gave_up)) {
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         const int row = FWD ? x.t.at + (i * TR + r) / a.pack : x.t.at + i * TR + r;
@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     int items = 0, done = 0;  // done: blocks of the tile so far, of all items
     int placed = 0;           // blocks of the ring in front of this item
-    while (take_item<false>(bar.feed, taken, x, wait, &bar.gave_up)) {
+    while (take_item<false>(bar.feed, taken, x, &bar.gave_up)) {
       const int rows = FWD ? TR / a.pack : TR, at = x.t.at + i * rows, off = x.t.nk - x.t.nq;
       const int w0 = (warp & 3) * 32;  // the warp's rows: tokens first .. last
       const int first = FWD ? at + w0 / a.pack : at + w0;
@@ -918,10 +918,11 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
       // ---- copies
       int works = 0, c = 0;
       Place at{0, 0};
-      while (take_item<true>(bar.feed, taken, x, wait, &bar.gave_up)) {
+      while (take_item<true>(bar.feed, taken, x, &bar.gave_up)) {
         if (x.n == 0) continue;
         const int row0 = (DQ ? x.t.q0 : x.t.k0) + x.t.at;
         if (works > 0) wait(&bar.r_empty, (works - 1) & 1);
+        if (bar.gave_up) continue;
         ++works;
         mbar_arrive_expect_tx(&bar.r_full, 2 * F::kTile);
         for (int i = 0; i < D / 64; ++i) {
@@ -956,7 +957,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
       constexpr uint32_t kOwn = kHead, kRing = kHead + 2 * F::kTile;
       int works = 0, c = 0;
       Place p1{0, 0}, p2{1, 0};  // of X1 and X2 of iteration c
-      while (take_item<false>(bar.feed, taken, x, wait, &bar.gave_up)) {
+      while (take_item<false>(bar.feed, taken, x, &bar.gave_up)) {
         x.make_uniform();
         if (x.n == 0) continue;
         const int xrows = DQ ? x.t.nk : x.t.nq;
@@ -1052,7 +1053,8 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
         mbar_wait(&bar.drained, 0, nullptr, 0);
       }
     } else if (warp == 14 && lane == 0) {
-      feed_items<SlopeItem<DQ, BN, TR>>(bar.feed, Turns(tiles_there<!DQ>(a) * per_tile), a, wait);
+      feed_items<SlopeItem<DQ, BN, TR>>(bar.feed, Turns(tiles_there<!DQ>(a) * per_tile), a,
+                                        &bar.gave_up);
     }
   } else if (group == 2) {
     // ---- results: a thread per row
@@ -1060,7 +1062,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
     const int r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     int works = 0;
-    while (take_item<false>(bar.feed, taken, x, wait, &bar.gave_up)) {
+    while (take_item<false>(bar.feed, taken, x, &bar.gave_up)) {
       const int row = x.t.at + r, side = DQ ? x.t.nq : x.t.nk;
       if (x.n > 0) {
         wait(&bar.o_full[0], works & 1);
@@ -1112,7 +1114,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
       if (lane == 0) mbar_arrive(b);
     };
     int c = 0;  // iterations of all items
-    while (take_item<false>(bar.feed, taken, x, wait, &bar.gave_up)) {
+    while (take_item<false>(bar.feed, taken, x, &bar.gave_up)) {
       const int off = x.t.nk - x.t.nq, first_row = x.t.at + (warp & 3) * 32, row = x.t.at + r;
       const int xrows = DQ ? x.t.nk : x.t.nq;
       float lse2 = INFINITY, delta = 0.f, ahead = 0.f;
@@ -1299,10 +1301,11 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
     if (warp == 12 && lane == 0) {
       // ---- copies: parts 0 X1 by rows, 1 X2 by rows, 2 X1 by columns
       int works = 0, c = 0;
-      while (take_item<true>(bar.feed, taken, x, wait, &bar.gave_up)) {
+      while (take_item<true>(bar.feed, taken, x, &bar.gave_up)) {
         if (x.n == 0) continue;
         const int row0 = (DQ ? x.t.q0 : x.t.k0) + x.t.at + rank * TR;
         if (works > 0) wait(&bar.r_empty, (works - 1) & 1);
+        if (bar.gave_up) continue;
         ++works;
         mbar_arrive_expect_tx(&bar.r_full, 2 * F::kTile);
         for (int i = 0; i < D / 64; ++i) {
@@ -1341,7 +1344,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
         wait(b, parity);
         if (lane == 0) arrive_first(&bar.peer[to]);
       };
-      while (take_item<false>(bar.feed, taken, x, wait, &bar.gave_up)) {
+      while (take_item<false>(bar.feed, taken, x, &bar.gave_up)) {
         if (x.n == 0) continue;
         tell(&bar.r_full, works & 1, 3);
         ++works;
@@ -1361,7 +1364,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
       const Desc kmaj(sdesc(base, 16, 1024)), mnmaj(sdesc(base, 16384, 1024));
       constexpr uint32_t kOwn = kHead, kParts = kHead + 2 * F::kTile;
       int works = 0, c = 0;
-      while (take_item<false>(bar.feed, taken, x, wait, &bar.gave_up)) {
+      while (take_item<false>(bar.feed, taken, x, &bar.gave_up)) {
         x.make_uniform();
         if (x.n == 0) continue;
         const int xrows = DQ ? x.t.nk : x.t.nq;
@@ -1426,7 +1429,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
       }
     } else if (warp == 14 && lane == 0) {
       feed_items<SlopeItem<DQ, BN, 2 * TR>>(bar.feed, Turns(tiles_there<!DQ>(a) * per_tile, 2), a,
-                                            wait);
+                                            &bar.gave_up);
     }
   } else if (group == 2) {
     // ---- results: a thread per row
@@ -1434,7 +1437,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
     const int r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     int works = 0;
-    while (take_item<false>(bar.feed, taken, x, wait, &bar.gave_up)) {
+    while (take_item<false>(bar.feed, taken, x, &bar.gave_up)) {
       const int row = x.t.at + rank * TR + r, side = DQ ? x.t.nq : x.t.nk;
       if (x.n > 0) {
         wait(&bar.o_full, works & 1);
@@ -1470,7 +1473,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
     const int half = group, r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     int c = 0;  // iterations of all items
-    while (take_item<false>(bar.feed, taken, x, wait, &bar.gave_up)) {
+    while (take_item<false>(bar.feed, taken, x, &bar.gave_up)) {
       const int off = x.t.nk - x.t.nq, at = x.t.at + rank * TR;
       const int first_row = at + (warp & 3) * 32, row = at + r;
       const int xrows = DQ ? x.t.nk : x.t.nq;

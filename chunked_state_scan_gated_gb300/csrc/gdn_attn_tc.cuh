@@ -155,6 +155,15 @@ __device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, int32_t
   }
 }
 
+// For the queue of items: twice the limit, so that whoever is late because of another wait is not given
+// up on, and no regard to *gave_up.  A lane or a warp.
+__device__ __forceinline__ bool wait_alone(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
+  for (int i = 0; i < 2; ++i)
+    if (mbar_wait(bar, parity, nullptr, 0)) return true;
+  *gave_up = 1;
+  return false;
+}
+
 // The load alone; its registers hold nothing before tmem_ld_end() of them.
 __device__ __forceinline__ void tmem_ld_begin(uint32_t taddr, float (&r)[64]) {
   asm volatile(
@@ -241,7 +250,8 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
         "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
-}// 16 consecutive fp32 columns of this thread's TMEM lane (warp-wide), in one load.
+}
+// 16 consecutive fp32 columns of this thread's TMEM lane (warp-wide), in one load.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
   uint32_t r[16];
   asm volatile(

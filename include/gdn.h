@@ -704,7 +704,8 @@ gdn_status gdn_slot_map(const gdn_slot_problem* p, const int32_t* ctx_len,
  *    is neither, and recorded in `status`.
  *  - Rows of q, k, v that belong to no sequence have no influence, whatever they hold; rows of the
  *    outputs that belong to no sequence are left as they were.  (A NaN or infinity in a key or
- *    value row of a sequence may reach the queries of the same sequence that do not see it.)
+ *    value row of a sequence may reach the queries of the same sequence that do not see it; in the
+ *    backward one in a query, o, lse or dO row the keys of its sequence that it does not see.)
  *  - fp32 softmax and sums.  On bf16, p and ds are rounded to bf16 for their products.
  *  - Deterministic: the same bits for the same call.
  *  - Workspace 256-byte aligned (none in most forwards of one sequence, whose size is 0); calls that

@@ -276,6 +276,16 @@ def test_attention_few_new_tokens_behind_a_long_context(D):
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_fp32_divides_keys_and_heads(D):
+    """The same in fp32; and gradients whose key tiles are few, so that their query heads are divided
+    (by 3 and by 5, where no power of two does) and tiles begin anywhere in a block of queries."""
+    check_seq([40, 3, 90], [3000, 9000, 90], 8, 2, D, F32, True, seed=24)
+    check_seq([5], [5000], 4, 4, D, F32, False, seed=25)
+    check_seq([130, 0, 77], [300, 20, 77], 15, 1, D, F32, True, seed=26)
+    check_seq([90, 1], [33, 100], 9, 3, D, F32, True, seed=27)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
 def test_attention_sequences_without_work_among_others(D):
     """Beside one long context, sequences of a few keys and of none: they share a class of work, so
     that a CTA meets tiles without keys between others."""
@@ -682,6 +692,21 @@ def test_decode8_matches_definition(case):
     assert gdn.gdn_check_device_status(word) == gdn.GDN_OK
     again = gdn.gdn_attn_decode8(*inp)
     assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_decode8_fp32_error_on_the_whole(D):
+    """Root mean square over o.  Scores (of about 1): q's two terms 2^-22, at random; sums of 64
+    columns 4 cuts of 2^-24 on average.  Weights: exp 2^-22, two terms 2^-22; o's sums 4 cuts.  In
+    quadrature (sums of cuts in full): sqrt(3 (2^-22)^2 + (2^-22)^2 + (2^-22)^2) < 2^-20."""
+    lens = [517, 131, 9, 300]
+    inp = dec_inputs(lens, 16, 2, D, 16, F32, seed=D + 5, spread=0.5)
+    o, _ = gdn.gdn_attn_decode8(*inp)
+    q, kc, vc, ks, vs, table, n = inp
+    kv, vv = (attention.values(u8(c), np.nan_to_num(n64(s))) for c, s in ((kc, ks), (vc, vs)))
+    ref, _ = decode.attn_decode(n64(q), np.nan_to_num(kv), np.nan_to_num(vv), table.cpu().numpy(),
+                                n.cpu().numpy(), D ** -0.5)
+    assert np.linalg.norm(n64(o) - ref) <= 2.0 ** -20 * np.linalg.norm(ref)
 
 
 @pytest.mark.parametrize("dt", [BF, F32])
