@@ -1244,7 +1244,7 @@ def gdn_attn_fwd(q, k, v, cu_seqlens=None, cu_seqlens_k=None, *, causal=True, sc
     if lse is not None or want_lse:
         lse, lp = _out("lse", lse, dev, torch.float32, q.shape[:-1], q.device, stream)
     wsp, n = None, gdn_attn_fwd_workspace_size(p) if ws is None else ws.numel()
-    if n:  # several sequences by offsets: a list of tiles
+    if n:  # a list of tiles, parts of the keys
         ws, wsp = _out("ws", ws, dev, torch.uint8, (n,), q.device, stream)
     _call("gdn_attn_fwd", dev, p, qp, kp, vp, cup, ckp, op, lp, wsp, n, _status(status, dev),
           _raw_stream(stream, dev))

@@ -8,8 +8,7 @@
 // one writer, no atomics, and sums in a fixed order.
 //
 // fp32: register tiles on CUDA cores, bound by their FMA rate (the split tf32 products of the
-// decode call would need two copies of every operand in shared memory).  Operands are transposed
-// as they enter shared memory, so that a thread's rows are one or two 16-byte reads per step.
+// decode call would need two copies of every operand in shared memory).
 #include <math.h>
 #include <string.h>
 
@@ -184,10 +183,13 @@ __global__ void __launch_bounds__(256) k_attn_rows(SeqArgs a) {
 
 // ----------------------------------------------------------------------- fp32, CUDA cores
 
-// The other side's operands come as chunks of 8 to 10 KB through a ring in shared memory (cp.async, a
-// chunk is about 1000 clocks of products), in two shapes: columns of 64 rows for the products over
-// D, whole rows for those over tokens.  A product over D keeps two sums, of the even and of the odd
-// columns, one over tokens two rows: either way two numbers to an instruction.
+// The other side's operands come as chunks of 18 KB through a ring in shared memory (cp.async), in two
+// shapes: columns of 64 rows for the products over D, whole rows for those over tokens.  A barrier
+// per chunk empties the warps' pipelines, which is why chunks are large (2048 tokens, 16 on 2 heads of
+// 128, forward / gradients: 450 / 1580 us with 9 KB, 387 / 1460 with 18).  A product over D keeps
+// two sums, of the even and of the odd columns, one over tokens two rows: either way two numbers to an
+// instruction.  The FMA pipes are busy 60% of the time, at two warps to a scheduler (registers:
+// accumulators of 128 numbers at D = 256).
 constexpr int ST = 64;  // rows and columns of a tile
 constexpr int LT = 68;  // floats between the columns of the weights: 16-byte aligned
 
@@ -233,7 +235,7 @@ __device__ __forceinline__ void copy_rows(float* dst, const float* src, int64_t 
 }
 
 constexpr int F_HALF = 128, F_NT = 2 * F_HALF, F_STAGES = 3;
-constexpr int F_KC = 32, F_KP = F_KC + 4;  // columns of a chunk of K, floats between its rows
+constexpr int F_KC = 64, F_KP = F_KC + 4;  // columns of a chunk of K, floats between its rows
 constexpr int F_SLOT = ST * F_KP;
 
 template <int D>
@@ -247,12 +249,13 @@ constexpr size_t fwd_smem() {
 
 // 64 queries of one head.  Two halves of the CTA take the blocks of 64 keys in turn, each with a
 // softmax of its own, and are joined at the end: a prompt's last tile, which takes the longest, is
-// done in half the time.  A thread has 8 rows (ty, ty + 8, ..) x 4 keys (tx, tx + 16, ..) of the
+// done in half the time (9 prompts up to 700 tokens, 12 heads of 64: 59 us; one token behind 13,972
+// keys, 16 heads of 128: 65 us).  A thread has 8 rows (ty, ty + 8, ..) x 4 keys (tx, tx + 16, ..) of the
 // scores, 8 rows x D/16 columns of o.
 template <int D>
 __global__ void __launch_bounds__(F_NT) k_attn_fwd_simt(SeqArgs a) {
   extern __shared__ __align__(16) float sm[];
-  constexpr int NV = D / 64, QP = D + 4, NK = D / F_KC, VR = 2048 / D;
+  constexpr int NV = D / 64, QP = D + 4, NK = D / F_KC, VR = ST * F_KC / D;
   const int half = threadIdx.x / F_HALF, tid = threadIdx.x % F_HALF;
   float *Q = sm, *ring = Q + ST * QP + half * fwd_half<D>(), *Pt = ring + F_STAGES * F_SLOT;
   float* ml = sm + ST * QP + 2 * fwd_half<D>();
@@ -335,10 +338,9 @@ __global__ void __launch_bounds__(F_NT) k_attn_fwd_simt(SeqArgs a) {
         for (int j = 0; j < 4; ++j) {
           const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(K + (tx + 16 * j) * F_KP + d);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            fma2(s2[i][j], x[i].x, y.x);
-            fma2(s2[i][j], x[i].y, y.y);
-          }
+          for (int i = 0; i < 8; ++i) fma2(s2[i][j], x[i].x, y.x);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) fma2(s2[i][j], x[i].y, y.y);
         }
       }
     }
@@ -458,17 +460,18 @@ __global__ void __launch_bounds__(F_NT) k_attn_fwd_simt(SeqArgs a) {
 }
 
 constexpr int B_NT = 256;
-constexpr int B_CC = 16, B_CP = B_CC + 4;  // columns of a chunk, floats between its rows
+constexpr int B_CC = 32, B_CP = B_CC + 4;  // columns of a chunk, floats between its rows
 constexpr int B_SLOT = 2 * ST * B_CP;
+constexpr int B_RUN = 16;  // blocks that are summed up at a time
 
-// Chunks on their way or in use: 2 where that lets two CTAs share an SM.
-template <int D, bool KV>
+// Chunks on their way or in use.
+template <bool KV>
 constexpr int bwd_stages() {
-  return D == 128 && !KV ? 2 : 3;
+  return KV ? 3 : 2;
 }
 template <int D, bool KV>
 constexpr size_t bwd_smem() {
-  return (size_t)(2 * ST * (D + 4) + bwd_stages<D, KV>() * B_SLOT + (KV ? 2 : 1) * ST * LT) * 4;
+  return (size_t)(2 * ST * (D + 4) + bwd_stages<KV>() * B_SLOT + (KV ? 2 : 1) * ST * LT) * 4;
 }
 template <int D, bool KV>
 constexpr int bwd_ctas() {
@@ -478,13 +481,16 @@ constexpr int bwd_ctas() {
 // KV: 64 keys of one key head, dk and dv over all queries of its query heads; else 64 queries of
 // one head, dq over the keys that they see.  A thread has 4 rows x 4 columns (tx, tx + 16, ..) of
 // the scores and 4 rows x D/16 columns of each gradient.  The own side's two operands (k, v or q,
-// dO) stay in shared memory.
+// dO) stay in shared memory.  Scores are computed twice, 7 products in place of 5, so that every
+// gradient has one writer (3 rows of 8781 tokens, 2 heads of 128, not causal: 19.4 ms, 42 TFLOP/s
+// of what is executed).
 template <int D, bool KV>
 __global__ void __launch_bounds__(B_NT, bwd_ctas<D, KV>()) k_attn_bwd_simt(SeqArgs a) {
   extern __shared__ __align__(16) float sm[];
-  constexpr int NV = D / 64, NP = KV ? 2 : 1, RP = D + 4, STAGES = bwd_stages<D, KV>();
-  constexpr int C1 = D / B_CC, XR = 2048 / (D * NP);  // chunks of columns; rows of a chunk of rows
-  float *R1 = sm, *R2 = R1 + ST * RP, *ring = R2 + ST * RP, *dS = ring + STAGES * B_SLOT;
+  constexpr int NV = D / 64, NP = KV ? 2 : 1, RP = D + 4, STAGES = bwd_stages<KV>();
+  constexpr int CC = B_CC, CP = B_CP, SLOT = B_SLOT;
+  constexpr int C1 = D / CC, XR = 2 * ST * CC / (D * NP);  // chunks of columns; rows of a chunk of rows
+  float *R1 = sm, *R2 = R1 + ST * RP, *ring = R2 + ST * RP, *dS = ring + STAGES * SLOT;
   float* P = dS + (KV ? ST * LT : 0);
   if (!a.late) after_previous();
   before_next();
@@ -511,10 +517,10 @@ __global__ void __launch_bounds__(B_NT, bwd_ctas<D, KV>()) k_attn_bwd_simt(SeqAr
   auto fetch = [&]() {
     if (fh < h1) {
       const float *x1 = KV ? q_of(fh) : kv_k, *x2 = KV ? do_of(fh) : kv_v;
-      float* to = ring + fs * B_SLOT;
+      float* to = ring + fs * SLOT;
       if (fc < C1) {
-        copy_rows<ST, B_CC, B_CP, B_NT>(to, x1 + fb * s1 + fc * B_CC, s1, end - fb);
-        copy_rows<ST, B_CC, B_CP, B_NT>(to + ST * B_CP, x2 + fb * s2 + fc * B_CC, s2, end - fb);
+        copy_rows<ST, CC, CP, B_NT>(to, x1 + fb * s1 + fc * CC, s1, end - fb);
+        copy_rows<ST, CC, CP, B_NT>(to + ST * CP, x2 + fb * s2 + fc * CC, s2, end - fb);
       } else {
         const int at = fb + (fc - C1) * XR;
         copy_rows<XR, D, D, B_NT>(to, x1 + at * s1, s1, end - at);
@@ -537,7 +543,7 @@ __global__ void __launch_bounds__(B_NT, bwd_ctas<D, KV>()) k_attn_bwd_simt(SeqAr
     copies_wait<STAGES - 2>();
     __syncthreads();
     fetch();
-    const float* x = ring + slot * B_SLOT;
+    const float* x = ring + slot * SLOT;
     slot = slot + 1 == STAGES ? 0 : slot + 1;
     return x;
   };
@@ -548,13 +554,50 @@ __global__ void __launch_bounds__(B_NT, bwd_ctas<D, KV>()) k_attn_bwd_simt(SeqAr
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) fetch();  // the first group holds R1 and R2 too
   f32x2 acc[NP][2][NV][4];                       // rows 2i and 2i + 1 of the thread's
+  auto zero = [&]() {
 #pragma unroll
-  for (int z = 0; z < NP; ++z)
+    for (int z = 0; z < NP; ++z)
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int c = 0; c < NV; ++c)
-        acc[z][i][c][0] = acc[z][i][c][1] = acc[z][i][c][2] = acc[z][i][c][3] = 0;
+        for (int c = 0; c < NV; ++c)
+          acc[z][i][c][0] = acc[z][i][c][1] = acc[z][i][c][2] = acc[z][i][c][3] = 0;
+  };
+  zero();
+  // what has been summed up, to the gradients (or parts of them), in runs of B_RUN blocks: an
+  // accumulator's error grows with its terms (1363 tokens, 8 query heads to a key head: dv 1.4e-6 off in
+  // one run, 8.3e-7 in runs of 16 blocks, in the same time)
+  int blocks = 0;
+  bool begun = false;
+  auto flush = [&]() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (ty * 4 + i >= rows) continue;
+      const int64_t row = (int64_t)((KV ? t.k0 : t.q0) + t.at + ty * 4 + i) * heads + hh;
+#pragma unroll
+      for (int z = 0; z < NP; ++z) {
+        float* to = (float*)(z ? a.dv : KV ? a.dk : a.dq);
+        if (KV && a.splits > 1) to = (z ? a.part_v : a.part_k) + part * a.Nk * a.Hk * D;
+        to += row * D + tx * 4;
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+          float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (begun) sum = *reinterpret_cast<const float4*>(to + c * 64);
+          float x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 y = parts_of(acc[z][i / 2][c][e]);
+            x[e] = (i % 2 ? y.y : y.x) * (z ? 1.f : a.scale);
+          }
+          *reinterpret_cast<float4*>(to + c * 64) =
+              make_float4(sum.x + x[0], sum.y + x[1], sum.z + x[2], sum.w + x[3]);
+        }
+      }
+    }
+    zero();
+    blocks = 0;
+    begun = true;
+  };
   for (int h = h0; h < h1; ++h) {
     const float* lse = a.lse2 + (int64_t)h * a.Nq + t.q0;
     const float* delta = a.delta + (int64_t)h * a.Nq + t.q0;
@@ -573,8 +616,8 @@ __global__ void __launch_bounds__(B_NT, bwd_ctas<D, KV>()) k_attn_bwd_simt(SeqAr
 #pragma unroll
         for (int z = 0; z < 2; ++z)
 #pragma unroll
-          for (int d = 0; d < B_CC; d += 4) {
-            const float* own = (z ? R2 : R1) + ty * 4 * RP + c * B_CC + d;
+          for (int d = 0; d < CC; d += 4) {
+            const float* own = (z ? R2 : R1) + ty * 4 * RP + c * CC + d;
             ulonglong2 r[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -582,12 +625,11 @@ __global__ void __launch_bounds__(B_NT, bwd_ctas<D, KV>()) k_attn_bwd_simt(SeqAr
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(
-                  x + z * ST * B_CP + (tx + 16 * j) * B_CP + d);
+                  x + z * ST * CP + (tx + 16 * j) * CP + d);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                fma2((z ? dp : s)[i][j], r[i].x, y.x);
-                fma2((z ? dp : s)[i][j], r[i].y, y.y);
-              }
+              for (int i = 0; i < 4; ++i) fma2((z ? dp : s)[i][j], r[i].x, y.x);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) fma2((z ? dp : s)[i][j], r[i].y, y.y);
             }
           }
       }
@@ -633,28 +675,10 @@ __global__ void __launch_bounds__(B_NT, bwd_ctas<D, KV>()) k_attn_bwd_simt(SeqAr
             }
           }
       }
+      if (++blocks == B_RUN) flush();
     }
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (ty * 4 + i >= rows) continue;
-    const int64_t row = (int64_t)((KV ? t.k0 : t.q0) + t.at + ty * 4 + i) * heads + hh;
-#pragma unroll
-    for (int z = 0; z < NP; ++z)
-#pragma unroll
-      for (int c = 0; c < NV; ++c) {
-        float x[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 y = parts_of(acc[z][i / 2][c][e]);
-          x[e] = (i % 2 ? y.y : y.x) * (z ? 1.f : a.scale);
-        }
-        float* to = (float*)(z ? a.dv : KV ? a.dk : a.dq);
-        if (KV && a.splits > 1) to = (z ? a.part_v : a.part_k) + part * a.Nk * a.Hk * D;
-        to += row * D + c * 64 + tx * 4;
-        *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
-      }
-  }
+  if (blocks > 0 || !begun) flush();
   if (a.late) after_previous();
 }
 
