@@ -158,8 +158,21 @@ __device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, int32_t
 // For the queue of items: twice the limit, so that whoever is late because of another wait is not given
 // up on, and no regard to *gave_up.  A lane or a warp.
 __device__ __forceinline__ bool wait_alone(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
-  for (int i = 0; i < 2; ++i)
-    if (mbar_wait(bar, parity, nullptr, 0)) return true;
+  const uint32_t addr = smem_u32(bar);
+  uint64_t t0 = 0;
+  while (true) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(addr), "r"(parity)
+        : "memory");
+    if (done) return true;
+    const uint64_t now = global_timer();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > 2 * kWaitLimitNs) break;
+  }
   *gave_up = 1;
   return false;
 }
