@@ -1,5 +1,5 @@
 // gdn_attn_seq.cu -- attention of packed sequences and its gradients: the calls, their schedule,
-// and the fp32 kernels (the bf16 ones are in gdn_attn_seq_tc.cu).
+// and the fp32 kernels (the bf16 ones, and those that join parts, are in gdn_attn_seq_tc.cu).
 //
 // Forward, per query row: s_j = scale q.k_j, one pass over the keys with the running maximum m and
 // sum l of a softmax, o = sum_j exp(s_j - m) v_j / l, lse = m + log l.  Backward, from lse and
@@ -743,10 +743,12 @@ Layout layout(const gdn_attn_seq_problem* p, bool bwd, int rq, int rk) {
   const size_t part = y.splits > 1 ? up((size_t)y.splits * p->Nk * p->Hk * p->D * 4) : 0;
   y.part_v = y.part_k + part;
   y.part_o = y.part_v + part;
-  // bf16 forward: tiles for less than one wave over many keys (a few new tokens behind a long
-  // context) leave SMs idle, so the keys of every tile are divided, 512 at least to a part on average;
-  // the parts of o are fp32 and k_attn_merge joins them (64 tokens behind 31936, 32 on 8 heads of 128:
-  // 338 us without, 80 with; 256 tiles of 9 sequences behind up to 16000 tokens: 308 and 330).
+  // Forward: tiles for less than one wave over many keys (a few new tokens behind a long context)
+  // leave SMs idle, so the keys of every tile are divided, 512 (fp32: 256) at least to a part on
+  // average; the parts of o are fp32 and k_attn_merge joins them (bf16, 32 on 8 heads of 128: 64 tokens
+  // behind 31936 338 us without, 53 with; with more tiles they cost more than they bring: 256 tiles of 9
+  // sequences behind up to 16000 tokens 335 without, 348 in two parts, 4096 tokens 104 and 193.  fp32:
+  // one token behind 13,972 keys, 16 heads of 128, 507 and 65).
   y.parts = 1;
   const int64_t items = (int64_t)y.mq * (p->Hq / (bf16 ? tc_pack(G) : 1));
   if (!bwd && items > 0) {

@@ -1,22 +1,26 @@
 // gdn_attn_seq_tc.cu -- the bf16 kernels of gdn_attn_fwd and gdn_attn_bwd, on tcgen05.
 //
-// Two kernels serve both directions.  A CTA keeps tiles of 128 rows of its own side in shared
-// memory (the M of every product) and streams blocks of the other side through a ring by TMA:
+// A CTA (k_slope_pair: a pair) keeps tiles of 128 rows of its own side in shared memory (the M of every
+// product) and streams blocks of 128 rows of the other side through a ring by TMA:
 //   k_flash: S = R X1^T;  P = f(S);  acc += P X2
 //     forward: R = queries, X1 = keys, X2 = values, P = exp2(S sl - m), with the row's running
-//     maximum and sum;  dv: R = keys, X1 = queries, X2 = dO, P = exp2(S sl - lse2)
-//   k_slope: S = R1 X1^T;  dP = R2 X2^T;  dS = P (dP - delta);  acc += dS X1 (and acc' += P X2)
-//     dq: R = queries, dO, X = keys, values;  dk (and dv): R = keys, values, X = queries, dO
+//     maximum and sum;  dv (D = 256): R = keys, X1 = queries, X2 = dO, P = exp2(S sl - lse2)
+//   k_slope (D <= 128), k_slope_pair (D = 256): S = R1 X1^T;  dP = R2 X2^T;  dS = P (dP - delta);
+//     acc += dS X1 (and acc' += P X2)
+//     dq: R = queries, dO, X = keys, values;  dk (D <= 128: and dv): R = keys, values, X = queries, dO
 // The gradients of a row have one writer: no atomics, the same bits every time.
 //
 // S, dP and the accumulators are in TMEM; P (dS) goes back as bf16 over the columns of its S and is
 // the A operand of the last product from there, so that the weights never pass through shared
 // memory.  X1 and X2 are K-major for S and dP and MN-major for the accumulation: one copy serves
-// both.  One thread issues all products, one all copies; the other warps do the softmax, a thread
-// per row.
+// both (the pair's halves differ between the two, so X1 comes twice there).  One thread issues all
+// products, one all copies, one warp finds the next items, four write results; eight do the softmax, a
+// thread per row or half of one.
 //
-// Bound by the tensor cores; the weights' bf16 rounding (2^-9 of a weight, as much as o's own
-// rounding adds) is what lets the last product run at their full rate.
+// Bound by the tensor cores and, in long calls, by the chip's power (16384 tokens, 32 heads on 8 of 128,
+// causal: forward 1.28 ms = 1.71 PFLOP/s, backward 4.76 ms; 16 on 2 of 256: 1.32 and 6.06); the weights'
+// bf16 rounding (2^-9 of a weight, as much as o's own rounding adds) is what lets the last product run
+// at their full rate.
 #include <cuda.h>
 #include <cuda_bf16.h>
 
