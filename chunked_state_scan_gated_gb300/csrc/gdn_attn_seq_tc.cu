@@ -123,19 +123,37 @@ __device__ inline void drain(Bars& bar, int works, int stages, int stage, int tu
       mbar_wait(&bar.full[i], (i < stage ? turn : turn - 1) & 1, nullptr, 0);
 }
 
-// 32 columns of an output row, times f, as bf16 or (a part of dk or dv) as fp32.
+__device__ __forceinline__ void store32(void* dst, const uint32_t (&w)[8]) {  // 32-byte aligned
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(w[0]), "r"(w[1]),
+               "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+// 32 columns of an output row, times f, as bf16 or (a part of o, dk or dv) as fp32.  A thread's row is
+// far from its neighbour's, so that a store fills a sector of 32 bytes or half of one: by 32 bytes where
+// the output's alignment allows it (64 prompts of 250 tokens, 32 on 8 heads: D = 128 forward 99 and 95
+// us, D = 256 backward 666 and 645).  Parts are always aligned to 32.
 __device__ __forceinline__ void write_row(__nv_bfloat16* dst, const float (&y)[32], float f) {
 #pragma unroll
-  for (int e = 0; e < 32; e += 8)
-    *reinterpret_cast<uint4*>(dst + e) =
-        make_uint4(bf16x2(y[e] * f, y[e + 1] * f), bf16x2(y[e + 2] * f, y[e + 3] * f),
-                   bf16x2(y[e + 4] * f, y[e + 5] * f), bf16x2(y[e + 6] * f, y[e + 7] * f));
+  for (int e = 0; e < 32; e += 16) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = bf16x2(y[e + 2 * i] * f, y[e + 2 * i + 1] * f);
+    if (((uintptr_t)dst & 31) == 0) {
+      store32(dst + e, w);
+    } else {
+      *reinterpret_cast<uint4*>(dst + e) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(dst + e + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  }
 }
 __device__ __forceinline__ void write_row(float* dst, const float (&y)[32], float f) {
 #pragma unroll
-  for (int e = 0; e < 32; e += 4)
-    *reinterpret_cast<float4*>(dst + e) =
-        make_float4(y[e] * f, y[e + 1] * f, y[e + 2] * f, y[e + 3] * f);
+  for (int e = 0; e < 32; e += 8) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(y[e + i] * f);
+    store32(dst + e, w);
+  }
 }
 // Columns c .. c + 31 of row `row` (of all key rows) of dk (dv: second), of the query heads from
 // `head` on.

@@ -317,6 +317,28 @@ def test_attention_rows_far_apart(dt, D):
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_outputs_aligned_to_16_bytes(D):
+    """Outputs that begin in the middle of 32 bytes get the bits that others get, and nothing beside
+    them is written."""
+    q, k, v, cu, ck = seq_inputs([40, 300, 7], [90, 300, 7], 4, 2, D, BF, 31)
+    cuq, cuk = i32(cu), i32(ck)
+    dO = rand(torch.Generator().manual_seed(32), q.shape, BF)
+    o, lse = gdn.gdn_attn_fwd(q, k, v, cuq, cuk, o=torch.full_like(q, 7.0))
+    base = [torch.full_like(x, 7.0) for x in (q, k, k)]
+    gdn.gdn_attn_bwd(q, k, v, o, lse, dO, cuq, cuk, dq=base[0], dk=base[1], dv=base[2])
+    odd = []
+    for x in (q, q, k, k):
+        flat = torch.full((x.numel() + 16,), 7.0, dtype=BF, device="cuda")
+        odd.append((flat, flat[8:8 + x.numel()].view(x.shape)))
+        assert odd[-1][1].data_ptr() % 32 == 16
+    gdn.gdn_attn_fwd(q, k, v, cuq, cuk, o=odd[0][1])
+    gdn.gdn_attn_bwd(q, k, v, o, lse, dO, cuq, cuk, dq=odd[1][1], dk=odd[2][1], dv=odd[3][1])
+    for (flat, x), want in zip(odd, [o] + base):
+        assert torch.equal(x, want)
+        assert (flat[:8] == 7).all() and (flat[-8:] == 7).all()
+
+
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("n_seqs", [1, 3])
 def test_attention_offsets_out_of_order_are_cut(dt, n_seqs):
