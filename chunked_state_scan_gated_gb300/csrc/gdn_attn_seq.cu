@@ -733,14 +733,14 @@ Layout layout(const gdn_attn_seq_problem* p, bool bwd, int rq, int rk) {
   y.lse2 = lists && bwd ? up(y.lk + y.mk * sizeof(Tile)) : y.lk;
   y.delta = y.lse2 + (bwd ? up((size_t)p->Nq * p->Hq * 4) : 0);
   y.part_k = y.delta + (bwd ? up((size_t)p->Nq * p->Hq * 4) : 0);
-  // A key tile's query heads go to several CTAs where there are fewer tiles than 4 per SM (fp32: 2, its
-  // tiles are smaller); each writes a part of dk and dv in fp32, which k_attn_sum adds up (16001 tokens,
-  // 16 on 2 heads of 256, bf16: one part 7.9 ms, 8: 6.0; the parts cost 16 bytes per element and part).
+  // A key tile's query heads go to several CTAs where there are fewer tiles than 4 per SM; each writes a
+  // part of dk and dv in fp32, which k_attn_sum adds up (bf16, 16001 tokens, 16 on 2 heads of 256: one
+  // part 7.9 ms, 8: 6.0; the parts cost 16 bytes per element and part).
   y.splits = 1;
   const bool bf16 = p->dtype == GDN_BF16;
   const int64_t G = p->Hq / p->Hk, tiles = (int64_t)y.mk * p->Hk * (bf16 ? rk / 128 : 1);
   if (bwd && tiles > 0)
-    for (int64_t s = 2; s <= G && tiles * y.splits < (bf16 ? 608 : 304); ++s)
+    for (int64_t s = 2; s <= G && tiles * y.splits < 608; ++s)
       if (G % s == 0) y.splits = (int)s;
   const size_t part = y.splits > 1 ? up((size_t)y.splits * p->Nk * p->Hk * p->D * 4) : 0;
   y.part_v = y.part_k + part;
