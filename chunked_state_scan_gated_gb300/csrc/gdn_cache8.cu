@@ -26,6 +26,7 @@ constexpr int C8_NT = 256;
 constexpr int C8_W = C8_NT / 32;
 constexpr int C8_ROWS = 16;   // packed token rows of a CTA
 constexpr int C8_BLOCK = 16;  // tokens that share a scale
+constexpr int C8_MANY = 4096, C8_CTAS = 608;  // requests beyond which there are so many CTAs at most
 
 struct Cache8Args {
   int64_t N, B, pages, max_blocks, ks, vs;
@@ -52,28 +53,55 @@ __device__ __forceinline__ int64_t request_of(const int32_t* cu, int64_t B, int6
   }
 }
 
-// Where the CTA's token rows are: request, position in it, end of its packed rows (0: none).
+// The same where offsets may be anything: they count as cut to [0, N] and raised to the largest before
+// them, so the request is the one in front of the first that is above t; from the first offset on.
+__device__ __forceinline__ int64_t request_through(const Cache8Args& ar, int64_t t, int64_t* first,
+                                                   int64_t* end) {
+  const int lane = threadIdx.x & 31, n = (int)ar.N;
+  int top = 0;
+  for (int64_t i0 = 0; i0 <= ar.B; i0 += 32) {
+    const int64_t i = i0 + lane;
+    const int c = i <= ar.B ? max(0, min(ar.cu[i], n)) : 0;
+    const unsigned over = __ballot_sync(0xffffffffu, c > t);
+    const int k = over ? __ffs(over) - 1 : 32;
+    top = max(top, __reduce_max_sync(0xffffffffu, lane < k ? c : 0));
+    if (over) {
+      *first = top;
+      *end = __shfl_sync(0xffffffffu, c, k);
+      return i0 + k - 1;
+    }
+  }
+  return -1;
+}
+
+// Where 16 token rows are: request, position in it, end of its packed rows (0: none).
 struct Rows {
+  int64_t t0;   // the first
+  int ordered;  // whether the offsets are in order
   int64_t pos[C8_ROWS];
   int32_t b[C8_ROWS], end[C8_ROWS];
   int32_t lead[C8_ROWS];
 };
 
-template <bool WRITE>
-__device__ __forceinline__ void find_rows(const Cache8Args& ar, Rows* r, int* bad) {
+// ORDERED: the offsets are in order and within the rows.
+template <bool WRITE, bool ORDERED>
+__device__ __forceinline__ void find_rows(const Cache8Args& ar, int64_t t0, Rows* r) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int i = 0; i < C8_ROWS / C8_W; ++i) {
     const int slot = warp + i * C8_W;
-    const int64_t t = (int64_t)blockIdx.x * C8_ROWS + slot;
-    const int64_t b = t < ar.N ? request_of(ar.cu, ar.B, t) : -1;
-    int64_t first = 0, end = 0, ctx = 0;
+    const int64_t t = t0 + slot;
+    int64_t b = -1, first = 0, end = 0, ctx = 0;
+    if (t < ar.N) b = ORDERED ? request_of(ar.cu, ar.B, t) : request_through(ar, t, &first, &end);
     if (b >= 0) {
-      first = ar.cu[b];
-      end = min((int64_t)ar.cu[b + 1], ar.N);
+      if (ORDERED) {
+        first = ar.cu[b];
+        end = ar.cu[b + 1];
+      }
       if (WRITE) ctx = max(ar.ctx[b], 0);
-      // an offset below zero (an invalid one) gives no position
-      if (first < 0 || end <= t) end = 0;
+      if (end <= t) end = 0;
+    } else {
+      end = 0;
     }
     if (lane == 0) {
       r->b[slot] = (int32_t)b;
@@ -82,11 +110,44 @@ __device__ __forceinline__ void find_rows(const Cache8Args& ar, Rows* r, int* ba
       r->lead[slot] = end > 0 && (t == first || (ctx + t - first) % C8_BLOCK == 0);
     }
   }
-  if (blockIdx.x == 0 && blockIdx.y == 0)
-    for (int64_t b = threadIdx.x; b <= ar.B; b += C8_NT) {
-      const int64_t c = ar.cu[b], before = b > 0 ? ar.cu[b - 1] : 0;
-      if (c < before || c > ar.N || (WRITE && b < ar.B && ar.ctx[b] < 0)) *bad = 1;
-    }
+}
+
+// A CTA's first rows.  Only all offsets together tell whether they are in order, and no launch before
+// this one looks at them: every CTA does, while its rows are searched for as if they were (37 requests
+// of 500 to 4000 tokens, bf16: written 105.5 us without that, 106.9 with it at 8 heads of 128, 65 and 68
+// at 2 of 256; read back the same; 250 tokens 4.9 and 5.1).
+template <bool WRITE>
+__device__ __forceinline__ void find_first_rows(const Cache8Args& ar, Rows* r, int* bad) {
+  const int64_t t0 = (int64_t)blockIdx.x * C8_ROWS, b0 = threadIdx.x;
+  const int32_t c0 = b0 < ar.B ? ar.cu[b0] : 0, c1 = b0 < ar.B ? ar.cu[b0 + 1] : 0;
+  find_rows<WRITE, true>(ar, t0, r);
+  int out = c0 < 0 || c0 > ar.N || c1 < c0;
+#pragma unroll 8
+  for (int b = (int)b0 + C8_NT; b < (int)ar.B; b += C8_NT) {
+    const int32_t x = ar.cu[b], y = ar.cu[b + 1];
+    out |= x < 0 || x > (int)ar.N || y < x;
+  }
+  if (b0 == 0) out |= ar.cu[ar.B] > ar.N;
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    *bad = out;
+    if (WRITE)
+      for (int64_t b = b0; b < ar.B; b += C8_NT) *bad |= ar.ctx[b] < 0;
+  }
+  if (threadIdx.x == 0) r->t0 = t0;
+  out = __syncthreads_or(out);
+  if (threadIdx.x == 0) r->ordered = !out;
+  if (out) {
+    find_rows<WRITE, false>(ar, t0, r);
+    __syncthreads();
+  }
+}
+template <bool WRITE>
+__device__ __forceinline__ void find_more_rows(const Cache8Args& ar, Rows* r) {
+  const int64_t t0 = r->t0 + (int64_t)gridDim.x * C8_ROWS;
+  __syncthreads();  // the rows before are done
+  if (threadIdx.x == 0) r->t0 = t0;
+  if (r->ordered) find_rows<WRITE, true>(ar, t0, r);
+  else find_rows<WRITE, false>(ar, t0, r);
   __syncthreads();
 }
 
@@ -153,7 +214,7 @@ constexpr int write_ctas() {
   return x <= 16 ? 5 : x <= 32 ? 4 : x <= 64 ? 3 : 1;
 }
 
-template <int D, typename T>
+template <int D, typename T, bool MANY>
 __global__ void __launch_bounds__(C8_NT, write_ctas<D, T>()) k_cache_write8(Cache8Args ar) {
   constexpr int EL = 16 / (int)sizeof(T);       // elements of a load
   constexpr int LR = D / EL;                    // loads of a row
@@ -164,105 +225,109 @@ __global__ void __launch_bounds__(C8_NT, write_ctas<D, T>()) k_cache_write8(Cach
   after_previous();
   before_next();
   int bad = 0;
-  find_rows<true>(ar, &rows, &bad);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const unsigned leads = __ballot_sync(0xffffffffu, lane < C8_ROWS && rows.lead[lane & 15]);
-  const int per = 2 * ar.Hk, units = __popc(leads) * per;
-  for (int u = blockIdx.y * C8_W + warp; u < units; u += gridDim.y * C8_W) {
-    const int slot = __fns(leads, 0, u / per + 1), h = (u % per) >> 1;
-    const bool isv = u & 1;
-    const int64_t t0 = (int64_t)blockIdx.x * C8_ROWS + slot, pos = rows.pos[slot];
-    const int in = (int)(pos % C8_BLOCK);  // earlier tokens of the block
-    const int n = min(C8_BLOCK - in, (int)(rows.end[slot] - t0));
-    const int64_t row = cache_row(ar, rows.b[slot], pos);
-    if (row < 0) {
-      bad = 1;
-      continue;
-    }
-    const int64_t ts = isv ? ar.vs : ar.ks;
-    const T* src = reinterpret_cast<const T*>(isv ? ar.v : ar.k) + t0 * ts + (int64_t)h * D;
-    float* sc = (isv ? ar.vsc : ar.ksc) + (row / C8_BLOCK) * ar.Hk + h;
-    uint8_t* dst = (isv ? ar.vc : ar.kc) + (row * ar.Hk + h) * (int64_t)D;  // the first new row
-    const int64_t dr = (int64_t)ar.Hk * D;
-    const int r0 = LR >= 32 ? 0 : lane / LR, c0 = LR >= 32 ? lane : lane % LR;
-    uint4 x[NIT][CPL];
-#pragma unroll
-    for (int i = 0; i < NIT; ++i)
-#pragma unroll
-      for (int c = 0; c < CPL; ++c) {
-        x[i][c] = make_uint4(0, 0, 0, 0);
-        if (i * RPI + r0 < n)
-          x[i][c] = *reinterpret_cast<const uint4*>(src + (i * RPI + r0) * ts +
-                                                    (c0 + c * 32) * EL);
+  find_first_rows<true>(ar, &rows, &bad);
+  while (true) {  // MANY: several runs of rows
+    const unsigned leads = __ballot_sync(0xffffffffu, lane < C8_ROWS && rows.lead[lane & 15]);
+    const int per = 2 * ar.Hk, units = __popc(leads) * per;
+    for (int u = blockIdx.y * C8_W + warp; u < units; u += gridDim.y * C8_W) {
+      const int slot = __fns(leads, 0, u / per + 1), h = (u % per) >> 1;
+      const bool isv = u & 1;
+      const int64_t t0 = rows.t0 + slot, pos = rows.pos[slot];
+      const int in = (int)(pos % C8_BLOCK);  // earlier tokens of the block
+      const int n = min(C8_BLOCK - in, (int)(rows.end[slot] - t0));
+      const int64_t row = cache_row(ar, rows.b[slot], pos);
+      if (row < 0) {
+        bad = 1;
+        continue;
       }
-    const float before = in > 0 ? *sc : 0.f;
-    uint32_t bits = 0;
-#pragma unroll
-    for (int i = 0; i < NIT; ++i)
-#pragma unroll
-      for (int c = 0; c < CPL; ++c) bits = top_bits<T>(bits, x[i][c]);
-    if (sizeof(T) == 2) bits = max(bits << 16, bits & 0xffff0000u);
-    bits = __reduce_max_sync(0xffffffffu, bits);
-    const bool finite = bits < 0x7f800000u;  // uniform in the warp
-    float top = __uint_as_float(bits);
-    if (!finite) {
-      top = 0.f;
+      const int64_t ts = isv ? ar.vs : ar.ks;
+      const T* src = reinterpret_cast<const T*>(isv ? ar.v : ar.k) + t0 * ts + (int64_t)h * D;
+      float* sc = (isv ? ar.vsc : ar.ksc) + (row / C8_BLOCK) * ar.Hk + h;
+      uint8_t* dst = (isv ? ar.vc : ar.kc) + (row * ar.Hk + h) * (int64_t)D;  // the first new row
+      const int64_t dr = (int64_t)ar.Hk * D;
+      const int r0 = LR >= 32 ? 0 : lane / LR, c0 = LR >= 32 ? lane : lane % LR;
+      uint4 x[NIT][CPL];
 #pragma unroll
       for (int i = 0; i < NIT; ++i)
 #pragma unroll
-        for (int c = 0; c < CPL; ++c)
-#pragma unroll
-          for (int e = 0; e < EL; ++e) {
-            const float y = fabsf(element<T>(x[i][c], e));
-            top = fmaxf(top, y < INFINITY ? y : 0.f);
-          }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    }
-    const float s = fmaxf(scale_for(top), before), inv = 1.f / s;  // powers of two: exact
-    if (in > 0 && s != before) {
-      // the earlier tokens' codes at the new scale, 16 bytes at a time
-      const float f = before * inv;
-      for (int j = lane; j < in * (D / 16); j += 32) {
-        uint4* at = reinterpret_cast<uint4*>(dst - (in - j / (D / 16)) * dr + j % (D / 16) * 16);
-        uint4 v = *at;
-        uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 a = values2(w[i] & 0xffffu), b = values2(w[i] >> 16);
-          w[i] = codes2<false>(a.x * f, a.y * f) | codes2<false>(b.x * f, b.y * f) << 16;
+        for (int c = 0; c < CPL; ++c) {
+          x[i][c] = make_uint4(0, 0, 0, 0);
+          if (i * RPI + r0 < n)
+            x[i][c] = *reinterpret_cast<const uint4*>(src + (i * RPI + r0) * ts +
+                                                      (c0 + c * 32) * EL);
         }
-        *at = v;
-      }
-    }
-    auto store = [&](auto fin) {
-      constexpr bool kFin = decltype(fin)::value;
+      const float before = in > 0 ? *sc : 0.f;
+      uint32_t bits = 0;
 #pragma unroll
       for (int i = 0; i < NIT; ++i)
-        if (i * RPI + r0 < n)
 #pragma unroll
-          for (int c = 0; c < CPL; ++c) {
-            uint32_t w[EL / 4];
+        for (int c = 0; c < CPL; ++c) bits = top_bits<T>(bits, x[i][c]);
+      if (sizeof(T) == 2) bits = max(bits << 16, bits & 0xffff0000u);
+      bits = __reduce_max_sync(0xffffffffu, bits);
+      const bool finite = bits < 0x7f800000u;  // uniform in the warp
+      float top = __uint_as_float(bits);
+      if (!finite) {
+        top = 0.f;
 #pragma unroll
-            for (int e = 0; e < EL; e += 4) {
-              const uint4& v = x[i][c];
-              w[e / 4] =
-                  codes2<kFin>(element<T>(v, e) * inv, element<T>(v, e + 1) * inv) |
-                  codes2<kFin>(element<T>(v, e + 2) * inv, element<T>(v, e + 3) * inv) << 16;
+        for (int i = 0; i < NIT; ++i)
+#pragma unroll
+          for (int c = 0; c < CPL; ++c)
+#pragma unroll
+            for (int e = 0; e < EL; ++e) {
+              const float y = fabsf(element<T>(x[i][c], e));
+              top = fmaxf(top, y < INFINITY ? y : 0.f);
             }
-            uint8_t* at = dst + (i * RPI + r0) * dr + (c0 + c * 32) * EL;
-            if constexpr (EL == 8) *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
-            else *reinterpret_cast<uint32_t*>(at) = w[0];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      }
+      const float s = fmaxf(scale_for(top), before), inv = 1.f / s;  // powers of two: exact
+      if (in > 0 && s != before) {
+        // the earlier tokens' codes at the new scale, 16 bytes at a time
+        const float f = before * inv;
+        for (int j = lane; j < in * (D / 16); j += 32) {
+          uint4* at = reinterpret_cast<uint4*>(dst - (in - j / (D / 16)) * dr + j % (D / 16) * 16);
+          uint4 v = *at;
+          uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 a = values2(w[i] & 0xffffu), b = values2(w[i] >> 16);
+            w[i] = codes2<false>(a.x * f, a.y * f) | codes2<false>(b.x * f, b.y * f) << 16;
           }
-    };
-    if (finite) store(std::true_type());
-    else store(std::false_type());
-    if (lane == 0) *sc = s;
+          *at = v;
+        }
+      }
+      auto store = [&](auto fin) {
+        constexpr bool kFin = decltype(fin)::value;
+#pragma unroll
+        for (int i = 0; i < NIT; ++i)
+          if (i * RPI + r0 < n)
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) {
+              uint32_t w[EL / 4];
+#pragma unroll
+              for (int e = 0; e < EL; e += 4) {
+                const uint4& v = x[i][c];
+                w[e / 4] =
+                    codes2<kFin>(element<T>(v, e) * inv, element<T>(v, e + 1) * inv) |
+                    codes2<kFin>(element<T>(v, e + 2) * inv, element<T>(v, e + 3) * inv) << 16;
+              }
+              uint8_t* at = dst + (i * RPI + r0) * dr + (c0 + c * 32) * EL;
+              if constexpr (EL == 8) *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+              else *reinterpret_cast<uint32_t*>(at) = w[0];
+            }
+      };
+      if (finite) store(std::true_type());
+      else store(std::false_type());
+      if (lane == 0) *sc = s;
+    }
+    if (!MANY || rows.t0 + (int64_t)gridDim.x * C8_ROWS >= ar.N) break;
+    find_more_rows<true>(ar, &rows);
   }
   if (bad && ar.status) atomicOr(ar.status, kStatusClamped);
 }
 
-template <int D, typename T>
+template <int D, typename T, bool MANY>
 __global__ void __launch_bounds__(C8_NT) k_cache_read8(Cache8Args ar) {
   constexpr int CH = D / 16;  // 16-byte loads of a head's row
   __shared__ Rows rows;
@@ -270,56 +335,60 @@ __global__ void __launch_bounds__(C8_NT) k_cache_read8(Cache8Args ar) {
   after_previous();
   before_next();
   int bad = 0;
-  find_rows<false>(ar, &rows, &bad);
-  if (threadIdx.x < C8_ROWS) {
-    int64_t r = -2;  // no token
-    if (rows.end[threadIdx.x] > 0) {
-      r = cache_row(ar, rows.b[threadIdx.x], rows.pos[threadIdx.x]);
-      if (r < 0) bad = 1;
-    }
-    at[threadIdx.x] = r;
-  }
-  __syncthreads();
-  const int per = ar.Hk * CH, all = C8_ROWS * per * 2;
-#pragma unroll 4
-  for (int i = blockIdx.y * C8_NT + threadIdx.x; i < all; i += gridDim.y * C8_NT) {
-    const int slot = i / (2 * per), j = i % (2 * per);
-    const bool isv = j >= per;
-    const int c = isv ? j - per : j;
-    const int64_t r = at[slot];
-    if (r == -2) continue;
-    T* out = reinterpret_cast<T*>(isv ? ar.vo : ar.ko) +
-             (((int64_t)blockIdx.x * C8_ROWS + slot) * per + c) * 16;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    float s = 0.f;
-    if (r >= 0) {
-      v = *reinterpret_cast<const uint4*>((isv ? ar.vc : ar.kc) + (r * per + c) * 16);
-      s = (isv ? ar.vsc : ar.ksc)[(r / C8_BLOCK) * ar.Hk + c / CH];
-    }
-    float x[16];
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const float2 a = values2(word(v, w) & 0xffffu), b = values2(word(v, w) >> 16);
-      x[4 * w] = a.x * s;
-      x[4 * w + 1] = a.y * s;
-      x[4 * w + 2] = b.x * s;
-      x[4 * w + 3] = b.y * s;
-    }
-    if constexpr (sizeof(T) == 2) {
-      uint32_t y[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const __nv_bfloat162 z = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
-        y[e] = *reinterpret_cast<const uint32_t*>(&z);
+  find_first_rows<false>(ar, &rows, &bad);
+  while (true) {
+    if (threadIdx.x < C8_ROWS) {
+      int64_t r = -2;  // no token
+      if (rows.end[threadIdx.x] > 0) {
+        r = cache_row(ar, rows.b[threadIdx.x], rows.pos[threadIdx.x]);
+        if (r < 0) bad = 1;
       }
-      reinterpret_cast<uint4*>(out)[0] = make_uint4(y[0], y[1], y[2], y[3]);
-      reinterpret_cast<uint4*>(out)[1] = make_uint4(y[4], y[5], y[6], y[7]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        reinterpret_cast<float4*>(out)[e] =
-            make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+      at[threadIdx.x] = r;
     }
+    __syncthreads();
+    const int per = ar.Hk * CH, all = C8_ROWS * per * 2;
+#pragma unroll 4
+    for (int i = blockIdx.y * C8_NT + threadIdx.x; i < all; i += gridDim.y * C8_NT) {
+      const int slot = i / (2 * per), j = i % (2 * per);
+      const bool isv = j >= per;
+      const int c = isv ? j - per : j;
+      const int64_t r = at[slot];
+      if (r == -2) continue;
+      T* out = reinterpret_cast<T*>(isv ? ar.vo : ar.ko) +
+               ((rows.t0 + slot) * per + c) * 16;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      float s = 0.f;
+      if (r >= 0) {
+        v = *reinterpret_cast<const uint4*>((isv ? ar.vc : ar.kc) + (r * per + c) * 16);
+        s = (isv ? ar.vsc : ar.ksc)[(r / C8_BLOCK) * ar.Hk + c / CH];
+      }
+      float x[16];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float2 a = values2(word(v, w) & 0xffffu), b = values2(word(v, w) >> 16);
+        x[4 * w] = a.x * s;
+        x[4 * w + 1] = a.y * s;
+        x[4 * w + 2] = b.x * s;
+        x[4 * w + 3] = b.y * s;
+      }
+      if constexpr (sizeof(T) == 2) {
+        uint32_t y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const __nv_bfloat162 z = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+          y[e] = *reinterpret_cast<const uint32_t*>(&z);
+        }
+        reinterpret_cast<uint4*>(out)[0] = make_uint4(y[0], y[1], y[2], y[3]);
+        reinterpret_cast<uint4*>(out)[1] = make_uint4(y[4], y[5], y[6], y[7]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          reinterpret_cast<float4*>(out)[e] =
+              make_float4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+      }
+    }
+    if (!MANY || rows.t0 + (int64_t)gridDim.x * C8_ROWS >= ar.N) break;
+    find_more_rows<false>(ar, &rows);
   }
   if (bad && ar.status) atomicOr(ar.status, kStatusClamped);
 }
@@ -354,15 +423,21 @@ gdn_status check(const gdn_cache8_problem* p, const void* k, const void* v, cons
   return GDN_OK;
 }
 
-template <template <int, typename> class K>
+template <template <int, typename, bool> class K>
 cudaError_t run(const gdn_cache8_problem* p, const Cache8Args& ar, int items, cudaStream_t st) {
-  // CTAs along the rows; few rows (a decode step): the heads of a CTA's rows go to several
-  const int64_t x = (p->N + C8_ROWS - 1) / C8_ROWS;
+  // CTAs along the rows; with very many requests so few that all of them reading all offsets costs
+  // little, each for several runs of rows (100,000 requests of a token, one head of 64: written 194 us
+  // without that limit and 160 with it, read back 113 and 80; 1,048,576: 1760 and 955 with it).
+  int64_t x = (p->N + C8_ROWS - 1) / C8_ROWS;
+  const bool many = p->B > C8_MANY && x > C8_CTAS;
+  if (many) x = C8_CTAS;
+  // few rows (a decode step): the heads of a CTA's rows go to several
   int64_t y = x >= 304 ? 1 : (304 + x - 1) / x;
   if (y > items) y = items;
   const dim3 grid((unsigned)x, (unsigned)(y < 1 ? 1 : y));
   auto go = [&](auto d, auto t) {
-    return launch_behind(K<d(), decltype(t)>::fn(), grid, C8_NT, 0, st, ar);
+    return many ? launch_behind(K<d(), decltype(t), true>::fn(), grid, C8_NT, 0, st, ar)
+                : launch_behind(K<d(), decltype(t), false>::fn(), grid, C8_NT, 0, st, ar);
   };
   using D64 = std::integral_constant<int, 64>;
   using D128 = std::integral_constant<int, 128>;
@@ -373,11 +448,11 @@ cudaError_t run(const gdn_cache8_problem* p, const Cache8Args& ar, int items, cu
   }
   return p->D == 64 ? go(D64(), 0.f) : p->D == 128 ? go(D128(), 0.f) : go(D256(), 0.f);
 }
-template <int D, typename T> struct Write {
-  static auto fn() { return k_cache_write8<D, T>; }
+template <int D, typename T, bool MANY> struct Write {
+  static auto fn() { return k_cache_write8<D, T, MANY>; }
 };
-template <int D, typename T> struct Read {
-  static auto fn() { return k_cache_read8<D, T>; }
+template <int D, typename T, bool MANY> struct Read {
+  static auto fn() { return k_cache_read8<D, T, MANY>; }
 };
 
 Cache8Args args(const gdn_cache8_problem* p, const int32_t* table, const int32_t* cu,

@@ -12,11 +12,13 @@ import numpy as np
 BLOCK = 16
 
 
+def cut(cu, n):
+    """Offsets as they count: outside [0, n] or below an earlier one they are cut or raised."""
+    return np.maximum.accumulate(np.clip(np.asarray(cu, dtype=np.int64), 0, n))
+
+
 def sequences(cu_q, cu_k, Nq, Nk):
-    """(query rows, key rows) of every sequence; offsets outside the rows or below an earlier one
-    are cut or raised."""
-    def cut(cu, n):
-        return np.maximum.accumulate(np.clip(np.asarray(cu, dtype=np.int64), 0, n))
+    """(query rows, key rows) of every sequence."""
     a, b = cut(cu_q, Nq), cut(cu_k, Nk)
     return [(slice(a[i], a[i + 1]), slice(b[i], b[i + 1])) for i in range(len(a) - 1)]
 
@@ -112,6 +114,7 @@ def cache_write8(x, cache, scale, block_table, ctx_len, cu_seqlens):
     x = np.asarray(x, dtype=np.float64)
     cache, scale = np.array(cache), np.array(scale, dtype=np.float64)
     pages, P, Hk, _ = cache.shape
+    cu_seqlens = cut(cu_seqlens, len(x))
     for b, ctx in enumerate(ctx_len):
         t, end, pos = int(cu_seqlens[b]), int(cu_seqlens[b + 1]), max(int(ctx), 0)
         while t < end:
@@ -145,6 +148,7 @@ def cache_read8(cache, scale, block_table, cu_seqlens, n_tokens):
     val = values(cache, scale)
     pages, P, Hk, D = val.shape
     out = np.full((n_tokens, Hk, D), np.nan)
+    cu_seqlens = cut(cu_seqlens, n_tokens)
     for b in range(len(cu_seqlens) - 1):
         for j in range(int(cu_seqlens[b + 1]) - int(cu_seqlens[b])):
             i = j // P

@@ -122,3 +122,16 @@ def test_decode_over_the_values_is_the_forward_of_one_query():
     k, v = (attention.cache_read8(*c, table, [0, n], n) for c in (kc, vc))
     for a, b in zip(got, attention.attn_fwd(q, k, v, [0, 1], [0, n])):
         np.testing.assert_allclose(a, b, atol=1e-12)
+
+
+@pytest.mark.parametrize("bad,good", [([0, 30, 20, 60], [0, 30, 30, 60]), ([-7, 10, 20, 90], [0, 10, 20, 60]),
+                                      ([70, 10, 20, 30], [60, 60, 60, 60])])
+def test_cache_offsets_that_are_not_ordered_are_cut(bad, good):
+    P, Hk, D = 16, 1, 4
+    x, table = rand((60, Hk, D)), np.arange(15).reshape(3, 5)
+    zero = np.zeros((15, P, Hk, D), np.uint8), np.zeros((15, 1, Hk))
+    a, b = (attention.cache_write8(x, *zero, table, [3, 0, 20], cu) for cu in (bad, good))
+    for y, z in zip(a, b):
+        np.testing.assert_array_equal(y, z)
+    np.testing.assert_array_equal(attention.cache_read8(*a, table, bad, 60),
+                                  attention.cache_read8(*b, table, good, 60))
