@@ -11,11 +11,13 @@
 //     2^-39 of it is lost below), fp32 ones go as two f16 terms (2^-22).
 //   - a score is the product times the row's and the block's factors, in fp32; K's scale is one
 //     number per 16-key block, uniform in the warp.
-//   - V's scale goes into the weights: p vs / vref, where vref follows the largest scale that the
-//     warp has met (its accumulators are rescaled when one is more than 4 times as large, which is
-//     rare).  Weights are at most 2^4 (the scores' lazy reference) x 2^2 (the scales') and are held
-//     2^9 times that, 2^15 at most, so that f16 keeps 2^-11 of a weight down to 2^-23 of vref and
-//     2^-34 vref below.  bf16 q: one f16 term (an eighth of o's own rounding); fp32 q: two (2^-22).
+//   - V's scale goes into the weights: w = p vs, held as w 2^7 / R.  R follows the largest w of the head:
+//     it shrinks with the weights when the scores' reference rises, and is raised to a tile's largest w
+//     when the reference rises or a block's scale is above 16 R (both rare; then the accumulators are
+//     rescaled).  Weights are at most 2^4 (the scores' lazy reference), so that f16 holds 2^15 at most;
+//     it keeps 2^-11 of a w down to 2^-21 R and 2^-32 R below.  R is never above the largest w: a block
+//     counts by its weight, however large its scale.  bf16 q: one f16 term (an eighth of o's own
+//     rounding); fp32 q: two (2^-22).
 #include <cuda_fp16.h>
 
 #include "gdn_attn_split.cuh"
@@ -34,7 +36,8 @@ struct Cache<Q8<TO>> {
 
 // 4 KB of K and of V to a warp's tile (8 KB at D = 256): what is on its way per SM, 64 KB, and the
 // work per tile weigh against each other (131001 tokens, 8 heads of 128: 16 keys and 4 CTAs 56.3 us,
-// 32 and 3 57.8, 32 and 2 55.0; 812,553 tokens, 2 heads of 256: 16 and 2 159, 32 and 2 149).
+// 32 and 3 57.8, 32 and 2 55.0, which is 53.3 with R by head; 812,553 tokens, 2 heads of 256: 16 and 2
+// 159, 32 and 2 149, now 144).
 template <typename TO> struct Cfg<64, Q8<TO>, 1> : Fit<32, 4, 1> {};
 template <typename TO> struct Cfg<128, Q8<TO>, 1> : Fit<32, 2, 1> {};
 template <typename TO> struct Cfg<256, Q8<TO>, 1> : Fit<32, 2, 1> {};
@@ -43,8 +46,9 @@ template <typename TO> struct Cfg<128, Q8<TO>, 2> : Fit<32, 2, 1> {};
 template <typename TO> struct Cfg<256, Q8<TO>, 2> : Fit<16, 2, 1> {};
 
 constexpr float A8_LAZY = 4.f;   // log2 units
-constexpr float A8_UP = 512.f;   // 2^9, on the weights
-constexpr float A8_OVER = 4.f;   // how far a scale may be above vref
+constexpr float A8_UP = 0x1p7f;      // what R is in f16
+constexpr float A8_OVER = 16.f;      // how far a scale may be above R
+constexpr float A8_MOST = 0x1p100f;  // of A8_UP / R: R is 2^-93 at least
 
 // Q in shared memory as f16 (fp32: the second terms behind the first), rows 16 bytes longer than D
 // elements: the 8 lanes of a 16-byte read phase (2 rows x 4 chunks of 32 bytes) fall on different
@@ -109,6 +113,18 @@ __device__ __forceinline__ void load(uint32_t* dst, const uint8_t* p, bool in) {
     dst[0] = v.x;
     dst[1] = v.y;
   }
+}
+
+__device__ __forceinline__ float rcp(float x) {  // 2^-23 off
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// The largest of the 8 lanes that hold a head's keys.
+__device__ __forceinline__ float over_keys(float x) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
 }
 
 // `heads` query rows from q on to shared memory, in f16 with their factors (zeros past them).
@@ -267,7 +283,10 @@ __device__ void run_piece8(const AttnArgs& ar, char* smem, int64_t b, int n, int
     qf[q][0] = f.x;
     qf[q][1] = f.y;
   }
-  float vref = 0.f, rv = 0.f;  // the largest scale of V, and 2^9 over it
+  float rv[NG][2];  // A8_UP / R of heads 2t, 2t + 1
+  float vok = 0.f;  // A8_OVER times the least R of the warp's heads
+#pragma unroll
+  for (int q = 0; q < NG; ++q) rv[q][0] = rv[q][1] = A8_MOST;
 #pragma unroll 1
   for (int tile = t0; tile < t1; ++tile) {
     int64_t nxt[NK];
@@ -330,32 +349,36 @@ __device__ void run_piece8(const AttnArgs& ar, char* smem, int64_t b, int n, int
     float vtop = 0.f;
 #pragma unroll
     for (int i = 0; i < NK; ++i) vtop = fmaxf(vtop, vs[i]);
-    const float fv = vtop > A8_OVER * vref ? vref / vtop : 1.f;  // uniform in the warp
-    if (fv != 1.f) {
-      vref = vtop;
-      rv = A8_UP / vtop;
-    }
     // the scores' reference follows the maximum lazily, as in gdn_attn.cu
-    if (fv != 1.f || __any_sync(0xffffffffu, up)) {
+    if (vtop > vok || __any_sync(0xffffffffu, up)) {
+      float most = 0.f;
 #pragma unroll
       for (int q = 0; q < NG; ++q) {
         float f[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          float m = mx[q][j];
+          const float m = fmaxf(over_keys(mx[q][j]), a.m[q][j]), base = m == -INFINITY ? 0.f : m;
+          float w = 0.f;  // the tile's largest
 #pragma unroll
-          for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-          m = fmaxf(m, a.m[q][j]);
-          f[j] = m == a.m[q][j] ? 1.f : ex2((a.m[q][j] - m) * ar.sl);  // 0 from -inf
-          a.l[q][j] *= f[j];
+          for (int i = 0; i < NK; ++i)
+            w = fmaxf(w, ex2((fmaxf(s[q][i][j], s[q][i][j + 2]) - base) * ar.sl) * vs[i]);
+          w = over_keys(w);
+          const float e = m == a.m[q][j] ? 1.f : ex2((a.m[q][j] - m) * ar.sl);  // 0 from -inf
+          a.l[q][j] *= e;
           a.m[q][j] = m;
-          f[j] *= fv;
+          const float r = rv[q][j] * rcp(e);  // infinite from 0
+          rv[q][j] = fminf(w * r > A8_UP ? A8_UP * rcp(w) : r, A8_MOST);
+          f[j] = rv[q][j] * rcp(r);
+          most = fmaxf(most, rv[q][j]);
         }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) a.o[q][i][j] *= f[j & 1];
       }
+#pragma unroll
+      for (int o = 1; o < 4; o <<= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+      vok = A8_OVER * A8_UP * rcp(most);
     }
 #pragma unroll
     for (int q = 0; q < NG; ++q)
@@ -366,7 +389,7 @@ __device__ void run_piece8(const AttnArgs& ar, char* smem, int64_t b, int n, int
         for (int i = 0; i < NK; ++i) {
           const float p = ex2((s[q][i][j] - base) * ar.sl);
           a.l[q][j & 1] += p;
-          s[q][i][j] = p * (vs[i] * rv);
+          s[q][i][j] = p * (vs[i] * rv[q][j & 1]);
         }
       }
     // fp32: the tensor cores cut an accumulator's low bits off at every product, so a tile's
@@ -415,13 +438,12 @@ __device__ void run_piece8(const AttnArgs& ar, char* smem, int64_t b, int n, int
       rows[i] = nrows[i];
     }
   }
-  const float back = vref * (1.f / A8_UP);
 #pragma unroll
   for (int q = 0; q < NG; ++q) {
 #pragma unroll
     for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) a.o[q][i][j] *= back;
+      for (int j = 0; j < 4; ++j) a.o[q][i][j] *= rcp(rv[q][j & 1]);
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll

@@ -790,8 +790,10 @@ gdn_status gdn_cache_read8(const gdn_cache8_problem* p, const void* k_cache, con
 
 /*
  * gdn_attn_decode over that cache: the same call with k_cache and v_cache in e4m3 and their
- * scales; q and o in p->dtype.  The softmax weights go into their product with v in f16, rounded
- * (bf16 q: 2^-11 of a weight) or as two terms (fp32 q).  Errors as gdn_attn_decode.
+ * scales; q and o in p->dtype.  The softmax weights, times their blocks' scales of v, go into their
+ * product with v's numbers in f16, rounded (bf16 q: off by 2^-11) or as two terms (fp32 q: 2^-22);
+ * those below 2^-21 of the head's largest (of 2^-93, if that is more) are off by 2^-32 of it.
+ * Errors as gdn_attn_decode.
  */
 gdn_status gdn_attn_decode8_workspace_size(const gdn_attn_problem* p, size_t* bytes);
 gdn_status gdn_attn_decode8(const gdn_attn_problem* p, const void* q, const void* k_cache,

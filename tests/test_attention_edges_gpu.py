@@ -1,12 +1,14 @@
 """GPU tests of the full-attention calls and of the 8-bit cache at places where a definition is easily
-missed: offsets out of order.  Bounds are counted as in test_attention_gpu.py."""
+missed: offsets out of order, blocks whose scale is far above the others'.  Bounds are counted as in
+test_attention_gpu.py."""
 import numpy as np
 import pytest
 import torch
 
 import chunked_state_scan_gated_gb300 as gdn
-from oracle import attention
-from test_attention_gpu import BF, F8, F32, filled, i32, n64, rand, same, step_of, u8
+from oracle import attention, decode
+from test_attention_gpu import (BF, F8, F32, check_dec, dec_inputs, filled, i32, n64, rand, same,
+                                step_of, u8)
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +62,49 @@ def test_cache_offsets_out_of_order_among_many_requests():
     check_cut(cu, [i % 20 for i in range(700)], 700, 64, BF, Hk=1)
     cu[500], cu[3] = 500, 650
     check_cut(cu, [i % 20 for i in range(700)], 700, 64, BF, Hk=1)
+
+
+# ------------------------------------------------------------------ decode over the 8-bit cache
+
+@pytest.mark.parametrize("place", [0, 7, 18])
+@pytest.mark.parametrize("D,Hq,up", [(64, 16, 16), (128, 8, 24), (128, 32, 40), (256, 16, 30),
+                                     (256, 32, 20)])
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
+def test_decode8_blocks_count_by_their_weight_whatever_their_scale(dt, D, Hq, up, place):
+    """One block of V is 2^up larger than the others.  Odd heads see it alone (scores of about 60),
+    even ones do not (-60), wherever it is.  Root mean square over each head's o: fp32 as in
+    test_decode8_fp32_error_on_the_whole, 2^-20.  bf16: o's own rounding 2^-8 at most, weights 2^-11
+    and scores 2^-19 far below it: 1.1 2^-8."""
+    lens = [300, 517]
+    q, kc, vc, ks, vs, table, n = dec_inputs(lens, Hq, 2, D, 16, dt, seed=D + place, spread=0.0)
+    q.abs_()
+    q[:, 1::2] *= -1
+    for b in range(2):
+        page = int(table[b, place])
+        rows = min(16, lens[b] - 16 * place)
+        kc[page, :rows] = torch.tensor(-1.0).to(F8)
+        ks[page] = 60 / (0.8 * D ** 0.5)
+        vs[page] *= 2.0 ** up
+    o, lse = gdn.gdn_attn_decode8(q, kc, vc, ks, vs, table, n)
+    kv, vv = (attention.values(u8(c), np.nan_to_num(n64(s))) for c, s in ((kc, ks), (vc, vs)))
+    ref, rl = decode.attn_decode(n64(q), np.nan_to_num(kv), np.nan_to_num(vv), table.cpu().numpy(),
+                                 n.cpu().numpy(), D ** -0.5)
+    assert (np.abs(ref[:, 1::2]).max() > 2.0 ** (up - 6)) and np.abs(ref[:, ::2]).max() < 8
+    err = np.linalg.norm(n64(o) - ref, axis=-1) / np.linalg.norm(ref, axis=-1)
+    assert err.max() <= (1.1 * 2.0 ** -8 if dt == BF else 2.0 ** -20), err
+    assert np.abs(n64(lse) - rl).max() <= 2.0 ** -15 + 2.0 ** -19 * np.abs(rl).max()
+
+
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
+def test_decode8_scales_at_the_ends_of_their_range(dt):
+    """V's scales of 2^-100, 2^100 and 0 (a block never written) beside each other; a context of
+    zeros."""
+    inp = dec_inputs([200, 60, 33], 8, 2, 64, 16, dt, seed=40, spread=0.0)
+    vs, table = inp[4], inp[5]
+    vs[table[0, :12].long()] = 2.0 ** -100
+    for i, scale in enumerate((2.0 ** -100, 2.0 ** 100, 0.0)):
+        vs[table[1, i].long()] = scale
+    vs[table[2, :3].long()] = 0.0
+    o, lse = gdn.gdn_attn_decode8(*inp)
+    check_dec(*inp, o, lse)
+    assert (o[0] != 0).any() and (o[2] == 0).all()
