@@ -1236,7 +1236,9 @@ def gdn_attn_fwd(q, k, v, cu_seqlens=None, cu_seqlens_k=None, *, causal=True, sc
     (int32 on the device).  causal: the queries are the last of the sequence's keys, and see none
     behind their own place.  Without offsets: one sequence, or q [B, T, Hq, D] and k, v
     [B, Tk, Hk, D].  q, k, v may be slices of one projection.  Returns (o like q, contiguous, lse
-    [..., Hq] fp32 or None); rows behind the last sequence are left as they are."""
+    [..., Hq] fp32 or None); rows behind the last sequence are left as they are.  Offsets that had to be
+    cut, and a call that a kernel gave up (its results are incomplete), show in `status` alone: pass a
+    status_word() and look at it with gdn_check_device_status."""
     dev, dt = _device_of(q), q.dtype
     p, qp, kp, vp, cup, ckp = _seq_problem(q, k, v, cu_seqlens, cu_seqlens_k, dev, causal, scale)
     o, op = _out("o", o, dev, dt, q.shape, q.device, stream)
@@ -1253,7 +1255,8 @@ def gdn_attn_fwd(q, k, v, cu_seqlens=None, cu_seqlens_k=None, *, causal=True, sc
 
 def gdn_attn_bwd(q, k, v, o, lse, dO, cu_seqlens=None, cu_seqlens_k=None, *, causal=True,
                  scale=0.0, dq=None, dk=None, dv=None, ws=None, status=None, stream=None):
-    """Backward of gdn_attn_fwd from its o and lse: (dq like q, dk, dv like k), contiguous."""
+    """Backward of gdn_attn_fwd from its o and lse: (dq like q, dk, dv like k), contiguous.  `status` as
+    there."""
     dev, dt = _device_of(q), q.dtype
     p, qp, kp, vp, cup, ckp = _seq_problem(q, k, v, cu_seqlens, cu_seqlens_k, dev, causal, scale)
     dq, dqp = _out("dq", dq, dev, dt, q.shape, q.device, stream)

@@ -110,7 +110,7 @@ struct Bars {
   uint64_t r_full, r_empty, full[8], empty[8], s_full[2], p_full[2], p_rest[2], pv[2], o_full[2],
       o_empty[2], l_full[2], l_empty[2], drained;
   uint32_t tmem;
-  int gave_up;
+  Alive alive;
 };
 static_assert(sizeof(Bars) <= 512, "");
 
@@ -243,27 +243,28 @@ struct Turns {
 // once: all others see it after the same items, so that their barriers of some warps stay matched.
 template <typename ITEM>
 __device__ __forceinline__ void feed_items(Feed& f, Turns turns, const SeqArgs& a,
-                                           volatile int* gave_up) {
+                                           Alive& alive) {
   static_assert(sizeof(ITEM) <= sizeof(f.item[0]), "");
   int turn = 0;
   auto put = [&](const ITEM& x) {
     const int s = turn & 1;
-    if (turn >= 2) wait_alone(&f.empty[s], ((turn >> 1) - 1) & 1, gave_up);
+    if (turn >= 2) wait_alone(&f.empty[s], ((turn >> 1) - 1) & 1, alive);
     *reinterpret_cast<ITEM*>(f.item[s]) = x;
     mbar_arrive(&f.full[s]);
+    alive.moved = clock64();
     ++turn;
   };
   ITEM x;
-  for (int idx; !*gave_up && (idx = turns.next()) >= 0;)
+  for (int idx; !alive.gave_up && (idx = turns.next()) >= 0;)
     if (x.find(a, idx)) put(x);
   x.n = -1;
   put(x);
 }
 // The others': the next item; false: there is none.  By whole warps, or (ALONE) by one lane.
 template <bool ALONE, typename ITEM>
-__device__ __forceinline__ bool take_item(Feed& f, int& turn, ITEM& x, volatile int* gave_up) {
+__device__ __forceinline__ bool take_item(Feed& f, int& turn, ITEM& x, Alive& alive) {
   const int s = turn & 1;
-  if (!wait_alone(&f.full[s], (turn >> 1) & 1, gave_up)) return false;
+  if (!wait_alone(&f.full[s], (turn >> 1) & 1, alive)) return false;
   ++turn;
   x = *reinterpret_cast<const ITEM*>(f.item[s]);
   if (!ALONE) __syncwarp();
@@ -373,19 +374,20 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
     }
     mbar_init(&bar.drained, 1);
     bar.feed.init();
-    bar.gave_up = 0;
+    bar.alive.gave_up = 0;
     fence_barrier_init();
   }
   if (warp == 0) tmem_alloc(&bar.tmem, 512);
   tc_fence_before();
   if (!a.late) after_previous();
   before_next();
+  if (tid == 0) bar.alive.moved = clock64();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uniform(bar.tmem);
   // columns: S 0 and 1 at 0 and 128, then the accumulators
   auto acc_of = [&](int t) { return tmem + 256 + t * D; };
-  auto wait = [&](uint64_t* b, uint32_t parity) { wait_for(b, parity, a.status, &bar.gave_up); };
+  auto wait = [&](uint64_t* b, uint32_t parity) { wait_for(b, parity, bar.alive); };
   if (FWD && blockIdx.x == 0 && tid == 0) check_single(a);
   const int per_tile =
       FWD ? a.Hq / a.pack * a.parts : a.tk.rows / TR * a.Hk * a.splits;  // items
@@ -397,11 +399,11 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
     if (warp == 12 && lane == 0) {
       // ---- copies
       int stage = 0, turn = 0, works = 0;
-      while (take_item<true>(bar.feed, taken, x, &bar.gave_up)) {
+      while (take_item<true>(bar.feed, taken, x, bar.alive)) {
         if (x.n == 0) continue;
         const int rows = FWD ? TR / a.pack : TR;
         if (works > 0) wait(&bar.r_empty, (works - 1) & 1);
-        if (bar.gave_up) continue;
+        if (bar.alive.gave_up) continue;
         ++works;
         mbar_arrive_expect_tx(&bar.r_full, NT * F::kTile);
         for (int i = 0; i < NT; ++i)
@@ -411,13 +413,14 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
         auto block = [&](const CUtensorMap* m, int g, int j) {
           for (int c = 0; c < NC; ++c) {
             if (turn > 0) wait(&bar.empty[stage], (turn - 1) & 1);
-            if (bar.gave_up) return;
+            if (bar.alive.gave_up) return;
             mbar_arrive_expect_tx(&bar.full[stage], F::kStage);
             for (int y = 0; y < F::kAtoms; ++y)
               tma_load_3d(ring + stage * F::kStage + y * 16384, m, c * F::kCols + y * 64,
                           FWD ? x.hk : x.head + g, (FWD ? x.t.k0 : x.t.q0) + j * 128,
                           &bar.full[stage]);
             if (++stage == ST) stage = 0, ++turn;
+            bar.alive.moved = clock64();
           }
         };
         int g1 = 0, j1 = x.j0, g2 = 0, j2 = x.j0;
@@ -435,7 +438,7 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
           if (NT == 1 && it > 0) second();
         }
       }
-      if (bar.gave_up) drain(bar, works, ST, stage, turn);
+      if (bar.alive.gave_up) drain(bar, works, ST, stage, turn);
     } else if (warp == 13) {
       // ---- products
       const uint32_t issue = elected();
@@ -453,7 +456,7 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
       auto next = [&]() {
         if (++stage == ST) stage = 0, ++turn;
       };
-      while (take_item<false>(bar.feed, taken, x, &bar.gave_up)) {
+      while (take_item<false>(bar.feed, taken, x, bar.alive)) {
         x.make_uniform();
         if (x.n == 0) continue;
         const int xrows = FWD ? x.t.nk : x.t.nq;
@@ -565,12 +568,12 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
           scored += x.n;
         }
       }
-      if (bar.gave_up) {  // products in flight end before the TMEM is given back
+      if (bar.alive.gave_up) {  // products in flight end before the TMEM is given back
         commit_to(&bar.drained, issue);
         mbar_wait(&bar.drained, 0, nullptr, 0);
       }
     } else if (warp == 14 && lane == 0) {
-      feed_items<Item<D, FWD>>(bar.feed, Turns(tiles_there<!FWD>(a) * per_tile), a, &bar.gave_up);
+      feed_items<Item<D, FWD>>(bar.feed, Turns(tiles_there<!FWD>(a) * per_tile), a, bar.alive);
     }
   } else if (group == 2) {
     // ---- results: a thread per row
@@ -578,7 +581,7 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
     const int r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     int items = 0, works[2] = {0, 0};
-    while (take_item<false>(bar.feed, taken, x, &bar.gave_up)) {
+    while (take_item<false>(bar.feed, taken, x, bar.alive)) {
 #pragma unroll
       for (int i = 0; i < NT; ++i) {
         const int row = FWD ? x.t.at + (i * TR + r) / a.pack : x.t.at + i * TR + r;
@@ -630,7 +633,7 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     int items = 0, done = 0;  // done: blocks of the tile so far, of all items
     int placed = 0;           // blocks of the ring in front of this item
-    while (take_item<false>(bar.feed, taken, x, &bar.gave_up)) {
+    while (take_item<false>(bar.feed, taken, x, bar.alive)) {
       const int rows = FWD ? TR / a.pack : TR, at = x.t.at + i * rows, off = x.t.nk - x.t.nq;
       const int w0 = (warp & 3) * 32;  // the warp's rows: tokens first .. last
       const int first = FWD ? at + w0 / a.pack : at + w0;
@@ -814,6 +817,7 @@ __global__ void __launch_bounds__(Flash<D>::kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && bar.alive.gave_up && a.status) atomicOr(a.status, kStatusTimeout);
   if (warp == 0) tmem_dealloc(tmem, 512);
   if (a.late) after_previous();
 }
@@ -916,18 +920,19 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
     mbar_init(&bar.o_empty[0], 4);
     mbar_init(&bar.drained, 1);
     bar.feed.init();
-    bar.gave_up = 0;
+    bar.alive.gave_up = 0;
     fence_barrier_init();
   }
   if (warp == 0) tmem_alloc(&bar.tmem, 512);
   tc_fence_before();
   if (!a.late) after_previous();
   before_next();
+  if (tid == 0) bar.alive.moved = clock64();
   __syncthreads();
   tc_fence_after();
   // columns: S (two buffers, or one), dP, the accumulators
   const uint32_t tmem = uniform(bar.tmem), t_dp = tmem + (DQ ? 2 : 1) * BN, t_acc = t_dp + BN;
-  auto wait = [&](uint64_t* b, uint32_t parity) { wait_for(b, parity, a.status, &bar.gave_up); };
+  auto wait = [&](uint64_t* b, uint32_t parity) { wait_for(b, parity, bar.alive); };
   const int per_tile = DQ ? a.Hq : a.Hk * a.splits;  // items
   SlopeItem<DQ, BN, TR> x;
   int taken = 0;
@@ -940,11 +945,11 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
       // ---- copies
       int works = 0, c = 0;
       Place at{0, 0};
-      while (take_item<true>(bar.feed, taken, x, &bar.gave_up)) {
+      while (take_item<true>(bar.feed, taken, x, bar.alive)) {
         if (x.n == 0) continue;
         const int row0 = (DQ ? x.t.q0 : x.t.k0) + x.t.at;
         if (works > 0) wait(&bar.r_empty, (works - 1) & 1);
-        if (bar.gave_up) continue;
+        if (bar.alive.gave_up) continue;
         ++works;
         mbar_arrive_expect_tx(&bar.r_full, 2 * F::kTile);
         for (int i = 0; i < D / 64; ++i) {
@@ -953,7 +958,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
                       &bar.r_full);
         }
         int g = 0, j = x.j0;
-        for (int it = 0; it < x.n && !bar.gave_up; ++it, ++c) {
+        for (int it = 0; it < x.n && !bar.alive.gave_up; ++it, ++c) {
           for (int y = 0; y < 2; ++y) {
             if (2 * c + y >= ST) wait(&bar.empty[at.stage], at.parity ^ 1);
             mbar_arrive_expect_tx(&bar.full[at.stage], F::kStage);
@@ -963,10 +968,11 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
                           &bar.full[at.stage]);
             at = at.template on<ST>(1);
           }
+          bar.alive.moved = clock64();
           if ((j = x.after(j)) == x.j0) ++g;
         }
       }
-      if (bar.gave_up) {  // the copies have to land before the CTA ends
+      if (bar.alive.gave_up) {  // the copies have to land before the CTA ends
         if (works > 0) mbar_wait(&bar.r_full, (works - 1) & 1, nullptr, 0);
         for (int p = max(0, 2 * c - ST); p < 2 * c; ++p)
           mbar_wait(&bar.full[place(p).stage], place(p).parity, nullptr, 0);
@@ -979,7 +985,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
       constexpr uint32_t kOwn = kHead, kRing = kHead + 2 * F::kTile;
       int works = 0, c = 0;
       Place p1{0, 0}, p2{1, 0};  // of X1 and X2 of iteration c
-      while (take_item<false>(bar.feed, taken, x, &bar.gave_up)) {
+      while (take_item<false>(bar.feed, taken, x, bar.alive)) {
         x.make_uniform();
         if (x.n == 0) continue;
         const int xrows = DQ ? x.t.nk : x.t.nq;
@@ -1070,13 +1076,13 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
           }
         }
       }
-      if (bar.gave_up) {
+      if (bar.alive.gave_up) {
         commit_to(&bar.drained, issue);
         mbar_wait(&bar.drained, 0, nullptr, 0);
       }
     } else if (warp == 14 && lane == 0) {
       feed_items<SlopeItem<DQ, BN, TR>>(bar.feed, Turns(tiles_there<!DQ>(a) * per_tile), a,
-                                        &bar.gave_up);
+                                        bar.alive);
     }
   } else if (group == 2) {
     // ---- results: a thread per row
@@ -1084,7 +1090,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
     const int r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     int works = 0;
-    while (take_item<false>(bar.feed, taken, x, &bar.gave_up)) {
+    while (take_item<false>(bar.feed, taken, x, bar.alive)) {
       const int row = x.t.at + r, side = DQ ? x.t.nq : x.t.nk;
       if (x.n > 0) {
         wait(&bar.o_full[0], works & 1);
@@ -1136,7 +1142,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
       if (lane == 0) mbar_arrive(b);
     };
     int c = 0;  // iterations of all items
-    while (take_item<false>(bar.feed, taken, x, &bar.gave_up)) {
+    while (take_item<false>(bar.feed, taken, x, bar.alive)) {
       const int off = x.t.nk - x.t.nq, first_row = x.t.at + (warp & 3) * 32, row = x.t.at + r;
       const int xrows = DQ ? x.t.nk : x.t.nq;
       float lse2 = INFINITY, delta = 0.f, ahead = 0.f;
@@ -1232,6 +1238,7 @@ __global__ void __launch_bounds__(Slope<D>::kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && bar.alive.gave_up && a.status) atomicOr(a.status, kStatusTimeout);
   if (warp == 0) tmem_dealloc(tmem, 512);
   if (a.late) after_previous();
 }
@@ -1258,7 +1265,7 @@ struct PairBars {
                                                // (full[3], r_full), what both have read or written
   uint64_t drained;
   uint32_t tmem;
-  int gave_up;
+  Alive alive;
 };
 static_assert(sizeof(PairBars) <= 512, "");
 
@@ -1300,19 +1307,20 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
     mbar_init(&bar.ds_full, 16);
     mbar_init(&bar.o_empty, 8);
     bar.feed.init();
-    bar.gave_up = 0;
+    bar.alive.gave_up = 0;
     fence_barrier_init();
   }
   if (warp == 0) pair_tmem_alloc(&bar.tmem);
   tc_fence_before();
   if (!a.late) after_previous();
   before_next();
+  if (tid == 0) bar.alive.moved = clock64();
   __syncthreads();
   pair_sync();
   tc_fence_after();
   const uint32_t tmem = uniform(bar.tmem), t_dp = tmem + BN, t_acc = tmem + 2 * BN;
   auto wait = [&](uint64_t* b, uint32_t parity) {
-    wait_for<true>(b, parity, a.status, &bar.gave_up);
+    wait_for<true>(b, parity, bar.alive);
   };
   const int per_tile = DQ ? a.Hq : a.Hk * a.splits;  // items
   SlopeItem<DQ, BN, 2 * TR> x;
@@ -1323,11 +1331,11 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
     if (warp == 12 && lane == 0) {
       // ---- copies: parts 0 X1 by rows, 1 X2 by rows, 2 X1 by columns
       int works = 0, c = 0;
-      while (take_item<true>(bar.feed, taken, x, &bar.gave_up)) {
+      while (take_item<true>(bar.feed, taken, x, bar.alive)) {
         if (x.n == 0) continue;
         const int row0 = (DQ ? x.t.q0 : x.t.k0) + x.t.at + rank * TR;
         if (works > 0) wait(&bar.r_empty, (works - 1) & 1);
-        if (bar.gave_up) continue;
+        if (bar.alive.gave_up) continue;
         ++works;
         mbar_arrive_expect_tx(&bar.r_full, 2 * F::kTile);
         for (int i = 0; i < D / 64; ++i) {
@@ -1336,7 +1344,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
                       &bar.r_full);
         }
         int g = 0, j = x.j0;
-        for (int it = 0; it < x.n && !bar.gave_up; ++it, ++c) {
+        for (int it = 0; it < x.n && !bar.alive.gave_up; ++it, ++c) {
           const int head = DQ ? x.hk : x.head + g, row = (DQ ? x.t.k0 : x.t.q0) + j * BN;
           for (int y = 0; y < 3; ++y) {
             if (c > 0) wait(&bar.empty[y], (c - 1) & 1);
@@ -1351,10 +1359,11 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
                 tma_load_3d(to + i * 16384, &m1c, rank * 128 + i * 64, head, row, &bar.full[y]);
             }
           }
+          bar.alive.moved = clock64();
           if ((j = x.after(j)) == x.j0) ++g;
         }
       }
-      if (bar.gave_up) {  // the copies have to land before the CTA ends
+      if (bar.alive.gave_up) {  // the copies have to land before the CTA ends
         if (works > 0) mbar_wait(&bar.r_full, (works - 1) & 1, nullptr, 0);
         if (c > 0)
           for (int y = 0; y < 3; ++y) mbar_wait(&bar.full[y], (c - 1) & 1, nullptr, 0);
@@ -1366,7 +1375,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
         wait(b, parity);
         if (lane == 0) arrive_first(&bar.peer[to]);
       };
-      while (take_item<false>(bar.feed, taken, x, &bar.gave_up)) {
+      while (take_item<false>(bar.feed, taken, x, bar.alive)) {
         if (x.n == 0) continue;
         tell(&bar.r_full, works & 1, 3);
         ++works;
@@ -1386,7 +1395,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
       const Desc kmaj(sdesc(base, 16, 1024)), mnmaj(sdesc(base, 16384, 1024));
       constexpr uint32_t kOwn = kHead, kParts = kHead + 2 * F::kTile;
       int works = 0, c = 0;
-      while (take_item<false>(bar.feed, taken, x, &bar.gave_up)) {
+      while (take_item<false>(bar.feed, taken, x, bar.alive)) {
         x.make_uniform();
         if (x.n == 0) continue;
         const int xrows = DQ ? x.t.nk : x.t.nq;
@@ -1445,13 +1454,13 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
           j = x.after(j);
         }
       }
-      if (bar.gave_up) {
+      if (bar.alive.gave_up) {
         pair_commit(&bar.drained, issue);
         mbar_wait(&bar.drained, 0, nullptr, 0);
       }
     } else if (warp == 14 && lane == 0) {
       feed_items<SlopeItem<DQ, BN, 2 * TR>>(bar.feed, Turns(tiles_there<!DQ>(a) * per_tile, 2), a,
-                                            &bar.gave_up);
+                                            bar.alive);
     }
   } else if (group == 2) {
     // ---- results: a thread per row
@@ -1459,7 +1468,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
     const int r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     int works = 0;
-    while (take_item<false>(bar.feed, taken, x, &bar.gave_up)) {
+    while (take_item<false>(bar.feed, taken, x, bar.alive)) {
       const int row = x.t.at + rank * TR + r, side = DQ ? x.t.nq : x.t.nk;
       if (x.n > 0) {
         wait(&bar.o_full, works & 1);
@@ -1495,7 +1504,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
     const int half = group, r = tid & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     int c = 0;  // iterations of all items
-    while (take_item<false>(bar.feed, taken, x, &bar.gave_up)) {
+    while (take_item<false>(bar.feed, taken, x, bar.alive)) {
       const int off = x.t.nk - x.t.nq, at = x.t.at + rank * TR;
       const int first_row = at + (warp & 3) * 32, row = at + r;
       const int xrows = DQ ? x.t.nk : x.t.nq;
@@ -1586,6 +1595,7 @@ __global__ void __launch_bounds__(Pair::kThreads, 1) __cluster_dims__(2, 1, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && bar.alive.gave_up && a.status) atomicOr(a.status, kStatusTimeout);
   __syncwarp();
   pair_sync();  // neither CTA's barriers or TMEM are used any more
   if (warp == 0) pair_tmem_dealloc(tmem);

@@ -5,6 +5,7 @@
 
 #include "gdn_attn_seq.cuh"
 #include "gdn_tc_common.cuh"
+#include "gdn_wait.cuh"
 
 namespace gdn {
 namespace seq {
@@ -121,59 +122,64 @@ __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// A wait of at most kWaitLimitNs; once one has run out (status, *gave_up), the others of the CTA
-// give up at once, so that it ends.
-// PAIR: what the other CTA of a pair did before it arrived is seen too.
-template <bool PAIR = false>
-__device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, int32_t* status,
-                                         volatile int* gave_up) {
-  const uint32_t addr = smem_u32(bar);
-  uint64_t t0 = 0;
-  for (uint32_t it = 0;; ++it) {
-    uint32_t done;
-    if constexpr (PAIR)
-      asm volatile(
+// What the waits of a CTA share, in shared memory.
+struct Alive {
+  volatile uint64_t moved;  // when a block was last sent for, or an item found
+  volatile int gave_up;     // a wait has run out
+};
+
+constexpr uint64_t kStillCycles = 4000000000ull;  // about 2 s
+
+template <bool PAIR>
+__device__ __forceinline__ bool arrived(uint32_t addr, uint32_t parity) {
+  uint32_t done;
+  if constexpr (PAIR)
+    asm volatile(
         "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
         " selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(done)
         : "r"(addr), "r"(parity)
         : "memory");
-    else
-      asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(addr), "r"(parity)
-        : "memory");
-    if (done) return;
-    if (it == 0) t0 = global_timer();
-    else if (*gave_up || global_timer() - t0 > kWaitLimitNs) {
-      if (!*gave_up && status) atomicOr(status, kStatusTimeout);
-      *gave_up = 1;
-      return;
-    }
-  }
-}
-
-// For the queue of items: twice the limit, so that whoever is late because of another wait is not given
-// up on, and no regard to *gave_up.  A lane or a warp.
-__device__ __forceinline__ bool wait_alone(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
-  const uint32_t addr = smem_u32(bar);
-  uint64_t t0 = 0;
-  while (true) {
-    uint32_t done;
+  else
     asm volatile(
         "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
         " selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(done)
         : "r"(addr), "r"(parity)
         : "memory");
-    if (done) return true;
+  return done;
+}
+
+// A wait that is given up when it has taken kWaitLimitNs and nothing has moved for as long, or another
+// was given up, so that the CTA ends.
+// PAIR: what the other CTA of a pair did before it arrived is seen too.
+template <bool PAIR = false>
+__device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, Alive& alive) {
+  const uint32_t addr = smem_u32(bar);
+  uint64_t t0 = 0;
+  for (uint32_t it = 0;; ++it) {
+    if (arrived<PAIR>(addr, parity)) return;
+    if (it == 0) t0 = global_timer();
+    else if (alive.gave_up ||
+             (global_timer() - t0 > kWaitLimitNs && stands_still(clock64(), alive.moved, kStillCycles))) {
+      alive.gave_up = 1;
+      return;
+    }
+  }
+}
+
+// For the queue of items: twice the limit, so that whoever is late because of another wait is not given
+// up on, and no regard to gave_up.  A lane or a warp.
+__device__ __forceinline__ bool wait_alone(uint64_t* bar, uint32_t parity, Alive& alive) {
+  const uint32_t addr = smem_u32(bar);
+  uint64_t t0 = 0;
+  while (true) {
+    if (arrived<false>(addr, parity)) return true;
     const uint64_t now = global_timer();
     if (t0 == 0) t0 = now;
-    if (now - t0 > 2 * kWaitLimitNs) break;
+    if (now - t0 > 2 * kWaitLimitNs && stands_still(clock64(), alive.moved, 2 * kStillCycles)) break;
   }
-  *gave_up = 1;
+  alive.gave_up = 1;
   return false;
 }
 

@@ -706,8 +706,12 @@ gdn_status gdn_slot_map(const gdn_slot_problem* p, const int32_t* ctx_len,
  *    outputs that belong to no sequence are left as they were.  (A NaN or infinity in a key or
  *    value row of a sequence may reach the queries of the same sequence that do not see it; in the
  *    backward one in a query, o, lse or dO row the keys of its sequence that it does not see.)
- *  - fp32 softmax and sums.  On bf16, p and ds are rounded to bf16 for their products.
+ *  - fp32 softmax and sums.  On bf16, p and ds are rounded to bf16 for their products, and the tensor
+ *    cores cut their fp32 sums off at every 16 rows added: a sum over n rows comes out about n 2^-30 of
+ *    itself too small (n = Nk for o; Nq times the query heads of a key head for dk, dv).
  *  - Deterministic: the same bits for the same call.
+ *  - A bf16 call on which nothing moves for about 2 s is given up: its outputs are then incomplete, which
+ *    only `status` tells (GDN_ERR_DEVICE_TIMEOUT).  How long a call takes does not matter.
  *  - Workspace 256-byte aligned (none in most forwards of one sequence, whose size is 0); calls that
  *    can run at the same time need one each.
  * Errors: null or misaligned pointer, sizes < 0, Hq % Hk != 0, n_seqs < 1 with rows given, cu_q
