@@ -1,5 +1,6 @@
 """GPU tests of the full-attention calls and of the 8-bit cache at places where a definition is easily
-missed: offsets out of order, blocks whose scale is far above the others'.  Bounds are counted as in
+missed: offsets out of order, blocks whose scale is far above the others', groups of query heads that a
+tile holds whole, in part or twice over.  Bounds are counted as in
 test_attention_gpu.py."""
 import numpy as np
 import pytest
@@ -7,8 +8,8 @@ import torch
 
 import chunked_state_scan_gated_gb300 as gdn
 from oracle import attention, decode
-from test_attention_gpu import (BF, F8, F32, check_dec, dec_inputs, filled, i32, n64, rand, same,
-                                step_of, u8)
+from test_attention_gpu import (BF, F8, F32, check_dec, check_seq, dec_inputs, filled, i32, n64,
+                                rand, same, step_of, u8)
 
 pytestmark = pytest.mark.gpu
 
@@ -18,6 +19,30 @@ def _lib():
     if not torch.cuda.is_available():
         pytest.skip("no CUDA device")
     gdn.load_library()
+
+
+# ------------------------------------------------------------------ attention over packed rows
+
+GROUPS = [(16, 1), (32, 2), (48, 1), (6, 1), (12, 2), (24, 1), (5, 1)]
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Hq,Hk", GROUPS)
+def test_attention_of_groups_of_any_size(Hq, Hk, D):
+    """A forward tile holds the largest power of two of a key head's query heads, up to 16: groups of
+    16 and of several 16, and groups of which it holds a part; at ends of tiles of 8, 16 and 128 tokens,
+    over the prompt and over a longer context."""
+    lens = [7, 8, 9, 15, 16, 17, 129]
+    check_seq(lens, None, Hq, Hk, D, BF, True, seed=Hq + D)
+    check_seq(lens, [50, 8, 300, 15, 700, 9, 400], Hq, Hk, D, BF, True, seed=Hq + D + 1)
+    check_seq([33, 2], [20, 140], Hq, Hk, D, BF, False, seed=Hq + D + 2)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Hq,Hk", GROUPS)
+def test_attention_of_groups_of_any_size_with_divided_keys(Hq, Hk, D):
+    """The same where the keys of every tile are divided and joined."""
+    check_seq([5, 3, 17], [6000, 2500, 900], Hq, Hk, D, BF, True, seed=Hq + D + 3)
 
 
 # --------------------------------------------------------------------------- the 8-bit cache
