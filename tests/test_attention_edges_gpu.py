@@ -1,6 +1,6 @@
 """GPU tests of the full-attention calls and of the 8-bit cache at places where a definition is easily
 missed: offsets out of order, blocks whose scale is far above the others', groups of query heads that a
-tile holds whole, in part or twice over.  Bounds are counted as in
+tile holds whole, in part or twice over, fp32 accuracy in the norm.  Bounds are counted as in
 test_attention_gpu.py."""
 import numpy as np
 import pytest
@@ -8,7 +8,7 @@ import torch
 
 import chunked_state_scan_gated_gb300 as gdn
 from oracle import attention, decode
-from test_attention_gpu import (BF, F8, F32, check_dec, check_seq, dec_inputs, filled, i32, n64,
+from test_attention_gpu import (BF, F8, F32, U, check_dec, check_seq, dec_inputs, filled, i32, n64,
                                 rand, same, step_of, u8)
 
 pytestmark = pytest.mark.gpu
@@ -43,6 +43,66 @@ def test_attention_of_groups_of_any_size(Hq, Hk, D):
 def test_attention_of_groups_of_any_size_with_divided_keys(Hq, Hk, D):
     """The same where the keys of every tile are divided and joined."""
     check_seq([5, 3, 17], [6000, 2500, 900], Hq, Hk, D, BF, True, seed=Hq + D + 3)
+
+
+# A rounding to fp32 is off by 0.425 U of the value in the root mean square (uniform within half a
+# step, mantissas spread over their logarithm): STEP U^2.  A sum of n terms of random sign that is
+# rounded at each is off by n STEP U^2 of its square at most (where the first terms are the largest;
+# half of that where all are alike).
+STEP = 0.425 ** 2
+
+
+def fp32_errors(D, n, run):
+    """Bounds (relative, in the norm) of o over n keys and of dq, dk, dv for q, k, v, dO of standard
+    normal numbers: errors of a weight, in quadrature, with the sums', times 1.25.  Scores are of about
+    1, sums of D products in two halves: STEP D / 4.  Forward: scaled and subtracted at 5 at most, ex2
+    2^-22, n keys in two halves.  Backward: rounded at 8 (the lse of 1400 keys) once as a sum, once times
+    log2(e), whose own error is 0.22 U; dP as the scores; gradients summed in runs of `run` rows."""
+    score = STEP * D / 4
+    o = score + STEP * (1 + 25) + 16 + STEP * n / 2
+    p = score + 2 * STEP * 64 + (0.22 * 8) ** 2 + 16
+    ds = p + score + 1
+    return {k: 1.25 * U * x ** 0.5 for k, x in (("o", o), ("dq", ds + STEP * run),
+                                                ("dk", ds + STEP * run), ("dv", p + STEP * run))}
+
+
+def norm_within(name, x, ref, bound):
+    err = np.linalg.norm(n64(x) - ref) / np.linalg.norm(ref)
+    print(f"{name}: {err:.3g}, bound {bound:.3g}")
+    assert err <= bound, (name, err, bound)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_fp32_error_on_the_whole(D):
+    """1400 tokens, 16 query heads to a key head, so many key heads that no key tile's query heads are
+    divided: 22,400 rows to a sum, which only runs of 16 blocks of 64 keep this accurate (in one run
+    45 U and more).  One key head and its query heads against the definition."""
+    n, Hk, G = 1400, 28, 16
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    q, k, v, dO = (torch.randn((n, h, D), generator=gen, device="cuda")
+                   for h in (Hk * G, Hk, Hk, Hk * G))
+    o, lse = gdn.gdn_attn_fwd(q, k, v)
+    dq, dk, dv = gdn.gdn_attn_bwd(q, k, v, o, lse, dO)
+    at, hk = slice(9 * G, 10 * G), slice(9, 10)
+    x = [n64(t) for t in (q[:, at], k[:, hk], v[:, hk])]
+    bound = fp32_errors(D, n, 1024)
+    norm_within("o", o[:, at], attention.attn_fwd(*x, [0, n], [0, n])[0], bound["o"])
+    refs = attention.attn_bwd(*x, n64(o[:, at]), n64(lse[:, at]), n64(dO[:, at]), [0, n], [0, n])
+    for name, got, ref in zip(("dq", "dk", "dv"), (dq[:, at], dk[:, hk], dv[:, hk]), refs):
+        norm_within(name, got, ref, bound[name])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_fp32_error_over_a_long_context(D):
+    """64 queries behind 12,224 keys, so many heads that no tile's keys are divided."""
+    n, Hk, G = 12288, 19, 4
+    gen = torch.Generator(device="cuda").manual_seed(D + 1)
+    q = torch.randn((64, Hk * G, D), generator=gen, device="cuda")
+    k, v = (torch.randn((n, Hk, D), generator=gen, device="cuda") for _ in range(2))
+    o, _ = gdn.gdn_attn_fwd(q, k, v, i32([0, 64]), i32([0, n]))
+    x = [n64(t) for t in (q[:, 8:12], k[:, 2:3], v[:, 2:3])]
+    norm_within("o", o[:, 8:12], attention.attn_fwd(*x, [0, 64], [0, n])[0],
+                fp32_errors(D, n, 1024)["o"])
 
 
 # --------------------------------------------------------------------------- the 8-bit cache
