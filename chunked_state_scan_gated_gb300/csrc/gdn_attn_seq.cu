@@ -932,11 +932,10 @@ gdn_status gdn_attn_bwd(const gdn_attn_seq_problem* p, const void* q, const void
     const bool bf16 = p->dtype == GDN_BF16;
     const int64_t rows = (int64_t)a.Nq * a.Hq;
     const int lanes = D * (bf16 ? 2 : 4) / 16, per = 256 / (lanes < 32 ? lanes : 32);
-    const unsigned grid = (unsigned)((rows + per - 1) / per);
-    cudaError_t e = cudaSuccess;
-    if (grid > 0)
-      e = bf16 ? launch_behind(k_attn_rows<D, __nv_bfloat16>, dim3(grid), 256, 0, st, a)
-               : launch_behind(k_attn_rows<D, float>, dim3(grid), 256, 0, st, a);
+    // one CTA at least: it looks at a single sequence's offsets
+    const unsigned grid = rows > 0 ? (unsigned)((rows + per - 1) / per) : 1;
+    cudaError_t e = bf16 ? launch_behind(k_attn_rows<D, __nv_bfloat16>, dim3(grid), 256, 0, st, a)
+                         : launch_behind(k_attn_rows<D, float>, dim3(grid), 256, 0, st, a);
     if (e != cudaSuccess) return e;
     if (bf16) return launch_bwd_tc(a, D, st);
     e = launch_simt<k_attn_bwd_simt<D, true>>((int64_t)a.tk.most * a.Hk * a.splits, B_NT,

@@ -701,7 +701,7 @@ gdn_status gdn_slot_map(const gdn_slot_problem* p, const int32_t* ctx_len,
  *  - cu_q, cu_k int32 [n_seqs+1] in device memory; cu_k NULL: cu_q (Nk = Nq).  cu_q NULL (cu_k
  *    too): the rows of q are n_seqs sequences of Nq / n_seqs, those of k n_seqs of Nk / n_seqs.
  *    An offset outside the rows, or below the one before it, is raised or cut to the nearest that
- *    is neither, and recorded in `status`.
+ *    is neither, and recorded in `status` (a forward without query rows looks at none).
  *  - Rows of q, k, v that belong to no sequence have no influence, whatever they hold; rows of the
  *    outputs that belong to no sequence are left as they were.  (A NaN or infinity in a key or
  *    value row of a sequence may reach the queries of the same sequence that do not see it; in the

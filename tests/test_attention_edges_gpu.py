@@ -45,6 +45,21 @@ def test_attention_of_groups_of_any_size_with_divided_keys(Hq, Hk, D):
     check_seq([5, 3, 17], [6000, 2500, 900], Hq, Hk, D, BF, True, seed=Hq + D + 3)
 
 
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("cu,ck,fine", [([0, 0], [0, 70], True), ([0, 3], [0, 70], False),
+                                        ([0, 0], [-1, 70], False), ([0, 0], [0, 71], False),
+                                        ([0, 0, 0], [0, 30, 70], True),
+                                        ([0, 0, 1], [0, 30, 70], False)])
+def test_attention_gradients_without_queries_check_their_offsets(cu, ck, fine, dt):
+    k = torch.randn(70, 2, 64, device="cuda").to(dt)
+    q, lse = torch.empty((0, 4, 64), dtype=dt, device="cuda"), torch.empty((0, 4), device="cuda")
+    word = gdn.status_word()
+    out = [torch.full_like(k, 7.0) for _ in range(2)]
+    gdn.gdn_attn_bwd(q, k, k, q, lse, q, i32(cu), i32(ck), dk=out[0], dv=out[1], status=word)
+    assert gdn.gdn_check_device_status(word) == (gdn.GDN_OK if fine else gdn.GDN_ERR_INVALID_ARG)
+    assert not out[0].any() and not out[1].any()
+
+
 # A rounding to fp32 is off by 0.425 U of the value in the root mean square (uniform within half a
 # step, mantissas spread over their logarithm): STEP U^2.  A sum of n terms of random sign that is
 # rounded at each is off by n STEP U^2 of its square at most (where the first terms are the largest;
