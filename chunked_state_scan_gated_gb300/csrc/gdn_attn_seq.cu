@@ -7,8 +7,9 @@
 // queries that see it) or of queries (dq: all keys that they see), so that every gradient row has
 // one writer, no atomics, and sums in a fixed order.
 //
-// fp32: register tiles on CUDA cores, bound by their FMA rate (the split tf32 products of the
-// decode call would need two copies of every operand in shared memory).
+// fp32: register tiles on CUDA cores, whose FMA pipes are busy 55 to 64% of the time behind the reads of
+// shared memory (below).  Split products on the tensor cores, as in the decode call, would keep two or
+// three terms of every operand in shared memory (two of 64 rows of 128: 64 KB); they are not built.
 #include <math.h>
 #include <string.h>
 
@@ -32,7 +33,10 @@ struct PlanSide {
 };
 
 // The list of tiles, those with the most work first (in the order of 1024 classes of work; within
-// a class in any order, which no result depends on).  CTA 0: query tiles, CTA 1: key tiles.
+// a class in any order, which no result depends on).  CTA 0: query tiles, CTA 1: key tiles.  One CTA
+// goes over the offsets three times, 1024 at a time, in front of everything else: 5 to 6 us of a forward
+// of 16 x 1000 or 64 x 250 tokens (157 and 96 us; no difference in the gradients), but 110 us for 4096
+// sequences and 2.6 ms for 100,000.
 __global__ void __launch_bounds__(PL_NT) k_attn_plan(SeqArgs a, PlanSide s0, PlanSide s1) {
   __shared__ int s_start[PL_BUCKETS], s_warp[2][32], s_carry[2], s_max;
   __shared__ int s_q0[PL_NT], s_nq[PL_NT], s_k0[PL_NT], s_nk[PL_NT];
@@ -251,8 +255,8 @@ constexpr size_t fwd_smem() {
 
 // 64 queries of one head.  Two halves of the CTA take the blocks of 64 keys in turn, each with a
 // softmax of its own, and are joined at the end: a prompt's last tile, which takes the longest, is
-// done in half the time (9 prompts up to 700 tokens, 12 heads of 64: 59 us; one token behind 13,972
-// keys, 16 heads of 128: 65 us).  A thread has 8 rows (ty, ty + 8, ..) x 4 keys (tx, tx + 16, ..) of the
+// done in half the time (9 prompts up to 700 tokens, 12 heads of 64: 58 us; one token behind 13,972
+// keys, 4 heads of 128: 64 us, 16 heads 169).  A thread has 8 rows (ty, ty + 8, ..) x 4 keys (tx, tx + 16, ..) of the
 // scores, 8 rows x D/16 columns of o.
 template <int D>
 __global__ void __launch_bounds__(F_NT) k_attn_fwd_simt(SeqArgs a) {
@@ -750,7 +754,7 @@ Layout layout(const gdn_attn_seq_problem* p, bool bwd, int rq, int rk) {
   // average; the parts of o are fp32 and k_attn_merge joins them (bf16, 32 on 8 heads of 128: 64 tokens
   // behind 31936 338 us without, 53 with; with more tiles they cost more than they bring: 256 tiles of 9
   // sequences behind up to 16000 tokens 335 without, 348 in two parts, 4096 tokens 104 and 193.  fp32:
-  // one token behind 13,972 keys, 16 heads of 128, 507 and 65).
+  // one token behind 13,972 keys, 16 heads of 128, 1387 and 169; 4 heads 1384 and 64).
   y.parts = 1;
   const int64_t items = (int64_t)y.mq * (p->Hq / (bf16 ? tc_pack(G) : 1));
   if (!bwd && items > 0) {

@@ -18,7 +18,7 @@
 // thread per row or half of one.
 //
 // Bound by the tensor cores and, in long calls, by the chip's power (16384 tokens, 32 heads on 8 of 128,
-// causal: forward 1.28 ms = 1.71 PFLOP/s, backward 4.76 ms; 16 on 2 of 256: 1.32 and 6.06); the weights'
+// causal: forward 1.30 ms = 1.69 PFLOP/s, backward 4.73 ms; 16 on 2 of 256: 1.27 and 6.00); the weights'
 // bf16 rounding (2^-9 of a weight, as much as o's own rounding adds) is what lets the last product run
 // at their full rate.
 #include <cuda.h>
