@@ -8,8 +8,8 @@ import torch
 
 import chunked_state_scan_gated_gb300 as gdn
 from oracle import attention, decode
-from test_attention_gpu import (BF, F8, F32, U, check_dec, check_seq, dec_inputs, filled, i32, n64,
-                                rand, same, step_of, u8)
+from test_attention_gpu import (BF, F8, F32, U, check_cache, check_dec, check_seq, dec_inputs,
+                                filled, i32, n64, rand, same, step_of, u8)
 
 pytestmark = pytest.mark.gpu
 
@@ -122,11 +122,12 @@ def test_attention_fp32_error_over_a_long_context(D):
 
 # --------------------------------------------------------------------------- the 8-bit cache
 
-def check_cut(cu, ctx, N, D, dt, P=16, Hk=2, seed=0):
-    """Codes, scales and rows read back are those of the offsets as they count."""
+def check_cut(cu, ctx, N, D, dt, P=16, Hk=2, seed=0, room=None):
+    """Codes, scales and rows read back are those of the offsets as they count; `room` tokens (None: N)
+    at most to a request."""
     gen = torch.Generator().manual_seed(seed)
     B = len(ctx)
-    table, pages, _ = step_of([0] * B, [N + max(max(ctx), 0)] * B, P, seed=seed)
+    table, pages, _ = step_of([0] * B, [(room or N) + max(max(ctx), 0)] * B, P, seed=seed)
     caches = [filled(gen, pages, P, Hk, D) for _ in range(2)]
     before = [(u8(c).copy(), n64(s)) for c, s in caches]
     k, v = rand(gen, (N, Hk, D), dt), rand(gen, (N, Hk, D), dt)
@@ -162,6 +163,19 @@ def test_cache_offsets_out_of_order_among_many_requests():
     check_cut(cu, [i % 20 for i in range(700)], 700, 64, BF, Hk=1)
     cu[500], cu[3] = 500, 650
     check_cut(cu, [i % 20 for i in range(700)], 700, 64, BF, Hk=1)
+
+
+@pytest.mark.parametrize("dt,D", [(BF, 64), (F32, 64), (BF, 256)])
+def test_cache_of_very_many_requests(dt, D):
+    """So many that a CTA takes several runs of rows; the offsets in order, and not."""
+    B = 6000
+    new = [(0, 1, 2, 1, 5, 3, 1)[i % 7] for i in range(B)]
+    ctx = [i * 7 % 40 for i in range(B)]
+    check_cache(ctx, new, 1, D, 16, dt, seed=D)
+    if D == 64:
+        cu = np.cumsum([0] + new).tolist()
+        cu[4000], cu[90], cu[5999] = cu[3993], cu[97], cu[5990]
+        check_cut(cu, ctx, cu[-1], D, dt, Hk=1, room=40)
 
 
 # ------------------------------------------------------------------ decode over the 8-bit cache
